@@ -65,7 +65,8 @@ struct Trace {
 } g_trace;
 const char* const KIND_NAMES[K_COUNT] = {"gemm_small_m", "gdn", "attn_split", "attn_combine", "kv_append", "embed",
                                          "rmsnorm", "swiglu", "gdn_gates", "argmax", "accept", "commit", "zero",
-                                         "conv", "gated_norm", "gemm_combine", "tile_weights"};
+                                         "conv", "gated_norm", "gemm_combine", "tile_weights", "qk_norm_rope",
+                                         "kv_pages", "tree_positions", "tree_accept", "kv_append_path", "attn_tree"};
 }  // namespace
 
 void trace_pre(cudaStream_t s) {
@@ -152,6 +153,21 @@ xv_status encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, co
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(XV_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return XV_OK;
+}
+
+xv_status kv_pages_check(const xv_kv_pages* pages, int Hkv, int hd, KvPages* kv, int* Lmax) {
+    if (!pages || !pages->page_table) return fail(XV_ERR_ARG, "paged KV: null page table");
+    if (pages->page_size < 64 || pages->page_size % 64)
+        return fail(XV_ERR_UNSUPPORTED, "paged KV: page_size must be a positive multiple of 64 (got %d)", pages->page_size);
+    if (pages->max_pages < 1 || pages->n_pages < 1) return fail(XV_ERR_ARG, "paged KV: max_pages and n_pages must be positive");
+    if (static_cast<long long>(pages->page_size) * pages->max_pages > (1ll << 30))
+        return fail(XV_ERR_UNSUPPORTED, "paged KV: page_size * max_pages exceeds 2^30 positions");
+    if (static_cast<long long>(pages->n_pages) * Hkv * pages->page_size * hd > (1ll << 40))
+        return fail(XV_ERR_UNSUPPORTED, "paged KV: pool too large");
+    if (static_cast<long long>(pages->n_pages) * Hkv > (1ll << 31)) return fail(XV_ERR_UNSUPPORTED, "paged KV: too many pages");
+    *kv = KvPages{pages->page_table, pages->page_size, pages->max_pages, pages->n_pages};
+    *Lmax = pages->page_size * pages->max_pages;
     return XV_OK;
 }
 
@@ -443,22 +459,6 @@ xv_status xv_attn_decode_rows(const uint16_t* q, long long q_stride, const uint1
     if (!aligned16(ws)) return fail(XV_ERR_UNSUPPORTED, "attn: workspace must be 16-byte aligned");
     return attn_launch(q, q_stride, kc, vc, kv_contiguous(B, Lmax), ctx_len, 0, R, B, Hq, Hkv, hd, max_ctx, scale, gate,
                        gate_stride, out, out_stride, ws, ws_bytes, reinterpret_cast<cudaStream_t>(s));
-}
-
-// A page table and its sizes as the kernels take them; Lmax = the positions a sequence can hold.
-static xv_status kv_pages_check(const xv_kv_pages* pages, int Hkv, int hd, KvPages* kv, int* Lmax) {
-    if (!pages || !pages->page_table) return fail(XV_ERR_ARG, "paged KV: null page table");
-    if (pages->page_size < 64 || pages->page_size % 64)
-        return fail(XV_ERR_UNSUPPORTED, "paged KV: page_size must be a positive multiple of 64 (got %d)", pages->page_size);
-    if (pages->max_pages < 1 || pages->n_pages < 1) return fail(XV_ERR_ARG, "paged KV: max_pages and n_pages must be positive");
-    if (static_cast<long long>(pages->page_size) * pages->max_pages > (1ll << 30))
-        return fail(XV_ERR_UNSUPPORTED, "paged KV: page_size * max_pages exceeds 2^30 positions");
-    if (static_cast<long long>(pages->n_pages) * Hkv * pages->page_size * hd > (1ll << 40))
-        return fail(XV_ERR_UNSUPPORTED, "paged KV: pool too large");
-    if (static_cast<long long>(pages->n_pages) * Hkv > (1ll << 31)) return fail(XV_ERR_UNSUPPORTED, "paged KV: too many pages");
-    *kv = KvPages{pages->page_table, pages->page_size, pages->max_pages, pages->n_pages};
-    *Lmax = pages->page_size * pages->max_pages;
-    return XV_OK;
 }
 
 xv_status xv_attn_decode_rows_paged(const uint16_t* q, long long q_stride, const uint16_t* kpool, const uint16_t* vpool,

@@ -1,0 +1,284 @@
+// Page tables, slots and positions of a paged KV cache, built on the device from the requests'
+// lengths (the host counterpart is model.KvPagePool: the same pages in the same order).
+//
+// The free pages are a stack.  Finished requests (n_new = -1) push theirs, a request's last page
+// first; then every other request b pops the pages its ctx_len[b] + n_new[b] positions need beyond
+// the held[b] it has, in request order.  With R pages pushed and F free before, the k-th page
+// popped is stack entry F + R - 1 - k, so two exclusive sums over the requests (pages pushed, pages
+// popped) tell every request its pages, and a third one (rows) tells every new row its request.
+//
+// Kernel 1 (one CTA) forms the three sums and the new counters; kernel 2 moves the pages and writes
+// the rows, every CTA on its own: an entry it pops is read from the stack below F or, at F and
+// above, from the table row of the request that pushed it, and nothing it reads is written by
+// another CTA (the stack is written at F and above, a table row past its request's held pages, a
+// finished request's row not at all).  Both are latency: a few dependent reads, then a few bytes
+// per row.
+#include "xv_internal.h"
+#include "xv_ptx.cuh"
+
+namespace xv {
+namespace {
+
+constexpr int PG_THREADS = 1024;   // kernel 1
+constexpr int PG_WORK = 256;       // kernel 2
+
+struct PagesArgs {
+    int32_t* table;
+    int page, max_pages, n_pages;
+    int32_t* free_pages;
+    const int32_t* n_free_in;
+    int32_t* n_free_out;
+    const int32_t* held_in;
+    int32_t* held_out;
+    const int32_t* ctx_len;
+    const int32_t* n_new;
+    int B;
+    int32_t* row_start;
+    int32_t* pos;
+    long long* slots;
+    int max_rows;
+    // workspace: [0] free pages before, [1] pages pushed, [2] 1 when pages may be popped, then per
+    // request held pages before, pages needed (-1: finished), first push and first pop
+    int32_t* ws;
+    unsigned* err;
+};
+
+__device__ __forceinline__ int32_t* ws_held(const PagesArgs& A) { return A.ws + 4; }
+__device__ __forceinline__ int32_t* ws_need(const PagesArgs& A) { return A.ws + 4 + A.B; }
+__device__ __forceinline__ int32_t* ws_push(const PagesArgs& A) { return A.ws + 4 + 2ll * A.B; }
+__device__ __forceinline__ int32_t* ws_pop(const PagesArgs& A) { return A.ws + 4 + 3ll * A.B; }
+
+// Exclusive sums of three values over the CTA's threads; tot receives the CTA's totals.  Every
+// request's values are at most 2^30, so the sums are formed in 64 bits.
+__device__ __forceinline__ void block_scan3(long long v[3], long long tot[3], long long (*sm)[33]) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long inc[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        inc[q] = v[q];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc[q], off);
+            if (lane >= off) inc[q] += o;
+        }
+        if (lane == 31) sm[q][w] = inc[q];
+    }
+    __syncthreads();
+    if (w < 3) {
+        long long x = lane < PG_THREADS / 32 ? sm[w][lane] : 0, s = x;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, s, off);
+            if (lane >= off) s += o;
+        }
+        sm[w][lane] = s - x;
+        if (lane == 31) sm[w][32] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        v[q] = sm[q][w] + inc[q] - v[q];
+        tot[q] = sm[q][32];
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(PG_THREADS) kv_pages_scan_kernel(PagesArgs A) {
+    griddep_launch();
+    griddep_wait();
+    __shared__ long long sm[3][33];
+    const int tid = threadIdx.x;
+    const int F0 = *A.n_free_in;
+    const bool sane = F0 >= 0 && F0 <= A.n_pages;
+    const int F = sane ? F0 : 0;
+    const long long cap = static_cast<long long>(A.page) * A.max_pages;
+    long long carry[3] = {0, 0, 0};   // pushed, popped, rows
+    unsigned bad = sane ? 0u : ERR_BAD_COUNT;
+    for (int b0 = 0; b0 < A.B; b0 += PG_THREADS) {
+        const int b = b0 + tid;
+        long long v[3] = {0, 0, 0};
+        int held = 0, need = 0;
+        if (b < A.B) {
+            held = A.held_in[b];
+            int n = A.n_new[b];
+            const int ctx = A.ctx_len[b];
+            if (held < 0 || held > A.max_pages) {
+                bad |= ERR_BAD_COUNT;
+                held = held < 0 ? 0 : A.max_pages;
+            }
+            if (n == -1) {
+                v[0] = held;
+                need = -1;
+            } else {
+                if (n < -1 || ctx < 0 || static_cast<long long>(ctx) + n > cap) {
+                    bad |= n < -1 ? ERR_BAD_COUNT : ERR_BAD_LENGTH;
+                    n = 0;
+                } else {
+                    need = static_cast<int>((static_cast<long long>(ctx) + n + A.page - 1) / A.page);
+                }
+                v[1] = need > held ? need - held : 0;
+                v[2] = n;
+            }
+        }
+        long long tot[3];
+        block_scan3(v, tot, sm);
+        if (b < A.B) {
+            ws_held(A)[b] = held;
+            ws_need(A)[b] = need;
+            // sums past the pool or past int are refused below; clamp what is stored
+            ws_push(A)[b] = static_cast<int32_t>(min(carry[0] + v[0], 1ll << 30));
+            ws_pop(A)[b] = static_cast<int32_t>(min(carry[1] + v[1], 1ll << 30));
+            A.row_start[b] = static_cast<int32_t>(min(carry[2] + v[2], static_cast<long long>(A.max_rows)));
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) carry[q] += tot[q];
+    }
+    const bool push_ok = sane && F + carry[0] <= A.n_pages;
+    const long long R = push_ok ? carry[0] : 0;
+    const bool pop_ok = push_ok && carry[1] <= F + R;
+    if (!push_ok) bad |= ERR_BAD_COUNT;
+    if (push_ok && !pop_ok) bad |= ERR_NO_PAGES;
+    if (carry[2] > A.max_rows) bad |= ERR_BAD_COUNT;
+    if (bad) atomicOr(A.err, bad);
+    // held and n_free may be updated in place: every input has been read (each thread re-reads
+    // only its own requests' entries)
+    for (int b = tid; b < A.B; b += PG_THREADS) {
+        const int held = ws_held(A)[b], need = ws_need(A)[b];
+        A.held_out[b] = need < 0 ? (push_ok ? 0 : held) : (pop_ok && need > held ? need : held);
+    }
+    if (tid == 0) {
+        A.ws[0] = F;
+        A.ws[1] = static_cast<int32_t>(R);
+        A.ws[2] = (push_ok ? 1 : 0) | (pop_ok ? 2 : 0);
+        A.row_start[A.B] = static_cast<int32_t>(min(carry[2], static_cast<long long>(A.max_rows)));
+        *A.n_free_out = sane ? static_cast<int32_t>(F + R - (pop_ok ? carry[1] : 0)) : F0;
+    }
+}
+
+// The last request b in [0, B) with start[b] <= x, by a 32-way search of the whole warp (start is
+// nondecreasing, start[0] <= x).
+__device__ __forceinline__ int warp_find(const int32_t* start, int B, int x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = B;   // the answer lies in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, i = lo + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, lane * step < n && start[i] <= x);
+        const int k = 31 - __clz(m);   // lane 0 always holds
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
+}
+// The same by one thread.
+__device__ __forceinline__ int thread_find(const int32_t* start, int B, int x) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Stack entry i of the stack after the pushes (F entries before them).
+__device__ __forceinline__ int stack_entry(const PagesArgs& A, int F, int i) {
+    if (i < F) return A.free_pages[i];
+    // pushed in this call: the last request that starts at or before it (requests that push
+    // nothing share their successor's start, so the last one is the pusher)
+    const int x = i - F, b = thread_find(ws_push(A), A.B, x);
+    const int j = ws_held(A)[b] - 1 - (x - ws_push(A)[b]);
+    return A.table[static_cast<long long>(b) * A.max_pages + j];
+}
+
+// Page j of request b after this call, -1 where it has none.
+__device__ __forceinline__ int page_of(const PagesArgs& A, int F, int R, int flags, int b, int j) {
+    const int held = ws_held(A)[b];
+    if (j < held) return A.table[static_cast<long long>(b) * A.max_pages + j];
+    if (!(flags & 2)) return -1;
+    return stack_entry(A, F, F + R - 1 - (ws_pop(A)[b] + j - held));
+}
+
+// CTAs [0, seq_ctas): a warp per request moves its pages.  The others: a warp per 32 new rows.
+__global__ void __launch_bounds__(PG_WORK) kv_pages_write_kernel(PagesArgs A, int seq_ctas) {
+    griddep_launch();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int F = A.ws[0], R = A.ws[1], flags = A.ws[2];
+    if (static_cast<int>(blockIdx.x) < seq_ctas) {
+        const int b = blockIdx.x * (PG_WORK / 32) + w;
+        if (b >= A.B) return;
+        const int held = ws_held(A)[b], need = ws_need(A)[b];
+        int32_t* row = A.table + static_cast<long long>(b) * A.max_pages;
+        if (need < 0) {
+            if (!(flags & 1)) return;
+            const int top = F + ws_push(A)[b] + held - 1;
+            for (int j = lane; j < held; j += 32) {
+                const int pg = row[j];
+                if (pg < 0 || pg >= A.n_pages) atomicOr(A.err, ERR_BAD_PAGE);
+                A.free_pages[top - j] = pg;
+            }
+        } else if (flags & 2) {
+            for (int j = held + lane; j < need; j += 32) {
+                const int pg = page_of(A, F, R, flags, b, j);
+                if (pg < 0 || pg >= A.n_pages) atomicOr(A.err, ERR_BAD_PAGE);
+                row[j] = pg;
+            }
+        }
+        return;
+    }
+    const int total = A.row_start[A.B];
+    const int t0 = ((static_cast<int>(blockIdx.x) - seq_ctas) * (PG_WORK / 32) + w) * 32;
+    if (t0 >= total) return;
+    int b = warp_find(A.row_start, A.B, t0);
+    const int t = t0 + lane;
+    if (t >= total) return;
+    while (b + 1 < A.B && A.row_start[b + 1] <= t) ++b;
+    const int p = A.ctx_len[b] + t - A.row_start[b], j = p / A.page;
+    int pg = page_of(A, F, R, flags, b, j);
+    if (pg < -1 || pg >= A.n_pages || (pg < 0 && (flags & 2))) {
+        atomicOr(A.err, ERR_BAD_PAGE);
+        pg = -1;
+    }
+    A.pos[t] = p;
+    A.slots[t] = pg < 0 ? -1 : static_cast<long long>(pg) * A.page + (p - j * A.page);
+}
+
+}  // namespace
+}  // namespace xv
+
+using namespace xv;
+
+extern "C" {
+
+size_t xv_kv_pages_workspace_size(int B) { return B < 1 ? 0 : (16ull + 16ull * B + 255) / 256 * 256; }
+
+xv_status xv_kv_pages_update(int32_t* page_table, int page_size, int max_pages, int n_pages, int32_t* free_pages,
+                             const int32_t* n_free, int32_t* n_free_out, const int32_t* held, int32_t* held_out,
+                             const int32_t* ctx_len, const int32_t* n_new, int B, int32_t* row_start, int32_t* pos,
+                             long long* slots, int max_rows, void* ws, size_t ws_bytes, xv_stream s) {
+    if (!free_pages || !n_free || !n_free_out || !held || !held_out || !ctx_len || !n_new || !row_start || !pos || !slots)
+        return fail(XV_ERR_ARG, "kv_pages_update: null pointer");
+    if (B < 1 || max_rows < 1) return fail(XV_ERR_ARG, "kv_pages_update: need B >= 1 and max_rows >= 1");
+    if (B > 65535 || max_rows > (1 << 30)) return fail(XV_ERR_UNSUPPORTED, "kv_pages_update: B above 65535 or max_rows above 2^30");
+    KvPages kv{};
+    int Lmax = 0;
+    const xv_kv_pages pages{page_table, page_size, max_pages, n_pages};
+    if (xv_status st = kv_pages_check(&pages, 1, 1, &kv, &Lmax)) return st;
+    const size_t need = xv_kv_pages_workspace_size(B);
+    if (!ws || ws_bytes < need) return fail(XV_ERR_WORKSPACE, "kv_pages_update: workspace of %zu bytes needed", need);
+    if (!aligned16(ws)) return fail(XV_ERR_UNSUPPORTED, "kv_pages_update: workspace must be 16-byte aligned");
+    unsigned* err = device_error_word();
+    if (!err) return fail(XV_ERR_CUDA, "kv_pages_update: device error word unavailable");
+    PagesArgs a{page_table, kv.page, kv.max_pages, kv.n_pages, free_pages, n_free, n_free_out, held, held_out, ctx_len,
+                n_new, B, row_start, pos, slots, max_rows, static_cast<int32_t*>(ws), err};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
+    trace_pre(st);
+    launch_k(kv_pages_scan_kernel, dim3(1), dim3(PG_THREADS), 0, st, a);
+    if (xv_status e = launched("kv_pages_scan_kernel", st, K_PAGES, 32ll * B)) return e;
+    const int seq_ctas = ceil_div(B, PG_WORK / 32);
+    trace_pre(st);
+    launch_k(kv_pages_write_kernel, dim3(seq_ctas + ceil_div(max_rows, PG_WORK)), dim3(PG_WORK), 0, st, a, seq_ctas);
+    return launched("kv_pages_write_kernel", st, K_PAGES, 12ll * max_rows + 16ll * B);
+}
+
+}  // extern "C"

@@ -15,7 +15,8 @@ xv_status fail(xv_status code, const char* fmt, ...);
 xv_status cuda_check(cudaError_t e, const char* what);
 // Kernel kinds of the launch trace.
 enum Kind : int { K_GEMM = 0, K_GDN, K_ATTN_SPLIT, K_ATTN_COMBINE, K_KV_APPEND, K_EMBED, K_RMSNORM, K_SWIGLU,
-                  K_GATES, K_ARGMAX, K_ACCEPT, K_COMMIT, K_ZERO, K_CONV, K_GNORM, K_GEMM_COMBINE, K_TILE, K_COUNT };
+                  K_GATES, K_ARGMAX, K_ACCEPT, K_COMMIT, K_ZERO, K_CONV, K_GNORM, K_GEMM_COMBINE, K_TILE, K_ROPE,
+                  K_PAGES, K_TREE_POS, K_TREE_ACCEPT, K_KV_APPEND_PATH, K_ATTN_TREE, K_COUNT };
 // Call right before a launch on stream s (records the opening trace event when tracing).
 void trace_pre(cudaStream_t s);
 // Checks the launch just made on the calling thread, counts it and closes its trace record.
@@ -172,6 +173,9 @@ struct KvPages {
     const int32_t* table;
     int page, max_pages, n_pages;
 };
+// Checks a caller's page description and gives it as the kernels take it; *Lmax = the positions a
+// sequence can hold.
+xv_status kv_pages_check(const xv_kv_pages* pages, int Hkv, int hd, KvPages* kv, int* Lmax);
 inline KvPages kv_contiguous(int B, int Lmax) { return KvPages{nullptr, Lmax, 1, B}; }
 // Row r of sequence b sees ctx_len[b] + len_bias + r positions; max_len bounds every such length.
 xv_status attn_launch(const uint16_t* q, long long q_stride, const uint16_t* kc, const uint16_t* vc, const KvPages& kv,

@@ -14,7 +14,9 @@ enum : unsigned {
     ERR_BAD_TOKEN = 1u << 1,      // a token id outside [0, vocab)
     ERR_BAD_LENGTH = 1u << 2,     // a context length outside the range the launch was sized for
     ERR_BAD_COUNT = 1u << 3,      // a commit/keep count or a per-sequence k outside its range
-    ERR_BAD_PAGE = 1u << 4,       // a KV page table entry outside the pool
+    ERR_BAD_PAGE = 1u << 4,       // a KV page table entry or a slot outside the pool
+    ERR_BAD_TREE = 1u << 5,       // a draft tree's parent that is not an earlier node (or -1)
+    ERR_NO_PAGES = 1u << 6,       // fewer free KV pages than the requests need
 };
 
 // Upper bound on the time one mbarrier wait may take before it records an

@@ -66,6 +66,10 @@ class BlockState(ctypes.Structure):
                 ("kv_pages", KvPages), ("last_k_seq", vp)]
 
 
+class QkRope(ctypes.Structure):
+    _fields_ = [("q_norm", vp), ("k_norm", vp), ("eps", c_float), ("freq", vp), ("rot", c_int), ("interleaved", c_int)]
+
+
 _lib = None
 
 _SIGS = {
@@ -106,6 +110,23 @@ _SIGS = {
     "xv_attn_decode_rows_paged": ([vp, c_ll, vp, vp, ctypes.POINTER(KvPages), vp, c_int, c_int, c_int, c_int, c_int,
                                    c_int, c_float, vp, c_ll, vp, c_ll, vp, c_sz, vp], c_int),
     "xv_kv_append_paged": ([vp, c_ll, vp, c_int, c_int, c_int, c_int, ctypes.POINTER(KvPages), vp, vp, vp], c_int),
+    "xv_kv_pages_workspace_size": ([c_int], c_sz),
+    "xv_kv_pages_update": ([vp, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, c_int, vp, vp, vp, c_int, vp, c_sz, vp],
+                           c_int),
+    "xv_qk_norm_rope": ([vp, c_ll, vp, c_ll, vp, c_ll, vp, c_ll, ctypes.POINTER(QkRope), vp, vp, c_int, c_int, c_int,
+                         c_int, vp], c_int),
+    "xv_qk_norm_rope_append": ([vp, c_ll, vp, c_ll, vp, c_ll, ctypes.POINTER(QkRope), vp, vp, vp, c_int, c_int, c_int,
+                                c_int, c_int, c_int, vp, vp, vp], c_int),
+    "xv_tree_positions": ([vp, vp, vp, c_int, c_int, vp, vp], c_int),
+    "xv_attn_tree_workspace_size": ([c_int, c_int, c_int, c_int, c_int], c_sz),
+    "xv_attn_tree": ([vp, c_ll, vp, vp, vp, vp, c_ll, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+                      vp, c_ll, vp, c_ll, vp, c_sz, vp], c_int),
+    "xv_attn_tree_paged": ([vp, c_ll, vp, vp, ctypes.POINTER(KvPages), vp, vp, c_ll, vp, vp, c_int, c_int, c_int, c_int,
+                            c_int, c_int, c_float, vp, c_ll, vp, c_ll, vp, c_sz, vp], c_int),
+    "xv_tree_accept": ([vp, vp, vp, vp, c_int, c_int, vp, vp, vp, vp], c_int),
+    "xv_kv_append_path": ([vp, c_ll, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, vp, vp, vp], c_int),
+    "xv_kv_append_path_paged": ([vp, c_ll, vp, vp, vp, c_int, c_int, c_int, c_int, ctypes.POINTER(KvPages), vp, vp, vp],
+                                c_int),
     "xv_gdn_in_dim": ([ctypes.POINTER(BlockConfig)], c_int),
     "xv_gdn_hist_stride": ([ctypes.POINTER(BlockConfig)], c_int),
     "xv_attn_in_dim": ([ctypes.POINTER(BlockConfig)], c_int),
@@ -374,6 +395,106 @@ def xv_attn_decode_rows_paged(q, q_stride, kpool, vpool, pages: KvPages, ctx_len
 def xv_kv_append_paged(kv_src, src_stride, ctx_len, R, B, Hkv, hd, pages: KvPages, kpool, vpool, stream=None):
     _check(lib().xv_kv_append_paged(_ptr(kv_src), src_stride, _ptr(ctx_len), R, B, Hkv, hd, ctypes.byref(pages),
                                     _ptr(kpool), _ptr(vpool), _stream(stream)))
+
+
+def xv_kv_pages_workspace_size(B: int) -> int:
+    return int(lib().xv_kv_pages_workspace_size(B))
+
+
+def xv_kv_pages_update(pages: KvPages, free_pages, n_free, held, ctx_len, n_new, row_start, pos, slots, ws,
+                       n_free_out=None, held_out=None, stream=None):
+    """Pages, positions and slots of every request's new rows (the C header has the rules); the
+    requests are the entries of ctx_len.  n_free and held are updated in place unless
+    n_free_out / held_out are given."""
+    B = ctx_len.numel()
+    if free_pages.numel() < pages.n_pages or row_start.numel() < B + 1 or pos.numel() < slots.numel():
+        raise ValueError("free_pages needs n_pages entries, row_start B + 1 and pos as many as slots")
+    _check(lib().xv_kv_pages_update(pages.page_table, pages.page_size, pages.max_pages, pages.n_pages, _ptr(free_pages),
+                                    _ptr(n_free), _ptr(n_free if n_free_out is None else n_free_out), _ptr(held),
+                                    _ptr(held if held_out is None else held_out), _ptr(ctx_len), _ptr(n_new), B,
+                                    _ptr(row_start), _ptr(pos), _ptr(slots), slots.numel(), _ptr(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------- head norms and rotation
+
+def rope_freqs(rot: int, base: float = 10000.0, scale: float = 1.0, device="cuda") -> torch.Tensor:
+    """The frequencies base^(-2i/rot) / scale, i < rot/2, as the library takes them: turns per
+    position in 64-bit binary fractions (int64 holding the uint64 bits)."""
+    import math
+    f = [round(base ** (-2.0 * i / rot) / scale / (2.0 * math.pi) * 2.0 ** 64) % 2 ** 64 for i in range(rot // 2)]
+    return torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in f], dtype=torch.int64, device=device)
+
+
+def _qk_rope(q_norm, k_norm, eps, freqs, interleaved):
+    return QkRope(None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(), eps,
+                  None if freqs is None else freqs.data_ptr(), 0 if freqs is None else 2 * freqs.numel(),
+                  int(interleaved))
+
+
+def xv_qk_norm_rope(q, k, pos, Hq, Hkv, hd, q_out, k_out, q_norm=None, k_norm=None, eps=1e-6, freqs=None,
+                    interleaved=False, n_rows=None, stream=None):
+    """Norms and rotates the heads of q [M, >= Hq*hd] into q_out and of k [M, >= Hkv*hd] into k_out
+    (each may be its input); freqs from :func:`rope_freqs` (None: no rotation)."""
+    r = _qk_rope(q_norm, k_norm, eps, freqs, interleaved)
+    _check(lib().xv_qk_norm_rope(_ptr(q), _row_stride(q), _ptr(q_out), _row_stride(q_out), _ptr(k), _row_stride(k),
+                                 _ptr(k_out), _row_stride(k_out), ctypes.byref(r), _ptr(pos), _ptr(n_rows), q.shape[0],
+                                 Hq, Hkv, hd, _stream(stream)))
+
+
+def xv_qk_norm_rope_append(q, kv, pos, slots, Hq, Hkv, hd, q_out, kpool, vpool, page_size, n_pages, q_norm=None,
+                           k_norm=None, eps=1e-6, freqs=None, interleaved=False, n_rows=None, stream=None):
+    """The same with the k heads of kv [M, k | v], normed and rotated, and its v heads written to
+    slots (int64 [M]) of the pools."""
+    r = _qk_rope(q_norm, k_norm, eps, freqs, interleaved)
+    _check(lib().xv_qk_norm_rope_append(_ptr(q), _row_stride(q), _ptr(q_out), _row_stride(q_out), _ptr(kv),
+                                        _row_stride(kv), ctypes.byref(r), _ptr(pos), _ptr(slots), _ptr(n_rows),
+                                        q.shape[0], Hq, Hkv, hd, page_size, n_pages, _ptr(kpool), _ptr(vpool),
+                                        _stream(stream)))
+
+
+# ------------------------------------------------------ a tree of drafts
+
+def xv_tree_positions(parent, n_nodes, ctx_len, pos, stream=None):
+    B, N = parent.shape
+    _check(lib().xv_tree_positions(_ptr(parent), _ptr(n_nodes), _ptr(ctx_len), N, B, _ptr(pos), _stream(stream)))
+
+
+def xv_attn_tree_workspace_size(B, N, Hq, hd, max_ctx) -> int:
+    return int(lib().xv_attn_tree_workspace_size(B, N, Hq, hd, max_ctx))
+
+
+def xv_attn_tree(q, kc, vc, ctx_len, kv_src, parent, n_nodes, N, B, Hq, Hkv, hd, Lmax, max_ctx, scale, out, ws,
+                 gate=None, stream=None):
+    """q, kv_src, out and gate are row tensors [B*N, ...] (row strides taken from them)."""
+    _check(lib().xv_attn_tree(_ptr(q), _row_stride(q), _ptr(kc), _ptr(vc), _ptr(ctx_len), _ptr(kv_src),
+                              _row_stride(kv_src), _ptr(parent), _ptr(n_nodes), N, B, Hq, Hkv, hd, Lmax, max_ctx, scale,
+                              _ptr(gate), 0 if gate is None else _row_stride(gate), _ptr(out), _row_stride(out), _ptr(ws),
+                              ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def xv_attn_tree_paged(q, kpool, vpool, pages: KvPages, ctx_len, kv_src, parent, n_nodes, N, B, Hq, Hkv, hd, max_ctx,
+                       scale, out, ws, gate=None, stream=None):
+    _check(lib().xv_attn_tree_paged(_ptr(q), _row_stride(q), _ptr(kpool), _ptr(vpool), ctypes.byref(pages), _ptr(ctx_len),
+                                    _ptr(kv_src), _row_stride(kv_src), _ptr(parent), _ptr(n_nodes), N, B, Hq, Hkv, hd,
+                                    max_ctx, scale, _ptr(gate), 0 if gate is None else _row_stride(gate), _ptr(out),
+                                    _row_stride(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def xv_tree_accept(tokens, parent, n_nodes, argmax, path, n_keep, next_token, stream=None):
+    B, N = parent.shape
+    _check(lib().xv_tree_accept(_ptr(tokens), _ptr(parent), _ptr(n_nodes), _ptr(argmax), N, B, _ptr(path), _ptr(n_keep),
+                                _ptr(next_token), _stream(stream)))
+
+
+def xv_kv_append_path(kv_src, path, n_keep, ctx_len, N, B, Hkv, hd, Lmax, kc, vc, stream=None):
+    _check(lib().xv_kv_append_path(_ptr(kv_src), _row_stride(kv_src), _ptr(path), _ptr(n_keep), _ptr(ctx_len), N, B, Hkv,
+                                   hd, Lmax, _ptr(kc), _ptr(vc), _stream(stream)))
+
+
+def xv_kv_append_path_paged(kv_src, path, n_keep, ctx_len, N, B, Hkv, hd, pages: KvPages, kpool, vpool, stream=None):
+    _check(lib().xv_kv_append_path_paged(_ptr(kv_src), _row_stride(kv_src), _ptr(path), _ptr(n_keep), _ptr(ctx_len), N,
+                                         B, Hkv, hd, ctypes.byref(pages), _ptr(kpool), _ptr(vpool), _stream(stream)))
 
 
 # ------------------------------------------------------------------ block

@@ -72,8 +72,9 @@ const char* xv_last_error(void);
  * recorded bits (code may be NULL): 1 a bounded wait gave up, 2 a token id
  * outside [0, vocab), 4 a context length outside what the launch was sized
  * for, 8 a commit count or per-sequence k outside its range, 16 a KV page
- * table entry outside the pool.  The only call in the library that
- * synchronises. */
+ * table entry or slot outside the pool, 32 a draft tree's parent that is not
+ * an earlier node or -1, 64 fewer free KV pages than the requests need.  The
+ * only call in the library that synchronises. */
 xv_status xv_device_check(xv_stream s, unsigned* code);
 
 /* Number of kernels this library has launched in this process (host counter). */
@@ -378,6 +379,159 @@ xv_status xv_attn_decode_rows_paged(const uint16_t* q, long long q_stride, const
 /* xv_kv_append into paged pools. */
 xv_status xv_kv_append_paged(const uint16_t* kv_src, long long src_stride, const int32_t* ctx_len, int R, int B,
                              int Hkv, int hd, const xv_kv_pages* pages, uint16_t* kpool, uint16_t* vpool, xv_stream s);
+
+/* Page tables and slots on the device.  Each of B requests has ctx_len[b]
+ * positions in the cache, held[b] table entries filled, and n_new[b] >= 0 new
+ * rows to place after them, or n_new[b] = -1 when it is finished.  The free
+ * pages are a stack: free_pages[0 .. *n_free), the top last, room for n_pages
+ * entries.  The call
+ *   1. pushes the held pages of the finished requests, in request order, a
+ *      request's last page first (their table rows stay as they are);
+ *   2. pops, in request order, the pages every other request needs for
+ *      ctx_len[b] + n_new[b] positions beyond those it holds, into its table
+ *      row from entry held[b] on (entries past the new held[b] stay);
+ *   3. writes *n_free_out and held_out[b] (0 for a finished request), which may
+ *      be n_free and held themselves;
+ *   4. writes row_start [B + 1], the exclusive sums of the new rows, and for
+ *      row t of request b (row_start[b] <= t < row_start[b + 1]) its position
+ *      pos[t] = ctx_len[b] + t - row_start[b] and its slot
+ *      slots[t] = page * page_size + position % page_size.  Entries from
+ *      row_start[B] on stay as they are.
+ * These are the pages the host would give: a release of each finished request,
+ * then a request for each other one, in order, from a last-in-first-out list.
+ * ctx_len and n_new are not changed.  All pointers are device memory; pos and
+ * slots hold max_rows entries; the table is [B, max_pages] with page_size a
+ * positive multiple of 64, as in xv_kv_pages.  Workspace:
+ * xv_kv_pages_workspace_size(B) bytes, 16-byte aligned (0 for B < 1).
+ * Errors: XV_ERR_ARG (null pointer, B, max_rows, max_pages or n_pages < 1),
+ * XV_ERR_UNSUPPORTED (page_size, B above 65535, max_rows above 2^30, more than
+ * 2^30 positions per request, unaligned workspace), XV_ERR_WORKSPACE,
+ * XV_ERR_CUDA.  Recorded for xv_device_check: too few free pages (64; no
+ * request gets a page then, rows without one get slot -1), a request past
+ * page_size * max_pages positions or with a negative length (4), n_new below
+ * -1, held outside [0, max_pages], more rows than max_rows, a stack count that
+ * does not fit the pool (8; such a request gets no rows, rows past max_rows
+ * are dropped, an unfit stack is left as it is and nobody gets pages), a page
+ * outside the pool (16; its rows get slot -1). */
+size_t xv_kv_pages_workspace_size(int B);
+xv_status xv_kv_pages_update(int32_t* page_table, int page_size, int max_pages, int n_pages, int32_t* free_pages,
+                             const int32_t* n_free, int32_t* n_free_out, const int32_t* held, int32_t* held_out,
+                             const int32_t* ctx_len, const int32_t* n_new, int B, int32_t* row_start, int32_t* pos,
+                             long long* slots, int max_rows, void* ws, size_t ws_bytes, xv_stream s);
+
+/* ------------------------------------------- head norms and rotation
+ * Per-head RMSNorm of queries and keys and their position rotation, in one
+ * pass.  For a head x of hd values of a row at position p, in fp32, rounded to
+ * bf16 once:
+ *     y = x / sqrt(mean(x^2) + eps) * (1 + w)      (y = x when w is NULL)
+ *     (y_i, y_j) <- (y_i cos a - y_j sin a, y_j cos a + y_i sin a), a = p f_i
+ * over the rot/2 pairs of its first rot values, (i, i + rot/2), or
+ * (2i, 2i + 1) with interleaved != 0.  freq[i] is f_i in turns per position as
+ * a 64-bit binary fraction, round(f_i / (2 pi) * 2^64): the angle is exact to
+ * far below an fp32's last place at every 32-bit position. */
+typedef struct {
+    const uint16_t* q_norm;   /* [hd] or NULL (no norm) */
+    const uint16_t* k_norm;   /* [hd] or NULL */
+    float eps;
+    const uint64_t* freq;     /* [rot / 2] device; may be NULL when rot = 0 */
+    int rot;                  /* rotated values per head, a multiple of 16 up to hd */
+    int interleaved;
+} xv_qk_rope;
+
+/* M rows: q [M, Hq*hd] -> q_out, k [M, Hkv*hd] -> k_out; row strides in
+ * elements.  q_out may be q and k_out may be k (in place); otherwise inputs and
+ * outputs must not overlap.  pos [M] int32 device (NULL when rot = 0).  n_rows: device
+ * count of rows to do (rows from *n_rows on are left as they were; above M: M),
+ * or NULL for all M.  hd in {64, 128, 256}; rows, strides and norm weights 16-byte aligned.
+ * Errors: XV_ERR_ARG (null pointer, sizes < 1, rot outside [0, hd], a row
+ * stride below its row), XV_ERR_UNSUPPORTED (hd, rot % 16, alignment, Hq or Hkv
+ * above 65535), XV_ERR_CUDA. */
+xv_status xv_qk_norm_rope(const uint16_t* q, long long q_stride, uint16_t* q_out, long long q_out_stride,
+                          const uint16_t* k, long long k_stride, uint16_t* k_out, long long k_out_stride,
+                          const xv_qk_rope* rope, const int32_t* pos, const int32_t* n_rows, int M, int Hq, int Hkv,
+                          int hd, xv_stream s);
+
+/* The same with K and V written into a cache: row r's normed and rotated k
+ * heads and its v heads (kv row: k at column 0, v at column Hkv*hd) go to slot
+ * slots[r] of the pools [n_pages, Hkv, page_size, hd] (slot = page * page_size
+ * + row inside the page; a contiguous cache [B, Hkv, Lmax, hd] is B pages of
+ * Lmax).  A row with slot -1 writes only its q.  A slot outside the pool is
+ * recorded (16) and treated as -1; two rows of a call must not share a slot.
+ * Errors as above, and XV_ERR_ARG for null slots or pools, page_size or n_pages
+ * < 1. */
+xv_status xv_qk_norm_rope_append(const uint16_t* q, long long q_stride, uint16_t* q_out, long long q_out_stride,
+                                 const uint16_t* kv, long long kv_stride, const xv_qk_rope* rope, const int32_t* pos,
+                                 const long long* slots, const int32_t* n_rows, int M, int Hq, int Hkv, int hd,
+                                 int page_size, int n_pages, uint16_t* kpool, uint16_t* vpool, xv_stream s);
+
+/* ------------------------------------------------- a tree of drafts
+ * Up to XV_KMAX nodes per sequence: parent [B, N] int32 device, parent[b*N + i]
+ * < i or -1; node 0 is the last committed token, every other node a draft that
+ * continues its parent.  n_nodes [B] int32 device, the nodes of each sequence's
+ * tree (0..N; rows from n_nodes[b] on are neither read nor written), or NULL for
+ * N everywhere.  Node i is row b*N + i of every row array.  ctx_len [B] int32
+ * device counts the tokens committed to the cache (0 is allowed, and unlike in
+ * xv_attn_decode_rows it does not include the rows' own tokens): a node at
+ * depth d (steps to its root) stands at position ctx_len[b] + d.  A parent that
+ * is not an earlier node is recorded (32) and read as -1, n_nodes outside
+ * [0, N] recorded (8) and clamped.
+ * Errors of all calls below: XV_ERR_ARG (null pointer, sizes < 1, row strides
+ * below their rows), XV_ERR_UNSUPPORTED (N above XV_KMAX, B above 65535,
+ * unaligned rows or caches), XV_ERR_CUDA. */
+
+/* pos[b*N + i] = ctx_len[b] + depth of node i, for xv_qk_norm_rope. */
+xv_status xv_tree_positions(const int32_t* parent, const int32_t* n_nodes, const int32_t* ctx_len, int N, int B,
+                            int32_t* pos, xv_stream s);
+
+/* Attention of every node over the cache's ctx_len[b] positions and its own
+ * path (its ancestors and itself): per q head h, kv head h / (Hq/Hkv),
+ *     out = softmax(q . K^T * scale) V.
+ * The tree's own K and V are read from kv_src (row b*N + i: k at column 0, v at
+ * column Hkv*hd, row stride src_stride), not from the cache; only a kept path
+ * enters it (xv_kv_append_path).  A row has the bits of an xv_attn_decode_rows
+ * row at its position over a cache that holds its path (hd 64 and 256), whatever
+ * the other nodes hold, non-finite values included.
+ *   q [B*N, Hq*hd], out [B*N, Hq*hd], optional gate as in xv_attn_decode_rows;
+ *   kc, vc [B, Hkv, Lmax, hd] (or pools, _paged); hd in {64, 128, 256}, Hq a
+ *   multiple of Hkv, at most 128 q heads per kv head; 0 <= max_ctx <= Lmax
+ *   (page_size * max_pages) bounds every ctx_len[b].
+ * Workspace: xv_attn_tree_workspace_size(B, N, Hq, hd, max_ctx) bytes, 16-byte
+ * aligned (0 for sizes outside what the call takes).  A sequence whose
+ * ctx_len[b] falls outside [0, max_ctx] is skipped and recorded (4), a page
+ * outside the pool recorded (16) and read as page 0.  XV_ERR_WORKSPACE when the
+ * workspace is missing or too small. */
+size_t xv_attn_tree_workspace_size(int B, int N, int Hq, int hd, int max_ctx);
+xv_status xv_attn_tree(const uint16_t* q, long long q_stride, const uint16_t* kc, const uint16_t* vc,
+                       const int32_t* ctx_len, const uint16_t* kv_src, long long src_stride, const int32_t* parent,
+                       const int32_t* n_nodes, int N, int B, int Hq, int Hkv, int hd, int Lmax, int max_ctx, float scale,
+                       const uint16_t* gate, long long gate_stride, uint16_t* out, long long out_stride, void* ws,
+                       size_t ws_bytes, xv_stream s);
+xv_status xv_attn_tree_paged(const uint16_t* q, long long q_stride, const uint16_t* kpool, const uint16_t* vpool,
+                             const xv_kv_pages* pages, const int32_t* ctx_len, const uint16_t* kv_src, long long src_stride,
+                             const int32_t* parent, const int32_t* n_nodes, int N, int B, int Hq, int Hkv, int hd,
+                             int max_ctx, float scale, const uint16_t* gate, long long gate_stride, uint16_t* out,
+                             long long out_stride, void* ws, size_t ws_bytes, xv_stream s);
+
+/* Greedy walk ([post]: temperature 0, every draft compared with the target's
+ * argmax): from node 0, as long as a child's token equals argmax[b*N + cur] (the
+ * target's token after node cur), to the lowest such child.  path[b*N + t] =
+ * the t-th node kept (node 0 first), -1 from n_keep[b] on; n_keep[b] >= 1 (0 for
+ * a sequence without nodes); next_token[b] = the target's token after the last
+ * kept node (-1 without nodes). */
+xv_status xv_tree_accept(const int32_t* tokens, const int32_t* parent, const int32_t* n_nodes, const int32_t* argmax, int N,
+                         int B, int32_t* path, int32_t* n_keep, int32_t* next_token, xv_stream s);
+
+/* Commits a kept path: K and V of node path[b*N + t], t < n_keep[b], go from
+ * its kv_src row (as for xv_attn_tree) to position ctx_len[b] + t of sequence b.
+ * ctx_len is not changed.  n_keep outside [0, N] is recorded (8) and clamped; a
+ * node outside [0, N) (8), a position outside the cache (4) or a page outside
+ * the pool (16) is recorded and the row skipped.  hd a multiple of 8. */
+xv_status xv_kv_append_path(const uint16_t* kv_src, long long src_stride, const int32_t* path, const int32_t* n_keep,
+                            const int32_t* ctx_len, int N, int B, int Hkv, int hd, int Lmax, uint16_t* kc, uint16_t* vc,
+                            xv_stream s);
+xv_status xv_kv_append_path_paged(const uint16_t* kv_src, long long src_stride, const int32_t* path, const int32_t* n_keep,
+                                  const int32_t* ctx_len, int N, int B, int Hkv, int hd, const xv_kv_pages* pages,
+                                  uint16_t* kpool, uint16_t* vpool, xv_stream s);
 
 /* ------------------------------------------------------------ the block
  * A stack of decoder layers (each: x + mixer(rmsnorm(x)), then
