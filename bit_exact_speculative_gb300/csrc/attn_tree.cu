@@ -1,4 +1,28 @@
-// Attention of a tree of drafted tokens over a bf16 KV cache.
+// Attention of a tree of drafted tokens over a bf16 KV cache, on tcgen05, with the bits of decode.
+//
+// Every row (node, q head) attends to the cache's ctx positions and to its own path, and is computed
+// by the operations of a decode row at its position (attn.cu): splits at fixed absolute positions,
+// tiles of 64 positions, an fp32 online softmax over the tiles in order with the sum l taken position
+// by position, P rounded to bf16, P V accumulated 16 positions (one MMA K step) at a time, the splits
+// combined in split order.  A tree changes nothing of that below position 16 * (ctx / 16): those
+// positions are the same for every row.  Above, rows disagree about what stands at a position:
+//   - scores: Q K^T against all nodes at once (one 64-column tile, each score its own dot product); a
+//     row masks the nodes off its path.  Nodes are numbered after their parents, so a row's path in
+//     node order is in position order, and adding the masked zeros leaves its sum's bits alone;
+//   - P V: the 16 positions of one K step stay one K step.  For every node t that is the last of its
+//     path inside a 16-position group (a leaf, or the group's last position), a block of 16 V rows is
+//     gathered: the cache's rows below ctx, then t's ancestors in the group, zeros past t.  A row has
+//     its p in the block its path runs through, p = 0 in all others, and blocks go in position order,
+//     so what each row accumulates, K step by K step, is a decode row's sequence with no-ops between.
+// A non-finite V value would turn those no-ops into NaN (0 * inf), so the gather replaces it by zero
+// and the epilogue adds p * v itself, for the rows whose path holds it.
+//
+// Work items (split, row tile, kv head, sequence); a row tile is up to 128 rows: as many whole nodes,
+// Hq/Hkv rows each, as fit, spread evenly over the tiles.  Per item, as in attn.cu: K and V tiles by
+// TMA into rings, Q by TMA into the A operand, S = Q K^T and O += P V in tensor memory, softmax one
+// thread per row.  The full 128 rows of the MMA are used: at 64 nodes x 6 q heads per kv head an SM
+// does 128 x 64 scores per K tile, so wide trees over long contexts are bound by the tensor core and
+// the softmax, small ones by the K/V stream, short contexts by latency.
 #include <cmath>
 
 #include "xv_internal.h"
@@ -6,6 +30,33 @@
 
 namespace xv {
 namespace {
+
+constexpr int T = ATTN_TILE;
+constexpr float NEG_INF = -INFINITY;
+constexpr float RESCALE_SLACK = 2.f;   // as the decode rows' (log2 units)
+typedef unsigned long long u64;
+
+// Shared-memory plan (offsets from a 1024-byte aligned base), 128-byte swizzle throughout:
+//   Q      CB blocks of [128 rows][64 dims]
+//   P[2]   [128 rows][64 positions] bf16
+//   K ring SK stages of CB blocks of [64 positions][64 dims]; V ring SV stages, the same
+template <int HD>
+struct TreeShape {
+    static constexpr int CB = HD / 64;
+    static constexpr int QBLK = 128 * 128;
+    static constexpr int BLK = T * 128;
+    static constexpr int TILE_BYTES = CB * BLK;
+    static constexpr int SK = HD == 256 ? 2 : 4;
+    static constexpr int SV = SK;
+    static constexpr int P_OFF = CB * QBLK;
+    static constexpr int K_OFF = P_OFF + 2 * QBLK;
+    static constexpr int V_OFF = K_OFF + SK * TILE_BYTES;
+    static constexpr int BAR_OFF = V_OFF + SV * TILE_BYTES;
+    static constexpr int N_BARS = 2 * SK + 2 * SV + 15;
+    static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
+    // columns: S[2] (64 each), O (HD), the tree's scores (64)
+    static constexpr uint32_t TMEM_COLS = HD == 64 ? 256 : 512;
+};
 
 struct TreeArgs {
     const uint16_t* q;
@@ -25,109 +76,932 @@ struct TreeArgs {
     uint16_t* out;
     long long out_stride;
     unsigned* err;
+    int G, NT, nrt, nsplit;   // q heads per kv head; nodes per row tile, row tiles, splits the launch is sized for
+    float* opart;             // [B*N*Hq][nsplit][HD]
+    float2* ml;               // [B*N*Hq][nsplit]
+    int32_t* nsp;             // [B*N] splits of each node's rows
 };
 
-// One CTA per (node, q head): warp w takes visible positions w, w + 8, ...; an online softmax per
-// warp, merged at the end.
-template <int HD>
-__global__ void __launch_bounds__(256) attn_tree_kernel(TreeArgs A) {
-    griddep_launch();
-    griddep_wait();
-    constexpr int E = HD / 32;
-    __shared__ float sm_m[8], sm_l[8], sm_o[8][HD];
-    __shared__ int chain[XV_KMAX];
-    const int h = blockIdx.x % A.Hq, row = blockIdx.x / A.Hq, b = row / A.N, i = row % A.N, g = h / (A.Hq / A.Hkv);
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int n = A.n_nodes ? A.n_nodes[b] : A.N, ctx = A.ctx_len[b];
-    const bool short_ctx = ctx < 0 || ctx > A.max_ctx;
-    if (threadIdx.x == 0 && (n < 0 || n > A.N)) atomicOr(A.err, ERR_BAD_COUNT);
-    if (threadIdx.x == 0 && short_ctx) atomicOr(A.err, ERR_BAD_LENGTH);
-    if (short_ctx || i >= n) return;     // i < N: a count above N is clamped by it
-    int depth = 0;
-    for (int a = i; a >= 0;) {
-        if (threadIdx.x == 0) chain[depth] = a;
-        ++depth;
-        int p = A.parent[static_cast<long long>(b) * A.N + a];
-        if (p < -1 || p >= a) {
-            if (threadIdx.x == 0) atomicOr(A.err, ERR_BAD_TREE);
-            p = -1;
-        }
-        a = p;
-    }
-    __syncthreads();
-    float q[E], o[E], m = -INFINITY, l = 0.f;
+// warps 0-3 softmax and epilogue (thread = row = TMEM lane), 4 K, 5 V, 6 MMA, 7 Q
+constexpr int TREE_THREADS = 256;
+
+struct TreeItem {
+    int b, g, rt, split, ctx, n, p_begin;
+    int nfull;        // whole tiles of cache positions
+    int c;            // cache positions of the tail tile (the tile that holds position ctx)
+    bool tail0, tail1;   // this split holds the tail tile; the tile after it
+    bool live, bad_ctx, bad_n;
+    __device__ __forceinline__ bool tail() const { return tail0 || tail1; }
+    __device__ __forceinline__ int kreg() const { return nfull + (tail0 && c > 0 ? 1 : 0); }      // K tiles of cache positions
+    __device__ __forceinline__ int vreg() const { return nfull + (tail0 && c >= 16 ? 1 : 0); }    // V tiles of them
+    __device__ __forceinline__ int node0(int NT) const { return rt * NT; }
+};
+
+__device__ __forceinline__ TreeItem tree_item(const TreeArgs& A, int it) {
+    TreeItem I;
+    I.split = it % A.nsplit;
+    int rest = it / A.nsplit;
+    I.rt = rest % A.nrt;
+    rest /= A.nrt;
+    I.g = rest % A.Hkv;
+    I.b = rest / A.Hkv;
+    I.ctx = __ldg(A.ctx_len + I.b);
+    const int n = A.n_nodes ? __ldg(A.n_nodes + I.b) : A.N;
+    I.bad_ctx = I.ctx < 0 || I.ctx > A.max_ctx;
+    I.bad_n = n < 0 || n > A.N;
+    I.n = min(max(n, 0), A.N);
+    I.p_begin = attn_split_begin(I.split);
+    const int p_end = attn_split_begin(I.split + 1), t0 = I.ctx & ~(T - 1);
+    I.c = I.ctx - t0;
+    I.nfull = I.p_begin < t0 ? (min(t0, p_end) - I.p_begin) / T : 0;
+    I.tail0 = t0 >= I.p_begin && t0 < p_end;
+    // a node stands in the tile after the tail when its depth is at least T - c
+    I.tail1 = I.n - 1 >= T - I.c && t0 + T >= I.p_begin && t0 + T < p_end;
+    I.live = !I.bad_ctx && I.rt * A.NT < I.n && (I.nfull > 0 || I.tail0 || I.tail1);
+    return I;
+}
+
+// What the rows of one tail item know about their tree; positions are relative to the tail tile.
+struct TreeInfo {
+    u64 anc[XV_KMAX];          // the path from the root: ancestors and the node itself
+    u64 tile0;                 // nodes standing in the tail tile
+    u64 ends;                  // nodes at the last position of a 16-position group
+    u64 vbad;                  // nodes whose V holds a non-finite value (set by the gather)
+    unsigned cbad;             // the same for the cache positions of the blocks' first group
+    uint8_t pos[XV_KMAX];      // c + depth
+    uint8_t rep[XV_KMAX];      // the terminal node whose block holds the node
+    uint8_t idx[XV_KMAX];      // block number of a terminal node
+    uint8_t list[XV_KMAX];     // terminal node of a block: blocks by group, then node
+    uint8_t slot[64];          // gather: node of each slot of the four blocks of a step (255: none)
+    int8_t jump[XV_KMAX];
+    int nb0, nb1;              // blocks of the tail tile, of the tile after it
+};
+
+// Fills the info of an item (one warp, nodes lane and lane + 32).
+__device__ __forceinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane) {
+    constexpr unsigned ALL = 0xffffffffu;
+    int par[2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf16_to_f32(A.q[row * A.q_stride + h * HD + e * 32 + lane]);
-        o[e] = 0.f;
-    }
-    for (int p = w; p < ctx + depth; p += 8) {
-        const uint16_t *kp, *vp;
-        if (p < ctx) {
-            int at = p, pg = b;
-            if (A.kv.table) {
-                pg = A.kv.table[static_cast<long long>(b) * A.kv.max_pages + p / A.kv.page];
-                at = p % A.kv.page;
-                if (pg < 0 || pg >= A.kv.n_pages) {
-                    if (lane == 0) atomicOr(A.err, ERR_BAD_PAGE);
-                    pg = 0;
-                }
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        par[u] = -1;
+        if (i < I.n) {
+            par[u] = __ldg(A.parent + static_cast<long long>(I.b) * A.N + i);
+            if (par[u] < -1 || par[u] >= i) {
+                atomicOr(A.err, ERR_BAD_TREE);
+                par[u] = -1;
             }
-            const long long off = ((static_cast<long long>(pg) * A.Hkv + g) * A.kv.page + at) * HD;
-            kp = A.kc + off;
-            vp = A.vc + off;
-        } else {
-            kp = A.src + (static_cast<long long>(b) * A.N + chain[depth - 1 - (p - ctx)]) * A.src_stride + g * HD;
-            vp = kp + A.Hkv * HD;
         }
-        float s = 0.f;
+        S->anc[i] = 1ull << i;
+        S->jump[i] = static_cast<int8_t>(par[u]);
+    }
+    __syncwarp();
+    for (int span = 1; span < I.n; span <<= 1) {   // pointer doubling
+        u64 a[2];
+        int8_t j[2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += q[e] * bf16_to_f32(kp[e * 32 + lane]);
+        for (int u = 0; u < 2; ++u) {
+            const int i = lane + 32 * u, p = S->jump[i];
+            a[u] = S->anc[i] | (p >= 0 ? S->anc[p] : 0ull);
+            j[u] = p >= 0 ? S->jump[p] : -1;
+        }
+        __syncwarp();
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= A.sl2;
-        const float mn = fmaxf(m, s), al = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(s - mn);
-        l = l * al + pr;
+        for (int u = 0; u < 2; ++u) {
+            S->anc[lane + 32 * u] = a[u];
+            S->jump[lane + 32 * u] = j[u];
+        }
+        __syncwarp();
+    }
+    u64 kid = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * al + pr * bf16_to_f32(vp[e * 32 + lane]);
-        m = mn;
+    for (int u = 0; u < 2; ++u)
+        if (par[u] >= 0) kid |= 1ull << par[u];
+    kid = (static_cast<u64>(__reduce_or_sync(ALL, static_cast<unsigned>(kid >> 32))) << 32) |
+          __reduce_or_sync(ALL, static_cast<unsigned>(kid));
+    int pos[2];
+    bool real[2], last[2], term[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        real[u] = i < I.n;
+        pos[u] = I.c + __popcll(S->anc[i]) - 1;
+        S->pos[i] = static_cast<uint8_t>(pos[u]);
+        last[u] = real[u] && (pos[u] & 15) == 15;
+        term[u] = real[u] && (last[u] || !((kid >> i) & 1));
+    }
+    auto mask = [&](const bool* f) { return (static_cast<u64>(__ballot_sync(ALL, f[1])) << 32) | __ballot_sync(ALL, f[0]); };
+    const u64 terms = mask(term), ends = mask(last);
+    const bool first[2] = {real[0] && pos[0] < T, real[1] && pos[1] < T};
+    const u64 tile0 = mask(first);
+    __syncwarp();
+    // the block of a node: the lowest terminal node at or below it in its group
+    int rep[2] = {0, 0};
+    bool found[2] = {!real[0], !real[1]};
+    for (u64 t = terms; t; t &= t - 1) {
+        const int i = __ffsll(static_cast<long long>(t)) - 1;
+        const u64 a = S->anc[i];
+        const int grp = S->pos[i] >> 4;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (!found[u] && ((a >> (lane + 32 * u)) & 1) && grp == (pos[u] >> 4)) {
+                rep[u] = i;
+                found[u] = true;
+            }
+    }
+    // the blocks this row tile's nodes run through
+    u64 need = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        S->rep[i] = static_cast<uint8_t>(rep[u]);
+        if (real[u] && i >= I.node0(A.NT) && i < I.node0(A.NT) + A.NT) need |= (1ull << rep[u]) | (S->anc[i] & ends);
+    }
+    need = (static_cast<u64>(__reduce_or_sync(ALL, static_cast<unsigned>(need >> 32))) << 32) |
+           __reduce_or_sync(ALL, static_cast<unsigned>(need));
+    int before = 0, nb0 = 0;
+#pragma unroll
+    for (int grp = 0; grp < 8; ++grp) {
+        const bool in[2] = {((need >> lane) & 1) && (pos[0] >> 4) == grp, ((need >> (lane + 32)) & 1) && (pos[1] >> 4) == grp};
+        const u64 gm = mask(in);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (in[u]) {
+                const int i = lane + 32 * u, x = before + __popcll(gm & ((1ull << i) - 1));
+                S->idx[i] = static_cast<uint8_t>(x);
+                S->list[x] = static_cast<uint8_t>(i);
+            }
+        before += __popcll(gm);
+        if (grp == 3) nb0 = before;
     }
     if (lane == 0) {
-        sm_m[w] = m;
-        sm_l[w] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[w][e * 32 + lane] = o[e];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int j = 0; j < 8; ++j) M = fmaxf(M, sm_m[j]);
-    for (int j = 0; j < 8; ++j) L += sm_l[j] > 0.f ? sm_l[j] * exp2f(sm_m[j] - M) : 0.f;
-    for (int d = threadIdx.x; d < HD; d += 256) {
-        float acc = 0.f;
-        for (int j = 0; j < 8; ++j) acc += sm_l[j] > 0.f ? sm_o[j][d] * exp2f(sm_m[j] - M) : 0.f;
-        float y = acc / L;
-        if (A.gate) {
-            const float gt = bf16_to_f32(A.gate[row * A.gate_stride + h * HD + d]);
-            y = bf16_to_f32(f32_to_bf16(y)) / (1.f + expf(-gt));
-        }
-        A.out[row * A.out_stride + h * HD + d] = f32_to_bf16(y);
+        S->tile0 = tile0;
+        S->ends = ends;
+        S->vbad = 0;
+        S->cbad = 0;
+        S->nb0 = nb0;
+        S->nb1 = before - nb0;
     }
 }
+
+// Page of position p of sequence b and the row inside it; an entry outside the pool is recorded and
+// replaced by page 0.
+__device__ __forceinline__ int tree_page(const KvPages& kv, int b, int p, int* row, unsigned* err) {
+    if (!kv.table) {
+        *row = p;
+        return b;
+    }
+    const int j = p / kv.page;
+    *row = p - j * kv.page;
+    int pg = __ldg(kv.table + static_cast<long long>(b) * kv.max_pages + j);
+    if (pg < 0 || pg >= kv.n_pages) {
+        atomicOr(err, ERR_BAD_PAGE);
+        pg = 0;
+    }
+    return pg;
+}
+
+// Zeroes the non-finite bf16 values of a word; true when there was one.
+__device__ __forceinline__ bool drop_non_finite(uint32_t& w) {
+    const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
+    if (lo) w &= 0xFFFF0000u;
+    if (hi) w &= 0x0000FFFFu;
+    return lo || hi;
+}
+
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    tmem_ld_wait();
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld16(taddr + c * 16, s + c * 16);
+    tmem_ld_wait();
+}
+
+// p = exp2(s - m) of 64 scores: packs them as bf16 pairs and adds them to ts in order (the decode
+// rows' operations; a dead tile's p are 0).
+__device__ __forceinline__ void exp_row(const float* s, float m, bool dead, uint32_t* pk, float& ts) {
+#pragma unroll
+    for (int j = 0; j < T; j += 2) {
+        const float a0 = dead ? 0.f : ex2_approx(__fsub_rn(s[j], m));
+        const float a1 = dead ? 0.f : ex2_approx(__fsub_rn(s[j + 1], m));
+        ts = __fadd_rn(__fadd_rn(ts, a0), a1);
+        pk[j / 2] = pack_bf16x2(a0, a1);
+    }
+}
+
+template <int HD, bool MULTI>
+__global__ void __launch_bounds__(TREE_THREADS, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmT, TreeArgs A) {
+    using S = TreeShape<HD>;
+    constexpr int CB = S::CB, SK = S::SK, SV = S::SV, TILE_BYTES = S::TILE_BYTES, BLK = S::BLK, QBLK = S::QBLK;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int s_abort;
+    __shared__ TreeInfo info;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const uint32_t sQ = base, sP = base + S::P_OFF;
+    auto sK = [&](int st) { return base + S::K_OFF + st * TILE_BYTES; };
+    auto sV = [&](int st) { return base + S::V_OFF + st * TILE_BYTES; };
+    const uint32_t bar0 = base + S::BAR_OFF;
+    auto fullK = [&](int st) { return bar0 + 8u * st; };
+    auto emptyK = [&](int st) { return bar0 + 8u * (SK + st); };
+    auto fullV = [&](int st) { return bar0 + 8u * (2 * SK + st); };
+    auto emptyV = [&](int st) { return bar0 + 8u * (2 * SK + SV + st); };
+    const uint32_t bx = bar0 + 8u * (2 * SK + 2 * SV);
+    auto sbar = [&](int j) { return bx + 8u * j; };           // S[j] written
+    auto sfree = [&](int j) { return bx + 8u * (2 + j); };    // S[j] read
+    auto pready = [&](int j) { return bx + 8u * (4 + j); };   // P[j] written (and O rescaled)
+    auto pfree = [&](int j) { return bx + 8u * (6 + j); };    // the P V step of P[j] has completed
+    // once per tail item: the tree's scores written, read; its info filled; its blocks gathered
+    const uint32_t tbar = bx + 8u * 8, tfree = bx + 8u * 9, tready = bx + 8u * 10, vdone = bx + 8u * 11;
+    const uint32_t qfull = bx + 8u * 12, qdone = bx + 8u * 13, done = bx + 8u * 14;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_items = A.nsplit * A.nrt * A.Hkv * A.B;
+    // one CTA per item: blocks take the items split-slowest; persistent CTAs: a contiguous range
+    // numbered split-fastest (consecutive items mostly share Q)
+    const int per_split = n_items / A.nsplit;
+    const int it0 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x) * n_items / gridDim.x)
+                          : (static_cast<int>(blockIdx.x) % per_split) * A.nsplit + static_cast<int>(blockIdx.x) / per_split;
+    const int it1 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * n_items / gridDim.x) : it0 + 1;
+    griddep_wait();
+    int first = it0;
+    while (first < it1 && !tree_item(A, first).live) ++first;
+    if (tid == 0)
+        for (int it = it0; it < it1; ++it) {
+            const TreeItem I = tree_item(A, it);
+            if (I.split == 0 && I.rt == 0 && I.g == 0) {
+                if (I.bad_ctx) atomicOr(A.err, ERR_BAD_LENGTH);
+                if (I.bad_n) atomicOr(A.err, ERR_BAD_COUNT);
+            }
+        }
+    if (first == it1) {
+        griddep_launch();
+        return;   // nothing live here: no barrier or tensor memory was set up
+    }
+    if (tid == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmT);
+        for (int st = 0; st < SK; ++st) {
+            mbar_init(fullK(st), 1);
+            mbar_init(emptyK(st), 1);
+        }
+        for (int st = 0; st < SV; ++st) {
+            mbar_init(fullV(st), 1);
+            mbar_init(emptyV(st), 1);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(sbar(j), 1);
+            mbar_init(sfree(j), 128);
+            mbar_init(pready(j), 128);
+            mbar_init(pfree(j), 1);
+        }
+        mbar_init(tbar, 1);
+        mbar_init(tfree, 128);
+        mbar_init(tready, 1);
+        mbar_init(vdone, 1);
+        mbar_init(qfull, 1);
+        mbar_init(qdone, 1);
+        mbar_init(done, 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == 6) {
+        tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // only now: a dependent kernel must not take the tensor memory this one still has to allocate
+    griddep_launch();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tS = tmem, tO = tmem + 128, tT = tmem + 128 + HD;
+
+    // bounded waits; after the first one that gives up, every later wait returns at once
+    auto W = [&](uint32_t bar, uint32_t par) -> bool {
+        if (s_abort) return false;
+        if (!mbar_wait_sleep(bar, par, A.err)) {
+            s_abort = 1;
+            return false;
+        }
+        return true;
+    };
+    auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
+    auto same_q = [](const TreeItem& x, int b, int g, int rt) { return x.b == b && x.g == g && x.rt == rt; };
+
+    if (warp == 7) {
+        // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before
+        if (lane == 0) {
+            int nq = 0, qb = -1, qg = -1, qrt = -1;
+            for (int it = first; it < it1; ++it) {
+                const TreeItem I = tree_item(A, it);
+                if (!I.live || same_q(I, qb, qg, qrt)) continue;
+                qb = I.b, qg = I.g, qrt = I.rt;
+                if (nq > 0 && !W(qdone, (nq - 1) & 1u)) break;
+                mbar_arrive_expect_tx(qfull, CB * A.NT * A.G * 128);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) tma_load_3d(sQ + cb * QBLK, &tmQ, cb * 64, I.g * A.G, I.b * A.N + I.rt * A.NT, qfull);
+                ++nq;
+            }
+            if (nq > 0) mbar_wait(qfull, (nq - 1) & 1u, A.err);   // every issued copy lands before the CTA may leave
+        }
+    } else if (warp == 4) {
+        // ---- K tiles of the cache, then the tree's
+        if (lane == 0) {
+            int t = 0;
+            bool ok = true;
+            for (int it = first; ok && it < it1; ++it) {
+                const TreeItem I = tree_item(A, it);
+                if (!I.live) continue;
+                const int nreg = I.kreg(), nk = nreg + (I.tail() ? 1 : 0);
+                for (int i = 0; i < nk; ++i) {
+                    const int st = t % SK;
+                    if (t >= SK && !W(emptyK(st), ((t / SK) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(fullK(st), TILE_BYTES);
+                    if (i < nreg) {
+                        int row;
+                        const int z = tree_page(A.kv, I.b, I.p_begin + i * T, &row, A.err) * A.Hkv + I.g;
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb) tma_load_3d(sK(st) + cb * BLK, &tmK, cb * 64, row, z, fullK(st));
+                    } else {
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb) tma_load_2d(sK(st) + cb * BLK, &tmT, I.g * HD + cb * 64, I.b * A.N, fullK(st));
+                    }
+                    ++t;
+                }
+            }
+            for (int j = t > SK ? t - SK : 0; j < t; ++j) mbar_wait(fullK(j % SK), (j / SK) & 1u, A.err);
+        }
+    } else if (warp == 5) {
+        // ---- V tiles of the cache, then the blocks, four to a tile
+        int t = 0, nt = 0;
+        bool ok = true;
+        for (int it = first; ok && it < it1; ++it) {
+            const TreeItem I = tree_item(A, it);
+            if (!I.live) continue;
+            if (lane == 0) {
+                for (int i = 0; i < I.vreg(); ++i) {
+                    const int st = t % SV;
+                    if (t >= SV && !W(emptyV(st), ((t / SV) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(fullV(st), TILE_BYTES);
+                    int row;
+                    const int z = tree_page(A.kv, I.b, I.p_begin + i * T, &row, A.err) * A.Hkv + I.g;
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) tma_load_3d(sV(st) + cb * BLK, &tmV, cb * 64, row, z, fullV(st));
+                    ++t;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            t = __shfl_sync(0xffffffffu, t, 0);
+            if (!ok || !I.tail()) continue;
+            if (!WW(tready, nt & 1u)) break;
+            ++nt;
+            const int t0 = I.ctx - I.c, nb0 = info.nb0, nb1 = info.nb1;
+#pragma unroll 1
+            for (int half = 0; ok && half < 2; ++half) {
+                if (half ? !I.tail1 : !I.tail0) continue;
+                const int x1 = half ? nb0 + nb1 : nb0;
+#pragma unroll 1
+                for (int x0 = half ? nb0 : 0; x0 < x1; x0 += 4, ++t) {
+                    const int st = t % SV, nslot = min(4, x1 - x0) * 16;
+                    if (t >= SV && !WW(emptyV(st), ((t / SV) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    info.slot[lane] = info.slot[lane + 32] = 255;
+                    __syncwarp();
+                    for (int k = 0; k < nslot / 16; ++k) {
+                        const int term = info.list[x0 + k], grp = info.pos[term] >> 4;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int i = lane + 32 * u, p = info.pos[i];
+                            if (((info.anc[term] >> i) & 1) && (p >> 4) == grp) info.slot[k * 16 + (p & 15)] = static_cast<uint8_t>(i);
+                        }
+                    }
+                    __syncwarp();
+                    uint8_t* dst = smem + (sV(st) - base);
+                    constexpr int CH = HD / 8, U = 8;   // 16-byte chunks per row; loads in flight per lane
+                    for (int i0 = lane; i0 < nslot * CH; i0 += 32 * U) {
+                        uint4 v[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int i = i0 + 32 * u, s = i / CH, ch = i % CH;
+                            v[u] = make_uint4(0, 0, 0, 0);
+                            if (i >= nslot * CH) continue;
+                            const int grp = info.pos[info.list[x0 + s / 16]] >> 4, p = grp * 16 + s % 16, node = info.slot[s];
+                            const uint16_t* src = nullptr;
+                            if (p < I.c) {
+                                int row;
+                                const long long z = static_cast<long long>(tree_page(A.kv, I.b, t0 + p, &row, A.err)) * A.Hkv + I.g;
+                                src = A.vc + (z * A.kv.page + row) * HD;
+                            } else if (node != 255) {
+                                src = A.src + (static_cast<long long>(I.b) * A.N + node) * A.src_stride +
+                                      static_cast<long long>(A.Hkv + I.g) * HD;
+                            }
+                            if (src) v[u] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int i = i0 + 32 * u, s = i / CH, ch = i % CH;
+                            if (i >= nslot * CH) continue;
+                            bool bad = drop_non_finite(v[u].x);
+                            bad |= drop_non_finite(v[u].y);
+                            bad |= drop_non_finite(v[u].z);
+                            bad |= drop_non_finite(v[u].w);
+                            if (bad) {
+                                const int node = info.slot[s];
+                                if (node != 255) atomicOr(&info.vbad, 1ull << node);
+                                else atomicOr(&info.cbad, 1u << (s % 16));
+                            }
+                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * BLK + s * 128 + (((ch & 7) ^ (s & 7)) * 16)) = v[u];
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(fullV(st));
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(vdone);
+        }
+        if (lane == 0)
+            for (int j = t > SV ? t - SV : 0; j < t; ++j) mbar_wait(fullV(j % SV), (j / SV) & 1u, A.err);
+    } else if (warp == 6) {
+        // ---- MMA issuer: Q K^T runs one tile ahead of P V inside an item
+        if (lane == 0) {
+            constexpr uint32_t IDS = idesc_bf16_f32(128, T), IDO = idesc_bf16_f32(128, HD, true);
+            constexpr uint32_t VBLK = CB > 1 ? BLK : 1024;   // as in attn.cu: unused with a single block
+            int tk = 0, ts = 0, pv = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1, nb0 = 0, nb1 = 0;
+            bool ok = true;
+            auto mma_qk = [&](uint32_t d) {
+                const int st = tk % SK;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    tc_mma_bf16(d, sw128_kmajor_desc(sQ + (ks >> 2) * QBLK + (ks & 3) * 32),
+                                sw128_kmajor_desc(sK(st) + (ks >> 2) * BLK + (ks & 3) * 32), IDS, ks > 0 ? 1u : 0u);
+            };
+            auto qk = [&](bool tree) -> bool {
+                const int st = tk % SK;
+                if (!W(fullK(st), (tk / SK) & 1u)) return false;
+                if (tree) {
+                    // the block counts are read before the tree's scores are announced: the softmax
+                    // warps wait for those before they may refill the info
+                    if (!W(tready, nt & 1u) || (nt > 0 && !W(tfree, (nt - 1) & 1u))) return false;
+                    nb0 = info.nb0;
+                    nb1 = info.nb1;
+                    ++nt;
+                    mma_qk(tT);
+                    tc_commit(tbar);
+                } else {
+                    if (ts >= 2 && !W(sfree(ts & 1), ((ts - 2) >> 1) & 1u)) return false;
+                    mma_qk(tS + (ts & 1) * T);
+                    tc_commit(sbar(ts & 1));
+                    ++ts;
+                }
+                tc_commit(emptyK(st));
+                ++tk;
+                return true;
+            };
+            int pv0 = 0;   // the item's first P V step
+            auto pvs = [&](int ksteps) -> bool {
+                const int sv = pv % SV;
+                if (!W(pready(pv & 1), (pv >> 1) & 1u) || !W(fullV(sv), (pv / SV) & 1u)) return false;
+                tc_fence_after();
+                for (int kk = 0; kk < ksteps; ++kk)
+                    tc_mma_bf16(tO, sw128_kmajor_desc(sP + (pv & 1) * QBLK + kk * 32),
+                                sw128_mnmajor_desc(sV(sv) + kk * 2048, VBLK, 1024), IDO, (pv > pv0 || kk > 0) ? 1u : 0u);
+                tc_commit(pfree(pv & 1));
+                tc_commit(emptyV(sv));
+                ++pv;
+                return true;
+            };
+            for (int it = first; ok && it < it1; ++it) {
+                const TreeItem I = tree_item(A, it);
+                if (!I.live) continue;
+                if (!same_q(I, qb, qg, qrt)) {
+                    if (nq > 0) tc_commit(qdone);
+                    if (!W(qfull, nq & 1u)) break;
+                    ++nq;
+                    qb = I.b, qg = I.g, qrt = I.rt;
+                }
+                const int nreg = I.kreg(), nqk = nreg + (I.tail() ? 1 : 0);
+                int qi = 0;
+                auto next_qk = [&]() -> bool {
+                    if (qi >= nqk) return true;
+                    return qk(qi++ >= nreg);
+                };
+                pv0 = pv;
+                ok = next_qk();
+                for (int i = 0; ok && i < I.nfull; ++i) ok = next_qk() && pvs(4);
+                while (ok && qi < nqk) ok = next_qk();
+                if (ok && I.tail0 && I.c >= 16) ok = pvs(I.c / 16);
+                for (int x = 0; ok && I.tail0 && x < nb0; x += 4) ok = pvs(min(4, nb0 - x));
+                for (int x = 0; ok && I.tail1 && x < nb1; x += 4) ok = pvs(min(4, nb1 - x));
+            }
+            tc_commit(done);   // every MMA issued is complete before the CTA may leave
+            mbar_wait(done, 0u, A.err);
+        }
+    } else {
+        // ---- softmax and epilogue: thread = row rho of the tile (node rho / G, q head rho % G)
+        const int rho = tid;
+        const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+        uint8_t* prow = smem + S::P_OFF + rho * 128;
+        const int nl = rho / A.G, gh = rho - nl * A.G;
+        int ts = 0, pv = 0, nt = 0;
+        bool ok = true;
+        for (int it = first; ok && it < it1; ++it) {
+            const TreeItem I = tree_item(A, it);
+            if (!I.live) continue;
+            if (warp == 0 && I.tail()) {
+                // every use of the previous tail item's info lies before its epilogue
+                tree_info(&info, A, I, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tready);
+            }
+            const int node = I.node0(A.NT) + nl, pv0 = pv;
+            const bool valid = nl < A.NT && node < I.n;
+            float m = NEG_INF, l = 0.f;
+            // the reference max moves to mx: O (once P V steps have been issued) and l are rescaled
+            auto rescale = [&](float al) -> bool {
+                if (pv == pv0 || !__any_sync(0xffffffffu, al != 1.f)) return true;
+                if (!WW(pfree((pv - 1) & 1), ((pv - 1) >> 1) & 1u)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < HD / 64; ++c) {
+                    float o[64];
+                    tmem_ld64(tO + lane_off + c * 64, o);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) o[e] = __fmul_rn(o[e], al);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) tmem_st16(tO + lane_off + c * 64 + q4 * 16, o + q4 * 16);
+                }
+                tmem_st_wait();
+                return true;
+            };
+            auto pslot = [&]() -> bool { return pv < 2 || WW(pfree(pv & 1), ((pv - 2) >> 1) & 1u); };
+            auto put_p = [&]() {   // this thread's P row is complete
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(pready(pv & 1));
+                ++pv;
+            };
+            auto write_p = [&](const uint32_t* pk) {
+#pragma unroll
+                for (int c = 0; c < T / 8; ++c)
+                    *reinterpret_cast<uint4*>(prow + (pv & 1) * QBLK + ((c ^ (rho & 7)) * 16)) =
+                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            };
+            auto new_max = [&](float mx) { return (m == NEG_INF || mx > __fadd_rn(m, RESCALE_SLACK)) ? mx : m; };
+            for (int i = 0; ok && i < I.nfull; ++i, ++ts) {
+                if (!WW(sbar(ts & 1), (ts >> 1) & 1u)) { ok = false; break; }
+                tc_fence_after();
+                float s[T];
+                tmem_ld64(tS + lane_off + (ts & 1) * T, s);
+                tc_fence_before();
+                mbar_arrive(sfree(ts & 1));
+                float mx = NEG_INF;
+#pragma unroll
+                for (int j = 0; j < T; ++j) {
+                    s[j] = __fmul_rn(s[j], A.sl2);
+                    mx = fmaxf(mx, s[j]);
+                }
+                const float mn = new_max(mx);
+                const bool dead = mn == NEG_INF;
+                const float al = (dead || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn));
+                float sum = 0.f;
+                uint32_t pk[T / 2];
+                exp_row(s, mn, dead, pk, sum);
+                l = __fadd_rn(__fmul_rn(l, al), sum);
+                m = mn;
+                if (!rescale(al) || !pslot()) { ok = false; break; }
+                write_p(pk);
+                put_p();
+            }
+            if (!ok) break;
+            u64 path = 0, in0 = 0;
+            float m0 = NEG_INF;      // the reference max of the tail tile (the rare epilogue's)
+            unsigned cnz = 0;        // cache positions of the first block group whose p is not 0
+            int npos = 0;            // position of the node, relative to the tail tile
+            if (I.tail()) {
+                if (!WW(tready, nt & 1u) || !WW(tbar, nt & 1u)) break;
+                tc_fence_after();
+                path = valid ? info.anc[node] : 0;
+                npos = valid ? info.pos[node] : 0;
+                in0 = info.tile0;
+                // block of the path in each of the 8 groups of the two tiles (255: none)
+                uint32_t blk[2] = {~0u, ~0u};
+                auto set_blk = [&](int grp, int x) {
+                    const int sh = 8 * (grp & 3);
+                    if (grp < 4) blk[0] = (blk[0] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
+                    else blk[1] = (blk[1] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
+                };
+                if (valid) {
+                    for (u64 e = path & info.ends; e; e &= e - 1) {
+                        const int a = __ffsll(static_cast<long long>(e)) - 1;
+                        set_blk(info.pos[a] >> 4, info.idx[a]);
+                    }
+                    set_blk(npos >> 4, info.idx[info.rep[node]]);
+                }
+                __syncwarp();
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (half ? !I.tail1 : !I.tail0) continue;
+                    const u64 mine = half ? path & ~in0 : path & in0;
+                    const bool has_a = !half && I.c > 0;
+                    float s[T];
+                    uint32_t pa[T / 2], pt[T / 2];
+                    float mx = NEG_INF, sum = 0.f;
+                    auto load_a = [&]() {
+                        tmem_ld64(tS + lane_off + (ts & 1) * T, s);
+#pragma unroll
+                        for (int j = 0; j < T; ++j) s[j] = j < I.c && valid ? __fmul_rn(s[j], A.sl2) : NEG_INF;
+                    };
+                    auto load_t = [&]() {
+                        tmem_ld64(tT + lane_off, s);
+#pragma unroll
+                        for (int j = 0; j < T; ++j) s[j] = (mine >> j) & 1 ? __fmul_rn(s[j], A.sl2) : NEG_INF;
+                    };
+                    if (has_a) {
+                        if (!WW(sbar(ts & 1), (ts >> 1) & 1u)) { ok = false; break; }
+                        tc_fence_after();
+                        load_a();
+#pragma unroll
+                        for (int j = 0; j < T; ++j) mx = fmaxf(mx, s[j]);
+                    }
+                    load_t();
+#pragma unroll
+                    for (int j = 0; j < T; ++j) mx = fmaxf(mx, s[j]);
+                    const float mn = new_max(mx);
+                    const bool dead = mn == NEG_INF;
+                    const float al = (dead || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn));
+                    if (has_a) {
+                        load_a();
+                        tc_fence_before();
+                        mbar_arrive(sfree(ts & 1));
+                        ++ts;
+                        exp_row(s, mn, dead, pa, sum);
+                        load_t();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < T / 2; ++j) pa[j] = 0;
+                    }
+                    exp_row(s, mn, dead, pt, sum);
+                    l = __fadd_rn(__fmul_rn(l, al), sum);
+                    m = mn;
+                    if (!half) m0 = mn;
+                    if (!rescale(al)) { ok = false; break; }
+                    if (has_a && I.c >= 16) {
+                        if (!pslot()) { ok = false; break; }
+                        write_p(pa);   // its first c / 16 K steps are used
+                        put_p();
+                    }
+                    // the first group's cache positions, in whose block p stands before the nodes'
+                    uint32_t sh[8];
+                    const int gs = half ? -1 : I.c >> 4;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sh[e] = gs == 0 ? pa[e] : gs == 1 ? pa[8 + e] : gs == 2 ? pa[16 + e] : gs == 3 ? pa[24 + e] : 0u;
+                    if (!half) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) cnz |= ((sh[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((sh[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
+                    }
+                    const int nb = half ? info.nb1 : info.nb0, xb = half ? info.nb0 : 0;
+                    const uint32_t bl = blk[half];
+#pragma unroll 1
+                    for (int x0 = 0; x0 < nb; x0 += 4) {
+                        if (!pslot()) { ok = false; break; }
+                        uint8_t* pr = prow + (pv & 1) * QBLK;
+                        bool here = false;   // one of this row's blocks is among the step's four
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int x = static_cast<int>((bl >> (8 * q)) & 255u) - xb;
+                            here |= ((bl >> (8 * q)) & 255u) != 255u && (x >> 2) == (x0 >> 2);
+                        }
+#pragma unroll
+                        for (int c = 0; c < T / 8; ++c) *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(0, 0, 0, 0);
+                        if (here) {
+                            if (gs >= 0) {
+                                const int x = static_cast<int>((bl >> (8 * gs)) & 255u) - xb;
+                                if ((x >> 2) == (x0 >> 2)) {
+                                    const int c = (x & 3) * 2;
+                                    *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+                                    *reinterpret_cast<uint4*>(pr + (((c + 1) ^ (rho & 7)) * 16)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < T; ++j) {
+                                if ((mine >> j) & 1) {
+                                    const int p = info.pos[j], x = static_cast<int>((bl >> (8 * ((p >> 4) & 3))) & 255u) - xb;
+                                    if ((x >> 2) == (x0 >> 2)) {
+                                        const int sl = (x & 3) * 16 + (p & 15);
+                                        *reinterpret_cast<uint16_t*>(pr + (((sl >> 3) ^ (rho & 7)) * 16) + (sl & 7) * 2) =
+                                            static_cast<uint16_t>(j & 1 ? pt[j / 2] >> 16 : pt[j / 2]);
+                                    }
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        put_p();
+                    }
+                    if (!ok) break;
+                }
+                if (!ok || !WW(vdone, nt & 1u)) break;
+            }
+            // ---- epilogue: m, l and O of the rows that reach into this split
+            const bool live = valid && (!I.tail() || I.ctx - I.c + npos >= I.p_begin);
+            const long long brow = static_cast<long long>(I.b) * A.N + node;
+            if (I.tail0 && valid && I.g == 0 && gh == 0) A.nsp[brow] = attn_split_count(I.ctx - I.c + npos + 1);
+            if (pv > pv0) {
+                if (!WW(pfree((pv - 1) & 1), ((pv - 1) >> 1) & 1u)) break;
+                tc_fence_after();
+                u64 vbad = 0;
+                unsigned cbad = 0;
+                if (I.tail()) {
+                    vbad = info.vbad;
+                    cbad = info.cbad;
+                }
+                const long long idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
+                float* op = A.opart + idx * HD;
+#pragma unroll 1
+                for (int c = 0; c < HD / 64; ++c) {
+                    float o[64];
+                    __syncwarp();
+                    tmem_ld64(tO + lane_off + c * 64, o);
+                    // rare: non-finite V values the gather has left out
+                    for (u64 e = vbad; e; e &= e - 1) {
+                        const int i = __ffsll(static_cast<long long>(e)) - 1;
+                        __syncwarp();
+                        const float s = __fmul_rn(tmem_ld1(tT + lane_off + i), A.sl2);
+                        const bool here0 = (in0 >> i) & 1;
+                        if (((path >> i) & 1) && (here0 ? I.tail0 : I.tail1)) {
+                            const float p = bf16_to_f32(f32_to_bf16(ex2_approx(__fsub_rn(s, here0 ? m0 : m))));
+                            const uint16_t* v = A.src + (static_cast<long long>(I.b) * A.N + i) * A.src_stride +
+                                                static_cast<long long>(A.Hkv + I.g) * HD + c * 64;
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if ((v[k] & 0x7F80) == 0x7F80) o[k] = __fmaf_rn(p, bf16_to_f32(v[k]), o[k]);
+                        }
+                    }
+                    for (unsigned e = cbad; e; e &= e - 1) {
+                        const int i = __ffs(e) - 1, t0 = I.ctx - I.c;
+                        int row;
+                        const long long z = static_cast<long long>(tree_page(A.kv, I.b, t0 + (I.c & ~15) + i, &row, A.err)) * A.Hkv + I.g;
+                        const uint16_t* v = A.vc + (z * A.kv.page + row) * HD + c * 64;
+                        const float p = (cnz >> i) & 1 ? 1.f : 0.f;
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if ((v[k] & 0x7F80) == 0x7F80) o[k] = __fmaf_rn(p, bf16_to_f32(v[k]), o[k]);
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4)
+                            *reinterpret_cast<float4*>(op + c * 64 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (live) A.ml[idx] = make_float2(m, l);
+                tc_fence_before();
+            }
+            if (I.tail()) {
+                mbar_arrive(tfree);
+                ++nt;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 6) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::TMEM_COLS);
+    }
+}
+
+// Combine of a row's splits, the decode rows' operations: w_s = exp2(m_s - M), L += w_s l_s,
+// acc += w_s o_s in split order, out = acc / L (and the output gate).  A thread owns two values of a
+// row and keeps the loads of several splits in flight; every thread of a row forms the few weights
+// itself (the row's m and l come from L1), so nothing is exchanged.
+constexpr int COMB_THREADS = 128;
+
+__global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(TreeArgs A, int hd) {
+    griddep_launch();
+    griddep_wait();
+    const int per = hd / 2, rows = COMB_THREADS / per;
+    const long long row = static_cast<long long>(blockIdx.x) * rows + threadIdx.x / per;
+    if (row >= static_cast<long long>(A.B) * A.N * A.Hq) return;
+    const long long br = row / A.Hq;
+    const int h = static_cast<int>(row - br * A.Hq), b = static_cast<int>(br / A.N), i = static_cast<int>(br - static_cast<long long>(b) * A.N);
+    const int ctx = A.ctx_len[b], n = A.n_nodes ? A.n_nodes[b] : A.N;
+    if (ctx < 0 || ctx > A.max_ctx || i >= n) return;   // reported by the split kernel
+    const int ns = min(A.nsp[br], A.nsplit), d = 2 * (threadIdx.x % per);
+    const float2* ml = A.ml + row * A.nsplit;
+    const float* op = A.opart + row * A.nsplit * hd + d;
+    float M = NEG_INF;
+    for (int s = 0; s < ns; ++s) M = fmaxf(M, ml[s].x);
+    float L = 0.f, a0 = 0.f, a1 = 0.f;
+    constexpr int U = 8;
+    for (int s0 = 0; s0 < ns; s0 += U) {
+        float2 o[U], w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u < ns) {
+                o[u] = *reinterpret_cast<const float2*>(op + static_cast<long long>(s0 + u) * hd);
+                w[u] = ml[s0 + u];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u < ns) {
+                const float x = exp2f(__fsub_rn(w[u].x, M));
+                L = __fadd_rn(L, __fmul_rn(x, w[u].y));
+                a0 = __fadd_rn(a0, __fmul_rn(x, o[u].x));
+                a1 = __fadd_rn(a1, __fmul_rn(x, o[u].y));
+            }
+    }
+    float y0 = __fdiv_rn(a0, L), y1 = __fdiv_rn(a1, L);
+    const long long col = static_cast<long long>(h) * hd + d;
+    if (A.gate) {
+        const uint16_t* gp = A.gate + br * A.gate_stride + col;
+        y0 = __fmul_rn(bf16_to_f32(f32_to_bf16(y0)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(gp[0])))));
+        y1 = __fmul_rn(bf16_to_f32(f32_to_bf16(y1)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(gp[1])))));
+    }
+    uint16_t* out = A.out + br * A.out_stride + col;
+    out[0] = f32_to_bf16(y0);
+    out[1] = f32_to_bf16(y1);
+}
+
+inline size_t r256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 size_t tree_workspace(int B, int N, int Hq, int hd, int max_ctx) {
-    (void)B, (void)N, (void)Hq, (void)hd, (void)max_ctx;
-    return 256;
+    const size_t rows = static_cast<size_t>(B) * N * Hq * attn_split_count(max_ctx + N);
+    return r256(rows * hd * sizeof(float)) + r256(rows * sizeof(float2)) + r256(4ull * B * N);
 }
 
-xv_status tree_launch(TreeArgs a, int hd, cudaStream_t s) {
+template <int HD>
+xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, cudaStream_t s) {
+    using S = TreeShape<HD>;
+    int sms = 0;
+    for (const void* f : {reinterpret_cast<const void*>(attn_tree_kernel<HD, true>), reinterpret_cast<const void*>(attn_tree_kernel<HD, false>)})
+        if (xv_status st = kernel_smem_once(f, S::SMEM, false, "attn_tree: set shared memory size")) return st;
+    if (xv_status st = device_sm_count(&sms)) return st;
+    const long long n_items = static_cast<long long>(a.nsplit) * a.nrt * a.Hkv * a.B;
+    if (n_items > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: %lld work items", n_items);
+    // past two waves of items, persistent CTAs (the rule of the decode rows' launch)
+    const bool multi = n_items > 2ll * sms;
+    trace_pre(s);
+    if (multi) launch_k(attn_tree_kernel<HD, true>, dim3(sms), dim3(TREE_THREADS), S::SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
+    else launch_k(attn_tree_kernel<HD, false>, dim3(static_cast<unsigned>(n_items)), dim3(TREE_THREADS), S::SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
+    return launched("attn_tree_kernel", s, K_ATTN_TREE,
+                    4ll * a.B * a.Hkv * a.max_ctx * HD + 4ll * a.B * a.N * (a.Hq + a.Hkv) * HD + 4ll * a.B * a.N * a.Hq * a.nsplit * (HD + 2));
+}
+
+xv_status tree_launch(TreeArgs a, int hd, void* ws, cudaStream_t s) {
     a.err = device_error_word();
     if (!a.err) return fail(XV_ERR_CUDA, "attn_tree: device error word unavailable");
-    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.N * a.Hq));
+    a.G = a.Hq / a.Hkv;
+    const int fit = 128 / a.G;             // whole nodes a row tile holds
+    a.nrt = ceil_div(a.N, fit);
+    a.NT = ceil_div(a.N, a.nrt);
+    a.nsplit = attn_split_count(a.max_ctx + a.N);
+    const size_t rows = static_cast<size_t>(a.B) * a.N * a.Hq * a.nsplit;
+    a.opart = static_cast<float*>(ws);
+    a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + r256(rows * hd * sizeof(float)));
+    a.nsp = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(a.ml) + r256(rows * sizeof(float2)));
+    CUtensorMap tm[4];
+    const uint64_t u = 2;
+    const uint64_t qd[3] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.B) * a.N};
+    const uint64_t qs[2] = {hd * u, a.q_stride * u};
+    const uint32_t qb[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.NT)};
+    if (xv_status st = encode_tiled(&tm[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
+    const uint64_t kd[3] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(a.kv.page), static_cast<uint64_t>(a.kv.n_pages) * a.Hkv};
+    const uint64_t ks[2] = {hd * u, static_cast<uint64_t>(a.kv.page) * hd * u};
+    const uint32_t kb[3] = {64, static_cast<uint32_t>(T), 1};
+    if (xv_status st = encode_tiled(&tm[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.kc, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
+    if (xv_status st = encode_tiled(&tm[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.vc, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
+    const uint64_t td[2] = {static_cast<uint64_t>(a.Hkv) * hd, static_cast<uint64_t>(a.B) * a.N};
+    const uint64_t tst[1] = {a.src_stride * u};
+    const uint32_t tb[2] = {64, static_cast<uint32_t>(T)};
+    if (xv_status st = encode_tiled(&tm[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.src, td, tst, tb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
+    xv_status st = hd == 256 ? tree_launch_split<256>(tm, a, s) : hd == 128 ? tree_launch_split<128>(tm, a, s) : tree_launch_split<64>(tm, a, s);
+    if (st) return st;
+    const long long nrow = static_cast<long long>(a.B) * a.N * a.Hq;
     trace_pre(s);
-    if (hd == 256) launch_k(attn_tree_kernel<256>, grid, dim3(256), 0, s, a);
-    else if (hd == 128) launch_k(attn_tree_kernel<128>, grid, dim3(256), 0, s, a);
-    else launch_k(attn_tree_kernel<64>, grid, dim3(256), 0, s, a);
-    return launched("attn_tree_kernel", s, K_ATTN_TREE, 4ll * a.B * a.Hkv * a.max_ctx * hd);
+    launch_k(attn_tree_combine_kernel, dim3(ceil_div(nrow, COMB_THREADS / (hd / 2))), dim3(COMB_THREADS), 0, s, a, hd);
+    return launched("attn_tree_combine_kernel", s, K_ATTN_TREE, 4ll * nrow * a.nsplit * (hd + 2) + 2ll * nrow * hd * (a.gate ? 2 : 1));
 }
 
 xv_status tree_checks(const TreeArgs& a, int hd, int Lmax, const void* ws, size_t ws_bytes) {
@@ -169,10 +1043,11 @@ xv_status xv_attn_tree(const uint16_t* q, long long q_stride, const uint16_t* kc
                        const uint16_t* gate, long long gate_stride, uint16_t* out, long long out_stride, void* ws,
                        size_t ws_bytes, xv_stream s) {
     TreeArgs a{q, q_stride, kc, vc, kv_contiguous(B, Lmax), ctx_len, kv_src, src_stride, parent, n_nodes, N, B, Hq, Hkv,
-               max_ctx, scale * 1.4426950408889634f, gate, gate_stride, out, out_stride, nullptr};
+               max_ctx, scale * 1.4426950408889634f, gate, gate_stride, out, out_stride, nullptr, 0, 0, 0, 0, nullptr, nullptr,
+               nullptr};
     if (xv_status st = tree_checks(a, hd, Lmax, ws, ws_bytes)) return st;
     if (static_cast<long long>(B) * Hkv > (1ll << 31)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: cache too large");
-    return tree_launch(a, hd, reinterpret_cast<cudaStream_t>(s));
+    return tree_launch(a, hd, ws, reinterpret_cast<cudaStream_t>(s));
 }
 
 xv_status xv_attn_tree_paged(const uint16_t* q, long long q_stride, const uint16_t* kpool, const uint16_t* vpool,
@@ -184,9 +1059,10 @@ xv_status xv_attn_tree_paged(const uint16_t* q, long long q_stride, const uint16
     int Lmax = 0;
     if (xv_status st = kv_pages_check(pages, Hkv, hd, &kv, &Lmax)) return st;
     TreeArgs a{q, q_stride, kpool, vpool, kv, ctx_len, kv_src, src_stride, parent, n_nodes, N, B, Hq, Hkv,
-               max_ctx, scale * 1.4426950408889634f, gate, gate_stride, out, out_stride, nullptr};
+               max_ctx, scale * 1.4426950408889634f, gate, gate_stride, out, out_stride, nullptr, 0, 0, 0, 0, nullptr, nullptr,
+               nullptr};
     if (xv_status st = tree_checks(a, hd, Lmax, ws, ws_bytes)) return st;
-    return tree_launch(a, hd, reinterpret_cast<cudaStream_t>(s));
+    return tree_launch(a, hd, ws, reinterpret_cast<cudaStream_t>(s));
 }
 
 }  // extern "C"

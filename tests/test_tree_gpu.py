@@ -135,6 +135,122 @@ def test_attention_against_the_formula(xv, hd, Hq, Hkv, N, ctx, kind, gate):
     assert xv.xv_device_check() == 0
 
 
+def decode_bits(xv, proj, kc, vc, ctx, par, b, N, i, Hq, Hkv, hd, gate):
+    """xv_attn_decode_rows for node i of sequence b over a cache that holds its path at ctx.."""
+    path = chain_of(par, i)
+    r = proj.reshape(-1, N, 2 * Hq + 2 * Hkv, hd)[b]
+    L = ctx + len(path)
+    K, V = (np.concatenate([c[b, :, :ctx], r[path, o: o + Hkv].transpose(1, 0, 2)], 1)[None] for c, o in
+            ((kc, 2 * Hq), (vc, 2 * Hq + Hkv)))
+    one = dev(np.ascontiguousarray(proj.reshape(-1, proj.shape[1])[b * N + i][None]))
+    out = torch.empty((1, Hq * hd), dtype=torch.int16, device="cuda")
+    ws = xv.workspace(xv.xv_attn_workspace_size(1, 1, Hq, hd, L))
+    W = proj.shape[1]
+    xv.xv_attn_decode_rows(one, W, dev(K), dev(V), i32([L]), 1, 1, Hq, Hkv, hd, L, L, hd ** -0.5, out, Hq * hd, ws,
+                           gate=one[:, Hq * hd:] if gate else None, gate_stride=W if gate else 0)
+    return out[0]
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,N,ctx,kind,gate", [
+    (256, 24, 4, 16, [2183], "mixed", True), (64, 2, 1, 64, [128, 0, 63], "mixed", False),
+    (64, 6, 2, 64, [15, 16, 17, 448, 470, 512], "star", False), (256, 6, 1, 64, [4090, 4064], "mixed", True),
+    (64, 1, 1, 64, [47, 4095, 500], "chain", False), (256, 4, 4, 31, [6140, 100], "forest", False),
+    (64, 128, 1, 9, [70], "pairs", False), (256, 12, 2, 40, [40, 33], "pairs", True), (64, 4, 2, 64, [30, 1], "wide", False)])
+def test_rows_have_the_bits_of_decode_rows(xv, hd, Hq, Hkv, N, ctx, kind, gate):
+    """Every node's row, at depths that cross 16-position groups, tiles and splits, has the bits of a
+    decode row over a contiguous cache that holds its path."""
+    B = len(ctx)
+    rng = np.random.default_rng(hd + N)
+    trees = [tree(kind, N - 3 * b, rng) for b in range(B)]
+    proj, (kc, vc) = rows(5, B, N, Hq, Hkv, hd, f"b{hd}{Hq}{N}"), cache(5, B, Hkv, max(ctx) + 1, hd, f"b{hd}{Hq}{N}")
+    got = run(xv, dev(proj), dev(kc), dev(vc), ctx, parents(trees, N), i32([len(t) for t in trees]), N, Hq, Hkv, hd, gate=gate)
+    for b, par in enumerate(trees):
+        for i in range(len(par)):
+            one = decode_bits(xv, proj, kc, vc, ctx[b], par, b, N, i, Hq, Hkv, hd, gate)
+            assert same_bits(got[b * N + i], one), f"sequence {b} (ctx {ctx[b]}) node {i}"
+    assert xv.xv_device_check() == 0
+
+
+def test_other_branches_and_garbage_change_nothing(xv):
+    """NaN and infinities in the cache past ctx, and in the K and V of nodes off a row's path, leave
+    the row's bits; rows whose path holds one give what a decode row gives."""
+    hd, Hq, Hkv, N, ctx = 64, 4, 2, 24, 37
+    rng = np.random.default_rng(2)
+    par = tree("mixed", N, rng)
+    proj, (kc, vc) = rows(6, 1, N, Hq, Hkv, hd, "nan"), cache(6, 1, Hkv, 80, hd, "nan")
+    clean = run(xv, dev(proj), dev(kc), dev(vc), [ctx], parents([par], N), None, N, Hq, Hkv, hd)
+    kc[:, :, ctx:], vc[:, :, ctx:] = 0x7FC0, 0x7F80
+    assert same_bits(clean, run(xv, dev(proj), dev(kc), dev(vc), [ctx], parents([par], N), None, N, Hq, Hkv, hd))
+    bad = proj.reshape(N, 2 * Hq + 2 * Hkv, hd).copy()
+    spoiled = [9, 17, 23]
+    bad[9, 2 * Hq + Hkv, 5], bad[17, 2 * Hq + Hkv + 1, 63], bad[23, 2 * Hq, 0] = 0x7F80, 0x7FC0, 0xFF80
+    bad = bad.reshape(N, -1)
+    got = run(xv, dev(bad), dev(kc), dev(vc), [ctx], parents([par], N), None, N, Hq, Hkv, hd)
+    for i in range(N):
+        if not set(chain_of(par, i)) & set(spoiled):
+            assert same_bits(got[i], clean[i]), i
+        else:
+            want = f64(host_u16(decode_bits(xv, bad, kc, vc, ctx, par, 0, N, i, Hq, Hkv, hd, False)))
+            have = f64(host_u16(got[i]))
+            assert np.array_equal(np.isnan(have), np.isnan(want)) and np.array_equal(have[~np.isnan(want)], want[~np.isnan(want)]), i
+    vc[:, :, 33, 7] = 0xFF80      # visible to every row, in the group the tree starts in
+    got = run(xv, dev(proj), dev(kc), dev(vc), [ctx], parents([par], N), None, N, Hq, Hkv, hd)
+    for i in range(N):
+        want = f64(host_u16(decode_bits(xv, proj, kc, vc, ctx, par, 0, N, i, Hq, Hkv, hd, False)))
+        have = f64(host_u16(got[i]))
+        assert np.isneginf(have.reshape(Hq, hd)[:, 7]).all()
+        assert np.array_equal(have, want), i
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,N,page,ctx,kind", [(256, 24, 4, 16, 64, [2183, 640, 64], "mixed"), (64, 6, 2, 64, 128, [500, 1], "wide"),
+                                                       (128, 8, 8, 9, 192, [191, 192, 193, 4100], "pairs")])
+def test_paged_equals_contiguous(xv, hd, Hq, Hkv, N, page, ctx, kind):
+    B, rng = len(ctx), np.random.default_rng(page)
+    trees = [tree(kind, N, rng) for _ in ctx]
+    Lmax = -(-max(ctx) // page) * page
+    mp = Lmax // page
+    proj, (kc, vc) = rows(7, B, N, Hq, Hkv, hd, f"p{hd}"), cache(7, B, Hkv, Lmax, hd, f"p{hd}")
+    n_pages = B * mp + 3
+    table = rng.permutation(n_pages)[: B * mp].reshape(B, mp).astype(np.int32)
+    pools = []
+    for c in (kc, vc):
+        pool = np.zeros((n_pages, Hkv, page, hd), np.uint16)
+        for b in range(B):
+            for j in range(mp):
+                pool[table[b, j]] = c[b, :, j * page:(j + 1) * page]
+        pools.append(dev(pool))
+    X, par = dev(proj), parents(trees, N)
+    want = run(xv, X, dev(kc), dev(vc), ctx, par, None, N, Hq, Hkv, hd)
+    tab, out = dev(table), torch.empty_like(want)
+    xv.xv_attn_tree_paged(X, pools[0], pools[1], xv.kv_pages(tab, page, n_pages), i32(ctx), X[:, 2 * Hq * hd:], par, None, N, B, Hq,
+                          Hkv, hd, max(ctx), hd ** -0.5, out, xv.workspace(xv.xv_attn_tree_workspace_size(B, N, Hq, hd, max(ctx))))
+    assert same_bits(out, want) and xv.xv_device_check() == 0
+
+
+def test_batched_and_persistent_equal_alone(xv):
+    """Mixed lengths and node counts in one call, enough items for persistent CTAs that cross
+    sequences and reload Q between row tiles: every sequence's rows equal its own call's."""
+    hd, Hq, Hkv, N = 256, 24, 4, 64
+    ctx = [20000, 9001, 1, 513, 2183, 0, 64, 4096]
+    rng = np.random.default_rng(5)
+    counts = [64, 40, 64, 1, 64, 22, 0, 63]
+    trees = [tree(["mixed", "wide", "pairs", "chain"][b % 4], n, rng) if n else [] for b, n in enumerate(counts)]
+    B, Lmax = len(ctx), 20000
+    proj, (kc, vc) = rows(8, B, N, Hq, Hkv, hd, "batch"), cache(8, B, Hkv, Lmax, hd, "batch")
+    X, K, V = dev(proj), dev(kc), dev(vc)
+    out = run(xv, X, K, V, ctx, parents(trees, N), i32(counts), N, Hq, Hkv, hd, gate=True, fill=3)
+    for b in range(B):
+        if not counts[b]:
+            continue
+        one = run(xv, X[b * N:(b + 1) * N].contiguous(), K[b:b + 1], V[b:b + 1], [ctx[b]], parents([trees[b]], N), i32([counts[b]]),
+                  N, Hq, Hkv, hd, gate=True, fill=3)
+        assert same_bits(out[b * N:(b + 1) * N], one), f"sequence {b}"
+    check(out, proj, kc, vc, ctx, trees, N, Hq, Hkv, hd, True, "batch", nodes=(0, 13, 39, 62))
+    for _ in range(20):
+        assert same_bits(out, run(xv, X, K, V, ctx, parents(trees, N), i32(counts), N, Hq, Hkv, hd, gate=True, fill=3))
+    assert xv.xv_device_check() == 0
+
+
 def walk(par, tokens, argmax):
     kept = [0]
     while True:
