@@ -52,7 +52,7 @@ struct TreeShape {
     static constexpr int K_OFF = P_OFF + 2 * QBLK;
     static constexpr int V_OFF = K_OFF + SK * TILE_BYTES;
     static constexpr int BAR_OFF = V_OFF + SV * TILE_BYTES;
-    static constexpr int N_BARS = 2 * SK + 2 * SV + 15;
+    static constexpr int N_BARS = 2 * SK + 2 * SV + 16;
     static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
     // columns: S[2] (64 each), O (HD), the tree's scores (64)
     static constexpr uint32_t TMEM_COLS = HD == 64 ? 256 : 512;
@@ -82,7 +82,7 @@ struct TreeArgs {
     int32_t* nsp;             // [B*N] splits of each node's rows
 };
 
-// warps 0-3 softmax and epilogue (thread = row = TMEM lane), 4 K, 5 V, 6 MMA, 7 Q
+// warps 0-3 softmax and epilogue (thread = row = TMEM lane), 4 K, 5 V, 6 MMA, 7 Q; 5 and 7 the gather
 constexpr int TREE_THREADS = 256;
 
 struct TreeItem {
@@ -132,7 +132,6 @@ struct TreeInfo {
     uint8_t rep[XV_KMAX];      // the terminal node whose block holds the node
     uint8_t idx[XV_KMAX];      // block number of a terminal node
     uint8_t list[XV_KMAX];     // terminal node of a block: blocks by group, then node
-    uint8_t slot[64];          // gather: node of each slot of the four blocks of a step (255: none)
     int8_t jump[XV_KMAX];
     int nb0, nb1;              // blocks of the tail tile, of the tile after it
 };
@@ -261,12 +260,69 @@ __device__ __forceinline__ int tree_page(const KvPages& kv, int b, int p, int* r
     return pg;
 }
 
-// Zeroes the non-finite bf16 values of a word; true when there was one.
-__device__ __forceinline__ bool drop_non_finite(uint32_t& w) {
-    const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
-    if (lo) w &= 0xFFFF0000u;
-    if (hi) w &= 0x0000FFFFu;
-    return lo || hi;
+// Whether a pair of bf16 values holds a non-finite one: an exponent field of all ones carries into
+// the sign's place.
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// One gather step: V rows of the blocks x0 .. x0 + nblk - 1 (16 slots each) into a V stage, by one
+// warp.  A lane finds the source rows of slots lane and lane + 32; a row is HD / 8 chunks of 16 bytes
+// through registers (U loads in flight per lane), non-finite values dropped and noted on the way.
+template <int HD>
+__device__ __forceinline__ void gather_blocks(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x0, int nblk, int lane) {
+    constexpr int CH = HD / 8, ROWS = 32 / CH, U = HD == 64 ? 16 : 32;
+    const uint16_t* src[2];
+    int who[2];   // node, or 64 + position of a cache row in its group
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int sl = lane + 32 * u, k = sl >> 4;
+        src[u] = nullptr;
+        who[u] = 0;
+        if (k >= nblk) continue;
+        const int term = S->list[x0 + k], tp = S->pos[term], p = (tp & ~15) + (sl & 15);
+        if (p < I.c) {
+            int row;
+            const long long z = static_cast<long long>(tree_page(A.kv, I.b, I.ctx - I.c + p, &row, A.err)) * A.Hkv + I.g;
+            src[u] = A.vc + (z * A.kv.page + row) * HD;
+            who[u] = 64 + (sl & 15);
+        } else if (p <= tp) {
+            u64 m = S->anc[term];   // the ancestor tp - p steps up: a path's nodes ascend
+            for (int up = tp - p; up > 0; --up) m ^= 1ull << (63 - __clzll(static_cast<long long>(m)));
+            who[u] = 63 - __clzll(static_cast<long long>(m));
+            src[u] = A.src + (static_cast<long long>(I.b) * A.N + who[u]) * A.src_stride + static_cast<long long>(A.Hkv + I.g) * HD;
+        }
+    }
+    const int ch = lane % CH;
+    uint8_t* d = dst + (ch >> 3) * (T * 128);
+#pragma unroll 1
+    for (int s0 = 0; s0 < nblk * 16; s0 += U * ROWS) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * ROWS + lane / CH;   // slot; the same half of the 64 for the whole warp
+            const u64 a = reinterpret_cast<u64>((s0 + u * ROWS) < 32 ? src[0] : src[1]);
+            const u64 q = __shfl_sync(0xffffffffu, a, s & 31);
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (q && s < nblk * 16) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + ch);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * ROWS + lane / CH;
+            const int w = __shfl_sync(0xffffffffu, (s0 + u * ROWS) < 32 ? who[0] : who[1], s & 31);
+            if (non_finite(v[u].x) | non_finite(v[u].y) | non_finite(v[u].z) | non_finite(v[u].w)) {
+                uint32_t* x = reinterpret_cast<uint32_t*>(&v[u]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u;
+                    if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0x0000FFFFu;
+                }
+                if (w < 64) atomicOr(&S->vbad, 1ull << w);
+                else atomicOr(&S->cbad, 1u << (w - 64));
+            }
+            if (s < nblk * 16) *reinterpret_cast<uint4*>(d + s * 128 + (((ch & 7) ^ (s & 7)) * 16)) = v[u];
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
@@ -322,6 +378,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // once per tail item: the tree's scores written, read; its info filled; its blocks gathered
     const uint32_t tbar = bx + 8u * 8, tfree = bx + 8u * 9, tready = bx + 8u * 10, vdone = bx + 8u * 11;
     const uint32_t qfull = bx + 8u * 12, qdone = bx + 8u * 13, done = bx + 8u * 14;
+    // warp 5 has issued a tail item's V tiles: every stage's last use but one is then complete, so warp
+    // 7's waits on the stages are never two phases behind
+    const uint32_t vgo = bx + 8u * 15;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_items = A.nsplit * A.nrt * A.Hkv * A.B;
@@ -368,7 +427,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         mbar_init(tbar, 1);
         mbar_init(tfree, 128);
         mbar_init(tready, 1);
-        mbar_init(vdone, 1);
+        mbar_init(vdone, 2);
+        mbar_init(vgo, 1);
         mbar_init(qfull, 1);
         mbar_init(qdone, 1);
         mbar_init(done, 1);
@@ -399,22 +459,49 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
     auto same_q = [](const TreeItem& x, int b, int g, int rt) { return x.b == b && x.g == g && x.rt == rt; };
 
+    // the block steps of a tail item, the odd or the even ones; t counts the V tiles and steps
+    auto gather = [&](const TreeItem& I, int& t, int odd) -> bool {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            if (half ? !I.tail1 : !I.tail0) continue;
+            const int nb0 = info.nb0, x1 = half ? nb0 + info.nb1 : nb0;
+#pragma unroll 1
+            for (int x0 = half ? nb0 : 0; x0 < x1; x0 += 4, ++t) {
+                if ((t & 1) != odd) continue;
+                const int st = t % SV;
+                if (t >= SV && !WW(emptyV(st), ((t / SV) & 1u) ^ 1u)) return false;
+                gather_blocks<HD>(&info, A, I, smem + (sV(st) - base), x0, min(4, x1 - x0), lane);
+                if (lane == 0) mbar_arrive(fullV(st));
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vdone);
+        return true;
+    };
     if (warp == 7) {
-        // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before
-        if (lane == 0) {
-            int nq = 0, qb = -1, qg = -1, qrt = -1;
-            for (int it = first; it < it1; ++it) {
-                const TreeItem I = tree_item(A, it);
-                if (!I.live || same_q(I, qb, qg, qrt)) continue;
+        // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before, and
+        // the odd block steps
+        int nq = 0, t = 0, nt = 0, qb = -1, qg = -1, qrt = -1;
+        for (int it = first; it < it1; ++it) {
+            const TreeItem I = tree_item(A, it);
+            if (!I.live) continue;
+            if (!same_q(I, qb, qg, qrt)) {
                 qb = I.b, qg = I.g, qrt = I.rt;
-                if (nq > 0 && !W(qdone, (nq - 1) & 1u)) break;
-                mbar_arrive_expect_tx(qfull, CB * A.NT * A.G * 128);
+                if (nq > 0 && !WW(qdone, (nq - 1) & 1u)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(qfull, CB * A.NT * A.G * 128);
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb) tma_load_3d(sQ + cb * QBLK, &tmQ, cb * 64, I.g * A.G, I.b * A.N + I.rt * A.NT, qfull);
+                    for (int cb = 0; cb < CB; ++cb) tma_load_3d(sQ + cb * QBLK, &tmQ, cb * 64, I.g * A.G, I.b * A.N + I.rt * A.NT, qfull);
+                }
                 ++nq;
             }
-            if (nq > 0) mbar_wait(qfull, (nq - 1) & 1u, A.err);   // every issued copy lands before the CTA may leave
+            t += I.vreg();
+            if (!I.tail()) continue;
+            if (!WW(vgo, nt & 1u) || !WW(tready, nt & 1u)) break;
+            ++nt;
+            if (!gather(I, t, 1)) break;
         }
+        if (lane == 0 && nq > 0) mbar_wait(qfull, (nq - 1) & 1u, A.err);   // every issued copy lands before the CTA may leave
     } else if (warp == 4) {
         // ---- K tiles of the cache, then the tree's
         if (lane == 0) {
@@ -446,7 +533,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             for (int j = t > SK ? t - SK : 0; j < t; ++j) mbar_wait(fullK(j % SK), (j / SK) & 1u, A.err);
         }
     } else if (warp == 5) {
-        // ---- V tiles of the cache, then the blocks, four to a tile
+        // ---- V tiles of the cache, then the even block steps (four blocks to a V tile)
         int t = 0, nt = 0;
         bool ok = true;
         for (int it = first; ok && it < it1; ++it) {
@@ -470,75 +557,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             t = __shfl_sync(0xffffffffu, t, 0);
             if (!ok || !I.tail()) continue;
+            if (lane == 0) mbar_arrive(vgo);
             if (!WW(tready, nt & 1u)) break;
             ++nt;
-            const int t0 = I.ctx - I.c, nb0 = info.nb0, nb1 = info.nb1;
-#pragma unroll 1
-            for (int half = 0; ok && half < 2; ++half) {
-                if (half ? !I.tail1 : !I.tail0) continue;
-                const int x1 = half ? nb0 + nb1 : nb0;
-#pragma unroll 1
-                for (int x0 = half ? nb0 : 0; x0 < x1; x0 += 4, ++t) {
-                    const int st = t % SV, nslot = min(4, x1 - x0) * 16;
-                    if (t >= SV && !WW(emptyV(st), ((t / SV) & 1u) ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    info.slot[lane] = info.slot[lane + 32] = 255;
-                    __syncwarp();
-                    for (int k = 0; k < nslot / 16; ++k) {
-                        const int term = info.list[x0 + k], grp = info.pos[term] >> 4;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int i = lane + 32 * u, p = info.pos[i];
-                            if (((info.anc[term] >> i) & 1) && (p >> 4) == grp) info.slot[k * 16 + (p & 15)] = static_cast<uint8_t>(i);
-                        }
-                    }
-                    __syncwarp();
-                    uint8_t* dst = smem + (sV(st) - base);
-                    constexpr int CH = HD / 8, U = 8;   // 16-byte chunks per row; loads in flight per lane
-                    for (int i0 = lane; i0 < nslot * CH; i0 += 32 * U) {
-                        uint4 v[U];
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int i = i0 + 32 * u, s = i / CH, ch = i % CH;
-                            v[u] = make_uint4(0, 0, 0, 0);
-                            if (i >= nslot * CH) continue;
-                            const int grp = info.pos[info.list[x0 + s / 16]] >> 4, p = grp * 16 + s % 16, node = info.slot[s];
-                            const uint16_t* src = nullptr;
-                            if (p < I.c) {
-                                int row;
-                                const long long z = static_cast<long long>(tree_page(A.kv, I.b, t0 + p, &row, A.err)) * A.Hkv + I.g;
-                                src = A.vc + (z * A.kv.page + row) * HD;
-                            } else if (node != 255) {
-                                src = A.src + (static_cast<long long>(I.b) * A.N + node) * A.src_stride +
-                                      static_cast<long long>(A.Hkv + I.g) * HD;
-                            }
-                            if (src) v[u] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
-                        }
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int i = i0 + 32 * u, s = i / CH, ch = i % CH;
-                            if (i >= nslot * CH) continue;
-                            bool bad = drop_non_finite(v[u].x);
-                            bad |= drop_non_finite(v[u].y);
-                            bad |= drop_non_finite(v[u].z);
-                            bad |= drop_non_finite(v[u].w);
-                            if (bad) {
-                                const int node = info.slot[s];
-                                if (node != 255) atomicOr(&info.vbad, 1ull << node);
-                                else atomicOr(&info.cbad, 1u << (s % 16));
-                            }
-                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * BLK + s * 128 + (((ch & 7) ^ (s & 7)) * 16)) = v[u];
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(fullV(st));
-                }
-            }
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(vdone);
+            if (!gather(I, t, 0)) break;
         }
         if (lane == 0)
             for (int j = t > SV ? t - SV : 0; j < t; ++j) mbar_wait(fullV(j % SV), (j / SV) & 1u, A.err);
@@ -807,6 +829,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                             }
 #pragma unroll
                             for (int j = 0; j < T; ++j) {
+                                if (j >= I.n) break;
                                 if ((mine >> j) & 1) {
                                     const int p = info.pos[j], x = static_cast<int>((bl >> (8 * ((p >> 4) & 3))) & 255u) - xb;
                                     if ((x >> 2) == (x0 >> 2)) {
