@@ -38,24 +38,35 @@ typedef unsigned long long u64;
 
 // Shared-memory plan (offsets from a 1024-byte aligned base), 128-byte swizzle throughout:
 //   Q      CB blocks of [128 rows][64 dims]
-//   P[2]   [128 rows][64 positions] bf16
-//   K ring SK stages of CB blocks of [64 positions][64 dims]; V ring SV stages, the same
+//   K ring SK stages of CB blocks of [64 positions][64 dims]; V ring SV stages, the same (SV even)
+//   PB[2]  [128 rows][64 slots] bf16, the P of the block steps; at hd 256 they take the stage of the
+//          tree's K tile, which is done with by then
+//   barriers, hand-over values, tree info
+// P of the cache's tiles goes through tensor memory: at hd 256 the 32 KB it would take here are the
+// third K stage.
+struct TreeInfo;
 template <int HD>
 struct TreeShape {
     static constexpr int CB = HD / 64;
     static constexpr int QBLK = 128 * 128;
     static constexpr int BLK = T * 128;
     static constexpr int TILE_BYTES = CB * BLK;
-    static constexpr int SK = HD == 256 ? 2 : 4;
-    static constexpr int SV = SK;
-    static constexpr int P_OFF = CB * QBLK;
-    static constexpr int K_OFF = P_OFF + 2 * QBLK;
+    static constexpr bool PB_IN_K = HD == 256;
+    static constexpr int SK = HD == 256 ? 3 : 5;
+    static constexpr int SV = HD == 256 ? 2 : 4;
+    static constexpr int K_OFF = CB * QBLK;
     static constexpr int V_OFF = K_OFF + SK * TILE_BYTES;
-    static constexpr int BAR_OFF = V_OFF + SV * TILE_BYTES;
-    static constexpr int N_BARS = 2 * SK + 2 * SV + 16;
-    static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
-    // columns: S[2] (64 each), O (HD), the tree's scores (64)
-    static constexpr uint32_t TMEM_COLS = HD == 64 ? 256 : 512;
+    static constexpr int PB_OFF = V_OFF + SV * TILE_BYTES;
+    static constexpr int BAR_OFF = PB_OFF + (PB_IN_K ? 0 : 2 * QBLK);
+    static constexpr int N_BARS = 2 * SK + 2 * SV + 25;
+    static constexpr int M_OFF = BAR_OFF + 8 * ((N_BARS + 1) / 2 * 2);   // float[128]
+    static constexpr int SUM_OFF = M_OFF + 512;                          // float[2][128]
+    static constexpr int INFO_OFF = SUM_OFF + 1024;
+    // the plan needs its base on a 1024-byte boundary: dynamic shared memory starts on one (it is all
+    // this kernel has); with room to spare a full kilobyte of slack is taken all the same
+    static constexpr int SLACK = HD == 256 ? 0 : 1024;
+    // tensor-memory columns: S[2] (64 each), O (HD), the tree's scores (64), P[2] (32 each)
+    static constexpr uint32_t TMEM_COLS = 512;
 };
 
 struct TreeArgs {
@@ -82,8 +93,9 @@ struct TreeArgs {
     int32_t* nsp;             // [B*N] splits of each node's rows
 };
 
-// warps 0-3 softmax and epilogue (thread = row = TMEM lane), 4 K, 5 V, 6 MMA, 7 Q; 5 and 7 the gather
-constexpr int TREE_THREADS = 256;
+// warps 0-3 softmax of an item's even tiles, tail and epilogue, 4-7 softmax of its odd tiles (thread =
+// row = TMEM lane), 8 K, 9 V, 10 MMA, 11 Q; 9 and 11 the gather
+constexpr int TREE_THREADS = 384;
 
 struct TreeItem {
     int b, g, rt, split, ctx, n, p_begin;
@@ -132,13 +144,13 @@ struct TreeInfo {
     uint8_t rep[XV_KMAX];      // the terminal node whose block holds the node
     uint8_t idx[XV_KMAX];      // block number of a terminal node
     uint8_t list[XV_KMAX];     // terminal node of a block: blocks by group, then node
-    int8_t jump[XV_KMAX];
     int nb0, nb1;              // blocks of the tail tile, of the tile after it
 };
 
 // Fills the info of an item (one warp, nodes lane and lane + 32).
 __device__ __forceinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane) {
     constexpr unsigned ALL = 0xffffffffu;
+    int8_t* jump = reinterpret_cast<int8_t*>(S->list);   // list is filled last
     int par[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -152,7 +164,7 @@ __device__ __forceinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const 
             }
         }
         S->anc[i] = 1ull << i;
-        S->jump[i] = static_cast<int8_t>(par[u]);
+        jump[i] = static_cast<int8_t>(par[u]);
     }
     __syncwarp();
     for (int span = 1; span < I.n; span <<= 1) {   // pointer doubling
@@ -160,15 +172,15 @@ __device__ __forceinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const 
         int8_t j[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int i = lane + 32 * u, p = S->jump[i];
+            const int i = lane + 32 * u, p = jump[i];
             a[u] = S->anc[i] | (p >= 0 ? S->anc[p] : 0ull);
-            j[u] = p >= 0 ? S->jump[p] : -1;
+            j[u] = p >= 0 ? jump[p] : -1;
         }
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             S->anc[lane + 32 * u] = a[u];
-            S->jump[lane + 32 * u] = j[u];
+            jump[lane + 32 * u] = j[u];
         }
         __syncwarp();
     }
@@ -269,7 +281,7 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7F80
 // through registers (U loads in flight per lane), non-finite values dropped and noted on the way.
 template <int HD>
 __device__ __forceinline__ void gather_blocks(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x0, int nblk, int lane) {
-    constexpr int CH = HD / 8, ROWS = 32 / CH, U = HD == 64 ? 16 : 32;
+    constexpr int CH = HD / 8, ROWS = 32 / CH, U = 16;
     const uint16_t* src[2];
     int who[2];   // node, or 64 + position of a cache row in its group
 #pragma unroll
@@ -337,16 +349,123 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* s) {
     tmem_ld_wait();
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[h + e]);
+        tmem_st16(taddr + h, f);
+    }
+    tmem_st_wait();
+}
+// MMA issue.  One thread issues an SM's MMAs, and what it computes for each one bounds the kernel as
+// soon as a tile's MMAs are short: with both 64-bit descriptors put together from addresses per MMA
+// it needed ~150 cycles each (20 a tile at hd 256), three times the tensor core's own time.  So a
+// descriptor's constant upper half stays in the instruction and its lower half (the address / 16, and
+// an MN-major operand's block stride) is one add away from a base formed once per tile, four K steps
+// to an asm statement.
+constexpr uint32_t DESC_HI = (1u << 30) | (1u << 14) | (1024u >> 4);   // 128-byte swizzle, version, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead = 16u) { return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
+
+// D (+)= A B^T over 64 K elements, A and B K-major in shared memory (K steps 32 bytes apart);
+// acc: whether the first of them accumulates.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(DESC_HI)
+        : "memory");
+}
+// One K step (16 positions), A in tensor memory (a row per lane, two K elements per column) or
+// K-major in shared memory, B MN-major.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(DESC_HI)
+        : "memory");
+}
+// The four K steps of a whole tile's P V: P's are 8 columns apart, V's 2048 bytes.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(DESC_HI)
+        : "memory");
+}
+
+// Two fp32 operations in one instruction, each rounded as the single one.
+__device__ __forceinline__ void mul2(float& a, float& b, float x) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Largest of 64 scores (a maximum is exact in any order; NaN are passed over).
+__device__ __forceinline__ float max64(const float* s) {
+    float x[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+    for (int j = 0; j < T; j += 2) x[(j / 2) & 3] = max3(x[(j / 2) & 3], s[j], s[j + 1]);
+    return fmaxf(max3(x[0], x[1], x[2]), x[3]);
+}
+// The running maximum after a tile whose largest score is mx, and what O and l are rescaled by.
+__device__ __forceinline__ float new_max(float m, float mx) { return (m == NEG_INF || mx > __fadd_rn(m, RESCALE_SLACK)) ? mx : m; }
+__device__ __forceinline__ float alpha(float m, float mn) { return (mn == NEG_INF || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn)); }
 // p = exp2(s - m) of 64 scores: packs them as bf16 pairs and adds them to ts in order (the decode
-// rows' operations; a dead tile's p are 0).
-__device__ __forceinline__ void exp_row(const float* s, float m, bool dead, uint32_t* pk, float& ts) {
+// rows' operations; the p of a row that has seen no score yet are 0).
+__device__ __forceinline__ void exp_row(float* s, float m, uint32_t* pk, float& ts) {
+    if (m == NEG_INF) {   // rare: no score, or only NaN, so far
+#pragma unroll
+        for (int j = 0; j < T; ++j) s[j] = NEG_INF;
+        m = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < T; j += 2) {
-        const float a0 = dead ? 0.f : ex2_approx(__fsub_rn(s[j], m));
-        const float a1 = dead ? 0.f : ex2_approx(__fsub_rn(s[j + 1], m));
+        add2(s[j], s[j + 1], -m);
+        const float a0 = ex2_approx(s[j]), a1 = ex2_approx(s[j + 1]);
         ts = __fadd_rn(__fadd_rn(ts, a0), a1);
         pk[j / 2] = pack_bf16x2(a0, a1);
     }
+}
+
+// The rest of a bounded wait whose first test failed; kept out of line, as the waiting code is warm
+// in few places and its space in the instruction cache is not free.
+__device__ __noinline__ bool tree_wait(uint32_t bar, uint32_t par, unsigned* err, volatile int* abort) {
+    if (*abort) return false;
+    if (mbar_wait_sleep(bar, par, err)) return true;
+    *abort = 1;
+    return false;
 }
 
 template <int HD, bool MULTI>
@@ -355,14 +474,16 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmT, TreeArgs A) {
     using S = TreeShape<HD>;
     constexpr int CB = S::CB, SK = S::SK, SV = S::SV, TILE_BYTES = S::TILE_BYTES, BLK = S::BLK, QBLK = S::QBLK;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t tmem_slot;
-    __shared__ volatile int s_abort;
-    __shared__ TreeInfo info;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
-    const uint32_t sQ = base, sP = base + S::P_OFF;
+    TreeInfo& info = *reinterpret_cast<TreeInfo*>(smem + S::INFO_OFF);
+    float* m_sm = reinterpret_cast<float*>(smem + S::M_OFF);         // running maximum after the last tile
+    float* sum_sm = reinterpret_cast<float*>(smem + S::SUM_OFF);     // [2][128] sums of the odd tiles
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::INFO_OFF + sizeof(TreeInfo));
+    volatile int& s_abort = *reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t sQ = base;
     auto sK = [&](int st) { return base + S::K_OFF + st * TILE_BYTES; };
     auto sV = [&](int st) { return base + S::V_OFF + st * TILE_BYTES; };
     const uint32_t bar0 = base + S::BAR_OFF;
@@ -371,16 +492,23 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto fullV = [&](int st) { return bar0 + 8u * (2 * SK + st); };
     auto emptyV = [&](int st) { return bar0 + 8u * (2 * SK + SV + st); };
     const uint32_t bx = bar0 + 8u * (2 * SK + 2 * SV);
+    // by the softmax group j of a cache tile: i & 1 for an item's i-th whole tile, 0 for its tail tile
     auto sbar = [&](int j) { return bx + 8u * j; };           // S[j] written
     auto sfree = [&](int j) { return bx + 8u * (2 + j); };    // S[j] read
     auto pready = [&](int j) { return bx + 8u * (4 + j); };   // P[j] written (and O rescaled)
-    auto pfree = [&](int j) { return bx + 8u * (6 + j); };    // the P V step of P[j] has completed
-    // once per tail item: the tree's scores written, read; its info filled; its blocks gathered
-    const uint32_t tbar = bx + 8u * 8, tfree = bx + 8u * 9, tready = bx + 8u * 10, vdone = bx + 8u * 11;
-    const uint32_t qfull = bx + 8u * 12, qdone = bx + 8u * 13, done = bx + 8u * 14;
-    // warp 5 has issued a tail item's V tiles: every stage's last use but one is then complete, so warp
-    // 7's waits on the stages are never two phases behind
-    const uint32_t vgo = bx + 8u * 15;
+    auto pfree = [&](int j) { return bx + 8u * (6 + j); };    // the tile's P V step has completed
+    auto mpub = [&](int j) { return bx + 8u * (8 + j); };     // the running maximum after the tile is known (to the next tile's group)
+    // by the parity of a block step's number
+    auto bready = [&](int j) { return bx + 8u * (10 + j); };
+    auto bfree = [&](int j) { return bx + 8u * (12 + j); };
+    // once per tail item: the tree's scores written, read; its info filled; its blocks gathered; its
+    // V tiles requested (every stage's last use but one is then complete, so warp 11's waits on the
+    // stages are never two phases behind)
+    const uint32_t tbar = bx + 8u * 14, tfree = bx + 8u * 15, tready = bx + 8u * 16, vdone = bx + 8u * 17, vgo = bx + 8u * 18;
+    const uint32_t qfull = bx + 8u * 19, qdone = bx + 8u * 20, ofree = bx + 8u * 21, done = bx + 8u * 22;
+    // by the parity of group 1's tile: its sum is in shared memory (and its P handed over).  Two of
+    // them, as group 1 may end its next tile before group 0 comes to take this one's sum.
+    auto spub = [&](int j) { return bx + 8u * (23 + j); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_items = A.nsplit * A.nrt * A.Hkv * A.B;
@@ -401,9 +529,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 if (I.bad_n) atomicOr(A.err, ERR_BAD_COUNT);
             }
         }
-    if (first == it1) {
+    if (first == it1 || base - raw > S::SLACK) {
+        if (first != it1 && tid == 0) atomicOr(A.err, ERR_WAIT_TIMEOUT);   // an unaligned base: see SLACK
         griddep_launch();
-        return;   // nothing live here: no barrier or tensor memory was set up
+        return;   // no barrier or tensor memory was set up
     }
     if (tid == 0) {
         tma_prefetch_desc(&tmQ);
@@ -423,6 +552,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             mbar_init(sfree(j), 128);
             mbar_init(pready(j), 128);
             mbar_init(pfree(j), 1);
+            mbar_init(mpub(j), 128);
+            mbar_init(spub(j), 128);
+            mbar_init(bready(j), 128);
+            mbar_init(bfree(j), 1);
         }
         mbar_init(tbar, 1);
         mbar_init(tfree, 128);
@@ -431,12 +564,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         mbar_init(vgo, 1);
         mbar_init(qfull, 1);
         mbar_init(qdone, 1);
+        mbar_init(ofree, 128);
         mbar_init(done, 1);
         fence_mbar_init();
         s_abort = 0;
     }
-    if (warp == 6) {
-        tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
+    if (warp == 10) {
+        tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -444,18 +578,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     tc_fence_after();
     // only now: a dependent kernel must not take the tensor memory this one still has to allocate
     griddep_launch();
-    const uint32_t tmem = tmem_slot;
-    const uint32_t tS = tmem, tO = tmem + 128, tT = tmem + 128 + HD;
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tO = tmem + 128, tT = tmem + 128 + HD, tP = tT + 64;
 
-    // bounded waits; after the first one that gives up, every later wait returns at once
-    auto W = [&](uint32_t bar, uint32_t par) -> bool {
-        if (s_abort) return false;
-        if (!mbar_wait_sleep(bar, par, A.err)) {
-            s_abort = 1;
-            return false;
-        }
-        return true;
-    };
+    // bounded waits; after the first one that gives up, every later one that would have to wait returns at once
+    auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || tree_wait(bar, par, A.err, &s_abort); };
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
     auto same_q = [](const TreeItem& x, int b, int g, int rt) { return x.b == b && x.g == g && x.rt == rt; };
 
@@ -478,7 +605,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         if (lane == 0) mbar_arrive(vdone);
         return true;
     };
-    if (warp == 7) {
+    if (warp == 11) {
         // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before, and
         // the odd block steps
         int nq = 0, t = 0, nt = 0, qb = -1, qg = -1, qrt = -1;
@@ -502,7 +629,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!gather(I, t, 1)) break;
         }
         if (lane == 0 && nq > 0) mbar_wait(qfull, (nq - 1) & 1u, A.err);   // every issued copy lands before the CTA may leave
-    } else if (warp == 4) {
+    } else if (warp == 8) {
         // ---- K tiles of the cache, then the tree's
         if (lane == 0) {
             int t = 0;
@@ -532,7 +659,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             }
             for (int j = t > SK ? t - SK : 0; j < t; ++j) mbar_wait(fullK(j % SK), (j / SK) & 1u, A.err);
         }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         // ---- V tiles of the cache, then the even block steps (four blocks to a V tile)
         int t = 0, nt = 0;
         bool ok = true;
@@ -557,63 +684,97 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             t = __shfl_sync(0xffffffffu, t, 0);
             if (!ok || !I.tail()) continue;
-            if (lane == 0) mbar_arrive(vgo);
             if (!WW(tready, nt & 1u)) break;
+            if (lane == 0) mbar_arrive(vgo);   // after tready: warp 11 has then taken the one before
             ++nt;
             if (!gather(I, t, 0)) break;
         }
         if (lane == 0)
             for (int j = t > SV ? t - SV : 0; j < t; ++j) mbar_wait(fullV(j % SV), (j / SV) & 1u, A.err);
-    } else if (warp == 6) {
-        // ---- MMA issuer: Q K^T runs one tile ahead of P V inside an item
+    } else if (warp == 10) {
+        // ---- MMA issuer: Q K^T runs two tiles ahead of P V (both softmax groups have a tile), from
+        // an item without a tail into the next one's cache tiles
         if (lane == 0) {
             constexpr uint32_t IDS = idesc_bf16_f32(128, T), IDO = idesc_bf16_f32(128, HD, true);
             constexpr uint32_t VBLK = CB > 1 ? BLK : 1024;   // as in attn.cu: unused with a single block
-            int tk = 0, ts = 0, pv = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1, nb0 = 0, nb1 = 0;
-            bool ok = true;
-            auto mma_qk = [&](uint32_t d) {
-                const int st = tk % SK;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < HD / 16; ++ks)
-                    tc_mma_bf16(d, sw128_kmajor_desc(sQ + (ks >> 2) * QBLK + (ks & 3) * 32),
-                                sw128_kmajor_desc(sK(st) + (ks >> 2) * BLK + (ks & 3) * 32), IDS, ks > 0 ? 1u : 0u);
-            };
-            auto qk = [&](bool tree) -> bool {
+            // tk: K tiles; nq_g, np_g: Q K^T and P V steps of group g's tiles; bs: block steps; v: V tiles
+            int tk = 0, nq_0 = 0, nq_1 = 0, np_0 = 0, np_1 = 0, bs = 0, v = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1, nb0 = 0, nb1 = 0;
+            int nitem = 0;
+            bool ok = true, first_pv = true;
+            // Q K^T of a cache tile of group g, or of the tree (g = 2)
+            auto issue_qk = [&](int g) -> bool {
                 const int st = tk % SK;
                 if (!W(fullK(st), (tk / SK) & 1u)) return false;
-                if (tree) {
+                uint32_t d, ready;
+                if (g == 2) {
                     // the block counts are read before the tree's scores are announced: the softmax
                     // warps wait for those before they may refill the info
                     if (!W(tready, nt & 1u) || (nt > 0 && !W(tfree, (nt - 1) & 1u))) return false;
                     nb0 = info.nb0;
                     nb1 = info.nb1;
                     ++nt;
-                    mma_qk(tT);
-                    tc_commit(tbar);
+                    d = tT;
+                    ready = tbar;
                 } else {
-                    if (ts >= 2 && !W(sfree(ts & 1), ((ts - 2) >> 1) & 1u)) return false;
-                    mma_qk(tS + (ts & 1) * T);
-                    tc_commit(sbar(ts & 1));
-                    ++ts;
+                    const int n = g ? nq_1 : nq_0;
+                    if (n > 0 && !W(sfree(g), (n - 1) & 1u)) return false;
+                    if (g) ++nq_1;
+                    else ++nq_0;
+                    d = tS + g * T;
+                    ready = sbar(g);
                 }
-                tc_commit(emptyK(st));
+                tc_fence_after();
+                const uint32_t q = desc_lo(sQ), k = desc_lo(sK(st));
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) mma4_ss(d, q + cb * (QBLK / 16), k + cb * (BLK / 16), IDS, cb > 0 ? 1u : 0u);
+                tc_commit(ready);
+                // at hd 256 the tree's stage goes on as the block steps' P and is freed by their end
+                if (!S::PB_IN_K || g != 2) tc_commit(emptyK(st));
                 ++tk;
                 return true;
             };
-            int pv0 = 0;   // the item's first P V step
-            auto pvs = [&](int ksteps) -> bool {
-                const int sv = pv % SV;
-                if (!W(pready(pv & 1), (pv >> 1) & 1u) || !W(fullV(sv), (pv / SV) & 1u)) return false;
-                tc_fence_after();
-                for (int kk = 0; kk < ksteps; ++kk)
-                    tc_mma_bf16(tO, sw128_kmajor_desc(sP + (pv & 1) * QBLK + kk * 32),
-                                sw128_mnmajor_desc(sV(sv) + kk * 2048, VBLK, 1024), IDO, (pv > pv0 || kk > 0) ? 1u : 0u);
-                tc_commit(pfree(pv & 1));
-                tc_commit(emptyV(sv));
-                ++pv;
+            // an item's first P V step overwrites O: the epilogue of the item before has read it
+            auto begin_pv = [&]() -> bool {
+                if (!first_pv) return true;
+                return nitem == 0 || W(ofree, (nitem - 1) & 1u);
+            };
+            auto pv_tile = [&](int g, int ksteps) -> bool {   // a cache tile's P V (of its first ksteps groups)
+                const int sv = v % SV, n = g ? np_1 : np_0;
+                if (!begin_pv() || !W(pready(g), n & 1u)) return false;
+                if (ksteps > 0) {
+                    if (!W(fullV(sv), (v / SV) & 1u)) return false;
+                    tc_fence_after();
+                    const uint32_t b = desc_lo(sV(sv), VBLK);
+                    if (ksteps == 4) {
+                        mma4_ts(tO, tP + g * 32, b, IDO, first_pv ? 0u : 1u);
+                    } else {
+                        for (int kk = 0; kk < ksteps; ++kk) mma_ts(tO, tP + g * 32 + kk * 8, b + kk * 128, IDO, !first_pv || kk > 0 ? 1u : 0u);
+                    }
+                    first_pv = false;
+                }
+                tc_commit(pfree(g));
+                if (ksteps > 0) {
+                    tc_commit(emptyV(sv));
+                    ++v;
+                }
+                if (g) ++np_1;
+                else ++np_0;
                 return true;
             };
+            auto pv_block = [&](int nblk, uint32_t sPB) -> bool {
+                const int sv = v % SV;
+                if (!begin_pv() || !W(bready(bs & 1), (bs >> 1) & 1u) || !W(fullV(sv), (v / SV) & 1u)) return false;
+                tc_fence_after();
+                const uint32_t a = desc_lo(sPB + (bs & 1) * QBLK), b = desc_lo(sV(sv), VBLK);
+                for (int kk = 0; kk < nblk; ++kk) mma_ss(tO, a + kk * 2, b + kk * 128, IDO, !first_pv || kk > 0 ? 1u : 0u);
+                first_pv = false;
+                tc_commit(bfree(bs & 1));
+                tc_commit(emptyV(sv));
+                ++v;
+                ++bs;
+                return true;
+            };
+            int pre = 0;   // Q K^T of the coming item's tiles already issued
             for (int it = first; ok && it < it1; ++it) {
                 const TreeItem I = tree_item(A, it);
                 if (!I.live) continue;
@@ -624,99 +785,160 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     qb = I.b, qg = I.g, qrt = I.rt;
                 }
                 const int nreg = I.kreg(), nqk = nreg + (I.tail() ? 1 : 0);
-                int qi = 0;
-                auto next_qk = [&]() -> bool {
-                    if (qi >= nqk) return true;
-                    return qk(qi++ >= nreg);
-                };
-                pv0 = pv;
-                ok = next_qk();
-                for (int i = 0; ok && i < I.nfull; ++i) ok = next_qk() && pvs(4);
-                while (ok && qi < nqk) ok = next_qk();
-                if (ok && I.tail0 && I.c >= 16) ok = pvs(I.c / 16);
-                for (int x = 0; ok && I.tail0 && x < nb0; x += 4) ok = pvs(min(4, nb0 - x));
-                for (int x = 0; ok && I.tail1 && x < nb1; x += 4) ok = pvs(min(4, nb1 - x));
+                // Cache tiles of the next item that may be taken ahead: it is the next split of the
+                // same rows.  Two tiles of one group in it may not: the second waits for the first to
+                // be read, which group 0 does only after this item's epilogue.
+                int next_n = 0, next_full = 0;
+                if (MULTI && !I.tail() && it + 1 < it1) {
+                    const TreeItem J = tree_item(A, it + 1);
+                    if (J.live) {
+                        next_full = J.nfull;
+                        next_n = min(J.kreg(), J.nfull >= 2 ? 2 : 1);
+                    }
+                }
+                int qi = pre;   // Q K^T issued: this item's, then the next one's
+                first_pv = true;
+#pragma unroll 1
+                for (int i = 0; ok && i <= nreg; ++i) {
+                    // two tiles ahead of P V; past the last tile whatever is left (the tree's scores)
+#pragma unroll 1
+                    while (ok && qi < min(i + 3, nqk + next_n)) {
+                        const int j = qi < nqk ? qi : qi - nqk;
+                        ok = issue_qk(qi < nqk ? (j >= nreg ? 2 : j < I.nfull ? j & 1 : 0) : j < next_full ? j & 1 : 0);
+                        ++qi;
+                    }
+                    if (ok && i < nreg) ok = pv_tile(i < I.nfull ? i & 1 : 0, i < I.nfull ? 4 : I.c / 16);
+                }
+                pre = qi - nqk;
+                const uint32_t sPB = S::PB_IN_K ? sK((tk + SK - 1) % SK) : base + S::PB_OFF;   // after the tree's K tile
+                for (int x = 0; ok && I.tail0 && x < nb0; x += 4) ok = pv_block(min(4, nb0 - x), sPB);
+                for (int x = 0; ok && I.tail1 && x < nb1; x += 4) ok = pv_block(min(4, nb1 - x), sPB);
+                if (ok && first_pv) ok = begin_pv();
+                ++nitem;
             }
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             mbar_wait(done, 0u, A.err);
         }
     } else {
-        // ---- softmax and epilogue: thread = row rho of the tile (node rho / G, q head rho % G)
-        const int rho = tid;
-        const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-        uint8_t* prow = smem + S::P_OFF + rho * 128;
+        // ---- softmax: thread = row rho of the tile (node rho / G, q head rho % G).  Group 0 (warps
+        // 0-3) takes an item's even tiles, group 1 the odd ones: while one exponentiates, the other
+        // loads and takes its maximum.  The running maximum is handed from tile to tile as soon as it
+        // is known; group 0 keeps l, adding an odd tile's sum when it comes to its own next tile.
+        const int grp = warp >> 2, rho = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int nl = rho / A.G, gh = rho - nl * A.G;
-        int ts = 0, pv = 0, nt = 0;
+        // n: own tiles; n1 (group 0): tiles of group 1 taken; n0 (group 1): tiles of group 0 in the
+        // items before; npub (group 1): maxima taken from group 0
+        int n = 0, n1 = 0, n0 = 0, npub = 0, bs = 0, nt = 0, tk = 0;
         bool ok = true;
+        // O (once a P V step of the item has been issued; `bar` completes with its last) times al
+        auto rescale = [&](float al, bool any_pv, uint32_t bar, uint32_t par) -> bool {
+            if (!any_pv || !__any_sync(0xffffffffu, al != 1.f)) return true;
+            if (!WW(bar, par)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                float o[32];
+                tmem_ld16(tO + lane_off + c * 32, o);
+                tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __fmul_rn(o[e], al);
+                tmem_st16(tO + lane_off + c * 32, o);
+                tmem_st16(tO + lane_off + c * 32 + 16, o + 16);
+            }
+            tmem_st_wait();
+            return true;
+        };
+        // P of the group's tile into tensor memory, once the P V step of its tile before has read it
+        auto put_p = [&](const uint32_t* pk) -> bool {
+            if (n > 0 && !WW(pfree(grp), (n - 1) & 1u)) return false;
+            tc_fence_after();
+            tmem_st32(tP + grp * 32 + lane_off, pk);
+            tc_fence_before();
+            mbar_arrive(pready(grp));
+            return true;
+        };
         for (int it = first; ok && it < it1; ++it) {
             const TreeItem I = tree_item(A, it);
             if (!I.live) continue;
             if (warp == 0 && I.tail()) {
-                // every use of the previous tail item's info lies before its epilogue
+                // the previous tail item's info is no longer read
+                if (nt > 0 && !WW(tfree, (nt - 1) & 1u)) break;
                 tree_info(&info, A, I, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tready);
             }
-            const int node = I.node0(A.NT) + nl, pv0 = pv;
+            const int node = I.node0(A.NT) + nl;
             const bool valid = nl < A.NT && node < I.n;
             float m = NEG_INF, l = 0.f;
-            // the reference max moves to mx: O (once P V steps have been issued) and l are rescaled
-            auto rescale = [&](float al) -> bool {
-                if (pv == pv0 || !__any_sync(0xffffffffu, al != 1.f)) return true;
-                if (!WW(pfree((pv - 1) & 1), ((pv - 1) >> 1) & 1u)) return false;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < HD / 64; ++c) {
-                    float o[64];
-                    tmem_ld64(tO + lane_off + c * 64, o);
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) o[e] = __fmul_rn(o[e], al);
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) tmem_st16(tO + lane_off + c * 64 + q4 * 16, o + q4 * 16);
-                }
-                tmem_st_wait();
+            // group 0: the maximum and, when its own exponentials are done, the sum of the odd tile
+            // before its next one or the item's end
+            float al_odd = 1.f;
+            auto take_max = [&]() -> bool {
+                if (!WW(mpub(1), n1 & 1u)) return false;
+                const float mo = m_sm[rho];
+                al_odd = alpha(m, mo);
+                m = mo;
                 return true;
             };
-            auto pslot = [&]() -> bool { return pv < 2 || WW(pfree(pv & 1), ((pv - 2) >> 1) & 1u); };
-            auto put_p = [&]() {   // this thread's P row is complete
-                fence_proxy_async_smem();
-                tc_fence_before();
-                mbar_arrive(pready(pv & 1));
-                ++pv;
+            auto take_sum = [&]() -> bool {
+                if (!WW(spub(n1 & 1), (n1 >> 1) & 1u)) return false;
+                l = __fadd_rn(__fmul_rn(l, al_odd), sum_sm[(n1 & 1) * 128 + rho]);
+                ++n1;
+                return true;
             };
-            auto write_p = [&](const uint32_t* pk) {
-#pragma unroll
-                for (int c = 0; c < T / 8; ++c)
-                    *reinterpret_cast<uint4*>(prow + (pv & 1) * QBLK + ((c ^ (rho & 7)) * 16)) =
-                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-            };
-            auto new_max = [&](float mx) { return (m == NEG_INF || mx > __fadd_rn(m, RESCALE_SLACK)) ? mx : m; };
-            for (int i = 0; ok && i < I.nfull; ++i, ++ts) {
-                if (!WW(sbar(ts & 1), (ts >> 1) & 1u)) { ok = false; break; }
+#pragma unroll 1
+            for (int i = grp; i < I.nfull; i += 2) {
+                if (!WW(sbar(grp), n & 1u)) { ok = false; break; }
                 tc_fence_after();
                 float s[T];
-                tmem_ld64(tS + lane_off + (ts & 1) * T, s);
+                tmem_ld64(tS + lane_off + grp * T, s);
                 tc_fence_before();
-                mbar_arrive(sfree(ts & 1));
-                float mx = NEG_INF;
+                mbar_arrive(sfree(grp));
 #pragma unroll
-                for (int j = 0; j < T; ++j) {
-                    s[j] = __fmul_rn(s[j], A.sl2);
-                    mx = fmaxf(mx, s[j]);
+                for (int j = 0; j < T; j += 2) mul2(s[j], s[j + 1], A.sl2);
+                const float mx = max64(s);
+                if (grp == 0) {
+                    if (i > 0 && !take_max()) { ok = false; break; }
+                } else {
+                    if (!WW(mpub(0), npub & 1u)) { ok = false; break; }
+                    ++npub;
+                    m = m_sm[rho];
                 }
-                const float mn = new_max(mx);
-                const bool dead = mn == NEG_INF;
-                const float al = (dead || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn));
+                const float mn = new_max(m, mx), al = alpha(m, mn);
+                m = mn;
+                if (grp == 1 || i + 1 < I.nfull) {   // someone takes it
+                    m_sm[rho] = mn;
+                    mbar_arrive(mpub(grp));
+                }
                 float sum = 0.f;
                 uint32_t pk[T / 2];
-                exp_row(s, mn, dead, pk, sum);
-                l = __fadd_rn(__fmul_rn(l, al), sum);
-                m = mn;
-                if (!rescale(al) || !pslot()) { ok = false; break; }
-                write_p(pk);
-                put_p();
+                exp_row(s, mn, pk, sum);
+                if (grp == 0) {
+                    if (i > 0 && !take_sum()) { ok = false; break; }
+                    l = __fadd_rn(__fmul_rn(l, al), sum);
+                } else {
+                    sum_sm[(n & 1) * 128 + rho] = sum;
+                }
+                // the P V step before is the other group's
+                if (!rescale(al, i > 0, pfree(1 - grp), (grp ? n0 + i / 2 : n1 - 1) & 1u) || !put_p(pk)) { ok = false; break; }
+                if (grp == 1) mbar_arrive(spub(n & 1));
+                ++n;
             }
             if (!ok) break;
+            if (grp == 1) {   // tails and epilogues are group 0's
+                n0 += (I.nfull + 1) / 2 + (I.tail0 && I.c > 0 ? 1 : 0);
+                continue;
+            }
+            const bool last_odd = I.nfull > 0 && !(I.nfull & 1);
+            if (last_odd && (!take_max() || !take_sum())) break;
+            // completes with the last P V step of the item's whole tiles
+            const uint32_t last_bar = pfree(last_odd ? 1 : 0), last_par = ((last_odd ? n1 : n) - 1) & 1u;
+            const int tail_st = (tk + I.kreg()) % SK;   // K stage of the tree's tile
+            tk += I.kreg() + (I.tail() ? 1 : 0);
+            uint8_t* prow = smem + (S::PB_IN_K ? S::K_OFF + tail_st * TILE_BYTES : S::PB_OFF) + rho * 128;
+            bool any_pv = I.nfull > 0, any_block = false;
             u64 path = 0, in0 = 0;
             float m0 = NEG_INF;      // the reference max of the tail tile (the rare epilogue's)
             unsigned cnz = 0;        // cache positions of the first block group whose p is not 0
@@ -729,9 +951,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 in0 = info.tile0;
                 // block of the path in each of the 8 groups of the two tiles (255: none)
                 uint32_t blk[2] = {~0u, ~0u};
-                auto set_blk = [&](int grp, int x) {
-                    const int sh = 8 * (grp & 3);
-                    if (grp < 4) blk[0] = (blk[0] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
+                auto set_blk = [&](int g16, int x) {
+                    const int sh = 8 * (g16 & 3);
+                    if (g16 < 4) blk[0] = (blk[0] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
                     else blk[1] = (blk[1] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
                 };
                 if (valid) {
@@ -748,10 +970,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     const u64 mine = half ? path & ~in0 : path & in0;
                     const bool has_a = !half && I.c > 0;
                     float s[T];
-                    uint32_t pa[T / 2], pt[T / 2];
+                    uint32_t pk[T / 2];
                     float mx = NEG_INF, sum = 0.f;
                     auto load_a = [&]() {
-                        tmem_ld64(tS + lane_off + (ts & 1) * T, s);
+                        tmem_ld64(tS + lane_off, s);
 #pragma unroll
                         for (int j = 0; j < T; ++j) s[j] = j < I.c && valid ? __fmul_rn(s[j], A.sl2) : NEG_INF;
                     };
@@ -761,55 +983,46 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         for (int j = 0; j < T; ++j) s[j] = (mine >> j) & 1 ? __fmul_rn(s[j], A.sl2) : NEG_INF;
                     };
                     if (has_a) {
-                        if (!WW(sbar(ts & 1), (ts >> 1) & 1u)) { ok = false; break; }
+                        if (!WW(sbar(0), n & 1u)) { ok = false; break; }
                         tc_fence_after();
                         load_a();
-#pragma unroll
-                        for (int j = 0; j < T; ++j) mx = fmaxf(mx, s[j]);
+                        mx = max64(s);
                     }
                     load_t();
-#pragma unroll
-                    for (int j = 0; j < T; ++j) mx = fmaxf(mx, s[j]);
-                    const float mn = new_max(mx);
-                    const bool dead = mn == NEG_INF;
-                    const float al = (dead || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn));
+                    mx = fmaxf(mx, max64(s));
+                    const float mn = new_max(m, mx), al = alpha(m, mn);
+                    // the last P V step so far: a block step of the tail tile, or a cache tile's
+                    if (!(any_block ? rescale(al, true, bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u)
+                                    : rescale(al, any_pv, last_bar, last_par))) {
+                        ok = false;
+                        break;
+                    }
+                    // the first group's cache positions, in whose block p stands before the nodes'
+                    uint32_t sh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    const int gs = half ? -1 : I.c >> 4;
                     if (has_a) {
                         load_a();
-                        tc_fence_before();
-                        mbar_arrive(sfree(ts & 1));
-                        ++ts;
-                        exp_row(s, mn, dead, pa, sum);
-                        load_t();
-                    } else {
+                        exp_row(s, mn, pk, sum);
 #pragma unroll
-                        for (int j = 0; j < T / 2; ++j) pa[j] = 0;
+                        for (int e = 0; e < 8; ++e) sh[e] = gs == 0 ? pk[e] : gs == 1 ? pk[8 + e] : gs == 2 ? pk[16 + e] : pk[24 + e];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) cnz |= ((sh[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((sh[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
+                        tc_fence_before();
+                        mbar_arrive(sfree(0));
+                        if (!put_p(pk)) { ok = false; break; }   // its first c / 16 K steps are used
+                        ++n;
+                        load_t();
                     }
-                    exp_row(s, mn, dead, pt, sum);
+                    exp_row(s, mn, pk, sum);
                     l = __fadd_rn(__fmul_rn(l, al), sum);
                     m = mn;
                     if (!half) m0 = mn;
-                    if (!rescale(al)) { ok = false; break; }
-                    if (has_a && I.c >= 16) {
-                        if (!pslot()) { ok = false; break; }
-                        write_p(pa);   // its first c / 16 K steps are used
-                        put_p();
-                    }
-                    // the first group's cache positions, in whose block p stands before the nodes'
-                    uint32_t sh[8];
-                    const int gs = half ? -1 : I.c >> 4;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sh[e] = gs == 0 ? pa[e] : gs == 1 ? pa[8 + e] : gs == 2 ? pa[16 + e] : gs == 3 ? pa[24 + e] : 0u;
-                    if (!half) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) cnz |= ((sh[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((sh[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
-                    }
                     const int nb = half ? info.nb1 : info.nb0, xb = half ? info.nb0 : 0;
                     const uint32_t bl = blk[half];
 #pragma unroll 1
-                    for (int x0 = 0; x0 < nb; x0 += 4) {
-                        if (!pslot()) { ok = false; break; }
-                        uint8_t* pr = prow + (pv & 1) * QBLK;
+                    for (int x0 = 0; x0 < nb; x0 += 4, ++bs) {
+                        if (bs >= 2 && !WW(bfree(bs & 1), ((bs - 2) >> 1) & 1u)) { ok = false; break; }
+                        uint8_t* pr = prow + (bs & 1) * QBLK;
                         bool here = false;   // one of this row's blocks is among the step's four
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -835,13 +1048,16 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                                     if ((x >> 2) == (x0 >> 2)) {
                                         const int sl = (x & 3) * 16 + (p & 15);
                                         *reinterpret_cast<uint16_t*>(pr + (((sl >> 3) ^ (rho & 7)) * 16) + (sl & 7) * 2) =
-                                            static_cast<uint16_t>(j & 1 ? pt[j / 2] >> 16 : pt[j / 2]);
+                                            static_cast<uint16_t>(j & 1 ? pk[j / 2] >> 16 : pk[j / 2]);
                                     }
                                 }
                             }
                         }
                         __syncwarp();
-                        put_p();
+                        fence_proxy_async_smem();
+                        tc_fence_before();
+                        mbar_arrive(bready(bs & 1));
+                        any_block = true;
                     }
                     if (!ok) break;
                 }
@@ -851,8 +1067,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             const bool live = valid && (!I.tail() || I.ctx - I.c + npos >= I.p_begin);
             const long long brow = static_cast<long long>(I.b) * A.N + node;
             if (I.tail0 && valid && I.g == 0 && gh == 0) A.nsp[brow] = attn_split_count(I.ctx - I.c + npos + 1);
-            if (pv > pv0) {
-                if (!WW(pfree((pv - 1) & 1), ((pv - 1) >> 1) & 1u)) break;
+            if (any_pv || any_block) {
+                if (!(any_block ? WW(bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u) : WW(last_bar, last_par))) break;
                 tc_fence_after();
                 u64 vbad = 0;
                 unsigned cbad = 0;
@@ -901,15 +1117,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 if (live) A.ml[idx] = make_float2(m, l);
                 tc_fence_before();
             }
+            mbar_arrive(ofree);
             if (I.tail()) {
                 mbar_arrive(tfree);
+                if (S::PB_IN_K && tid == 0) mbar_arrive(emptyK(tail_st));
                 ++nt;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 6) {
+    if (warp == 10) {
         tc_fence_after();
         tmem_dealloc(tmem, S::TMEM_COLS);
     }
@@ -975,19 +1193,25 @@ size_t tree_workspace(int B, int N, int Hq, int hd, int max_ctx) {
 }
 
 template <int HD>
+constexpr int tree_smem() {
+    return TreeShape<HD>::SLACK + TreeShape<HD>::INFO_OFF + static_cast<int>(sizeof(TreeInfo)) + 16;
+}
+static_assert(tree_smem<256>() <= 227 * 1024 && tree_smem<128>() <= 227 * 1024 && tree_smem<64>() <= 227 * 1024, "shared memory");
+
+template <int HD>
 xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, cudaStream_t s) {
-    using S = TreeShape<HD>;
+    constexpr int SMEM = tree_smem<HD>();
     int sms = 0;
     for (const void* f : {reinterpret_cast<const void*>(attn_tree_kernel<HD, true>), reinterpret_cast<const void*>(attn_tree_kernel<HD, false>)})
-        if (xv_status st = kernel_smem_once(f, S::SMEM, false, "attn_tree: set shared memory size")) return st;
+        if (xv_status st = kernel_smem_once(f, SMEM, false, "attn_tree: set shared memory size")) return st;
     if (xv_status st = device_sm_count(&sms)) return st;
     const long long n_items = static_cast<long long>(a.nsplit) * a.nrt * a.Hkv * a.B;
     if (n_items > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: %lld work items", n_items);
     // past two waves of items, persistent CTAs (the rule of the decode rows' launch)
     const bool multi = n_items > 2ll * sms;
     trace_pre(s);
-    if (multi) launch_k(attn_tree_kernel<HD, true>, dim3(sms), dim3(TREE_THREADS), S::SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
-    else launch_k(attn_tree_kernel<HD, false>, dim3(static_cast<unsigned>(n_items)), dim3(TREE_THREADS), S::SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
+    if (multi) launch_k(attn_tree_kernel<HD, true>, dim3(sms), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
+    else launch_k(attn_tree_kernel<HD, false>, dim3(static_cast<unsigned>(n_items)), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
     return launched("attn_tree_kernel", s, K_ATTN_TREE,
                     4ll * a.B * a.Hkv * a.max_ctx * HD + 4ll * a.B * a.N * (a.Hq + a.Hkv) * HD + 4ll * a.B * a.N * a.Hq * a.nsplit * (HD + 2));
 }
