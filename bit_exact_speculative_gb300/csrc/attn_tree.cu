@@ -109,7 +109,9 @@ struct TreeItem {
     __device__ __forceinline__ int node0(int NT) const { return rt * NT; }
 };
 
-__device__ __forceinline__ TreeItem tree_item(const TreeArgs& A, int it) {
+// Out of line, like everything below that runs once per item: the roles' loops share the SM's
+// instruction cache, and the code around them decides how much of it they get.
+__device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
     TreeItem I;
     I.split = it % A.nsplit;
     int rest = it / A.nsplit;
@@ -136,11 +138,11 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs& A, int it) {
 // What the rows of one tail item know about their tree; positions are relative to the tail tile.
 struct TreeInfo {
     u64 anc[XV_KMAX];          // the path from the root: ancestors and the node itself
+    uint8_t pos[XV_KMAX];      // c + depth (16-byte aligned)
     u64 tile0;                 // nodes standing in the tail tile
     u64 ends;                  // nodes at the last position of a 16-position group
     u64 vbad;                  // nodes whose V holds a non-finite value (set by the gather)
     unsigned cbad;             // the same for the cache positions of the blocks' first group
-    uint8_t pos[XV_KMAX];      // c + depth
     uint8_t rep[XV_KMAX];      // the terminal node whose block holds the node
     uint8_t idx[XV_KMAX];      // block number of a terminal node
     uint8_t list[XV_KMAX];     // terminal node of a block: blocks by group, then node
@@ -148,7 +150,7 @@ struct TreeInfo {
 };
 
 // Fills the info of an item (one warp, nodes lane and lane + 32).
-__device__ __forceinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane) {
+__device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane) {
     constexpr unsigned ALL = 0xffffffffu;
     int8_t* jump = reinterpret_cast<int8_t*>(S->list);   // list is filled last
     int par[2];
@@ -231,7 +233,7 @@ __device__ __forceinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const 
     need = (static_cast<u64>(__reduce_or_sync(ALL, static_cast<unsigned>(need >> 32))) << 32) |
            __reduce_or_sync(ALL, static_cast<unsigned>(need));
     int before = 0, nb0 = 0;
-#pragma unroll
+#pragma unroll 1
     for (int grp = 0; grp < 8; ++grp) {
         const bool in[2] = {((need >> lane) & 1) && (pos[0] >> 4) == grp, ((need >> (lane + 32)) & 1) && (pos[1] >> 4) == grp};
         const u64 gm = mask(in);
@@ -280,8 +282,8 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7F80
 // warp.  A lane finds the source rows of slots lane and lane + 32; a row is HD / 8 chunks of 16 bytes
 // through registers (U loads in flight per lane), non-finite values dropped and noted on the way.
 template <int HD>
-__device__ __forceinline__ void gather_blocks(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x0, int nblk, int lane) {
-    constexpr int CH = HD / 8, ROWS = 32 / CH, U = 16;
+__device__ __noinline__ void gather_blocks(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x0, int nblk, int lane) {
+    constexpr int CH = HD / 8, ROWS = 32 / CH, U = 8;
     const uint16_t* src[2];
     int who[2];   // node, or 64 + position of a cache row in its group
 #pragma unroll
@@ -349,6 +351,11 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* s) {
     tmem_ld_wait();
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 #pragma unroll
     for (int h = 0; h < 32; h += 16) {
@@ -459,8 +466,7 @@ __device__ __forceinline__ void exp_row(float* s, float m, uint32_t* pk, float& 
     }
 }
 
-// The rest of a bounded wait whose first test failed; kept out of line, as the waiting code is warm
-// in few places and its space in the instruction cache is not free.
+// The rest of a bounded wait whose first test failed.
 __device__ __noinline__ bool tree_wait(uint32_t bar, uint32_t par, unsigned* err, volatile int* abort) {
     if (*abort) return false;
     if (mbar_wait_sleep(bar, par, err)) return true;
@@ -468,10 +474,46 @@ __device__ __noinline__ bool tree_wait(uint32_t bar, uint32_t par, unsigned* err
     return false;
 }
 
+// Rare: what the non-finite V values left out by the gather add to a row's partial output, p * v
+// each (p is the row's bf16 weight: 0 * inf is a NaN as in the product).  Whole warps; op is the
+// row's partial, null for rows that have none in this split.
+struct TreeBad {
+    u64 path, in0, vbad;
+    unsigned cbad, cnz;
+    float m0, m1;      // reference maxima of the tail tile and of the tile after it
+    uint32_t scores;   // the row's tree scores in tensor memory
+    bool use0, use1;   // which of the two tiles this split holds
+    int b, g, ctx, c, hd;
+    float* op;
+};
+__device__ __noinline__ void tree_add_bad(const TreeArgs& A, const TreeBad& F) {
+    auto add = [&](const uint16_t* v, float p) {
+        for (int k = 0; k < F.hd; ++k)
+            if ((v[k] & 0x7F80) == 0x7F80) F.op[k] = __fmaf_rn(p, bf16_to_f32(v[k]), F.op[k]);
+    };
+    for (u64 e = F.vbad; e; e &= e - 1) {
+        const int i = __ffsll(static_cast<long long>(e)) - 1;
+        __syncwarp();
+        const float s = __fmul_rn(tmem_ld1(F.scores + i), A.sl2);
+        const bool first = (F.in0 >> i) & 1;
+        if (F.op && ((F.path >> i) & 1) && (first ? F.use0 : F.use1))
+            add(A.src + (static_cast<long long>(F.b) * A.N + i) * A.src_stride + static_cast<long long>(A.Hkv + F.g) * F.hd,
+                bf16_to_f32(f32_to_bf16(ex2_approx(__fsub_rn(s, first ? F.m0 : F.m1)))));
+    }
+    for (unsigned e = F.cbad; e; e &= e - 1) {
+        const int i = __ffs(e) - 1;
+        int row;
+        const long long z = static_cast<long long>(tree_page(A.kv, F.b, F.ctx - F.c + (F.c & ~15) + i, &row, A.err)) * A.Hkv + F.g;
+        if (F.op) add(A.vc + (z * A.kv.page + row) * F.hd, (F.cnz >> i) & 1 ? 1.f : 0.f);
+    }
+    __syncwarp();
+}
+
 template <int HD, bool MULTI>
 __global__ void __launch_bounds__(TREE_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmT, TreeArgs A) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmT,
+                     const __grid_constant__ TreeArgs A) {
     using S = TreeShape<HD>;
     constexpr int CB = S::CB, SK = S::SK, SV = S::SV, TILE_BYTES = S::TILE_BYTES, BLK = S::BLK, QBLK = S::QBLK;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -583,6 +625,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 
     // bounded waits; after the first one that gives up, every later one that would have to wait returns at once
     auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || tree_wait(bar, par, A.err, &s_abort); };
+    // a wait for one's own copies or MMAs before leaving: also after an abort
+    auto drain = [&](uint32_t bar, uint32_t par) {
+        int none = 0;
+        if (!mbar_try_wait(bar, par)) tree_wait(bar, par, A.err, &none);
+    };
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
     auto same_q = [](const TreeItem& x, int b, int g, int rt) { return x.b == b && x.g == g && x.rt == rt; };
 
@@ -628,7 +675,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             ++nt;
             if (!gather(I, t, 1)) break;
         }
-        if (lane == 0 && nq > 0) mbar_wait(qfull, (nq - 1) & 1u, A.err);   // every issued copy lands before the CTA may leave
+        if (lane == 0 && nq > 0) drain(qfull, (nq - 1) & 1u);   // every issued copy lands before the CTA may leave
     } else if (warp == 8) {
         // ---- K tiles of the cache, then the tree's
         if (lane == 0) {
@@ -657,7 +704,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     ++t;
                 }
             }
-            for (int j = t > SK ? t - SK : 0; j < t; ++j) mbar_wait(fullK(j % SK), (j / SK) & 1u, A.err);
+            for (int j = t > SK ? t - SK : 0; j < t; ++j) drain(fullK(j % SK), (j / SK) & 1u);
         }
     } else if (warp == 9) {
         // ---- V tiles of the cache, then the even block steps (four blocks to a V tile)
@@ -690,7 +737,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!gather(I, t, 0)) break;
         }
         if (lane == 0)
-            for (int j = t > SV ? t - SV : 0; j < t; ++j) mbar_wait(fullV(j % SV), (j / SV) & 1u, A.err);
+            for (int j = t > SV ? t - SV : 0; j < t; ++j) drain(fullV(j % SV), (j / SV) & 1u);
     } else if (warp == 10) {
         // ---- MMA issuer: Q K^T runs two tiles ahead of P V (both softmax groups have a tile), from
         // an item without a tail into the next one's cache tiles
@@ -817,7 +864,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 ++nitem;
             }
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
-            mbar_wait(done, 0u, A.err);
+            drain(done, 0u);
         }
     } else {
         // ---- softmax: thread = row rho of the tile (node rho / G, q head rho % G).  Group 0 (warps
@@ -969,51 +1016,76 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     if (half ? !I.tail1 : !I.tail0) continue;
                     const u64 mine = half ? path & ~in0 : path & in0;
                     const bool has_a = !half && I.c > 0;
-                    float s[T];
-                    uint32_t pk[T / 2];
+                    const u64 a_mask = has_a && valid ? (1ull << I.c) - 1 : 0ull;
+                    // scores 16 r .. 16 r + 15 of the cache's part of the tile (r < 4) or of the tree
+                    // (r - 4), -inf where this row does not look; 16 at a time in rolled loops, as
+                    // this code runs once per item
+                    float s[16];
+                    auto load16 = [&](int r) {
+                        tmem_ld16((r < 4 ? tS : tT - 64) + lane_off + 16 * r, s);
+                        tmem_ld_wait();
+                        const unsigned in = static_cast<unsigned>((r < 4 ? a_mask >> (16 * r) : mine >> (16 * r - 64))) & 0xFFFFu;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) s[j] = (in >> j) & 1 ? __fmul_rn(s[j], A.sl2) : NEG_INF;
+                    };
                     float mx = NEG_INF, sum = 0.f;
-                    auto load_a = [&]() {
-                        tmem_ld64(tS + lane_off, s);
-#pragma unroll
-                        for (int j = 0; j < T; ++j) s[j] = j < I.c && valid ? __fmul_rn(s[j], A.sl2) : NEG_INF;
-                    };
-                    auto load_t = [&]() {
-                        tmem_ld64(tT + lane_off, s);
-#pragma unroll
-                        for (int j = 0; j < T; ++j) s[j] = (mine >> j) & 1 ? __fmul_rn(s[j], A.sl2) : NEG_INF;
-                    };
                     if (has_a) {
                         if (!WW(sbar(0), n & 1u)) { ok = false; break; }
                         tc_fence_after();
-                        load_a();
-                        mx = max64(s);
                     }
-                    load_t();
-                    mx = fmaxf(mx, max64(s));
+#pragma unroll 1
+                    for (int r = has_a ? 0 : 4; r < 8; ++r) {
+                        load16(r);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) mx = max3(mx, s[j], s[j + 1]);
+                    }
                     const float mn = new_max(m, mx), al = alpha(m, mn);
+                    const bool dead = mn == NEG_INF;
                     // the last P V step so far: a block step of the tail tile, or a cache tile's
                     if (!(any_block ? rescale(al, true, bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u)
                                     : rescale(al, any_pv, last_bar, last_par))) {
                         ok = false;
                         break;
                     }
+                    // p of 16 scores as bf16 pairs (0 where no score has been seen at all)
+                    uint32_t pk[8];
+                    auto exp16 = [&](float& ts) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float a0 = dead ? 0.f : ex2_approx(__fsub_rn(s[j], mn)), a1 = dead ? 0.f : ex2_approx(__fsub_rn(s[j + 1], mn));
+                            ts = __fadd_rn(__fadd_rn(ts, a0), a1);
+                            pk[j / 2] = pack_bf16x2(a0, a1);
+                        }
+                    };
                     // the first group's cache positions, in whose block p stands before the nodes'
                     uint32_t sh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     const int gs = half ? -1 : I.c >> 4;
                     if (has_a) {
-                        load_a();
-                        exp_row(s, mn, pk, sum);
+                        if (n > 0 && !WW(pfree(0), (n - 1) & 1u)) { ok = false; break; }
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int r = has_a ? 0 : 4; r < 8; ++r) {
+                        load16(r);
+                        exp16(sum);
+                        if (r < 4) {
+                            tmem_st8(tP + lane_off + 8 * r, pk);   // its first c / 16 K steps are used
+                            if (r == gs) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) sh[e] = gs == 0 ? pk[e] : gs == 1 ? pk[8 + e] : gs == 2 ? pk[16 + e] : pk[24 + e];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) cnz |= ((sh[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((sh[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
+                                for (int e = 0; e < 8; ++e) {
+                                    sh[e] = pk[e];
+                                    cnz |= ((pk[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((pk[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
+                                }
+                            }
+                        }
+                    }
+                    if (has_a) {
+                        tmem_st_wait();
                         tc_fence_before();
                         mbar_arrive(sfree(0));
-                        if (!put_p(pk)) { ok = false; break; }   // its first c / 16 K steps are used
+                        mbar_arrive(pready(0));
                         ++n;
-                        load_t();
                     }
-                    exp_row(s, mn, pk, sum);
                     l = __fadd_rn(__fmul_rn(l, al), sum);
                     m = mn;
                     if (!half) m0 = mn;
@@ -1031,26 +1103,33 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         }
 #pragma unroll
                         for (int c = 0; c < T / 8; ++c) *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(0, 0, 0, 0);
-                        if (here) {
-                            if (gs >= 0) {
-                                const int x = static_cast<int>((bl >> (8 * gs)) & 255u) - xb;
-                                if ((x >> 2) == (x0 >> 2)) {
-                                    const int c = (x & 3) * 2;
-                                    *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
-                                    *reinterpret_cast<uint4*>(pr + (((c + 1) ^ (rho & 7)) * 16)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
-                                }
+                        if (here && gs >= 0) {
+                            const int x = static_cast<int>((bl >> (8 * gs)) & 255u) - xb;
+                            if ((x >> 2) == (x0 >> 2)) {
+                                const int c = (x & 3) * 2;
+                                *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+                                *reinterpret_cast<uint4*>(pr + (((c + 1) ^ (rho & 7)) * 16)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
                             }
+                        }
+                        if (__any_sync(0xffffffffu, here)) {
+                            float unused = 0.f;
+#pragma unroll 1
+                            for (int r = 4; 16 * (r - 4) < I.n; ++r) {   // the tree's p again, to their slots
+                                load16(r);
+                                exp16(unused);
+                                const uint4 ps = *reinterpret_cast<const uint4*>(info.pos + 16 * (r - 4));
+                                const uint32_t pw[4] = {ps.x, ps.y, ps.z, ps.w};
+                                const unsigned in = here ? static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu : 0u;
 #pragma unroll
-                            for (int j = 0; j < T; ++j) {
-                                if (j >= I.n) break;
-                                if ((mine >> j) & 1) {
-                                    const int p = info.pos[j], x = static_cast<int>((bl >> (8 * ((p >> 4) & 3))) & 255u) - xb;
-                                    if ((x >> 2) == (x0 >> 2)) {
+                                for (int j = 0; j < 16; ++j) {
+                                    const int p = (pw[j / 4] >> (8 * (j & 3))) & 255, x = static_cast<int>((bl >> (8 * ((p >> 4) & 3))) & 255u) - xb;
+                                    if (((in >> j) & 1) && (x >> 2) == (x0 >> 2)) {
                                         const int sl = (x & 3) * 16 + (p & 15);
                                         *reinterpret_cast<uint16_t*>(pr + (((sl >> 3) ^ (rho & 7)) * 16) + (sl & 7) * 2) =
                                             static_cast<uint16_t>(j & 1 ? pk[j / 2] >> 16 : pk[j / 2]);
                                     }
                                 }
+                                __syncwarp();
                             }
                         }
                         __syncwarp();
@@ -1079,40 +1158,23 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 const long long idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
                 float* op = A.opart + idx * HD;
 #pragma unroll 1
-                for (int c = 0; c < HD / 64; ++c) {
-                    float o[64];
+                for (int c = 0; c < HD / 32; ++c) {
+                    float o[32];
                     __syncwarp();
-                    tmem_ld64(tO + lane_off + c * 64, o);
-                    // rare: non-finite V values the gather has left out
-                    for (u64 e = vbad; e; e &= e - 1) {
-                        const int i = __ffsll(static_cast<long long>(e)) - 1;
-                        __syncwarp();
-                        const float s = __fmul_rn(tmem_ld1(tT + lane_off + i), A.sl2);
-                        const bool here0 = (in0 >> i) & 1;
-                        if (((path >> i) & 1) && (here0 ? I.tail0 : I.tail1)) {
-                            const float p = bf16_to_f32(f32_to_bf16(ex2_approx(__fsub_rn(s, here0 ? m0 : m))));
-                            const uint16_t* v = A.src + (static_cast<long long>(I.b) * A.N + i) * A.src_stride +
-                                                static_cast<long long>(A.Hkv + I.g) * HD + c * 64;
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if ((v[k] & 0x7F80) == 0x7F80) o[k] = __fmaf_rn(p, bf16_to_f32(v[k]), o[k]);
-                        }
-                    }
-                    for (unsigned e = cbad; e; e &= e - 1) {
-                        const int i = __ffs(e) - 1, t0 = I.ctx - I.c;
-                        int row;
-                        const long long z = static_cast<long long>(tree_page(A.kv, I.b, t0 + (I.c & ~15) + i, &row, A.err)) * A.Hkv + I.g;
-                        const uint16_t* v = A.vc + (z * A.kv.page + row) * HD + c * 64;
-                        const float p = (cnz >> i) & 1 ? 1.f : 0.f;
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if ((v[k] & 0x7F80) == 0x7F80) o[k] = __fmaf_rn(p, bf16_to_f32(v[k]), o[k]);
-                    }
+                    tmem_ld16(tO + lane_off + c * 32, o);
+                    tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
+                    tmem_ld_wait();
                     if (live) {
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4)
-                            *reinterpret_cast<float4*>(op + c * 64 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(op + c * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
+                }
+                if (vbad || cbad) {
+                    __syncwarp();
+                    const TreeBad F{path, in0, vbad, cbad, cnz, m0, m, tT + lane_off, I.tail0, I.tail1, I.b, I.g, I.ctx, I.c, HD,
+                                    live ? op : nullptr};
+                    tree_add_bad(A, F);
                 }
                 if (live) A.ml[idx] = make_float2(m, l);
                 tc_fence_before();
