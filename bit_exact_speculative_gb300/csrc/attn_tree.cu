@@ -58,7 +58,7 @@ struct TreeShape {
     static constexpr int V_OFF = K_OFF + SK * TILE_BYTES;
     static constexpr int PB_OFF = V_OFF + SV * TILE_BYTES;
     static constexpr int BAR_OFF = PB_OFF + (PB_IN_K ? 0 : 2 * QBLK);
-    static constexpr int N_BARS = 2 * SK + 2 * SV + 25;
+    static constexpr int N_BARS = 2 * SK + 2 * SV + 28;
     static constexpr int M_OFF = BAR_OFF + 8 * ((N_BARS + 1) / 2 * 2);   // float[128]
     static constexpr int SUM_OFF = M_OFF + 512;                          // float[2][128]
     static constexpr int INFO_OFF = SUM_OFF + 1024;
@@ -94,8 +94,8 @@ struct TreeArgs {
 };
 
 // warps 0-3 softmax of an item's even tiles, tail and epilogue, 4-7 softmax of its odd tiles (thread =
-// row = TMEM lane), 8 K, 9 V, 10 MMA, 11 Q; 9 and 11 the gather
-constexpr int TREE_THREADS = 384;
+// row = TMEM lane), 8 K, 9 V, 10 Q K^T, 11 Q, 12 P V; 9 and 11 the gather
+constexpr int TREE_THREADS = 416;
 
 struct TreeItem {
     int b, g, rt, split, ctx, n, p_begin;
@@ -538,7 +538,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto sbar = [&](int j) { return bx + 8u * j; };           // S[j] written
     auto sfree = [&](int j) { return bx + 8u * (2 + j); };    // S[j] read
     auto pready = [&](int j) { return bx + 8u * (4 + j); };   // P[j] written (and O rescaled)
-    auto pfree = [&](int j) { return bx + 8u * (6 + j); };    // the tile's P V step has completed
+    // the P V step of group j's tile n has completed: two barriers per group, as a wait may come while
+    // the tile before is still on its way
+    auto pfree = [&](int j, int n) { return bx + 8u * (j ? 25 + (n & 1) : (n & 1) ? 6 : 7); };
     auto mpub = [&](int j) { return bx + 8u * (8 + j); };     // the running maximum after the tile is known (to the next tile's group)
     // by the parity of a block step's number
     auto bready = [&](int j) { return bx + 8u * (10 + j); };
@@ -551,6 +553,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // by the parity of group 1's tile: its sum is in shared memory (and its P handed over).  Two of
     // them, as group 1 may end its next tile before group 0 comes to take this one's sum.
     auto spub = [&](int j) { return bx + 8u * (23 + j); };
+    const uint32_t done2 = bx + 8u * 27;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_items = A.nsplit * A.nrt * A.Hkv * A.B;
@@ -593,14 +596,15 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             mbar_init(sbar(j), 1);
             mbar_init(sfree(j), 128);
             mbar_init(pready(j), 128);
-            mbar_init(pfree(j), 1);
+            mbar_init(pfree(0, j), 1);
+            mbar_init(pfree(1, j), 1);
             mbar_init(mpub(j), 128);
             mbar_init(spub(j), 128);
             mbar_init(bready(j), 128);
             mbar_init(bfree(j), 1);
         }
         mbar_init(tbar, 1);
-        mbar_init(tfree, 128);
+        mbar_init(tfree, 129);
         mbar_init(tready, 1);
         mbar_init(vdone, 2);
         mbar_init(vgo, 1);
@@ -608,6 +612,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         mbar_init(qdone, 1);
         mbar_init(ofree, 128);
         mbar_init(done, 1);
+        mbar_init(done2, 1);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -739,89 +744,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         if (lane == 0)
             for (int j = t > SV ? t - SV : 0; j < t; ++j) drain(fullV(j % SV), (j / SV) & 1u);
     } else if (warp == 10) {
-        // ---- MMA issuer: Q K^T runs two tiles ahead of P V (both softmax groups have a tile), from
-        // an item without a tail into the next one's cache tiles
+        // ---- Q K^T, as far ahead as the two score buffers allow.  It and P V are issued by a warp each:
+        // a tile's barrier tests and commits take an issuer ~1000 cycles beside the ~1000 of its MMAs,
+        // and with one issuer for both the tensor core stood idle meanwhile.
         if (lane == 0) {
-            constexpr uint32_t IDS = idesc_bf16_f32(128, T), IDO = idesc_bf16_f32(128, HD, true);
-            constexpr uint32_t VBLK = CB > 1 ? BLK : 1024;   // as in attn.cu: unused with a single block
-            // tk: K tiles; nq_g, np_g: Q K^T and P V steps of group g's tiles; bs: block steps; v: V tiles
-            int tk = 0, nq_0 = 0, nq_1 = 0, np_0 = 0, np_1 = 0, bs = 0, v = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1, nb0 = 0, nb1 = 0;
-            int nitem = 0;
-            bool ok = true, first_pv = true;
-            // Q K^T of a cache tile of group g, or of the tree (g = 2)
-            auto issue_qk = [&](int g) -> bool {
-                const int st = tk % SK;
-                if (!W(fullK(st), (tk / SK) & 1u)) return false;
-                uint32_t d, ready;
-                if (g == 2) {
-                    // the block counts are read before the tree's scores are announced: the softmax
-                    // warps wait for those before they may refill the info
-                    if (!W(tready, nt & 1u) || (nt > 0 && !W(tfree, (nt - 1) & 1u))) return false;
-                    nb0 = info.nb0;
-                    nb1 = info.nb1;
-                    ++nt;
-                    d = tT;
-                    ready = tbar;
-                } else {
-                    const int n = g ? nq_1 : nq_0;
-                    if (n > 0 && !W(sfree(g), (n - 1) & 1u)) return false;
-                    if (g) ++nq_1;
-                    else ++nq_0;
-                    d = tS + g * T;
-                    ready = sbar(g);
-                }
-                tc_fence_after();
-                const uint32_t q = desc_lo(sQ), k = desc_lo(sK(st));
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) mma4_ss(d, q + cb * (QBLK / 16), k + cb * (BLK / 16), IDS, cb > 0 ? 1u : 0u);
-                tc_commit(ready);
-                // at hd 256 the tree's stage goes on as the block steps' P and is freed by their end
-                if (!S::PB_IN_K || g != 2) tc_commit(emptyK(st));
-                ++tk;
-                return true;
-            };
-            // an item's first P V step overwrites O: the epilogue of the item before has read it
-            auto begin_pv = [&]() -> bool {
-                if (!first_pv) return true;
-                return nitem == 0 || W(ofree, (nitem - 1) & 1u);
-            };
-            auto pv_tile = [&](int g, int ksteps) -> bool {   // a cache tile's P V (of its first ksteps groups)
-                const int sv = v % SV, n = g ? np_1 : np_0;
-                if (!begin_pv() || !W(pready(g), n & 1u)) return false;
-                if (ksteps > 0) {
-                    if (!W(fullV(sv), (v / SV) & 1u)) return false;
-                    tc_fence_after();
-                    const uint32_t b = desc_lo(sV(sv), VBLK);
-                    if (ksteps == 4) {
-                        mma4_ts(tO, tP + g * 32, b, IDO, first_pv ? 0u : 1u);
-                    } else {
-                        for (int kk = 0; kk < ksteps; ++kk) mma_ts(tO, tP + g * 32 + kk * 8, b + kk * 128, IDO, !first_pv || kk > 0 ? 1u : 0u);
-                    }
-                    first_pv = false;
-                }
-                tc_commit(pfree(g));
-                if (ksteps > 0) {
-                    tc_commit(emptyV(sv));
-                    ++v;
-                }
-                if (g) ++np_1;
-                else ++np_0;
-                return true;
-            };
-            auto pv_block = [&](int nblk, uint32_t sPB) -> bool {
-                const int sv = v % SV;
-                if (!begin_pv() || !W(bready(bs & 1), (bs >> 1) & 1u) || !W(fullV(sv), (v / SV) & 1u)) return false;
-                tc_fence_after();
-                const uint32_t a = desc_lo(sPB + (bs & 1) * QBLK), b = desc_lo(sV(sv), VBLK);
-                for (int kk = 0; kk < nblk; ++kk) mma_ss(tO, a + kk * 2, b + kk * 128, IDO, !first_pv || kk > 0 ? 1u : 0u);
-                first_pv = false;
-                tc_commit(bfree(bs & 1));
-                tc_commit(emptyV(sv));
-                ++v;
-                ++bs;
-                return true;
-            };
-            int pre = 0;   // Q K^T of the coming item's tiles already issued
+            constexpr uint32_t IDS = idesc_bf16_f32(128, T);
+            int tk = 0, n0 = 0, n1 = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1;
+            bool ok = true;
             for (int it = first; ok && it < it1; ++it) {
                 const TreeItem I = tree_item(A, it);
                 if (!I.live) continue;
@@ -832,39 +761,109 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     qb = I.b, qg = I.g, qrt = I.rt;
                 }
                 const int nreg = I.kreg(), nqk = nreg + (I.tail() ? 1 : 0);
-                // Cache tiles of the next item that may be taken ahead: it is the next split of the
-                // same rows.  Two tiles of one group in it may not: the second waits for the first to
-                // be read, which group 0 does only after this item's epilogue.
-                int next_n = 0, next_full = 0;
-                if (MULTI && !I.tail() && it + 1 < it1) {
-                    const TreeItem J = tree_item(A, it + 1);
-                    if (J.live) {
-                        next_full = J.nfull;
-                        next_n = min(J.kreg(), J.nfull >= 2 ? 2 : 1);
-                    }
-                }
-                int qi = pre;   // Q K^T issued: this item's, then the next one's
-                first_pv = true;
 #pragma unroll 1
-                for (int i = 0; ok && i <= nreg; ++i) {
-                    // two tiles ahead of P V; past the last tile whatever is left (the tree's scores)
-#pragma unroll 1
-                    while (ok && qi < min(i + 3, nqk + next_n)) {
-                        const int j = qi < nqk ? qi : qi - nqk;
-                        ok = issue_qk(qi < nqk ? (j >= nreg ? 2 : j < I.nfull ? j & 1 : 0) : j < next_full ? j & 1 : 0);
-                        ++qi;
+                for (int i = 0; i < nqk; ++i) {
+                    const int st = tk % SK;
+                    ok = W(fullK(st), (tk / SK) & 1u);
+                    uint32_t d, ready;
+                    if (i >= nreg) {   // the tree's scores
+                        ok = ok && (nt == 0 || W(tfree, (nt - 1) & 1u));
+                        ++nt;
+                        d = tT;
+                        ready = tbar;
+                    } else {
+                        const bool odd = i < I.nfull && (i & 1);
+                        const int n = odd ? n1++ : n0++;
+                        ok = ok && (n == 0 || W(sfree(odd), (n - 1) & 1u));
+                        d = tS + (odd ? T : 0);
+                        ready = sbar(odd);
                     }
-                    if (ok && i < nreg) ok = pv_tile(i < I.nfull ? i & 1 : 0, i < I.nfull ? 4 : I.c / 16);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t q = desc_lo(sQ), k = desc_lo(sK(st));
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) mma4_ss(d, q + cb * (QBLK / 16), k + cb * (BLK / 16), IDS, cb > 0 ? 1u : 0u);
+                    tc_commit(ready);
+                    // at hd 256 the tree's stage goes on as the block steps' P and is freed by their end
+                    if (!S::PB_IN_K || i < nreg) tc_commit(emptyK(st));
+                    ++tk;
                 }
-                pre = qi - nqk;
-                const uint32_t sPB = S::PB_IN_K ? sK((tk + SK - 1) % SK) : base + S::PB_OFF;   // after the tree's K tile
-                for (int x = 0; ok && I.tail0 && x < nb0; x += 4) ok = pv_block(min(4, nb0 - x), sPB);
-                for (int x = 0; ok && I.tail1 && x < nb1; x += 4) ok = pv_block(min(4, nb1 - x), sPB);
-                if (ok && first_pv) ok = begin_pv();
-                ++nitem;
             }
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             drain(done, 0u);
+        }
+    } else if (warp == 12) {
+        // ---- P V
+        if (lane == 0) {
+            constexpr uint32_t IDO = idesc_bf16_f32(128, HD, true);
+            constexpr uint32_t VBLK = CB > 1 ? BLK : 1024;   // as in attn.cu: unused with a single block
+            // tk: K tiles; np_g: steps of group g's tiles; bs: block steps; v: V tiles; nitem: items with a step
+            int tk = 0, np_0 = 0, np_1 = 0, bs = 0, v = 0, nt = 0, nitem = 0;
+            bool ok = true;
+            for (int it = first; ok && it < it1; ++it) {
+                const TreeItem I = tree_item(A, it);
+                if (!I.live) continue;
+                const int nreg = I.kreg();
+                bool first_pv = true;
+                // an item's first step overwrites O: the epilogue before it has read it
+                auto begin_pv = [&]() -> bool { return !first_pv || nitem == 0 || W(ofree, (nitem - 1) & 1u); };
+#pragma unroll 1
+                for (int i = 0; i < nreg; ++i) {
+                    const bool odd = i < I.nfull && (i & 1);
+                    const int ksteps = i < I.nfull ? 4 : I.c / 16, sv = v % SV, n = odd ? np_1++ : np_0++;
+                    ok = begin_pv() && W(pready(odd), n & 1u) && (ksteps == 0 || W(fullV(sv), (v / SV) & 1u));
+                    if (!ok) break;
+                    if (ksteps > 0) {
+                        tc_fence_after();
+                        const uint32_t b = desc_lo(sV(sv), VBLK), p = tP + (odd ? 32 : 0);
+                        if (ksteps == 4) {
+                            mma4_ts(tO, p, b, IDO, first_pv ? 0u : 1u);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk < ksteps; ++kk) mma_ts(tO, p + kk * 8, b + kk * 128, IDO, !first_pv || kk > 0 ? 1u : 0u);
+                        }
+                        first_pv = false;
+                    }
+                    tc_commit(pfree(odd, n));
+                    if (ksteps > 0) {
+                        tc_commit(emptyV(sv));
+                        ++v;
+                    }
+                }
+                tk += nreg;
+                if (ok && I.tail()) {
+                    if (!W(tready, nt & 1u)) break;
+                    const int nb0 = I.tail0 ? info.nb0 : 0, nb1 = I.tail1 ? info.nb1 : 0;
+                    mbar_arrive(tfree);   // the info is not read here any more
+                    ++nt;
+                    const uint32_t sPB = S::PB_IN_K ? sK(tk % SK) : base + S::PB_OFF;   // the tree's K stage
+                    ++tk;
+#pragma unroll 1
+                    for (int x = 0, left = nb0; ok && (left > 0 || x < 1); ) {
+                        if (left <= 0) {   // the tile after the tail
+                            ++x;
+                            left = nb1;
+                            continue;
+                        }
+                        const int sv = v % SV, nblk = min(4, left);
+                        ok = begin_pv() && W(bready(bs & 1), (bs >> 1) & 1u) && W(fullV(sv), (v / SV) & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a = desc_lo(sPB + (bs & 1) * QBLK), b = desc_lo(sV(sv), VBLK);
+#pragma unroll 1
+                        for (int kk = 0; kk < nblk; ++kk) mma_ss(tO, a + kk * 2, b + kk * 128, IDO, !first_pv || kk > 0 ? 1u : 0u);
+                        first_pv = false;
+                        tc_commit(bfree(bs & 1));
+                        tc_commit(emptyV(sv));
+                        ++v;
+                        ++bs;
+                        left -= 4;
+                    }
+                }
+                if (!first_pv) ++nitem;
+            }
+            tc_commit(done2);
+            drain(done2, 0u);
         }
     } else {
         // ---- softmax: thread = row rho of the tile (node rho / G, q head rho % G).  Group 0 (warps
@@ -899,7 +898,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         };
         // P of the group's tile into tensor memory, once the P V step of its tile before has read it
         auto put_p = [&](const uint32_t* pk) -> bool {
-            if (n > 0 && !WW(pfree(grp), (n - 1) & 1u)) return false;
+            if (n > 0 && !WW(pfree(grp, n - 1), ((n - 1) >> 1) & 1u)) return false;
             tc_fence_after();
             tmem_st32(tP + grp * 32 + lane_off, pk);
             tc_fence_before();
@@ -969,7 +968,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     sum_sm[(n & 1) * 128 + rho] = sum;
                 }
                 // the P V step before is the other group's
-                if (!rescale(al, i > 0, pfree(1 - grp), (grp ? n0 + i / 2 : n1 - 1) & 1u) || !put_p(pk)) { ok = false; break; }
+                const int before = grp ? n0 + i / 2 : n1 - 1;
+                if (!rescale(al, i > 0, pfree(1 - grp, before), (before >> 1) & 1u) || !put_p(pk)) { ok = false; break; }
                 if (grp == 1) mbar_arrive(spub(n & 1));
                 ++n;
             }
@@ -981,7 +981,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             const bool last_odd = I.nfull > 0 && !(I.nfull & 1);
             if (last_odd && (!take_max() || !take_sum())) break;
             // completes with the last P V step of the item's whole tiles
-            const uint32_t last_bar = pfree(last_odd ? 1 : 0), last_par = ((last_odd ? n1 : n) - 1) & 1u;
+            const int last = (last_odd ? n1 : n) - 1;
+            const uint32_t last_bar = pfree(last_odd, last), last_par = (last >> 1) & 1u;
             const int tail_st = (tk + I.kreg()) % SK;   // K stage of the tree's tile
             tk += I.kreg() + (I.tail() ? 1 : 0);
             uint8_t* prow = smem + (S::PB_IN_K ? S::K_OFF + tail_st * TILE_BYTES : S::PB_OFF) + rho * 128;
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     uint32_t sh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     const int gs = half ? -1 : I.c >> 4;
                     if (has_a) {
-                        if (n > 0 && !WW(pfree(0), (n - 1) & 1u)) { ok = false; break; }
+                        if (n > 0 && !WW(pfree(0, n - 1), ((n - 1) >> 1) & 1u)) { ok = false; break; }
                         tc_fence_after();
                     }
 #pragma unroll 1
@@ -1178,8 +1179,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 }
                 if (live) A.ml[idx] = make_float2(m, l);
                 tc_fence_before();
+                mbar_arrive(ofree);
             }
-            mbar_arrive(ofree);
             if (I.tail()) {
                 mbar_arrive(tfree);
                 if (S::PB_IN_K && tid == 0) mbar_arrive(emptyK(tail_st));
