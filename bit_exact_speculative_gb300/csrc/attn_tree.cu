@@ -94,7 +94,7 @@ struct TreeArgs {
 };
 
 // warps 0-3 softmax of an item's even tiles, tail and epilogue, 4-7 softmax of its odd tiles (thread =
-// row = TMEM lane), 8 K, 9 V, 10 Q K^T, 11 Q, 12 P V; 9 and 11 the gather
+// row = TMEM lane) and the gather, 8 K, 9 V, 10 Q K^T, 11 Q and the tree's info, 12 P V
 constexpr int TREE_THREADS = 416;
 
 struct TreeItem {
@@ -278,65 +278,52 @@ __device__ __forceinline__ int tree_page(const KvPages& kv, int b, int p, int* r
 // the sign's place.
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
-// One gather step: V rows of the blocks x0 .. x0 + nblk - 1 (16 slots each) into a V stage, by one
-// warp.  A lane finds the source rows of slots lane and lane + 32; a row is HD / 8 chunks of 16 bytes
-// through registers (U loads in flight per lane), non-finite values dropped and noted on the way.
+// Gathers the V rows of block x (16 slots) into its quarter of a V stage, by one warp.  A lane finds
+// the source row of slot lane % 16; a row is HD / 8 chunks of 16 bytes, all of a lane's loads in
+// flight together; non-finite values are dropped and noted on the way.
 template <int HD>
-__device__ __noinline__ void gather_blocks(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x0, int nblk, int lane) {
-    constexpr int CH = HD / 8, ROWS = 32 / CH, U = 8;
-    const uint16_t* src[2];
-    int who[2];   // node, or 64 + position of a cache row in its group
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int sl = lane + 32 * u, k = sl >> 4;
-        src[u] = nullptr;
-        who[u] = 0;
-        if (k >= nblk) continue;
-        const int term = S->list[x0 + k], tp = S->pos[term], p = (tp & ~15) + (sl & 15);
-        if (p < I.c) {
-            int row;
-            const long long z = static_cast<long long>(tree_page(A.kv, I.b, I.ctx - I.c + p, &row, A.err)) * A.Hkv + I.g;
-            src[u] = A.vc + (z * A.kv.page + row) * HD;
-            who[u] = 64 + (sl & 15);
-        } else if (p <= tp) {
-            u64 m = S->anc[term];   // the ancestor tp - p steps up: a path's nodes ascend
-            for (int up = tp - p; up > 0; --up) m ^= 1ull << (63 - __clzll(static_cast<long long>(m)));
-            who[u] = 63 - __clzll(static_cast<long long>(m));
-            src[u] = A.src + (static_cast<long long>(I.b) * A.N + who[u]) * A.src_stride + static_cast<long long>(A.Hkv + I.g) * HD;
-        }
+__device__ __noinline__ void gather_block(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x, int quarter, int lane) {
+    constexpr int CH = HD / 8, ROWS = 32 / CH, U = 16 / ROWS;
+    const int term = S->list[x], tp = S->pos[term], p = (tp & ~15) + (lane & 15);
+    const uint16_t* src = nullptr;
+    int who = 0;   // node, or 64 + position of a cache row in its group
+    if (p < I.c) {
+        int row;
+        const long long z = static_cast<long long>(tree_page(A.kv, I.b, I.ctx - I.c + p, &row, A.err)) * A.Hkv + I.g;
+        src = A.vc + (z * A.kv.page + row) * HD;
+        who = 64 + (lane & 15);
+    } else if (p <= tp) {
+        u64 m = S->anc[term];   // the ancestor tp - p steps up: a path's nodes ascend
+        for (int up = tp - p; up > 0; --up) m ^= 1ull << (63 - __clzll(static_cast<long long>(m)));
+        who = 63 - __clzll(static_cast<long long>(m));
+        src = A.src + (static_cast<long long>(I.b) * A.N + who) * A.src_stride + static_cast<long long>(A.Hkv + I.g) * HD;
     }
+    __syncwarp();
     const int ch = lane % CH;
     uint8_t* d = dst + (ch >> 3) * (T * 128);
-#pragma unroll 1
-    for (int s0 = 0; s0 < nblk * 16; s0 += U * ROWS) {
-        uint4 v[U];
+    uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * ROWS + lane / CH;   // slot; the same half of the 64 for the whole warp
-            const u64 a = reinterpret_cast<u64>((s0 + u * ROWS) < 32 ? src[0] : src[1]);
-            const u64 q = __shfl_sync(0xffffffffu, a, s & 31);
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (q && s < nblk * 16) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + ch);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * ROWS + lane / CH;
-            const int w = __shfl_sync(0xffffffffu, (s0 + u * ROWS) < 32 ? who[0] : who[1], s & 31);
-            if (non_finite(v[u].x) | non_finite(v[u].y) | non_finite(v[u].z) | non_finite(v[u].w)) {
-                uint32_t* x = reinterpret_cast<uint32_t*>(&v[u]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u;
-                    if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0x0000FFFFu;
-                }
-                if (w < 64) atomicOr(&S->vbad, 1ull << w);
-                else atomicOr(&S->cbad, 1u << (w - 64));
-            }
-            if (s < nblk * 16) *reinterpret_cast<uint4*>(d + s * 128 + (((ch & 7) ^ (s & 7)) * 16)) = v[u];
-        }
+    for (int u = 0; u < U; ++u) {
+        const u64 q = __shfl_sync(0xffffffffu, reinterpret_cast<u64>(src), u * ROWS + lane / CH);
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (q) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + ch);
     }
-    fence_proxy_async_smem();
-    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int r = u * ROWS + lane / CH, s = quarter * 16 + r;
+        const int w = __shfl_sync(0xffffffffu, who, r);
+        if (non_finite(v[u].x) | non_finite(v[u].y) | non_finite(v[u].z) | non_finite(v[u].w)) {
+            uint32_t* e = reinterpret_cast<uint32_t*>(&v[u]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+                if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
+            }
+            if (w < 64) atomicOr(&S->vbad, 1ull << w);
+            else atomicOr(&S->cbad, 1u << (w - 64));
+        }
+        *reinterpret_cast<uint4*>(d + s * 128 + (((ch & 7) ^ (s & 7)) * 16)) = v[u];
+    }
 }
 
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
@@ -545,9 +532,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // by the parity of a block step's number
     auto bready = [&](int j) { return bx + 8u * (10 + j); };
     auto bfree = [&](int j) { return bx + 8u * (12 + j); };
-    // once per tail item: the tree's scores written, read; its info filled; its blocks gathered; its
-    // V tiles requested (every stage's last use but one is then complete, so warp 11's waits on the
-    // stages are never two phases behind)
+    // once per tail item: the tree's scores written; all that it holds (scores, info) read; its info
+    // filled; its blocks gathered; its V tiles requested (every stage's last use but one is then
+    // complete, so the gather's waits on the stages are never two phases behind)
     const uint32_t tbar = bx + 8u * 14, tfree = bx + 8u * 15, tready = bx + 8u * 16, vdone = bx + 8u * 17, vgo = bx + 8u * 18;
     const uint32_t qfull = bx + 8u * 19, qdone = bx + 8u * 20, ofree = bx + 8u * 21, done = bx + 8u * 22;
     // by the parity of group 1's tile: its sum is in shared memory (and its P handed over).  Two of
@@ -563,10 +550,31 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     const int it0 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x) * n_items / gridDim.x)
                           : (static_cast<int>(blockIdx.x) % per_split) * A.nsplit + static_cast<int>(blockIdx.x) / per_split;
     const int it1 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * n_items / gridDim.x) : it0 + 1;
+    // barrier i of the list above; the stages' barriers come first
+    if (tid < S::N_BARS && base - raw <= S::SLACK) {
+        const int j = tid - (2 * SK + 2 * SV);
+        const int count = j < 0 ? (tid >= 2 * SK && tid < 2 * SK + SV ? 5 : 1)   // fullV: the gather's warps and V's
+                          : j == 2 || j == 3 || j == 4 || j == 5 || j == 8 || j == 9 || j == 10 || j == 11 ? 128
+                          : j == 23 || j == 24 || j == 21                               ? 128
+                          : j == 15                                                     ? 128 + 1 + 1 + 4   // group 0, P V, V, group 1's warps
+                          : j == 17                                                     ? 4
+                                                                                        : 1;
+        mbar_init(bar0 + 8u * tid, count);
+        fence_mbar_init();
+    }
+    if (tid == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmT);
+        if (base - raw <= S::SLACK) s_abort = 0;
+    }
     griddep_wait();
     int first = it0;
-    while (first < it1 && !tree_item(A, first).live) ++first;
-    if (tid == 0)
+    TreeItem I0 = tree_item(A, first);
+    while (!I0.live && ++first < it1) I0 = tree_item(A, first);
+    // ctx or n_nodes out of range: the first item of the sequence says so
+    auto report = [&]() {
         for (int it = it0; it < it1; ++it) {
             const TreeItem I = tree_item(A, it);
             if (I.split == 0 && I.rt == 0 && I.g == 0) {
@@ -574,48 +582,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 if (I.bad_n) atomicOr(A.err, ERR_BAD_COUNT);
             }
         }
+    };
     if (first == it1 || base - raw > S::SLACK) {
+        if (tid == 0) report();
         if (first != it1 && tid == 0) atomicOr(A.err, ERR_WAIT_TIMEOUT);   // an unaligned base: see SLACK
         griddep_launch();
-        return;   // no barrier or tensor memory was set up
+        return;   // no tensor memory was set up
     }
-    if (tid == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-        tma_prefetch_desc(&tmT);
-        for (int st = 0; st < SK; ++st) {
-            mbar_init(fullK(st), 1);
-            mbar_init(emptyK(st), 1);
-        }
-        for (int st = 0; st < SV; ++st) {
-            mbar_init(fullV(st), 1);
-            mbar_init(emptyV(st), 1);
-        }
-        for (int j = 0; j < 2; ++j) {
-            mbar_init(sbar(j), 1);
-            mbar_init(sfree(j), 128);
-            mbar_init(pready(j), 128);
-            mbar_init(pfree(0, j), 1);
-            mbar_init(pfree(1, j), 1);
-            mbar_init(mpub(j), 128);
-            mbar_init(spub(j), 128);
-            mbar_init(bready(j), 128);
-            mbar_init(bfree(j), 1);
-        }
-        mbar_init(tbar, 1);
-        mbar_init(tfree, 129);
-        mbar_init(tready, 1);
-        mbar_init(vdone, 2);
-        mbar_init(vgo, 1);
-        mbar_init(qfull, 1);
-        mbar_init(qdone, 1);
-        mbar_init(ofree, 128);
-        mbar_init(done, 1);
-        mbar_init(done2, 1);
-        fence_mbar_init();
-        s_abort = 0;
-    }
+    auto item = [&](int it) -> TreeItem { return it == first ? I0 : tree_item(A, it); };
     if (warp == 10) {
         tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
@@ -638,31 +612,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
     auto same_q = [](const TreeItem& x, int b, int g, int rt) { return x.b == b && x.g == g && x.rt == rt; };
 
-    // the block steps of a tail item, the odd or the even ones; t counts the V tiles and steps
-    auto gather = [&](const TreeItem& I, int& t, int odd) -> bool {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            if (half ? !I.tail1 : !I.tail0) continue;
-            const int nb0 = info.nb0, x1 = half ? nb0 + info.nb1 : nb0;
-#pragma unroll 1
-            for (int x0 = half ? nb0 : 0; x0 < x1; x0 += 4, ++t) {
-                if ((t & 1) != odd) continue;
-                const int st = t % SV;
-                if (t >= SV && !WW(emptyV(st), ((t / SV) & 1u) ^ 1u)) return false;
-                gather_blocks<HD>(&info, A, I, smem + (sV(st) - base), x0, min(4, x1 - x0), lane);
-                if (lane == 0) mbar_arrive(fullV(st));
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vdone);
-        return true;
-    };
     if (warp == 11) {
         // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before, and
-        // the odd block steps
-        int nq = 0, t = 0, nt = 0, qb = -1, qg = -1, qrt = -1;
+        // what there is to know of a tail item's tree
+        int nq = 0, nt = 0, qb = -1, qg = -1, qrt = -1;
         for (int it = first; it < it1; ++it) {
-            const TreeItem I = tree_item(A, it);
+            const TreeItem I = item(it);
             if (!I.live) continue;
             if (!same_q(I, qb, qg, qrt)) {
                 qb = I.b, qg = I.g, qrt = I.rt;
@@ -674,20 +629,24 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 }
                 ++nq;
             }
-            t += I.vreg();
             if (!I.tail()) continue;
-            if (!WW(vgo, nt & 1u) || !WW(tready, nt & 1u)) break;
+            if (nt > 0 && !WW(tfree, (nt - 1) & 1u)) break;
             ++nt;
-            if (!gather(I, t, 1)) break;
+            tree_info(&info, A, I, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tready);
         }
-        if (lane == 0 && nq > 0) drain(qfull, (nq - 1) & 1u);   // every issued copy lands before the CTA may leave
+        if (lane == 0) {
+            report();
+            if (nq > 0) drain(qfull, (nq - 1) & 1u);   // every issued copy lands before the CTA may leave
+        }
     } else if (warp == 8) {
         // ---- K tiles of the cache, then the tree's
         if (lane == 0) {
             int t = 0;
             bool ok = true;
             for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = tree_item(A, it);
+                const TreeItem I = item(it);
                 if (!I.live) continue;
                 const int nreg = I.kreg(), nk = nreg + (I.tail() ? 1 : 0);
                 for (int i = 0; i < nk; ++i) {
@@ -712,37 +671,47 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             for (int j = t > SK ? t - SK : 0; j < t; ++j) drain(fullK(j % SK), (j / SK) & 1u);
         }
     } else if (warp == 9) {
-        // ---- V tiles of the cache, then the even block steps (four blocks to a V tile)
-        int t = 0, nt = 0;
-        bool ok = true;
-        for (int it = first; ok && it < it1; ++it) {
-            const TreeItem I = tree_item(A, it);
-            if (!I.live) continue;
-            if (lane == 0) {
-                for (int i = 0; i < I.vreg(); ++i) {
+        // ---- V tiles of the cache; a tail's block steps are group 1's
+        if (lane == 0) {
+            int t = 0, nt = 0;
+            unsigned mine = 0;   // bit j: use t - 1 - j of the ring was a copy of this warp's
+            bool ok = true;
+            for (int it = first; ok && it < it1; ++it) {
+                const TreeItem I = item(it);
+                if (!I.live) continue;
+                const int nv = I.vreg();
+                for (int i = 0; i < nv; ++i, ++t) {
                     const int st = t % SV;
                     if (t >= SV && !W(emptyV(st), ((t / SV) & 1u) ^ 1u)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(fullV(st), TILE_BYTES);
+                    for (int k = 0; k < 4; ++k) mbar_arrive(fullV(st));   // a gathered stage's other arrivals
                     int row;
                     const int z = tree_page(A.kv, I.b, I.p_begin + i * T, &row, A.err) * A.Hkv + I.g;
 #pragma unroll
                     for (int cb = 0; cb < CB; ++cb) tma_load_3d(sV(st) + cb * BLK, &tmV, cb * 64, row, z, fullV(st));
+                    mine = mine << 1 | 1u;
+                }
+                if (!ok || !I.tail()) continue;
+                if (!W(tready, nt & 1u)) break;
+                mbar_arrive(vgo);   // after tready: group 1 has then taken the one before
+                ++nt;
+                int steps = (I.tail0 ? (info.nb0 + 3) / 4 : 0) + (I.tail1 ? (info.nb1 + 3) / 4 : 0);
+                mbar_arrive(tfree);
+                for (; ok && steps > 0; --steps) {
+                    ok = t < SV || W(emptyV(t % SV), ((t / SV) & 1u) ^ 1u);
+                    if (!ok) break;
+                    mbar_arrive(fullV(t % SV));   // the fifth arrival keeps this warp in step with the ring
+                    mine <<= 1;
                     ++t;
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            t = __shfl_sync(0xffffffffu, t, 0);
-            if (!ok || !I.tail()) continue;
-            if (!WW(tready, nt & 1u)) break;
-            if (lane == 0) mbar_arrive(vgo);   // after tready: warp 11 has then taken the one before
-            ++nt;
-            if (!gather(I, t, 0)) break;
+            // every issued copy lands before the CTA may leave
+            for (int j = 1; j <= SV && j <= t; ++j)
+                if ((mine >> (j - 1)) & 1) drain(fullV((t - j) % SV), ((t - j) / SV) & 1u);
         }
-        if (lane == 0)
-            for (int j = t > SV ? t - SV : 0; j < t; ++j) drain(fullV(j % SV), (j / SV) & 1u);
     } else if (warp == 10) {
         // ---- Q K^T, as far ahead as the two score buffers allow.  It and P V are issued by a warp each:
         // a tile's barrier tests and commits take an issuer ~1000 cycles beside the ~1000 of its MMAs,
@@ -752,7 +721,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             int tk = 0, n0 = 0, n1 = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1;
             bool ok = true;
             for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = tree_item(A, it);
+                const TreeItem I = item(it);
                 if (!I.live) continue;
                 if (!same_q(I, qb, qg, qrt)) {
                     if (nq > 0) tc_commit(qdone);
@@ -801,7 +770,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             int tk = 0, np_0 = 0, np_1 = 0, bs = 0, v = 0, nt = 0, nitem = 0;
             bool ok = true;
             for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = tree_item(A, it);
+                const TreeItem I = item(it);
                 if (!I.live) continue;
                 const int nreg = I.kreg();
                 bool first_pv = true;
@@ -874,8 +843,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int nl = rho / A.G, gh = rho - nl * A.G;
         // n: own tiles; n1 (group 0): tiles of group 1 taken; n0 (group 1): tiles of group 0 in the
-        // items before; npub (group 1): maxima taken from group 0
-        int n = 0, n1 = 0, n0 = 0, npub = 0, bs = 0, nt = 0, tk = 0;
+        // items before; npub (group 1): maxima taken from group 0; tv (group 1): V tiles and block steps
+        int n = 0, n1 = 0, n0 = 0, npub = 0, bs = 0, nt = 0, tk = 0, tv = 0;
         bool ok = true;
         // O (once a P V step of the item has been issued; `bar` completes with its last) times al
         auto rescale = [&](float al, bool any_pv, uint32_t bar, uint32_t par) -> bool {
@@ -906,15 +875,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             return true;
         };
         for (int it = first; ok && it < it1; ++it) {
-            const TreeItem I = tree_item(A, it);
+            const TreeItem I = item(it);
             if (!I.live) continue;
-            if (warp == 0 && I.tail()) {
-                // the previous tail item's info is no longer read
-                if (nt > 0 && !WW(tfree, (nt - 1) & 1u)) break;
-                tree_info(&info, A, I, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tready);
-            }
             const int node = I.node0(A.NT) + nl;
             const bool valid = nl < A.NT && node < I.n;
             float m = NEG_INF, l = 0.f;
@@ -974,8 +936,33 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 ++n;
             }
             if (!ok) break;
-            if (grp == 1) {   // tails and epilogues are group 0's
+            if (grp == 1) {
+                // tails' softmax and epilogues are group 0's; here the V rows of the block steps, a
+                // block per warp
                 n0 += (I.nfull + 1) / 2 + (I.tail0 && I.c > 0 ? 1 : 0);
+                tv += I.vreg();
+                if (!I.tail()) continue;
+                if (!WW(vgo, nt & 1u) || !WW(tready, nt & 1u)) break;
+                ++nt;
+#pragma unroll 1
+                for (int half = 0; ok && half < 2; ++half) {
+                    if (half ? !I.tail1 : !I.tail0) continue;
+                    const int nb0 = info.nb0, x1 = half ? nb0 + info.nb1 : nb0;
+#pragma unroll 1
+                    for (int x0 = half ? nb0 : 0; x0 < x1; x0 += 4, ++tv) {
+                        const int st = tv % SV, x = x0 + (warp & 3);
+                        if (tv >= SV && !WW(emptyV(st), ((tv / SV) & 1u) ^ 1u)) { ok = false; break; }
+                        if (x < x1) gather_block<HD>(&info, A, I, smem + (sV(st) - base), x, warp & 3, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(fullV(st));
+                    }
+                }
+                __syncwarp();
+                if (ok && lane == 0) {
+                    mbar_arrive(vdone);
+                    mbar_arrive(tfree);
+                }
                 continue;
             }
             const bool last_odd = I.nfull > 0 && !(I.nfull & 1);
@@ -1034,8 +1021,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         if (!WW(sbar(0), n & 1u)) { ok = false; break; }
                         tc_fence_after();
                     }
+                    // the parts that hold a cache position or a node
+                    const int r0 = has_a ? 0 : 4, ra = (I.c + 15) / 16, r1 = 4 + (I.n + 15) / 16;
 #pragma unroll 1
-                    for (int r = has_a ? 0 : 4; r < 8; ++r) {
+                    for (int r = r0; r < r1; r = r + 1 == ra ? 4 : r + 1) {
                         load16(r);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) mx = max3(mx, s[j], s[j + 1]);
@@ -1066,7 +1055,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         tc_fence_after();
                     }
 #pragma unroll 1
-                    for (int r = has_a ? 0 : 4; r < 8; ++r) {
+                    for (int r = r0; r < r1; r = r + 1 == ra ? 4 : r + 1) {
                         load16(r);
                         exp16(sum);
                         if (r < 4) {
@@ -1158,6 +1147,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 }
                 const long long idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
                 float* op = A.opart + idx * HD;
+                // A lane holds 32 columns of its own row; eight lanes exchange 16-byte pieces so that
+                // each store instruction writes whole 128-byte lines of four rows (a row per lane wrote
+                // half sectors: 5 us for the 128 KB of a full item at hd 256)
+                u64 rowp[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) rowp[j] = __shfl_sync(0xffffffffu, live ? reinterpret_cast<u64>(op) : 0ull, (lane & 24) + j);
+                const int b8 = lane & 7;
 #pragma unroll 1
                 for (int c = 0; c < HD / 32; ++c) {
                     float o[32];
@@ -1165,14 +1161,25 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     tmem_ld16(tO + lane_off + c * 32, o);
                     tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
                     tmem_ld_wait();
-                    if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(op + c * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    }
+                    for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!(j & d))
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const bool up = b8 & d;
+                                    const float y = __shfl_xor_sync(0xffffffffu, up ? o[4 * j + e] : o[4 * (j | d) + e], d);
+                                    if (up) o[4 * j + e] = y;
+                                    else o[4 * (j | d) + e] = y;
+                                }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (rowp[j])
+                            *(reinterpret_cast<float4*>(rowp[j]) + c * 8 + b8) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
                 if (vbad || cbad) {
-                    __syncwarp();
+                    __syncwarp();   // the rows' partials were written by other lanes
                     const TreeBad F{path, in0, vbad, cbad, cnz, m0, m, tT + lane_off, I.tail0, I.tail1, I.b, I.g, I.ctx, I.c, HD,
                                     live ? op : nullptr};
                     tree_add_bad(A, F);
