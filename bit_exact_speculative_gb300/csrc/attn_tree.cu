@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // complete, so the gather's waits on the stages are never two phases behind)
     const uint32_t tbar = bx + 8u * 14, tfree = bx + 8u * 15, tready = bx + 8u * 16, vdone = bx + 8u * 17, vgo = bx + 8u * 18;
     const uint32_t qfull = bx + 8u * 19, qdone = bx + 8u * 20, ofree = bx + 8u * 21, done = bx + 8u * 22;
-    // by the parity of group 1's tile: its sum is in shared memory (and its P handed over).  Two of
-    // them, as group 1 may end its next tile before group 0 comes to take this one's sum.
+    // by the parity of group 1's tile: its sum is in shared memory.  Two of them, as group 1 may end its
+    // next tile before group 0 comes to take this one's sum.
     auto spub = [&](int j) { return bx + 8u * (23 + j); };
     const uint32_t done2 = bx + 8u * 27;
 
@@ -589,7 +589,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         griddep_launch();
         return;   // no tensor memory was set up
     }
-    auto item = [&](int it) -> TreeItem { return it == first ? I0 : tree_item(A, it); };
+    // the next item, in the roles' loops
+    auto next = [&](int it, TreeItem& I) {
+        if (it < it1) I = tree_item(A, it);
+    };
     if (warp == 10) {
         tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
@@ -604,6 +607,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 
     // bounded waits; after the first one that gives up, every later one that would have to wait returns at once
     auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || tree_wait(bar, par, A.err, &s_abort); };
+    // two barriers tested side by side
+    auto W2 = [&](uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) -> bool {
+        const bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+        return (r0 || tree_wait(b0, p0, A.err, &s_abort)) && (r1 || tree_wait(b1, p1, A.err, &s_abort));
+    };
     // a wait for one's own copies or MMAs before leaving: also after an abort
     auto drain = [&](uint32_t bar, uint32_t par) {
         int none = 0;
@@ -616,8 +624,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before, and
         // what there is to know of a tail item's tree
         int nq = 0, nt = 0, qb = -1, qg = -1, qrt = -1;
-        for (int it = first; it < it1; ++it) {
-            const TreeItem I = item(it);
+        TreeItem I = I0;
+        for (int it = first; it < it1; next(++it, I)) {
             if (!I.live) continue;
             if (!same_q(I, qb, qg, qrt)) {
                 qb = I.b, qg = I.g, qrt = I.rt;
@@ -645,8 +653,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         if (lane == 0) {
             int t = 0;
             bool ok = true;
-            for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = item(it);
+            TreeItem I = I0;
+            for (int it = first; ok && it < it1; next(++it, I)) {
                 if (!I.live) continue;
                 const int nreg = I.kreg(), nk = nreg + (I.tail() ? 1 : 0);
                 for (int i = 0; i < nk; ++i) {
@@ -676,8 +684,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             int t = 0, nt = 0;
             unsigned mine = 0;   // bit j: use t - 1 - j of the ring was a copy of this warp's
             bool ok = true;
-            for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = item(it);
+            TreeItem I = I0;
+            for (int it = first; ok && it < it1; next(++it, I)) {
                 if (!I.live) continue;
                 const int nv = I.vreg();
                 for (int i = 0; i < nv; ++i, ++t) {
@@ -718,10 +726,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         // and with one issuer for both the tensor core stood idle meanwhile.
         if (lane == 0) {
             constexpr uint32_t IDS = idesc_bf16_f32(128, T);
-            int tk = 0, n0 = 0, n1 = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1;
+            int st = 0, n0 = 0, n1 = 0, nt = 0, nq = 0, qb = -1, qg = -1, qrt = -1;
+            uint32_t ph = 0;
             bool ok = true;
-            for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = item(it);
+            TreeItem I = I0;
+            for (int it = first; ok && it < it1; next(++it, I)) {
                 if (!I.live) continue;
                 if (!same_q(I, qb, qg, qrt)) {
                     if (nq > 0) tc_commit(qdone);
@@ -732,19 +741,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 const int nreg = I.kreg(), nqk = nreg + (I.tail() ? 1 : 0);
 #pragma unroll 1
                 for (int i = 0; i < nqk; ++i) {
-                    const int st = tk % SK;
-                    ok = W(fullK(st), (tk / SK) & 1u);
                     uint32_t d, ready;
                     if (i >= nreg) {   // the tree's scores
-                        ok = ok && (nt == 0 || W(tfree, (nt - 1) & 1u));
+                        ok = W(fullK(st), ph) && (nt == 0 || W(tfree, (nt - 1) & 1u));
                         ++nt;
                         d = tT;
                         ready = tbar;
                     } else {
-                        const bool odd = i < I.nfull && (i & 1);
-                        const int n = odd ? n1++ : n0++;
-                        ok = ok && (n == 0 || W(sfree(odd), (n - 1) & 1u));
-                        d = tS + (odd ? T : 0);
+                        const uint32_t odd = i < I.nfull ? i & 1 : 0;
+                        const uint32_t n = odd ? n1++ : n0++;
+                        ok = n == 0 ? W(fullK(st), ph) : W2(fullK(st), ph, sfree(odd), (n - 1) & 1u);
+                        d = tS + odd * T;
                         ready = sbar(odd);
                     }
                     if (!ok) break;
@@ -755,7 +762,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     tc_commit(ready);
                     // at hd 256 the tree's stage goes on as the block steps' P and is freed by their end
                     if (!S::PB_IN_K || i < nreg) tc_commit(emptyK(st));
-                    ++tk;
+                    if (++st == SK) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
@@ -769,8 +779,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             // tk: K tiles; np_g: steps of group g's tiles; bs: block steps; v: V tiles; nitem: items with a step
             int tk = 0, np_0 = 0, np_1 = 0, bs = 0, v = 0, nt = 0, nitem = 0;
             bool ok = true;
-            for (int it = first; ok && it < it1; ++it) {
-                const TreeItem I = item(it);
+            TreeItem I = I0;
+            for (int it = first; ok && it < it1; next(++it, I)) {
                 if (!I.live) continue;
                 const int nreg = I.kreg();
                 bool first_pv = true;
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 for (int i = 0; i < nreg; ++i) {
                     const bool odd = i < I.nfull && (i & 1);
                     const int ksteps = i < I.nfull ? 4 : I.c / 16, sv = v % SV, n = odd ? np_1++ : np_0++;
-                    ok = begin_pv() && W(pready(odd), n & 1u) && (ksteps == 0 || W(fullV(sv), (v / SV) & 1u));
+                    ok = begin_pv() && (ksteps == 0 ? W(pready(odd), n & 1u) : W2(pready(odd), n & 1u, fullV(sv), (v / SV) & 1u));
                     if (!ok) break;
                     if (ksteps > 0) {
                         tc_fence_after();
@@ -852,30 +862,26 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!WW(bar, par)) return false;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-                float o[32];
-                tmem_ld16(tO + lane_off + c * 32, o);
-                tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
-                tmem_ld_wait();
+            for (int c = 0; c < HD / 64; ++c) {
+                float o[64];
+                tmem_ld64(tO + lane_off + c * 64, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __fmul_rn(o[e], al);
-                tmem_st16(tO + lane_off + c * 32, o);
-                tmem_st16(tO + lane_off + c * 32 + 16, o + 16);
+                for (int e = 0; e < 64; e += 2) mul2(o[e], o[e + 1], al);
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) tmem_st16(tO + lane_off + c * 64 + q4 * 16, o + q4 * 16);
             }
             tmem_st_wait();
             return true;
         };
         // P of the group's tile into tensor memory, once the P V step of its tile before has read it
-        auto put_p = [&](const uint32_t* pk) -> bool {
+        auto write_p = [&](const uint32_t* pk) -> bool {
             if (n > 0 && !WW(pfree(grp, n - 1), ((n - 1) >> 1) & 1u)) return false;
             tc_fence_after();
             tmem_st32(tP + grp * 32 + lane_off, pk);
-            tc_fence_before();
-            mbar_arrive(pready(grp));
             return true;
         };
-        for (int it = first; ok && it < it1; ++it) {
-            const TreeItem I = item(it);
+        TreeItem I = I0;
+        for (int it = first; ok && it < it1; next(++it, I)) {
             if (!I.live) continue;
             const int node = I.node0(A.NT) + nl;
             const bool valid = nl < A.NT && node < I.n;
@@ -914,7 +920,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     ++npub;
                     m = m_sm[rho];
                 }
-                const float mn = new_max(m, mx), al = alpha(m, mn);
+                const float mn = new_max(m, mx);
+                // a row that is no node's holds whatever its Q was: it must not have O rescaled for it
+                const float al = valid ? alpha(m, mn) : 1.f;
                 m = mn;
                 if (grp == 1 || i + 1 < I.nfull) {   // someone takes it
                     m_sm[rho] = mn;
@@ -928,11 +936,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     l = __fadd_rn(__fmul_rn(l, al), sum);
                 } else {
                     sum_sm[(n & 1) * 128 + rho] = sum;
+                    mbar_arrive(spub(n & 1));
                 }
                 // the P V step before is the other group's
                 const int before = grp ? n0 + i / 2 : n1 - 1;
-                if (!rescale(al, i > 0, pfree(1 - grp, before), (before >> 1) & 1u) || !put_p(pk)) { ok = false; break; }
-                if (grp == 1) mbar_arrive(spub(n & 1));
+                if (!write_p(pk) || !rescale(al, i > 0, pfree(1 - grp, before), (before >> 1) & 1u)) { ok = false; break; }
+                tc_fence_before();
+                mbar_arrive(pready(grp));
                 ++n;
             }
             if (!ok) break;
@@ -1204,44 +1214,49 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 }
 
 // Combine of a row's splits, the decode rows' operations: w_s = exp2(m_s - M), L += w_s l_s,
-// acc += w_s o_s in split order, out = acc / L (and the output gate).  A thread owns two values of a
-// row and keeps the loads of several splits in flight; every thread of a row forms the few weights
-// itself (the row's m and l come from L1), so nothing is exchanged.
+// acc += w_s o_s in split order, out = acc / L (and the output gate).  A warp owns 64 columns of a row,
+// two per lane.  It reads the row's m and l 32 splits at a time, a split per lane, and forms each
+// weight once; 16 splits' partials are in flight per lane.
 constexpr int COMB_THREADS = 128;
 
-__global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(TreeArgs A, int hd) {
+__global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const __grid_constant__ TreeArgs A, int hd) {
     griddep_launch();
     griddep_wait();
-    const int per = hd / 2, rows = COMB_THREADS / per;
-    const long long row = static_cast<long long>(blockIdx.x) * rows + threadIdx.x / per;
+    const int per = hd / 64, lane = threadIdx.x & 31;   // warps per row
+    const long long wid = static_cast<long long>(blockIdx.x) * (COMB_THREADS / 32) + (threadIdx.x >> 5), row = wid / per;
     if (row >= static_cast<long long>(A.B) * A.N * A.Hq) return;
     const long long br = row / A.Hq;
     const int h = static_cast<int>(row - br * A.Hq), b = static_cast<int>(br / A.N), i = static_cast<int>(br - static_cast<long long>(b) * A.N);
     const int ctx = A.ctx_len[b], n = A.n_nodes ? A.n_nodes[b] : A.N;
     if (ctx < 0 || ctx > A.max_ctx || i >= n) return;   // reported by the split kernel
-    const int ns = min(A.nsp[br], A.nsplit), d = 2 * (threadIdx.x % per);
+    const int ns = min(A.nsp[br], A.nsplit), d = static_cast<int>(wid - row * per) * 64 + 2 * lane;
     const float2* ml = A.ml + row * A.nsplit;
     const float* op = A.opart + row * A.nsplit * hd + d;
     float M = NEG_INF;
-    for (int s = 0; s < ns; ++s) M = fmaxf(M, ml[s].x);
+    for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[s].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f, a0 = 0.f, a1 = 0.f;
-    constexpr int U = 8;
-    for (int s0 = 0; s0 < ns; s0 += U) {
-        float2 o[U], w[U];
+    constexpr int U = 16;
+    for (int s0 = 0; s0 < ns; s0 += 32) {
+        const float2 v = s0 + lane < ns ? ml[s0 + lane] : make_float2(NEG_INF, 0.f);
+        const float w = exp2f(__fsub_rn(v.x, M)), wl = __fmul_rn(w, v.y);
+#pragma unroll 1
+        for (int t0 = 0; t0 < 32 && s0 + t0 < ns; t0 += U) {
+            float2 o[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (s0 + u < ns) {
-                o[u] = *reinterpret_cast<const float2*>(op + static_cast<long long>(s0 + u) * hd);
-                w[u] = ml[s0 + u];
-            }
+            for (int u = 0; u < U; ++u)
+                if (s0 + t0 + u < ns) o[u] = *reinterpret_cast<const float2*>(op + static_cast<long long>(s0 + t0 + u) * hd);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (s0 + u < ns) {
-                const float x = exp2f(__fsub_rn(w[u].x, M));
-                L = __fadd_rn(L, __fmul_rn(x, w[u].y));
-                a0 = __fadd_rn(a0, __fmul_rn(x, o[u].x));
-                a1 = __fadd_rn(a1, __fmul_rn(x, o[u].y));
+            for (int u = 0; u < U; ++u) {
+                const float x = __shfl_sync(0xffffffffu, w, t0 + u), xl = __shfl_sync(0xffffffffu, wl, t0 + u);
+                if (s0 + t0 + u < ns) {
+                    L = __fadd_rn(L, xl);
+                    a0 = __fadd_rn(a0, __fmul_rn(x, o[u].x));
+                    a1 = __fadd_rn(a1, __fmul_rn(x, o[u].y));
+                }
             }
+        }
     }
     float y0 = __fdiv_rn(a0, L), y1 = __fdiv_rn(a1, L);
     const long long col = static_cast<long long>(h) * hd + d;
@@ -1317,7 +1332,7 @@ xv_status tree_launch(TreeArgs a, int hd, void* ws, cudaStream_t s) {
     if (st) return st;
     const long long nrow = static_cast<long long>(a.B) * a.N * a.Hq;
     trace_pre(s);
-    launch_k(attn_tree_combine_kernel, dim3(ceil_div(nrow, COMB_THREADS / (hd / 2))), dim3(COMB_THREADS), 0, s, a, hd);
+    launch_k(attn_tree_combine_kernel, dim3(ceil_div(nrow * (hd / 64), COMB_THREADS / 32)), dim3(COMB_THREADS), 0, s, a, hd);
     return launched("attn_tree_combine_kernel", s, K_ATTN_TREE, 4ll * nrow * a.nsplit * (hd + 2) + 2ll * nrow * hd * (a.gate ? 2 : 1));
 }
 
