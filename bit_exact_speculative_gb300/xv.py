@@ -173,19 +173,24 @@ def _check(code: int):
         raise XVError(code, lib().xv_last_error().decode(errors="replace"))
 
 
+# A call's host time is a few microseconds, of the order of a short kernel's: pointers and streams go
+# to ctypes as plain ints (the signatures make them void*), and the current stream is asked for as its
+# handle (a torch.cuda.Stream object costs ~3 us).
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    assert t.dim() >= 2 and t.stride(-1) == 1, "rows must be contiguous"
-    return t.stride(-2) if t.dim() == 2 else t.stride(0)
+    s = t.stride()
+    assert len(s) >= 2 and s[-1] == 1, "rows must be contiguous"
+    return s[0]
 
 
 # ------------------------------------------------------------------ misc
@@ -300,7 +305,7 @@ def xv_gemm_small_m(X, W, Y, ws, stream=None):
     else:
         fn = lib().xv_gemm_small_m_f32out if f32 else lib().xv_gemm_small_m
     _check(fn(_ptr(X), _row_stride(X), _ptr(W), _ptr(Y), _row_stride(Y), M, N, K, _ptr(ws),
-              0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+              0 if ws is None else ws.nbytes, _stream(stream)))
     return Y
 
 
@@ -368,7 +373,7 @@ def xv_attn_decode_rows(q, q_stride, kc, vc, ctx_len, R, B, Hq, Hkv, hd, Lmax, m
                         gate=None, gate_stride=0, stream=None):
     _check(lib().xv_attn_decode_rows(_ptr(q), q_stride, _ptr(kc), _ptr(vc), _ptr(ctx_len), R, B, Hq, Hkv, hd, Lmax,
                                      max_ctx, float(scale), _ptr(gate), gate_stride, _ptr(out), out_stride, _ptr(ws),
-                                     ws.numel() * ws.element_size(), _stream(stream)))
+                                     ws.nbytes, _stream(stream)))
 
 
 def xv_kv_append(kv_src, src_stride, ctx_len, R, B, Hkv, hd, Lmax, kc, vc, stream=None):
@@ -389,7 +394,7 @@ def xv_attn_decode_rows_paged(q, q_stride, kpool, vpool, pages: KvPages, ctx_len
     _check(lib().xv_attn_decode_rows_paged(_ptr(q), q_stride, _ptr(kpool), _ptr(vpool), ctypes.byref(pages),
                                            _ptr(ctx_len), R, B, Hq, Hkv, hd, max_ctx, float(scale), _ptr(gate),
                                            gate_stride, _ptr(out), out_stride, _ptr(ws),
-                                           ws.numel() * ws.element_size(), _stream(stream)))
+                                           ws.nbytes, _stream(stream)))
 
 
 def xv_kv_append_paged(kv_src, src_stride, ctx_len, R, B, Hkv, hd, pages: KvPages, kpool, vpool, stream=None):
@@ -413,7 +418,7 @@ def xv_kv_pages_update(pages: KvPages, free_pages, n_free, held, ctx_len, n_new,
                                     _ptr(n_free), _ptr(n_free if n_free_out is None else n_free_out), _ptr(held),
                                     _ptr(held if held_out is None else held_out), _ptr(ctx_len), _ptr(n_new), B,
                                     _ptr(row_start), _ptr(pos), _ptr(slots), slots.numel(), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _stream(stream)))
+                                    ws.nbytes, _stream(stream)))
 
 
 # ------------------------------------------------- head norms and rotation
@@ -470,7 +475,7 @@ def xv_attn_tree(q, kc, vc, ctx_len, kv_src, parent, n_nodes, N, B, Hq, Hkv, hd,
     _check(lib().xv_attn_tree(_ptr(q), _row_stride(q), _ptr(kc), _ptr(vc), _ptr(ctx_len), _ptr(kv_src),
                               _row_stride(kv_src), _ptr(parent), _ptr(n_nodes), N, B, Hq, Hkv, hd, Lmax, max_ctx, scale,
                               _ptr(gate), 0 if gate is None else _row_stride(gate), _ptr(out), _row_stride(out), _ptr(ws),
-                              ws.numel() * ws.element_size(), _stream(stream)))
+                              ws.nbytes, _stream(stream)))
 
 
 def xv_attn_tree_paged(q, kpool, vpool, pages: KvPages, ctx_len, kv_src, parent, n_nodes, N, B, Hq, Hkv, hd, max_ctx,
@@ -478,7 +483,7 @@ def xv_attn_tree_paged(q, kpool, vpool, pages: KvPages, ctx_len, kv_src, parent,
     _check(lib().xv_attn_tree_paged(_ptr(q), _row_stride(q), _ptr(kpool), _ptr(vpool), ctypes.byref(pages), _ptr(ctx_len),
                                     _ptr(kv_src), _row_stride(kv_src), _ptr(parent), _ptr(n_nodes), N, B, Hq, Hkv, hd,
                                     max_ctx, scale, _ptr(gate), 0 if gate is None else _row_stride(gate), _ptr(out),
-                                    _row_stride(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                    _row_stride(out), _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def xv_tree_accept(tokens, parent, n_nodes, argmax, path, n_keep, next_token, stream=None):
@@ -568,13 +573,13 @@ class Block:
 def xv_verify_block(blk: Block, tokens, k: int, logits, argmax, n_accept, ws, stream=None):
     _check(lib().xv_verify_block(ctypes.byref(blk.cfg), ctypes.byref(blk.weights), ctypes.byref(blk.state),
                                  _ptr(tokens), k, _ptr(logits), _ptr(argmax), _ptr(n_accept), _ptr(ws),
-                                 ws.numel() * ws.element_size(), _stream(stream)))
+                                 ws.nbytes, _stream(stream)))
 
 
 def xv_verify_block_commit_accepted(blk: Block, tokens, k: int, logits, argmax, n_accept, ws, stream=None):
     _check(lib().xv_verify_block_commit_accepted(ctypes.byref(blk.cfg), ctypes.byref(blk.weights),
                                                  ctypes.byref(blk.state), _ptr(tokens), k, _ptr(logits), _ptr(argmax),
-                                                 _ptr(n_accept), _ptr(ws), ws.numel() * ws.element_size(),
+                                                 _ptr(n_accept), _ptr(ws), ws.nbytes,
                                                  _stream(stream)))
 
 
@@ -589,13 +594,13 @@ def xv_block_step_host(blk: Block, host_tokens, dev_tokens, k: int, dev_results,
             raise ValueError(f"{name}: {n} contiguous int32 in {'host' if host else 'device'} memory needed")
     _check(lib().xv_block_step_host(ctypes.byref(blk.cfg), ctypes.byref(blk.weights), ctypes.byref(blk.state),
                                     _ptr(host_tokens), _ptr(dev_tokens), k, _ptr(dev_results), _ptr(host_results),
-                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                    _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def xv_verify_block_ragged(blk: Block, tokens, k: int, k_seq, logits, argmax, n_accept, ws, stream=None):
     _check(lib().xv_verify_block_ragged(ctypes.byref(blk.cfg), ctypes.byref(blk.weights), ctypes.byref(blk.state),
                                         _ptr(tokens), k, _ptr(k_seq), _ptr(logits), _ptr(argmax), _ptr(n_accept),
-                                        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                        _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def xv_block_commit(blk: Block, n_keep, stream=None):
@@ -609,7 +614,7 @@ def xv_block_commit_accepted(blk: Block, n_accept, stream=None):
 def xv_block_prefill(blk: Block, tokens, T: int, chunk: int, last_logits, last_argmax, ws, stream=None):
     _check(lib().xv_block_prefill(ctypes.byref(blk.cfg), ctypes.byref(blk.weights), ctypes.byref(blk.state),
                                   _ptr(tokens), T, chunk, _ptr(last_logits), _ptr(last_argmax), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)))
+                                  ws.nbytes, _stream(stream)))
 
 
 def xv_block_flush(blk: Block, stream=None):
