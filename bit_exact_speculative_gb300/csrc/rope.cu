@@ -9,11 +9,13 @@
 // modulo 2^64 is the angle modulo one turn to 2^-64 * p of a turn, for any 32-bit p.  An fp32
 // angle p * f_i would be off by p * 2^-24 radians (0.008 at 131072 positions, 0.03 at 500000).
 //
-// What bounds it: every value is read once and written once with ~10 operations between, so HBM
-// for long row counts and one load-to-store latency for a verify step's few rows.  A head takes
-// hd/8 lanes of 16 bytes each, its sum of squares a fixed shuffle tree inside them, so a head's
-// bits depend on that head, its weight and its position alone.  cos and sin are formed once per
-// row and shared by the row's heads through shared memory.
+// What bounds it: every value is read once and written once.  8192 rows of 40 + 8 heads of 128: 47.6 us
+// for 201 MB, 4.2 TB/s, 0.63 of the measured copy rate; more or fewer resident CTAs change nothing, the
+// ~110 instructions a lane needs per 8 values share the issue slots with the loads.  A verify step's 8
+// rows: 2.0 us, one load-to-store latency.  A head takes hd/8 lanes of 16 bytes each, its sum of
+// squares a fixed shuffle tree inside them, so a head's bits depend on that head, its weight and its
+// position alone.  fp32 pairs go two to an instruction; cos and sin are formed once per row and read
+// as rows of floats (as (cos, sin) pairs, the lanes' reads met in the same banks 16 deep).
 #include "xv_internal.h"
 #include "xv_ptx.cuh"
 
@@ -46,7 +48,8 @@ struct RopeArgs {
 };
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_U = 4;    // heads whose loads a lane group has in flight together
+constexpr int ROPE_U = 4;    // units whose loads a lane group has in flight together
+constexpr int ROPE_ROWS = 16;   // rows per CTA, at most
 
 __device__ __forceinline__ void rope_unpack(const uint4& v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -59,100 +62,157 @@ __device__ __forceinline__ void rope_unpack(const uint4& v, float* f) {
 __device__ __forceinline__ uint4 rope_pack(const float* f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
+// Two fp32 operations in one instruction: (a, b) *= (x, y), and (a, b) * (x, y) + (u, v).
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float a, float b, float x, float y, float& u, float& v) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
+        "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "+f"(u), "+f"(v) : "f"(a), "f"(b), "f"(x), "f"(y));
+}
 
-// CTA (x, y): row x, heads y*HPB .. (HPB = heads per pass * passes); a head per LPH lanes.
-template <int HD>
-__global__ void __launch_bounds__(ROPE_THREADS) qk_norm_rope_kernel(RopeArgs A, int heads_per_cta) {
+// CTA (x, y): rows x * rpc .. of `rpc` rows, of each row's heads y * hpc .. of `hpc` (rpc > 1 only
+// with every head of a row in the CTA).  A unit, one head of one row, takes LPH lanes; HPP units run at
+// a time, and the loads of up to ROPE_U passes go out before what the angles need.  cos, sin and -sin
+// of the CTA's rows stand in shared memory as rows of floats, read 16 bytes at a time.
+constexpr int ROPE_TAB = 1024;   // floats per table: rpc * rot / 2 of them are used
+
+template <int HD, bool INTER>
+__global__ void __launch_bounds__(ROPE_THREADS, 4) qk_norm_rope_kernel(const __grid_constant__ RopeArgs A, int hpc, int rpc, unsigned inv_h) {
     griddep_launch();
-    constexpr int LPH = HD / 8, HPP = ROPE_THREADS / LPH;   // lanes per head, heads per pass
-    __shared__ float2 cs[HD / 2];
-    const long long row = blockIdx.x;
+    constexpr int LPH = HD / 8, HPP = ROPE_THREADS / LPH;   // lanes per unit, units per pass
+    __shared__ __align__(16) float tab[3][ROPE_TAB];
+    __shared__ long long s_at[ROPE_ROWS];   // element of a row's first kv head in the pools, -1: nowhere
+    const long long row0 = static_cast<long long>(blockIdx.x) * rpc;
     const int tid = threadIdx.x, c = tid % LPH, hs = tid / LPH;
-    griddep_wait();
-    if (A.n_rows && row >= *A.n_rows) return;
     const int H = A.Hq + A.Hkv + (A.k_out ? 0 : A.Hkv);
-    const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, H);
-    long long slot = 0;
-    if (!A.k_out) {
-        slot = A.slots[row];
+    const int h0 = blockIdx.y * hpc, nh = min(hpc, H - h0);
+    griddep_wait();
+    const long long M = A.n_rows ? min(A.M, max(*A.n_rows, 0)) : A.M;
+    const int nrow = static_cast<int>(min(static_cast<long long>(rpc), M - row0));
+    if (nrow <= 0) return;
+    const int units = nrow * nh;
+    // unit -> (row, head): the product form of the division is exact for unit < 512 (rpc > 1)
+    auto split = [&](int u, int* h) {
+        const int r = rpc > 1 ? static_cast<int>((u * inv_h) >> 16) : 0;
+        *h = h0 + u - r * nh;
+        return r;
+    };
+    uint4 raw[ROPE_U];
+    auto load = [&](int u0) {
+#pragma unroll
+        for (int k = 0; k < ROPE_U; ++k) {
+            const int u = u0 + k * HPP + hs;
+            raw[k] = make_uint4(0, 0, 0, 0);
+            if (u < units) {
+                int h;
+                const long long row = row0 + split(u, &h);
+                raw[k] = *(reinterpret_cast<const uint4*>(h < A.Hq ? A.q + row * A.q_stride + static_cast<long long>(h) * HD
+                                                                   : A.kv + row * A.kv_stride + static_cast<long long>(h - A.Hq) * HD) + c);
+            }
+        }
+    };
+    load(0);
+    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+    if (A.q_norm) wq = __ldg(reinterpret_cast<const uint4*>(A.q_norm) + c);
+    if (A.k_norm) wk = __ldg(reinterpret_cast<const uint4*>(A.k_norm) + c);
+    const int half = A.rot / 2;
+    for (int i = tid; i < nrow * half; i += ROPE_THREADS) {
+        const int r = i / half;
+        const unsigned long long turns = static_cast<unsigned long long>(static_cast<long long>(A.pos[row0 + r])) * A.freq[i - r * half];
+        float sn, cn;
+        sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f, &sn, &cn);
+        tab[0][i] = cn;
+        tab[1][i] = sn;
+        tab[2][i] = -sn;
+    }
+    if (!A.k_out && tid >= ROPE_THREADS - nrow) {
+        const int r = ROPE_THREADS - 1 - tid;
+        long long slot = A.slots[row0 + r];
         if (slot >= A.n_slots || slot < -1) {
-            if (tid == 0 && blockIdx.y == 0) atomicOr(A.err, ERR_BAD_PAGE);
+            if (blockIdx.y == 0) atomicOr(A.err, ERR_BAD_PAGE);
             slot = -1;
         }
-    }
-    if (tid < A.rot / 2) {
-        const unsigned long long turns = static_cast<unsigned long long>(static_cast<long long>(A.pos[row])) * A.freq[tid];
-        float s, co;
-        sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f, &s, &co);
-        cs[tid] = make_float2(co, s);
+        const long long pg = slot / A.page;
+        s_at[r] = slot < 0 ? -1 : (pg * A.Hkv * A.page + (slot - pg * A.page)) * HD;
     }
     __syncthreads();
-    for (int hb = h0; hb < h1; hb += HPP * ROPE_U) {
-        uint4 raw[ROPE_U];
+    // this lane's values of a head meet frequencies f0 ..: 8 of them, or 4 when interleaved
+    const bool in = 8 * c < A.rot, lo = 8 * c < half;
+    const int f0 = INTER ? 4 * c : 8 * c - (lo ? 0 : half);
+    const int lane = tid & 31, partner = !INTER && in ? (lo ? lane + half / 8 : lane - half / 8) : lane;
+    for (int u0 = 0; u0 < units; u0 += HPP * ROPE_U) {
+        if (u0) load(u0);
 #pragma unroll
-        for (int u = 0; u < ROPE_U; ++u) {
-            const int h = hb + u * HPP + hs;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (h < h1) {
-                const uint16_t* src = h < A.Hq ? A.q + row * A.q_stride + static_cast<long long>(h) * HD
-                                               : A.kv + row * A.kv_stride + static_cast<long long>(h - A.Hq) * HD;
-                raw[u] = *reinterpret_cast<const uint4*>(src + c * 8);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < ROPE_U; ++u) {
-            const int h = hb + u * HPP + hs;
-            if (hb + u * HPP >= h1) break;           // the same for the whole CTA
+        for (int k = 0; k < ROPE_U; ++k) {
+            const int u = u0 + k * HPP + hs;
+            if (u0 + k * HPP >= units) break;           // the same for the whole CTA
+            int h;
+            const int r = split(min(u, units - 1), &h);
             const bool isq = h < A.Hq, isv = h >= A.Hq + A.Hkv;
             float x[8];
-            rope_unpack(raw[u], x);
-            const uint16_t* w = isq ? A.q_norm : A.k_norm;
-            float ss = 0.f;
+            rope_unpack(raw[k], x);
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = __fmaf_rn(x[e], x[e], ss);
+            for (int e = 0; e < 8; e += 2) fma2(x[e], x[e + 1], x[e], x[e + 1], s0, s1);
+            float ss = __fadd_rn(s0, s1);
 #pragma unroll
             for (int off = LPH / 2; off > 0; off >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, off));
-            if (w && !isv) {
-                const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.f / HD), A.eps)));
+            if (isq ? A.q_norm != nullptr : A.k_norm != nullptr) {
+                const float inv = rsqrtf(__fmaf_rn(ss, 1.f / HD, A.eps));
                 float wf[8];
-                rope_unpack(*reinterpret_cast<const uint4*>(w + c * 8), wf);
+                rope_unpack(isq ? wq : wk, wf);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], inv), __fadd_rn(1.f, wf[e]));
-            }
-            const int half = A.rot / 2;
-            if (A.inter) {
-                if (8 * c < A.rot && !isv) {
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float2 t = cs[4 * c + e / 2];
-                        const float a = x[e], b = x[e + 1];
-                        x[e] = a * t.x - b * t.y;
-                        x[e + 1] = b * t.x + a * t.y;
-                    }
-                }
-            } else if (A.rot) {
-                // the partner values sit half/8 lanes away in the same head
-                const bool lo = 8 * c < half, in = 8 * c < A.rot;
-                const int lane = tid & 31, partner = in ? (lo ? lane + half / 8 : lane - half / 8) : lane;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float o = __shfl_sync(0xffffffffu, x[e], partner);
-                    if (in && !isv) {
-                        const float2 t = cs[8 * c + e - (lo ? 0 : half)];
-                        x[e] = lo ? x[e] * t.x - o * t.y : x[e] * t.x + o * t.y;
-                    }
+                for (int e = 0; e < 8; e += 2) {
+                    float g0 = inv, g1 = inv;   // inv (1 + w)
+                    fma2(wf[e], wf[e + 1], inv, inv, g0, g1);
+                    mul2(x[e], x[e + 1], g0, g1);
                 }
             }
-            if (h >= h1) continue;
-            const uint4 y = isv ? raw[u] : rope_pack(x);
+            if (half) {
+                if constexpr (INTER) {
+                    if (in) {
+                        const float4 cn = *reinterpret_cast<const float4*>(&tab[0][r * half + f0]);
+                        const float4 sn = *reinterpret_cast<const float4*>(&tab[1][r * half + f0]);
+                        const float cv[4] = {cn.x, cn.y, cn.z, cn.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = x[2 * e], b = x[2 * e + 1];
+                            mul2(x[2 * e], x[2 * e + 1], cv[e], cv[e]);
+                            fma2(-b, a, sv[e], sv[e], x[2 * e], x[2 * e + 1]);
+                        }
+                    }
+                } else {
+                    // the partner values sit half/8 lanes away in the same head
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, x[e], partner);
+                    if (in) {
+                        const float4* ct = reinterpret_cast<const float4*>(&tab[0][r * half + f0]);
+                        const float4* st = reinterpret_cast<const float4*>(&tab[lo ? 2 : 1][r * half + f0]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const float4 cn = ct[q], sn = st[q];
+                            mul2(x[4 * q], x[4 * q + 1], cn.x, cn.y);
+                            mul2(x[4 * q + 2], x[4 * q + 3], cn.z, cn.w);
+                            fma2(o[4 * q], o[4 * q + 1], sn.x, sn.y, x[4 * q], x[4 * q + 1]);
+                            fma2(o[4 * q + 2], o[4 * q + 3], sn.z, sn.w, x[4 * q + 2], x[4 * q + 3]);
+                        }
+                    }
+                }
+            }
+            if (u >= units) continue;
+            const uint4 y = isv ? raw[k] : rope_pack(x);
+            const long long row = row0 + r;
             if (isq) {
                 *reinterpret_cast<uint4*>(A.q_out + row * A.qo_stride + static_cast<long long>(h) * HD + c * 8) = y;
             } else if (A.k_out) {
                 *reinterpret_cast<uint4*>(A.k_out + row * A.ko_stride + static_cast<long long>(h - A.Hq) * HD + c * 8) = y;
-            } else if (slot >= 0) {
+            } else if (s_at[r] >= 0) {
                 const int g = h - A.Hq - (isv ? A.Hkv : 0);
-                const long long pg = slot / A.page, at = slot - pg * A.page;
-                *reinterpret_cast<uint4*>((isv ? A.vpool : A.kpool) + ((pg * A.Hkv + g) * A.page + at) * HD + c * 8) = y;
+                *reinterpret_cast<uint4*>((isv ? A.vpool : A.kpool) + s_at[r] + static_cast<long long>(g) * A.page * HD + c * 8) = y;
             }
         }
     }
@@ -179,13 +239,25 @@ xv_status rope_launch(RopeArgs a, int hd, cudaStream_t s) {
     a.err = device_error_word();
     if (!a.err) return fail(XV_ERR_CUDA, "qk_norm_rope: device error word unavailable");
     const int H = a.Hq + a.Hkv + (a.k_out ? 0 : a.Hkv), hpp = ROPE_THREADS * 8 / hd;
-    int per = H;
-    if (a.M < 1024) per = hpp;
-    const dim3 grid(a.M, ceil_div(H, per));
+    // Few rows: one pass of heads per CTA, so that a row's heads spread over the SMs; more: as many
+    // passes as keep the CTAs to one wave (8 of 256 threads per SM), up to the ROPE_U whose loads go
+    // out together; many rows of few heads: as many rows as fill those passes.  Measured: 500 rows of
+    // 32 heads of 256, one pass 8.7 us, this rule 6.0; 8192 rows of 24 heads of 64, a row per CTA
+    // 30.7 us, this rule 15.0.
+    int sms = 0;
+    if (xv_status st = device_sm_count(&sms)) return st;
+    int hpc = hpp, rpc = 1;
+    while (hpc < ROPE_U * hpp && hpc < H && static_cast<long long>(a.M) * ceil_div(H, hpc) > 8ll * sms) hpc += hpp;
+    if (hpc >= H) {
+        hpc = H;
+        while (rpc < ROPE_ROWS && (rpc + 1) * H <= ROPE_U * hpp && (rpc + 1) * a.rot / 2 <= ROPE_TAB && a.M / (rpc + 1) >= 8 * sms) ++rpc;
+    }
+    const dim3 grid(ceil_div(a.M, rpc), ceil_div(H, hpc));
+    const unsigned inv_h = (65536u + hpc - 1) / hpc;
     trace_pre(s);
-    if (hd == 256) launch_k(qk_norm_rope_kernel<256>, grid, dim3(ROPE_THREADS), 0, s, a, per);
-    else if (hd == 128) launch_k(qk_norm_rope_kernel<128>, grid, dim3(ROPE_THREADS), 0, s, a, per);
-    else launch_k(qk_norm_rope_kernel<64>, grid, dim3(ROPE_THREADS), 0, s, a, per);
+    auto go = [&](auto kern) { launch_k(kern, grid, dim3(ROPE_THREADS), 0, s, a, hpc, rpc, inv_h); };
+    if (a.inter) hd == 256 ? go(qk_norm_rope_kernel<256, true>) : hd == 128 ? go(qk_norm_rope_kernel<128, true>) : go(qk_norm_rope_kernel<64, true>);
+    else hd == 256 ? go(qk_norm_rope_kernel<256, false>) : hd == 128 ? go(qk_norm_rope_kernel<128, false>) : go(qk_norm_rope_kernel<64, false>);
     return launched("qk_norm_rope_kernel", s, K_ROPE, 4ll * a.M * H * hd);
 }
 
