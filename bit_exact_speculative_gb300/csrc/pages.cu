@@ -7,12 +7,15 @@
 // popped is stack entry F + R - 1 - k, so two exclusive sums over the requests (pages pushed, pages
 // popped) tell every request its pages, and a third one (rows) tells every new row its request.
 //
-// Kernel 1 (one CTA) forms the three sums and the new counters; kernel 2 moves the pages and writes
-// the rows, every CTA on its own: an entry it pops is read from the stack below F or, at F and
-// above, from the table row of the request that pushed it, and nothing it reads is written by
-// another CTA (the stack is written at F and above, a table row past its request's held pages, a
-// finished request's row not at all).  Both are latency: a few dependent reads, then a few bytes
-// per row.
+// Up to PG_SMALL requests, one kernel: every CTA forms the three sums for itself in shared memory (a few
+// KB from L2) and takes its share of the requests' page moves and of the rows, a warp's worth at a time.
+// An entry it pops is read from the stack below F or, at F and above, from the table row of the request
+// that pushed it, and nothing it reads is written by another CTA: the stack is written at F and above, a
+// table row past its request's held pages, a finished request's row not at all; the new counters, which
+// may stand in the old ones' place, are written by the CTA that is the last to have read those.
+// More requests: a first kernel (one CTA) leaves the sums in the workspace for the second.
+// All of it is latency, a chain of dependent reads: 8 requests 4.8 us as two kernels and 3.7 as one, 500
+// requests with 9,000 rows 6.8 and 4.8, 1024 requests with 60,000 rows 7.6 and 7.5.
 #include "xv_internal.h"
 #include "xv_ptx.cuh"
 
@@ -21,6 +24,7 @@ namespace {
 
 constexpr int PG_THREADS = 1024;   // kernel 1
 constexpr int PG_WORK = 256;       // kernel 2
+constexpr int PG_SMALL = 1024;     // requests the single kernel takes
 
 struct PagesArgs {
     int32_t* table;
@@ -37,16 +41,24 @@ struct PagesArgs {
     int32_t* pos;
     long long* slots;
     int max_rows;
-    // workspace: [0] free pages before, [1] pages pushed, [2] 1 when pages may be popped, then per
-    // request held pages before, pages needed (-1: finished), first push and first pop
+    // workspace: [0] CTAs that have read the counters (zero between calls); for more than PG_SMALL requests
+    // [1] free pages before, [2] pages pushed, [3] bit 0 pages may be pushed, bit 1 popped, then the sums
     int32_t* ws;
     unsigned* err;
 };
 
-__device__ __forceinline__ int32_t* ws_held(const PagesArgs& A) { return A.ws + 4; }
-__device__ __forceinline__ int32_t* ws_need(const PagesArgs& A) { return A.ws + 4 + A.B; }
-__device__ __forceinline__ int32_t* ws_push(const PagesArgs& A) { return A.ws + 4 + 2ll * A.B; }
-__device__ __forceinline__ int32_t* ws_pop(const PagesArgs& A) { return A.ws + 4 + 3ll * A.B; }
+// The sums over the requests, in the workspace or in shared memory, and what follows from them.
+struct PagesSums {
+    int32_t *held, *need, *push, *pop;   // pages held before; needed (-1: finished); first push; first pop
+    const int32_t* start;                // [B + 1] first rows
+    int F, R;                            // free pages before, pages pushed
+    bool push_ok, pop_ok;
+};
+__device__ __forceinline__ PagesSums ws_sums(const PagesArgs& A) {
+    int32_t* w = A.ws + 4;
+    const long long B = A.B;
+    return PagesSums{w, w + B, w + 2 * B, w + 3 * B, A.row_start, A.ws[1], A.ws[2], (A.ws[3] & 1) != 0, (A.ws[3] & 2) != 0};
+}
 
 // Exclusive sums of three values over the CTA's threads; tot receives the CTA's totals.  Every
 // request's values are at most 2^30, so the sums are formed in 64 bits.
@@ -83,14 +95,14 @@ __device__ __forceinline__ void block_scan3(long long v[3], long long tot[3], lo
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(PG_THREADS) kv_pages_scan_kernel(PagesArgs A) {
-    griddep_launch();
-    griddep_wait();
+// The sums of all requests by one CTA of PG_THREADS, into P's arrays and `start` [B + 1]; rows are
+// clamped to max_rows.  report: record what is out of range, and *popped = the pages popped.
+__device__ __forceinline__ void pages_scan(const PagesArgs& A, PagesSums& P, int32_t* start, bool report, int* popped) {
     __shared__ long long sm[3][33];
     const int tid = threadIdx.x;
     const int F0 = *A.n_free_in;
     const bool sane = F0 >= 0 && F0 <= A.n_pages;
-    const int F = sane ? F0 : 0;
+    P.F = sane ? F0 : 0;
     const long long cap = static_cast<long long>(A.page) * A.max_pages;
     long long carry[3] = {0, 0, 0};   // pushed, popped, rows
     unsigned bad = sane ? 0u : ERR_BAD_COUNT;
@@ -123,36 +135,35 @@ __global__ void __launch_bounds__(PG_THREADS) kv_pages_scan_kernel(PagesArgs A) 
         long long tot[3];
         block_scan3(v, tot, sm);
         if (b < A.B) {
-            ws_held(A)[b] = held;
-            ws_need(A)[b] = need;
+            P.held[b] = held;
+            P.need[b] = need;
             // sums past the pool or past int are refused below; clamp what is stored
-            ws_push(A)[b] = static_cast<int32_t>(min(carry[0] + v[0], 1ll << 30));
-            ws_pop(A)[b] = static_cast<int32_t>(min(carry[1] + v[1], 1ll << 30));
-            A.row_start[b] = static_cast<int32_t>(min(carry[2] + v[2], static_cast<long long>(A.max_rows)));
+            P.push[b] = static_cast<int32_t>(min(carry[0] + v[0], 1ll << 30));
+            P.pop[b] = static_cast<int32_t>(min(carry[1] + v[1], 1ll << 30));
+            start[b] = static_cast<int32_t>(min(carry[2] + v[2], static_cast<long long>(A.max_rows)));
         }
 #pragma unroll
         for (int q = 0; q < 3; ++q) carry[q] += tot[q];
     }
-    const bool push_ok = sane && F + carry[0] <= A.n_pages;
-    const long long R = push_ok ? carry[0] : 0;
-    const bool pop_ok = push_ok && carry[1] <= F + R;
-    if (!push_ok) bad |= ERR_BAD_COUNT;
-    if (push_ok && !pop_ok) bad |= ERR_NO_PAGES;
+    P.push_ok = sane && P.F + carry[0] <= A.n_pages;
+    P.R = P.push_ok ? static_cast<int>(carry[0]) : 0;
+    P.pop_ok = P.push_ok && carry[1] <= P.F + P.R;
+    *popped = P.pop_ok ? static_cast<int>(carry[1]) : 0;
+    if (!P.push_ok) bad |= ERR_BAD_COUNT;
+    if (P.push_ok && !P.pop_ok) bad |= ERR_NO_PAGES;
     if (carry[2] > A.max_rows) bad |= ERR_BAD_COUNT;
-    if (bad) atomicOr(A.err, bad);
-    // held and n_free may be updated in place: every input has been read (each thread re-reads
-    // only its own requests' entries)
-    for (int b = tid; b < A.B; b += PG_THREADS) {
-        const int held = ws_held(A)[b], need = ws_need(A)[b];
-        A.held_out[b] = need < 0 ? (push_ok ? 0 : held) : (pop_ok && need > held ? need : held);
+    if (report && bad) atomicOr(A.err, bad);
+    if (tid == 0) start[A.B] = static_cast<int32_t>(min(carry[2], static_cast<long long>(A.max_rows)));
+    if (!sane) P.F = F0;   // handed back as it is (nothing is popped)
+}
+
+// held and n_free after the call; they may be the arrays the scan has read.
+__device__ __forceinline__ void pages_finish(const PagesArgs& A, const PagesSums& P, int popped) {
+    for (int b = threadIdx.x; b < A.B; b += PG_THREADS) {
+        const int held = P.held[b], need = P.need[b];
+        A.held_out[b] = need < 0 ? (P.push_ok ? 0 : held) : (P.pop_ok && need > held ? need : held);
     }
-    if (tid == 0) {
-        A.ws[0] = F;
-        A.ws[1] = static_cast<int32_t>(R);
-        A.ws[2] = (push_ok ? 1 : 0) | (pop_ok ? 2 : 0);
-        A.row_start[A.B] = static_cast<int32_t>(min(carry[2], static_cast<long long>(A.max_rows)));
-        *A.n_free_out = sane ? static_cast<int32_t>(F + R - (pop_ok ? carry[1] : 0)) : F0;
-    }
+    if (threadIdx.x == 0) *A.n_free_out = P.F + P.R - popped;
 }
 
 // The last request b in [0, B) with start[b] <= x, by a 32-way search of the whole warp (start is
@@ -180,67 +191,114 @@ __device__ __forceinline__ int thread_find(const int32_t* start, int B, int x) {
     return lo;
 }
 
-// Stack entry i of the stack after the pushes (F entries before them).
-__device__ __forceinline__ int stack_entry(const PagesArgs& A, int F, int i) {
-    if (i < F) return A.free_pages[i];
+// Page j of request b after this call, -1 where it has none.
+__device__ __forceinline__ int page_of(const PagesArgs& A, const PagesSums& P, int b, int j) {
+    const int held = P.held[b];
+    if (j < held) return A.table[static_cast<long long>(b) * A.max_pages + j];
+    if (!P.pop_ok) return -1;
+    const int i = P.F + P.R - 1 - (P.pop[b] + j - held);   // entry of the stack after the pushes
+    if (i < P.F) return A.free_pages[i];
     // pushed in this call: the last request that starts at or before it (requests that push
     // nothing share their successor's start, so the last one is the pusher)
-    const int x = i - F, b = thread_find(ws_push(A), A.B, x);
-    const int j = ws_held(A)[b] - 1 - (x - ws_push(A)[b]);
-    return A.table[static_cast<long long>(b) * A.max_pages + j];
+    const int x = i - P.F, p = thread_find(P.push, A.B, x);
+    return A.table[static_cast<long long>(p) * A.max_pages + P.held[p] - 1 - (x - P.push[p])];
 }
 
-// Page j of request b after this call, -1 where it has none.
-__device__ __forceinline__ int page_of(const PagesArgs& A, int F, int R, int flags, int b, int j) {
-    const int held = ws_held(A)[b];
-    if (j < held) return A.table[static_cast<long long>(b) * A.max_pages + j];
-    if (!(flags & 2)) return -1;
-    return stack_entry(A, F, F + R - 1 - (ws_pop(A)[b] + j - held));
+// One warp: the pages request b pushes or pops.
+__device__ __forceinline__ void move_pages(const PagesArgs& A, const PagesSums& P, int b) {
+    const int lane = threadIdx.x & 31, held = P.held[b], need = P.need[b];
+    int32_t* row = A.table + static_cast<long long>(b) * A.max_pages;
+    if (need < 0) {
+        if (!P.push_ok) return;
+        const int top = P.F + P.push[b] + held - 1;
+        for (int j = lane; j < held; j += 32) {
+            const int pg = row[j];
+            if (pg < 0 || pg >= A.n_pages) atomicOr(A.err, ERR_BAD_PAGE);
+            A.free_pages[top - j] = pg;
+        }
+    } else if (P.pop_ok) {
+        for (int j = held + lane; j < need; j += 32) {
+            const int pg = page_of(A, P, b, j);
+            if (pg < 0 || pg >= A.n_pages) atomicOr(A.err, ERR_BAD_PAGE);
+            row[j] = pg;
+        }
+    }
 }
 
-// CTAs [0, seq_ctas): a warp per request moves its pages.  The others: a warp per 32 new rows.
-__global__ void __launch_bounds__(PG_WORK) kv_pages_write_kernel(PagesArgs A, int seq_ctas) {
+// One warp: position and slot of rows t0 .. t0 + 31.
+__device__ __forceinline__ void write_rows(const PagesArgs& A, const PagesSums& P, int t0, int total) {
+    int b = warp_find(P.start, A.B, t0);
+    const int t = t0 + (threadIdx.x & 31);
+    if (t < total) {
+        while (b + 1 < A.B && P.start[b + 1] <= t) ++b;
+        const int p = A.ctx_len[b] + t - P.start[b], j = p / A.page;
+        int pg = page_of(A, P, b, j);
+        if (pg < -1 || pg >= A.n_pages || (pg < 0 && P.pop_ok)) {
+            atomicOr(A.err, ERR_BAD_PAGE);
+            pg = -1;
+        }
+        A.pos[t] = p;
+        A.slots[t] = pg < 0 ? -1 : static_cast<long long>(pg) * A.page + (p - j * A.page);
+    }
+    __syncwarp();
+}
+
+__global__ void __launch_bounds__(PG_THREADS) kv_pages_kernel(const __grid_constant__ PagesArgs A) {
+    griddep_launch();
+    __shared__ int32_t held[PG_SMALL], need[PG_SMALL], push[PG_SMALL], pop[PG_SMALL], start[PG_SMALL + 1];
+    __shared__ bool last;
+    griddep_wait();
+    PagesSums P{held, need, push, pop, start, 0, 0, false, false};
+    int popped;
+    pages_scan(A, P, start, blockIdx.x == 0, &popped);
+    __syncthreads();
+    if (threadIdx.x == 0) {   // this CTA has read held and n_free
+        const unsigned n = atomicAdd(reinterpret_cast<unsigned*>(A.ws), 1u);
+        last = n + 1 == gridDim.x;
+        if (last) *A.ws = 0;
+    }
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b <= A.B; b += PG_THREADS) A.row_start[b] = start[b];
+    const int total = start[A.B], W = gridDim.x * (PG_THREADS / 32);
+    const long long tasks = A.B + (total + 31ll) / 32;
+    for (long long t = blockIdx.x * (PG_THREADS / 32) + (threadIdx.x >> 5); t < tasks; t += W) {
+        if (t < A.B) move_pages(A, P, static_cast<int>(t));
+        else write_rows(A, P, static_cast<int>(t - A.B) * 32, total);
+    }
+    __syncthreads();
+    if (last) pages_finish(A, P, popped);
+}
+
+__global__ void __launch_bounds__(PG_THREADS) kv_pages_scan_kernel(const __grid_constant__ PagesArgs A) {
     griddep_launch();
     griddep_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int F = A.ws[0], R = A.ws[1], flags = A.ws[2];
+    int32_t* w = A.ws + 4;
+    const long long B = A.B;
+    PagesSums P{w, w + B, w + 2 * B, w + 3 * B, A.row_start, 0, 0, false, false};
+    int popped;
+    pages_scan(A, P, A.row_start, true, &popped);
+    pages_finish(A, P, popped);   // a thread reads the entries it wrote itself
+    if (threadIdx.x == 0) {
+        A.ws[1] = P.F;
+        A.ws[2] = P.R;
+        A.ws[3] = (P.push_ok ? 1 : 0) | (P.pop_ok ? 2 : 0);
+    }
+}
+
+// CTAs [0, seq_ctas): a warp per request.  The others: a warp per 32 new rows.
+__global__ void __launch_bounds__(PG_WORK) kv_pages_write_kernel(const __grid_constant__ PagesArgs A, int seq_ctas) {
+    griddep_launch();
+    griddep_wait();
+    const int w = threadIdx.x >> 5;
+    const PagesSums P = ws_sums(A);
     if (static_cast<int>(blockIdx.x) < seq_ctas) {
         const int b = blockIdx.x * (PG_WORK / 32) + w;
-        if (b >= A.B) return;
-        const int held = ws_held(A)[b], need = ws_need(A)[b];
-        int32_t* row = A.table + static_cast<long long>(b) * A.max_pages;
-        if (need < 0) {
-            if (!(flags & 1)) return;
-            const int top = F + ws_push(A)[b] + held - 1;
-            for (int j = lane; j < held; j += 32) {
-                const int pg = row[j];
-                if (pg < 0 || pg >= A.n_pages) atomicOr(A.err, ERR_BAD_PAGE);
-                A.free_pages[top - j] = pg;
-            }
-        } else if (flags & 2) {
-            for (int j = held + lane; j < need; j += 32) {
-                const int pg = page_of(A, F, R, flags, b, j);
-                if (pg < 0 || pg >= A.n_pages) atomicOr(A.err, ERR_BAD_PAGE);
-                row[j] = pg;
-            }
-        }
+        if (b < A.B) move_pages(A, P, b);
         return;
     }
     const int total = A.row_start[A.B];
     const int t0 = ((static_cast<int>(blockIdx.x) - seq_ctas) * (PG_WORK / 32) + w) * 32;
-    if (t0 >= total) return;
-    int b = warp_find(A.row_start, A.B, t0);
-    const int t = t0 + lane;
-    if (t >= total) return;
-    while (b + 1 < A.B && A.row_start[b + 1] <= t) ++b;
-    const int p = A.ctx_len[b] + t - A.row_start[b], j = p / A.page;
-    int pg = page_of(A, F, R, flags, b, j);
-    if (pg < -1 || pg >= A.n_pages || (pg < 0 && (flags & 2))) {
-        atomicOr(A.err, ERR_BAD_PAGE);
-        pg = -1;
-    }
-    A.pos[t] = p;
-    A.slots[t] = pg < 0 ? -1 : static_cast<long long>(pg) * A.page + (p - j * A.page);
+    if (t0 < total) write_rows(A, P, t0, total);
 }
 
 }  // namespace
@@ -272,6 +330,15 @@ xv_status xv_kv_pages_update(int32_t* page_table, int page_size, int max_pages, 
     PagesArgs a{page_table, kv.page, kv.max_pages, kv.n_pages, free_pages, n_free, n_free_out, held, held_out, ctx_len,
                 n_new, B, row_start, pos, slots, max_rows, static_cast<int32_t*>(ws), err};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
+    if (B <= PG_SMALL) {
+        // a warp task per request and per 32 rows, 32 to a CTA, up to an SM's worth of CTAs each
+        int sms = 0;
+        if (xv_status e = device_sm_count(&sms)) return e;
+        const int ctas = ceil_div(B + (max_rows + 31ll) / 32, PG_THREADS / 32);
+        trace_pre(st);
+        launch_k(kv_pages_kernel, dim3(ctas < sms ? ctas : sms), dim3(PG_THREADS), 0, st, a);
+        return launched("kv_pages_kernel", st, K_PAGES, 12ll * max_rows + 48ll * B);
+    }
     trace_pre(st);
     launch_k(kv_pages_scan_kernel, dim3(1), dim3(PG_THREADS), 0, st, a);
     if (xv_status e = launched("kv_pages_scan_kernel", st, K_PAGES, 32ll * B)) return e;
