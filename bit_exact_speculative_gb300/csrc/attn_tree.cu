@@ -58,14 +58,16 @@ struct TreeShape {
     static constexpr int V_OFF = K_OFF + SK * TILE_BYTES;
     static constexpr int PB_OFF = V_OFF + SV * TILE_BYTES;
     static constexpr int BAR_OFF = PB_OFF + (PB_IN_K ? 0 : 2 * QBLK);
-    static constexpr int N_BARS = 2 * SK + 2 * SV + 28;
+    static constexpr int N_BARS = 2 * SK + 2 * SV + 29;
     static constexpr int M_OFF = BAR_OFF + 8 * ((N_BARS + 1) / 2 * 2);   // float[128]
     static constexpr int SUM_OFF = M_OFF + 512;                          // float[2][128]
     static constexpr int INFO_OFF = SUM_OFF + 1024;
     // the plan needs its base on a 1024-byte boundary: dynamic shared memory starts on one (it is all
     // this kernel has); with room to spare a full kilobyte of slack is taken all the same
     static constexpr int SLACK = HD == 256 ? 0 : 1024;
-    // tensor-memory columns: S[2] (64 each), O (HD), the tree's scores (64), P[2] (32 each)
+    // tensor-memory columns: S[2] (64 each), O (HD; at hd 64 and 128 two of them, item by item), the
+    // tree's scores (64), P[2] (32 each)
+    static constexpr int NO = HD == 256 ? 1 : 2;
     static constexpr uint32_t TMEM_COLS = 512;
 };
 
@@ -536,7 +538,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // filled; its blocks gathered; its V tiles requested (every stage's last use but one is then
     // complete, so the gather's waits on the stages are never two phases behind)
     const uint32_t tbar = bx + 8u * 14, tfree = bx + 8u * 15, tready = bx + 8u * 16, vdone = bx + 8u * 17, vgo = bx + 8u * 18;
-    const uint32_t qfull = bx + 8u * 19, qdone = bx + 8u * 20, ofree = bx + 8u * 21, done = bx + 8u * 22;
+    const uint32_t qfull = bx + 8u * 19, qdone = bx + 8u * 20, done = bx + 8u * 22;
+    auto ofree = [&](int j) { return bx + 8u * (j ? 28 : 21); };   // by O buffer: read out
     // by the parity of group 1's tile: its sum is in shared memory.  Two of them, as group 1 may end its
     // next tile before group 0 comes to take this one's sum.
     auto spub = [&](int j) { return bx + 8u * (23 + j); };
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const int j = tid - (2 * SK + 2 * SV);
         const int count = j < 0 ? (tid >= 2 * SK && tid < 2 * SK + SV ? 5 : 1)   // fullV: the gather's warps and V's
                           : j == 2 || j == 3 || j == 4 || j == 5 || j == 8 || j == 9 || j == 10 || j == 11 ? 128
-                          : j == 23 || j == 24 || j == 21                               ? 128
+                          : j == 23 || j == 24 || j == 21 || j == 28                    ? 128
                           : j == 15                                                     ? 128 + 1 + 1 + 4   // group 0, P V, V, group 1's warps
                           : j == 17                                                     ? 4
                                                                                         : 1;
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // only now: a dependent kernel must not take the tensor memory this one still has to allocate
     griddep_launch();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tS = tmem, tO = tmem + 128, tT = tmem + 128 + HD, tP = tT + 64;
+    const uint32_t tS = tmem, tO0 = tmem + 128, tT = tO0 + S::NO * HD, tP = tT + 64;
 
     // bounded waits; after the first one that gives up, every later one that would have to wait returns at once
     auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || tree_wait(bar, par, A.err, &s_abort); };
@@ -784,8 +787,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 if (!I.live) continue;
                 const int nreg = I.kreg();
                 bool first_pv = true;
-                // an item's first step overwrites O: the epilogue before it has read it
-                auto begin_pv = [&]() -> bool { return !first_pv || nitem == 0 || W(ofree, (nitem - 1) & 1u); };
+                const int ob = nitem % S::NO;
+                const uint32_t tO = tO0 + ob * HD;
+                // an item's first step overwrites its O buffer: the epilogue before has read it
+                auto begin_pv = [&]() -> bool { return !first_pv || nitem < S::NO || W(ofree(ob), (nitem / S::NO - 1) & 1u); };
 #pragma unroll 1
                 for (int i = 0; i < nreg; ++i) {
                     const bool odd = i < I.nfull && (i & 1);
@@ -853,8 +858,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int nl = rho / A.G, gh = rho - nl * A.G;
         // n: own tiles; n1 (group 0): tiles of group 1 taken; n0 (group 1): tiles of group 0 in the
-        // items before; npub (group 1): maxima taken from group 0; tv (group 1): V tiles and block steps
-        int n = 0, n1 = 0, n0 = 0, npub = 0, bs = 0, nt = 0, tk = 0, tv = 0;
+        // items before; npub (group 1): maxima taken from group 0; tv (group 1): V tiles and block steps;
+        // nitem: items with a P V step
+        int n = 0, n1 = 0, n0 = 0, npub = 0, bs = 0, nt = 0, tk = 0, tv = 0, nitem = 0;
+        uint32_t tO = tO0;
         bool ok = true;
         // O (once a P V step of the item has been issued; `bar` completes with its last) times al
         auto rescale = [&](float al, bool any_pv, uint32_t bar, uint32_t par) -> bool {
@@ -873,6 +880,41 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             tmem_st_wait();
             return true;
         };
+        // O of an item to its rows' partials (null: a row without one), once its last P V step has
+        // completed.  A lane holds 32 columns of its own row; eight lanes exchange 16-byte pieces so
+        // that each store instruction writes whole 128-byte lines of four rows (a row per lane wrote
+        // half sectors: 5 us for the 128 KB of a full item at hd 256).
+        auto store_o = [&](float* op) {
+            u64 rowp[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rowp[j] = __shfl_sync(0xffffffffu, reinterpret_cast<u64>(op), (lane & 24) + j);
+            const int b8 = lane & 7;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                float o[32];
+                __syncwarp();
+                tmem_ld16(tO + lane_off + c * 32, o);
+                tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
+                tmem_ld_wait();
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (!(j & d))
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool up = b8 & d;
+                                const float y = __shfl_xor_sync(0xffffffffu, up ? o[4 * j + e] : o[4 * (j | d) + e], d);
+                                if (up) o[4 * j + e] = y;
+                                else o[4 * (j | d) + e] = y;
+                            }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (rowp[j])
+                        *(reinterpret_cast<float4*>(rowp[j]) + c * 8 + b8) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+            tc_fence_before();
+        };
         // P of the group's tile into tensor memory, once the P V step of its tile before has read it
         auto write_p = [&](const uint32_t* pk) -> bool {
             if (n > 0 && !WW(pfree(grp, n - 1), ((n - 1) >> 1) & 1u)) return false;
@@ -885,6 +927,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!I.live) continue;
             const int node = I.node0(A.NT) + nl;
             const bool valid = nl < A.NT && node < I.n;
+            const long long brow = static_cast<long long>(I.b) * A.N + node, idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
+            tO = tO0 + nitem % S::NO * HD;
             float m = NEG_INF, l = 0.f;
             // group 0: the maximum and, when its own exponentials are done, the sum of the odd tile
             // before its next one or the item's end
@@ -951,9 +995,19 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 // block per warp
                 n0 += (I.nfull + 1) / 2 + (I.tail0 && I.c > 0 ? 1 : 0);
                 tv += I.vreg();
-                if (!I.tail()) continue;
+                if (!I.tail()) {
+                    // a split below ctx: whole tiles, an even number, the last one this group's.  Its O
+                    // is read out here while group 0 begins the next item.
+                    if (!WW(pfree(1, n - 1), ((n - 1) >> 1) & 1u)) break;
+                    tc_fence_after();
+                    store_o(valid ? A.opart + idx * HD : nullptr);
+                    mbar_arrive(ofree(nitem % S::NO));
+                    ++nitem;
+                    continue;
+                }
                 if (!WW(vgo, nt & 1u) || !WW(tready, nt & 1u)) break;
                 ++nt;
+                if (I.nfull > 0 || I.tail0 || info.nb1 > 0) ++nitem;   // a tail tile always has a block
 #pragma unroll 1
                 for (int half = 0; ok && half < 2; ++half) {
                     if (half ? !I.tail1 : !I.tail0) continue;
@@ -978,6 +1032,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             const bool last_odd = I.nfull > 0 && !(I.nfull & 1);
             if (last_odd && (!take_max() || !take_sum())) break;
             // completes with the last P V step of the item's whole tiles
+            if (!I.tail()) {
+                if (valid) A.ml[idx] = make_float2(m, l);
+                ++nitem;
+                tk += I.kreg();
+                continue;
+            }
             const int last = (last_odd ? n1 : n) - 1;
             const uint32_t last_bar = pfree(last_odd, last), last_par = (last >> 1) & 1u;
             const int tail_st = (tk + I.kreg()) % SK;   // K stage of the tree's tile
@@ -1144,7 +1204,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             }
             // ---- epilogue: m, l and O of the rows that reach into this split
             const bool live = valid && (!I.tail() || I.ctx - I.c + npos >= I.p_begin);
-            const long long brow = static_cast<long long>(I.b) * A.N + node;
             if (I.tail0 && valid && I.g == 0 && gh == 0) A.nsp[brow] = attn_split_count(I.ctx - I.c + npos + 1);
             if (any_pv || any_block) {
                 if (!(any_block ? WW(bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u) : WW(last_bar, last_par))) break;
@@ -1155,39 +1214,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     vbad = info.vbad;
                     cbad = info.cbad;
                 }
-                const long long idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
                 float* op = A.opart + idx * HD;
-                // A lane holds 32 columns of its own row; eight lanes exchange 16-byte pieces so that
-                // each store instruction writes whole 128-byte lines of four rows (a row per lane wrote
-                // half sectors: 5 us for the 128 KB of a full item at hd 256)
-                u64 rowp[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) rowp[j] = __shfl_sync(0xffffffffu, live ? reinterpret_cast<u64>(op) : 0ull, (lane & 24) + j);
-                const int b8 = lane & 7;
-#pragma unroll 1
-                for (int c = 0; c < HD / 32; ++c) {
-                    float o[32];
-                    __syncwarp();
-                    tmem_ld16(tO + lane_off + c * 32, o);
-                    tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int d = 1; d < 8; d <<= 1)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (!(j & d))
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const bool up = b8 & d;
-                                    const float y = __shfl_xor_sync(0xffffffffu, up ? o[4 * j + e] : o[4 * (j | d) + e], d);
-                                    if (up) o[4 * j + e] = y;
-                                    else o[4 * (j | d) + e] = y;
-                                }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (rowp[j])
-                            *(reinterpret_cast<float4*>(rowp[j]) + c * 8 + b8) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                }
+                store_o(live ? op : nullptr);
                 if (vbad || cbad) {
                     __syncwarp();   // the rows' partials were written by other lanes
                     const TreeBad F{path, in0, vbad, cbad, cnz, m0, m, tT + lane_off, I.tail0, I.tail1, I.b, I.g, I.ctx, I.c, HD,
@@ -1195,8 +1223,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     tree_add_bad(A, F);
                 }
                 if (live) A.ml[idx] = make_float2(m, l);
-                tc_fence_before();
-                mbar_arrive(ofree);
+                mbar_arrive(ofree(nitem % S::NO));
+                ++nitem;
             }
             if (I.tail()) {
                 mbar_arrive(tfree);
