@@ -90,7 +90,7 @@ struct TreeArgs {
     long long out_stride;
     unsigned* err;
     int G, NT, nrt, nsplit;   // q heads per kv head; nodes per row tile, row tiles, splits the launch is sized for
-    float* opart;             // [B*N*Hq][nsplit][HD]
+    float* opart;             // partial outputs, [B][Hkv][nsplit][row tile][HD / 4][rows of the tile][4]
     float2* ml;               // [B*N*Hq][nsplit]
     int32_t* nsp;             // [B*N] splits of each node's rows
 };
@@ -472,13 +472,16 @@ struct TreeBad {
     float m0, m1;      // reference maxima of the tail tile and of the tile after it
     uint32_t scores;   // the row's tree scores in tensor memory
     bool use0, use1;   // which of the two tiles this split holds
-    int b, g, ctx, c, hd;
+    int b, g, ctx, c, hd, pitch;
     float* op;
 };
 __device__ __noinline__ void tree_add_bad(const TreeArgs& A, const TreeBad& F) {
     auto add = [&](const uint16_t* v, float p) {
         for (int k = 0; k < F.hd; ++k)
-            if ((v[k] & 0x7F80) == 0x7F80) F.op[k] = __fmaf_rn(p, bf16_to_f32(v[k]), F.op[k]);
+            if ((v[k] & 0x7F80) == 0x7F80) {
+                float& o = F.op[(k >> 2) * F.pitch + (k & 3)];
+                o = __fmaf_rn(p, bf16_to_f32(v[k]), o);
+            }
     };
     for (u64 e = F.vbad; e; e &= e - 1) {
         const int i = __ffsll(static_cast<long long>(e)) - 1;
@@ -556,12 +559,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // barrier i of the list above; the stages' barriers come first
     if (tid < S::N_BARS && base - raw <= S::SLACK) {
         const int j = tid - (2 * SK + 2 * SV);
-        const int count = j < 0 ? (tid >= 2 * SK && tid < 2 * SK + SV ? 5 : 1)   // fullV: the gather's warps and V's
-                          : j == 2 || j == 3 || j == 4 || j == 5 || j == 8 || j == 9 || j == 10 || j == 11 ? 128
-                          : j == 23 || j == 24 || j == 21 || j == 28                    ? 128
-                          : j == 15                                                     ? 128 + 1 + 1 + 4   // group 0, P V, V, group 1's warps
-                          : j == 17                                                     ? 4
-                                                                                        : 1;
+        // arrivals: 1 where a thread or the hardware arrives; a softmax group's 128 on sfree, pready,
+        // mpub, bready, spub and ofree
+        constexpr u64 BY_GROUP = 0x11A00F3Cull;
+        int count = 1;
+        if (j < 0) count = tid >= 2 * SK && tid < 2 * SK + SV ? 5 : 1;   // fullV: the gather's warps and V's
+        else if ((BY_GROUP >> j) & 1) count = 128;
+        else if (j == 15) count = 128 + 1 + 1 + 4;   // tfree: group 0, P V, V, group 1's warps
+        else if (j == 17) count = 4;                 // vdone: group 1's warps
         mbar_init(bar0 + 8u * tid, count);
         fence_mbar_init();
     }
@@ -862,6 +867,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         // nitem: items with a P V step
         int n = 0, n1 = 0, n0 = 0, npub = 0, bs = 0, nt = 0, tk = 0, tv = 0, nitem = 0;
         uint32_t tO = tO0;
+        int pitch = 0;   // floats between a row's pieces of four columns in the partials
         bool ok = true;
         // O (once a P V step of the item has been issued; `bar` completes with its last) times al
         auto rescale = [&](float al, bool any_pv, uint32_t bar, uint32_t par) -> bool {
@@ -881,37 +887,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             return true;
         };
         // O of an item to its rows' partials (null: a row without one), once its last P V step has
-        // completed.  A lane holds 32 columns of its own row; eight lanes exchange 16-byte pieces so
-        // that each store instruction writes whole 128-byte lines of four rows (a row per lane wrote
-        // half sectors: 5 us for the 128 KB of a full item at hd 256).
+        // completed.  The partials hold four columns of a tile's rows side by side, so a lane writes its
+        // own row and a warp whole 128-byte lines (with [row][HD] partials, rows transposed by shuffles,
+        // the 128 columns of a warp took 4700 cycles).
         auto store_o = [&](float* op) {
-            u64 rowp[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) rowp[j] = __shfl_sync(0xffffffffu, reinterpret_cast<u64>(op), (lane & 24) + j);
-            const int b8 = lane & 7;
+            if (__any_sync(0xffffffffu, op != nullptr)) {
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-                float o[32];
-                __syncwarp();
-                tmem_ld16(tO + lane_off + c * 32, o);
-                tmem_ld16(tO + lane_off + c * 32 + 16, o + 16);
-                tmem_ld_wait();
+                for (int c = 0; c < HD / 64; ++c) {
+                    float o[64];
+                    tmem_ld64(tO + lane_off + c * 64, o);
+                    if (op)
 #pragma unroll
-                for (int d = 1; d < 8; d <<= 1)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!(j & d))
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const bool up = b8 & d;
-                                const float y = __shfl_xor_sync(0xffffffffu, up ? o[4 * j + e] : o[4 * (j | d) + e], d);
-                                if (up) o[4 * j + e] = y;
-                                else o[4 * (j | d) + e] = y;
-                            }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (rowp[j])
-                        *(reinterpret_cast<float4*>(rowp[j]) + c * 8 + b8) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 16; ++j)
+                            *reinterpret_cast<float4*>(op + (c * 16 + j) * pitch) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
             }
             tc_fence_before();
         };
@@ -928,6 +917,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             const int node = I.node0(A.NT) + nl;
             const bool valid = nl < A.NT && node < I.n;
             const long long brow = static_cast<long long>(I.b) * A.N + node, idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
+            const int tile0 = I.rt * A.NT, tile_rows = min(A.NT, A.N - tile0) * A.G;
+            float* const part = A.opart + (((static_cast<long long>(I.b) * A.Hkv + I.g) * A.nsplit + I.split) * A.N + tile0) * A.G * HD + rho * 4;
+            pitch = tile_rows * 4;
             tO = tO0 + nitem % S::NO * HD;
             float m = NEG_INF, l = 0.f;
             // group 0: the maximum and, when its own exponentials are done, the sum of the odd tile
@@ -1000,7 +992,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     // is read out here while group 0 begins the next item.
                     if (!WW(pfree(1, n - 1), ((n - 1) >> 1) & 1u)) break;
                     tc_fence_after();
-                    store_o(valid ? A.opart + idx * HD : nullptr);
+                    store_o(valid ? part : nullptr);
                     mbar_arrive(ofree(nitem % S::NO));
                     ++nitem;
                     continue;
@@ -1214,12 +1206,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     vbad = info.vbad;
                     cbad = info.cbad;
                 }
-                float* op = A.opart + idx * HD;
-                store_o(live ? op : nullptr);
+                store_o(live ? part : nullptr);
                 if (vbad || cbad) {
-                    __syncwarp();   // the rows' partials were written by other lanes
-                    const TreeBad F{path, in0, vbad, cbad, cnz, m0, m, tT + lane_off, I.tail0, I.tail1, I.b, I.g, I.ctx, I.c, HD,
-                                    live ? op : nullptr};
+                    const TreeBad F{path, in0, vbad, cbad, cnz, m0, m, tT + lane_off, I.tail0, I.tail1, I.b, I.g, I.ctx, I.c, HD, pitch,
+                                    live ? part : nullptr};
                     tree_add_bad(A, F);
                 }
                 if (live) A.ml[idx] = make_float2(m, l);
@@ -1242,60 +1232,75 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 }
 
 // Combine of a row's splits, the decode rows' operations: w_s = exp2(m_s - M), L += w_s l_s,
-// acc += w_s o_s in split order, out = acc / L (and the output gate).  A warp owns 64 columns of a row,
-// two per lane.  It reads the row's m and l 32 splits at a time, a split per lane, and forms each
-// weight once; 16 splits' partials are in flight per lane.
+// acc += w_s o_s in split order, out = acc / L (and the output gate).  A warp owns 16 columns of eight
+// rows, four per lane: each of its loads takes whole 128-byte lines of the partials.  The four lanes of a
+// row read its m and l and form its weights, each weight once a warp; eight splits are in flight.
 constexpr int COMB_THREADS = 128;
 
 __global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const __grid_constant__ TreeArgs A, int hd) {
     griddep_launch();
     griddep_wait();
-    const int per = hd / 64, lane = threadIdx.x & 31;   // warps per row
-    const long long wid = static_cast<long long>(blockIdx.x) * (COMB_THREADS / 32) + (threadIdx.x >> 5), row = wid / per;
-    if (row >= static_cast<long long>(A.B) * A.N * A.Hq) return;
-    const long long br = row / A.Hq;
-    const int h = static_cast<int>(row - br * A.Hq), b = static_cast<int>(br / A.N), i = static_cast<int>(br - static_cast<long long>(b) * A.N);
+    // rows here run node by node within a sequence and kv head: [B][Hkv][N][G]
+    const int per = hd / 16, lane = threadIdx.x & 31, row8 = lane & 7, c4 = lane >> 3;
+    const int wid = static_cast<int>(blockIdx.x) * (COMB_THREADS / 32) + (threadIdx.x >> 5);
+    const int rows = A.N * A.G, groups = (rows + 7) / 8;
+    const int col = wid % per * 16 + 4 * c4, bg = wid / per / groups, r = (wid / per - bg * groups) * 8 + row8;
+    const int b = bg / A.Hkv, g = bg - b * A.Hkv;
+    if (b >= A.B) return;
     const int ctx = A.ctx_len[b], n = A.n_nodes ? A.n_nodes[b] : A.N;
-    if (ctx < 0 || ctx > A.max_ctx || i >= n) return;   // reported by the split kernel
-    const int ns = min(A.nsp[br], A.nsplit), d = static_cast<int>(wid - row * per) * 64 + 2 * lane;
-    const float2* ml = A.ml + row * A.nsplit;
-    const float* op = A.opart + row * A.nsplit * hd + d;
+    const int i = r / A.G, h = g * A.G + r - i * A.G;
+    const bool on = r < rows && i < n && ctx >= 0 && ctx <= A.max_ctx;   // else reported by the split kernel
+    const long long br = static_cast<long long>(b) * A.N + i;
+    const int ns = on ? min(A.nsp[br], A.nsplit) : 0, ns_max = __reduce_max_sync(0xffffffffu, ns);
+    const float2* ml = A.ml + (br * A.Hq + h) * A.nsplit;
+    const int tile0 = i / A.NT * A.NT, pitch = min(A.NT, A.N - tile0) * A.G * 4;   // of its row tile
+    const long long split_len = static_cast<long long>(rows) * hd;
+    const float* op = A.opart + static_cast<long long>(bg) * A.nsplit * split_len + static_cast<long long>(tile0) * A.G * hd +
+                      static_cast<long long>(col / 4) * pitch + (r - tile0 * A.G) * 4;
     float M = NEG_INF;
-    for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[s].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float L = 0.f, a0 = 0.f, a1 = 0.f;
-    constexpr int U = 16;
-    for (int s0 = 0; s0 < ns; s0 += 32) {
-        const float2 v = s0 + lane < ns ? ml[s0 + lane] : make_float2(NEG_INF, 0.f);
-        const float w = exp2f(__fsub_rn(v.x, M)), wl = __fmul_rn(w, v.y);
+#pragma unroll 4
+    for (int s = c4; s < ns; s += 4) M = fmaxf(M, ml[s].x);
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+    float L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 8;
 #pragma unroll 1
-        for (int t0 = 0; t0 < 32 && s0 + t0 < ns; t0 += U) {
-            float2 o[U];
+    for (int s0 = 0; s0 < ns_max; s0 += U, op += U * split_len) {
+        float4 o[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (s0 + t0 + u < ns) o[u] = *reinterpret_cast<const float2*>(op + static_cast<long long>(s0 + t0 + u) * hd);
+        for (int u = 0; u < U; ++u)
+            if (s0 + u < ns) o[u] = *reinterpret_cast<const float4*>(op + u * split_len);
+        float w[U / 4], wl[U / 4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float x = __shfl_sync(0xffffffffu, w, t0 + u), xl = __shfl_sync(0xffffffffu, wl, t0 + u);
-                if (s0 + t0 + u < ns) {
-                    L = __fadd_rn(L, xl);
-                    a0 = __fadd_rn(a0, __fmul_rn(x, o[u].x));
-                    a1 = __fadd_rn(a1, __fmul_rn(x, o[u].y));
-                }
+        for (int k = 0; k < U / 4; ++k) {
+            const float2 v = s0 + 4 * k + c4 < ns ? ml[s0 + 4 * k + c4] : make_float2(NEG_INF, 0.f);
+            w[k] = exp2f(__fsub_rn(v.x, M));
+            wl[k] = __fmul_rn(w[k], v.y);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float x = __shfl_sync(0xffffffffu, w[u / 4], u % 4 * 8 + row8), xl = __shfl_sync(0xffffffffu, wl[u / 4], u % 4 * 8 + row8);
+            if (s0 + u < ns) {
+                L = __fadd_rn(L, xl);
+                a[0] = __fadd_rn(a[0], __fmul_rn(x, o[u].x));
+                a[1] = __fadd_rn(a[1], __fmul_rn(x, o[u].y));
+                a[2] = __fadd_rn(a[2], __fmul_rn(x, o[u].z));
+                a[3] = __fadd_rn(a[3], __fmul_rn(x, o[u].w));
             }
         }
     }
-    float y0 = __fdiv_rn(a0, L), y1 = __fdiv_rn(a1, L);
-    const long long col = static_cast<long long>(h) * hd + d;
-    if (A.gate) {
-        const uint16_t* gp = A.gate + br * A.gate_stride + col;
-        y0 = __fmul_rn(bf16_to_f32(f32_to_bf16(y0)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(gp[0])))));
-        y1 = __fmul_rn(bf16_to_f32(f32_to_bf16(y1)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(gp[1])))));
+    if (!on) return;
+    const long long c = static_cast<long long>(h) * hd + col;
+    uint16_t* out = A.out + br * A.out_stride + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float y = __fdiv_rn(a[e], L);
+        if (A.gate) {
+            const float t = bf16_to_f32(A.gate[br * A.gate_stride + c + e]);
+            y = __fmul_rn(bf16_to_f32(f32_to_bf16(y)), __frcp_rn(__fadd_rn(1.f, expf(-t))));
+        }
+        out[e] = f32_to_bf16(y);
     }
-    uint16_t* out = A.out + br * A.out_stride + col;
-    out[0] = f32_to_bf16(y0);
-    out[1] = f32_to_bf16(y1);
 }
 
 inline size_t r256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1360,7 +1365,8 @@ xv_status tree_launch(TreeArgs a, int hd, void* ws, cudaStream_t s) {
     if (st) return st;
     const long long nrow = static_cast<long long>(a.B) * a.N * a.Hq;
     trace_pre(s);
-    launch_k(attn_tree_combine_kernel, dim3(ceil_div(nrow * (hd / 64), COMB_THREADS / 32)), dim3(COMB_THREADS), 0, s, a, hd);
+    const long long warps = static_cast<long long>(a.B) * a.Hkv * ((a.N * a.G + 7) / 8) * (hd / 16);
+    launch_k(attn_tree_combine_kernel, dim3(static_cast<unsigned>(ceil_div(warps, COMB_THREADS / 32))), dim3(COMB_THREADS), 0, s, a, hd);
     return launched("attn_tree_combine_kernel", s, K_ATTN_TREE, 4ll * nrow * a.nsplit * (hd + 2) + 2ll * nrow * hd * (a.gate ? 2 : 1));
 }
 
