@@ -608,8 +608,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // only now: a dependent kernel must not take the tensor memory this one still has to allocate
-    griddep_launch();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO0 = tmem + 128, tT = tO0 + S::NO * HD, tP = tT + 64;
 
@@ -776,6 +774,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     }
                 }
             }
+            // only now: the combine's CTAs, launched as the first SMs fall idle, would all crowd onto those
+            // (16 nodes at 131072 positions: 131 us, so 111)
+            griddep_launch();
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             drain(done, 0u);
         }
@@ -1258,7 +1259,7 @@ __global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const _
     const float* op = A.opart + static_cast<long long>(bg) * A.nsplit * split_len + static_cast<long long>(tile0) * A.G * hd +
                       static_cast<long long>(col / 4) * pitch + (r - tile0 * A.G) * 4;
     float M = NEG_INF;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = c4; s < ns; s += 4) M = fmaxf(M, ml[s].x);
     M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
     M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
