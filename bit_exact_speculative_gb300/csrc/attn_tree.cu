@@ -111,6 +111,17 @@ struct TreeItem {
     __device__ __forceinline__ int node0(int NT) const { return rt * NT; }
 };
 
+// what follows from b, rt and split
+__device__ __forceinline__ void tree_item_split(TreeItem& I, int NT) {
+    I.p_begin = attn_split_begin(I.split);
+    const int p_end = attn_split_begin(I.split + 1), t0 = I.ctx - I.c;
+    I.nfull = I.p_begin < t0 ? (min(t0, p_end) - I.p_begin) / T : 0;
+    I.tail0 = t0 >= I.p_begin && t0 < p_end;
+    // a node stands in the tile after the tail when its depth is at least T - c
+    I.tail1 = I.n - 1 >= T - I.c && t0 + T >= I.p_begin && t0 + T < p_end;
+    I.live = !I.bad_ctx && I.rt * NT < I.n && (I.nfull > 0 || I.tail0 || I.tail1);
+}
+
 // Out of line, like everything below that runs once per item: the roles' loops share the SM's
 // instruction cache, and the code around them decides how much of it they get.
 __device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
@@ -126,14 +137,8 @@ __device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
     I.bad_ctx = I.ctx < 0 || I.ctx > A.max_ctx;
     I.bad_n = n < 0 || n > A.N;
     I.n = min(max(n, 0), A.N);
-    I.p_begin = attn_split_begin(I.split);
-    const int p_end = attn_split_begin(I.split + 1), t0 = I.ctx & ~(T - 1);
-    I.c = I.ctx - t0;
-    I.nfull = I.p_begin < t0 ? (min(t0, p_end) - I.p_begin) / T : 0;
-    I.tail0 = t0 >= I.p_begin && t0 < p_end;
-    // a node stands in the tile after the tail when its depth is at least T - c
-    I.tail1 = I.n - 1 >= T - I.c && t0 + T >= I.p_begin && t0 + T < p_end;
-    I.live = !I.bad_ctx && I.rt * A.NT < I.n && (I.nfull > 0 || I.tail0 || I.tail1);
+    I.c = I.ctx & (T - 1);
+    tree_item_split(I, A.NT);
     return I;
 }
 
@@ -362,6 +367,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 // an MN-major operand's block stride) is one add away from a base formed once per tile, four K steps
 // to an asm statement.
 constexpr uint32_t DESC_HI = (1u << 30) | (1u << 14) | (1024u >> 4);   // 128-byte swizzle, version, 8-row groups 1024 bytes apart
+// Arrival that hands over tensor memory and nothing else: after tc_fence_before it needs no release of
+// its own, and a releasing one waits for the thread's stores to global memory (2400 cycles after the
+// read-out of O at hd 128).
+__device__ __forceinline__ void arrive_tc(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead = 16u) { return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
 
 // D (+)= A B^T over 64 K elements, A and B K-major in shared memory (K steps 32 bytes apart);
@@ -597,9 +609,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         griddep_launch();
         return;   // no tensor memory was set up
     }
-    // the next item, in the roles' loops
+    // the next item, in the roles' loops; within a row tile without the call, whose divisions and loads
+    // took 2500 cycles in a role's way
     auto next = [&](int it, TreeItem& I) {
-        if (it < it1) I = tree_item(A, it);
+        if (it >= it1) return;
+        if (++I.split < A.nsplit) tree_item_split(I, A.NT);
+        else I = tree_item(A, it);
     };
     if (warp == 10) {
         tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
@@ -946,7 +961,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 float s[T];
                 tmem_ld64(tS + lane_off + grp * T, s);
                 tc_fence_before();
-                mbar_arrive(sfree(grp));
+                arrive_tc(sfree(grp));
 #pragma unroll
                 for (int j = 0; j < T; j += 2) mul2(s[j], s[j + 1], A.sl2);
                 const float mx = max64(s);
@@ -979,7 +994,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 const int before = grp ? n0 + i / 2 : n1 - 1;
                 if (!write_p(pk) || !rescale(al, i > 0, pfree(1 - grp, before), (before >> 1) & 1u)) { ok = false; break; }
                 tc_fence_before();
-                mbar_arrive(pready(grp));
+                arrive_tc(pready(grp));
                 ++n;
             }
             if (!ok) break;
@@ -994,7 +1009,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     if (!WW(pfree(1, n - 1), ((n - 1) >> 1) & 1u)) break;
                     tc_fence_after();
                     store_o(valid ? part : nullptr);
-                    mbar_arrive(ofree(nitem % S::NO));
+                    arrive_tc(ofree(nitem % S::NO));
                     ++nitem;
                     continue;
                 }
@@ -1135,7 +1150,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     if (has_a) {
                         tmem_st_wait();
                         tc_fence_before();
-                        mbar_arrive(sfree(0));
+                        arrive_tc(sfree(0));
                         mbar_arrive(pready(0));
                         ++n;
                     }
@@ -1214,7 +1229,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     tree_add_bad(A, F);
                 }
                 if (live) A.ml[idx] = make_float2(m, l);
-                mbar_arrive(ofree(nitem % S::NO));
+                arrive_tc(ofree(nitem % S::NO));
                 ++nitem;
             }
             if (I.tail()) {
