@@ -142,6 +142,67 @@ __device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
     return I;
 }
 
+// The items [*it0, *it1) of persistent CTA `blockIdx.x`: contiguous shares of the batch by weight, a tile
+// weighing 1 and an item ITEM_WEIGHT more (2 to 8 measured alike), so that sequences of different lengths
+// even out (32 of 4000 to 8000 positions: 242 us by item counts, 215 so).  A cut is a
+// weight between 0 and the total; its item is found from prefix sums over the sequences, a run of them
+// per thread.  `sm`: one word per warp and the two results, not written before the next barrier.
+constexpr int ITEM_WEIGHT = 4;
+__device__ __forceinline__ int tree_weight(int split) { return split * ITEM_WEIGHT + attn_split_begin(split) / T; }   // splits before
+__device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* it0, int* it1) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
+    const int run = (A.B + blockDim.x - 1) / blockDim.x, b0 = min(tid * run, A.B), b1 = min(b0 + run, A.B);
+    // row tiles with a node; weight of each of sequence b's (kv head, row tile) pairs
+    auto tiles = [&](int b, int& weight) -> int {
+        const int ctx = __ldg(A.ctx_len + b), n = min(max(A.n_nodes ? __ldg(A.n_nodes + b) : A.N, 0), A.N);
+        if (ctx < 0 || ctx > A.max_ctx) return 0;
+        weight = attn_split_count(ctx + n) * ITEM_WEIGHT + (ctx + n) / T + 4;
+        return (n + A.NT - 1) / A.NT * A.Hkv;
+    };
+    long long own = 0;
+    for (int b = b0; b < b1; ++b) {
+        int w = 0;
+        const int t = tiles(b, w);
+        own += static_cast<long long>(t) * w;
+    }
+    long long incl = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    if (lane == 31) sm[warp] = incl;
+    if (tid < 2) sm[n_warps + tid] = static_cast<long long>(A.nsplit) * A.nrt * A.Hkv * A.B;   // past the last item
+    __syncthreads();
+    long long total = 0, before = incl - own;
+    for (int w = 0; w < n_warps; ++w) {
+        if (w < warp) before += sm[w];
+        total += sm[w];
+    }
+    for (int e = 0; e < 2; ++e) {
+        long long x = total * (blockIdx.x + e) / gridDim.x;
+        if (x < before || x >= before + own) continue;
+        x -= before;
+        for (int b = b0; b < b1; ++b) {
+            int w = 0;
+            const int t = tiles(b, w);
+            const long long all = static_cast<long long>(t) * w;
+            if (x >= all) {
+                x -= all;
+                continue;
+            }
+            const int j = static_cast<int>(x / w), rest = static_cast<int>(x - static_cast<long long>(j) * w), live = t / A.Hkv;
+            int split = 0;   // the cut goes to the nearer end of the item it falls into
+            while (split < A.nsplit && tree_weight(split) + tree_weight(split + 1) <= 2 * rest) ++split;
+            sm[n_warps + e] = ((static_cast<long long>(b) * A.Hkv + j / live) * A.nrt + j % live) * A.nsplit + split;
+            break;
+        }
+    }
+    __syncthreads();
+    *it0 = static_cast<int>(blockIdx.x == 0 ? 0 : sm[n_warps]);
+    *it1 = static_cast<int>(sm[n_warps + 1]);
+}
+
 // What the rows of one tail item know about their tree; positions are relative to the tail tile.
 struct TreeInfo {
     u64 anc[XV_KMAX];          // the path from the root: ancestors and the node itself
@@ -561,13 +622,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     const uint32_t done2 = bx + 8u * 27;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n_items = A.nsplit * A.nrt * A.Hkv * A.B;
     // one CTA per item: blocks take the items split-slowest; persistent CTAs: a contiguous range
     // numbered split-fastest (consecutive items mostly share Q)
-    const int per_split = n_items / A.nsplit;
-    const int it0 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x) * n_items / gridDim.x)
-                          : (static_cast<int>(blockIdx.x) % per_split) * A.nsplit + static_cast<int>(blockIdx.x) / per_split;
-    const int it1 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * n_items / gridDim.x) : it0 + 1;
+    int it0, it1;
+    if constexpr (!MULTI) {
+        const int per_split = A.nrt * A.Hkv * A.B;
+        it0 = (static_cast<int>(blockIdx.x) % per_split) * A.nsplit + static_cast<int>(blockIdx.x) / per_split;
+        it1 = it0 + 1;
+    }
     // barrier i of the list above; the stages' barriers come first
     if (tid < S::N_BARS && base - raw <= S::SLACK) {
         const int j = tid - (2 * SK + 2 * SV);
@@ -590,9 +652,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         if (base - raw <= S::SLACK) s_abort = 0;
     }
     griddep_wait();
+    if constexpr (MULTI) tree_share(A, reinterpret_cast<long long*>(&info), &it0, &it1);
     int first = it0;
-    TreeItem I0 = tree_item(A, first);
-    while (!I0.live && ++first < it1) I0 = tree_item(A, first);
+    TreeItem I0;
+    I0.live = false;
+    for (; first < it1; ++first) {
+        I0 = tree_item(A, first);
+        if (I0.live) break;
+    }
     // ctx or n_nodes out of range: the first item of the sequence says so
     auto report = [&]() {
         for (int it = it0; it < it1; ++it) {
@@ -603,9 +670,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             }
         }
     };
-    if (first == it1 || base - raw > S::SLACK) {
+    if (first >= it1 || base - raw > S::SLACK) {
         if (tid == 0) report();
-        if (first != it1 && tid == 0) atomicOr(A.err, ERR_WAIT_TIMEOUT);   // an unaligned base: see SLACK
+        if (first < it1 && tid == 0) atomicOr(A.err, ERR_WAIT_TIMEOUT);   // an unaligned base: see SLACK
         griddep_launch();
         return;   // no tensor memory was set up
     }
