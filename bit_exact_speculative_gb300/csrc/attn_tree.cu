@@ -122,24 +122,24 @@ __device__ __forceinline__ void tree_item_split(TreeItem& I, int NT) {
     I.live = !I.bad_ctx && I.rt * NT < I.n && (I.nfull > 0 || I.tail0 || I.tail1);
 }
 
-// Out of line, like everything below that runs once per item: the roles' loops share the SM's
-// instruction cache, and the code around them decides how much of it they get.
-__device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
+__device__ __forceinline__ TreeItem tree_item_at(const TreeArgs& A, int b, int g, int rt, int split) {
     TreeItem I;
-    I.split = it % A.nsplit;
-    int rest = it / A.nsplit;
-    I.rt = rest % A.nrt;
-    rest /= A.nrt;
-    I.g = rest % A.Hkv;
-    I.b = rest / A.Hkv;
-    I.ctx = __ldg(A.ctx_len + I.b);
-    const int n = A.n_nodes ? __ldg(A.n_nodes + I.b) : A.N;
+    I.b = b, I.g = g, I.rt = rt, I.split = split;
+    I.ctx = __ldg(A.ctx_len + b);
+    const int n = A.n_nodes ? __ldg(A.n_nodes + b) : A.N;
     I.bad_ctx = I.ctx < 0 || I.ctx > A.max_ctx;
     I.bad_n = n < 0 || n > A.N;
     I.n = min(max(n, 0), A.N);
     I.c = I.ctx & (T - 1);
     tree_item_split(I, A.NT);
     return I;
+}
+
+// Out of line, like everything below that runs once per item: the roles' loops share the SM's
+// instruction cache, and the code around them decides how much of it they get.
+__device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
+    const int split = it % A.nsplit, tile = it / A.nsplit, head = tile / A.nrt;
+    return tree_item_at(A, head / A.Hkv, head % A.Hkv, tile % A.nrt, split);
 }
 
 // The items [*it0, *it1) of persistent CTA `blockIdx.x`: contiguous shares of the batch by weight, a tile
@@ -218,20 +218,21 @@ struct TreeInfo {
 };
 
 // Fills the info of an item (one warp, nodes lane and lane + 32).
-__device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane) {
+// Parent of node i as the tree has it (-1 past the last); the load, apart from its use.
+__device__ __forceinline__ int tree_parent(const TreeArgs& A, const TreeItem& I, int i) {
+    return i < I.n ? __ldg(A.parent + static_cast<long long>(I.b) * A.N + i) : -1;
+}
+
+__device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane, int par0, int par1) {
     constexpr unsigned ALL = 0xffffffffu;
     int8_t* jump = reinterpret_cast<int8_t*>(S->list);   // list is filled last
-    int par[2];
+    int par[2] = {par0, par1};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int i = lane + 32 * u;
-        par[u] = -1;
-        if (i < I.n) {
-            par[u] = __ldg(A.parent + static_cast<long long>(I.b) * A.N + i);
-            if (par[u] < -1 || par[u] >= i) {
-                atomicOr(A.err, ERR_BAD_TREE);
-                par[u] = -1;
-            }
+        if (par[u] < -1 || par[u] >= i) {
+            atomicOr(A.err, ERR_BAD_TREE);
+            par[u] = -1;
         }
         S->anc[i] = 1ull << i;
         jump[i] = static_cast<int8_t>(par[u]);
@@ -301,8 +302,9 @@ __device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const Tre
     need = (static_cast<u64>(__reduce_or_sync(ALL, static_cast<unsigned>(need >> 32))) << 32) |
            __reduce_or_sync(ALL, static_cast<unsigned>(need));
     int before = 0, nb0 = 0;
+    const int g1 = (I.c + I.n - 1) >> 4;   // the last group a node can stand in
 #pragma unroll 1
-    for (int grp = 0; grp < 8; ++grp) {
+    for (int grp = I.c >> 4; grp <= g1; ++grp) {
         const bool in[2] = {((need >> lane) & 1) && (pos[0] >> 4) == grp, ((need >> (lane + 32)) & 1) && (pos[1] >> 4) == grp};
         const u64 gm = mask(in);
 #pragma unroll
@@ -313,7 +315,7 @@ __device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const Tre
                 S->list[x] = static_cast<uint8_t>(i);
             }
         before += __popcll(gm);
-        if (grp == 3) nb0 = before;
+        if (grp < 4) nb0 = before;
     }
     if (lane == 0) {
         S->tile0 = tile0;
@@ -622,14 +624,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     const uint32_t done2 = bx + 8u * 27;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // one CTA per item: blocks take the items split-slowest; persistent CTAs: a contiguous range
-    // numbered split-fastest (consecutive items mostly share Q)
-    int it0, it1;
-    if constexpr (!MULTI) {
-        const int per_split = A.nrt * A.Hkv * A.B;
-        it0 = (static_cast<int>(blockIdx.x) % per_split) * A.nsplit + static_cast<int>(blockIdx.x) / per_split;
-        it1 = it0 + 1;
-    }
+    // one CTA per item: the block (row tile, kv head and sequence, split), splits slowest; persistent
+    // CTAs: a contiguous range numbered split-fastest (consecutive items mostly share Q)
+    int it0 = 0, it1 = 1;
     // barrier i of the list above; the stages' barriers come first
     if (tid < S::N_BARS && base - raw <= S::SLACK) {
         const int j = tid - (2 * SK + 2 * SV);
@@ -652,23 +649,30 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         if (base - raw <= S::SLACK) s_abort = 0;
     }
     griddep_wait();
-    if constexpr (MULTI) tree_share(A, reinterpret_cast<long long*>(&info), &it0, &it1);
-    int first = it0;
+    int first = 0;
     TreeItem I0;
-    I0.live = false;
-    for (; first < it1; ++first) {
-        I0 = tree_item(A, first);
-        if (I0.live) break;
+    if constexpr (MULTI) {
+        tree_share(A, reinterpret_cast<long long*>(&info), &it0, &it1);
+        I0.live = false;
+        for (first = it0; first < it1; ++first) {
+            I0 = tree_item(A, first);
+            if (I0.live) break;
+        }
+    } else {
+        I0 = tree_item_at(A, blockIdx.y / A.Hkv, blockIdx.y % A.Hkv, blockIdx.x, blockIdx.z);
+        first = I0.live ? 0 : 1;
     }
     // ctx or n_nodes out of range: the first item of the sequence says so
-    auto report = [&]() {
-        for (int it = it0; it < it1; ++it) {
-            const TreeItem I = tree_item(A, it);
-            if (I.split == 0 && I.rt == 0 && I.g == 0) {
-                if (I.bad_ctx) atomicOr(A.err, ERR_BAD_LENGTH);
-                if (I.bad_n) atomicOr(A.err, ERR_BAD_COUNT);
-            }
+    auto report_item = [&](const TreeItem& I) {
+        if (I.split == 0 && I.rt == 0 && I.g == 0) {
+            if (I.bad_ctx) atomicOr(A.err, ERR_BAD_LENGTH);
+            if (I.bad_n) atomicOr(A.err, ERR_BAD_COUNT);
         }
+    };
+    auto report = [&]() {
+        if constexpr (!MULTI) report_item(I0);
+        else
+            for (int it = it0; it < it1; ++it) report_item(tree_item(A, it));
     };
     if (first >= it1 || base - raw > S::SLACK) {
         if (tid == 0) report();
@@ -679,10 +683,15 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // the next item, in the roles' loops; within a row tile without the call, whose divisions and loads
     // took 2500 cycles in a role's way
     auto next = [&](int it, TreeItem& I) {
-        if (it >= it1) return;
+        if (!MULTI || it >= it1) return;
         if (++I.split < A.nsplit) tree_item_split(I, A.NT);
         else I = tree_item(A, it);
     };
+    int par0 = -1, par1 = -1;   // a single item's parents, on their way meanwhile
+    if (!MULTI && warp == 11) {
+        par0 = tree_parent(A, I0, lane);
+        par1 = tree_parent(A, I0, lane + 32);
+    }
     if (warp == 10) {
         tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
@@ -728,7 +737,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!I.tail()) continue;
             if (nt > 0 && !WW(tfree, (nt - 1) & 1u)) break;
             ++nt;
-            tree_info(&info, A, I, lane);
+            if (MULTI) {
+                par0 = tree_parent(A, I, lane);
+                par1 = tree_parent(A, I, lane + 32);
+            }
+            tree_info(&info, A, I, lane, par0, par1);
             __syncwarp();
             if (lane == 0) mbar_arrive(tready);
         }
@@ -1230,20 +1243,22 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     for (int x0 = 0; x0 < nb; x0 += 4, ++bs) {
                         if (bs >= 2 && !WW(bfree(bs & 1), ((bs - 2) >> 1) & 1u)) { ok = false; break; }
                         uint8_t* pr = prow + (bs & 1) * QBLK;
-                        bool here = false;   // one of this row's blocks is among the step's four
+                        // per group of the tile a byte: where the row's block begins in its swizzled row
+                        // of 128 bytes, 255 if the block is none of the step's four
+                        uint32_t at = 0;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int x = static_cast<int>((bl >> (8 * q)) & 255u) - xb;
-                            here |= ((bl >> (8 * q)) & 255u) != 255u && (x >> 2) == (x0 >> 2);
+                            const unsigned b8 = (bl >> (8 * q)) & 255u, x = b8 - xb;
+                            at |= (b8 != 255u && (x >> 2) == static_cast<unsigned>(x0) >> 2 ? (((x & 3u) * 2u) ^ (rho & 7u)) * 16u : 255u) << (8 * q);
                         }
+                        const bool here = at != ~0u;
 #pragma unroll
-                        for (int c = 0; c < T / 8; ++c) *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(0, 0, 0, 0);
-                        if (here && gs >= 0) {
-                            const int x = static_cast<int>((bl >> (8 * gs)) & 255u) - xb;
-                            if ((x >> 2) == (x0 >> 2)) {
-                                const int c = (x & 3) * 2;
-                                *reinterpret_cast<uint4*>(pr + ((c ^ (rho & 7)) * 16)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
-                                *reinterpret_cast<uint4*>(pr + (((c + 1) ^ (rho & 7)) * 16)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
+                        for (int c = 0; c < T / 8; ++c) *reinterpret_cast<uint4*>(pr + c * 16) = make_uint4(0, 0, 0, 0);
+                        if (gs >= 0) {
+                            const unsigned o = (at >> (8 * gs)) & 255u;
+                            if (o != 255u) {
+                                *reinterpret_cast<uint4*>(pr + o) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+                                *reinterpret_cast<uint4*>(pr + (o ^ 16u)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
                             }
                         }
                         if (__any_sync(0xffffffffu, here)) {
@@ -1254,15 +1269,16 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                                 exp16(unused);
                                 const uint4 ps = *reinterpret_cast<const uint4*>(info.pos + 16 * (r - 4));
                                 const uint32_t pw[4] = {ps.x, ps.y, ps.z, ps.w};
-                                const unsigned in = here ? static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu : 0u;
+                                const unsigned in = static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu;
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) {
-                                    const int p = (pw[j / 4] >> (8 * (j & 3))) & 255, x = static_cast<int>((bl >> (8 * ((p >> 4) & 3))) & 255u) - xb;
-                                    if (((in >> j) & 1) && (x >> 2) == (x0 >> 2)) {
-                                        const int sl = (x & 3) * 16 + (p & 15);
-                                        *reinterpret_cast<uint16_t*>(pr + (((sl >> 3) ^ (rho & 7)) * 16) + (sl & 7) * 2) =
+                                    if (j == 8 && 16 * (r - 4) + 8 >= I.n) break;
+                                    // node 16 (r - 4) + j at position p: byte 2 (p % 16) of the block of group p / 16 % 4
+                                    const uint32_t p = pw[j / 4] >> (8 * (j & 3));
+                                    const unsigned o = (at >> ((p >> 1) & 24u)) & 255u;
+                                    if (((in >> j) & 1) && o != 255u)
+                                        *reinterpret_cast<uint16_t*>(pr + (o ^ ((p & 15u) * 2u))) =
                                             static_cast<uint16_t>(j & 1 ? pk[j / 2] >> 16 : pk[j / 2]);
-                                    }
                                 }
                                 __syncwarp();
                             }
@@ -1412,7 +1428,7 @@ xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, cudaStream
     const bool multi = n_items > 2ll * sms;
     trace_pre(s);
     if (multi) launch_k(attn_tree_kernel<HD, true>, dim3(sms), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
-    else launch_k(attn_tree_kernel<HD, false>, dim3(static_cast<unsigned>(n_items)), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
+    else launch_k(attn_tree_kernel<HD, false>, dim3(a.nrt, a.Hkv * a.B, a.nsplit), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
     return launched("attn_tree_kernel", s, K_ATTN_TREE,
                     4ll * a.B * a.Hkv * a.max_ctx * HD + 4ll * a.B * a.N * (a.Hq + a.Hkv) * HD + 4ll * a.B * a.N * a.Hq * a.nsplit * (HD + 2));
 }
