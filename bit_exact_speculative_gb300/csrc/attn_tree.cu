@@ -58,7 +58,7 @@ struct TreeShape {
     static constexpr int V_OFF = K_OFF + SK * TILE_BYTES;
     static constexpr int PB_OFF = V_OFF + SV * TILE_BYTES;
     static constexpr int BAR_OFF = PB_OFF + (PB_IN_K ? 0 : 2 * QBLK);
-    static constexpr int N_BARS = 2 * SK + 2 * SV + 29;
+    static constexpr int N_BARS = 2 * SK + 2 * SV + 28;
     static constexpr int M_OFF = BAR_OFF + 8 * ((N_BARS + 1) / 2 * 2);   // float[128]
     static constexpr int SUM_OFF = M_OFF + 512;                          // float[2][128]
     static constexpr int INFO_OFF = SUM_OFF + 1024;
@@ -96,15 +96,16 @@ struct TreeArgs {
 };
 
 // warps 0-3 softmax of an item's even tiles, tail and epilogue, 4-7 softmax of its odd tiles (thread =
-// row = TMEM lane) and the gather, 8 K, 9 V, 10 Q K^T, 11 Q and the tree's info, 12 P V
-constexpr int TREE_THREADS = 416;
+// row = TMEM lane) and the gather, 8 K, 9 V and the tree's info, 10 Q and Q K^T, 11 P V.  Three warps per
+// SM sub-partition: a thirteenth warp would leave each thread 128 registers instead of 168.
+constexpr int TREE_THREADS = 384;
 
 struct TreeItem {
     int b, g, rt, split, ctx, n, p_begin;
     int nfull;        // whole tiles of cache positions
     int c;            // cache positions of the tail tile (the tile that holds position ctx)
     bool tail0, tail1;   // this split holds the tail tile; the tile after it
-    bool live, bad_ctx, bad_n;
+    bool live;
     __device__ __forceinline__ bool tail() const { return tail0 || tail1; }
     __device__ __forceinline__ int kreg() const { return nfull + (tail0 && c > 0 ? 1 : 0); }      // K tiles of cache positions
     __device__ __forceinline__ int vreg() const { return nfull + (tail0 && c >= 16 ? 1 : 0); }    // V tiles of them
@@ -119,17 +120,16 @@ __device__ __forceinline__ void tree_item_split(TreeItem& I, int NT) {
     I.tail0 = t0 >= I.p_begin && t0 < p_end;
     // a node stands in the tile after the tail when its depth is at least T - c
     I.tail1 = I.n - 1 >= T - I.c && t0 + T >= I.p_begin && t0 + T < p_end;
-    I.live = !I.bad_ctx && I.rt * NT < I.n && (I.nfull > 0 || I.tail0 || I.tail1);
+    I.live = I.rt * NT < I.n && (I.nfull > 0 || I.tail0 || I.tail1);
 }
 
 __device__ __forceinline__ TreeItem tree_item_at(const TreeArgs& A, int b, int g, int rt, int split) {
     TreeItem I;
     I.b = b, I.g = g, I.rt = rt, I.split = split;
-    I.ctx = __ldg(A.ctx_len + b);
-    const int n = A.n_nodes ? __ldg(A.n_nodes + b) : A.N;
-    I.bad_ctx = I.ctx < 0 || I.ctx > A.max_ctx;
-    I.bad_n = n < 0 || n > A.N;
-    I.n = min(max(n, 0), A.N);
+    const int ctx = __ldg(A.ctx_len + b), n = A.n_nodes ? __ldg(A.n_nodes + b) : A.N;
+    const bool bad = ctx < 0 || ctx > A.max_ctx;   // no nodes then
+    I.ctx = bad ? 0 : ctx;
+    I.n = bad ? 0 : min(max(n, 0), A.N);
     I.c = I.ctx & (T - 1);
     tree_item_split(I, A.NT);
     return I;
@@ -140,6 +140,13 @@ __device__ __forceinline__ TreeItem tree_item_at(const TreeArgs& A, int b, int g
 __device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
     const int split = it % A.nsplit, tile = it / A.nsplit, head = tile / A.nrt;
     return tree_item_at(A, head / A.Hkv, head % A.Hkv, tile % A.nrt, split);
+}
+
+// ctx or n_nodes out of range: once per sequence
+__device__ __forceinline__ void tree_report(const TreeArgs& A, int b) {
+    const int ctx = __ldg(A.ctx_len + b), n = A.n_nodes ? __ldg(A.n_nodes + b) : A.N;
+    if (ctx < 0 || ctx > A.max_ctx) atomicOr(A.err, ERR_BAD_LENGTH);
+    if (n < 0 || n > A.N) atomicOr(A.err, ERR_BAD_COUNT);
 }
 
 // The items [*it0, *it1) of persistent CTA `blockIdx.x`: contiguous shares of the batch by weight, a tile
@@ -163,6 +170,7 @@ __device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* i
     for (int b = b0; b < b1; ++b) {
         int w = 0;
         const int t = tiles(b, w);
+        if (blockIdx.x == 0) tree_report(A, b);
         own += static_cast<long long>(t) * w;
     }
     long long incl = own;
@@ -613,11 +621,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto bready = [&](int j) { return bx + 8u * (10 + j); };
     auto bfree = [&](int j) { return bx + 8u * (12 + j); };
     // once per tail item: the tree's scores written; all that it holds (scores, info) read; its info
-    // filled; its blocks gathered; its V tiles requested (every stage's last use but one is then
-    // complete, so the gather's waits on the stages are never two phases behind)
-    const uint32_t tbar = bx + 8u * 14, tfree = bx + 8u * 15, tready = bx + 8u * 16, vdone = bx + 8u * 17, vgo = bx + 8u * 18;
+    // filled and its V tiles requested (every stage's last use but one is then complete, so the
+    // gather's waits on the stages are never two phases behind); its blocks gathered
+    const uint32_t tbar = bx + 8u * 14, tfree = bx + 8u * 15, tready = bx + 8u * 16, vdone = bx + 8u * 17;
     const uint32_t qfull = bx + 8u * 19, qdone = bx + 8u * 20, done = bx + 8u * 22;
-    auto ofree = [&](int j) { return bx + 8u * (j ? 28 : 21); };   // by O buffer: read out
+    auto ofree = [&](int j) { return bx + 8u * (j ? 18 : 21); };   // by O buffer: read out
     // by the parity of group 1's tile: its sum is in shared memory.  Two of them, as group 1 may end its
     // next tile before group 0 comes to take this one's sum.
     auto spub = [&](int j) { return bx + 8u * (23 + j); };
@@ -632,11 +640,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const int j = tid - (2 * SK + 2 * SV);
         // arrivals: 1 where a thread or the hardware arrives; a softmax group's 128 on sfree, pready,
         // mpub, bready, spub and ofree
-        constexpr u64 BY_GROUP = 0x11A00F3Cull;
+        constexpr u64 BY_GROUP = 0x1A40F3Cull;
         int count = 1;
         if (j < 0) count = tid >= 2 * SK && tid < 2 * SK + SV ? 5 : 1;   // fullV: the gather's warps and V's
         else if ((BY_GROUP >> j) & 1) count = 128;
-        else if (j == 15) count = 128 + 1 + 1 + 4;   // tfree: group 0, P V, V, group 1's warps
+        else if (j == 15) count = 128 + 1 + 4;   // tfree: group 0, P V, group 1's warps
         else if (j == 17) count = 4;                 // vdone: group 1's warps
         mbar_init(bar0 + 8u * tid, count);
         fence_mbar_init();
@@ -661,21 +669,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     } else {
         I0 = tree_item_at(A, blockIdx.y / A.Hkv, blockIdx.y % A.Hkv, blockIdx.x, blockIdx.z);
         first = I0.live ? 0 : 1;
+        if (tid == 0 && I0.g == 0 && I0.rt == 0 && I0.split == 0) tree_report(A, I0.b);
     }
-    // ctx or n_nodes out of range: the first item of the sequence says so
-    auto report_item = [&](const TreeItem& I) {
-        if (I.split == 0 && I.rt == 0 && I.g == 0) {
-            if (I.bad_ctx) atomicOr(A.err, ERR_BAD_LENGTH);
-            if (I.bad_n) atomicOr(A.err, ERR_BAD_COUNT);
-        }
-    };
-    auto report = [&]() {
-        if constexpr (!MULTI) report_item(I0);
-        else
-            for (int it = it0; it < it1; ++it) report_item(tree_item(A, it));
-    };
     if (first >= it1 || base - raw > S::SLACK) {
-        if (tid == 0) report();
         if (first < it1 && tid == 0) atomicOr(A.err, ERR_WAIT_TIMEOUT);   // an unaligned base: see SLACK
         griddep_launch();
         return;   // no tensor memory was set up
@@ -688,7 +684,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         else I = tree_item(A, it);
     };
     int par0 = -1, par1 = -1;   // a single item's parents, on their way meanwhile
-    if (!MULTI && warp == 11) {
+    if (!MULTI && warp == 9) {
         par0 = tree_parent(A, I0, lane);
         par1 = tree_parent(A, I0, lane + 32);
     }
@@ -717,39 +713,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
     auto same_q = [](const TreeItem& x, int b, int g, int rt) { return x.b == b && x.g == g && x.rt == rt; };
 
-    if (warp == 11) {
-        // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before, and
-        // what there is to know of a tail item's tree
-        int nq = 0, nt = 0, qb = -1, qg = -1, qrt = -1;
-        TreeItem I = I0;
-        for (int it = first; it < it1; next(++it, I)) {
-            if (!I.live) continue;
-            if (!same_q(I, qb, qg, qrt)) {
-                qb = I.b, qg = I.g, qrt = I.rt;
-                if (nq > 0 && !WW(qdone, (nq - 1) & 1u)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(qfull, CB * A.NT * A.G * 128);
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) tma_load_3d(sQ + cb * QBLK, &tmQ, cb * 64, I.g * A.G, I.b * A.N + I.rt * A.NT, qfull);
-                }
-                ++nq;
-            }
-            if (!I.tail()) continue;
-            if (nt > 0 && !WW(tfree, (nt - 1) & 1u)) break;
-            ++nt;
-            if (MULTI) {
-                par0 = tree_parent(A, I, lane);
-                par1 = tree_parent(A, I, lane + 32);
-            }
-            tree_info(&info, A, I, lane, par0, par1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tready);
-        }
-        if (lane == 0) {
-            report();
-            if (nq > 0) drain(qfull, (nq - 1) & 1u);   // every issued copy lands before the CTA may leave
-        }
-    } else if (warp == 8) {
+    if (warp == 8) {
         // ---- K tiles of the cache, then the tree's
         if (lane == 0) {
             int t = 0;
@@ -780,14 +744,15 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             for (int j = t > SK ? t - SK : 0; j < t; ++j) drain(fullK(j % SK), (j / SK) & 1u);
         }
     } else if (warp == 9) {
-        // ---- V tiles of the cache; a tail's block steps are group 1's
-        if (lane == 0) {
-            int t = 0, nt = 0;
-            unsigned mine = 0;   // bit j: use t - 1 - j of the ring was a copy of this warp's
-            bool ok = true;
-            TreeItem I = I0;
-            for (int it = first; ok && it < it1; next(++it, I)) {
-                if (!I.live) continue;
+        // ---- V tiles of the cache (a tail's block steps are group 1's), then what there is to know of
+        // a tail item's tree
+        int t = 0, nt = 0;
+        unsigned mine = 0;   // bit j: use t - 1 - j of the ring was a copy of this warp's
+        bool ok = true;
+        TreeItem I = I0;
+        for (int it = first; ok && it < it1; next(++it, I)) {
+            if (!I.live) continue;
+            if (lane == 0) {
                 const int nv = I.vreg();
                 for (int i = 0; i < nv; ++i, ++t) {
                     const int st = t % SV;
@@ -803,12 +768,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     for (int cb = 0; cb < CB; ++cb) tma_load_3d(sV(st) + cb * BLK, &tmV, cb * 64, row, z, fullV(st));
                     mine = mine << 1 | 1u;
                 }
-                if (!ok || !I.tail()) continue;
-                if (!W(tready, nt & 1u)) break;
-                mbar_arrive(vgo);   // after tready: group 1 has then taken the one before
-                ++nt;
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok || !I.tail()) continue;
+            if (MULTI) {
+                par0 = tree_parent(A, I, lane);
+                par1 = tree_parent(A, I, lane + 32);
+            }
+            if (nt > 0 && !WW(tfree, (nt - 1) & 1u)) break;
+            ++nt;
+            tree_info(&info, A, I, lane, par0, par1);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(tready);
                 int steps = (I.tail0 ? (info.nb0 + 3) / 4 : 0) + (I.tail1 ? (info.nb1 + 3) / 4 : 0);
-                mbar_arrive(tfree);
                 for (; ok && steps > 0; --steps) {
                     ok = t < SV || W(emptyV(t % SV), ((t / SV) & 1u) ^ 1u);
                     if (!ok) break;
@@ -817,12 +790,15 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     ++t;
                 }
             }
-            // every issued copy lands before the CTA may leave
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        // every issued copy lands before the CTA may leave
+        if (lane == 0)
             for (int j = 1; j <= SV && j <= t; ++j)
                 if ((mine >> (j - 1)) & 1) drain(fullV((t - j) % SV), ((t - j) / SV) & 1u);
-        }
     } else if (warp == 10) {
-        // ---- Q K^T, as far ahead as the two score buffers allow.  It and P V are issued by a warp each:
+        // ---- Q of every item whose (sequence, kv head, row tile) differs from the one before, and Q K^T,
+        // as far ahead as the two score buffers allow.  It and P V are issued by a warp each:
         // a tile's barrier tests and commits take an issuer ~1000 cycles beside the ~1000 of its MMAs,
         // and with one issuer for both the tensor core stood idle meanwhile.
         if (lane == 0) {
@@ -834,9 +810,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             for (int it = first; ok && it < it1; next(++it, I)) {
                 if (!I.live) continue;
                 if (!same_q(I, qb, qg, qrt)) {
-                    if (nq > 0) tc_commit(qdone);
-                    if (!W(qfull, nq & 1u)) break;
-                    ++nq;
+                    if (nq > 0) {
+                        tc_commit(qdone);
+                        if (!W(qdone, (nq - 1) & 1u)) break;
+                    }
+                    mbar_arrive_expect_tx(qfull, CB * A.NT * A.G * 128);
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) tma_load_3d(sQ + cb * QBLK, &tmQ, cb * 64, I.g * A.G, I.b * A.N + I.rt * A.NT, qfull);
+                    if (!W(qfull, nq++ & 1u)) break;
                     qb = I.b, qg = I.g, qrt = I.rt;
                 }
                 const int nreg = I.kreg(), nqk = nreg + (I.tail() ? 1 : 0);
@@ -872,10 +853,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             // only now: the combine's CTAs, launched as the first SMs fall idle, would all crowd onto those
             // (16 nodes at 131072 positions: 131 us, so 111)
             griddep_launch();
+            if (nq > 0) drain(qfull, (nq - 1) & 1u);   // every issued copy lands before the CTA may leave
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             drain(done, 0u);
         }
-    } else if (warp == 12) {
+    } else if (warp == 11) {
         // ---- P V
         if (lane == 0) {
             constexpr uint32_t IDO = idesc_bf16_f32(128, HD, true);
@@ -1093,7 +1075,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     ++nitem;
                     continue;
                 }
-                if (!WW(vgo, nt & 1u) || !WW(tready, nt & 1u)) break;
+                if (!WW(tready, nt & 1u)) break;
                 ++nt;
                 if (I.nfull > 0 || I.tail0 || info.nb1 > 0) ++nitem;   // a tail tile always has a block
 #pragma unroll 1
@@ -1479,6 +1461,7 @@ xv_status tree_checks(const TreeArgs& a, int hd, int Lmax, const void* ws, size_
     if (a.max_ctx < 0 || a.max_ctx > Lmax) return fail(XV_ERR_ARG, "attn_tree: need 0 <= max_ctx <= Lmax");
     if (a.B > 65535 || a.Hkv > 65535) return fail(XV_ERR_UNSUPPORTED, "attn_tree: B and Hkv must be below 65536");
     if (static_cast<long long>(a.B) * a.N * a.Hq > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: more than 2^30 rows");
+    if (static_cast<long long>(a.kv.n_pages) * a.Hkv >= (1ll << 31)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: cache too large");
     const long long w = static_cast<long long>(a.Hq) * hd, kw = 2ll * a.Hkv * hd;
     if (a.q_stride < w || a.out_stride < w || a.src_stride < kw) return fail(XV_ERR_ARG, "attn_tree: a row stride is below its row");
     if (a.gate && a.gate_stride < w) return fail(XV_ERR_ARG, "attn_tree: gate_stride below Hq*hd");
@@ -1511,7 +1494,6 @@ xv_status xv_attn_tree(const uint16_t* q, long long q_stride, const uint16_t* kc
                max_ctx, scale * 1.4426950408889634f, gate, gate_stride, out, out_stride, nullptr, 0, 0, 0, 0, nullptr, nullptr,
                nullptr};
     if (xv_status st = tree_checks(a, hd, Lmax, ws, ws_bytes)) return st;
-    if (static_cast<long long>(B) * Hkv > (1ll << 31)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: cache too large");
     return tree_launch(a, hd, ws, reinterpret_cast<cudaStream_t>(s));
 }
 
