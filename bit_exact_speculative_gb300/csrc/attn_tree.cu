@@ -97,7 +97,8 @@ struct TreeArgs {
 
 // warps 0-3 softmax of an item's even tiles, tail and epilogue, 4-7 softmax of its odd tiles (thread =
 // row = TMEM lane) and the gather, 8 K, 9 V and the tree's info, 10 Q and Q K^T, 11 P V.  Three warps per
-// SM sub-partition: a thirteenth warp would leave each thread 128 registers instead of 168.
+// SM sub-partition leave each thread 168 registers, a thirteenth would leave 128: the softmax then
+// waits on its own dependences and spills (32 x 13 nodes at 4000 to 8000 positions: 178 us, 265 with 128).
 constexpr int TREE_THREADS = 384;
 
 struct TreeItem {
@@ -149,12 +150,13 @@ __device__ __forceinline__ void tree_report(const TreeArgs& A, int b) {
     if (n < 0 || n > A.N) atomicOr(A.err, ERR_BAD_COUNT);
 }
 
-// The items [*it0, *it1) of persistent CTA `blockIdx.x`: contiguous shares of the batch by weight, a tile
-// weighing 1 and an item ITEM_WEIGHT more (2 to 8 measured alike), so that sequences of different lengths
-// even out (32 of 4000 to 8000 positions: 242 us by item counts, 215 so).  A cut is a
-// weight between 0 and the total; its item is found from prefix sums over the sequences, a run of them
-// per thread.  `sm`: one word per warp and the two results, not written before the next barrier.
-constexpr int ITEM_WEIGHT = 4;
+// The items [*it0, *it1) of persistent CTA `blockIdx.x`: contiguous shares of the batch by weight, so that
+// sequences of different lengths even out (32 x 13 nodes at 4000 to 8000 positions: 242 us with shares of
+// equal item counts, 215 so).  A tile weighs 1, an item ITEM_WEIGHT more (2 to 8 measured alike) and a
+// tree's tail TAIL_WEIGHT (64 nodes at 32768 positions: 118 us with 4, 105 with 16).  A cut is a weight
+// between 0 and the total; its item is found from prefix sums over the sequences, a run of them per
+// thread.  `sm`: one word per warp and the two results, not written before the next barrier.
+constexpr int ITEM_WEIGHT = 4, TAIL_WEIGHT = 16;
 __device__ __forceinline__ int tree_weight(int split) { return split * ITEM_WEIGHT + attn_split_begin(split) / T; }   // splits before
 __device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* it0, int* it1) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
@@ -163,7 +165,7 @@ __device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* i
     auto tiles = [&](int b, int& weight) -> int {
         const int ctx = __ldg(A.ctx_len + b), n = min(max(A.n_nodes ? __ldg(A.n_nodes + b) : A.N, 0), A.N);
         if (ctx < 0 || ctx > A.max_ctx) return 0;
-        weight = attn_split_count(ctx + n) * ITEM_WEIGHT + (ctx + n) / T + 4;
+        weight = attn_split_count(ctx + n) * ITEM_WEIGHT + (ctx + n) / T + TAIL_WEIGHT;
         return (n + A.NT - 1) / A.NT * A.Hkv;
     };
     long long own = 0;
@@ -1101,192 +1103,186 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             }
             const bool last_odd = I.nfull > 0 && !(I.nfull & 1);
             if (last_odd && (!take_max() || !take_sum())) break;
-            // completes with the last P V step of the item's whole tiles
-            if (!I.tail()) {
+            if (!I.tail()) {   // the rest is group 1's
                 if (valid) A.ml[idx] = make_float2(m, l);
                 ++nitem;
                 tk += I.kreg();
                 continue;
             }
+            // completes with the last P V step of the item's whole tiles
             const int last = (last_odd ? n1 : n) - 1;
             const uint32_t last_bar = pfree(last_odd, last), last_par = (last >> 1) & 1u;
             const int tail_st = (tk + I.kreg()) % SK;   // K stage of the tree's tile
-            tk += I.kreg() + (I.tail() ? 1 : 0);
+            tk += I.kreg() + 1;
             uint8_t* prow = smem + (S::PB_IN_K ? S::K_OFF + tail_st * TILE_BYTES : S::PB_OFF) + rho * 128;
             bool any_pv = I.nfull > 0, any_block = false;
             u64 path = 0, in0 = 0;
             float m0 = NEG_INF;      // the reference max of the tail tile (the rare epilogue's)
             unsigned cnz = 0;        // cache positions of the first block group whose p is not 0
             int npos = 0;            // position of the node, relative to the tail tile
-            if (I.tail()) {
-                if (!WW(tready, nt & 1u) || !WW(tbar, nt & 1u)) break;
-                tc_fence_after();
-                path = valid ? info.anc[node] : 0;
-                npos = valid ? info.pos[node] : 0;
-                in0 = info.tile0;
-                // block of the path in each of the 8 groups of the two tiles (255: none)
-                uint32_t blk[2] = {~0u, ~0u};
-                auto set_blk = [&](int g16, int x) {
-                    const int sh = 8 * (g16 & 3);
-                    if (g16 < 4) blk[0] = (blk[0] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
-                    else blk[1] = (blk[1] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
-                };
-                if (valid) {
-                    for (u64 e = path & info.ends; e; e &= e - 1) {
-                        const int a = __ffsll(static_cast<long long>(e)) - 1;
-                        set_blk(info.pos[a] >> 4, info.idx[a]);
-                    }
-                    set_blk(npos >> 4, info.idx[info.rep[node]]);
+            if (!WW(tready, nt & 1u) || !WW(tbar, nt & 1u)) break;
+            tc_fence_after();
+            path = valid ? info.anc[node] : 0;
+            npos = valid ? info.pos[node] : 0;
+            in0 = info.tile0;
+            // block of the path in each of the 8 groups of the two tiles (255: none)
+            uint32_t blk[2] = {~0u, ~0u};
+            auto set_blk = [&](int g16, int x) {
+                const int sh = 8 * (g16 & 3);
+                if (g16 < 4) blk[0] = (blk[0] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
+                else blk[1] = (blk[1] & ~(255u << sh)) | (static_cast<uint32_t>(x) << sh);
+            };
+            if (valid) {
+                for (u64 e = path & info.ends; e; e &= e - 1) {
+                    const int a = __ffsll(static_cast<long long>(e)) - 1;
+                    set_blk(info.pos[a] >> 4, info.idx[a]);
                 }
-                __syncwarp();
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (half ? !I.tail1 : !I.tail0) continue;
-                    const u64 mine = half ? path & ~in0 : path & in0;
-                    const bool has_a = !half && I.c > 0;
-                    const u64 a_mask = has_a && valid ? (1ull << I.c) - 1 : 0ull;
-                    // scores 16 r .. 16 r + 15 of the cache's part of the tile (r < 4) or of the tree
-                    // (r - 4), -inf where this row does not look; 16 at a time in rolled loops, as
-                    // this code runs once per item
-                    float s[16];
-                    auto load16 = [&](int r) {
-                        tmem_ld16((r < 4 ? tS : tT - 64) + lane_off + 16 * r, s);
-                        tmem_ld_wait();
-                        const unsigned in = static_cast<unsigned>((r < 4 ? a_mask >> (16 * r) : mine >> (16 * r - 64))) & 0xFFFFu;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) s[j] = (in >> j) & 1 ? __fmul_rn(s[j], A.sl2) : NEG_INF;
-                    };
-                    float mx = NEG_INF, sum = 0.f;
-                    if (has_a) {
-                        if (!WW(sbar(0), n & 1u)) { ok = false; break; }
-                        tc_fence_after();
-                    }
-                    // the parts that hold a cache position or a node
-                    const int r0 = has_a ? 0 : 4, ra = (I.c + 15) / 16, r1 = 4 + (I.n + 15) / 16;
-#pragma unroll 1
-                    for (int r = r0; r < r1; r = r + 1 == ra ? 4 : r + 1) {
-                        load16(r);
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) mx = max3(mx, s[j], s[j + 1]);
-                    }
-                    const float mn = new_max(m, mx), al = alpha(m, mn);
-                    const bool dead = mn == NEG_INF;
-                    // the last P V step so far: a block step of the tail tile, or a cache tile's
-                    if (!(any_block ? rescale(al, true, bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u)
-                                    : rescale(al, any_pv, last_bar, last_par))) {
-                        ok = false;
-                        break;
-                    }
-                    // p of 16 scores as bf16 pairs (0 where no score has been seen at all)
-                    uint32_t pk[8];
-                    auto exp16 = [&](float& ts) {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float a0 = dead ? 0.f : ex2_approx(__fsub_rn(s[j], mn)), a1 = dead ? 0.f : ex2_approx(__fsub_rn(s[j + 1], mn));
-                            ts = __fadd_rn(__fadd_rn(ts, a0), a1);
-                            pk[j / 2] = pack_bf16x2(a0, a1);
-                        }
-                    };
-                    // the first group's cache positions, in whose block p stands before the nodes'
-                    uint32_t sh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    const int gs = half ? -1 : I.c >> 4;
-                    if (has_a) {
-                        if (n > 0 && !WW(pfree(0, n - 1), ((n - 1) >> 1) & 1u)) { ok = false; break; }
-                        tc_fence_after();
-                    }
-#pragma unroll 1
-                    for (int r = r0; r < r1; r = r + 1 == ra ? 4 : r + 1) {
-                        load16(r);
-                        exp16(sum);
-                        if (r < 4) {
-                            tmem_st8(tP + lane_off + 8 * r, pk);   // its first c / 16 K steps are used
-                            if (r == gs) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    sh[e] = pk[e];
-                                    cnz |= ((pk[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((pk[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
-                                }
-                            }
-                        }
-                    }
-                    if (has_a) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        arrive_tc(sfree(0));
-                        mbar_arrive(pready(0));
-                        ++n;
-                    }
-                    l = __fadd_rn(__fmul_rn(l, al), sum);
-                    m = mn;
-                    if (!half) m0 = mn;
-                    const int nb = half ? info.nb1 : info.nb0, xb = half ? info.nb0 : 0;
-                    const uint32_t bl = blk[half];
-#pragma unroll 1
-                    for (int x0 = 0; x0 < nb; x0 += 4, ++bs) {
-                        if (bs >= 2 && !WW(bfree(bs & 1), ((bs - 2) >> 1) & 1u)) { ok = false; break; }
-                        uint8_t* pr = prow + (bs & 1) * QBLK;
-                        // per group of the tile a byte: where the row's block begins in its swizzled row
-                        // of 128 bytes, 255 if the block is none of the step's four
-                        uint32_t at = 0;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const unsigned b8 = (bl >> (8 * q)) & 255u, x = b8 - xb;
-                            at |= (b8 != 255u && (x >> 2) == static_cast<unsigned>(x0) >> 2 ? (((x & 3u) * 2u) ^ (rho & 7u)) * 16u : 255u) << (8 * q);
-                        }
-                        const bool here = at != ~0u;
-#pragma unroll
-                        for (int c = 0; c < T / 8; ++c) *reinterpret_cast<uint4*>(pr + c * 16) = make_uint4(0, 0, 0, 0);
-                        if (gs >= 0) {
-                            const unsigned o = (at >> (8 * gs)) & 255u;
-                            if (o != 255u) {
-                                *reinterpret_cast<uint4*>(pr + o) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
-                                *reinterpret_cast<uint4*>(pr + (o ^ 16u)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
-                            }
-                        }
-                        if (__any_sync(0xffffffffu, here)) {
-                            float unused = 0.f;
-#pragma unroll 1
-                            for (int r = 4; 16 * (r - 4) < I.n; ++r) {   // the tree's p again, to their slots
-                                load16(r);
-                                exp16(unused);
-                                const uint4 ps = *reinterpret_cast<const uint4*>(info.pos + 16 * (r - 4));
-                                const uint32_t pw[4] = {ps.x, ps.y, ps.z, ps.w};
-                                const unsigned in = static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu;
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    if (j == 8 && 16 * (r - 4) + 8 >= I.n) break;
-                                    // node 16 (r - 4) + j at position p: byte 2 (p % 16) of the block of group p / 16 % 4
-                                    const uint32_t p = pw[j / 4] >> (8 * (j & 3));
-                                    const unsigned o = (at >> ((p >> 1) & 24u)) & 255u;
-                                    if (((in >> j) & 1) && o != 255u)
-                                        *reinterpret_cast<uint16_t*>(pr + (o ^ ((p & 15u) * 2u))) =
-                                            static_cast<uint16_t>(j & 1 ? pk[j / 2] >> 16 : pk[j / 2]);
-                                }
-                                __syncwarp();
-                            }
-                        }
-                        __syncwarp();
-                        fence_proxy_async_smem();
-                        tc_fence_before();
-                        mbar_arrive(bready(bs & 1));
-                        any_block = true;
-                    }
-                    if (!ok) break;
-                }
-                if (!ok || !WW(vdone, nt & 1u)) break;
+                set_blk(npos >> 4, info.idx[info.rep[node]]);
             }
+            __syncwarp();
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (half ? !I.tail1 : !I.tail0) continue;
+                const u64 mine = half ? path & ~in0 : path & in0;
+                const bool has_a = !half && I.c > 0;
+                const u64 a_mask = has_a && valid ? (1ull << I.c) - 1 : 0ull;
+                // scores 16 r .. 16 r + 15 of the cache's part of the tile (r < 4) or of the tree
+                // (r - 4), -inf where this row does not look; 16 at a time in rolled loops, as
+                // this code runs once per item
+                float s[16];
+                auto load16 = [&](int r) {
+                    tmem_ld16((r < 4 ? tS : tT - 64) + lane_off + 16 * r, s);
+                    tmem_ld_wait();
+                    const unsigned in = static_cast<unsigned>((r < 4 ? a_mask >> (16 * r) : mine >> (16 * r - 64))) & 0xFFFFu;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = (in >> j) & 1 ? __fmul_rn(s[j], A.sl2) : NEG_INF;
+                };
+                float mx = NEG_INF, sum = 0.f;
+                if (has_a) {
+                    if (!WW(sbar(0), n & 1u)) { ok = false; break; }
+                    tc_fence_after();
+                }
+                // the parts that hold a cache position or a node
+                const int r0 = has_a ? 0 : 4, ra = (I.c + 15) / 16, r1 = 4 + (I.n + 15) / 16;
+#pragma unroll 1
+                for (int r = r0; r < r1; r = r + 1 == ra ? 4 : r + 1) {
+                    load16(r);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) mx = max3(mx, s[j], s[j + 1]);
+                }
+                const float mn = new_max(m, mx), al = alpha(m, mn);
+                const bool dead = mn == NEG_INF;
+                // the last P V step so far: a block step of the tail tile, or a cache tile's
+                if (!(any_block ? rescale(al, true, bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u)
+                                : rescale(al, any_pv, last_bar, last_par))) {
+                    ok = false;
+                    break;
+                }
+                // p of 16 scores as bf16 pairs (0 where no score has been seen at all)
+                uint32_t pk[8];
+                auto exp16 = [&](float& ts) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float a0 = dead ? 0.f : ex2_approx(__fsub_rn(s[j], mn)), a1 = dead ? 0.f : ex2_approx(__fsub_rn(s[j + 1], mn));
+                        ts = __fadd_rn(__fadd_rn(ts, a0), a1);
+                        pk[j / 2] = pack_bf16x2(a0, a1);
+                    }
+                };
+                // the first group's cache positions, in whose block p stands before the nodes'
+                uint32_t sh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                const int gs = half ? -1 : I.c >> 4;
+                if (has_a) {
+                    if (n > 0 && !WW(pfree(0, n - 1), ((n - 1) >> 1) & 1u)) { ok = false; break; }
+                    tc_fence_after();
+                }
+#pragma unroll 1
+                for (int r = r0; r < r1; r = r + 1 == ra ? 4 : r + 1) {
+                    load16(r);
+                    exp16(sum);
+                    if (r < 4) {
+                        tmem_st8(tP + lane_off + 8 * r, pk);   // its first c / 16 K steps are used
+                        if (r == gs) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                sh[e] = pk[e];
+                                cnz |= ((pk[e] & 0x7FFFu) ? 1u << (2 * e) : 0u) | ((pk[e] & 0x7FFF0000u) ? 2u << (2 * e) : 0u);
+                            }
+                        }
+                    }
+                }
+                if (has_a) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    arrive_tc(sfree(0));
+                    mbar_arrive(pready(0));
+                    ++n;
+                }
+                l = __fadd_rn(__fmul_rn(l, al), sum);
+                m = mn;
+                if (!half) m0 = mn;
+                const int nb = half ? info.nb1 : info.nb0, xb = half ? info.nb0 : 0;
+                const uint32_t bl = blk[half];
+#pragma unroll 1
+                for (int x0 = 0; x0 < nb; x0 += 4, ++bs) {
+                    if (bs >= 2 && !WW(bfree(bs & 1), ((bs - 2) >> 1) & 1u)) { ok = false; break; }
+                    uint8_t* pr = prow + (bs & 1) * QBLK;
+                    // per group of the tile a byte: where the row's block begins in its swizzled row
+                    // of 128 bytes, 255 if the block is none of the step's four
+                    uint32_t at = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const unsigned b8 = (bl >> (8 * q)) & 255u, x = b8 - xb;
+                        at |= (b8 != 255u && (x >> 2) == static_cast<unsigned>(x0) >> 2 ? (((x & 3u) * 2u) ^ (rho & 7u)) * 16u : 255u) << (8 * q);
+                    }
+                    const bool here = at != ~0u;
+#pragma unroll
+                    for (int c = 0; c < T / 8; ++c) *reinterpret_cast<uint4*>(pr + c * 16) = make_uint4(0, 0, 0, 0);
+                    if (gs >= 0) {
+                        const unsigned o = (at >> (8 * gs)) & 255u;
+                        if (o != 255u) {
+                            *reinterpret_cast<uint4*>(pr + o) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+                            *reinterpret_cast<uint4*>(pr + (o ^ 16u)) = make_uint4(sh[4], sh[5], sh[6], sh[7]);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, here)) {
+                        float unused = 0.f;
+#pragma unroll 1
+                        for (int r = 4; 16 * (r - 4) < I.n; ++r) {   // the tree's p again, to their slots
+                            load16(r);
+                            exp16(unused);
+                            const uint4 ps = *reinterpret_cast<const uint4*>(info.pos + 16 * (r - 4));
+                            const uint32_t pw[4] = {ps.x, ps.y, ps.z, ps.w};
+                            const unsigned in = static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                if (j == 8 && 16 * (r - 4) + 8 >= I.n) break;
+                                // node 16 (r - 4) + j at position p: byte 2 (p % 16) of the block of group p / 16 % 4
+                                const uint32_t p = pw[j / 4] >> (8 * (j & 3));
+                                const unsigned o = (at >> ((p >> 1) & 24u)) & 255u;
+                                if (((in >> j) & 1) && o != 255u)
+                                    *reinterpret_cast<uint16_t*>(pr + (o ^ ((p & 15u) * 2u))) =
+                                        static_cast<uint16_t>(j & 1 ? pk[j / 2] >> 16 : pk[j / 2]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    __syncwarp();
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(bready(bs & 1));
+                    any_block = true;
+                }
+                if (!ok) break;
+            }
+            if (!ok || !WW(vdone, nt & 1u)) break;
             // ---- epilogue: m, l and O of the rows that reach into this split
-            const bool live = valid && (!I.tail() || I.ctx - I.c + npos >= I.p_begin);
+            const bool live = valid && I.ctx - I.c + npos >= I.p_begin;
             if (I.tail0 && valid && I.g == 0 && gh == 0) A.nsp[brow] = attn_split_count(I.ctx - I.c + npos + 1);
             if (any_pv || any_block) {
                 if (!(any_block ? WW(bfree((bs - 1) & 1), ((bs - 1) >> 1) & 1u) : WW(last_bar, last_par))) break;
                 tc_fence_after();
-                u64 vbad = 0;
-                unsigned cbad = 0;
-                if (I.tail()) {
-                    vbad = info.vbad;
-                    cbad = info.cbad;
-                }
+                const u64 vbad = info.vbad;
+                const unsigned cbad = info.cbad;
                 store_o(live ? part : nullptr);
                 if (vbad || cbad) {
                     const TreeBad F{path, in0, vbad, cbad, cnz, m0, m, tT + lane_off, I.tail0, I.tail1, I.b, I.g, I.ctx, I.c, HD, pitch,
@@ -1297,11 +1293,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 arrive_tc(ofree(nitem % S::NO));
                 ++nitem;
             }
-            if (I.tail()) {
-                mbar_arrive(tfree);
-                if (S::PB_IN_K && tid == 0) mbar_arrive(emptyK(tail_st));
-                ++nt;
-            }
+            mbar_arrive(tfree);
+            if (S::PB_IN_K && tid == 0) mbar_arrive(emptyK(tail_st));
+            ++nt;
         }
     }
     tc_fence_before();
