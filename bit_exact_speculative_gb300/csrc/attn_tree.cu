@@ -586,6 +586,13 @@ __device__ __noinline__ void tree_add_bad(const TreeArgs& A, const TreeBad& F) {
     __syncwarp();
 }
 
+// A value of the output: acc / L, with the gate's product where there is one.
+__device__ __forceinline__ uint16_t tree_out(float acc, float L, const uint16_t* gate) {
+    float y = __fdiv_rn(acc, L);
+    if (gate) y = __fmul_rn(bf16_to_f32(f32_to_bf16(y)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(*gate)))));
+    return f32_to_bf16(y);
+}
+
 template <int HD, bool MULTI>
 __global__ void __launch_bounds__(TREE_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -697,6 +704,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // one split per row: the partials stay in shared memory, where the K and V rings were, and the whole
+    // CTA forms the output from them.  Without the combine's launch 8 nodes at 128 positions take 6.7 us,
+    // with it 8.3.
+    const bool direct = !MULTI && A.nsplit == 1;
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO0 = tmem + 128, tT = tO0 + S::NO * HD, tP = tT + 64;
 
@@ -998,7 +1009,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             const bool valid = nl < A.NT && node < I.n;
             const long long brow = static_cast<long long>(I.b) * A.N + node, idx = (brow * A.Hq + I.g * A.G + gh) * A.nsplit + I.split;
             const int tile0 = I.rt * A.NT, tile_rows = min(A.NT, A.N - tile0) * A.G;
-            float* const part = A.opart + (((static_cast<long long>(I.b) * A.Hkv + I.g) * A.nsplit + I.split) * A.N + tile0) * A.G * HD + rho * 4;
+            float* const part = direct ? reinterpret_cast<float*>(smem + S::K_OFF) + rho * 4 : A.opart + (((static_cast<long long>(I.b) * A.Hkv + I.g) * A.nsplit + I.split) * A.N + tile0) * A.G * HD + rho * 4;
             pitch = tile_rows * 4;
             tO = tO0 + nitem % S::NO * HD;
             float m = NEG_INF, l = 0.f;
@@ -1289,7 +1300,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                                     live ? part : nullptr};
                     tree_add_bad(A, F);
                 }
-                if (live) A.ml[idx] = make_float2(m, l);
+                if (direct) {
+                    m_sm[rho] = m;
+                    sum_sm[rho] = l;
+                } else if (live)
+                    A.ml[idx] = make_float2(m, l);
                 arrive_tc(ofree(nitem % S::NO));
                 ++nitem;
             }
@@ -1303,6 +1318,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     if (warp == 10) {
         tc_fence_after();
         tmem_dealloc(tmem, S::TMEM_COLS);
+    }
+    if (direct) {   // the combine's operations for one split
+        const int node0 = I0.node0(A.NT), rows = min(A.NT, I0.n - node0) * A.G, pitch = min(A.NT, A.N - node0) * A.G * 4;
+        const float* part = reinterpret_cast<const float*>(smem + S::K_OFF);
+        for (int e = tid; e < rows * (HD / 4); e += TREE_THREADS) {
+            const int row = e / (HD / 4), c4 = e % (HD / 4), i = row / A.G, h = I0.g * A.G + row - i * A.G;
+            const float4 o = *reinterpret_cast<const float4*>(part + c4 * pitch + row * 4);
+            const float w = exp2f(__fsub_rn(m_sm[row], fmaxf(NEG_INF, m_sm[row]))), L = __fadd_rn(0.f, __fmul_rn(w, sum_sm[row]));
+            const long long br = static_cast<long long>(I0.b) * A.N + node0 + i, c = static_cast<long long>(h) * HD + c4 * 4;
+            const float a[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                A.out[br * A.out_stride + c + k] = tree_out(__fadd_rn(0.f, __fmul_rn(w, a[k])), L, A.gate ? A.gate + br * A.gate_stride + c + k : nullptr);
+        }
     }
 }
 
@@ -1368,14 +1397,7 @@ __global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const _
     const long long c = static_cast<long long>(h) * hd + col;
     uint16_t* out = A.out + br * A.out_stride + c;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float y = __fdiv_rn(a[e], L);
-        if (A.gate) {
-            const float t = bf16_to_f32(A.gate[br * A.gate_stride + c + e]);
-            y = __fmul_rn(bf16_to_f32(f32_to_bf16(y)), __frcp_rn(__fadd_rn(1.f, expf(-t))));
-        }
-        out[e] = f32_to_bf16(y);
-    }
+    for (int e = 0; e < 4; ++e) out[e] = tree_out(a[e], L, A.gate ? A.gate + br * A.gate_stride + c + e : nullptr);
 }
 
 inline size_t r256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1392,7 +1414,7 @@ constexpr int tree_smem() {
 static_assert(tree_smem<256>() <= 227 * 1024 && tree_smem<128>() <= 227 * 1024 && tree_smem<64>() <= 227 * 1024, "shared memory");
 
 template <int HD>
-xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, cudaStream_t s) {
+xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, bool* combined, cudaStream_t s) {
     constexpr int SMEM = tree_smem<HD>();
     int sms = 0;
     for (const void* f : {reinterpret_cast<const void*>(attn_tree_kernel<HD, true>), reinterpret_cast<const void*>(attn_tree_kernel<HD, false>)})
@@ -1400,8 +1422,10 @@ xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, cudaStream
     if (xv_status st = device_sm_count(&sms)) return st;
     const long long n_items = static_cast<long long>(a.nsplit) * a.nrt * a.Hkv * a.B;
     if (n_items > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: %lld work items", n_items);
-    // past two waves of items, persistent CTAs (the rule of the decode rows' launch)
+    // past two waves of items, persistent CTAs (the rule of the decode rows' launch); rows of one split
+    // are finished by the split kernel where its CTA has one item
     const bool multi = n_items > 2ll * sms;
+    *combined = !multi && a.nsplit == 1;
     trace_pre(s);
     if (multi) launch_k(attn_tree_kernel<HD, true>, dim3(sms), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
     else launch_k(attn_tree_kernel<HD, false>, dim3(a.nrt, a.Hkv * a.B, a.nsplit), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
@@ -1436,8 +1460,10 @@ xv_status tree_launch(TreeArgs a, int hd, void* ws, cudaStream_t s) {
     const uint64_t tst[1] = {a.src_stride * u};
     const uint32_t tb[2] = {64, static_cast<uint32_t>(T)};
     if (xv_status st = encode_tiled(&tm[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.src, td, tst, tb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
-    xv_status st = hd == 256 ? tree_launch_split<256>(tm, a, s) : hd == 128 ? tree_launch_split<128>(tm, a, s) : tree_launch_split<64>(tm, a, s);
-    if (st) return st;
+    bool combined = false;
+    xv_status st = hd == 256 ? tree_launch_split<256>(tm, a, &combined, s)
+                 : hd == 128 ? tree_launch_split<128>(tm, a, &combined, s) : tree_launch_split<64>(tm, a, &combined, s);
+    if (st || combined) return st;
     const long long nrow = static_cast<long long>(a.B) * a.N * a.Hq;
     trace_pre(s);
     const long long warps = static_cast<long long>(a.B) * a.Hkv * ((a.N * a.G + 7) / 8) * (hd / 16);

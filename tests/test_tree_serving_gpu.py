@@ -71,18 +71,19 @@ def test_bad_sequences_of_a_large_batch_leave_the_others(xv):
     assert bits(xv) == 0 and (got == 3).all()
 
 
-def test_outputs_of_any_stride_and_alignment(xv):
+@pytest.mark.parametrize("ctx", [[100, 31], [700, 100]])   # one split; two and a combine
+def test_outputs_of_any_stride_and_alignment(xv, ctx):
     """out and gate rows need no alignment: odd strides, a first element off 16 bytes."""
-    hd, Hq, Hkv, N, ctx = 64, 4, 2, 9, [100, 31]
+    hd, Hq, Hkv, N, L = 64, 4, 2, 9, ctx[0]
     trees = [tree("mixed", N, np.random.default_rng(1))] * 2
-    proj, (kc, vc) = rows(13, 2, N, Hq, Hkv, hd, "odd"), cache(13, 2, Hkv, 100, hd, "odd")
+    proj, (kc, vc) = rows(13, 2, N, Hq, Hkv, hd, "odd"), cache(13, 2, Hkv, L, hd, "odd")
     X, K, V, par = dev(proj), dev(kc), dev(vc), parents(trees, N)
     want = run(xv, X, K, V, ctx, par, None, N, Hq, Hkv, hd, gate=True)
     wide = torch.full((2 * N, Hq * hd + 7), 5, dtype=torch.int16, device="cuda")
     gates = torch.zeros((2 * N, Hq * hd + 3), dtype=torch.int16, device="cuda")
     gates[:, 1: 1 + Hq * hd] = X[:, Hq * hd: 2 * Hq * hd]
-    xv.xv_attn_tree(X, K, V, i32(ctx), X[:, 2 * Hq * hd:], par, None, N, 2, Hq, Hkv, hd, 100, 100, hd ** -0.5, wide[:, 3: 3 + Hq * hd],
-                    xv.workspace(xv.xv_attn_tree_workspace_size(2, N, Hq, hd, 100)), gate=gates[:, 1: 1 + Hq * hd])
+    xv.xv_attn_tree(X, K, V, i32(ctx), X[:, 2 * Hq * hd:], par, None, N, 2, Hq, Hkv, hd, L, L, hd ** -0.5, wide[:, 3: 3 + Hq * hd],
+                    xv.workspace(xv.xv_attn_tree_workspace_size(2, N, Hq, hd, L)), gate=gates[:, 1: 1 + Hq * hd])
     assert same_bits(wide[:, 3: 3 + Hq * hd].contiguous(), want)
     assert (wide[:, :3] == 5).all() and (wide[:, 3 + Hq * hd:] == 5).all() and xv.xv_device_check() == 0
 
