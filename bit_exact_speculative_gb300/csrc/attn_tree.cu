@@ -137,10 +137,12 @@ __device__ __forceinline__ TreeItem tree_item_at(const TreeArgs& A, int b, int g
 }
 
 // Out of line, like everything below that runs once per item: the roles' loops share the SM's
-// instruction cache, and the code around them decides how much of it they get.
-__device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it) {
-    const int split = it % A.nsplit, tile = it / A.nsplit, head = tile / A.nrt;
-    return tree_item_at(A, head / A.Hkv, head % A.Hkv, tile % A.nrt, split);
+// instruction cache, and the code around them decides how much of it they get.  Items go by value: one
+// whose address is taken lives in local memory, and the loops read it there.
+__device__ __noinline__ TreeItem tree_item(const TreeArgs& A, int it, int rt) {
+    // items are numbered split-fastest, then row tiles (rt < 0) or those of row tile rt alone
+    const int split = it % A.nsplit, tile = it / A.nsplit, head = rt < 0 ? tile / A.nrt : tile;
+    return tree_item_at(A, head / A.Hkv, head % A.Hkv, rt < 0 ? tile % A.nrt : rt, split);
 }
 
 // ctx or n_nodes out of range: once per sequence
@@ -156,11 +158,16 @@ __device__ __forceinline__ void tree_report(const TreeArgs& A, int b) {
 // tree's tail TAIL_WEIGHT (64 nodes at 32768 positions: 118 us with 4, 105 with 16).  A cut is a weight
 // between 0 and the total; its item is found from prefix sums over the sequences, a run of them per
 // thread.  `sm`: one word per warp and the two results, not written before the next barrier.
+//
+// Where all trees have all row tiles (and at least 7/8 of the CTAs form whole bundles), a share goes to a
+// bundle of nrt CTAs, one per row tile (*rt; else -1): they read the same K and V tiles at the same time,
+// once from HBM and then from L2.  With a share per CTA the row tiles of a split ran far apart (63 nodes in
+// three row tiles at 131072 positions: 306 us, 245 so).
 constexpr int ITEM_WEIGHT = 4, TAIL_WEIGHT = 16;
 __device__ __forceinline__ int tree_weight(int split) { return split * ITEM_WEIGHT + attn_split_begin(split) / T; }   // splits before
-__device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* it0, int* it1) {
+__device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* it0, int* it1, int* rt) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
-    const int run = (A.B + blockDim.x - 1) / blockDim.x, b0 = min(tid * run, A.B), b1 = min(b0 + run, A.B);
+    const int run = (A.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x), b0 = min(tid * run, A.B), b1 = min(b0 + run, A.B);
     // row tiles with a node; weight of each of sequence b's (kv head, row tile) pairs
     auto tiles = [&](int b, int& weight) -> int {
         const int ctx = __ldg(A.ctx_len + b), n = min(max(A.n_nodes ? __ldg(A.n_nodes + b) : A.N, 0), A.N);
@@ -169,9 +176,11 @@ __device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* i
         return (n + A.NT - 1) / A.NT * A.Hkv;
     };
     long long own = 0;
+    bool full = true;
     for (int b = b0; b < b1; ++b) {
         int w = 0;
         const int t = tiles(b, w);
+        full = full && (t == 0 || t == A.nrt * A.Hkv);
         if (blockIdx.x == 0) tree_report(A, b);
         own += static_cast<long long>(t) * w;
     }
@@ -182,35 +191,40 @@ __device__ __noinline__ void tree_share(const TreeArgs& A, long long* sm, int* i
         if (lane >= off) incl += y;
     }
     if (lane == 31) sm[warp] = incl;
-    if (tid < 2) sm[n_warps + tid] = static_cast<long long>(A.nsplit) * A.nrt * A.Hkv * A.B;   // past the last item
-    __syncthreads();
+    if (tid < 2) sm[n_warps + tid] = -1;   // past the last item
+    const int bundles = gridDim.x / A.nrt;
+    const bool bundled = __syncthreads_and(full) && bundles * A.nrt * 8 >= static_cast<int>(gridDim.x) * 7;
     long long total = 0, before = incl - own;
     for (int w = 0; w < n_warps; ++w) {
         if (w < warp) before += sm[w];
         total += sm[w];
     }
-    for (int e = 0; e < 2; ++e) {
-        long long x = total * (blockIdx.x + e) / gridDim.x;
+    const int per = bundled ? A.nrt : 1, share = blockIdx.x / per, shares = gridDim.x / per;   // CTAs a share has
+    *rt = bundled ? static_cast<int>(blockIdx.x) % A.nrt : -1;
+    total /= per, before /= per, own /= per;   // without remainders
+    for (int e = 0; e < 2 && share < shares; ++e) {
+        long long x = total * (share + e) / shares;
         if (x < before || x >= before + own) continue;
         x -= before;
         for (int b = b0; b < b1; ++b) {
             int w = 0;
-            const int t = tiles(b, w);
+            const int t = tiles(b, w) / per;
             const long long all = static_cast<long long>(t) * w;
             if (x >= all) {
                 x -= all;
                 continue;
             }
-            const int j = static_cast<int>(x / w), rest = static_cast<int>(x - static_cast<long long>(j) * w), live = t / A.Hkv;
+            const int j = static_cast<int>(x / w), rest = static_cast<int>(x - static_cast<long long>(j) * w), live = t / A.Hkv;   // row tiles
             int split = 0;   // the cut goes to the nearer end of the item it falls into
             while (split < A.nsplit && tree_weight(split) + tree_weight(split + 1) <= 2 * rest) ++split;
-            sm[n_warps + e] = ((static_cast<long long>(b) * A.Hkv + j / live) * A.nrt + j % live) * A.nsplit + split;
+            sm[n_warps + e] = ((static_cast<long long>(b) * A.Hkv + j / live) * (A.nrt / per) + j % live) * A.nsplit + split;
             break;
         }
     }
     __syncthreads();
-    *it0 = static_cast<int>(blockIdx.x == 0 ? 0 : sm[n_warps]);
-    *it1 = static_cast<int>(sm[n_warps + 1]);
+    const int end = A.B * A.Hkv * (A.nrt / per) * A.nsplit;
+    *it0 = sm[n_warps] < 0 ? end : static_cast<int>(sm[n_warps]);
+    *it1 = sm[n_warps + 1] < 0 ? end : static_cast<int>(sm[n_warps + 1]);
 }
 
 // What the rows of one tail item know about their tree; positions are relative to the tail tile.
@@ -233,7 +247,7 @@ __device__ __forceinline__ int tree_parent(const TreeArgs& A, const TreeItem& I,
     return i < I.n ? __ldg(A.parent + static_cast<long long>(I.b) * A.N + i) : -1;
 }
 
-__device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem& I, int lane, int par0, int par1) {
+__device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem I, int lane, int par0, int par1) {
     constexpr unsigned ALL = 0xffffffffu;
     int8_t* jump = reinterpret_cast<int8_t*>(S->list);   // list is filled last
     int par[2] = {par0, par1};
@@ -362,7 +376,7 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7F80
 // the source row of slot lane % 16; a row is HD / 8 chunks of 16 bytes, all of a lane's loads in
 // flight together; non-finite values are dropped and noted on the way.
 template <int HD>
-__device__ __noinline__ void gather_block(TreeInfo* S, const TreeArgs& A, const TreeItem& I, uint8_t* dst, int x, int quarter, int lane) {
+__device__ __noinline__ void gather_block(TreeInfo* S, const TreeArgs& A, const TreeItem I, uint8_t* dst, int x, int quarter, int lane) {
     constexpr int CH = HD / 8, ROWS = 32 / CH, U = 16 / ROWS;
     const int term = S->list[x], tp = S->pos[term], p = (tp & ~15) + (lane & 15);
     const uint16_t* src = nullptr;
@@ -418,20 +432,16 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* s) {
     tmem_ld_wait();
 }
 
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+                 "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-#pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-        float f[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[h + e]);
-        tmem_st16(taddr + h, f);
-    }
-    tmem_st_wait();
 }
 // MMA issue.  One thread issues an SM's MMAs, and what it computes for each one bounds the kernel as
 // soon as a tile's MMAs are short: with both 64-bit descriptors put together from addresses per MMA
@@ -514,29 +524,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 // Largest of 64 scores (a maximum is exact in any order; NaN are passed over).
-__device__ __forceinline__ float max64(const float* s) {
+__device__ __forceinline__ float max32(const float* s) {
     float x[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-    for (int j = 0; j < T; j += 2) x[(j / 2) & 3] = max3(x[(j / 2) & 3], s[j], s[j + 1]);
+    for (int j = 0; j < 32; j += 2) x[(j / 2) & 3] = max3(x[(j / 2) & 3], s[j], s[j + 1]);
     return fmaxf(max3(x[0], x[1], x[2]), x[3]);
 }
 // The running maximum after a tile whose largest score is mx, and what O and l are rescaled by.
 __device__ __forceinline__ float new_max(float m, float mx) { return (m == NEG_INF || mx > __fadd_rn(m, RESCALE_SLACK)) ? mx : m; }
 __device__ __forceinline__ float alpha(float m, float mn) { return (mn == NEG_INF || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn)); }
-// p = exp2(s - m) of 64 scores: packs them as bf16 pairs and adds them to ts in order (the decode
+// p = exp2(s - m) of 32 scores: packs them as bf16 pairs and adds them to ts in order (the decode
 // rows' operations; the p of a row that has seen no score yet are 0).
-__device__ __forceinline__ void exp_row(float* s, float m, uint32_t* pk, float& ts) {
+__device__ __forceinline__ void exp_half(float* s, float m, uint32_t* pk, float& ts) {
     if (m == NEG_INF) {   // rare: no score, or only NaN, so far
 #pragma unroll
-        for (int j = 0; j < T; ++j) s[j] = NEG_INF;
+        for (int j = 0; j < 32; ++j) s[j] = NEG_INF;
         m = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < T; j += 2) {
-        add2(s[j], s[j + 1], -m);
-        const float a0 = ex2_approx(s[j]), a1 = ex2_approx(s[j + 1]);
-        ts = __fadd_rn(__fadd_rn(ts, a0), a1);
-        pk[j / 2] = pack_bf16x2(a0, a1);
+    for (int j = 0; j < 32; j += 2) add2(s[j], s[j + 1], -m);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        s[j] = ex2_approx(s[j]), s[j + 1] = ex2_approx(s[j + 1]);
+        ts = __fadd_rn(__fadd_rn(ts, s[j]), s[j + 1]);
+        pk[j / 2] = pack_bf16x2(s[j], s[j + 1]);
     }
 }
 
@@ -643,7 +654,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // one CTA per item: the block (row tile, kv head and sequence, split), splits slowest; persistent
     // CTAs: a contiguous range numbered split-fastest (consecutive items mostly share Q)
-    int it0 = 0, it1 = 1;
+    int it0 = 0, it1 = 1, only_rt = -1;
     // barrier i of the list above; the stages' barriers come first
     if (tid < S::N_BARS && base - raw <= S::SLACK) {
         const int j = tid - (2 * SK + 2 * SV);
@@ -669,10 +680,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     int first = 0;
     TreeItem I0;
     if constexpr (MULTI) {
-        tree_share(A, reinterpret_cast<long long*>(&info), &it0, &it1);
+        tree_share(A, reinterpret_cast<long long*>(&info), &it0, &it1, &only_rt);
         I0.live = false;
         for (first = it0; first < it1; ++first) {
-            I0 = tree_item(A, first);
+            I0 = tree_item(A, first, only_rt);
             if (I0.live) break;
         }
     } else {
@@ -690,7 +701,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     auto next = [&](int it, TreeItem& I) {
         if (!MULTI || it >= it1) return;
         if (++I.split < A.nsplit) tree_item_split(I, A.NT);
-        else I = tree_item(A, it);
+        else I = tree_item(A, it, only_rt);
     };
     int par0 = -1, par1 = -1;   // a single item's parents, on their way meanwhile
     if (!MULTI && warp == 9) {
@@ -995,13 +1006,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             }
             tc_fence_before();
         };
-        // P of the group's tile into tensor memory, once the P V step of its tile before has read it
-        auto write_p = [&](const uint32_t* pk) -> bool {
-            if (n > 0 && !WW(pfree(grp, n - 1), ((n - 1) >> 1) & 1u)) return false;
-            tc_fence_after();
-            tmem_st32(tP + grp * 32 + lane_off, pk);
-            return true;
-        };
         TreeItem I = I0;
         for (int it = first; ok && it < it1; next(++it, I)) {
             if (!I.live) continue;
@@ -1033,13 +1037,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             for (int i = grp; i < I.nfull; i += 2) {
                 if (!WW(sbar(grp), n & 1u)) { ok = false; break; }
                 tc_fence_after();
-                float s[T];
-                tmem_ld64(tS + lane_off + grp * T, s);
-                tc_fence_before();
-                arrive_tc(sfree(grp));
+                float mx = NEG_INF;
 #pragma unroll
-                for (int j = 0; j < T; j += 2) mul2(s[j], s[j + 1], A.sl2);
-                const float mx = max64(s);
+                for (int h = 0; h < T; h += 32) {   // its maximum
+                    float s[32];
+                    tmem_ld16(tS + lane_off + grp * T + h, s);
+                    tmem_ld16(tS + lane_off + grp * T + h + 16, s + 16);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) mul2(s[j], s[j + 1], A.sl2);
+                    mx = fmaxf(mx, max32(s));
+                }
                 if (grp == 0) {
                     if (i > 0 && !take_max()) { ok = false; break; }
                 } else {
@@ -1056,8 +1064,25 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                     mbar_arrive(mpub(grp));
                 }
                 float sum = 0.f;
-                uint32_t pk[T / 2];
-                exp_row(s, mn, pk, sum);
+                if (n > 0 && !WW(pfree(grp, n - 1), ((n - 1) >> 1) & 1u)) { ok = false; break; }
+                tc_fence_after();
+                // the scores again, in two turns of one loop: unrolled it is twice the code and registers, and
+                // warps that wait for instructions were a fifth of the stalls (64 nodes at 131072 positions
+                // 309 us unrolled, 279 so; 32 x 13 nodes at 4000 to 8000: 199, 181)
+#pragma unroll 1
+                for (int h = 0; h < T; h += 32) {
+                    float s[32];
+                    uint32_t pk[16];
+                    tmem_ld16(tS + lane_off + grp * T + h, s);
+                    tmem_ld16(tS + lane_off + grp * T + h + 16, s + 16);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) mul2(s[j], s[j + 1], A.sl2);
+                    exp_half(s, mn, pk, sum);
+                    tmem_st16u(tP + grp * 32 + h / 2 + lane_off, pk);
+                }
+                tc_fence_before();
+                arrive_tc(sfree(grp));
                 if (grp == 0) {
                     if (i > 0 && !take_sum()) { ok = false; break; }
                     l = __fadd_rn(__fmul_rn(l, al), sum);
@@ -1067,7 +1092,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 }
                 // the P V step before is the other group's
                 const int before = grp ? n0 + i / 2 : n1 - 1;
-                if (!write_p(pk) || !rescale(al, i > 0, pfree(1 - grp, before), (before >> 1) & 1u)) { ok = false; break; }
+                if (!rescale(al, i > 0, pfree(1 - grp, before), (before >> 1) & 1u)) { ok = false; break; }
+                tmem_st_wait();
                 tc_fence_before();
                 arrive_tc(pready(grp));
                 ++n;
@@ -1259,11 +1285,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         float unused = 0.f;
 #pragma unroll 1
                         for (int r = 4; 16 * (r - 4) < I.n; ++r) {   // the tree's p again, to their slots
+                            const unsigned in = here ? static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu : 0u;
+                            if (!__any_sync(0xffffffffu, in)) continue;
                             load16(r);
                             exp16(unused);
                             const uint4 ps = *reinterpret_cast<const uint4*>(info.pos + 16 * (r - 4));
                             const uint32_t pw[4] = {ps.x, ps.y, ps.z, ps.w};
-                            const unsigned in = static_cast<unsigned>(mine >> (16 * r - 64)) & 0xFFFFu;
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 if (j == 8 && 16 * (r - 4) + 8 >= I.n) break;
