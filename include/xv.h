@@ -402,7 +402,8 @@ xv_status xv_kv_append_paged(const uint16_t* kv_src, long long src_stride, const
  * ctx_len and n_new are not changed.  All pointers are device memory; pos and
  * slots hold max_rows entries; the table is [B, max_pages] with page_size a
  * positive multiple of 64, as in xv_kv_pages.  Workspace:
- * xv_kv_pages_workspace_size(B) bytes, 16-byte aligned (0 for B < 1).
+ * xv_kv_pages_workspace_size(B) bytes, 16-byte aligned (0 for B < 1); it holds
+ * a counter that is zero between calls, so nothing else may write to it.
  * Errors: XV_ERR_ARG (null pointer, B, max_rows, max_pages or n_pages < 1),
  * XV_ERR_UNSUPPORTED (page_size, B above 65535, max_rows above 2^30, more than
  * 2^30 positions per request, unaligned workspace), XV_ERR_WORKSPACE,

@@ -51,6 +51,31 @@ def test_ragged_batches_equal_their_sequences_alone(xv, hd, Hq, Hkv, N, B, low, 
     assert xv.xv_device_check() == 0
 
 
+@pytest.mark.parametrize("hd,Hq,Hkv,N,B,low,high", [
+    (128, 32, 8, 40, 12, 100, 1500),    # two row tiles
+    (64, 16, 1, 56, 24, 400, 1200),     # seven
+    (256, 24, 4, 60, 4, 2000, 9000),    # three
+    (64, 64, 1, 63, 8, 0, 700),         # 32, the last one short; too many for whole bundles of CTAs
+    (64, 3, 1, 64, 200, 0, 200)])       # two, every item a tail
+def test_row_tiles_of_full_trees(xv, hd, Hq, Hkv, N, B, low, high):
+    """All trees have all their row tiles, which then go side by side to CTAs; some sequences have
+    none or a bad length."""
+    ctx, counts, trees, proj, (kc, vc) = batch(17, B, N, Hq, Hkv, hd, low, high)
+    rng = np.random.default_rng(1)
+    trees = [tree("mixed", N, rng) if b != 2 else [] for b in range(B)]
+    counts = [len(t) for t in trees]
+    X, K, V, par, n = dev(proj), dev(kc), dev(vc), parents(trees, N), i32(counts)
+    given = list(ctx)
+    given[3] = high + 1
+    out = run(xv, X, K, V, given, par, n, N, Hq, Hkv, hd, max_ctx=high, fill=3).reshape(B, N, -1)
+    assert bits(xv) == 4
+    for b in range(B):
+        one = run(xv, X[b * N:(b + 1) * N], K[b:b + 1], V[b:b + 1], [ctx[b]], par[b:b + 1], n[b:b + 1], N, Hq, Hkv, hd, fill=3)
+        assert (out[b] == 3).all() if b in (2, 3) else same_bits(out[b], one), f"sequence {b}: ctx {ctx[b]}"
+    check(out.reshape(B * N, -1)[: 2 * N], proj[: 2 * N], kc[:2], vc[:2], ctx[:2], trees[:2], N, Hq, Hkv, hd, False, "full", nodes=(0, 20, N - 1))
+    assert xv.xv_device_check() == 0
+
+
 def test_bad_sequences_of_a_large_batch_leave_the_others(xv):
     """Lengths out of range are reported and their rows left; all sequences bad is an empty call."""
     hd, Hq, Hkv, N, B = 128, 8, 2, 13, 80
