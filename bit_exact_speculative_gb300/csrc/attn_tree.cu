@@ -301,19 +301,29 @@ __device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const Tre
     const bool first[2] = {real[0] && pos[0] < T, real[1] && pos[1] < T};
     const u64 tile0 = mask(first);
     __syncwarp();
+    // nodes below each of the lane's two (and themselves): the ancestors' bits, transposed by ballots
+    // (a walk over 43 terminal nodes took 10000 cycles)
+    const u64 anc[2] = {S->anc[lane], S->anc[lane + 32]};
+    u64 below[2] = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const unsigned lo = static_cast<unsigned>(anc[0] >> (32 * h)), hi = static_cast<unsigned>(anc[1] >> (32 * h));
+#pragma unroll 2
+        for (int i = 0; i < 32 && 32 * h + i < I.n; ++i) {
+            const unsigned b0 = __ballot_sync(ALL, (lo >> i) & 1), b1 = __ballot_sync(ALL, (hi >> i) & 1);
+            if (lane == i) below[h] = (static_cast<u64>(b1) << 32) | b0;
+        }
+    }
     // the block of a node: the lowest terminal node at or below it in its group
     int rep[2] = {0, 0};
-    bool found[2] = {!real[0], !real[1]};
-    for (u64 t = terms; t; t &= t - 1) {
-        const int i = __ffsll(static_cast<long long>(t)) - 1;
-        const u64 a = S->anc[i];
-        const int grp = S->pos[i] >> 4;
+    const int g0 = I.c >> 4, g1 = (I.c + I.n - 1) >> 4;   // groups that nodes can stand in
+#pragma unroll 1
+    for (int grp = g0; grp <= g1; ++grp) {
+        const bool in[2] = {real[0] && (pos[0] >> 4) == grp, real[1] && (pos[1] >> 4) == grp};
+        const u64 gm = mask(in) & terms;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-            if (!found[u] && ((a >> (lane + 32 * u)) & 1) && grp == (pos[u] >> 4)) {
-                rep[u] = i;
-                found[u] = true;
-            }
+            if (in[u]) rep[u] = __ffsll(static_cast<long long>(below[u] & gm)) - 1;
     }
     // the blocks this row tile's nodes run through
     u64 need = 0;
@@ -321,14 +331,13 @@ __device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const Tre
     for (int u = 0; u < 2; ++u) {
         const int i = lane + 32 * u;
         S->rep[i] = static_cast<uint8_t>(rep[u]);
-        if (real[u] && i >= I.node0(A.NT) && i < I.node0(A.NT) + A.NT) need |= (1ull << rep[u]) | (S->anc[i] & ends);
+        if (real[u] && i >= I.node0(A.NT) && i < I.node0(A.NT) + A.NT) need |= (1ull << rep[u]) | (anc[u] & ends);
     }
     need = (static_cast<u64>(__reduce_or_sync(ALL, static_cast<unsigned>(need >> 32))) << 32) |
            __reduce_or_sync(ALL, static_cast<unsigned>(need));
     int before = 0, nb0 = 0;
-    const int g1 = (I.c + I.n - 1) >> 4;   // the last group a node can stand in
 #pragma unroll 1
-    for (int grp = I.c >> 4; grp <= g1; ++grp) {
+    for (int grp = g0; grp <= g1; ++grp) {
         const bool in[2] = {((need >> lane) & 1) && (pos[0] >> 4) == grp, ((need >> (lane + 32)) & 1) && (pos[1] >> 4) == grp};
         const u64 gm = mask(in);
 #pragma unroll
@@ -372,6 +381,25 @@ __device__ __forceinline__ int tree_page(const KvPages& kv, int b, int p, int* r
 // the sign's place.
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
+// Rare: non-finite values of a gathered block replaced by zeros, and whose they were noted.  A lane goes over the
+// 16 bytes that it wrote of every `rows`-th row.
+__device__ __noinline__ void gather_fix(TreeInfo* S, uint8_t* d, int quarter, int ch, int first, int rows, int who) {
+    for (int r0 = 0; r0 < 16; r0 += rows) {
+        const int r = r0 + first, s = quarter * 16 + r, w = __shfl_sync(0xffffffffu, who, r);
+        uint32_t* e = reinterpret_cast<uint32_t*>(d + s * 128 + (((ch & 7) ^ (s & 7)) * 16));
+        uint32_t any = 0;
+        for (int k = 0; k < 4; ++k) {
+            any |= non_finite(e[k]);
+            if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+            if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
+        }
+        if (any) {
+            if (w < 64) atomicOr(&S->vbad, 1ull << w);
+            else atomicOr(&S->cbad, 1u << (w - 64));
+        }
+    }
+}
+
 // Gathers the V rows of block x (16 slots) into its quarter of a V stage, by one warp.  A lane finds
 // the source row of slot lane % 16; a row is HD / 8 chunks of 16 bytes, all of a lane's loads in
 // flight together; non-finite values are dropped and noted on the way.
@@ -402,22 +430,14 @@ __device__ __noinline__ void gather_block(TreeInfo* S, const TreeArgs& A, const 
         v[u] = make_uint4(0, 0, 0, 0);
         if (q) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + ch);
     }
+    uint32_t bad = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int r = u * ROWS + lane / CH, s = quarter * 16 + r;
-        const int w = __shfl_sync(0xffffffffu, who, r);
-        if (non_finite(v[u].x) | non_finite(v[u].y) | non_finite(v[u].z) | non_finite(v[u].w)) {
-            uint32_t* e = reinterpret_cast<uint32_t*>(&v[u]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
-                if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
-            }
-            if (w < 64) atomicOr(&S->vbad, 1ull << w);
-            else atomicOr(&S->cbad, 1u << (w - 64));
-        }
+        const int s = quarter * 16 + u * ROWS + lane / CH;
+        bad |= non_finite(v[u].x) | non_finite(v[u].y) | non_finite(v[u].z) | non_finite(v[u].w);
         *reinterpret_cast<uint4*>(d + s * 128 + (((ch & 7) ^ (s & 7)) * 16)) = v[u];
     }
+    if (__any_sync(0xffffffffu, bad)) gather_fix(S, d, quarter, ch, lane / CH, ROWS, who);
 }
 
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
@@ -597,6 +617,11 @@ __device__ __noinline__ void tree_add_bad(const TreeArgs& A, const TreeBad& F) {
     __syncwarp();
 }
 
+// Whether a CTA of one item forms the output of its rows itself: up to DIRECT_MAX values (64 positions: 16 x 64
+// values 6.4 us, with the combine 8.3; 64 x 128 12.2 and 12.8; 24 x 256 with a gate 10.4 and 10.6; 96 x 256 with a
+// gate 26.3 and 17.6).
+constexpr int DIRECT_MAX = 6144;
+__host__ __device__ inline bool tree_direct(int rows, int hd) { return rows * hd <= DIRECT_MAX; }
 // A value of the output: acc / L, with the gate's product where there is one.
 __device__ __forceinline__ uint16_t tree_out(float acc, float L, const uint16_t* gate) {
     float y = __fdiv_rn(acc, L);
@@ -715,10 +740,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // one split per row: the partials stay in shared memory, where the K and V rings were, and the whole
-    // CTA forms the output from them.  Without the combine's launch 8 nodes at 128 positions take 6.7 us,
-    // with it 8.3.
-    const bool direct = !MULTI && A.nsplit == 1;
+    // one split per row and few rows: the partials stay in shared memory, where the K and V rings were,
+    // and the whole CTA forms the output from them, without the combine's launch
+    const bool direct = !MULTI && A.nsplit == 1 && tree_direct(A.NT * A.G, HD);
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO0 = tmem + 128, tT = tO0 + S::NO * HD, tP = tT + 64;
 
@@ -1452,7 +1476,7 @@ xv_status tree_launch_split(const CUtensorMap* tm, const TreeArgs& a, bool* comb
     // past two waves of items, persistent CTAs (the rule of the decode rows' launch); rows of one split
     // are finished by the split kernel where its CTA has one item
     const bool multi = n_items > 2ll * sms;
-    *combined = !multi && a.nsplit == 1;
+    *combined = !multi && a.nsplit == 1 && tree_direct(a.NT * a.G, HD);
     trace_pre(s);
     if (multi) launch_k(attn_tree_kernel<HD, true>, dim3(sms), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
     else launch_k(attn_tree_kernel<HD, false>, dim3(a.nrt, a.Hkv * a.B, a.nsplit), dim3(TREE_THREADS), SMEM, s, tm[0], tm[1], tm[2], tm[3], a);
