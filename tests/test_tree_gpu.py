@@ -202,6 +202,30 @@ def test_other_branches_and_garbage_change_nothing(xv):
         assert np.array_equal(have, want), i
 
 
+@pytest.mark.parametrize("hd,ctx", [(64, 37), (128, 37), (256, 37), (128, 1000), (256, 4133)])
+def test_non_finite_values_reach_their_columns_only(xv, hd, ctx):
+    """Infinities and NaN in V, of nodes and of a cache position in the tree's first group of 16: in
+    the rows that see them their column, every other value with the bits of the clean run."""
+    Hq, Hkv, N, g0 = 4, 2, 40, ctx & ~15
+    par = tree("mixed", N, np.random.default_rng(4))
+    proj, (kc, vc) = rows(9, 1, N, Hq, Hkv, hd, f"nf{hd}"), cache(9, 1, Hkv, ctx + 5, hd, f"nf{ctx}.{hd}")
+    clean = host_u16(run(xv, dev(proj), dev(kc), dev(vc), [ctx], parents([par], N), None, N, Hq, Hkv, hd)).reshape(N, Hq, hd)
+    heads = proj.reshape(N, 2 * Hq + 2 * Hkv, hd)
+    heads[9, 2 * Hq + Hkv, 5], heads[17, 2 * Hq + Hkv + 1, hd - 1], vc[0, 1, g0 + 1, 7] = 0x7F80, 0x7FC0, 0xFF80
+    got = host_u16(run(xv, dev(proj), dev(kc), dev(vc), [ctx], parents([par], N), None, N, Hq, Hkv, hd)).reshape(N, Hq, hd)
+    for i in range(N):
+        path = chain_of(par, i)
+        want = f64(clean[i])
+        if 9 in path:
+            want[:2, 5] = np.inf
+        if 17 in path:
+            want[2:, hd - 1] = np.nan
+        want[2:, 7] = -np.inf
+        have = f64(got[i])
+        assert np.array_equal(np.isnan(have), np.isnan(want)) and np.array_equal(have[~np.isnan(want)], want[~np.isnan(want)]), i
+    assert xv.xv_device_check() == 0
+
+
 @pytest.mark.parametrize("hd,Hq,Hkv,N,page,ctx,kind", [(256, 24, 4, 16, 64, [2183, 640, 64], "mixed"), (64, 6, 2, 64, 128, [500, 1], "wide"),
                                                        (128, 8, 8, 9, 192, [191, 192, 193, 4100], "pairs")])
 def test_paged_equals_contiguous(xv, hd, Hq, Hkv, N, page, ctx, kind):
