@@ -9,8 +9,8 @@
 // modulo 2^64 is the angle modulo one turn to 2^-64 * p of a turn, for any 32-bit p.  An fp32
 // angle p * f_i would be off by p * 2^-24 radians (0.008 at 131072 positions, 0.03 at 500000).
 //
-// What bounds it: every value is read once and written once.  8192 rows of 40 + 8 heads of 128: 47.6 us
-// for 201 MB, 4.2 TB/s, 0.63 of the measured copy rate; more or fewer resident CTAs change nothing, the
+// What bounds it: every value is read once and written once.  8192 rows of 40 + 8 heads of 128: 43.8 us
+// for 201 MB, 4.6 TB/s, 0.69 of the measured copy rate; more or fewer resident CTAs change nothing, the
 // ~110 instructions a lane needs per 8 values share the issue slots with the loads.  A verify step's 8
 // rows: 2.0 us, one load-to-store latency.  A head takes hd/8 lanes of 16 bytes each, its sum of
 // squares a fixed shuffle tree inside them, so a head's bits depend on that head, its weight and its
@@ -241,16 +241,22 @@ xv_status rope_launch(RopeArgs a, int hd, cudaStream_t s) {
     const int H = a.Hq + a.Hkv + (a.k_out ? 0 : a.Hkv), hpp = ROPE_THREADS * 8 / hd;
     // Few rows: one pass of heads per CTA, so that a row's heads spread over the SMs; more: as many
     // passes as keep the CTAs to one wave (8 of 256 threads per SM), up to the ROPE_U whose loads go
-    // out together; many rows of few heads: as many rows as fill those passes.  Measured: 500 rows of
-    // 32 heads of 256, one pass 8.7 us, this rule 6.0; 8192 rows of 24 heads of 64, a row per CTA
-    // 30.7 us, this rule 15.0.
+    // out together; many rows: several per CTA, up to four passes, so that the loads of a pass are all
+    // used and what a CTA does once is done for more.  Measured: 500 rows of 32 heads of 256, one pass
+    // 8.7 us, this rule 6.0; 8192 rows of 24 heads of 64, a row per CTA 30.7 us, five 15.0, six 17.1; of
+    // 48 heads of 128, a row 47.7, four 43; of 28 heads of 256, a row 60.8, four 54; 4096 rows of 32
+    // heads of 256, a row 31.4, three 32.1.
     int sms = 0;
     if (xv_status st = device_sm_count(&sms)) return st;
     int hpc = hpp, rpc = 1;
     while (hpc < ROPE_U * hpp && hpc < H && static_cast<long long>(a.M) * ceil_div(H, hpc) > 8ll * sms) hpc += hpp;
     if (hpc >= H) {
         hpc = H;
-        while (rpc < ROPE_ROWS && (rpc + 1) * H <= ROPE_U * hpp && (rpc + 1) * a.rot / 2 <= ROPE_TAB && a.M / (rpc + 1) >= 8 * sms) ++rpc;
+        // units of a full pass's loads, of r rows' passes: the r that leaves the least of them empty
+        const int pass = ROPE_U * hpp;
+        auto room = [&](int r) { return ceil_div(r * H, pass) * pass; };
+        for (int r = 2; r <= ROPE_ROWS && r * H <= 4 * pass && r * H < 512 && r * a.rot / 2 <= ROPE_TAB && a.M / r >= 8 * sms; ++r)
+            if (static_cast<long long>(r) * room(rpc) >= static_cast<long long>(rpc) * room(r)) rpc = r;
     }
     const dim3 grid(ceil_div(a.M, rpc), ceil_div(H, hpc));
     const unsigned inv_h = (65536u + hpc - 1) / hpc;

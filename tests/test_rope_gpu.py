@@ -57,7 +57,9 @@ def inputs(seed, M, Hq, Hkv, hd, sigma=1.0):
 @pytest.mark.parametrize("hd,Hq,Hkv,M,rot,inter,base", [
     (256, 24, 4, 8, 64, False, 1e7), (256, 24, 4, 3, 256, True, 1e4), (128, 32, 8, 1, 128, False, 1e6),
     (128, 5, 1, 70, 16, True, 1e4), (64, 2, 1, 9, 64, False, 1e4), (64, 7, 7, 1100, 48, True, 1e5),
-    (256, 3, 3, 1030, 32, False, 1e7), (64, 1, 1, 1, 0, False, 1e4), (128, 40, 2, 4, 96, False, 1e4)])
+    (256, 3, 3, 1030, 32, False, 1e7), (64, 1, 1, 1, 0, False, 1e4), (128, 40, 2, 4, 96, False, 1e4),
+    # several rows to a CTA
+    (64, 7, 7, 5001, 48, True, 1e5), (128, 12, 4, 4870, 128, False, 1e6), (64, 1, 1, 20011, 16, False, 1e4)])
 def test_rows_against_the_formula(xv, hd, Hq, Hkv, M, rot, inter, base):
     """Positions from 0 through 500000, negative ones among them."""
     proj, qn, kn = inputs(1, M, Hq, Hkv, hd)
@@ -120,7 +122,8 @@ def test_zero_heads_and_non_finite_values_stay_in_their_head(xv):
     assert np.array_equal(a, b) and np.array_equal(outs[0][1], outs[1][1])
 
 
-@pytest.mark.parametrize("hd,Hq,Hkv,M,page,inter", [(256, 24, 4, 9, 64, False), (128, 8, 2, 1500, 128, True), (64, 3, 1, 33, 192, False)])
+@pytest.mark.parametrize("hd,Hq,Hkv,M,page,inter", [(256, 24, 4, 9, 64, False), (128, 8, 2, 1500, 128, True), (64, 3, 1, 33, 192, False),
+                                                       (128, 32, 8, 4870, 128, True)])
 def test_append_writes_the_rows_bits_to_their_slots(xv, hd, Hq, Hkv, M, page, inter):
     """K as xv_qk_norm_rope gives it and V as it is, at the slots and nowhere else; a row with slot -1
     and rows from *n_rows on write no K or V (the latter no q either)."""
