@@ -23,6 +23,10 @@
 // thread per row.  The full 128 rows of the MMA are used: at 64 nodes x 6 q heads per kv head an SM
 // does 128 x 64 scores per K tile, so wide trees over long contexts are bound by the tensor core and
 // the softmax, small ones by the K/V stream, short contexts by latency.
+//
+// Measured (24 q / 4 kv heads of 256 unless said): 8 nodes at 131072 positions 101 us, 5.3 TB/s of K and V;
+// 64 nodes there 273 us, 755 TFLOP/s; 32 x 13 nodes at 4000 to 8000, 32 / 8 heads of 128, 178 us, 4.0 TB/s;
+// 16 nodes at 2183 16.7 us; 8 nodes at 128, 2 / 1 heads of 64, 6.5 us.
 #include <cmath>
 
 #include "xv_internal.h"
@@ -1390,6 +1394,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 // acc += w_s o_s in split order, out = acc / L (and the output gate).  A warp owns 16 columns of eight
 // rows, four per lane: each of its loads takes whole 128-byte lines of the partials.  The four lanes of a
 // row read its m and l and form its weights, each weight once a warp; eight splits are in flight.
+// 13312 rows of 128 in 10 splits 18 us, 1536 rows of 256 in 71 splits 26 us.
 constexpr int COMB_THREADS = 128;
 
 __global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const __grid_constant__ TreeArgs A, int hd) {
