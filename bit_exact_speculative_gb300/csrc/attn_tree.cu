@@ -158,10 +158,11 @@ __device__ __forceinline__ void tree_report(const TreeArgs& A, int b) {
 
 // The items [*it0, *it1) of persistent CTA `blockIdx.x`: contiguous shares of the batch by weight, so that
 // sequences of different lengths even out (32 x 13 nodes at 4000 to 8000 positions: 242 us with shares of
-// equal item counts, 215 so).  A tile weighs 1, an item ITEM_WEIGHT more (2 to 8 measured alike) and a
-// tree's tail TAIL_WEIGHT (64 nodes at 32768 positions: 118 us with 4, 105 with 16).  A cut is a weight
-// between 0 and the total; its item is found from prefix sums over the sequences, a run of them per
-// thread.  `sm`: one word per warp and the two results, not written before the next barrier.
+// equal item counts, 215 so).  A tile weighs 1, an item ITEM_WEIGHT more (1 to 4 measured alike) and a
+// tree's tail TAIL_WEIGHT (64 nodes at 32768 positions: 99 us with 4 to 8, 90 with 16; 8 x 40 nodes at
+// 9000: 123 and 115).  A cut is a weight between 0 and the total; its item is found from prefix sums over
+// the sequences, a run of them per thread.  `sm`: one word per warp and the two results, not written
+// before the next barrier.
 //
 // Where all trees have all row tiles (and at least 7/8 of the CTAs form whole bundles), a share goes to a
 // bundle of nrt CTAs, one per row tile (*rt; else -1): they read the same K and V tiles at the same time,
