@@ -8,6 +8,7 @@ library raises at import of the first call: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -17,6 +18,16 @@ LIB_PATH = os.path.join(_HERE, "libxv.so")
 
 vp = ctypes.c_void_p
 c_int, c_ll, c_sz, c_float = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
+
+
+class int_arg:
+    """An int argument.  ctypes passes a Python int as a C int by itself; its c_int type would make an
+    object of every one first (0.13 us against 0.04)."""
+    from_param = staticmethod(operator.index)
+
+
+long_arg = vp   # a 64-bit integer argument travels like an address, and void* converts it in 0.08 us, c_longlong in 0.13
+
 
 XV_OK, XV_ERR_ARG, XV_ERR_UNSUPPORTED, XV_ERR_WORKSPACE, XV_ERR_CUDA, XV_ERR_DEVICE_CHECK = 0, -1, -2, -3, -4, -5
 XV_GEMM_M_MAX = 64
@@ -58,6 +69,7 @@ class LayerState(ctypes.Structure):
 
 class KvPages(ctypes.Structure):
     _fields_ = [("page_table", vp), ("page_size", c_int), ("max_pages", c_int), ("n_pages", c_int)]
+    _table = None   # the table's tensor, where kv_pages made the struct
 
 
 class BlockState(ctypes.Structure):
@@ -111,21 +123,21 @@ _SIGS = {
                                    c_int, c_float, vp, c_ll, vp, c_ll, vp, c_sz, vp], c_int),
     "xv_kv_append_paged": ([vp, c_ll, vp, c_int, c_int, c_int, c_int, ctypes.POINTER(KvPages), vp, vp, vp], c_int),
     "xv_kv_pages_workspace_size": ([c_int], c_sz),
-    "xv_kv_pages_update": ([vp, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, c_int, vp, vp, vp, c_int, vp, c_sz, vp],
-                           c_int),
-    "xv_qk_norm_rope": ([vp, c_ll, vp, c_ll, vp, c_ll, vp, c_ll, ctypes.POINTER(QkRope), vp, vp, c_int, c_int, c_int,
-                         c_int, vp], c_int),
-    "xv_qk_norm_rope_append": ([vp, c_ll, vp, c_ll, vp, c_ll, ctypes.POINTER(QkRope), vp, vp, vp, c_int, c_int, c_int,
-                                c_int, c_int, c_int, vp, vp, vp], c_int),
-    "xv_tree_positions": ([vp, vp, vp, c_int, c_int, vp, vp], c_int),
+    "xv_kv_pages_update": ([vp, int_arg, int_arg, int_arg, vp, vp, vp, vp, vp, vp, vp, int_arg, vp, vp, vp, int_arg, vp, long_arg,
+                            vp], c_int),
+    "xv_qk_norm_rope": ([vp, long_arg, vp, long_arg, vp, long_arg, vp, long_arg, ctypes.POINTER(QkRope), vp, vp, int_arg, int_arg, int_arg,
+                         int_arg, vp], c_int),
+    "xv_qk_norm_rope_append": ([vp, long_arg, vp, long_arg, vp, long_arg, ctypes.POINTER(QkRope), vp, vp, vp, int_arg, int_arg, int_arg,
+                                int_arg, int_arg, int_arg, vp, vp, vp], c_int),
+    "xv_tree_positions": ([vp, vp, vp, int_arg, int_arg, vp, vp], c_int),
     "xv_attn_tree_workspace_size": ([c_int, c_int, c_int, c_int, c_int], c_sz),
-    "xv_attn_tree": ([vp, c_ll, vp, vp, vp, vp, c_ll, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float,
-                      vp, c_ll, vp, c_ll, vp, c_sz, vp], c_int),
-    "xv_attn_tree_paged": ([vp, c_ll, vp, vp, ctypes.POINTER(KvPages), vp, vp, c_ll, vp, vp, c_int, c_int, c_int, c_int,
-                            c_int, c_int, c_float, vp, c_ll, vp, c_ll, vp, c_sz, vp], c_int),
-    "xv_tree_accept": ([vp, vp, vp, vp, c_int, c_int, vp, vp, vp, vp], c_int),
-    "xv_kv_append_path": ([vp, c_ll, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, vp, vp, vp], c_int),
-    "xv_kv_append_path_paged": ([vp, c_ll, vp, vp, vp, c_int, c_int, c_int, c_int, ctypes.POINTER(KvPages), vp, vp, vp],
+    "xv_attn_tree": ([vp, long_arg, vp, vp, vp, vp, long_arg, vp, vp, int_arg, int_arg, int_arg, int_arg, int_arg, int_arg, int_arg,
+                      c_float, vp, long_arg, vp, long_arg, vp, long_arg, vp], c_int),
+    "xv_attn_tree_paged": ([vp, long_arg, vp, vp, ctypes.POINTER(KvPages), vp, vp, long_arg, vp, vp, int_arg, int_arg, int_arg, int_arg,
+                            int_arg, int_arg, c_float, vp, long_arg, vp, long_arg, vp, long_arg, vp], c_int),
+    "xv_tree_accept": ([vp, vp, vp, vp, int_arg, int_arg, vp, vp, vp, vp], c_int),
+    "xv_kv_append_path": ([vp, long_arg, vp, vp, vp, int_arg, int_arg, int_arg, int_arg, int_arg, vp, vp, vp], c_int),
+    "xv_kv_append_path_paged": ([vp, long_arg, vp, vp, vp, int_arg, int_arg, int_arg, int_arg, ctypes.POINTER(KvPages), vp, vp, vp],
                                 c_int),
     "xv_gdn_in_dim": ([ctypes.POINTER(BlockConfig)], c_int),
     "xv_gdn_hist_stride": ([ctypes.POINTER(BlockConfig)], c_int),
@@ -191,6 +203,67 @@ def _row_stride(t: torch.Tensor) -> int:
     s = t.stride()
     assert len(s) >= 2 and s[-1] == 1, "rows must be contiguous"
     return s[0]
+
+
+# The library sees addresses only: a tensor of another type, layout or size than it takes it for is
+# read or written past its end.  These give a tensor's address (_rows: and row stride) once it is what
+# the call needs, on the device of the call's first tensor; _on, last, gives the stream, on the device
+# that must hold them all.  An attribute of a tensor takes ~0.06 us, so each is read once.
+
+def _refuse(name, t, want):
+    raise ValueError(f"{name}: {want} on the call's device needed, got {str(t.dtype)[6:]} {list(t.shape)}, "
+                     f"strides {list(t.stride())}, on {t.device}")
+
+
+def _flat(name, t, n, dev, dtype=torch.int32):
+    """n or more contiguous entries."""
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, f"{n} contiguous {str(dtype)[6:]}")
+    return t.data_ptr()
+
+
+def _one(name, t, dev):
+    """One int32."""
+    if t.dtype is not torch.int32 or t.numel() < 1 or t.get_device() != dev:
+        _refuse(name, t, "1 int32")
+    return t.data_ptr()
+
+
+def _flat16(name, t, n, dev):
+    """n or more contiguous 2-byte values."""
+    if t.itemsize != 2 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, f"{n} contiguous 2-byte values")
+    return t.data_ptr()
+
+
+def _rows(name, t, m, width, dev):
+    """m or more rows (the first dimension) of width or more 2-byte values."""
+    shape, stride = t.shape, t.stride()
+    try:
+        (have, cols), (step, one) = shape, stride
+    except ValueError:   # another number of dimensions: a row's must lie densely
+        ok = len(shape) > 2 and shape[0] > 0 and t[0].is_contiguous()
+        (have, cols), (step, one) = (shape[0], t[0].numel()) if ok else (0, 0), (stride[0], 1) if ok else (0, 0)
+    if have < m or cols < width or one != 1 or t.itemsize != 2 or t.get_device() != dev:
+        _refuse(name, t, f"{m} rows of {width} contiguous 2-byte values")
+    return t.data_ptr(), step
+
+
+def _ws(t, dev):
+    if not t.is_contiguous() or t.get_device() != dev:
+        _refuse("ws", t, "a contiguous workspace")
+    return t.data_ptr()
+
+
+def _on(dev, stream=None):
+    cur = torch.cuda.current_device() if dev >= 0 else None
+    if cur != dev:
+        raise ValueError("tensors in the current device's memory needed, got " + ("host memory" if dev < 0 else f"cuda:{dev}"))
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream: one of cuda:{dev} needed, got one of {stream.device}")
+    return stream.cuda_stream
 
 
 # ------------------------------------------------------------------ misc
@@ -382,11 +455,20 @@ def xv_kv_append(kv_src, src_stride, ctx_len, R, B, Hkv, hd, Lmax, kc, vc, strea
 
 
 def kv_pages(page_table, page_size: int, n_pages: int) -> KvPages:
-    """The page description of a paged KV pool: page_table int32 [B, max_pages] on the device
-    (kept referenced by the returned struct)."""
+    """The page description of a paged KV pool: page_table int32 [B, max_pages], contiguous, on the
+    device (kept referenced by the returned struct)."""
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError(f"page_table: a contiguous int32 [B, max_pages] needed, got {str(page_table.dtype)[6:]} "
+                         f"{list(page_table.shape)}, strides {list(page_table.stride())}")
     pages = KvPages(page_table.data_ptr(), int(page_size), int(page_table.shape[1]), int(n_pages))
-    pages._table = page_table
+    pages._table, pages._rows, pages._dev = page_table, page_table.shape[0], page_table.get_device()
     return pages
+
+
+def _pages_of(pages: KvPages, B, dev):
+    """Checks that the table has a row for each of B sequences."""
+    if pages._table is not None and (pages._rows < B or pages._dev != dev):
+        _refuse("page_table", pages._table, f"{B} rows")
 
 
 def xv_attn_decode_rows_paged(q, q_stride, kpool, vpool, pages: KvPages, ctx_len, R, B, Hq, Hkv, hd, max_ctx, scale,
@@ -411,14 +493,17 @@ def xv_kv_pages_update(pages: KvPages, free_pages, n_free, held, ctx_len, n_new,
     """Pages, positions and slots of every request's new rows (the C header has the rules); the
     requests are the entries of ctx_len.  n_free and held are updated in place unless
     n_free_out / held_out are given."""
-    B = ctx_len.numel()
-    if free_pages.numel() < pages.n_pages or row_start.numel() < B + 1 or pos.numel() < slots.numel():
-        raise ValueError("free_pages needs n_pages entries, row_start B + 1 and pos as many as slots")
-    _check(lib().xv_kv_pages_update(pages.page_table, pages.page_size, pages.max_pages, pages.n_pages, _ptr(free_pages),
-                                    _ptr(n_free), _ptr(n_free if n_free_out is None else n_free_out), _ptr(held),
-                                    _ptr(held if held_out is None else held_out), _ptr(ctx_len), _ptr(n_new), B,
-                                    _ptr(row_start), _ptr(pos), _ptr(slots), slots.numel(), _ptr(ws),
-                                    ws.nbytes, _stream(stream)))
+    B, n_rows, dev = ctx_len.numel(), slots.numel(), ctx_len.get_device()
+    _pages_of(pages, B, dev)
+    nf, h = _one("n_free", n_free, dev), _flat("held", held, B, dev)
+    _check(lib().xv_kv_pages_update(pages.page_table, pages.page_size, pages.max_pages, pages.n_pages,
+                                    _flat("free_pages", free_pages, pages.n_pages, dev), nf,
+                                    nf if n_free_out is None else _one("n_free_out", n_free_out, dev), h,
+                                    h if held_out is None else _flat("held_out", held_out, B, dev),
+                                    _flat("ctx_len", ctx_len, B, dev), _flat("n_new", n_new, B, dev), B,
+                                    _flat("row_start", row_start, B + 1, dev), _flat("pos", pos, n_rows, dev),
+                                    _flat("slots", slots, n_rows, dev, torch.int64), n_rows, _ws(ws, dev), ws.nbytes,
+                                    _on(dev, stream)))
 
 
 # ------------------------------------------------- head norms and rotation
@@ -431,38 +516,57 @@ def rope_freqs(rot: int, base: float = 10000.0, scale: float = 1.0, device="cuda
     return torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in f], dtype=torch.int64, device=device)
 
 
-def _qk_rope(q_norm, k_norm, eps, freqs, interleaved):
-    return QkRope(None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(), eps,
-                  None if freqs is None else freqs.data_ptr(), 0 if freqs is None else 2 * freqs.numel(),
-                  int(interleaved))
+def _qk_rope(q_norm, k_norm, eps, freqs, interleaved, hd, dev):
+    return QkRope(None if q_norm is None else _flat16("q_norm", q_norm, hd, dev),
+                  None if k_norm is None else _flat16("k_norm", k_norm, hd, dev), eps,
+                  None if freqs is None else _flat("freqs", freqs, 0, dev, torch.int64),
+                  0 if freqs is None else 2 * freqs.numel(), int(interleaved))
 
 
 def xv_qk_norm_rope(q, k, pos, Hq, Hkv, hd, q_out, k_out, q_norm=None, k_norm=None, eps=1e-6, freqs=None,
                     interleaved=False, n_rows=None, stream=None):
     """Norms and rotates the heads of q [M, >= Hq*hd] into q_out and of k [M, >= Hkv*hd] into k_out
     (each may be its input); freqs from :func:`rope_freqs` (None: no rotation)."""
-    r = _qk_rope(q_norm, k_norm, eps, freqs, interleaved)
-    _check(lib().xv_qk_norm_rope(_ptr(q), _row_stride(q), _ptr(q_out), _row_stride(q_out), _ptr(k), _row_stride(k),
-                                 _ptr(k_out), _row_stride(k_out), ctypes.byref(r), _ptr(pos), _ptr(n_rows), q.shape[0],
-                                 Hq, Hkv, hd, _stream(stream)))
+    M, dev = q.shape[0], q.get_device()
+    r = _qk_rope(q_norm, k_norm, eps, freqs, interleaved, hd, dev)
+    a, sa = _rows("q", q, M, Hq * hd, dev)
+    b, sb = _rows("q_out", q_out, M, Hq * hd, dev)
+    c, sc = _rows("k", k, M, Hkv * hd, dev)
+    d, sd = _rows("k_out", k_out, M, Hkv * hd, dev)
+    _check(lib().xv_qk_norm_rope(a, sa, b, sb, c, sc, d, sd, ctypes.byref(r), None if pos is None else _flat("pos", pos, M, dev),
+                                 None if n_rows is None else _one("n_rows", n_rows, dev), M, Hq, Hkv, hd,
+                                 _on(dev, stream)))
 
 
 def xv_qk_norm_rope_append(q, kv, pos, slots, Hq, Hkv, hd, q_out, kpool, vpool, page_size, n_pages, q_norm=None,
                            k_norm=None, eps=1e-6, freqs=None, interleaved=False, n_rows=None, stream=None):
     """The same with the k heads of kv [M, k | v], normed and rotated, and its v heads written to
     slots (int64 [M]) of the pools."""
-    r = _qk_rope(q_norm, k_norm, eps, freqs, interleaved)
-    _check(lib().xv_qk_norm_rope_append(_ptr(q), _row_stride(q), _ptr(q_out), _row_stride(q_out), _ptr(kv),
-                                        _row_stride(kv), ctypes.byref(r), _ptr(pos), _ptr(slots), _ptr(n_rows),
-                                        q.shape[0], Hq, Hkv, hd, page_size, n_pages, _ptr(kpool), _ptr(vpool),
-                                        _stream(stream)))
+    M, dev = q.shape[0], q.get_device()
+    r = _qk_rope(q_norm, k_norm, eps, freqs, interleaved, hd, dev)
+    size = n_pages * Hkv * page_size * hd
+    a, sa = _rows("q", q, M, Hq * hd, dev)
+    b, sb = _rows("q_out", q_out, M, Hq * hd, dev)
+    c, sc = _rows("kv", kv, M, 2 * Hkv * hd, dev)
+    _check(lib().xv_qk_norm_rope_append(a, sa, b, sb, c, sc, ctypes.byref(r),
+                                        None if pos is None else _flat("pos", pos, M, dev),
+                                        _flat("slots", slots, M, dev, torch.int64),
+                                        None if n_rows is None else _one("n_rows", n_rows, dev), M, Hq, Hkv, hd,
+                                        page_size, n_pages, _flat16("kpool", kpool, size, dev),
+                                        _flat16("vpool", vpool, size, dev), _on(dev, stream)))
 
 
 # ------------------------------------------------------ a tree of drafts
 
+def _nodes(n_nodes, B, dev):
+    return None if n_nodes is None else _flat("n_nodes", n_nodes, B, dev)
+
+
 def xv_tree_positions(parent, n_nodes, ctx_len, pos, stream=None):
-    B, N = parent.shape
-    _check(lib().xv_tree_positions(_ptr(parent), _ptr(n_nodes), _ptr(ctx_len), N, B, _ptr(pos), _stream(stream)))
+    (B, N), dev = parent.shape, parent.get_device()
+    _check(lib().xv_tree_positions(_flat("parent", parent, B * N, dev), _nodes(n_nodes, B, dev),
+                                   _flat("ctx_len", ctx_len, B, dev), N, B, _flat("pos", pos, B * N, dev),
+                                   _on(dev, stream)))
 
 
 def xv_attn_tree_workspace_size(B, N, Hq, hd, max_ctx) -> int:
@@ -472,34 +576,56 @@ def xv_attn_tree_workspace_size(B, N, Hq, hd, max_ctx) -> int:
 def xv_attn_tree(q, kc, vc, ctx_len, kv_src, parent, n_nodes, N, B, Hq, Hkv, hd, Lmax, max_ctx, scale, out, ws,
                  gate=None, stream=None):
     """q, kv_src, out and gate are row tensors [B*N, ...] (row strides taken from them)."""
-    _check(lib().xv_attn_tree(_ptr(q), _row_stride(q), _ptr(kc), _ptr(vc), _ptr(ctx_len), _ptr(kv_src),
-                              _row_stride(kv_src), _ptr(parent), _ptr(n_nodes), N, B, Hq, Hkv, hd, Lmax, max_ctx, scale,
-                              _ptr(gate), 0 if gate is None else _row_stride(gate), _ptr(out), _row_stride(out), _ptr(ws),
-                              ws.nbytes, _stream(stream)))
+    M, w, size, dev = B * N, Hq * hd, B * Hkv * Lmax * hd, q.get_device()
+    a, sa = _rows("q", q, M, w, dev)
+    c, sc = _rows("kv_src", kv_src, M, 2 * Hkv * hd, dev)
+    g, sg = (None, 0) if gate is None else _rows("gate", gate, M, w, dev)
+    o, so = _rows("out", out, M, w, dev)
+    _check(lib().xv_attn_tree(a, sa, _flat16("kc", kc, size, dev), _flat16("vc", vc, size, dev),
+                              _flat("ctx_len", ctx_len, B, dev), c, sc, _flat("parent", parent, M, dev),
+                              _nodes(n_nodes, B, dev), N, B, Hq, Hkv, hd, Lmax, max_ctx, scale, g, sg, o, so, _ws(ws, dev),
+                              ws.nbytes, _on(dev, stream)))
 
 
 def xv_attn_tree_paged(q, kpool, vpool, pages: KvPages, ctx_len, kv_src, parent, n_nodes, N, B, Hq, Hkv, hd, max_ctx,
                        scale, out, ws, gate=None, stream=None):
-    _check(lib().xv_attn_tree_paged(_ptr(q), _row_stride(q), _ptr(kpool), _ptr(vpool), ctypes.byref(pages), _ptr(ctx_len),
-                                    _ptr(kv_src), _row_stride(kv_src), _ptr(parent), _ptr(n_nodes), N, B, Hq, Hkv, hd,
-                                    max_ctx, scale, _ptr(gate), 0 if gate is None else _row_stride(gate), _ptr(out),
-                                    _row_stride(out), _ptr(ws), ws.nbytes, _stream(stream)))
+    M, w, size, dev = B * N, Hq * hd, pages.n_pages * Hkv * pages.page_size * hd, q.get_device()
+    _pages_of(pages, B, dev)
+    a, sa = _rows("q", q, M, w, dev)
+    c, sc = _rows("kv_src", kv_src, M, 2 * Hkv * hd, dev)
+    g, sg = (None, 0) if gate is None else _rows("gate", gate, M, w, dev)
+    o, so = _rows("out", out, M, w, dev)
+    _check(lib().xv_attn_tree_paged(a, sa, _flat16("kpool", kpool, size, dev), _flat16("vpool", vpool, size, dev),
+                                    ctypes.byref(pages), _flat("ctx_len", ctx_len, B, dev), c, sc,
+                                    _flat("parent", parent, M, dev), _nodes(n_nodes, B, dev), N, B, Hq, Hkv, hd, max_ctx,
+                                    scale, g, sg, o, so, _ws(ws, dev), ws.nbytes, _on(dev, stream)))
 
 
 def xv_tree_accept(tokens, parent, n_nodes, argmax, path, n_keep, next_token, stream=None):
-    B, N = parent.shape
-    _check(lib().xv_tree_accept(_ptr(tokens), _ptr(parent), _ptr(n_nodes), _ptr(argmax), N, B, _ptr(path), _ptr(n_keep),
-                                _ptr(next_token), _stream(stream)))
+    (B, N), dev = parent.shape, parent.get_device()
+    _check(lib().xv_tree_accept(_flat("tokens", tokens, B * N, dev), _flat("parent", parent, B * N, dev),
+                                _nodes(n_nodes, B, dev), _flat("argmax", argmax, B * N, dev), N, B,
+                                _flat("path", path, B * N, dev), _flat("n_keep", n_keep, B, dev),
+                                _flat("next_token", next_token, B, dev), _on(dev, stream)))
 
 
 def xv_kv_append_path(kv_src, path, n_keep, ctx_len, N, B, Hkv, hd, Lmax, kc, vc, stream=None):
-    _check(lib().xv_kv_append_path(_ptr(kv_src), _row_stride(kv_src), _ptr(path), _ptr(n_keep), _ptr(ctx_len), N, B, Hkv,
-                                   hd, Lmax, _ptr(kc), _ptr(vc), _stream(stream)))
+    size, dev = B * Hkv * Lmax * hd, kv_src.get_device()
+    a, sa = _rows("kv_src", kv_src, B * N, 2 * Hkv * hd, dev)
+    _check(lib().xv_kv_append_path(a, sa, _flat("path", path, B * N, dev),
+                                   _flat("n_keep", n_keep, B, dev), _flat("ctx_len", ctx_len, B, dev), N, B, Hkv, hd,
+                                   Lmax, _flat16("kc", kc, size, dev), _flat16("vc", vc, size, dev), _on(dev, stream)))
 
 
 def xv_kv_append_path_paged(kv_src, path, n_keep, ctx_len, N, B, Hkv, hd, pages: KvPages, kpool, vpool, stream=None):
-    _check(lib().xv_kv_append_path_paged(_ptr(kv_src), _row_stride(kv_src), _ptr(path), _ptr(n_keep), _ptr(ctx_len), N,
-                                         B, Hkv, hd, ctypes.byref(pages), _ptr(kpool), _ptr(vpool), _stream(stream)))
+    size, dev = pages.n_pages * Hkv * pages.page_size * hd, kv_src.get_device()
+    _pages_of(pages, B, dev)
+    a, sa = _rows("kv_src", kv_src, B * N, 2 * Hkv * hd, dev)
+    _check(lib().xv_kv_append_path_paged(a, sa,
+                                         _flat("path", path, B * N, dev), _flat("n_keep", n_keep, B, dev),
+                                         _flat("ctx_len", ctx_len, B, dev), N, B, Hkv, hd, ctypes.byref(pages),
+                                         _flat16("kpool", kpool, size, dev), _flat16("vpool", vpool, size, dev),
+                                         _on(dev, stream)))
 
 
 # ------------------------------------------------------------------ block
