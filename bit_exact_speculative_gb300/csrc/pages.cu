@@ -14,7 +14,8 @@
 // table row past its request's held pages, a finished request's row not at all; new counters that take the
 // old ones' place are written by the CTA that is the last to have read those, as an atomic with acquire and
 // release tells (in place 3.5 us for 8 requests without rows and 4.0 for 500, apart 2.9 and 3.5).
-// More requests: a first kernel (one CTA) leaves the sums in the workspace for the second.
+// More requests: a first kernel (one CTA) leaves the sums in the workspace for the second; 1025 requests with a
+// row each 7.8 us, 8000 21, 65535 149, where the one CTA's 64 turns of sums are nearly all of it.
 // All of it is latency, a chain of dependent reads: 8 requests 4.8 us as two kernels and 3.6 as one, 500
 // requests with 14,371 rows 6.8 and 4.5, 1024 requests with 71,545 rows 7.6 and 7.4.
 #include "xv_internal.h"
@@ -192,6 +193,17 @@ __device__ __forceinline__ int thread_find(const int32_t* start, int B, int x) {
     }
     return lo;
 }
+// The same from request b on (start[b] <= x), in steps that double: rows of a warp mostly belong to the same
+// request or the next, but any number of requests without rows may lie between two of them (1024 requests,
+// rows in the first and the last: 40.5 us by single steps, 4.8 so; 65535: 3900 and 151).
+__device__ __forceinline__ int thread_find_on(const int32_t* start, int B, int b, int x) {
+    int hi = b + 1;
+    for (int step = 1; hi < B && start[hi] <= x; step *= 2) {
+        b = hi;
+        hi += step;
+    }
+    return b + thread_find(start + b, min(hi, B) - b, x);
+}
 
 // Page j of request b after this call, -1 where it has none.
 __device__ __forceinline__ int page_of(const PagesArgs& A, const PagesSums& P, int b, int j) {
@@ -229,10 +241,9 @@ __device__ __forceinline__ void move_pages(const PagesArgs& A, const PagesSums& 
 
 // One warp: position and slot of rows t0 .. t0 + 31.
 __device__ __forceinline__ void write_rows(const PagesArgs& A, const PagesSums& P, int t0, int total) {
-    int b = warp_find(P.start, A.B, t0);
-    const int t = t0 + (threadIdx.x & 31);
+    const int first = warp_find(P.start, A.B, t0), t = t0 + (threadIdx.x & 31);
     if (t < total) {
-        while (b + 1 < A.B && P.start[b + 1] <= t) ++b;
+        const int b = thread_find_on(P.start, A.B, first, t);
         const int p = A.ctx_len[b] + t - P.start[b], j = p / A.page;
         int pg = page_of(A, P, b, j);
         if (pg < -1 || pg >= A.n_pages || (pg < 0 && P.pop_ok)) {

@@ -66,3 +66,70 @@ def test_page_updates_in_place_equal_those_apart(xv, B):
         states.append(seen)
     assert all(torch.equal(a, b) for a, b in zip(*states))
     assert xv.xv_device_check() == 0
+
+
+def gpu_us(run, reps=20):
+    """Least time of a call among its like in a graph, in us."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        for _ in range(reps):
+            run()
+    best = float("inf")
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1000 / reps)
+    return best
+
+
+@pytest.mark.parametrize("B", [1, 2, 31, 33, 1024, 1025, 65535])
+@pytest.mark.parametrize("where", ["ends", "every 97th", "last"])
+def test_rows_find_their_request_past_idle_ones(xv, B, where):
+    """Few requests with new rows among many without: positions and slots, and no more time than a row
+    for every request takes (a walk from request to request took 6 times that for 1024 requests)."""
+    page, counts = 64, torch.zeros(B, dtype=torch.int32)
+    if where == "ends":
+        counts[0], counts[-1] = 21, 43
+    elif where == "last":
+        counts[-1] = 5
+    else:
+        counts[::97] = 1 + torch.arange(len(counts[::97]), dtype=torch.int32) % 3
+    idle = torch.arange(B) % 2 == 1      # idle, or finished without a page
+    ctx = (torch.arange(B, dtype=torch.int32) * 37) % 120
+    table = torch.full((B, 4), -1, dtype=torch.int32)
+    held = (ctx + page - 1) // page
+    first = torch.cumsum(held, 0) - held
+    for j in range(2):
+        table[held > j, j] = (first + j)[held > j].int()
+    done = idle & (counts == 0) & (held == 0)
+    n_pages = int(held.sum()) + 2 * B + 8
+    used, total = int(held.sum()), int(counts.sum())
+
+    def state(new, rows):
+        d = dict(pages=xv.kv_pages(table.cuda(), page, n_pages), held=held.int().cuda(), ctx_len=ctx.cuda(), n_new=new.cuda(),
+                 n_free=torch.tensor([n_pages - used], dtype=torch.int32).cuda(), row_start=torch.zeros(B + 1, dtype=torch.int32).cuda(),
+                 free_pages=torch.arange(used, used + n_pages, dtype=torch.int32).clamp_max(n_pages - 1).cuda(),
+                 pos=torch.full((rows,), -7, dtype=torch.int32).cuda(), slots=torch.full((rows,), -7, dtype=torch.int64).cuda(),
+                 ws=xv.workspace(xv.xv_kv_pages_workspace_size(B)))
+        return dict(d, n_free_out=torch.zeros_like(d["n_free"]), held_out=torch.zeros_like(d["held"]))
+
+    s = state(torch.where(done, torch.tensor(-1, dtype=torch.int32), counts), total + 3)
+    xv.xv_kv_pages_update(**s)
+    seq = torch.repeat_interleave(torch.arange(B), counts.long())
+    start = torch.cumsum(counts, 0) - counts
+    want = ctx[seq].long() + torch.arange(total) - start[seq]
+    after = s["pages"]._table.cpu().long()
+    assert s["pos"].tolist() == want.tolist() + [-7] * 3
+    assert s["slots"].tolist() == (after[seq, want // page] * page + want % page).tolist() + [-7] * 3
+    assert xv.xv_device_check() == 0
+    dense = state(torch.ones(B, dtype=torch.int32), B)
+    few, all_of_them = (gpu_us(lambda x=x: xv.xv_kv_pages_update(**x)) for x in (s, dense))
+    assert few <= 1.5 * all_of_them + 2, f"{few:.1f} us for {total} rows, {all_of_them:.1f} us for {B}"
