@@ -3,8 +3,8 @@
 // Every row (node, q head) attends to the cache's ctx positions and to its own path, and is computed
 // by the operations of a decode row at its position (attn.cu): splits at fixed absolute positions,
 // tiles of 64 positions, an fp32 online softmax over the tiles in order with the sum l taken position
-// by position, P rounded to bf16, P V accumulated 16 positions (one MMA K step) at a time, the splits
-// combined in split order.  A tree changes nothing of that below position 16 * (ctx / 16): those
+// by position, P rounded to bf16 (the tensor core takes it in V's type), P V accumulated 16 positions (one
+// MMA K step) at a time, the splits combined in split order.  A tree changes nothing of that below position 16 * (ctx / 16): those
 // positions are the same for every row.  Above, rows disagree about what stands at a position:
 //   - scores: Q K^T against all nodes at once (one 64-column tile, each score its own dot product); a
 //     row masks the nodes off its path.  Nodes are numbered after their parents, so a row's path in
@@ -627,10 +627,12 @@ __device__ __noinline__ void tree_add_bad(const TreeArgs& A, const TreeBad& F) {
 // gate 26.3 and 17.6).
 constexpr int DIRECT_MAX = 6144;
 __host__ __device__ inline bool tree_direct(int rows, int hd) { return rows * hd <= DIRECT_MAX; }
-// A value of the output: acc / L, with the gate's product where there is one.
-__device__ __forceinline__ uint16_t tree_out(float acc, float L, const uint16_t* gate) {
+// A value of the output: acc / L, with the gate's product where there is one.  At hd 64 and 256 the quotient
+// is rounded to bf16 before that product, as the decode rows round it; they take no hd 128, so there the
+// product is rounded alone.
+__device__ __forceinline__ uint16_t tree_out(float acc, float L, const uint16_t* gate, int hd) {
     float y = __fdiv_rn(acc, L);
-    if (gate) y = __fmul_rn(bf16_to_f32(f32_to_bf16(y)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(*gate)))));
+    if (gate) y = __fmul_rn(hd == 128 ? y : bf16_to_f32(f32_to_bf16(y)), __frcp_rn(__fadd_rn(1.f, expf(-bf16_to_f32(*gate)))));
     return f32_to_bf16(y);
 }
 
@@ -1386,7 +1388,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             const float a[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                A.out[br * A.out_stride + c + k] = tree_out(__fadd_rn(0.f, __fmul_rn(w, a[k])), L, A.gate ? A.gate + br * A.gate_stride + c + k : nullptr);
+                A.out[br * A.out_stride + c + k] = tree_out(__fadd_rn(0.f, __fmul_rn(w, a[k])), L, A.gate ? A.gate + br * A.gate_stride + c + k : nullptr, HD);
         }
     }
 }
@@ -1454,7 +1456,7 @@ __global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const _
     const long long c = static_cast<long long>(h) * hd + col;
     uint16_t* out = A.out + br * A.out_stride + c;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = tree_out(a[e], L, A.gate ? A.gate + br * A.gate_stride + c + e : nullptr);
+    for (int e = 0; e < 4; ++e) out[e] = tree_out(a[e], L, A.gate ? A.gate + br * A.gate_stride + c + e : nullptr, hd);
 }
 
 inline size_t r256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

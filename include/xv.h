@@ -491,7 +491,10 @@ xv_status xv_tree_positions(const int32_t* parent, const int32_t* n_nodes, const
  * column Hkv*hd, row stride src_stride), not from the cache; only a kept path
  * enters it (xv_kv_append_path).  A row has the bits of an xv_attn_decode_rows
  * row at its position over a cache that holds its path (hd 64 and 256), whatever
- * the other nodes hold, non-finite values included.
+ * the other nodes hold, non-finite values included.  Roundings to bf16: the
+ * weights exp(s - max) before their product with V (their sum takes them
+ * unrounded), the output, and, as in the decode rows, a gated output before its
+ * product with the gate too (not at hd 128, which they do not take).
  *   q [B*N, Hq*hd], out [B*N, Hq*hd], optional gate as in xv_attn_decode_rows;
  *   kc, vc [B, Hkv, Lmax, hd] (or pools, _paged); hd in {64, 128, 256}, Hq a
  *   multiple of Hkv, at most 128 q heads per kv head; 0 <= max_ctx <= Lmax

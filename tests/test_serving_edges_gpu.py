@@ -133,3 +133,37 @@ def test_rows_find_their_request_past_idle_ones(xv, B, where):
     dense = state(torch.ones(B, dtype=torch.int32), B)
     few, all_of_them = (gpu_us(lambda x=x: xv.xv_kv_pages_update(**x)) for x in (s, dense))
     assert few <= 1.5 * all_of_them + 2, f"{few:.1f} us for {total} rows, {all_of_them:.1f} us for {B}"
+
+
+@pytest.mark.parametrize("ctx", [3, 700])      # one split, finished in place; two and the combine
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_a_gated_output_is_rounded_once_where_no_decode_row_rounds_twice(xv, hd, ctx):
+    """Queries of zero and values of whole numbers make everything up to the quotient exact but for one
+    fp32 rounding, so a gated output o z is off by half a bf16 step and 2^-20 of it (the quotient's, the
+    product's and the logistic's fp32 roundings, 16 of them at most). At hd 64 and 256 a gated output has
+    the bits of the decode rows, which round o before the product: another 2^-8 of it."""
+    Hq, Hkv, N = 4, 2, 6
+    g = torch.Generator().manual_seed(hd + ctx)
+    proj = torch.randn((N, (2 * Hq + 2 * Hkv) * hd), generator=g).bfloat16()
+    proj[:, : Hq * hd] = 0
+    proj[:, (2 * Hq + Hkv) * hd:] = torch.randint(1, 200, (N, Hkv * hd), generator=g).bfloat16()
+    kc, vc = torch.randn((1, Hkv, ctx, hd), generator=g).bfloat16(), torch.randint(1, 200, (1, Hkv, ctx, hd), generator=g).bfloat16()
+    par = [-1, 0, 1, 1, 0, 3]
+    X, out = proj.cuda(), torch.zeros((N, Hq * hd), dtype=torch.bfloat16, device="cuda")
+    xv.xv_attn_tree(X, kc.cuda(), vc.cuda(), torch.tensor([ctx], dtype=torch.int32).cuda(), X[:, 2 * Hq * hd:],
+                    torch.tensor([par], dtype=torch.int32).cuda(), None, N, 1, Hq, Hkv, hd, ctx, ctx, 0.125, out,
+                    xv.workspace(xv.xv_attn_tree_workspace_size(1, N, Hq, hd, ctx)), gate=X[:, Hq * hd: 2 * Hq * hd])
+    v = proj[:, (2 * Hq + Hkv) * hd:].double().reshape(N, Hkv, hd)
+    z = torch.sigmoid(proj[:, Hq * hd: 2 * Hq * hd].double()).reshape(N, Hq, hd)
+    for i in range(N):
+        path, a = [], i
+        while a >= 0:
+            path.append(a)
+            a = par[a]
+        o = (vc[0].double().sum(1) + v[path].sum(0)) / (ctx + len(path))
+        want = o.repeat_interleave(Hq // Hkv, 0) * z[i]
+        half = 2.0 ** (torch.floor(torch.log2(want)) - 8)
+        tol = half + 2.0 ** -20 * want + (0 if hd == 128 else 2.0 ** -8 * want)
+        err = (out[i].double().cpu().reshape(Hq, hd) - want).abs()
+        assert (err <= tol).all(), f"node {i}: {int((err > tol).sum())} of {err.numel()} off, worst {float((err / tol).max()):.2f} of the bound"
+    assert xv.xv_device_check() == 0
