@@ -1461,6 +1461,9 @@ __global__ void __launch_bounds__(COMB_THREADS) attn_tree_combine_kernel(const _
 
 inline size_t r256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+constexpr int TREE_MAX_CTX = 1 << 30;   // positions are ints, and a tree stands past the last one
+constexpr long long TREE_MAX_ROWS = 1ll << 30;
+
 size_t tree_workspace(int B, int N, int Hq, int hd, int max_ctx) {
     const size_t rows = static_cast<size_t>(B) * N * Hq * attn_split_count(max_ctx + N);
     return r256(rows * hd * sizeof(float)) + r256(rows * sizeof(float2)) + r256(4ull * B * N);
@@ -1538,8 +1541,9 @@ xv_status tree_checks(const TreeArgs& a, int hd, int Lmax, const void* ws, size_
     if (hd != 64 && hd != 128 && hd != 256) return fail(XV_ERR_UNSUPPORTED, "attn_tree: hd must be 64, 128 or 256 (got %d)", hd);
     if (a.Hq / a.Hkv > 128) return fail(XV_ERR_UNSUPPORTED, "attn_tree: more than 128 q heads per kv head");
     if (a.max_ctx < 0 || a.max_ctx > Lmax) return fail(XV_ERR_ARG, "attn_tree: need 0 <= max_ctx <= Lmax");
+    if (a.max_ctx > TREE_MAX_CTX) return fail(XV_ERR_UNSUPPORTED, "attn_tree: max_ctx exceeds 2^30 positions");
     if (a.B > 65535 || a.Hkv > 65535) return fail(XV_ERR_UNSUPPORTED, "attn_tree: B and Hkv must be below 65536");
-    if (static_cast<long long>(a.B) * a.N * a.Hq > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: more than 2^30 rows");
+    if (static_cast<long long>(a.B) * a.N * a.Hq > TREE_MAX_ROWS) return fail(XV_ERR_UNSUPPORTED, "attn_tree: more than 2^30 rows");
     if (static_cast<long long>(a.kv.n_pages) * a.Hkv >= (1ll << 31)) return fail(XV_ERR_UNSUPPORTED, "attn_tree: cache too large");
     const long long w = static_cast<long long>(a.Hq) * hd, kw = 2ll * a.Hkv * hd;
     if (a.q_stride < w || a.out_stride < w || a.src_stride < kw) return fail(XV_ERR_ARG, "attn_tree: a row stride is below its row");
@@ -1560,7 +1564,8 @@ using namespace xv;
 extern "C" {
 
 size_t xv_attn_tree_workspace_size(int B, int N, int Hq, int hd, int max_ctx) {
-    if (B < 1 || N < 1 || N > XV_KMAX || Hq < 1 || hd < 1 || max_ctx < 0) return 0;
+    if (B < 1 || B > 65535 || N < 1 || N > XV_KMAX || Hq < 1 || (hd != 64 && hd != 128 && hd != 256)) return 0;
+    if (max_ctx < 0 || max_ctx > TREE_MAX_CTX || static_cast<long long>(B) * N * Hq > TREE_MAX_ROWS) return 0;
     return tree_workspace(B, N, Hq, hd, max_ctx);
 }
 

@@ -498,7 +498,7 @@ xv_status xv_tree_positions(const int32_t* parent, const int32_t* n_nodes, const
  *   q [B*N, Hq*hd], out [B*N, Hq*hd], optional gate as in xv_attn_decode_rows;
  *   kc, vc [B, Hkv, Lmax, hd] (or pools, _paged); hd in {64, 128, 256}, Hq a
  *   multiple of Hkv, at most 128 q heads per kv head; 0 <= max_ctx <= Lmax
- *   (page_size * max_pages) bounds every ctx_len[b].
+ *   (page_size * max_pages) and 2^30 bounds every ctx_len[b]; B*N*Hq at most 2^30.
  * Workspace: xv_attn_tree_workspace_size(B, N, Hq, hd, max_ctx) bytes, 16-byte
  * aligned (0 for sizes outside what the call takes).  A sequence whose
  * ctx_len[b] falls outside [0, max_ctx] is skipped and recorded (4), a page

@@ -144,3 +144,25 @@ def test_rows_may_be_strided_and_have_more_dimensions(xv):
             xv.xv_qk_norm_rope(**dict(args, q=q, q_out=q))
     with pytest.raises(ValueError, match="^q:"):      # heads apart
         xv.xv_qk_norm_rope(**dict(args, q=torch.zeros((M, Hq, 2 * hd), dtype=torch.bfloat16)[..., :hd]))
+
+
+def test_attn_tree_sizes_past_what_the_kernels_index(xv):
+    """Positions are 32-bit ints in the kernels, and max_ctx + N is one on the way: past 2^30 positions the
+    call is refused, whatever the workspace is said to hold, and no workspace is sized."""
+    import ctypes
+    P, L = ctypes.c_void_p(0x10000), xv.lib()
+
+    def call(Lmax, max_ctx):
+        return L.xv_attn_tree(P, 1024, P, P, P, P, 1024, P, None, 16, 2, 4, 2, 256, Lmax, max_ctx, 0.0625, None, 0, P, 1024, P,
+                              1 << 50, None)
+
+    top = 2 ** 31 - 1
+    for Lmax, max_ctx in ((top, top), (top, top - 16), (top, top - 15), (top, (1 << 30) + 1), ((1 << 30) + 1, (1 << 30) + 1)):
+        assert call(Lmax, max_ctx) == xv.XV_ERR_UNSUPPORTED, (Lmax, max_ctx)
+        assert b"2^30" in L.xv_last_error()
+        assert xv.xv_attn_tree_workspace_size(2, 16, 4, 256, max_ctx) == 0
+    size = xv.xv_attn_tree_workspace_size
+    assert size(2, 16, 4, 256, 1 << 30) > 0 and size(65535, 64, 4, 64, 0) > 0 and size(1, 1, 1, 128, 0) > 0
+    for bad in ((2, 16, 4, 96, 500), (2, 16, 4, 512, 500), (65536, 16, 4, 256, 500), (2, 16, 0, 256, 500), (2, 16, 4, 256, -1),
+                (65535, 64, 512, 256, 500)):      # the last: more than 2^30 rows
+        assert size(*bad) == 0, bad
