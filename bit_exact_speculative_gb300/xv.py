@@ -510,9 +510,15 @@ def xv_kv_pages_update(pages: KvPages, free_pages, n_free, held, ctx_len, n_new,
 
 def rope_freqs(rot: int, base: float = 10000.0, scale: float = 1.0, device="cuda") -> torch.Tensor:
     """The frequencies base^(-2i/rot) / scale, i < rot/2, as the library takes them: turns per
-    position in 64-bit binary fractions (int64 holding the uint64 bits)."""
-    import math
-    f = [round(base ** (-2.0 * i / rot) / scale / (2.0 * math.pi) * 2.0 ** 64) % 2 ** 64 for i in range(rot // 2)]
+    position in 64-bit binary fractions (int64 holding the uint64 bits), the nearest to each."""
+    from decimal import Context, Decimal, localcontext
+    f = []
+    with localcontext(Context(prec=40)):   # a double's 53 bits would be 2^-24 of a turn off at position 2^31
+        turns = 1 / (Decimal("6.283185307179586476925286766559005768394") * Decimal(scale))
+        step = Decimal(base) ** (Decimal(-2) / max(rot, 1))
+        for _ in range(rot // 2):
+            f.append(int((turns * 2 ** 64).to_integral_value()) % 2 ** 64)
+            turns *= step
     return torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in f], dtype=torch.int64, device=device)
 
 

@@ -166,3 +166,21 @@ def test_attn_tree_sizes_past_what_the_kernels_index(xv):
     for bad in ((2, 16, 4, 96, 500), (2, 16, 4, 512, 500), (65536, 16, 4, 256, 500), (2, 16, 0, 256, 500), (2, 16, 4, 256, -1),
                 (65535, 64, 512, 256, 500)):      # the last: more than 2^30 rows
         assert size(*bad) == 0, bad
+
+
+@pytest.mark.parametrize("rot,base,scale", [(64, 1e4, 1.0), (128, 1e7, 1.0), (16, 500000.0, 8.0), (256, 1e6, 0.3), (64, 10000, 4), (2, 1e4, 1.0)])
+def test_rope_freqs_are_the_nearest_fractions(xv, rot, base, scale):
+    """Every entry is the binary fraction of 64 bits nearest to its turns, so the angle at position 2^31 is
+    within 2^-33 of a turn; a double's 53 bits leave 2^-24, which an fp32 sine shows."""
+    from decimal import Context, Decimal, localcontext
+    from fractions import Fraction
+
+    with localcontext(Context(prec=60)):
+        def arctan_inverse(n):      # sum of (-1)^k / ((2 k + 1) n^(2 k + 1))
+            return sum((-1) ** k / (Decimal(2 * k + 1) * Decimal(n) ** (2 * k + 1)) for k in range(60))
+        pi = 16 * arctan_inverse(5) - 4 * arctan_inverse(239)
+        want = [(Decimal(-2 * i) / rot * Decimal(base).ln()).exp() / (2 * pi * Decimal(scale)) for i in range(rot // 2)]
+    got = xv.rope_freqs(rot, base, scale, device="cpu")
+    assert got.dtype == torch.int64 and got.shape == (rot // 2,)
+    for x, w in zip(got.tolist(), want):
+        assert abs(Fraction(x % 2 ** 64, 2 ** 64) - Fraction(w)) <= Fraction(500001, 1000000) / 2 ** 64
