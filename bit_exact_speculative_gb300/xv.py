@@ -187,7 +187,14 @@ def _check(code: int):
 
 # A call's host time is a few microseconds, of the order of a short kernel's: pointers and streams go
 # to ctypes as plain ints (the signatures make them void*), and the current stream is asked for as its
-# handle (a torch.cuda.Stream object costs ~3 us).
+# handle (a torch.cuda.Stream object costs ~3 us; it is asked where this torch has no such function).
+
+def _stream_by_object(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_by_object)
+
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
@@ -195,7 +202,7 @@ def _ptr(t):
 
 def _stream(stream=None):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -260,7 +267,7 @@ def _on(dev, stream=None):
     if cur != dev:
         raise ValueError("tensors in the current device's memory needed, got " + ("host memory" if dev < 0 else f"cuda:{dev}"))
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _raw_stream(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream: one of cuda:{dev} needed, got one of {stream.device}")
     return stream.cuda_stream

@@ -184,3 +184,18 @@ def test_rope_freqs_are_the_nearest_fractions(xv, rot, base, scale):
     assert got.dtype == torch.int64 and got.shape == (rot // 2,)
     for x, w in zip(got.tolist(), want):
         assert abs(Fraction(x % 2 ** 64, 2 ** 64) - Fraction(w)) <= Fraction(500001, 1000000) / 2 ** 64
+
+
+def test_the_current_stream_is_found_without_torchs_private_name(xv, monkeypatch):
+    """The raw handle comes from a private function of torch where there is one, else from the public
+    stream object: the same handle."""
+    import importlib.util
+    import types
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=700 + dev))
+    spec = importlib.util.spec_from_file_location("xv_without_private_names", xv.__file__)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m._stream() == 703 and m._on(3) == 703
