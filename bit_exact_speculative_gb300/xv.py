@@ -194,6 +194,8 @@ def _stream_by_object(device: int) -> int:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_by_object)
+# once a CUDA tensor exists: torch.cuda.current_device() without its check that CUDA is initialised (0.1 us against 0.23)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _ptr(t):
@@ -263,8 +265,7 @@ def _ws(t, dev):
 
 
 def _on(dev, stream=None):
-    cur = torch.cuda.current_device() if dev >= 0 else None
-    if cur != dev:
+    if dev < 0 or dev != _current_device():
         raise ValueError("tensors in the current device's memory needed, got " + ("host memory" if dev < 0 else f"cuda:{dev}"))
     if stream is None:
         return _raw_stream(dev)

@@ -187,12 +187,13 @@ def test_rope_freqs_are_the_nearest_fractions(xv, rot, base, scale):
 
 
 def test_the_current_stream_is_found_without_torchs_private_name(xv, monkeypatch):
-    """The raw handle comes from a private function of torch where there is one, else from the public
-    stream object: the same handle."""
+    """The raw handle and the device come from private functions of torch where there are such, else from
+    the public ones: the same."""
     import importlib.util
     import types
 
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=700 + dev))
     spec = importlib.util.spec_from_file_location("xv_without_private_names", xv.__file__)
