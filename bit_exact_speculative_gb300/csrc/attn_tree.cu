@@ -20,13 +20,14 @@
 // Work items (split, row tile, kv head, sequence); a row tile is up to 128 rows: as many whole nodes,
 // Hq/Hkv rows each, as fit, spread evenly over the tiles.  Per item, as in attn.cu: K and V tiles by
 // TMA into rings, Q by TMA into the A operand, S = Q K^T and O += P V in tensor memory, softmax one
-// thread per row.  The full 128 rows of the MMA are used: at 64 nodes x 6 q heads per kv head an SM
-// does 128 x 64 scores per K tile, so wide trees over long contexts are bound by the tensor core and
-// the softmax, small ones by the K/V stream, short contexts by latency.
+// thread per row.  An SM does 128 x 64 scores per K tile whatever rows hold nodes (63 nodes x 6 q heads
+// per kv head: three tiles of 126 rows; 64 nodes: four of 96), so wide trees over long contexts are bound
+// by the tensor core and the softmax, small ones by the K/V stream, batches of short contexts by their
+// trees' tails, which do not overlap in a CTA, single short contexts by latency.
 //
 // Measured (24 q / 4 kv heads of 256 unless said): 8 nodes at 131072 positions 101 us, 5.3 TB/s of K and V;
-// 64 nodes there 273 us, 755 TFLOP/s; 32 x 13 nodes at 4000 to 8000, 32 / 8 heads of 128, 178 us, 4.0 TB/s;
-// 16 nodes at 2183 16.7 us; 8 nodes at 128, 2 / 1 heads of 64, 6.5 us.
+// 64 nodes there 272 us, 757 TFLOP/s; 32 x 13 nodes at 4000 to 8000, 32 / 8 heads of 128, 178 us, 4.0 TB/s, and
+// at 1000 to 2000 93 us, 2.2 TB/s; 16 nodes at 2183 16.6 us; 8 nodes at 128, 2 / 1 heads of 64, 6.4 us.
 #include <cmath>
 
 #include "xv_internal.h"
@@ -246,12 +247,12 @@ struct TreeInfo {
     int nb0, nb1;              // blocks of the tail tile, of the tile after it
 };
 
-// Fills the info of an item (one warp, nodes lane and lane + 32).
 // Parent of node i as the tree has it (-1 past the last); the load, apart from its use.
 __device__ __forceinline__ int tree_parent(const TreeArgs& A, const TreeItem& I, int i) {
     return i < I.n ? __ldg(A.parent + static_cast<long long>(I.b) * A.N + i) : -1;
 }
 
+// Fills the info of an item (one warp, nodes lane and lane + 32, whose parents are par0 and par1).
 __device__ __noinline__ void tree_info(TreeInfo* S, const TreeArgs& A, const TreeItem I, int lane, int par0, int par1) {
     constexpr unsigned ALL = 0xffffffffu;
     int8_t* jump = reinterpret_cast<int8_t*>(S->list);   // list is filled last

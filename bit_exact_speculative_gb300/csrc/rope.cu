@@ -9,13 +9,13 @@
 // modulo 2^64 is the angle modulo one turn to 2^-64 * p of a turn, for any 32-bit p.  An fp32
 // angle p * f_i would be off by p * 2^-24 radians (0.008 at 131072 positions, 0.03 at 500000).
 //
-// What bounds it: every value is read once and written once.  8192 rows of 40 + 8 heads of 128: 43.8 us
+// What bounds it: every value is read once and written once.  8192 rows of 40 + 8 heads of 128: 43.7 us
 // for 201 MB, 4.6 TB/s, 0.69 of the measured copy rate; more or fewer resident CTAs change nothing, the
-// ~110 instructions a lane needs per 8 values share the issue slots with the loads.  A verify step's 8
-// rows: 2.0 us, one load-to-store latency.  A head takes hd/8 lanes of 16 bytes each, its sum of
-// squares a fixed shuffle tree inside them, so a head's bits depend on that head, its weight and its
-// position alone.  fp32 pairs go two to an instruction; cos and sin are formed once per row and read
-// as rows of floats (as (cos, sin) pairs, the lanes' reads met in the same banks 16 deep).
+// ~110 instructions a lane needs per 8 values (V's too, whose result is dropped) share the issue slots with
+// the loads.  A verify step's 8 rows: 2.0 us, one load-to-store latency.  A head takes hd/8 lanes of 16
+// bytes each, its sum of squares a fixed shuffle tree inside them, so a head's bits depend on that head, its
+// weight and its position alone.  fp32 pairs go two to an instruction; cos and sin are formed once per row and
+// read as rows of floats (as (cos, sin) pairs, the lanes' reads met in the same banks 16 deep).
 #include "xv_internal.h"
 #include "xv_ptx.cuh"
 

@@ -475,7 +475,8 @@ xv_status xv_qk_norm_rope_append(const uint16_t* q, long long q_stride, uint16_t
  * xv_attn_decode_rows it does not include the rows' own tokens): a node at
  * depth d (steps to its root) stands at position ctx_len[b] + d.  A parent that
  * is not an earlier node is recorded (32) and read as -1, n_nodes outside
- * [0, N] recorded (8) and clamped.
+ * [0, N] recorded (8) and clamped.  These calls serve attention layers; the GDN
+ * calls step chains and have no tree form.
  * Errors of all calls below: XV_ERR_ARG (null pointer, sizes < 1, row strides
  * below their rows), XV_ERR_UNSUPPORTED (N above XV_KMAX, B above 65535,
  * unaligned rows or caches), XV_ERR_CUDA. */
