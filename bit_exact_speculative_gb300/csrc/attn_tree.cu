@@ -4,8 +4,9 @@
 // by the operations of a decode row at its position (attn.cu): splits at fixed absolute positions,
 // tiles of 64 positions, an fp32 online softmax over the tiles in order with the sum l taken position
 // by position, P rounded to bf16 (the tensor core takes it in V's type), P V accumulated 16 positions (one
-// MMA K step) at a time, the splits combined in split order.  A tree changes nothing of that below position 16 * (ctx / 16): those
-// positions are the same for every row.  Above, rows disagree about what stands at a position:
+// MMA K step) at a time, the splits combined in split order.  A tree changes nothing of that below
+// position 16 * (ctx / 16): those positions are the same for every row.  Above, rows disagree about what
+// stands at a position:
 //   - scores: Q K^T against all nodes at once (one 64-column tile, each score its own dot product); a
 //     row masks the nodes off its path.  Nodes are numbered after their parents, so a row's path in
 //     node order is in position order, and adding the masked zeros leaves its sum's bits alone;

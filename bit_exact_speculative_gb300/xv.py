@@ -1,4 +1,4 @@
-"""Python binding of libxv.so: argument marshalling only.
+"""Python binding of libxv.so: argument marshalling, and checks of the tensors.
 
 Each function has the name of the C entry point it calls (include/xv.h) and
 takes torch CUDA tensors (any 2-byte dtype for bf16 data, int32, float32);

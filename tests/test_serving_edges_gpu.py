@@ -1,4 +1,5 @@
-"""Calls at the edges of what the serving operators take: tensors in host memory among the device's."""
+"""Calls at the edges of what the serving operators take: tensors in host memory among the device's, counters in
+place, batches of mostly idle requests, the roundings of a gated output."""
 import pytest
 import torch
 
