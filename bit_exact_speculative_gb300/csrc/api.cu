@@ -66,7 +66,8 @@ struct Trace {
 const char* const KIND_NAMES[K_COUNT] = {"gemm_small_m", "gdn", "attn_split", "attn_combine", "kv_append", "embed",
                                          "rmsnorm", "swiglu", "gdn_gates", "argmax", "accept", "commit", "zero",
                                          "conv", "gated_norm", "gemm_combine", "tile_weights", "qk_norm_rope",
-                                         "kv_pages", "tree_positions", "tree_accept", "kv_append_path", "attn_tree"};
+                                         "kv_pages", "tree_positions", "tree_accept", "kv_append_path", "attn_tree",
+                                         "kv_append_q8", "attn_q8", "logprobs"};
 }  // namespace
 
 void trace_pre(cudaStream_t s) {

@@ -16,7 +16,8 @@ xv_status cuda_check(cudaError_t e, const char* what);
 // Kernel kinds of the launch trace.
 enum Kind : int { K_GEMM = 0, K_GDN, K_ATTN_SPLIT, K_ATTN_COMBINE, K_KV_APPEND, K_EMBED, K_RMSNORM, K_SWIGLU,
                   K_GATES, K_ARGMAX, K_ACCEPT, K_COMMIT, K_ZERO, K_CONV, K_GNORM, K_GEMM_COMBINE, K_TILE, K_ROPE,
-                  K_PAGES, K_TREE_POS, K_TREE_ACCEPT, K_KV_APPEND_PATH, K_ATTN_TREE, K_COUNT };
+                  K_PAGES, K_TREE_POS, K_TREE_ACCEPT, K_KV_APPEND_PATH, K_ATTN_TREE, K_KV_APPEND_Q8, K_ATTN_Q8,
+                  K_LOGPROBS, K_COUNT };
 // Call right before a launch on stream s (records the opening trace event when tracing).
 void trace_pre(cudaStream_t s);
 // Checks the launch just made on the calling thread, counts it and closes its trace record.
@@ -185,6 +186,11 @@ xv_status attn_launch(const uint16_t* q, long long q_stride, const uint16_t* kc,
 // Row (b, r) of src goes to position ctx_len[b] + pos_bias + r.
 xv_status kv_append_launch(const uint16_t* src, long long src_stride, const int32_t* ctx_len, int pos_bias, int R,
                            int B, int Hkv, int hd, const KvPages& kv, uint16_t* kc, uint16_t* vc, cudaStream_t s);
+
+// ---- 8-bit cache (kv_q8.cu)
+xv_status kv_q8_check(const xv_kv_q8* c, const char* what);
+// The sizes of a contiguous cache [B, Hkv, Lmax, hd].
+xv_status kv_contiguous_check(int B, int Hkv, int hd, int Lmax, const char* what);
 
 // ---- glue (glue.cu)
 xv_status rmsnorm_launch(const uint16_t* x, const uint16_t* w, int M, int H, float eps, uint16_t* y, cudaStream_t s);

@@ -33,6 +33,7 @@ XV_OK, XV_ERR_ARG, XV_ERR_UNSUPPORTED, XV_ERR_WORKSPACE, XV_ERR_CUDA, XV_ERR_DEV
 XV_GEMM_M_MAX = 64
 XV_KMAX = 64
 XV_CONV_MAX = 8
+XV_TOP_MAX = 32
 
 
 class XVError(RuntimeError):
@@ -80,6 +81,14 @@ class BlockState(ctypes.Structure):
 
 class QkRope(ctypes.Structure):
     _fields_ = [("q_norm", vp), ("k_norm", vp), ("eps", c_float), ("freq", vp), ("rot", c_int), ("interleaved", c_int)]
+
+
+class KvQ8(ctypes.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("k_scale", vp), ("v_scale", vp)]
+    _codes = 0   # entries of the smallest code tensor, where kv_q8 made the struct
+    _scales = 0
+    _dev = -1
+    _keep = None
 
 
 _lib = None
@@ -139,6 +148,19 @@ _SIGS = {
     "xv_kv_append_path": ([vp, long_arg, vp, vp, vp, int_arg, int_arg, int_arg, int_arg, int_arg, vp, vp, vp], c_int),
     "xv_kv_append_path_paged": ([vp, long_arg, vp, vp, vp, int_arg, int_arg, int_arg, int_arg, ctypes.POINTER(KvPages), vp, vp, vp],
                                 c_int),
+    "xv_kv_append_q8": ([vp, long_arg, vp, vp, int_arg, int_arg, int_arg, int_arg, int_arg, ctypes.POINTER(KvQ8), vp], c_int),
+    "xv_kv_append_q8_paged": ([vp, long_arg, vp, vp, int_arg, int_arg, int_arg, int_arg, ctypes.POINTER(KvPages),
+                               ctypes.POINTER(KvQ8), vp], c_int),
+    "xv_attn_q8_split_begin": ([c_int], c_int),
+    "xv_attn_q8_workspace_size": ([c_int, c_int, c_int, c_int, c_int, c_int, c_int], c_sz),
+    "xv_attn_decode_rows_q8": ([vp, long_arg, ctypes.POINTER(KvQ8), vp, vp, int_arg, int_arg, int_arg, int_arg, int_arg, int_arg,
+                                int_arg, int_arg, int_arg, c_float, vp, long_arg, vp, long_arg, vp, long_arg, vp], c_int),
+    "xv_attn_decode_rows_q8_paged": ([vp, long_arg, ctypes.POINTER(KvQ8), ctypes.POINTER(KvPages), vp, vp, int_arg, int_arg,
+                                      int_arg, int_arg, int_arg, int_arg, int_arg, int_arg, c_float, vp, long_arg, vp, long_arg,
+                                      vp, long_arg, vp], c_int),
+    "xv_logprobs_workspace_size": ([c_int, c_int, c_int], c_sz),
+    "xv_logprobs": ([vp, long_arg, vp, vp, int_arg, int_arg, vp, vp, int_arg, vp, vp, vp, long_arg, vp], c_int),
+    "xv_logprobs_bf16": ([vp, long_arg, vp, vp, int_arg, int_arg, vp, vp, int_arg, vp, vp, vp, long_arg, vp], c_int),
     "xv_gdn_in_dim": ([ctypes.POINTER(BlockConfig)], c_int),
     "xv_gdn_hist_stride": ([ctypes.POINTER(BlockConfig)], c_int),
     "xv_attn_in_dim": ([ctypes.POINTER(BlockConfig)], c_int),
@@ -640,6 +662,118 @@ def xv_kv_append_path_paged(kv_src, path, n_keep, ctx_len, N, B, Hkv, hd, pages:
                                          _flat("ctx_len", ctx_len, B, dev), N, B, Hkv, hd, ctypes.byref(pages),
                                          _flat16("kpool", kpool, size, dev), _flat16("vpool", vpool, size, dev),
                                          _on(dev, stream)))
+
+
+# ------------------------------------------------- a KV cache held in 8 bits
+
+def kv_q8(k, v, k_scale, v_scale) -> KvQ8:
+    """The description of an 8-bit cache: codes k and v (uint8 or float8_e4m3fn, [B, Hkv, Lmax, hd] or
+    pools [n_pages, Hkv, page_size, hd]) and their scales (float32, without the last dimension), all
+    contiguous on one device (kept referenced by the returned struct)."""
+    dev = k.get_device()
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(name, t, "contiguous uint8 or float8_e4m3fn codes")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(name, t, "contiguous float32 scales")
+    q = KvQ8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    q._keep, q._dev = (k, v, k_scale, v_scale), dev
+    q._codes, q._scales = min(k.numel(), v.numel()), min(k_scale.numel(), v_scale.numel())
+    return q
+
+
+def _q8(cache: KvQ8, heads, hd, dev):
+    """Checks that the cache holds `heads` heads of tokens."""
+    if cache._dev != dev or cache._codes < heads * hd or cache._scales < heads:
+        raise ValueError(f"cache: {heads} heads of {hd} codes with their scales on the call's device needed, got {cache._codes} "
+                         f"codes and {cache._scales} scales on cuda:{cache._dev}")
+    return ctypes.byref(cache)
+
+
+def _counts(n_rows, B, dev):
+    return None if n_rows is None else _flat("n_rows", n_rows, B, dev)
+
+
+def xv_kv_append_q8(kv_src, ctx_len, R, B, Hkv, hd, Lmax, cache: KvQ8, n_rows=None, stream=None):
+    """Quantises the rows kv_src [B*R, k | v] into the cache (the C header has the rule)."""
+    dev = kv_src.get_device()
+    a, sa = _rows("kv_src", kv_src, B * R, 2 * Hkv * hd, dev)
+    _check(lib().xv_kv_append_q8(a, sa, _flat("ctx_len", ctx_len, B, dev), _counts(n_rows, B, dev), R, B, Hkv, hd, Lmax,
+                                 _q8(cache, B * Hkv * Lmax, hd, dev), _on(dev, stream)))
+
+
+def xv_kv_append_q8_paged(kv_src, ctx_len, R, B, Hkv, hd, pages: KvPages, cache: KvQ8, n_rows=None, stream=None):
+    dev = kv_src.get_device()
+    _pages_of(pages, B, dev)
+    a, sa = _rows("kv_src", kv_src, B * R, 2 * Hkv * hd, dev)
+    _check(lib().xv_kv_append_q8_paged(a, sa, _flat("ctx_len", ctx_len, B, dev), _counts(n_rows, B, dev), R, B, Hkv, hd,
+                                       ctypes.byref(pages), _q8(cache, pages.n_pages * Hkv * pages.page_size, hd, dev),
+                                       _on(dev, stream)))
+
+
+def xv_attn_q8_split_begin(s: int) -> int:
+    """First position of split s of the 8-bit cache's attention (fixed absolute boundaries)."""
+    return int(lib().xv_attn_q8_split_begin(s))
+
+
+def xv_attn_q8_workspace_size(B, R, Hq, hd, max_ctx, window=0, sinks=0) -> int:
+    return int(lib().xv_attn_q8_workspace_size(B, R, Hq, hd, max_ctx, window, sinks))
+
+
+def xv_attn_decode_rows_q8(q, cache: KvQ8, ctx_len, R, B, Hq, Hkv, hd, Lmax, max_ctx, scale, out, ws, window=0, sinks=0,
+                           gate=None, n_rows=None, stream=None):
+    """q, out and gate are row tensors [B*R, ...] (row strides taken from them)."""
+    M, w, dev = B * R, Hq * hd, q.get_device()
+    a, sa = _rows("q", q, M, w, dev)
+    g, sg = (None, 0) if gate is None else _rows("gate", gate, M, w, dev)
+    o, so = _rows("out", out, M, w, dev)
+    _check(lib().xv_attn_decode_rows_q8(a, sa, _q8(cache, B * Hkv * Lmax, hd, dev), _flat("ctx_len", ctx_len, B, dev),
+                                        _counts(n_rows, B, dev), R, B, Hq, Hkv, hd, Lmax, max_ctx, window, sinks, scale, g, sg,
+                                        o, so, _ws(ws, dev), ws.nbytes, _on(dev, stream)))
+
+
+def xv_attn_decode_rows_q8_paged(q, cache: KvQ8, pages: KvPages, ctx_len, R, B, Hq, Hkv, hd, max_ctx, scale, out, ws, window=0,
+                                 sinks=0, gate=None, n_rows=None, stream=None):
+    M, w, dev = B * R, Hq * hd, q.get_device()
+    _pages_of(pages, B, dev)
+    a, sa = _rows("q", q, M, w, dev)
+    g, sg = (None, 0) if gate is None else _rows("gate", gate, M, w, dev)
+    o, so = _rows("out", out, M, w, dev)
+    _check(lib().xv_attn_decode_rows_q8_paged(a, sa, _q8(cache, pages.n_pages * Hkv * pages.page_size, hd, dev),
+                                              ctypes.byref(pages), _flat("ctx_len", ctx_len, B, dev), _counts(n_rows, B, dev), R,
+                                              B, Hq, Hkv, hd, max_ctx, window, sinks, scale, g, sg, o, so, _ws(ws, dev),
+                                              ws.nbytes, _on(dev, stream)))
+
+
+# ------------------------------------------------------- scores of logits
+
+def xv_logprobs_workspace_size(M: int, V: int, top: int = 0) -> int:
+    return int(lib().xv_logprobs_workspace_size(M, V, top))
+
+
+def xv_logprobs(logits, tokens, logprob, ws, entropy=None, top_ids=None, top_logprobs=None, n_rows=None, stream=None):
+    """Scores of logits [M, V] (float32 or bfloat16, rows contiguous): logprob [M] of tokens [M]
+    (int32, -1 for none), entropy [M] and the top alternatives top_ids (int32) and top_logprobs [M, n],
+    each where given."""
+    (M, V), (ld, one), dev = logits.shape, logits.stride(), logits.get_device()
+    f32 = logits.dtype is torch.float32
+    if not f32 and logits.dtype is not torch.bfloat16 or one != 1 and V > 1:
+        _refuse("logits", logits, "float32 or bfloat16 [M, V] with contiguous rows")
+    top = 0
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs: both or neither")
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            _refuse("top_ids", top_ids, f"[{M}, top] int32")
+        top = top_ids.shape[1]
+    f = torch.float32
+    fn = lib().xv_logprobs if f32 else lib().xv_logprobs_bf16
+    _check(fn(logits.data_ptr(), max(ld, V) if M == 1 else ld, _flat("tokens", tokens, M, dev), None if n_rows is None else _one("n_rows", n_rows, dev),
+              M, V, _flat("logprob", logprob, M, dev, f), None if entropy is None else _flat("entropy", entropy, M, dev, f), top,
+              None if top_ids is None else _flat("top_ids", top_ids, M * top, dev),
+              None if top_ids is None else _flat("top_logprobs", top_logprobs, M * top, dev, f), _ws(ws, dev), ws.nbytes,
+              _on(dev, stream)))
 
 
 # ------------------------------------------------------------------ block

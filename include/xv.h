@@ -59,6 +59,7 @@ typedef int xv_status;
 #define XV_GEMM_M_MAX 64        /* rows per small-M GEMM call */
 #define XV_KMAX 64              /* tokens per sequence per verify (or prefill chunk) call */
 #define XV_CONV_MAX 8           /* widest causal convolution of a complete GDN layer */
+#define XV_TOP_MAX 32           /* top alternatives per row of xv_logprobs */
 
 /* Version of this header's ABI (XV_ABI_VERSION). */
 int xv_abi_version(void);
@@ -537,6 +538,104 @@ xv_status xv_kv_append_path(const uint16_t* kv_src, long long src_stride, const 
 xv_status xv_kv_append_path_paged(const uint16_t* kv_src, long long src_stride, const int32_t* path, const int32_t* n_keep,
                                   const int32_t* ctx_len, int N, int B, int Hkv, int hd, const xv_kv_pages* pages,
                                   uint16_t* kpool, uint16_t* vpool, xv_stream s);
+
+/* ------------------------------------------- a KV cache held in 8 bits
+ * Half the bytes of the bf16 cache.  A head of a token is hd e4m3 codes and one
+ * fp32 scale, for K and for V; the value is code * scale.  Codes are
+ * [B, Hkv, Lmax, hd] or pools [n_pages, Hkv, page_size, hd], scales the same
+ * without the last dimension; all 16-byte aligned.  A scale of its own per token
+ * and head (rather than one per block of tokens) keeps a committed token's codes
+ * and bits whatever is written beside it, so a verify still gives the bits of
+ * decoding its tokens one at a time. */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+} xv_kv_q8;
+
+/* Quantises and writes the K and V rows of a step: row (b, r) of kv_src (k at
+ * column 0, v at column Hkv*hd, row stride src_stride) goes to position
+ * ctx_len[b] - 1 + r of sequence b, for r < n_rows[b] (device [B], 0..R; NULL: R
+ * everywhere).  Other rows are not read, and nothing else is written.  Per head:
+ *     den = min(max(max |x_i|, 448 2^-40), 448 2^60), scale = den / 448,
+ *     code_i = e4m3(448 x_i / den)   (nearest, ties to even).
+ * A head with a non-finite value gets the scale NaN and codes 0, and reads as
+ * NaN.  hd in {64, 128, 256}; any R >= 1.  Errors: XV_ERR_ARG (null pointer,
+ * sizes < 1, src_stride < 2*Hkv*hd), XV_ERR_UNSUPPORTED (hd, unaligned rows or
+ * cache, more than 2^30 positions per sequence, B*R*Hkv above 2^29), XV_ERR_CUDA.
+ * Recorded for xv_device_check, the row skipped: a position outside the cache
+ * (4), a page outside the pool (16); and n_rows outside [0, R] (8, clamped). */
+xv_status xv_kv_append_q8(const uint16_t* kv_src, long long src_stride, const int32_t* ctx_len, const int32_t* n_rows, int R,
+                          int B, int Hkv, int hd, int Lmax, const xv_kv_q8* cache, xv_stream s);
+xv_status xv_kv_append_q8_paged(const uint16_t* kv_src, long long src_stride, const int32_t* ctx_len, const int32_t* n_rows,
+                                int R, int B, int Hkv, int hd, const xv_kv_pages* pages, const xv_kv_q8* cache, xv_stream s);
+
+/* Decode-row attention over that cache: row (b, r), r < n_rows[b], sees
+ * len = ctx_len[b] + r positions (its own last), or with window > 0 those of them
+ * at or past len - window and the first `sinks`:
+ *     out = softmax(scale q . K^T) V, times sigmoid(gate) when a gate is given,
+ * rounded to bf16 once.  Rows from n_rows[b] on are neither read nor written.
+ * Arguments as in xv_attn_decode_rows; n_rows as above.  A row's bits depend on
+ * its own length, q and visible positions alone: positions are cut into splits
+ * at fixed boundaries (xv_attn_q8_split_begin), tiles of 64 inside them, and the
+ * splits joined in order, so a verify row has the bits of the decode row at its
+ * position.  Only tiles with a visible position are read, so pages wholly before
+ * every row's window (and past the sinks) may be given up.  q is held as two e4m3
+ * terms (to 2^-18 of its row's largest value or 2^-9 of the value, whichever is larger),
+ * weights in fp16 before their product with V, sums in fp32.  A row that sees a
+ * NaN scale, or whose q is not finite, is NaN; other rows are not touched.  V
+ * scales are taken to lie in [2^-40, 2^60] (clamped to it), codes not to be NaN.
+ *   hd in {64, 128, 256}; 1 <= R <= XV_KMAX; Hq % Hkv == 0; window >= 0 (0:
+ *   none), sinks >= 0 (without a window they change nothing);
+ *   ctx_len[b] >= 1 and ctx_len[b] + n_rows[b] - 1 <= max_ctx <= Lmax.
+ * Workspace: xv_attn_q8_workspace_size(...) bytes, 16-byte aligned (0 for sizes
+ * outside what the call takes).  Errors: XV_ERR_ARG (null pointer, sizes < 1, Hq
+ * not a multiple of Hkv, max_ctx outside [1, Lmax], row strides below Hq*hd,
+ * window or sinks < 0), XV_ERR_UNSUPPORTED (hd, R > XV_KMAX, B or Hkv above 65535,
+ * unaligned rows, cache or workspace, more than 2^30 work items),
+ * XV_ERR_WORKSPACE, XV_ERR_CUDA.  A sequence whose ctx_len[b] or last row's
+ * length is out of range is skipped and recorded (4), n_rows outside [0, R]
+ * recorded (8) and clamped, a page outside the pool recorded (16) and read as
+ * page 0. */
+int xv_attn_q8_split_begin(int s);   /* -1 for s < 0 */
+size_t xv_attn_q8_workspace_size(int B, int R, int Hq, int hd, int max_ctx, int window, int sinks);
+xv_status xv_attn_decode_rows_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, const int32_t* ctx_len,
+                                 const int32_t* n_rows, int R, int B, int Hq, int Hkv, int hd, int Lmax, int max_ctx,
+                                 int window, int sinks, float scale, const uint16_t* gate, long long gate_stride,
+                                 uint16_t* out, long long out_stride, void* ws, size_t ws_bytes, xv_stream s);
+xv_status xv_attn_decode_rows_q8_paged(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, const xv_kv_pages* pages,
+                                       const int32_t* ctx_len, const int32_t* n_rows, int R, int B, int Hq, int Hkv, int hd,
+                                       int max_ctx, int window, int sinks, float scale, const uint16_t* gate,
+                                       long long gate_stride, uint16_t* out, long long out_stride, void* ws, size_t ws_bytes,
+                                       xv_stream s);
+
+/* ------------------------------------------------- scores of logits
+ * For each of M rows of V logits (fp32, or bf16; rows ld elements apart, at any
+ * element's alignment):
+ *     logprob[m] = x[tokens[m]] - log(sum exp x)      (0 when tokens[m] is -1)
+ *     entropy[m] = -sum p log p                       (NULL: not wanted)
+ *     top_ids, top_logprobs [M, top]: the `top` largest logits (0..XV_TOP_MAX) in
+ *     falling order, the lowest index first among equals ([post] compares token
+ *     ids and log probabilities), a NaN below every number.
+ * Each row is a fixed order of fp32 operations on that row alone: the same bits
+ * in a call of any M, at any position.  A logit of -inf is a masked token (p = 0);
+ * a row of nothing else has logprobs -inf and entropy 0; one with a NaN or +inf
+ * has NaN logprobs and entropy.  n_rows: device count of rows to do (rows from
+ * *n_rows on are left as they were), or NULL for all M.  Workspace:
+ * xv_logprobs_workspace_size(M, V, top) bytes, 16-byte aligned, zero-filled once
+ * (0 for sizes outside what the call takes).  Errors: XV_ERR_ARG (null pointer,
+ * M or V < 1, ld < V, top outside [0, V]), XV_ERR_UNSUPPORTED (top above
+ * XV_TOP_MAX, V above 2^19, M * ceil(V / 8192) above 2^31, unaligned workspace),
+ * XV_ERR_WORKSPACE, XV_ERR_CUDA.  A token outside [-1, V) is recorded (2) and its
+ * logprob NaN. */
+size_t xv_logprobs_workspace_size(int M, int V, int top);
+xv_status xv_logprobs(const float* logits, long long ld, const int32_t* tokens, const int32_t* n_rows, int M, int V,
+                      float* logprob, float* entropy, int top, int32_t* top_ids, float* top_logprobs, void* ws,
+                      size_t ws_bytes, xv_stream s);
+xv_status xv_logprobs_bf16(const uint16_t* logits, long long ld, const int32_t* tokens, const int32_t* n_rows, int M, int V,
+                           float* logprob, float* entropy, int top, int32_t* top_ids, float* top_logprobs, void* ws,
+                           size_t ws_bytes, xv_stream s);
 
 /* ------------------------------------------------------------ the block
  * A stack of decoder layers (each: x + mixer(rmsnorm(x)), then
