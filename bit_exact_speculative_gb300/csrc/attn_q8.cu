@@ -22,8 +22,10 @@
 //   O += P V    in fp16: P needs more range than two e4m3 terms have (a weight 2^-17 of the largest
 //               would be 0, and a long context can hold half its weight in such), so V is widened
 //               (exactly) by warps of their own between its TMA stage and the tensor core's operand.
-//               P_SHIFT puts p at up to 2^14: fp16 keeps weights to 2^-26 of the reference at full
-//               precision.  P is written over S in tensor memory, where the MMA reads it.
+//               P_SHIFT puts p at up to 2^15: fp16 keeps weights to 2^-21 of the reference at full
+//               precision (and to 2^-31 at all), and the reference may stay up to RESCALE_SLACK below
+//               the row's largest t_j: with a slack of 2 every fifth tile of a row waited for the
+//               P V before it to rescale O.  P is written over S in tensor memory, where the MMA reads it.
 //
 // Kernel 1 (attn_q8_kernel): work items (slot, 64-row tile, kv head, sequence); a slot is a split,
 // or with a window one of the splits that the window and the sinks can touch.  One CTA per item up
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int T = 64;                  // positions per tile
 constexpr float NEG_INF = -INFINITY;
-constexpr float P_SHIFT = 12.f, RESCALE_SLACK = 2.f;
+constexpr float P_SHIFT = 7.f, RESCALE_SLACK = 8.f;
 
 // Split boundaries: Q8_SHORT positions each below Q8_SWITCH, Q8_LONG beyond.
 constexpr int Q8_SHORT = 256, Q8_SWITCH = 4096, Q8_LONG = 1024;
@@ -64,6 +66,7 @@ struct Shape {
     static constexpr int SK = HD == 128 ? 3 : 4, SV = 3, SW = 2;
     static constexpr int CONV = HD == 256 ? 4 : 2;            // widening warps
     static constexpr int WARPS = 8 + CONV, THREADS = 32 * WARPS;
+    static constexpr int Q_THREADS = 32 * (4 + CONV);
     static constexpr int PER_SM = HD == 256 ? 1 : 2;
     static constexpr int SC = 4;                              // slots of prepared scales
     static constexpr int RAW = 8;                             // tiles whose scales are on their way
@@ -74,7 +77,7 @@ struct Shape {
     static constexpr int V_OFF = K_OFF + SK * CODE;
     static constexpr int W_OFF = V_OFF + SV * CODE;
     static constexpr int BAR_OFF = W_OFF + SW * VWIDE;
-    static constexpr int N_BARS = 2 * (SK + SV + SW + SC) + 2 + 2 + 2 + 4;
+    static constexpr int N_BARS = 2 * (SK + SV + SW + SC) + 2 + 2 + 2 + 5;
     static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
     static constexpr uint32_t O_COL = 2 * T;
     static constexpr uint32_t TMEM_COLS = HD == 256 ? 512 : 256;
@@ -116,7 +119,8 @@ struct Item {
     __device__ __forceinline__ int pos(int i) const { return p_begin + (i < head ? i : i + skip) * T; }
 };
 
-__device__ __forceinline__ Item q8_item(const Q8Args& A, int it, int nrt) {
+// (Out of line: in every role's loop the warps' code outgrew the instruction caches.)
+__device__ __noinline__ Item q8_item(const Q8Args& A, int it, int nrt) {
     Item I;
     I.slot = it % A.nslot;
     int rest = it / A.nslot;
@@ -278,20 +282,62 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool li
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Two fp32 operations in one instruction: (a, b) *= (x, y); (u, v) = (u, v) (x, y) + (a, b); (a, b) += (x, y).
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float& u, float& v, float x, float y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(u), "+f"(v) : "f"(x), "f"(y), "f"(a), "f"(b));
+}
+// (u, v) += (x, y) (a, b)
+__device__ __forceinline__ void fma2_acc(float& u, float& v, float x, float y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
+        "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "+f"(u), "+f"(v) : "f"(x), "f"(y), "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+// Bounded wait: after one of the CTA's waits has given up, every later one returns at once.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t par, volatile int* aborted, unsigned* err) {
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (mbar_try_wait(bar, par)) return true;
+        if (*aborted) return false;
+        if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+            atomicOr(err, ERR_WAIT_TIMEOUT);
+            *aborted = 1;
+            return false;
+        }
+    }
+}
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// The tiles of a CTA's items in order.
+// The tiles of a CTA's items in order.  With PLACE a whole warp steps, and lane i looks up where tile i
+// of an item lies, so that a page table's latency is met once per item.
+template <bool PLACE>
 struct Tiles {
     Item I;
-    int it, i;   // item, and the next tile of it
+    int it, i;       // item, and the next tile of it
+    int z, row;      // lane i: head of the pools and row in it of tile i
+    __device__ __forceinline__ void look(const Q8Args& A) {
+        if (!PLACE) return;
+        const int lane = threadIdx.x & 31;
+        if (lane < I.ntiles) z = q8_page(A.kv, I.b, I.pos(lane), &row, A.err) * A.Hkv + I.g;
+    }
     __device__ __forceinline__ void start(const Q8Args& A, int first, int nrt) {
         it = first;
-        i = 0;
+        i = z = row = 0;
         I = q8_item(A, it, nrt);
+        look(A);
     }
     // steps to the next tile; false past the last
     __device__ __forceinline__ bool step(const Q8Args& A, int it1, int nrt) {
@@ -299,11 +345,17 @@ struct Tiles {
         i = 0;
         while (++it < it1) {
             I = q8_item(A, it, nrt);
-            if (I.live) return true;
+            if (I.live) {
+                look(A);
+                return true;
+            }
         }
         return false;
     }
+    __device__ __forceinline__ int head() const { return __shfl_sync(0xffffffffu, z, i); }
+    __device__ __forceinline__ int place() const { return __shfl_sync(0xffffffffu, row, i); }
 };
+static_assert(Q8_LONG <= 32 * T && Q8_SHORT <= 32 * T, "a lane per tile of an item");
 
 // Warps of a CTA and what they do per tile t (counted over the CTA's items):
 //   2, 3   TMA of the K and V codes into their rings
@@ -349,7 +401,7 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
     auto sbar = [&](int j) { return bx + 8u * j; };           // S of a tile is complete
     auto pready = [&](int j) { return bx + 8u * (2 + j); };   // its P is in tensor memory
     auto pfree = [&](int j) { return bx + 8u * (4 + j); };    // its P V is complete
-    const uint32_t done = bx + 8u * 6, ofree = bx + 8u * 7, qfull = bx + 8u * 8, mlready = bx + 8u * 9;
+    const uint32_t done = bx + 8u * 6, ofree = bx + 8u * 7, qfull = bx + 8u * 8, mlready = bx + 8u * 9, qfirst = bx + 8u * 10;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nrt = (A.R * A.G + 63) / 64;
@@ -383,6 +435,7 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
         mbar_init(ofree, 64);
         mbar_init(qfull, 64);
         mbar_init(mlready, 64);
+        mbar_init(qfirst, S::Q_THREADS);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -390,63 +443,57 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
         tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
     }
-    // all threads load the first item's Q; the softmax warps reload it when an item's differs
-    load_q<HD, S::THREADS>(smem + S::Q_OFF, q_fac[0], A, q8_item(A, first, nrt), tid);
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = tmem_slot, tO = tS + S::O_COL;
+    // the warps that wait for tiles anyway load the first item's Q; the softmax warps reload it when an
+    // item's differs
+    if (warp < 2 || warp == 4 || warp == 5 || warp >= 8) {
+        load_q<HD, S::Q_THREADS>(smem + S::Q_OFF, q_fac[0], A, q8_item(A, first, nrt), tid - (warp < 2 ? 0 : warp < 8 ? 64 : 128));
+        fence_proxy_async_smem();
+        mbar_arrive(qfirst);
+    }
 
-    // bounded waits; after the first that gives up, every later one returns at once
-    auto W = [&](uint32_t bar, uint32_t par) -> bool {
-        if (s_abort) return false;
-        if (!mbar_wait_sleep(bar, par, A.err)) {
-            s_abort = 1;
-            return false;
-        }
-        return true;
-    };
+    auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || wait_slow(bar, par, &s_abort, A.err); };
     // the same verdict for every lane of a warp
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
     auto same_q = [](const Item& x, int b, int g, int rb) { return x.b == b && x.g == g && x.row_base == rb; };
 
     if (warp == 2 || warp == 3) {
         // ---- TMA
-        if (lane == 0) {
-            const bool isK = warp == 2;
-            const int NS = isK ? SK : SV;
-            const CUtensorMap* map = isK ? &tmK : &tmV;
-            int t = 0;
-            Tiles x;
-            x.start(A, first, nrt);
-            do {
-                const int st = t % NS;
-                if (t >= NS && !W(isK ? emptyK(st) : emptyV(st), ((t / NS) & 1u) ^ 1u)) break;
+        const bool isK = warp == 2;
+        const int NS = isK ? SK : SV;
+        const CUtensorMap* map = isK ? &tmK : &tmV;
+        int t = 0;
+        Tiles<true> x;
+        x.start(A, first, nrt);
+        do {
+            const int st = t % NS, z = x.head(), row = x.place();
+            if (t >= NS && !WW(isK ? emptyK(st) : emptyV(st), ((t / NS) & 1u) ^ 1u)) break;
+            if (lane == 0) {
                 const uint32_t fb = isK ? fullK(st) : fullV(st), dst = isK ? sK(st) : sV(st);
                 mbar_arrive_expect_tx(fb, S::CODE);
-                int row;
-                const int z = q8_page(A.kv, x.I.b, x.I.pos(x.i), &row, A.err) * A.Hkv + x.I.g;
 #pragma unroll
                 for (int cb = 0; cb < S::KB; ++cb) tma_load_3d(dst + cb * S::KBLK, map, cb * S::KROW, row, z, fb);
-                ++t;
-            } while (x.step(A, it1, nrt));
-            // every issued copy lands before the CTA may leave
-            for (int j = t > NS ? t - NS : 0; j < t; ++j) mbar_wait(isK ? fullK(j % NS) : fullV(j % NS), (j / NS) & 1u, A.err);
-        }
+            }
+            ++t;
+        } while (x.step(A, it1, nrt));
+        // every issued copy lands before the CTA may leave
+        for (int j = t > NS ? t - NS : 0; j < t; ++j) mbar_wait(isK ? fullK(j % NS) : fullV(j % NS), (j / NS) & 1u, A.err);
     } else if (warp == 7) {
         // ---- scales: every lane copies those of its two positions RAW - 1 tiles ahead, and reads only
         // what it copied itself
-        Tiles x, y;   // copying, preparing
+        Tiles<true> x;   // copying
+        Tiles<false> y;  // preparing
         x.start(A, first, nrt);
-        y = x;
+        y.start(A, first, nrt);
         bool more = true;
         int tc = 0;
         auto copy = [&]() {
             if (more) {
                 const int p = x.I.pos(x.i);
-                int row;
-                const long long at = (static_cast<long long>(q8_page(A.kv, x.I.b, p, &row, A.err)) * A.Hkv + x.I.g) * A.kv.page + row;
+                const long long at = static_cast<long long>(x.head()) * A.kv.page + x.place();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int j = lane + 32 * h;
@@ -488,7 +535,7 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
         constexpr int CPR = HD / 64, PASSES = 8 * CPR / CONV;   // column groups of 64 dims; passes per warp
         const int r8 = lane & 7, c4 = lane >> 3;
         int t = 0;
-        Tiles x;
+        Tiles<false> x;
         x.start(A, first, nrt);
         do {
             const int sv = t % SV, sw = t % SW;
@@ -543,7 +590,7 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
                 return true;
             };
             int t = 0, jl = 0, nq = 0, qb = -1, qg = -1, qrb = -1;
-            bool ok = true, pre = false;   // pre: this item's first S went out with the last item
+            bool ok = W(qfirst, 0u), pre = false;   // pre: this item's first S went out with the last item
             for (int it = first; ok && it < it1; ++it) {
                 const Item I = q8_item(A, it, nrt);
                 if (!I.live) continue;
@@ -622,7 +669,8 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
         const int rho = tid;
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
         int t = 0, jl = 0, nq = 0, qb = -1, qg = -1, qrb = -1;
-        for (int it = first; it < it1; ++it) {
+        const bool q_in = WW(qfirst, 0u);
+        for (int it = first; q_in && it < it1; ++it) {
             const Item I = q8_item(A, it, nrt);
             if (!I.live) continue;
             if constexpr (MULTI) {
@@ -655,54 +703,66 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
                     if (lane == 0) mbar_arrive(emptyS(sc));
                     continue;
                 }
-                float s[T];
-#pragma unroll
-                for (int k = 0; k < T / 16; ++k) tmem_ld16(tS + lane_off + (tt & 1) * T + k * 16, s + k * 16);
-                tmem_ld_wait();
                 const int p0 = I.pos(i);
+                const bool whole = __all_sync(0xffffffffu, !mine || (p0 >= from && p0 + T <= len));
+                // t_j of 32 positions, twice: for their maximum, and again for p (registers for 64 and code
+                // unrolled over them cost more than the second read)
+                auto scores = [&](int j0, float* s) {
+                    tmem_ld16(tS + lane_off + (tt & 1) * T + j0, s);
+                    tmem_ld16(tS + lane_off + (tt & 1) * T + j0 + 16, s + 16);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < T; j += 4) {
-                    const float4 ks = *reinterpret_cast<const float4*>(&sc_ks[sc][j]);
-                    const float4 lv = *reinterpret_cast<const float4*>(&sc_lv[sc][j]);
-                    s[j] = __fmaf_rn(__fmul_rn(s[j], c), ks.x, lv.x);
-                    s[j + 1] = __fmaf_rn(__fmul_rn(s[j + 1], c), ks.y, lv.y);
-                    s[j + 2] = __fmaf_rn(__fmul_rn(s[j + 2], c), ks.z, lv.z);
-                    s[j + 3] = __fmaf_rn(__fmul_rn(s[j + 3], c), ks.w, lv.w);
-                }
-                if (!__all_sync(0xffffffffu, !mine || (p0 >= from && p0 + T <= len))) {
-#pragma unroll
-                    for (int j = 0; j < T; ++j) {
-                        const int p = p0 + j;
-                        if (!(p < len && (p >= from || p < upto))) s[j] = NEG_INF;
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 ks = *reinterpret_cast<const float4*>(&sc_ks[sc][j0 + j]);
+                        const float4 lv = *reinterpret_cast<const float4*>(&sc_lv[sc][j0 + j]);
+                        mul2(s[j], s[j + 1], c, c);
+                        mul2(s[j + 2], s[j + 3], c, c);
+                        fma2(s[j], s[j + 1], ks.x, ks.y, lv.x, lv.y);
+                        fma2(s[j + 2], s[j + 3], ks.z, ks.w, lv.z, lv.w);
                     }
-                }
-                float mx = NEG_INF;
+                    if (!whole) {
 #pragma unroll
-                for (int j = 0; j < T; ++j) mx = fmaxf(mx, s[j]);
+                        for (int j = 0; j < 32; ++j) {
+                            const int p = p0 + j0 + j;
+                            if (!(p < len && (p >= from || p < upto))) s[j] = NEG_INF;
+                        }
+                    }
+                };
+                float mx4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll 1
+                for (int j0 = 0; j0 < T; j0 += 32) {
+                    float s[32];
+                    scores(j0, s);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) mx4[(j / 2) & 3] = fmaxf(mx4[(j / 2) & 3], fmaxf(s[j], s[j + 1]));
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 const float mn = (m == NEG_INF || mx > __fadd_rn(m, RESCALE_SLACK)) ? mx : m;
                 const bool dead = mn == NEG_INF;
                 const float al = (dead || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn));
                 const float mo = dead ? 0.f : __fsub_rn(mn, P_SHIFT);
-                float ts0 = 0.f, ts1 = 0.f;
-                // P over S: nothing reads this S any more
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float pk[16];
+                float ts[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int j0 = 0; j0 < T; j0 += 32) {
+                    float s[32], pk[16];
+                    scores(j0, s);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 iv = *reinterpret_cast<const float4*>(&sc_iv[sc][32 * h + j]);
-                        const float a0 = ex2_approx(__fsub_rn(s[32 * h + j], mo)), a1 = ex2_approx(__fsub_rn(s[32 * h + j + 1], mo));
-                        const float a2 = ex2_approx(__fsub_rn(s[32 * h + j + 2], mo)), a3 = ex2_approx(__fsub_rn(s[32 * h + j + 3], mo));
-                        ts0 = __fmaf_rn(a0, iv.x, ts0);
-                        ts1 = __fmaf_rn(a1, iv.y, ts1);
-                        ts0 = __fmaf_rn(a2, iv.z, ts0);
-                        ts1 = __fmaf_rn(a3, iv.w, ts1);
-                        pk[j / 2] = __uint_as_float(pack_f16x2(a0, a1));
-                        pk[j / 2 + 1] = __uint_as_float(pack_f16x2(a2, a3));
+                        const float4 iv = *reinterpret_cast<const float4*>(&sc_iv[sc][j0 + j]);
+                        float* p = s + j;
+                        add2(p[0], p[1], -mo, -mo);
+                        add2(p[2], p[3], -mo, -mo);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
+                        fma2_acc(ts[0], ts[1], p[0], p[1], iv.x, iv.y);
+                        fma2_acc(ts[2], ts[3], p[2], p[3], iv.z, iv.w);
+                        pk[j / 2] = __uint_as_float(pack_f16x2(p[0], p[1]));
+                        pk[j / 2 + 1] = __uint_as_float(pack_f16x2(p[2], p[3]));
                     }
-                    tmem_st16(tS + lane_off + (tt & 1) * T + 16 * h, pk);
+                    // over S columns that have been read: P of position j lies in column j / 2
+                    tmem_st16(tS + lane_off + (tt & 1) * T + j0 / 2, pk);
                 }
-                l = __fmaf_rn(l, al, __fadd_rn(ts0, ts1));
+                l = __fmaf_rn(l, al, __fadd_rn(__fadd_rn(ts[0], ts[1]), __fadd_rn(ts[2], ts[3])));
                 m = mn;
                 // O is rescaled once P V of the tile before has completed
                 if (i >= 1 && __any_sync(0xffffffffu, mine && al != 1.f)) {
