@@ -10,27 +10,32 @@
 //
 // Exactness ("Follow-up to my earlier post on Qwen3.8-27B decode speed", r/LocalLLaMA post: verify
 // attention as decode rows): positions are cut into splits at fixed absolute boundaries and tiles of
-// 64; a row goes through its tiles in order, a tile without a position it sees leaves its m, l and O
+// 128; a row goes through its tiles in order, a tile without a position it sees leaves its m, l and O
 // as they were, and its splits are joined in a fixed order.  A row's bits depend on its own length,
 // q and what it sees, not on the rows and sequences beside it.
 //
-// The products run on tcgen05, accumulators in tensor memory:
-//   S = Q K^T   in e4m3, K straight from its TMA stage.  A bf16 q is the sum of two e4m3 values (the
-//               nearest, and the nearest to what is left): both go through the tensor core into one
-//               accumulator, at fp8's rate as dear as one bf16 product and without a pass that widens
-//               K.  A row is scaled by a power of two first, its largest value into [128, 256).
-//   O += P V    in fp16: P needs more range than two e4m3 terms have (a weight 2^-17 of the largest
-//               would be 0, and a long context can hold half its weight in such), so V is widened
-//               (exactly) by warps of their own between its TMA stage and the tensor core's operand.
-//               P_SHIFT puts p at up to 2^15: fp16 keeps weights to 2^-21 of the reference at full
-//               precision (and to 2^-31 at all), and the reference may stay up to RESCALE_SLACK below
-//               the row's largest t_j: with a slack of 2 every fifth tile of a row waited for the
-//               P V before it to rescale O.  P is written over S in tensor memory, where the MMA reads it.
+// The products run on tcgen05 in fp8, the cache's codes straight from their TMA stages as the
+// 128-row operand A, the few query rows as N:
+//   S^T = K Q^T    [128 positions x rows].  A bf16 q is the sum of two e4m3 values (the nearest, and
+//                  the nearest to what is left), side by side in N; their two results are added.  A row
+//                  is scaled by a power of two first, its largest value into [128, 256).
+//   O^T += V^T P^T [dims x rows].  P is rounded to fp16 and goes in as the exact sum of four e5m2
+//                  values: e5m2 is fp16's upper byte, so cutting the byte off three times leaves
+//                  nothing (11 bits of significand, 3 by 3).  What is left after two is scaled by
+//                  2^6, against e5m2's smallest value, and has an accumulator of its own.  P_SHIFT
+//                  puts p at up to 2^15: P keeps weights to 2^-21 of the reference at full precision
+//                  and to 2^-29 at all (a long context can hold half its weight in such), and the
+//                  reference may stay up to RESCALE_SLACK below the row's largest t_j.
+// With rows in M instead (a first form: 64 rows of 128 used, P in fp16, V widened to fp16 by warps of
+// their own) a thread had a row and went through a tile's positions one by one: 2300 to 3500 cycles a
+// tile of 64, where the codes of 128 take 2800 to arrive (hd 256).  Here a thread has a position, its
+// scales are two registers, a batch's rows of one token cost what they are, and V is never widened.
 //
-// Kernel 1 (attn_q8_kernel): work items (slot, 64-row tile, kv head, sequence); a slot is a split,
-// or with a window one of the splits that the window and the sinks can touch.  One CTA per item up
-// to two waves of them, else persistent CTAs that walk contiguous ranges.  Kernel 2
+// Kernel 1 (attn_q8_kernel): work items (slot, row tile, kv head, sequence); a slot is a split, or
+// with a window one of the splits that the window and the sinks can touch.  One CTA per item where
+// all fit at once, else persistent CTAs that walk contiguous ranges of equal cost.  Kernel 2
 // (attn_q8_combine_kernel): one CTA per (row, q head) joins the row's splits.
+#include <algorithm>
 #include <cmath>
 
 #include "xv_internal.h"
@@ -39,12 +44,15 @@
 namespace xv {
 namespace {
 
-constexpr int T = 64;                  // positions per tile
+constexpr int T = 128;                 // positions per tile, in two halves of 64 (a page is a multiple of 64)
 constexpr float NEG_INF = -INFINITY;
 constexpr float P_SHIFT = 7.f, RESCALE_SLACK = 8.f;
+constexpr float DEAD = -3e38f;         // the reference of a row that has seen nothing: t - DEAD passes any slack
+constexpr float LOW_SCALE = 64.f;      // P's last two terms
 
 // Split boundaries: Q8_SHORT positions each below Q8_SWITCH, Q8_LONG beyond.
 constexpr int Q8_SHORT = 256, Q8_SWITCH = 4096, Q8_LONG = 1024;
+static_assert(Q8_SHORT % T == 0 && Q8_LONG <= 16 * T && Q8_SHORT <= Q8_LONG, "a lane per half tile of an item");
 __host__ __device__ inline int q8_split_begin(int s) {
     constexpr int NS = Q8_SWITCH / Q8_SHORT;
     return s < NS ? s * Q8_SHORT : Q8_SWITCH + (s - NS) * Q8_LONG;
@@ -54,36 +62,39 @@ __host__ __device__ inline int q8_split_of(int p) {
     return p < Q8_SWITCH ? p / Q8_SHORT : Q8_SWITCH / Q8_SHORT + (p - Q8_SWITCH) / Q8_LONG;
 }
 
-template <int HD>
+// NR: rows of a row tile, padded (a multiple of 8, as 2 NR is an N of the MMAs).
+template <int HD, int NR>
 struct Shape {
     static constexpr int KROW = HD < 128 ? HD : 128;          // bytes of a code row in a swizzled block
-    static constexpr int KB = HD / KROW;                      // code blocks [64 positions][KROW] per tile
+    static constexpr int KB = HD / KROW;                      // code blocks [128 positions][KROW] per tile
     static constexpr int KBLK = T * KROW;
     static constexpr int CODE = T * HD;                       // one K or V tile of codes
-    static constexpr int VB = HD / 64;                        // fp16 blocks [64 positions][64 dims]
-    static constexpr int VBLK = T * 128;
-    static constexpr int VWIDE = VB * VBLK;                   // one fp16 V tile
-    static constexpr int SK = HD == 128 ? 3 : 4, SV = 3, SW = 2;
-    static constexpr int CONV = HD == 256 ? 4 : 2;            // widening warps
-    static constexpr int WARPS = 8 + CONV, THREADS = 32 * WARPS;
-    static constexpr int Q_THREADS = 32 * (4 + CONV);
-    static constexpr int PER_SM = HD == 256 ? 1 : 2;
-    static constexpr int SC = 4;                              // slots of prepared scales
-    static constexpr int RAW = 8;                             // tiles whose scales are on their way
-    // the MMA reads 128 rows of Q: rows 64..127 of a block are what follows it, and end in tensor
-    // memory lanes that nobody reads
-    static constexpr int Q_OFF = 0;                           // nearest terms, then what is left
-    static constexpr int K_OFF = Q_OFF + 2 * CODE;
+    static constexpr int MB = HD > 128 ? 2 : 1;               // 128-dim blocks of O^T (hd 64: lanes 64.. unused)
+    static constexpr int QBLK = 2 * NR * KROW;                // Q block: nearest terms, then what is left
+    static constexpr int Q = KB * QBLK;
+    static constexpr int PT = T * 2 * NR;                     // terms 1 and 3, or 2 and 4, of a tile's P
+    static constexpr int PB = NR <= 24 ? 2 : 1;               // P buffers
+    // two CTAs per SM where their registers and rings allow it
+    static constexpr int PER_SM = HD <= 128 && NR <= 16 ? 2 : 1;
+    static constexpr int RAW = 4;                             // tiles of scales
+    static constexpr int STATIC = 2 * RAW * T * 4 + 15 * NR * 4 + 64;
+    static constexpr int ROOM = (PER_SM == 2 ? 233472 / 2 - 1024 : 232448) - STATIC - 1024 - 512 - Q - PB * 2 * PT;
+    static constexpr int STAGES = ROOM / CODE;
+    static constexpr int SV = STAGES < 11 ? (STAGES + 1) / 2 : 6, SK = STAGES < 12 ? STAGES - SV : 6;
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = Q_OFF + Q;
     static constexpr int V_OFF = K_OFF + SK * CODE;
-    static constexpr int W_OFF = V_OFF + SV * CODE;
-    static constexpr int BAR_OFF = W_OFF + SW * VWIDE;
-    static constexpr int N_BARS = 2 * (SK + SV + SW + SC) + 2 + 2 + 2 + 5;
+    static constexpr int P_OFF = V_OFF + SV * CODE;
+    static constexpr int BAR_OFF = P_OFF + PB * 2 * PT;
+    static constexpr int N_BARS = 2 * (SK + SV + RAW) + 4 + PB + 5;
     static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
-    static constexpr uint32_t O_COL = 2 * T;
-    static constexpr uint32_t TMEM_COLS = HD == 256 ? 512 : 256;
-    static_assert(O_COL + HD <= TMEM_COLS, "");
-    static_assert(KBLK % 1024 == 0 && VBLK % 1024 == 0 && PER_SM * (SMEM + 9 * 1024 + 256) <= 228 * 1024, "");
+    static constexpr uint32_t O_COL = 4 * NR;                 // S twice, then O: MB blocks of [terms 1, 2 | terms 3, 4]
+    static constexpr int COLS = 4 * NR + MB * 2 * NR;
+    static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(NR % 8 == 0 && NR <= 64 && COLS <= 512 && PER_SM * TMEM_COLS <= 512, "");
+    static_assert(SK >= 2 && SV >= 2 && 8 * N_BARS <= 512 && QBLK % 1024 == 0, "");
 };
+constexpr int THREADS = 384;
 
 struct Q8Args {
     const uint16_t* q;
@@ -94,6 +105,7 @@ struct Q8Args {
     const int32_t* ctx_len;
     const int32_t* n_rows;
     int R, G, Hq, Hkv, B;
+    int tile_rows, nrt;  // rows of a row tile, row tiles
     int nslot, nsink;    // slots per row, of which the first nsink are the sinks' splits
     int max_len, window, sinks;
     int shift;           // the window, where the slots past the sinks' begin at it; 0: slots are splits
@@ -112,46 +124,146 @@ __device__ __forceinline__ int q8_first(int L0, int shift, int nsink) {
     return shift && L0 > shift ? max(nsink, q8_split_of(L0 - shift)) : nsink;
 }
 
-struct Item {
-    int b, g, row_base, slot, L0, rows, maxlen, p_begin;
-    int ntiles, head, skip;   // live tiles: the split's first `head`, then from tile head + skip on
-    bool live, bad;
-    __device__ __forceinline__ int pos(int i) const { return p_begin + (i < head ? i : i + skip) * T; }
+// What a row tile of a sequence sees: positions below `end` for its last row; none of its rows those in
+// [sinks, lo).
+struct Sight {
+    int L0, rows, row_base, end, lo, sinks;   // rows <= 0: nothing to do
+    __device__ __forceinline__ void of(const Q8Args& A, int b, int rt) {
+        const int nr = q8_rows(A.n_rows, b, A.R);
+        L0 = __ldg(A.ctx_len + b);
+        row_base = rt * A.tile_rows;
+        rows = min(nr * A.G - row_base, A.tile_rows);
+        if (L0 < 1 || L0 > A.max_len - nr + 1) rows = 0;
+        end = lo = sinks = 0;
+        if (rows <= 0) return;
+        // what other rows see beside a row changes nothing of it
+        end = L0 + (row_base + rows - 1) / A.G;
+        const int minlen = L0 + row_base / A.G;
+        if (A.window && minlen > A.window) lo = minlen - A.window, sinks = A.sinks;
+    }
+    // whether a row sees any of the 64 positions at p
+    __device__ __forceinline__ bool half(int p) const { return p < end && (p + 64 > lo || p < sinks); }
+    // tiles of sinks before those of the windows
+    __device__ __forceinline__ int heads() const { return min(lo / T, (min(sinks, lo) + T - 1) / T); }
+    // cost of the splits before split s: two a tile, one a split
+    __device__ __forceinline__ int cost(int s) const {
+        const int last = q8_split_of(end - 1) + 1, h = heads(), n = s >= last ? (end + T - 1) / T : q8_split_begin(s) / T;
+        const int hs = h ? q8_split_of(h * T - 1) + 1 : 0, m = min(s, last);
+        return 2 * (min(n, h) + max(0, n - max(lo / T, h))) + min(m, hs) + max(0, m - max(q8_split_of(lo), hs));
+    }
 };
 
-// (Out of line: in every role's loop the warps' code outgrew the instruction caches.)
-__device__ __noinline__ Item q8_item(const Q8Args& A, int it, int nrt) {
-    Item I;
-    I.slot = it % A.nslot;
-    int rest = it / A.nslot;
-    I.row_base = (rest % nrt) * 64;
-    rest /= nrt;
-    I.g = rest % A.Hkv;
-    I.b = rest / A.Hkv;
-    const int nr = q8_rows(A.n_rows, I.b, A.R);
-    I.rows = nr * A.G;
-    I.L0 = __ldg(A.ctx_len + I.b);
-    I.bad = nr > 0 && (I.L0 < 1 || I.L0 > A.max_len - nr + 1);
-    I.live = !I.bad && I.row_base < I.rows;
-    I.ntiles = I.head = I.skip = I.maxlen = I.p_begin = 0;
-    if (!I.live) return I;
-    // the longest and the shortest length among the item's rows; what other rows see beside a row
-    // changes nothing of it
-    I.maxlen = I.L0 + (min(I.rows, I.row_base + 64) - 1) / A.G;
-    const int minlen = I.L0 + I.row_base / A.G;
-    const int split = I.slot < A.nsink ? I.slot : q8_first(I.L0, A.shift, A.nsink) + I.slot - A.nsink;
-    I.p_begin = q8_split_begin(split);
-    const int end = min(q8_split_begin(split + 1), I.maxlen);
-    const int nt = max(0, end - I.p_begin + T - 1) / T;
-    int lo = 0;   // first tile that a window reaches
-    if (A.window && minlen > A.window) {
-        lo = min(nt, max(0, minlen - A.window - I.p_begin) / T);
-        I.head = min(lo, max(0, A.sinks - I.p_begin + T - 1) / T);
+// Split of slot s, where the slots past the sinks' begin at split `first`.
+__device__ __forceinline__ int q8_slot_split(int s, int nsink, int first) { return s < nsink ? s : first + s - nsink; }
+
+// The work items of a CTA in order, those that see nothing left out.  Stepping divides by nothing but
+// powers of two: with the divisions of item -> (slot, row tile, head, sequence) in it, each warp's
+// step took 2000 cycles.
+struct Item {
+    int it, slot, rt, g, b, first;
+    Sight v;
+    int p_begin, ntiles, head, skip;   // live tiles: the split's first `head`, then from tile head + skip on
+    __device__ __forceinline__ int pos(int i) const { return p_begin + (i < head ? i : i + skip) * T; }
+    __device__ __forceinline__ void sight(const Q8Args& A) {
+        v.of(A, b, rt);
+        first = q8_first(v.L0, A.shift, A.nsink);
     }
-    I.skip = lo - I.head;
-    I.ntiles = nt - I.skip;
-    I.live = I.ntiles > 0;
-    return I;
+    __device__ __forceinline__ void place(const Q8Args& A) {
+        const int split = q8_slot_split(slot, A.nsink, first);
+        p_begin = q8_split_begin(split);
+        const int nt = (max(0, min(q8_split_begin(split + 1), v.end) - p_begin) + T - 1) / T;
+        const int low = min(nt, max(0, v.lo - p_begin) / T);   // first tile that a window reaches
+        head = min(low, (max(0, v.sinks - p_begin) + T - 1) / T);
+        skip = low - head;
+        ntiles = v.rows > 0 ? nt - skip : 0;
+    }
+    // the first live item of [i, it1); false if there is none
+    __device__ __forceinline__ bool open(const Q8Args& A, int i, int it1) {
+        it = i;
+        slot = i % A.nslot;
+        int rest = i / A.nslot;
+        rt = rest % A.nrt;
+        rest /= A.nrt;
+        g = rest % A.Hkv;
+        b = rest / A.Hkv;
+        if (it >= it1) return false;
+        sight(A);
+        place(A);
+        return ntiles > 0 || next(A, it1);
+    }
+    __device__ __forceinline__ bool next(const Q8Args& A, int it1) {
+        for (;;) {
+            ++it;
+            if (++slot == A.nslot || v.rows <= 0 || p_begin >= v.end) {   // splits past the end: none is live
+                it += A.nslot - slot;
+                slot = 0;
+                if (++rt == A.nrt) {
+                    rt = 0;
+                    if (++g == A.Hkv) g = 0, ++b;
+                }
+                if (it >= it1) return false;
+                sight(A);
+            }
+            if (it >= it1) return false;
+            place(A);
+            if (ntiles > 0) return true;
+        }
+    }
+    __device__ __forceinline__ bool same_q(const Item& o) const { return b == o.b && g == o.g && rt == o.rt; }
+};
+
+// The items of persistent CTA c of n: equal shares of the cost.  All of the CTA's threads.
+__device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it01) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per = (A.B + THREADS - 1) / THREADS;
+    auto whole = [&](int b, int* one, int* tiles) {   // cost of sequence b, of a row tile of a head of it, live row tiles
+        Sight v;
+        v.of(A, b, 0);
+        *one = v.rows > 0 ? v.cost(1 << 24) : 0;
+        *tiles = v.rows > 0 ? (q8_rows(A.n_rows, b, A.R) * A.G + A.tile_rows - 1) / A.tile_rows : 0;
+        return static_cast<long long>(*one) * *tiles * A.Hkv;
+    };
+    int one, tiles;
+    long long mine = 0;
+    for (int b = tid * per; b < min(A.B, (tid + 1) * per); ++b) mine += whole(b, &one, &tiles);
+    __shared__ long long warp_sum[THREADS / 32];
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    if (tid < 2) it01[tid] = A.nslot * A.nrt * A.Hkv * A.B;   // where no cost is left
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    // an item belongs to the CTA in whose share its cost begins
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        long long at = total * (c + e) / n - before;
+        if (at < 0 || at >= mine || mine == 0) continue;
+        int b = tid * per;
+        for (;; ++b) {
+            const long long x = whole(b, &one, &tiles);
+            if (at < x) break;
+            at -= x;
+        }
+        const int pair = static_cast<int>(at / one), off = static_cast<int>(at % one);   // (head, row tile), cost in it
+        Sight v;
+        v.of(A, b, 0);
+        const int first = q8_first(v.L0, A.shift, A.nsink);
+        int lo = 0, hi = A.nslot;   // the first slot whose cost begins at `off` or later
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (v.cost(q8_slot_split(mid, A.nsink, first)) >= off) hi = mid;
+            else lo = mid + 1;
+        }
+        it01[e] = ((b * A.Hkv + pair / tiles) * A.nrt + pair % tiles) * A.nslot + lo;
+    }
+    __syncthreads();
 }
 
 __device__ __forceinline__ int q8_page(const KvPages& kv, int b, int p, int* row, unsigned* err) {
@@ -190,22 +302,34 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
-// Live Q rows of an item -> tile row, as two e4m3 terms of q 2^e (the row's largest magnitude in
-// [128, 256)) in swizzled blocks, and fac[row] = 2^-e.  NT threads (whole warps) from t0.
-template <int HD, int NT>
+// Live Q rows of an item -> rows of N, as two e4m3 terms of q 2^e (the row's largest magnitude in
+// [128, 256)) in swizzled blocks, and fac[row] = sl2 2^-e; the rows behind them become 0.
+// NT threads (whole warps) from t0.
+template <int HD, int NR, int NT>
 __device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A, const Item& I, int t0) {
-    using S = Shape<HD>;
+    using S = Shape<HD, NR>;
     constexpr int LPH = HD / 8, RPP = NT / LPH, UN = 4;
-    const int n = min(64, I.rows - I.row_base), c = t0 % LPH;
-    for (int r0 = 0; r0 < n; r0 += RPP * UN) {
+    const int n = I.v.rows, c = t0 % LPH;
+#pragma unroll 1
+    for (int r0 = 0; r0 < NR; r0 += RPP * UN) {
         uint4 v[UN];
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
             const int row = r0 + k * RPP + t0 / LPH;
             v[k] = make_uint4(0, 0, 0, 0);
             if (row < n) {
-                const int r = (I.row_base + row) / A.G, h = I.g * A.G + (I.row_base + row) % A.G;
+                const int r = (I.v.row_base + row) / A.G, h = I.g * A.G + (I.v.row_base + row) % A.G;
                 v[k] = *reinterpret_cast<const uint4*>(A.q + (static_cast<long long>(I.b) * A.R + r) * A.q_stride +
                                                        static_cast<long long>(h) * HD + c * 8);
             }
@@ -219,7 +343,7 @@ __device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A,
             for (int i = 0; i < 4; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
 #pragma unroll
             for (int off = LPH / 2; off > 0; off >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, off));
-            if (row >= n) continue;
+            if (row >= NR) continue;
             const bool bad = big >= 0x7f80u;
             const int e = 134 - max(static_cast<int>(big >> 7), 8);   // 2^e: the exponent field to 134, e <= 126
             const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
@@ -235,10 +359,10 @@ __device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A,
             }
             const int byte = c * 8, blk = byte / S::KROW, chunk = (byte % S::KROW) >> 4;
             const int sw = S::KROW == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-            uint8_t* dst = sq + blk * S::KBLK + row * S::KROW + sw * 16 + (byte & 8);
+            uint8_t* dst = sq + blk * S::QBLK + row * S::KROW + sw * 16 + (byte & 8);
             *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + S::CODE) = make_uint2(lo[0], lo[1]);
-            if (c == 0) fac[row] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            *reinterpret_cast<uint2*>(dst + NR * S::KROW) = make_uint2(lo[0], lo[1]);
+            if (c == 0) fac[row] = __fmul_rn(A.sl2, __uint_as_float(static_cast<uint32_t>(127 - e) << 23));
         }
     }
 }
@@ -257,32 +381,77 @@ template <int ROW>
 __device__ __forceinline__ uint64_t kmajor_desc(uint32_t saddr) {
     return ROW == 128 ? sw128_kmajor_desc(saddr) : sw64_kmajor_desc(saddr);
 }
-// Instruction descriptor: fp32 accumulator; the input formats' fields are 0 for e4m3 (kind::f8f6f4)
-// and for fp16 (kind::f16) alike.
-constexpr uint32_t idesc0(int M, int N, bool b_mn_major = false) {
-    return (1u << 4) | (b_mn_major ? (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// MN-major operand of bytes in swizzled rows of ROW dims, 8 positions of them (8 ROW bytes) after another.
+// ROW = 128 fills M; with ROW = 64 the upper half of M repeats the lower (a stride of 0).
+template <int ROW>
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t saddr) {
+    uint64_t d = sw128_mnmajor_desc(saddr, 0, 8 * ROW);
+    if (ROW == 64) d ^= static_cast<uint64_t>(2 ^ 4) << 61;
+    return d;
 }
-// D (+)= A B^T, e4m3 operands in shared memory.
+// MN-major operand of bytes without swizzle: cores of 8 positions x 16 bytes of N, positions 128 bytes
+// a core, the next 16 of N `n_stride` bytes further.
+__device__ __forceinline__ uint64_t mnmajor_plain_desc(uint32_t saddr, uint32_t n_stride) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(128u >> 4) << 16;
+    d |= static_cast<uint64_t>(n_stride >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;
+}
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, A e4m3.
+constexpr uint32_t idesc_f8(int M, int N, bool b_e5m2, bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | (b_e5m2 ? (1u << 10) : 0u) | (a_mn_major ? (1u << 15) : 0u) | (b_mn_major ? (1u << 16) : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D (+)= A B^T, operands in shared memory.
 __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// D (+)= A B^T, fp16, A in tensor memory.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+// 32 lanes x 32 bits, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])),
+                 "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// Two fp32 operations in one instruction: (a, b) *= (x, y); (u, v) = (u, v) (x, y) + (a, b); (a, b) += (x, y).
+// Arrives on the mbarrier (one of its count) once the thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Barrier of the four softmax warps; with a flag, whether any thread's is set.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool f) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, 1, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+                 : "=r"(r)
+                 : "r"(f ? 1u : 0u)
+                 : "memory");
+    return r != 0;
+}
+// Largest value of a warp's lanes, NaN passed over.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two fp32 operations in one instruction: (a, b) *= (x, y); (u, v) = (u, v) (x, y) + (a, b);
+// (u, v) += (x, y) (a, b); (a, b) += (x, y).
 __device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
     asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
@@ -292,7 +461,6 @@ __device__ __forceinline__ void fma2(float& u, float& v, float x, float y, float
         "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(u), "+f"(v) : "f"(x), "f"(y), "f"(a), "f"(b));
 }
-// (u, v) += (x, y) (a, b)
 __device__ __forceinline__ void fma2_acc(float& u, float& v, float x, float y, float a, float b) {
     asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
         "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
@@ -301,6 +469,11 @@ __device__ __forceinline__ void fma2_acc(float& u, float& v, float x, float y, f
 __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
     asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 // Bounded wait: after one of the CTA's waits has given up, every later one returns at once.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t par, volatile int* aborted, unsigned* err) {
@@ -315,76 +488,82 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t par, volatile int*
         }
     }
 }
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// Sums of the warp's lanes, N values each: halves of the values go to halves of the lanes, so that it
+// takes about N shuffles.  The lane's sums end in v[0..] and are those of `first` on; the tree over the
+// lanes is the same for every N.
+template <int N, int OFF>
+__device__ __forceinline__ int warp_sums(float* v, int lane, int* first) {
+    if constexpr (OFF == 0) return N;
+    else if constexpr (N % 2 == 0) {
+        const bool up = lane & OFF;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float send = up ? v[i] : v[i + N / 2];
+            v[i] = __fadd_rn(up ? v[i + N / 2] : v[i], __shfl_xor_sync(0xffffffffu, send, OFF));
+        }
+        if (up) *first += N / 2;
+        return warp_sums<N / 2, OFF / 2>(v, lane, first);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], OFF));
+        return warp_sums<N, OFF / 2>(v, lane, first);
+    }
 }
 
-// The tiles of a CTA's items in order.  With PLACE a whole warp steps, and lane i looks up where tile i
-// of an item lies, so that a page table's latency is met once per item.
-template <bool PLACE>
+// The tiles of a CTA's items in order.  A whole warp steps, and lane 2 i + h looks up where half h of
+// tile i of an item lies, so that a page table's latency is met once per item.
 struct Tiles {
     Item I;
-    int it, i;       // item, and the next tile of it
-    int z, row;      // lane i: head of the pools and row in it of tile i
+    int i;           // the next tile of the item
+    int z, row;      // lane 2 i + h: head of the pools and row in it; z < 0 where no row sees the half
     __device__ __forceinline__ void look(const Q8Args& A) {
-        if (!PLACE) return;
-        const int lane = threadIdx.x & 31;
-        if (lane < I.ntiles) z = q8_page(A.kv, I.b, I.pos(lane), &row, A.err) * A.Hkv + I.g;
+        const int lane = threadIdx.x & 31, p = I.pos(lane >> 1) + 64 * (lane & 1);
+        z = -1, row = 0;
+        if (lane < 2 * I.ntiles && I.v.half(p)) z = q8_page(A.kv, I.b, p, &row, A.err) * A.Hkv + I.g;
     }
-    __device__ __forceinline__ void start(const Q8Args& A, int first, int nrt) {
-        it = first;
-        i = z = row = 0;
-        I = q8_item(A, it, nrt);
+    __device__ __forceinline__ void start(const Q8Args& A, const Item& first) {
+        I = first;
+        i = 0;
         look(A);
     }
     // steps to the next tile; false past the last
-    __device__ __forceinline__ bool step(const Q8Args& A, int it1, int nrt) {
+    __device__ __forceinline__ bool step(const Q8Args& A, int it1) {
         if (++i < I.ntiles) return true;
         i = 0;
-        while (++it < it1) {
-            I = q8_item(A, it, nrt);
-            if (I.live) {
-                look(A);
-                return true;
-            }
-        }
-        return false;
+        if (!I.next(A, it1)) return false;
+        look(A);
+        return true;
     }
-    __device__ __forceinline__ int head() const { return __shfl_sync(0xffffffffu, z, i); }
-    __device__ __forceinline__ int place() const { return __shfl_sync(0xffffffffu, row, i); }
+    __device__ __forceinline__ int head(int h) const { return __shfl_sync(0xffffffffu, z, 2 * i + h); }
+    __device__ __forceinline__ int place(int h) const { return __shfl_sync(0xffffffffu, row, 2 * i + h); }
 };
-static_assert(Q8_LONG <= 32 * T && Q8_SHORT <= 32 * T, "a lane per tile of an item");
 
 // Warps of a CTA and what they do per tile t (counted over the CTA's items):
-//   2, 3   TMA of the K and V codes into their rings
-//   7      the tile's scales: ks, log2(vs) and 1 / vs of its positions into a ring of prepared slots
-//   8..    widen the V codes to fp16 (positions past every row's length become 0)
-//   6      MMAs: S(t + 1) = Q K^T, then O += P(t) V; S(t) and P(t) share buffer t % 2: the S that
-//          overwrites a P is issued after the P V that reads it, and MMAs run in order
-//   0, 1   softmax, a thread per query row: S out of tensor memory, t_j, mask, reference (moved when
-//          the tile's largest t_j passes it by RESCALE_SLACK, and then O and l are rescaled), P back
-//   4, 5   an item's O, m and l to the workspace, while the next item's first tiles run
-template <int HD, bool MULTI>
-__global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
+//   0..3   softmax, a thread per position: S out of tensor memory, t_j, mask; the references stand
+//          unless some row's t_j passes its by RESCALE_SLACK (or the tile is an item's first): then
+//          the tile's maxima are found, and references, l and O moved; P to shared memory, l per thread
+//   4..7   an item's O, m and l to the workspace, while the next item's first tiles run
+//   8, 9   TMA of the K and V codes into their rings
+//   10     MMAs: S(t + 1) = K Q^T, then O += V^T P(t); the S that overwrites S(t - 1) is issued after
+//          the P V of that tile, whose P was made of it
+//   11     the positions' scales into a ring
+template <int HD, int NR>
+__global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
     attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args A) {
     griddep_launch();
-    using S = Shape<HD>;
-    constexpr int SK = S::SK, SV = S::SV, SW = S::SW, SC = S::SC, RAW = S::RAW, CONV = S::CONV;
+    using S = Shape<HD, NR>;
+    constexpr int SK = S::SK, SV = S::SV, RAW = S::RAW, PB = S::PB;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) float raw_k[RAW][T], raw_v[RAW][T];
+    __shared__ __align__(16) float q_fac[2][NR], mo_sm[NR], al_sm[NR], wmax[4][NR], l_sm[4][NR], m_sm[NR];
+    __shared__ long long at_sm[NR];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort;
-    __shared__ float2 ml_sm[64];                        // (m, l) of the item being written out
-    __shared__ float q_fac[2][64];                      // by the count of Q loads
-    __shared__ __align__(16) float sc_ks[SC][T], sc_lv[SC][T], sc_iv[SC][T];
-    __shared__ float raw_k[RAW][T], raw_v[RAW][T];
     const uint32_t rawb = smem_u32(smem_raw);
     const uint32_t base = (rawb + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - rawb);
     auto sK = [&](int st) { return base + S::K_OFF + st * S::CODE; };
     auto sV = [&](int st) { return base + S::V_OFF + st * S::CODE; };
-    auto sW = [&](int st) { return base + S::W_OFF + st * S::VWIDE; };
     const uint32_t bar0 = base + S::BAR_OFF;
     auto fullK = [&](int st) { return bar0 + 8u * st; };
     auto emptyK = [&](int st) { return bar0 + 8u * (SK + st); };
@@ -392,54 +571,50 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
     auto fullV = [&](int st) { return bar1 + 8u * st; };
     auto emptyV = [&](int st) { return bar1 + 8u * (SV + st); };
     const uint32_t bar2 = bar1 + 8u * 2 * SV;
-    auto fullW = [&](int st) { return bar2 + 8u * st; };
-    auto emptyW = [&](int st) { return bar2 + 8u * (SW + st); };
-    const uint32_t bar3 = bar2 + 8u * 2 * SW;
-    auto fullS = [&](int st) { return bar3 + 8u * st; };
-    auto emptyS = [&](int st) { return bar3 + 8u * (SC + st); };
-    const uint32_t bx = bar3 + 8u * 2 * SC;
-    auto sbar = [&](int j) { return bx + 8u * j; };           // S of a tile is complete
-    auto pready = [&](int j) { return bx + 8u * (2 + j); };   // its P is in tensor memory
-    auto pfree = [&](int j) { return bx + 8u * (4 + j); };    // its P V is complete
-    const uint32_t done = bx + 8u * 6, ofree = bx + 8u * 7, qfull = bx + 8u * 8, mlready = bx + 8u * 9, qfirst = bx + 8u * 10;
+    auto fullS = [&](int st) { return bar2 + 8u * st; };
+    auto emptyS = [&](int st) { return bar2 + 8u * (RAW + st); };
+    const uint32_t bx = bar2 + 8u * 2 * RAW;
+    auto sbar = [&](int j) { return bx + 8u * j; };            // S of a tile is complete
+    auto pready = [&](int j) { return bx + 8u * (2 + j); };    // its P is in shared memory, its S has been read
+    auto pfree = [&](int j) { return bx + 8u * (4 + j); };     // its P V is complete
+    const uint32_t by = bx + 8u * (4 + PB);
+    const uint32_t done = by, ofree = by + 8, qfull = by + 16, mlready = by + 24, qfirst = by + 32;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nrt = (A.R * A.G + 63) / 64;
-    const int n_items = A.nslot * nrt * A.Hkv * A.B;
+    const int n_items = A.nslot * A.nrt * A.Hkv * A.B;
     const int per_slot = n_items / A.nslot;
-    // one item per CTA: slots slowest, so that a row's last splits, often short, come last
-    const int it0 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x) * n_items / gridDim.x)
-                          : (static_cast<int>(blockIdx.x) % per_slot) * A.nslot + static_cast<int>(blockIdx.x) / per_slot;
-    const int it1 = MULTI ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * n_items / gridDim.x) : it0 + 1;
+    const bool multi = static_cast<int>(gridDim.x) < n_items;
     griddep_wait();
-    int first = it0;
-    while (first < it1 && !q8_item(A, first, nrt).live) ++first;
-    if (tid == 0)
-        for (int it = it0; it < it1; ++it) {
-            const Item I = q8_item(A, it, nrt);
-            if (I.slot || I.row_base || I.g) continue;
-            if (I.bad) atomicOr(A.err, ERR_BAD_LENGTH);
-            if (A.n_rows && (A.n_rows[I.b] < 0 || A.n_rows[I.b] > A.R)) atomicOr(A.err, ERR_BAD_COUNT);
-        }
-    if (first >= it1) return;   // nothing live here: no barrier or tensor memory was set up
+    for (int b = blockIdx.x + gridDim.x * tid; b < A.B; b += gridDim.x * THREADS) {
+        const int raw = A.n_rows ? A.n_rows[b] : A.R, nr = min(max(raw, 0), A.R), L0 = A.ctx_len[b];
+        if (raw != nr) atomicOr(A.err, ERR_BAD_COUNT);
+        if (nr > 0 && (L0 < 1 || L0 > A.max_len - nr + 1)) atomicOr(A.err, ERR_BAD_LENGTH);
+    }
+    // one item per CTA: slots slowest, so that a row's last splits, often short, come last
+    __shared__ int it01[2];
+    if (multi) q8_range(A, blockIdx.x, gridDim.x, it01);
+    const int it0 = multi ? it01[0] : (static_cast<int>(blockIdx.x) % per_slot) * A.nslot + static_cast<int>(blockIdx.x) / per_slot;
+    const int it1 = multi ? it01[1] : it0 + 1;
+    Item first;
+    if (!first.open(A, it0, it1)) return;   // nothing live here: no barrier or tensor memory was set up
 
-    if (tid == 0) {
+    if (tid == 256) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         for (int st = 0; st < SK; ++st) mbar_init(fullK(st), 1), mbar_init(emptyK(st), 1);
-        for (int st = 0; st < SV; ++st) mbar_init(fullV(st), 1), mbar_init(emptyV(st), CONV);
-        for (int st = 0; st < SW; ++st) mbar_init(fullW(st), CONV), mbar_init(emptyW(st), 1);
-        for (int st = 0; st < SC; ++st) mbar_init(fullS(st), 1), mbar_init(emptyS(st), 2);
-        for (int j = 0; j < 2; ++j) mbar_init(sbar(j), 1), mbar_init(pready(j), 64), mbar_init(pfree(j), 1);
+        for (int st = 0; st < SV; ++st) mbar_init(fullV(st), 1), mbar_init(emptyV(st), 1);
+        for (int st = 0; st < RAW; ++st) mbar_init(fullS(st), 32), mbar_init(emptyS(st), 4);
+        for (int j = 0; j < 2; ++j) mbar_init(sbar(j), 1), mbar_init(pready(j), 128);
+        for (int j = 0; j < PB; ++j) mbar_init(pfree(j), 1);
         mbar_init(done, 1);
-        mbar_init(ofree, 64);
-        mbar_init(qfull, 64);
-        mbar_init(mlready, 64);
-        mbar_init(qfirst, S::Q_THREADS);
+        mbar_init(ofree, 128);
+        mbar_init(qfull, 128);
+        mbar_init(mlready, 128);
+        mbar_init(qfirst, 256);
         fence_mbar_init();
         s_abort = 0;
     }
-    if (warp == 0) {
+    if (warp == 10) {
         tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
     }
@@ -447,10 +622,9 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = tmem_slot, tO = tS + S::O_COL;
-    // the warps that wait for tiles anyway load the first item's Q; the softmax warps reload it when an
-    // item's differs
-    if (warp < 2 || warp == 4 || warp == 5 || warp >= 8) {
-        load_q<HD, S::Q_THREADS>(smem + S::Q_OFF, q_fac[0], A, q8_item(A, first, nrt), tid - (warp < 2 ? 0 : warp < 8 ? 64 : 128));
+    // warps 0..7 load the first item's Q; the softmax warps reload it when an item's differs
+    if (warp < 8) {
+        load_q<HD, NR, 256>(smem + S::Q_OFF, q_fac[0], A, first, tid);
         fence_proxy_async_smem();
         mbar_arrive(qfirst);
     }
@@ -458,120 +632,60 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
     auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || wait_slow(bar, par, &s_abort, A.err); };
     // the same verdict for every lane of a warp
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
-    auto same_q = [](const Item& x, int b, int g, int rb) { return x.b == b && x.g == g && x.row_base == rb; };
 
-    if (warp == 2 || warp == 3) {
+    if (warp == 8 || warp == 9) {
         // ---- TMA
-        const bool isK = warp == 2;
+        const bool isK = warp == 8;
         const int NS = isK ? SK : SV;
         const CUtensorMap* map = isK ? &tmK : &tmV;
         int t = 0;
-        Tiles<true> x;
-        x.start(A, first, nrt);
+        Tiles x;
+        x.start(A, first);
         do {
-            const int st = t % NS, z = x.head(), row = x.place();
+            const int st = t % NS, z0 = x.head(0), z1 = x.head(1), r0 = x.place(0), r1 = x.place(1);
             if (t >= NS && !WW(isK ? emptyK(st) : emptyV(st), ((t / NS) & 1u) ^ 1u)) break;
             if (lane == 0) {
                 const uint32_t fb = isK ? fullK(st) : fullV(st), dst = isK ? sK(st) : sV(st);
-                mbar_arrive_expect_tx(fb, S::CODE);
+                mbar_arrive_expect_tx(fb, (z0 >= 0 ? S::CODE / 2 : 0) + (z1 >= 0 ? S::CODE / 2 : 0));
 #pragma unroll
-                for (int cb = 0; cb < S::KB; ++cb) tma_load_3d(dst + cb * S::KBLK, map, cb * S::KROW, row, z, fb);
+                for (int cb = 0; cb < S::KB; ++cb) {
+                    if (z0 >= 0) tma_load_3d(dst + cb * S::KBLK, map, cb * S::KROW, r0, z0, fb);
+                    if (z1 >= 0) tma_load_3d(dst + cb * S::KBLK + S::KBLK / 2, map, cb * S::KROW, r1, z1, fb);
+                }
             }
             ++t;
-        } while (x.step(A, it1, nrt));
+        } while (x.step(A, it1));
         // every issued copy lands before the CTA may leave
         for (int j = t > NS ? t - NS : 0; j < t; ++j) mbar_wait(isK ? fullK(j % NS) : fullV(j % NS), (j / NS) & 1u, A.err);
-    } else if (warp == 7) {
-        // ---- scales: every lane copies those of its two positions RAW - 1 tiles ahead, and reads only
-        // what it copied itself
-        Tiles<true> x;   // copying
-        Tiles<false> y;  // preparing
-        x.start(A, first, nrt);
-        y.start(A, first, nrt);
-        bool more = true;
-        int tc = 0;
-        auto copy = [&]() {
-            if (more) {
-                const int p = x.I.pos(x.i);
-                const long long at = static_cast<long long>(x.head()) * A.kv.page + x.place();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j = lane + 32 * h;
-                    const bool in = p + j < x.I.maxlen;
-                    const long long a = in ? at + j : 0;
-                    cp_async4(smem_u32(&raw_k[tc % RAW][j]), A.k_scale + a, in);
-                    cp_async4(smem_u32(&raw_v[tc % RAW][j]), A.v_scale + a, in);
-                }
-                ++tc;
-                more = x.step(A, it1, nrt);
-            }
-            cp_async_commit();   // a group per call, an empty one past the last tile
-        };
-        for (int i = 0; i < RAW - 1; ++i) copy();
+    } else if (warp == 11) {
+        // ---- scales
         int t = 0;
+        Tiles x;
+        x.start(A, first);
         do {
-            copy();   // into the slot that the last round has read
-            cp_async_wait<RAW - 1>();
-            const int st = t % SC;
-            if (t >= SC && !WW(emptyS(st), ((t / SC) & 1u) ^ 1u)) break;
+            const int st = t % RAW, p0 = x.I.pos(x.i);
+            int z[2], r[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = lane + 32 * h;
-                const bool in = y.I.pos(y.i) + j < y.I.maxlen;
-                const float vs = raw_v[t % RAW][j];
-                const float vc = fminf(fmaxf(vs, 0x1p-40f), 0x1p60f);   // a NaN becomes 2^-40
-                sc_ks[st][j] = in ? raw_k[t % RAW][j] : 0.f;
-                sc_lv[st][j] = !in ? 0.f : vs != vs ? vs : lg2_approx(vc);   // a NaN scale speaks through t_j alone
-                sc_iv[st][j] = in ? __frcp_rn(vc) : 1.f;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(fullS(st));
+            for (int h = 0; h < 2; ++h) z[h] = x.head(h), r[h] = x.place(h);
+            if (t >= RAW && !WW(emptyS(st), ((t / RAW) & 1u) ^ 1u)) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int j = lane + 32 * k;
+                    const bool in = z[h] >= 0 && p0 + 64 * h + j < x.I.v.end;
+                    const long long at = in ? static_cast<long long>(z[h]) * A.kv.page + r[h] + j : 0;
+                    cp_async4(smem_u32(&raw_k[st][64 * h + j]), A.k_scale + at, in);
+                    cp_async4(smem_u32(&raw_v[st][64 * h + j]), A.v_scale + at, in);
+                }
+            cp_async_arrive(fullS(st));
             ++t;
-        } while (y.step(A, it1, nrt));
+        } while (x.step(A, it1));
         cp_async_wait_all();
-    } else if (warp >= 8) {
-        // ---- V codes to fp16.  A lane takes 16 dims of a position: 8 positions x 4 such chunks per
-        // pass of a warp, so both sides of the swizzles meet every bank once per 8 lanes
-        constexpr int CPR = HD / 64, PASSES = 8 * CPR / CONV;   // column groups of 64 dims; passes per warp
-        const int r8 = lane & 7, c4 = lane >> 3;
-        int t = 0;
-        Tiles<false> x;
-        x.start(A, first, nrt);
-        do {
-            const int sv = t % SV, sw = t % SW;
-            if (!WW(fullV(sv), (t / SV) & 1u)) break;
-            if (t >= SW && !WW(emptyW(sw), ((t / SW) & 1u) ^ 1u)) break;
-            const int left = x.I.maxlen - x.I.pos(x.i);
-            const uint8_t* src = smem + (sV(sv) - base);
-            uint8_t* dst = smem + (sW(sw) - base);
-#pragma unroll 4
-            for (int i = 0; i < PASSES; ++i) {
-                const int u = (warp - 8) * PASSES + i, row = (u / CPR) * 8 + r8, cg = u % CPR;   // cg: 64 dims
-                const int byte = cg * 64 + c4 * 16, blk = byte / S::KROW, ch = (byte % S::KROW) >> 4;
-                const int chs = S::KROW == 128 ? ch ^ r8 : ch ^ (r8 >> 1);
-                const uint4 e = *reinterpret_cast<const uint4*>(src + blk * S::KBLK + row * S::KROW + chs * 16);
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                if (row < left) {
-                    a = make_uint4(f16x2_of(e.x & 0xffff), f16x2_of(e.x >> 16), f16x2_of(e.y & 0xffff), f16x2_of(e.y >> 16));
-                    b = make_uint4(f16x2_of(e.z & 0xffff), f16x2_of(e.z >> 16), f16x2_of(e.w & 0xffff), f16x2_of(e.w >> 16));
-                }
-                uint8_t* d = dst + cg * S::VBLK + row * 128;
-                *reinterpret_cast<uint4*>(d + (((2 * c4) ^ r8) * 16)) = a;
-                *reinterpret_cast<uint4*>(d + (((2 * c4 + 1) ^ r8) * 16)) = b;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(emptyV(sv));
-                mbar_arrive(fullW(sw));
-            }
-            ++t;
-        } while (x.step(A, it1, nrt));
-    } else if (warp == 6) {
+    } else if (warp == 10) {
         // ---- MMAs
         if (lane == 0) {
-            constexpr uint32_t IDS = idesc0(128, T), IDO = idesc0(128, HD, true);
-            constexpr uint32_t VBLK = S::VB > 1 ? S::VBLK : 1024;
+            constexpr uint32_t IDS = idesc_f8(128, 2 * NR, false, false, false), IDO = idesc_f8(128, 2 * NR, true, true, true);
             constexpr int KS = S::KROW / 32;   // MMAs of 32 codes per block row
             const uint32_t sQ = base + S::Q_OFF;
             auto qk = [&](int tt) -> bool {
@@ -579,225 +693,271 @@ __global__ void __launch_bounds__(Shape<HD>::THREADS, Shape<HD>::PER_SM)
                 if (!W(fullK(st), (tt / SK) & 1u)) return false;
                 tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < HD / 32; ++ks) {
-                    const uint32_t off = (ks / KS) * S::KBLK + (ks % KS) * 32;
-                    const uint64_t bd = kmajor_desc<S::KROW>(sK(st) + off);
-                    mma_fp8(tS + (tt & 1) * T, kmajor_desc<S::KROW>(sQ + off), bd, IDS, ks > 0 ? 1u : 0u);
-                    mma_fp8(tS + (tt & 1) * T, kmajor_desc<S::KROW>(sQ + S::CODE + off), bd, IDS, 1u);
-                }
+                for (int ks = 0; ks < HD / 32; ++ks)
+                    mma_fp8(tS + (tt & 1) * 2 * NR, kmajor_desc<S::KROW>(sK(st) + (ks / KS) * S::KBLK + (ks % KS) * 32),
+                            kmajor_desc<S::KROW>(sQ + (ks / KS) * S::QBLK + (ks % KS) * 32), IDS, ks > 0 ? 1u : 0u);
                 tc_commit(sbar(tt & 1));
                 tc_commit(emptyK(st));
                 return true;
             };
-            int t = 0, jl = 0, nq = 0, qb = -1, qg = -1, qrb = -1;
-            bool ok = W(qfirst, 0u), pre = false;   // pre: this item's first S went out with the last item
-            for (int it = first; ok && it < it1; ++it) {
-                const Item I = q8_item(A, it, nrt);
-                if (!I.live) continue;
-                if (MULTI && jl > 0 && !same_q(I, qb, qg, qrb)) {
-                    if (!W(qfull, nq & 1u)) break;
-                    ++nq;
-                }
-                qb = I.b, qg = I.g, qrb = I.row_base;
+            int t = 0, jl = 0, nq = 0;
+            bool ok = W(qfirst, 0u), more = true, pre = false;   // pre: this item's first S went out with the last item
+            Item I = first;
+            while (ok && more) {
                 if (!pre && !qk(t)) break;
-                pre = false;
-                bool next_same = false;   // the next live item has this Q: its first S goes out before the last P V
-                if (MULTI) {
-                    int nx = it + 1;
-                    while (nx < it1 && !q8_item(A, nx, nrt).live) ++nx;
-                    next_same = nx < it1 && same_q(q8_item(A, nx, nrt), I.b, I.g, I.row_base);
-                }
+                Item nx = I;
+                more = nx.next(A, it1);
+                pre = more && nx.same_q(I);   // the next item has this Q: its first S goes out before the last P V
                 for (int i = 0; i < I.ntiles; ++i) {
-                    const int tt = t + i, sw = tt % SW;
-                    if ((i + 1 < I.ntiles || next_same) && !qk(tt + 1)) { ok = false; break; }
-                    if (i + 1 == I.ntiles && next_same) pre = true;
-                    if (MULTI && i == 0 && jl > 0 && !W(ofree, (jl - 1) & 1u)) { ok = false; break; }
-                    if (!W(pready(tt & 1), (tt >> 1) & 1u) || !W(fullW(sw), (tt / SW) & 1u)) { ok = false; break; }
+                    const int tt = t + i, sv = tt % SV;
+                    if ((i + 1 < I.ntiles || pre) && !qk(tt + 1)) { ok = false; break; }
+                    if (i == 0 && jl > 0 && !W(ofree, (jl - 1) & 1u)) { ok = false; break; }
+                    if (!W(fullV(sv), (tt / SV) & 1u) || !W(pready(tt & 1), (tt >> 1) & 1u)) { ok = false; break; }
                     tc_fence_after();
+                    const uint32_t sP = base + S::P_OFF + (tt % PB) * 2 * S::PT;
 #pragma unroll
-                    for (int kk = 0; kk < T / 16; ++kk)   // 16 positions: 8 columns of P, two 8-row groups of V
-                        mma_f16_ta(tO, tS + (tt & 1) * T + kk * 8, sw128_mnmajor_desc(sW(sw) + kk * 2048, VBLK, 1024), IDO,
-                                   (i > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit(pfree(tt & 1));
-                    tc_commit(emptyW(sw));
+                    for (int mb = 0; mb < S::MB; ++mb)
+#pragma unroll
+                        for (int kk = 0; kk < T / 32; ++kk) {   // 32 positions
+                            const uint64_t ad = mnmajor_desc<S::KROW>(sV(sv) + mb * S::KBLK + kk * 32 * S::KROW);
+                            mma_fp8(tO + mb * 2 * NR, ad, mnmajor_plain_desc(sP + kk * 512, T * 16), IDO, (i > 0 || kk > 0) ? 1u : 0u);
+                            mma_fp8(tO + mb * 2 * NR, ad, mnmajor_plain_desc(sP + S::PT + kk * 512, T * 16), IDO, 1u);
+                        }
+                    tc_commit(pfree(tt % PB));
+                    tc_commit(emptyV(sv));
                 }
                 t += I.ntiles;
                 ++jl;
+                if (more && !pre && !W(qfull, nq++ & 1u)) break;
+                I = nx;
             }
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             mbar_wait(done, 0u, A.err);
         }
     } else if (warp >= 4) {
-        // ---- epilogue: thread = tile row rho (tensor memory lane rho)
-        const int rho = tid - 128;
+        // ---- epilogue: thread = dim of O^T (tensor memory lane), modulo 128
+        const int d = tid - 128;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int t = 0, jl = 0;
-        for (int it = first; it < it1; ++it) {
-            const Item I = q8_item(A, it, nrt);
-            if (!I.live) continue;
+        Item I = first;
+        do {
             const int tl = t + I.ntiles - 1;
-            if (!WW(mlready, jl & 1u) || !WW(pfree(tl & 1), (tl >> 1) & 1u)) break;
+            if (!WW(mlready, jl & 1u) || !WW(pfree(tl % PB), (tl / PB) & 1u)) break;
             tc_fence_after();
-            const int grow = I.row_base + rho;
-            const bool live = grow < I.rows;
-            const int r = grow / A.G, h = I.g * A.G + grow % A.G;
-            const long long idx = ((static_cast<long long>(I.b) * A.R + r) * A.Hq + h) * A.nslot + I.slot;
-            float* op = A.opart + idx * HD;
-            const float2 ml = ml_sm[rho];
-            if (__any_sync(0xffffffffu, live)) {
+            if (HD >= 128 || warp < 6) {
 #pragma unroll 1
-                for (int c = 0; c < HD / 32; ++c) {
-                    float o[32];
-#pragma unroll
-                    for (int q2 = 0; q2 < 2; ++q2) tmem_ld16(tO + lane_off + c * 32 + q2 * 16, o + q2 * 16);
+                for (int c = 0; c < S::MB * NR; c += 8) {
+                    const int mb = c / NR, r0 = c % NR;
+                    if (r0 >= I.v.rows) continue;
+                    float a[8], b[8];
+                    tmem_ld8(tO + lane_off + mb * 2 * NR + r0, a);
+                    tmem_ld8(tO + lane_off + mb * 2 * NR + NR + r0, b);
                     tmem_ld_wait();
-                    if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(op + c * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (r0 + e < I.v.rows) A.opart[at_sm[r0 + e] * HD + mb * 128 + d] = __fmaf_rn(b[e], 1.f / LOW_SCALE, a[e]);
                 }
-                if (live) A.ml[idx] = ml;
             }
+            if (d < I.v.rows)
+                A.ml[at_sm[d]] = make_float2(m_sm[d], __fadd_rn(__fadd_rn(l_sm[0][d], l_sm[1][d]), __fadd_rn(l_sm[2][d], l_sm[3][d])));
             tc_fence_before();
-            mbar_arrive(ofree);   // O (and ml_sm) may be overwritten by the next item
+            mbar_arrive(ofree);   // O, m and l may be overwritten by the next item
             t += I.ntiles;
             ++jl;
-        }
+        } while (I.next(A, it1));
     } else {
-        // ---- softmax: thread = tile row rho (tensor memory lane rho)
-        const int rho = tid;
+        // ---- softmax: thread = position of the tile (tensor memory lane).  A wait that gives up breaks
+        // no loop here, so that the four warps meet at the same barriers (later waits return at once)
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-        int t = 0, jl = 0, nq = 0, qb = -1, qg = -1, qrb = -1;
-        const bool q_in = WW(qfirst, 0u);
-        for (int it = first; q_in && it < it1; ++it) {
-            const Item I = q8_item(A, it, nrt);
-            if (!I.live) continue;
-            if constexpr (MULTI) {
-                if (jl > 0 && !same_q(I, qb, qg, qrb)) {
-                    // every S of the old Q is complete (this warp has seen the last), and the MMA warp
-                    // issues none of this item until qfull
-                    load_q<HD, 64>(smem + S::Q_OFF, q_fac[(nq + 1) & 1], A, I, rho);
-                    fence_proxy_async_smem();
-                    mbar_arrive(qfull);
-                    if (!WW(qfull, nq & 1u)) break;   // the other warp's factors too
-                    ++nq;
-                }
+        int t = 0, jl = 0, nq = 0;
+        long long at = 0;   // of row tid in the workspace, slot 0
+        bool fresh = true;
+        Item I = first;
+        W(qfirst, 0u);
+        __syncwarp();
+        for (;;) {
+            if (fresh) {
+                const int gr = I.v.row_base + tid;
+                at = ((static_cast<long long>(I.b) * A.R + gr / A.G) * A.Hq + I.g * A.G + gr % A.G) * A.nslot;
             }
-            qb = I.b, qg = I.g, qrb = I.row_base;
-            const int grow = I.row_base + rho;
-            const int len = grow < I.rows ? I.L0 + grow / A.G : 0;
-            const int from = A.window ? max(0, len - A.window) : 0;   // sees [from, len) and [0, upto)
-            const int upto = min(A.sinks, len);
-            const bool mine = grow < I.rows, any = I.row_base + 32 * warp < I.rows;   // a row; a row in the warp
-            const float c = mine ? __fmul_rn(A.sl2, q_fac[nq & 1][rho]) : 0.f;
-            float m = NEG_INF, l = 0.f;
-            bool ok = true;
+            if (fresh && jl > 0) {
+                // every S of the old Q is complete (this warp has seen the last), and the MMA warp
+                // issues none of this item until qfull
+                load_q<HD, NR, 128>(smem + S::Q_OFF, q_fac[(nq + 1) & 1], A, I, tid);
+                fence_proxy_async_smem();
+                mbar_arrive(qfull);
+                WW(qfull, nq & 1u);   // the other warps' factors too
+                ++nq;
+            }
+            const float* fac = q_fac[nq & 1];
+            float l[NR], m = NEG_INF;   // l of this thread's positions; m of row tid
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+#pragma unroll 1
             for (int i = 0; i < I.ntiles; ++i) {
-                const int tt = t + i, sc = tt % SC;
-                if (!WW(fullS(sc), (tt / SC) & 1u) || !WW(sbar(tt & 1), (tt >> 1) & 1u)) { ok = false; break; }
+                const int tt = t + i, st = tt % RAW, p0 = I.pos(i), p = p0 + tid;
+                // row n / G of length L0 + n / G (n = row_base + r) sees p from r = r_lo on, and with a
+                // window to r_hi unless p is a sink
+                const long long lo64 = static_cast<long long>(p - I.v.L0 + 1) * A.G - I.v.row_base;
+                const long long hi64 = (static_cast<long long>(p) + A.window - I.v.L0 + 1) * A.G - I.v.row_base;
+                const int r_lo = p >= I.v.end ? NR : static_cast<int>(max(0ll, min(lo64, static_cast<long long>(NR))));
+                const int r_hi = !A.window || p < A.sinks ? NR : static_cast<int>(max(0ll, min(hi64, static_cast<long long>(NR))));
+                const bool whole = __all_sync(0xffffffffu, r_lo == 0 && r_hi == NR);
+                WW(fullS(st), (tt / RAW) & 1u);
+                const float ks = raw_k[st][tid], vs = raw_v[st][tid];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(emptyS(st));
+                const float vc = fminf(fmaxf(vs, 0x1p-40f), 0x1p60f);   // a NaN becomes 2^-40
+                const float lv = vs != vs ? vs : lg2_approx(vc);        // a NaN scale speaks through t_j alone
+                const float iv = __frcp_rn(vc);
+                WW(sbar(tt & 1), (tt >> 1) & 1u);
                 tc_fence_after();
-                if (!any) {   // the whole warp's rows are behind the item's: their P is whatever S was
-                    tc_fence_before();
-                    mbar_arrive(pready(tt & 1));
-                    if (lane == 0) mbar_arrive(emptyS(sc));
-                    continue;
-                }
-                const int p0 = I.pos(i);
-                const bool whole = __all_sync(0xffffffffu, !mine || (p0 >= from && p0 + T <= len));
-                // t_j of 32 positions, twice: for their maximum, and again for p (registers for 64 and code
-                // unrolled over them cost more than the second read)
-                auto scores = [&](int j0, float* s) {
-                    tmem_ld16(tS + lane_off + (tt & 1) * T + j0, s);
-                    tmem_ld16(tS + lane_off + (tt & 1) * T + j0 + 16, s + 16);
+                float s[NR];   // t_j of the rows
+#pragma unroll
+                for (int r0 = 0; r0 < NR; r0 += 16) {
+                    float lo[16];
+                    constexpr int TWO = 16;
+                    const int n = NR - r0 < TWO ? 8 : TWO;
+                    if (n == 16) {
+                        tmem_ld16(tS + lane_off + (tt & 1) * 2 * NR + r0, s + r0);
+                        tmem_ld16(tS + lane_off + (tt & 1) * 2 * NR + NR + r0, lo);
+                    } else {
+                        tmem_ld8(tS + lane_off + (tt & 1) * 2 * NR + r0, s + r0);
+                        tmem_ld8(tS + lane_off + (tt & 1) * 2 * NR + NR + r0, lo);
+                    }
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 ks = *reinterpret_cast<const float4*>(&sc_ks[sc][j0 + j]);
-                        const float4 lv = *reinterpret_cast<const float4*>(&sc_lv[sc][j0 + j]);
-                        mul2(s[j], s[j + 1], c, c);
-                        mul2(s[j + 2], s[j + 3], c, c);
-                        fma2(s[j], s[j + 1], ks.x, ks.y, lv.x, lv.y);
-                        fma2(s[j + 2], s[j + 3], ks.z, ks.w, lv.z, lv.w);
+                    for (int k = 0; k < n; k += 4) {
+                        float* x = s + r0 + k;
+                        const float4 c = *reinterpret_cast<const float4*>(fac + r0 + k);
+                        add2(x[0], x[1], lo[k], lo[k + 1]);
+                        add2(x[2], x[3], lo[k + 2], lo[k + 3]);
+                        mul2(x[0], x[1], c.x, c.y);
+                        mul2(x[2], x[3], c.z, c.w);
+                        fma2(x[0], x[1], ks, ks, lv, lv);
+                        fma2(x[2], x[3], ks, ks, lv, lv);
                     }
-                    if (!whole) {
+                }
+                if (!whole) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int p = p0 + j0 + j;
-                            if (!(p < len && (p >= from || p < upto))) s[j] = NEG_INF;
+                    for (int r = 0; r < NR; ++r)
+                        if (r < r_lo || r >= r_hi) s[r] = NEG_INF;
+                }
+                bool move = i == 0;
+                if (!move) {
+                    float over = NEG_INF;
+#pragma unroll
+                    for (int r = 0; r < NR; r += 4) {
+                        const float4 mo = *reinterpret_cast<const float4*>(mo_sm + r);
+                        over = fmaxf(fmaxf(fmaxf(over, __fsub_rn(s[r], mo.x)), fmaxf(__fsub_rn(s[r + 1], mo.y), __fsub_rn(s[r + 2], mo.z))),
+                                     __fsub_rn(s[r + 3], mo.w));
+                    }
+                    move = softmax_any(over > P_SHIFT + RESCALE_SLACK);
+                }
+                if (move) {
+#pragma unroll
+                    for (int r = 0; r < NR; r += 4) {
+                        const float4 x = make_float4(warp_max(s[r]), warp_max(s[r + 1]), warp_max(s[r + 2]), warp_max(s[r + 3]));
+                        if (lane == 0) *reinterpret_cast<float4*>(&wmax[warp][r]) = x;
+                    }
+                    softmax_sync();
+                    bool scaled = false;
+                    if (tid < NR) {
+                        const float mx = fmaxf(fmaxf(wmax[0][tid], wmax[1][tid]), fmaxf(wmax[2][tid], wmax[3][tid]));
+                        const float old = m == NEG_INF ? DEAD : __fsub_rn(m, P_SHIFT);
+                        float al = 1.f;
+                        if (__fsub_rn(mx, old) > P_SHIFT + RESCALE_SLACK) {
+                            if (m != NEG_INF) al = ex2_approx(__fsub_rn(m, mx));
+                            m = mx;
                         }
+                        mo_sm[tid] = m == NEG_INF ? DEAD : __fsub_rn(m, P_SHIFT);
+                        al_sm[tid] = al;
+                        scaled = al != 1.f;
                     }
-                };
-                float mx4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    if (softmax_any(scaled)) {
+                        // O once P V of the tile before has completed
+                        WW(pfree((tt - 1) % PB), ((tt - 1) / PB) & 1u);
+                        tc_fence_after();
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) l[r] = __fmul_rn(l[r], al_sm[r]);
 #pragma unroll 1
-                for (int j0 = 0; j0 < T; j0 += 32) {
-                    float s[32];
-                    scores(j0, s);
+                        for (int c = 0; c < S::MB * 2 * NR; c += 8) {
+                            float o[8];
+                            tmem_ld8(tO + lane_off + c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) mx4[(j / 2) & 3] = fmaxf(mx4[(j / 2) & 3], fmaxf(s[j], s[j + 1]));
-                }
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                const float mn = (m == NEG_INF || mx > __fadd_rn(m, RESCALE_SLACK)) ? mx : m;
-                const bool dead = mn == NEG_INF;
-                const float al = (dead || mn == m) ? 1.f : ex2_approx(__fsub_rn(m, mn));
-                const float mo = dead ? 0.f : __fsub_rn(mn, P_SHIFT);
-                float ts[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int j0 = 0; j0 < T; j0 += 32) {
-                    float s[32], pk[16];
-                    scores(j0, s);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 iv = *reinterpret_cast<const float4*>(&sc_iv[sc][j0 + j]);
-                        float* p = s + j;
-                        add2(p[0], p[1], -mo, -mo);
-                        add2(p[2], p[3], -mo, -mo);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
-                        fma2_acc(ts[0], ts[1], p[0], p[1], iv.x, iv.y);
-                        fma2_acc(ts[2], ts[3], p[2], p[3], iv.z, iv.w);
-                        pk[j / 2] = __uint_as_float(pack_f16x2(p[0], p[1]));
-                        pk[j / 2 + 1] = __uint_as_float(pack_f16x2(p[2], p[3]));
-                    }
-                    // over S columns that have been read: P of position j lies in column j / 2
-                    tmem_st16(tS + lane_off + (tt & 1) * T + j0 / 2, pk);
-                }
-                l = __fmaf_rn(l, al, __fadd_rn(__fadd_rn(ts[0], ts[1]), __fadd_rn(ts[2], ts[3])));
-                m = mn;
-                // O is rescaled once P V of the tile before has completed
-                if (i >= 1 && __any_sync(0xffffffffu, mine && al != 1.f)) {
-                    if (!WW(pfree((tt - 1) & 1), ((tt - 1) >> 1) & 1u)) { ok = false; break; }
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int k = 0; k < HD / 32; ++k) {
-                        float o[32];
-#pragma unroll
-                        for (int q2 = 0; q2 < 2; ++q2) tmem_ld16(tO + lane_off + k * 32 + q2 * 16, o + q2 * 16);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __fmul_rn(o[e], al);
-#pragma unroll
-                        for (int q2 = 0; q2 < 2; ++q2) tmem_st16(tO + lane_off + k * 32 + q2 * 16, o + q2 * 16);
+                            for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(o[e], al_sm[c % NR + e]);
+                            tmem_st8(tO + lane_off + c, o);
+                        }
+                        tmem_st_wait();
                     }
                 }
-                tmem_st_wait();
+                // V codes that were not loaded or lie behind every row: zeros, as 0 times their NaN is NaN
+                const bool gap = p >= I.v.end || !I.v.half(p0 + (tid & 64));
+                if (__any_sync(0xffffffffu, gap)) {
+                    const int sv = tt % SV;
+                    WW(fullV(sv), (tt / SV) & 1u);
+                    if (gap) {
+#pragma unroll
+                        for (int cb = 0; cb < S::KB; ++cb)
+#pragma unroll
+                            for (int c = 0; c < S::KROW; c += 16)
+                                *reinterpret_cast<uint4*>(smem + S::V_OFF + sv * S::CODE + cb * S::KBLK + tid * S::KROW + c) =
+                                    make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (tt >= PB) WW(pfree(tt % PB), ((tt / PB) & 1u) ^ 1u);
+                uint8_t* P = smem + S::P_OFF + (tt % PB) * 2 * S::PT + tid * 16;
+                uint32_t a[NR / 2], b[NR / 2];   // bytes of the rows: terms 1, then 3; 2, then 4
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 mo = *reinterpret_cast<const float4*>(mo_sm + r);
+                    float* x = s + r;
+                    add2(x[0], x[1], -mo.x, -mo.y);
+                    add2(x[2], x[3], -mo.z, -mo.w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e]);
+                    fma2_acc(l[r], l[r + 1], x[0], x[1], iv, iv);
+                    fma2_acc(l[r + 2], l[r + 3], x[2], x[3], iv, iv);
+                    uint32_t u = pack_f16x2(x[0], x[1]), v = pack_f16x2(x[2], x[3]);
+                    constexpr uint32_t TOP = 0xff00ff00u, UP = 0x54005400u;   // 64, twice
+                    a[r / 4] = __byte_perm(u, v, 0x7531);
+                    u = sub_f16x2(u, u & TOP), v = sub_f16x2(v, v & TOP);
+                    b[r / 4] = __byte_perm(u, v, 0x7531);
+                    u = mul_f16x2(sub_f16x2(u, u & TOP), UP), v = mul_f16x2(sub_f16x2(v, v & TOP), UP);
+                    a[NR / 4 + r / 4] = __byte_perm(u, v, 0x7531);
+                    u = sub_f16x2(u, u & TOP), v = sub_f16x2(v, v & TOP);
+                    b[NR / 4 + r / 4] = __byte_perm(u, v, 0x7531);
+                }
+#pragma unroll
+                for (int c = 0; c < NR / 8; ++c) {
+                    *reinterpret_cast<uint4*>(P + c * T * 16) = make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(P + S::PT + c * T * 16) = make_uint4(b[4 * c], b[4 * c + 1], b[4 * c + 2], b[4 * c + 3]);
+                }
+                fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(pready(tt & 1));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(emptyS(sc));
             }
-            if (!ok) break;
             // hand m and l to the epilogue warps (once they are done with the previous item's)
-            if (MULTI && jl > 0 && !WW(ofree, (jl - 1) & 1u)) break;
-            ml_sm[rho] = make_float2(m, l);
+            if (jl > 0) WW(ofree, (jl - 1) & 1u);
+            int r0 = 0;
+            const int n = warp_sums<NR, 16>(l, lane, &r0);
+            // with 2^k rows the last lanes repeat sums, which is as well
+#pragma unroll
+            for (int k = 0; k < NR; ++k)
+                if (k < n) l_sm[warp][r0 + k] = l[k];
+            if (tid < I.v.rows) m_sm[tid] = m, at_sm[tid] = at + I.slot;
             mbar_arrive(mlready);
             t += I.ntiles;
             ++jl;
+            const Item was = I;
+            if (!I.next(A, it1)) break;
+            fresh = !I.same_q(was);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 10) {
         tc_fence_after();
         tmem_dealloc(tS, S::TMEM_COLS);
     }
@@ -919,26 +1079,36 @@ inline bool sizes_ok(int B, int R, int Hq, int hd, int max_ctx, int window, int 
            max_ctx <= (1 << 30) && window >= 0 && sinks >= 0 && static_cast<long long>(B) * R * Hq <= (1ll << 30);
 }
 
-template <int HD>
-xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a, const CombineArgs& c, cudaStream_t s) {
-    using S = Shape<HD>;
+// Row tiles: as few as 64 rows allow, and of even sizes.
+inline int row_tiles(int rows) { return (rows + 63) / 64; }
+
+template <int HD, int NR>
+xv_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a, cudaStream_t s) {
+    using S = Shape<HD, NR>;
     int sms = 0;
-    if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(attn_q8_kernel<HD, true>), S::SMEM, false, "attn_q8: set shared memory size"))
-        return st;
-    if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(attn_q8_kernel<HD, false>), S::SMEM, false, "attn_q8: set shared memory size"))
+    if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(attn_q8_kernel<HD, NR>), S::SMEM, false, "attn_q8: set shared memory size"))
         return st;
     if (xv_status st = device_sm_count(&sms)) return st;
-    const long long n_items = static_cast<long long>(a.nslot) * ((a.R * a.G + 63) / 64) * a.Hkv * a.B;
+    const long long n_items = static_cast<long long>(a.nslot) * a.nrt * a.Hkv * a.B;
     if (n_items > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_q8: %lld work items", n_items);
     const int room = sms * S::PER_SM;
-    const bool multi = n_items > 2ll * room;
-    const dim3 grid(static_cast<unsigned>(multi ? room : n_items));
     trace_pre(s);
-    if (multi) launch_k(attn_q8_kernel<HD, true>, grid, dim3(S::THREADS), S::SMEM, s, tmK, tmV, a);
-    else launch_k(attn_q8_kernel<HD, false>, grid, dim3(S::THREADS), S::SMEM, s, tmK, tmV, a);
+    launch_k(attn_q8_kernel<HD, NR>, dim3(static_cast<unsigned>(std::min<long long>(room, n_items))), dim3(THREADS), S::SMEM, s, tmK, tmV, a);
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq, seen = a.window && a.window < a.max_len ? a.window + a.sinks : a.max_len;
-    if (xv_status st = launched("attn_q8_kernel", s, K_ATTN_Q8, (2ll * HD + 8) * a.B * a.Hkv * seen + 2 * rows * HD + 4 * rows * a.nslot * (HD + 2)))
+    return launched("attn_q8_kernel", s, K_ATTN_Q8, (2ll * HD + 8) * a.B * a.Hkv * seen + 2 * rows * HD + 4 * rows * a.nslot * (HD + 2));
+}
+
+template <int HD>
+xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a, const CombineArgs& c, cudaStream_t s) {
+    const int n = a.tile_rows;
+    if (xv_status st = n <= 8    ? launch_attn<HD, 8>(tmK, tmV, a, s)
+                       : n <= 16 ? launch_attn<HD, 16>(tmK, tmV, a, s)
+                       : n <= 24 ? launch_attn<HD, 24>(tmK, tmV, a, s)
+                       : n <= 32 ? launch_attn<HD, 32>(tmK, tmV, a, s)
+                       : n <= 48 ? launch_attn<HD, 48>(tmK, tmV, a, s)
+                                 : launch_attn<HD, 64>(tmK, tmV, a, s))
         return st;
+    const long long rows = static_cast<long long>(a.B) * a.R * a.Hq;
     trace_pre(s);
     launch_k(attn_q8_combine_kernel<HD>, dim3(static_cast<unsigned>(rows)), dim3(CB_GROUPS * HD / 4), 0, s, c);
     return launched("attn_q8_combine_kernel", s, K_ATTN_Q8, 4 * rows * a.nslot * (HD + 2) + 2 * rows * HD * (c.gate ? 2 : 1));
@@ -968,7 +1138,7 @@ xv_status attn_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, 
     CUtensorMap tmK, tmV;
     const uint64_t dims[3] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(kv.page), static_cast<uint64_t>(kv.n_pages) * Hkv};
     const uint64_t strides[2] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(kv.page) * hd};
-    const uint32_t box[3] = {static_cast<uint32_t>(hd < 128 ? hd : 128), static_cast<uint32_t>(T), 1};
+    const uint32_t box[3] = {static_cast<uint32_t>(hd < 128 ? hd : 128), static_cast<uint32_t>(T / 2), 1};
     const CUtensorMapSwizzle sw = hd < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     if (xv_status st = encode_tiled(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cache->k, dims, strides, box, sw)) return st;
     if (xv_status st = encode_tiled(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cache->v, dims, strides, box, sw)) return st;
@@ -979,8 +1149,9 @@ xv_status attn_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, 
     const size_t rows = static_cast<size_t>(B) * R * Hq * nslot;
     float* opart = static_cast<float*>(ws);
     float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + round256(rows * hd * sizeof(float)));
-    const Q8Args a{q, q_stride, kv, cache->k_scale, cache->v_scale, ctx_len, n_rows, R, Hq / Hkv, Hq, Hkv, B, nslot, nsink, max_ctx,
-                   win, win ? sinks : 0, shift, scale * 1.4426950408889634f, opart, ml, err};
+    const int grp = R * (Hq / Hkv), nrt = row_tiles(grp);
+    const Q8Args a{q, q_stride, kv, cache->k_scale, cache->v_scale, ctx_len, n_rows, R, Hq / Hkv, Hq, Hkv, B,
+                   (grp + nrt - 1) / nrt, nrt, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, scale * 1.4426950408889634f, opart, ml, err};
     const CombineArgs c{ctx_len, n_rows, R, Hq, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, opart, ml, gate, gate_stride, out,
                         out_stride};
     return hd == 256 ? launch<256>(tmK, tmV, a, c, s) : hd == 128 ? launch<128>(tmK, tmV, a, c, s) : launch<64>(tmK, tmV, a, c, s);
