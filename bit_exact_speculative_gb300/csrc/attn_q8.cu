@@ -76,8 +76,11 @@ struct Shape {
     static constexpr int PB = NR <= 24 ? 2 : 1;               // P buffers
     // two CTAs per SM where their registers and rings allow it
     static constexpr int PER_SM = HD <= 128 && NR <= 16 ? 2 : 1;
-    static constexpr int RAW = 4;                             // tiles of scales
-    static constexpr int STATIC = 2 * RAW * T * 4 + 15 * NR * 4 + 64;
+    // softmax warpgroups of RW rows each: one thread's 48 rows took 3000 cycles a tile, and three times the code
+    static constexpr int RW = NR % 16 ? 8 : 16, WG = NR / RW;
+    static constexpr int THREADS = 128 * (WG + 2);
+    static constexpr int RAW = PER_SM == 2 ? 4 : 8;           // tiles of scales
+    static constexpr int STATIC = 3 * RAW * T * 4 + 15 * NR * 4 + 256;
     static constexpr int ROOM = (PER_SM == 2 ? 233472 / 2 - 1024 : 232448) - STATIC - 1024 - 512 - Q - PB * 2 * PT;
     static constexpr int STAGES = ROOM / CODE;
     static constexpr int SV = STAGES < 11 ? (STAGES + 1) / 2 : 6, SK = STAGES < 12 ? STAGES - SV : 6;
@@ -88,13 +91,12 @@ struct Shape {
     static constexpr int BAR_OFF = P_OFF + PB * 2 * PT;
     static constexpr int N_BARS = 2 * (SK + SV + RAW) + 4 + PB + 5;
     static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
-    static constexpr uint32_t O_COL = 4 * NR;                 // S twice, then O: MB blocks of [terms 1, 2 | terms 3, 4]
+    static constexpr uint32_t O_COL = 4 * NR;                 // S twice, then O: MB blocks, each per warpgroup [terms 1, 2 | terms 3, 4]
     static constexpr int COLS = 4 * NR + MB * 2 * NR;
     static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(NR % 8 == 0 && NR <= 64 && COLS <= 512 && PER_SM * TMEM_COLS <= 512, "");
     static_assert(SK >= 2 && SV >= 2 && 8 * N_BARS <= 512 && QBLK % 1024 == 0, "");
 };
-constexpr int THREADS = 384;
 
 struct Q8Args {
     const uint16_t* q;
@@ -128,18 +130,20 @@ __device__ __forceinline__ int q8_first(int L0, int shift, int nsink) {
 // [sinks, lo).
 struct Sight {
     int L0, rows, row_base, end, lo, sinks;   // rows <= 0: nothing to do
+    int from, upto;                           // every row sees [from, upto)
     __device__ __forceinline__ void of(const Q8Args& A, int b, int rt) {
         const int nr = q8_rows(A.n_rows, b, A.R);
         L0 = __ldg(A.ctx_len + b);
         row_base = rt * A.tile_rows;
         rows = min(nr * A.G - row_base, A.tile_rows);
         if (L0 < 1 || L0 > A.max_len - nr + 1) rows = 0;
-        end = lo = sinks = 0;
+        end = lo = sinks = from = upto = 0;
         if (rows <= 0) return;
         // what other rows see beside a row changes nothing of it
         end = L0 + (row_base + rows - 1) / A.G;
-        const int minlen = L0 + row_base / A.G;
-        if (A.window && minlen > A.window) lo = minlen - A.window, sinks = A.sinks;
+        upto = L0 + row_base / A.G;
+        if (A.window) from = max(0, end - A.window);
+        if (A.window && upto > A.window) lo = upto - A.window, sinks = A.sinks;
     }
     // whether a row sees any of the 64 positions at p
     __device__ __forceinline__ bool half(int p) const { return p < end && (p + 64 > lo || p < sinks); }
@@ -213,6 +217,7 @@ struct Item {
 };
 
 // The items of persistent CTA c of n: equal shares of the cost.  All of the CTA's threads.
+template <int THREADS>
 __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it01) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per = (A.B + THREADS - 1) / THREADS;
     auto whole = [&](int b, int* one, int* tiles) {   // cost of sequence b, of a row tile of a head of it, live row tiles
@@ -319,7 +324,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 template <int HD, int NR, int NT>
 __device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A, const Item& I, int t0) {
     using S = Shape<HD, NR>;
-    constexpr int LPH = HD / 8, RPP = NT / LPH, UN = 4;
+    constexpr int LPH = HD / 8, RPP = NT / LPH, UN = (NR + RPP - 1) / RPP < 4 ? (NR + RPP - 1) / RPP : 4;
     const int n = I.v.rows, c = t0 % LPH;
 #pragma unroll 1
     for (int r0 = 0; r0 < NR; r0 += RPP * UN) {
@@ -430,17 +435,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
-// Arrives on the mbarrier (one of its count) once the thread's cp.async copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-// Barrier of the four softmax warps; with a flag, whether any thread's is set.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool f) {
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Barriers of a softmax warpgroup; with a flag, whether any thread's is set.
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool wg_any(int id, bool f) {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, 1, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, %2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
                  : "=r"(r)
-                 : "r"(f ? 1u : 0u)
+                 : "r"(f ? 1u : 0u), "r"(id)
                  : "memory");
     return r != 0;
 }
@@ -539,22 +543,24 @@ struct Tiles {
 };
 
 // Warps of a CTA and what they do per tile t (counted over the CTA's items):
-//   0..3   softmax, a thread per position: S out of tensor memory, t_j, mask; the references stand
-//          unless some row's t_j passes its by RESCALE_SLACK (or the tile is an item's first): then
-//          the tile's maxima are found, and references, l and O moved; P to shared memory, l per thread
-//   4..7   an item's O, m and l to the workspace, while the next item's first tiles run
-//   8, 9   TMA of the K and V codes into their rings
-//   10     MMAs: S(t + 1) = K Q^T, then O += V^T P(t); the S that overwrites S(t - 1) is issued after
+//   0..4 WG - 1   softmax, warpgroup w for rows RW w.., a thread per position: S out of tensor memory,
+//          t_j, mask; the references stand unless some row's t_j passes its by RESCALE_SLACK (or the
+//          tile is an item's first): then the tile's maxima are found, and references, l and O moved;
+//          P to shared memory, l per thread
+//   then 4 an item's O, m and l to the workspace, while the next item's first tiles run
+//   2      TMA of the K and V codes into their rings
+//   1      MMAs: S(t + 1) = K Q^T, then O += V^T P(t); the S that overwrites S(t - 1) is issued after
 //          the P V of that tile, whose P was made of it
-//   11     the positions' scales into a ring
+//   1      the positions' scales: ks, log2(vs) and 1 / vs into a ring
 template <int HD, int NR>
-__global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
+__global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args A) {
     griddep_launch();
     using S = Shape<HD, NR>;
-    constexpr int SK = S::SK, SV = S::SV, RAW = S::RAW, PB = S::PB;
+    constexpr int SK = S::SK, SV = S::SV, RAW = S::RAW, PB = S::PB, RW = S::RW, WG = S::WG;
+    constexpr int W_OUT = 4 * WG, W_K = W_OUT + 4, W_V = W_K + 1, W_MMA = W_K + 2, W_SC = W_K + 3;   // warps
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(16) float raw_k[RAW][T], raw_v[RAW][T];
+    __shared__ __align__(16) float sc_k[RAW][T], sc_v[RAW][T], sc_i[RAW][T];
     __shared__ __align__(16) float q_fac[2][NR], mo_sm[NR], al_sm[NR], wmax[4][NR], l_sm[4][NR], m_sm[NR];
     __shared__ long long at_sm[NR];
     __shared__ uint32_t tmem_slot;
@@ -585,36 +591,36 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
     const int per_slot = n_items / A.nslot;
     const bool multi = static_cast<int>(gridDim.x) < n_items;
     griddep_wait();
-    for (int b = blockIdx.x + gridDim.x * tid; b < A.B; b += gridDim.x * THREADS) {
+    for (int b = blockIdx.x + gridDim.x * tid; b < A.B; b += gridDim.x * S::THREADS) {
         const int raw = A.n_rows ? A.n_rows[b] : A.R, nr = min(max(raw, 0), A.R), L0 = A.ctx_len[b];
         if (raw != nr) atomicOr(A.err, ERR_BAD_COUNT);
         if (nr > 0 && (L0 < 1 || L0 > A.max_len - nr + 1)) atomicOr(A.err, ERR_BAD_LENGTH);
     }
     // one item per CTA: slots slowest, so that a row's last splits, often short, come last
     __shared__ int it01[2];
-    if (multi) q8_range(A, blockIdx.x, gridDim.x, it01);
+    if (multi) q8_range<S::THREADS>(A, blockIdx.x, gridDim.x, it01);
     const int it0 = multi ? it01[0] : (static_cast<int>(blockIdx.x) % per_slot) * A.nslot + static_cast<int>(blockIdx.x) / per_slot;
     const int it1 = multi ? it01[1] : it0 + 1;
     Item first;
     if (!first.open(A, it0, it1)) return;   // nothing live here: no barrier or tensor memory was set up
 
-    if (tid == 256) {
+    if (tid == 32 * W_K) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         for (int st = 0; st < SK; ++st) mbar_init(fullK(st), 1), mbar_init(emptyK(st), 1);
         for (int st = 0; st < SV; ++st) mbar_init(fullV(st), 1), mbar_init(emptyV(st), 1);
-        for (int st = 0; st < RAW; ++st) mbar_init(fullS(st), 32), mbar_init(emptyS(st), 4);
-        for (int j = 0; j < 2; ++j) mbar_init(sbar(j), 1), mbar_init(pready(j), 128);
+        for (int st = 0; st < RAW; ++st) mbar_init(fullS(st), 1), mbar_init(emptyS(st), 4 * WG);
+        for (int j = 0; j < 2; ++j) mbar_init(sbar(j), 1), mbar_init(pready(j), 128 * WG);
         for (int j = 0; j < PB; ++j) mbar_init(pfree(j), 1);
         mbar_init(done, 1);
         mbar_init(ofree, 128);
-        mbar_init(qfull, 128);
-        mbar_init(mlready, 128);
-        mbar_init(qfirst, 256);
+        mbar_init(qfull, 128 * WG);
+        mbar_init(mlready, 128 * WG);
+        mbar_init(qfirst, 128 * (WG + 1));
         fence_mbar_init();
         s_abort = 0;
     }
-    if (warp == 10) {
+    if (warp == W_MMA) {
         tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
         tmem_relinquish();
     }
@@ -622,9 +628,9 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = tmem_slot, tO = tS + S::O_COL;
-    // warps 0..7 load the first item's Q; the softmax warps reload it when an item's differs
-    if (warp < 8) {
-        load_q<HD, NR, 256>(smem + S::Q_OFF, q_fac[0], A, first, tid);
+    // softmax and epilogue warps load the first item's Q; the softmax warps reload it when an item's differs
+    if (warp < W_K) {
+        load_q<HD, NR, 128 * (WG + 1)>(smem + S::Q_OFF, q_fac[0], A, first, tid);
         fence_proxy_async_smem();
         mbar_arrive(qfirst);
     }
@@ -633,9 +639,9 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
     // the same verdict for every lane of a warp
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
 
-    if (warp == 8 || warp == 9) {
+    if (warp == W_K || warp == W_V) {
         // ---- TMA
-        const bool isK = warp == 8;
+        const bool isK = warp == W_K;
         const int NS = isK ? SK : SV;
         const CUtensorMap* map = isK ? &tmK : &tmV;
         int t = 0;
@@ -657,32 +663,58 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
         } while (x.step(A, it1));
         // every issued copy lands before the CTA may leave
         for (int j = t > NS ? t - NS : 0; j < t; ++j) mbar_wait(isK ? fullK(j % NS) : fullV(j % NS), (j / NS) & 1u, A.err);
-    } else if (warp == 11) {
-        // ---- scales
-        int t = 0;
-        Tiles x;
+    } else if (warp == W_SC) {
+        // ---- scales: every lane copies those of its four positions RAW - 2 tiles ahead, and makes of them,
+        // in their place, what the softmax needs
+        Tiles x;   // copying
+        Item y = first;   // making
         x.start(A, first);
-        do {
-            const int st = t % RAW, p0 = x.I.pos(x.i);
-            int z[2], r[2];
+        bool more = true;
+        int tc = 0, t = 0, i = 0;
+        auto copy = [&]() -> bool {
+            if (more) {
+                const int st = tc % RAW, p0 = x.I.pos(x.i);
+                if (tc >= RAW && !WW(emptyS(st), ((tc / RAW) & 1u) ^ 1u)) return false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) z[h] = x.head(h), r[h] = x.place(h);
-            if (t >= RAW && !WW(emptyS(st), ((t / RAW) & 1u) ^ 1u)) break;
+                for (int h = 0; h < 2; ++h) {
+                    const int z = x.head(h), r = x.place(h);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int j = lane + 32 * k;
-                    const bool in = z[h] >= 0 && p0 + 64 * h + j < x.I.v.end;
-                    const long long at = in ? static_cast<long long>(z[h]) * A.kv.page + r[h] + j : 0;
-                    cp_async4(smem_u32(&raw_k[st][64 * h + j]), A.k_scale + at, in);
-                    cp_async4(smem_u32(&raw_v[st][64 * h + j]), A.v_scale + at, in);
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = lane + 32 * k;
+                        const bool in = z >= 0 && p0 + 64 * h + j < x.I.v.end;
+                        const long long at = in ? static_cast<long long>(z) * A.kv.page + r + j : 0;
+                        cp_async4(smem_u32(&sc_k[st][64 * h + j]), A.k_scale + at, in);
+                        cp_async4(smem_u32(&sc_v[st][64 * h + j]), A.v_scale + at, in);
+                    }
                 }
-            cp_async_arrive(fullS(st));
+                ++tc;
+                more = x.step(A, it1);
+            }
+            cp_async_commit();   // a group per call, an empty one past the last tile
+            return true;
+        };
+        bool ok = true;
+        for (int k = 0; k < RAW - 2; ++k) ok = ok && copy();
+        while (ok && copy()) {
+            cp_async_wait<RAW - 2>();
+            const int st = t % RAW;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float vs = sc_v[st][lane + 32 * k];
+                const float vc = fminf(fmaxf(vs, 0x1p-40f), 0x1p60f);              // a NaN becomes 2^-40
+                sc_v[st][lane + 32 * k] = vs != vs ? vs : lg2_approx(vc);          // a NaN scale speaks through t_j alone
+                sc_i[st][lane + 32 * k] = __frcp_rn(vc);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fullS(st));
             ++t;
-        } while (x.step(A, it1));
+            if (++i == y.ntiles) {
+                i = 0;
+                if (!y.next(A, it1)) break;
+            }
+        }
         cp_async_wait_all();
-    } else if (warp == 10) {
+    } else if (warp == W_MMA) {
         // ---- MMAs
         if (lane == 0) {
             constexpr uint32_t IDS = idesc_f8(128, 2 * NR, false, false, false), IDO = idesc_f8(128, 2 * NR, true, true, true);
@@ -734,9 +766,9 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             mbar_wait(done, 0u, A.err);
         }
-    } else if (warp >= 4) {
+    } else if (warp >= W_OUT) {
         // ---- epilogue: thread = dim of O^T (tensor memory lane), modulo 128
-        const int d = tid - 128;
+        const int d = tid - 32 * W_OUT;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int t = 0, jl = 0;
         Item I = first;
@@ -744,14 +776,15 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
             const int tl = t + I.ntiles - 1;
             if (!WW(mlready, jl & 1u) || !WW(pfree(tl % PB), (tl / PB) & 1u)) break;
             tc_fence_after();
-            if (HD >= 128 || warp < 6) {
+            if (HD >= 128 || warp < W_OUT + 2) {
 #pragma unroll 1
                 for (int c = 0; c < S::MB * NR; c += 8) {
                     const int mb = c / NR, r0 = c % NR;
                     if (r0 >= I.v.rows) continue;
                     float a[8], b[8];
-                    tmem_ld8(tO + lane_off + mb * 2 * NR + r0, a);
-                    tmem_ld8(tO + lane_off + mb * 2 * NR + NR + r0, b);
+                    const uint32_t col = tO + lane_off + mb * 2 * NR + r0 / RW * 2 * RW + r0 % RW;
+                    tmem_ld8(col, a);
+                    tmem_ld8(col + RW, b);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -766,152 +799,146 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
             ++jl;
         } while (I.next(A, it1));
     } else {
-        // ---- softmax: thread = position of the tile (tensor memory lane).  A wait that gives up breaks
-        // no loop here, so that the four warps meet at the same barriers (later waits return at once)
-        const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+        // ---- softmax: thread = position of the tile (tensor memory lane), rows r_wg..  A wait that gives up
+        // breaks no loop here, so that the four warps meet at the same barriers (later waits return at once)
+        const int wg = warp >> 2, r_wg = wg * RW, pt = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t cS = tS + lane_off + r_wg, cO = tO + lane_off + 2 * r_wg;
         int t = 0, jl = 0, nq = 0;
-        long long at = 0;   // of row tid in the workspace, slot 0
+        long long at = 0;   // of row r_wg + pt in the workspace, slot 0
         bool fresh = true;
         Item I = first;
         W(qfirst, 0u);
         __syncwarp();
         for (;;) {
             if (fresh) {
-                const int gr = I.v.row_base + tid;
+                const int gr = I.v.row_base + r_wg + pt;
                 at = ((static_cast<long long>(I.b) * A.R + gr / A.G) * A.Hq + I.g * A.G + gr % A.G) * A.nslot;
             }
             if (fresh && jl > 0) {
-                // every S of the old Q is complete (this warp has seen the last), and the MMA warp
-                // issues none of this item until qfull
-                load_q<HD, NR, 128>(smem + S::Q_OFF, q_fac[(nq + 1) & 1], A, I, tid);
+                // every S of the old Q is complete (this warp has seen the last), and the MMA warp issues
+                // none of this item until qfull
+                load_q<HD, NR, 128 * WG>(smem + S::Q_OFF, q_fac[(nq + 1) & 1], A, I, tid);
                 fence_proxy_async_smem();
                 mbar_arrive(qfull);
                 WW(qfull, nq & 1u);   // the other warps' factors too
                 ++nq;
             }
-            const float* fac = q_fac[nq & 1];
-            float l[NR], m = NEG_INF;   // l of this thread's positions; m of row tid
+            const float* fac = q_fac[nq & 1] + r_wg;
+            float l[RW], m = NEG_INF;   // l of this thread's positions; m of row r_wg + pt
 #pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+            for (int r = 0; r < RW; ++r) l[r] = 0.f;
 #pragma unroll 1
             for (int i = 0; i < I.ntiles; ++i) {
-                const int tt = t + i, st = tt % RAW, p0 = I.pos(i), p = p0 + tid;
-                // row n / G of length L0 + n / G (n = row_base + r) sees p from r = r_lo on, and with a
-                // window to r_hi unless p is a sink
-                const long long lo64 = static_cast<long long>(p - I.v.L0 + 1) * A.G - I.v.row_base;
-                const long long hi64 = (static_cast<long long>(p) + A.window - I.v.L0 + 1) * A.G - I.v.row_base;
-                const int r_lo = p >= I.v.end ? NR : static_cast<int>(max(0ll, min(lo64, static_cast<long long>(NR))));
-                const int r_hi = !A.window || p < A.sinks ? NR : static_cast<int>(max(0ll, min(hi64, static_cast<long long>(NR))));
-                const bool whole = __all_sync(0xffffffffu, r_lo == 0 && r_hi == NR);
+                const int tt = t + i, st = tt % RAW, p0 = I.pos(i);
+                const bool whole = p0 >= I.v.from && p0 + T <= I.v.upto;
                 WW(fullS(st), (tt / RAW) & 1u);
-                const float ks = raw_k[st][tid], vs = raw_v[st][tid];
+                const float ks = sc_k[st][pt], lv = sc_v[st][pt], iv = sc_i[st][pt];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(emptyS(st));
-                const float vc = fminf(fmaxf(vs, 0x1p-40f), 0x1p60f);   // a NaN becomes 2^-40
-                const float lv = vs != vs ? vs : lg2_approx(vc);        // a NaN scale speaks through t_j alone
-                const float iv = __frcp_rn(vc);
                 WW(sbar(tt & 1), (tt >> 1) & 1u);
                 tc_fence_after();
-                float s[NR];   // t_j of the rows
+                float s[RW], lo[RW];   // t_j of the rows
+                if constexpr (RW == 16) {
+                    tmem_ld16(cS + (tt & 1) * 2 * NR, s);
+                    tmem_ld16(cS + (tt & 1) * 2 * NR + NR, lo);
+                } else {
+                    tmem_ld8(cS + (tt & 1) * 2 * NR, s);
+                    tmem_ld8(cS + (tt & 1) * 2 * NR + NR, lo);
+                }
+                tmem_ld_wait();
 #pragma unroll
-                for (int r0 = 0; r0 < NR; r0 += 16) {
-                    float lo[16];
-                    constexpr int TWO = 16;
-                    const int n = NR - r0 < TWO ? 8 : TWO;
-                    if (n == 16) {
-                        tmem_ld16(tS + lane_off + (tt & 1) * 2 * NR + r0, s + r0);
-                        tmem_ld16(tS + lane_off + (tt & 1) * 2 * NR + NR + r0, lo);
-                    } else {
-                        tmem_ld8(tS + lane_off + (tt & 1) * 2 * NR + r0, s + r0);
-                        tmem_ld8(tS + lane_off + (tt & 1) * 2 * NR + NR + r0, lo);
-                    }
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int k = 0; k < n; k += 4) {
-                        float* x = s + r0 + k;
-                        const float4 c = *reinterpret_cast<const float4*>(fac + r0 + k);
-                        add2(x[0], x[1], lo[k], lo[k + 1]);
-                        add2(x[2], x[3], lo[k + 2], lo[k + 3]);
-                        mul2(x[0], x[1], c.x, c.y);
-                        mul2(x[2], x[3], c.z, c.w);
-                        fma2(x[0], x[1], ks, ks, lv, lv);
-                        fma2(x[2], x[3], ks, ks, lv, lv);
-                    }
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 c = *reinterpret_cast<const float4*>(fac + r);
+                    float* x = s + r;
+                    add2(x[0], x[1], lo[r], lo[r + 1]);
+                    add2(x[2], x[3], lo[r + 2], lo[r + 3]);
+                    mul2(x[0], x[1], c.x, c.y);
+                    mul2(x[2], x[3], c.z, c.w);
+                    fma2(x[0], x[1], ks, ks, lv, lv);
+                    fma2(x[2], x[3], ks, ks, lv, lv);
                 }
                 if (!whole) {
+                    // row n / G of length L0 + n / G (n = row_base + r) sees p from r = r_lo on, and with a
+                    // window to r_hi unless p is a sink
+                    const int p = p0 + pt;
+                    const long long n0 = I.v.row_base + r_wg;
+                    const long long r_lo = p >= I.v.end ? RW : static_cast<long long>(p - I.v.L0 + 1) * A.G - n0;
+                    const long long r_hi = !A.window || p < A.sinks ? RW : (static_cast<long long>(p) + A.window - I.v.L0 + 1) * A.G - n0;
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
+                    for (int r = 0; r < RW; ++r)
                         if (r < r_lo || r >= r_hi) s[r] = NEG_INF;
+                    // V codes that were not loaded or lie behind every row: zeros, as 0 times their NaN is NaN
+                    const bool gap = p >= I.v.end || !I.v.half(p0 + (pt & 64));
+                    if (wg == 0 && __any_sync(0xffffffffu, gap)) {
+                        const int sv = tt % SV;
+                        WW(fullV(sv), (tt / SV) & 1u);
+                        if (gap) {
+#pragma unroll 1
+                            for (int c = 0; c < HD; c += 16)
+                                *reinterpret_cast<uint4*>(smem + S::V_OFF + sv * S::CODE + c / S::KROW * S::KBLK + pt * S::KROW +
+                                                          c % S::KROW) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
                 }
                 bool move = i == 0;
                 if (!move) {
                     float over = NEG_INF;
 #pragma unroll
-                    for (int r = 0; r < NR; r += 4) {
-                        const float4 mo = *reinterpret_cast<const float4*>(mo_sm + r);
+                    for (int r = 0; r < RW; r += 4) {
+                        const float4 mo = *reinterpret_cast<const float4*>(mo_sm + r_wg + r);
                         over = fmaxf(fmaxf(fmaxf(over, __fsub_rn(s[r], mo.x)), fmaxf(__fsub_rn(s[r + 1], mo.y), __fsub_rn(s[r + 2], mo.z))),
                                      __fsub_rn(s[r + 3], mo.w));
                     }
-                    move = softmax_any(over > P_SHIFT + RESCALE_SLACK);
+                    move = wg_any(1 + wg, over > P_SHIFT + RESCALE_SLACK);
                 }
                 if (move) {
 #pragma unroll
-                    for (int r = 0; r < NR; r += 4) {
+                    for (int r = 0; r < RW; r += 4) {
                         const float4 x = make_float4(warp_max(s[r]), warp_max(s[r + 1]), warp_max(s[r + 2]), warp_max(s[r + 3]));
-                        if (lane == 0) *reinterpret_cast<float4*>(&wmax[warp][r]) = x;
+                        if (lane == 0) *reinterpret_cast<float4*>(&wmax[warp & 3][r_wg + r]) = x;
                     }
-                    softmax_sync();
+                    wg_sync(1 + wg);
                     bool scaled = false;
-                    if (tid < NR) {
-                        const float mx = fmaxf(fmaxf(wmax[0][tid], wmax[1][tid]), fmaxf(wmax[2][tid], wmax[3][tid]));
+                    if (pt < RW) {
+                        const int r = r_wg + pt;
+                        const float mx = fmaxf(fmaxf(wmax[0][r], wmax[1][r]), fmaxf(wmax[2][r], wmax[3][r]));
                         const float old = m == NEG_INF ? DEAD : __fsub_rn(m, P_SHIFT);
                         float al = 1.f;
                         if (__fsub_rn(mx, old) > P_SHIFT + RESCALE_SLACK) {
                             if (m != NEG_INF) al = ex2_approx(__fsub_rn(m, mx));
                             m = mx;
                         }
-                        mo_sm[tid] = m == NEG_INF ? DEAD : __fsub_rn(m, P_SHIFT);
-                        al_sm[tid] = al;
+                        mo_sm[r] = m == NEG_INF ? DEAD : __fsub_rn(m, P_SHIFT);
+                        al_sm[r] = al;
                         scaled = al != 1.f;
                     }
-                    if (softmax_any(scaled)) {
+                    if (wg_any(1 + wg, scaled)) {
                         // O once P V of the tile before has completed
                         WW(pfree((tt - 1) % PB), ((tt - 1) / PB) & 1u);
                         tc_fence_after();
 #pragma unroll
-                        for (int r = 0; r < NR; ++r) l[r] = __fmul_rn(l[r], al_sm[r]);
+                        for (int r = 0; r < RW; ++r) l[r] = __fmul_rn(l[r], al_sm[r_wg + r]);
 #pragma unroll 1
-                        for (int c = 0; c < S::MB * 2 * NR; c += 8) {
+                        for (int c = 0; c < S::MB * 2 * RW; c += 8) {
+                            const uint32_t col = cO + c / (2 * RW) * 2 * NR + c % (2 * RW);
                             float o[8];
-                            tmem_ld8(tO + lane_off + c, o);
+                            tmem_ld8(col, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(o[e], al_sm[c % NR + e]);
-                            tmem_st8(tO + lane_off + c, o);
+                            for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(o[e], al_sm[r_wg + c % RW + e]);
+                            tmem_st8(col, o);
                         }
                         tmem_st_wait();
                     }
                 }
-                // V codes that were not loaded or lie behind every row: zeros, as 0 times their NaN is NaN
-                const bool gap = p >= I.v.end || !I.v.half(p0 + (tid & 64));
-                if (__any_sync(0xffffffffu, gap)) {
-                    const int sv = tt % SV;
-                    WW(fullV(sv), (tt / SV) & 1u);
-                    if (gap) {
-#pragma unroll
-                        for (int cb = 0; cb < S::KB; ++cb)
-#pragma unroll
-                            for (int c = 0; c < S::KROW; c += 16)
-                                *reinterpret_cast<uint4*>(smem + S::V_OFF + sv * S::CODE + cb * S::KBLK + tid * S::KROW + c) =
-                                    make_uint4(0, 0, 0, 0);
-                    }
-                }
                 if (tt >= PB) WW(pfree(tt % PB), ((tt / PB) & 1u) ^ 1u);
-                uint8_t* P = smem + S::P_OFF + (tt % PB) * 2 * S::PT + tid * 16;
-                uint32_t a[NR / 2], b[NR / 2];   // bytes of the rows: terms 1, then 3; 2, then 4
+                // a thread's bytes of N: per warpgroup [terms 1 | terms 3], and [terms 2 | terms 4]
+                uint8_t* P = smem + S::P_OFF + (tt % PB) * 2 * S::PT + wg * (RW / 8) * T * 16 + pt * 16;
+                uint32_t a[RW / 2], b[RW / 2];
 #pragma unroll
-                for (int r = 0; r < NR; r += 4) {
-                    const float4 mo = *reinterpret_cast<const float4*>(mo_sm + r);
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 mo = *reinterpret_cast<const float4*>(mo_sm + r_wg + r);
                     float* x = s + r;
                     add2(x[0], x[1], -mo.x, -mo.y);
                     add2(x[2], x[3], -mo.z, -mo.w);
@@ -920,17 +947,17 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
                     fma2_acc(l[r], l[r + 1], x[0], x[1], iv, iv);
                     fma2_acc(l[r + 2], l[r + 3], x[2], x[3], iv, iv);
                     uint32_t u = pack_f16x2(x[0], x[1]), v = pack_f16x2(x[2], x[3]);
-                    constexpr uint32_t TOP = 0xff00ff00u, UP = 0x54005400u;   // 64, twice
+                    constexpr uint32_t TOP = 0xff00ff00u, UP = 0x54005400u;   // LOW_SCALE, twice
                     a[r / 4] = __byte_perm(u, v, 0x7531);
                     u = sub_f16x2(u, u & TOP), v = sub_f16x2(v, v & TOP);
                     b[r / 4] = __byte_perm(u, v, 0x7531);
                     u = mul_f16x2(sub_f16x2(u, u & TOP), UP), v = mul_f16x2(sub_f16x2(v, v & TOP), UP);
-                    a[NR / 4 + r / 4] = __byte_perm(u, v, 0x7531);
+                    a[RW / 4 + r / 4] = __byte_perm(u, v, 0x7531);
                     u = sub_f16x2(u, u & TOP), v = sub_f16x2(v, v & TOP);
-                    b[NR / 4 + r / 4] = __byte_perm(u, v, 0x7531);
+                    b[RW / 4 + r / 4] = __byte_perm(u, v, 0x7531);
                 }
 #pragma unroll
-                for (int c = 0; c < NR / 8; ++c) {
+                for (int c = 0; c < RW / 8; ++c) {
                     *reinterpret_cast<uint4*>(P + c * T * 16) = make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
                     *reinterpret_cast<uint4*>(P + S::PT + c * T * 16) = make_uint4(b[4 * c], b[4 * c + 1], b[4 * c + 2], b[4 * c + 3]);
                 }
@@ -940,13 +967,12 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
             }
             // hand m and l to the epilogue warps (once they are done with the previous item's)
             if (jl > 0) WW(ofree, (jl - 1) & 1u);
-            int r0 = 0;
-            const int n = warp_sums<NR, 16>(l, lane, &r0);
-            // with 2^k rows the last lanes repeat sums, which is as well
+            int r0 = r_wg;
+            const int n = warp_sums<RW, 16>(l, lane, &r0);   // (lanes that hold the same sums write the same)
 #pragma unroll
-            for (int k = 0; k < NR; ++k)
-                if (k < n) l_sm[warp][r0 + k] = l[k];
-            if (tid < I.v.rows) m_sm[tid] = m, at_sm[tid] = at + I.slot;
+            for (int k = 0; k < RW; ++k)
+                if (k < n) l_sm[warp & 3][r0 + k] = l[k];
+            if (pt < RW && r_wg + pt < I.v.rows) m_sm[r_wg + pt] = m, at_sm[r_wg + pt] = at + I.slot;
             mbar_arrive(mlready);
             t += I.ntiles;
             ++jl;
@@ -957,7 +983,7 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NR>::PER_SM)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 10) {
+    if (warp == W_MMA) {
         tc_fence_after();
         tmem_dealloc(tS, S::TMEM_COLS);
     }
@@ -1093,7 +1119,7 @@ xv_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Ar
     if (n_items > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_q8: %lld work items", n_items);
     const int room = sms * S::PER_SM;
     trace_pre(s);
-    launch_k(attn_q8_kernel<HD, NR>, dim3(static_cast<unsigned>(std::min<long long>(room, n_items))), dim3(THREADS), S::SMEM, s, tmK, tmV, a);
+    launch_k(attn_q8_kernel<HD, NR>, dim3(static_cast<unsigned>(std::min<long long>(room, n_items))), dim3(S::THREADS), S::SMEM, s, tmK, tmV, a);
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq, seen = a.window && a.window < a.max_len ? a.window + a.sinks : a.max_len;
     return launched("attn_q8_kernel", s, K_ATTN_Q8, (2ll * HD + 8) * a.B * a.Hkv * seen + 2 * rows * HD + 4 * rows * a.nslot * (HD + 2));
 }
