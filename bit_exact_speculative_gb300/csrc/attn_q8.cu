@@ -34,7 +34,7 @@
 // Kernel 1 (attn_q8_kernel): work items (slot, row tile, kv head, sequence); a slot is a split, or
 // with a window one of the splits that the window and the sinks can touch.  One CTA per item where
 // all fit at once, else persistent CTAs that walk contiguous ranges of equal cost.  Kernel 2
-// (attn_q8_combine_kernel): one CTA per (row, q head) joins the row's splits.
+// (attn_q8_combine_kernel) joins each row's splits.
 #include <algorithm>
 #include <cmath>
 
@@ -52,7 +52,7 @@ constexpr float LOW_SCALE = 64.f;      // P's last two terms
 
 // Split boundaries: Q8_SHORT positions each below Q8_SWITCH, Q8_LONG beyond.
 constexpr int Q8_SHORT = 256, Q8_SWITCH = 4096, Q8_LONG = 1024;
-static_assert(Q8_SHORT % T == 0 && Q8_LONG <= 16 * T && Q8_SHORT <= Q8_LONG, "a lane per half tile of an item");
+static_assert(Q8_SHORT % T == 0 && Q8_LONG <= 8 * T && Q8_SHORT <= Q8_LONG, "a lane per half tile of an item");
 __host__ __device__ inline int q8_split_begin(int s) {
     constexpr int NS = Q8_SWITCH / Q8_SHORT;
     return s < NS ? s * Q8_SHORT : Q8_SWITCH + (s - NS) * Q8_LONG;
@@ -79,17 +79,18 @@ struct Shape {
     // softmax warpgroups of RW rows each: one thread's 48 rows took 3000 cycles a tile, and three times the code
     static constexpr int RW = NR % 16 ? 8 : 16, WG = NR / RW;
     static constexpr int THREADS = 128 * (WG + 2);
-    static constexpr int RAW = PER_SM == 2 ? 4 : 8;           // tiles of scales
-    static constexpr int STATIC = 3 * RAW * T * 4 + 15 * NR * 4 + 256;
+    static constexpr int RAW = PER_SM == 1 || NR == 8 ? 8 : 6;           // tiles of scales
+    static constexpr int ITEMS = 8;                           // items on their way
+    static constexpr int STATIC = 3 * RAW * T * 4 + 15 * NR * 4 + ITEMS * 208 + 64;
     static constexpr int ROOM = (PER_SM == 2 ? 233472 / 2 - 1024 : 232448) - STATIC - 1024 - 512 - Q - PB * 2 * PT;
     static constexpr int STAGES = ROOM / CODE;
-    static constexpr int SV = STAGES < 11 ? (STAGES + 1) / 2 : 6, SK = STAGES < 12 ? STAGES - SV : 6;
+    static constexpr int SV = STAGES < 10 ? (STAGES + 1) / 2 : 5, SK = STAGES < 10 ? STAGES - SV : 5;
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = Q_OFF + Q;
     static constexpr int V_OFF = K_OFF + SK * CODE;
     static constexpr int P_OFF = V_OFF + SV * CODE;
     static constexpr int BAR_OFF = P_OFF + PB * 2 * PT;
-    static constexpr int N_BARS = 2 * (SK + SV + RAW) + 4 + PB + 5;
+    static constexpr int N_BARS = 2 * (SK + SV + RAW + ITEMS) + 4 + PB + 4;
     static constexpr int SMEM = 1024 + BAR_OFF + 8 * N_BARS;
     static constexpr uint32_t O_COL = 4 * NR;                 // S twice, then O: MB blocks, each per warpgroup [terms 1, 2 | terms 3, 4]
     static constexpr int COLS = 4 * NR + MB * 2 * NR;
@@ -160,9 +161,7 @@ struct Sight {
 // Split of slot s, where the slots past the sinks' begin at split `first`.
 __device__ __forceinline__ int q8_slot_split(int s, int nsink, int first) { return s < nsink ? s : first + s - nsink; }
 
-// The work items of a CTA in order, those that see nothing left out.  Stepping divides by nothing but
-// powers of two: with the divisions of item -> (slot, row tile, head, sequence) in it, each warp's
-// step took 2000 cycles.
+// The work items of a CTA in order, those that see nothing left out.
 struct Item {
     int it, slot, rt, g, b, first;
     Sight v;
@@ -216,75 +215,72 @@ struct Item {
     __device__ __forceinline__ bool same_q(const Item& o) const { return b == o.b && g == o.g && rt == o.rt; }
 };
 
-// The items of persistent CTA c of n: equal shares of the cost.  All of the CTA's threads.
-template <int THREADS>
-__device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it01) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per = (A.B + THREADS - 1) / THREADS;
-    auto whole = [&](int b, int* one, int* tiles) {   // cost of sequence b, of a row tile of a head of it, live row tiles
-        Sight v;
-        v.of(A, b, 0);
-        *one = v.rows > 0 ? v.cost(1 << 24) : 0;
-        *tiles = v.rows > 0 ? (q8_rows(A.n_rows, b, A.R) * A.G + A.tile_rows - 1) / A.tile_rows : 0;
-        return static_cast<long long>(*one) * *tiles * A.Hkv;
-    };
-    int one, tiles;
-    long long mine = 0;
-    for (int b = tid * per; b < min(A.B, (tid + 1) * per); ++b) mine += whole(b, &one, &tiles);
-    __shared__ long long warp_sum[THREADS / 32];
-    long long incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    if (tid < 2) it01[tid] = A.nslot * A.nrt * A.Hkv * A.B;   // where no cost is left
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
-    }
-    // an item belongs to the CTA in whose share its cost begins
+// The items [it[0], it[1]) of persistent CTA c of n: equal shares of the cost.  One warp.
+__device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0, before = 0, at[2];
+    it[0] = it[1] = A.nslot * A.nrt * A.Hkv * A.B;   // where no cost is left
 #pragma unroll 1
-    for (int e = 0; e < 2; ++e) {
-        long long at = total * (c + e) / n - before;
-        if (at < 0 || at >= mine || mine == 0) continue;
-        int b = tid * per;
-        for (;; ++b) {
-            const long long x = whole(b, &one, &tiles);
-            if (at < x) break;
-            at -= x;
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int b0 = 0; b0 < A.B; b0 += 32) {
+            Sight v;
+            int one = 0, tiles = 0;   // cost of a row tile of a head, live row tiles
+            if (b0 + lane < A.B) v.of(A, b0 + lane, 0);
+            if (b0 + lane < A.B && v.rows > 0) {
+                one = v.cost(1 << 24);
+                tiles = v.rows < A.tile_rows ? 1 : (q8_rows(A.n_rows, b0 + lane, A.R) * A.G + A.tile_rows - 1) / A.tile_rows;
+            }
+            long long x = static_cast<long long>(one) * (tiles * A.Hkv);
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += o;
+            }
+            const long long all = __shfl_sync(0xffffffffu, x, 31);
+            if (pass == 0) {
+                total += all;
+                continue;
+            }
+            // an item belongs to the CTA in whose share its cost begins
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+                long long off = at[e] - before;
+                if (off < 0 || off >= all) continue;
+                const int own = __ffs(__ballot_sync(0xffffffffu, x > off)) - 1;
+                off -= own ? __shfl_sync(0xffffffffu, x, own - 1) : 0;
+                const int o1 = __shfl_sync(0xffffffffu, one, own), tl = __shfl_sync(0xffffffffu, tiles, own);
+                const int pair = static_cast<int>(off) / o1, in = static_cast<int>(off) - pair * o1;   // (head, row tile), cost in it
+                Sight w;
+                w.of(A, b0 + own, 0);
+                const int first = q8_first(w.L0, A.shift, A.nsink);
+                int slot = 0;   // the first whose cost begins at `in` or later
+#pragma unroll 1
+                for (int s = 0; s < A.nslot; s += 32) {
+                    const unsigned less = __ballot_sync(0xffffffffu, s + lane < A.nslot && w.cost(q8_slot_split(s + lane, A.nsink, first)) < in);
+                    slot += __popc(less);
+                    if (less != 0xffffffffu) break;
+                }
+                const int h = pair / tl;
+                it[e] = (((b0 + own) * A.Hkv + h) * A.nrt + pair - h * tl) * A.nslot + slot;
+            }
+            before += all;
         }
-        const int pair = static_cast<int>(at / one), off = static_cast<int>(at % one);   // (head, row tile), cost in it
-        Sight v;
-        v.of(A, b, 0);
-        const int first = q8_first(v.L0, A.shift, A.nsink);
-        int lo = 0, hi = A.nslot;   // the first slot whose cost begins at `off` or later
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (v.cost(q8_slot_split(mid, A.nsink, first)) >= off) hi = mid;
-            else lo = mid + 1;
-        }
-        it01[e] = ((b * A.Hkv + pair / tiles) * A.nrt + pair % tiles) * A.nslot + lo;
+        at[0] = total * c / n;
+        at[1] = total * (c + 1) / n;
     }
-    __syncthreads();
 }
 
-__device__ __forceinline__ int q8_page(const KvPages& kv, int b, int p, int* row, unsigned* err) {
-    if (!kv.table) {
-        *row = p;
-        return b;
-    }
-    const int j = p / kv.page;
-    *row = p - j * kv.page;
-    int pg = kv.table[static_cast<long long>(b) * kv.max_pages + j];
-    if (pg < 0 || pg >= kv.n_pages) {
-        atomicOr(err, ERR_BAD_PAGE);
-        pg = 0;
-    }
-    return pg;
-}
+// An item as the CTA's warps get it.
+struct Work {
+    int ntiles, p_begin, head, skip, slot;   // ntiles = 0: no more items
+    int fresh, pre;                          // its Q is another than the last item's; the next item's is the same
+    int b, g;
+    Sight v;
+    int z[16], row[16];   // half h of tile i at 2 i + h: head of the pools, row in it; z < 0 where no row sees it
+    __device__ __forceinline__ int pos(int i) const { return p_begin + (i < head ? i : i + skip) * T; }
+};
+static_assert(sizeof(Work) <= 208, "");
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -322,7 +318,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // [128, 256)) in swizzled blocks, and fac[row] = sl2 2^-e; the rows behind them become 0.
 // NT threads (whole warps) from t0.
 template <int HD, int NR, int NT>
-__device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A, const Item& I, int t0) {
+__device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A, const Work& I, int t0) {
     using S = Shape<HD, NR>;
     constexpr int LPH = HD / 8, RPP = NT / LPH, UN = (NR + RPP - 1) / RPP < 4 ? (NR + RPP - 1) / RPP : 4;
     const int n = I.v.rows, c = t0 % LPH;
@@ -474,6 +470,19 @@ __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
     asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
 }
+// L2 policy of lines read once, or of any.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+    uint64_t p;
+    if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+        : "memory");
+}
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -514,55 +523,31 @@ __device__ __forceinline__ int warp_sums(float* v, int lane, int* first) {
     }
 }
 
-// The tiles of a CTA's items in order.  A whole warp steps, and lane 2 i + h looks up where half h of
-// tile i of an item lies, so that a page table's latency is met once per item.
-struct Tiles {
-    Item I;
-    int i;           // the next tile of the item
-    int z, row;      // lane 2 i + h: head of the pools and row in it; z < 0 where no row sees the half
-    __device__ __forceinline__ void look(const Q8Args& A) {
-        const int lane = threadIdx.x & 31, p = I.pos(lane >> 1) + 64 * (lane & 1);
-        z = -1, row = 0;
-        if (lane < 2 * I.ntiles && I.v.half(p)) z = q8_page(A.kv, I.b, p, &row, A.err) * A.Hkv + I.g;
-    }
-    __device__ __forceinline__ void start(const Q8Args& A, const Item& first) {
-        I = first;
-        i = 0;
-        look(A);
-    }
-    // steps to the next tile; false past the last
-    __device__ __forceinline__ bool step(const Q8Args& A, int it1) {
-        if (++i < I.ntiles) return true;
-        i = 0;
-        if (!I.next(A, it1)) return false;
-        look(A);
-        return true;
-    }
-    __device__ __forceinline__ int head(int h) const { return __shfl_sync(0xffffffffu, z, 2 * i + h); }
-    __device__ __forceinline__ int place(int h) const { return __shfl_sync(0xffffffffu, row, 2 * i + h); }
-};
-
 // Warps of a CTA and what they do per tile t (counted over the CTA's items):
 //   0..4 WG - 1   softmax, warpgroup w for rows RW w.., a thread per position: S out of tensor memory,
 //          t_j, mask; the references stand unless some row's t_j passes its by RESCALE_SLACK (or the
 //          tile is an item's first): then the tile's maxima are found, and references, l and O moved;
 //          P to shared memory, l per thread
 //   then 4 an item's O, m and l to the workspace, while the next item's first tiles run
-//   2      TMA of the K and V codes into their rings
+//   1      TMA of the K and V codes into their rings
 //   1      MMAs: S(t + 1) = K Q^T, then O += V^T P(t); the S that overwrites S(t - 1) is issued after
 //          the P V of that tile, whose P was made of it
 //   1      the positions' scales: ks, log2(vs) and 1 / vs into a ring
+//   1      the items, with their pages looked up, for all the others.  (With every warp stepping through
+//          the items itself the code outgrew the instruction caches: 113 KB, and 20 cycles an instruction.)
 template <int HD, int NR>
 __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args A) {
     griddep_launch();
     using S = Shape<HD, NR>;
     constexpr int SK = S::SK, SV = S::SV, RAW = S::RAW, PB = S::PB, RW = S::RW, WG = S::WG;
-    constexpr int W_OUT = 4 * WG, W_K = W_OUT + 4, W_V = W_K + 1, W_MMA = W_K + 2, W_SC = W_K + 3;   // warps
+    constexpr int IT = S::ITEMS;
+    constexpr int W_OUT = 4 * WG, W_TMA = W_OUT + 4, W_MMA = W_TMA + 1, W_SC = W_TMA + 2, W_IT = W_TMA + 3;   // warps
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float sc_k[RAW][T], sc_v[RAW][T], sc_i[RAW][T];
     __shared__ __align__(16) float q_fac[2][NR], mo_sm[NR], al_sm[NR], wmax[4][NR], l_sm[4][NR], m_sm[NR];
     __shared__ long long at_sm[NR];
+    __shared__ Work items[IT];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort;
     const uint32_t rawb = smem_u32(smem_raw);
@@ -584,39 +569,24 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     auto pready = [&](int j) { return bx + 8u * (2 + j); };    // its P is in shared memory, its S has been read
     auto pfree = [&](int j) { return bx + 8u * (4 + j); };     // its P V is complete
     const uint32_t by = bx + 8u * (4 + PB);
-    const uint32_t done = by, ofree = by + 8, qfull = by + 16, mlready = by + 24, qfirst = by + 32;
+    const uint32_t done = by, ofree = by + 8, qready = by + 16, mlready = by + 24, bi = by + 32;
+    auto fullI = [&](int n) { return bi + 8u * (n % IT); };
+    auto emptyI = [&](int n) { return bi + 8u * (IT + n % IT); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n_items = A.nslot * A.nrt * A.Hkv * A.B;
-    const int per_slot = n_items / A.nslot;
-    const bool multi = static_cast<int>(gridDim.x) < n_items;
-    griddep_wait();
-    for (int b = blockIdx.x + gridDim.x * tid; b < A.B; b += gridDim.x * S::THREADS) {
-        const int raw = A.n_rows ? A.n_rows[b] : A.R, nr = min(max(raw, 0), A.R), L0 = A.ctx_len[b];
-        if (raw != nr) atomicOr(A.err, ERR_BAD_COUNT);
-        if (nr > 0 && (L0 < 1 || L0 > A.max_len - nr + 1)) atomicOr(A.err, ERR_BAD_LENGTH);
-    }
-    // one item per CTA: slots slowest, so that a row's last splits, often short, come last
-    __shared__ int it01[2];
-    if (multi) q8_range<S::THREADS>(A, blockIdx.x, gridDim.x, it01);
-    const int it0 = multi ? it01[0] : (static_cast<int>(blockIdx.x) % per_slot) * A.nslot + static_cast<int>(blockIdx.x) / per_slot;
-    const int it1 = multi ? it01[1] : it0 + 1;
-    Item first;
-    if (!first.open(A, it0, it1)) return;   // nothing live here: no barrier or tensor memory was set up
-
-    if (tid == 32 * W_K) {
+    if (tid == 32 * W_TMA) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         for (int st = 0; st < SK; ++st) mbar_init(fullK(st), 1), mbar_init(emptyK(st), 1);
         for (int st = 0; st < SV; ++st) mbar_init(fullV(st), 1), mbar_init(emptyV(st), 1);
         for (int st = 0; st < RAW; ++st) mbar_init(fullS(st), 1), mbar_init(emptyS(st), 4 * WG);
+        for (int st = 0; st < IT; ++st) mbar_init(fullI(st), 1), mbar_init(emptyI(st), 4 * WG + 7);
         for (int j = 0; j < 2; ++j) mbar_init(sbar(j), 1), mbar_init(pready(j), 128 * WG);
         for (int j = 0; j < PB; ++j) mbar_init(pfree(j), 1);
         mbar_init(done, 1);
         mbar_init(ofree, 128);
-        mbar_init(qfull, 128 * WG);
+        mbar_init(qready, 128 * WG);
         mbar_init(mlready, 128 * WG);
-        mbar_init(qfirst, 128 * (WG + 1));
         fence_mbar_init();
         s_abort = 0;
     }
@@ -628,76 +598,116 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = tmem_slot, tO = tS + S::O_COL;
-    // softmax and epilogue warps load the first item's Q; the softmax warps reload it when an item's differs
-    if (warp < W_K) {
-        load_q<HD, NR, 128 * (WG + 1)>(smem + S::Q_OFF, q_fac[0], A, first, tid);
-        fence_proxy_async_smem();
-        mbar_arrive(qfirst);
-    }
+    griddep_wait();
 
     auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || wait_slow(bar, par, &s_abort, A.err); };
     // the same verdict for every lane of a warp
     auto WW = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, W(bar, par)); };
+    // the n-th item is there, and is not the end
+    auto item = [&](int n) -> bool { return WW(fullI(n), (n / IT) & 1u) && items[n % IT].ntiles > 0; };
+    // the warp has no more use for it
+    auto item_done = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(emptyI(n));
+    };
 
-    if (warp == W_K || warp == W_V) {
-        // ---- TMA
-        const bool isK = warp == W_K;
-        const int NS = isK ? SK : SV;
-        const CUtensorMap* map = isK ? &tmK : &tmV;
-        int t = 0;
-        Tiles x;
-        x.start(A, first);
-        do {
-            const int st = t % NS, z0 = x.head(0), z1 = x.head(1), r0 = x.place(0), r1 = x.place(1);
-            if (t >= NS && !WW(isK ? emptyK(st) : emptyV(st), ((t / NS) & 1u) ^ 1u)) break;
-            if (lane == 0) {
-                const uint32_t fb = isK ? fullK(st) : fullV(st), dst = isK ? sK(st) : sV(st);
-                mbar_arrive_expect_tx(fb, (z0 >= 0 ? S::CODE / 2 : 0) + (z1 >= 0 ? S::CODE / 2 : 0));
-#pragma unroll
-                for (int cb = 0; cb < S::KB; ++cb) {
-                    if (z0 >= 0) tma_load_3d(dst + cb * S::KBLK, map, cb * S::KROW, r0, z0, fb);
-                    if (z1 >= 0) tma_load_3d(dst + cb * S::KBLK + S::KBLK / 2, map, cb * S::KROW, r1, z1, fb);
+    if (warp == W_IT) {
+        // ---- items
+        const int n_items = A.nslot * A.nrt * A.Hkv * A.B, per_slot = n_items / A.nslot;
+        // one item per CTA: slots slowest, so that a row's last splits, often short, come last
+        int it[2] = {static_cast<int>(blockIdx.x) % per_slot * A.nslot + static_cast<int>(blockIdx.x) / per_slot, 0};
+        it[1] = it[0] + 1;
+        if (static_cast<int>(gridDim.x) < n_items) q8_range(A, blockIdx.x, gridDim.x, it);
+        Item I;
+        bool more = I.open(A, it[0], it[1]), fresh = true;
+        for (int n = 0;; ++n) {
+            if (n >= IT && !WW(emptyI(n), ((n / IT) & 1u) ^ 1u)) break;
+            Work& w = items[n % IT];
+            if (!more) {
+                if (lane == 0) {
+                    w.ntiles = 0;
+                    mbar_arrive(fullI(n));
                 }
+                break;
             }
-            ++t;
-        } while (x.step(A, it1));
+            const int p = I.pos(lane >> 1) + 64 * (lane & 1);
+            int z = -1, row = p;
+            if (lane < 2 * I.ntiles && I.v.half(p)) {
+                int page = I.b;
+                if (A.kv.table) {
+                    const int j = p / A.kv.page;
+                    row = p - j * A.kv.page;
+                    page = A.kv.table[static_cast<long long>(I.b) * A.kv.max_pages + j];
+                    if (page < 0 || page >= A.kv.n_pages) {
+                        atomicOr(A.err, ERR_BAD_PAGE);
+                        page = 0;
+                    }
+                }
+                z = page * A.Hkv + I.g;
+            }
+            if (lane < 16) w.z[lane] = z, w.row[lane] = row;
+            if (lane == 0) {
+                w.ntiles = I.ntiles, w.p_begin = I.p_begin, w.head = I.head, w.skip = I.skip, w.slot = I.slot;
+                w.b = I.b, w.g = I.g, w.v = I.v;
+            }
+            const Item was = I;
+            more = I.next(A, it[1]);
+            const bool pre = more && I.same_q(was);
+            if (lane == 0) w.fresh = fresh, w.pre = pre;
+            fresh = !pre;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fullI(n));
+        }
+        // lengths and counts outside their range see nothing, and are recorded
+        for (int b = blockIdx.x + gridDim.x * lane; b < A.B; b += gridDim.x * 32) {
+            const int raw = A.n_rows ? A.n_rows[b] : A.R, nr = min(max(raw, 0), A.R), L0 = A.ctx_len[b];
+            if (raw != nr) atomicOr(A.err, ERR_BAD_COUNT);
+            if (nr > 0 && (L0 < 1 || L0 > A.max_len - nr + 1)) atomicOr(A.err, ERR_BAD_LENGTH);
+        }
+    } else if (warp == W_TMA) {
+        // ---- TMA: K before V of a tile, the order in which their stages come free
+        // (codes that one row tile reads once are the first to leave L2, and the partial results stay)
+        const uint64_t policy = l2_policy(A.nrt == 1);
+        int t = 0;
+        for (int n = 0; item(n); ++n) {
+            const Work& w = items[n % IT];
+            const int nt = w.ntiles;
+            bool ok = true;
+            for (int i = 0; ok && i < nt; ++i, ++t) {
+#pragma unroll 1
+                for (int side = 0; ok && side < 2; ++side) {
+                    const int NS = side ? SV : SK, st = t % NS;
+                    const uint32_t fb = side ? fullV(st) : fullK(st), dst0 = side ? sV(st) : sK(st);
+                    if (t >= NS) ok = WW(side ? emptyV(st) : emptyK(st), ((t / NS) & 1u) ^ 1u);
+                    if (ok && lane == 0) {
+                        const CUtensorMap* map = side ? &tmV : &tmK;
+                        const int z0 = w.z[2 * i], z1 = w.z[2 * i + 1];
+                        mbar_arrive_expect_tx(fb, (z0 >= 0 ? S::CODE / 2 : 0) + (z1 >= 0 ? S::CODE / 2 : 0));
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int z = h ? z1 : z0, row = w.row[2 * i + h];
+                            if (z < 0) continue;
+#pragma unroll
+                            for (int cb = 0; cb < S::KB; ++cb)
+                                tma_load_3d_hint(dst0 + cb * S::KBLK + h * S::KBLK / 2, map, cb * S::KROW, row, z, fb, policy);
+                        }
+                    }
+                    // a stage that will not be filled ends the loads; what has been issued is waited for
+                }
+                if (!ok) break;
+            }
+            item_done(n);
+            if (!ok) break;
+        }
         // every issued copy lands before the CTA may leave
-        for (int j = t > NS ? t - NS : 0; j < t; ++j) mbar_wait(isK ? fullK(j % NS) : fullV(j % NS), (j / NS) & 1u, A.err);
+        for (int j = t > SK ? t - SK : 0; j < t; ++j) mbar_wait(fullK(j % SK), (j / SK) & 1u, A.err);
+        for (int j = t > SV ? t - SV : 0; j < t; ++j) mbar_wait(fullV(j % SV), (j / SV) & 1u, A.err);
     } else if (warp == W_SC) {
         // ---- scales: every lane copies those of its four positions RAW - 2 tiles ahead, and makes of them,
         // in their place, what the softmax needs
-        Tiles x;   // copying
-        Item y = first;   // making
-        x.start(A, first);
-        bool more = true;
-        int tc = 0, t = 0, i = 0;
-        auto copy = [&]() -> bool {
-            if (more) {
-                const int st = tc % RAW, p0 = x.I.pos(x.i);
-                if (tc >= RAW && !WW(emptyS(st), ((tc / RAW) & 1u) ^ 1u)) return false;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int z = x.head(h), r = x.place(h);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int j = lane + 32 * k;
-                        const bool in = z >= 0 && p0 + 64 * h + j < x.I.v.end;
-                        const long long at = in ? static_cast<long long>(z) * A.kv.page + r + j : 0;
-                        cp_async4(smem_u32(&sc_k[st][64 * h + j]), A.k_scale + at, in);
-                        cp_async4(smem_u32(&sc_v[st][64 * h + j]), A.v_scale + at, in);
-                    }
-                }
-                ++tc;
-                more = x.step(A, it1);
-            }
-            cp_async_commit();   // a group per call, an empty one past the last tile
-            return true;
-        };
-        bool ok = true;
-        for (int k = 0; k < RAW - 2; ++k) ok = ok && copy();
-        while (ok && copy()) {
-            cp_async_wait<RAW - 2>();
-            const int st = t % RAW;
+        int t = 0;   // tiles copied
+        auto make = [&](int m) {
+            const int st = m % RAW;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float vs = sc_v[st][lane + 32 * k];
@@ -707,10 +717,42 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(fullS(st));
-            ++t;
-            if (++i == y.ntiles) {
+        };
+        bool ok = true, live = true;
+        int m = 0, n = 0, i = 0, nt = 0;
+        // (one loop for the copies ahead, for both, and for what is left to make)
+        while (ok && (live || m < t)) {
+            if (live && i == nt) {
+                if (nt) item_done(n++);
+                live = item(n);
                 i = 0;
-                if (!y.next(A, it1)) break;
+                nt = live ? items[n % IT].ntiles : 0;
+            }
+            if (live) {
+                const Work& w = items[n % IT];
+                const int st = t % RAW, left = w.v.end - w.pos(i);
+                ok = t < RAW || WW(emptyS(st), ((t / RAW) & 1u) ^ 1u);
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int z = w.z[2 * i + h];
+                    const long long at = static_cast<long long>(z) * A.kv.page + w.row[2 * i + h];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = lane + 32 * k;
+                        const bool in = z >= 0 && 64 * h + j < left;
+                        cp_async4(smem_u32(&sc_k[st][64 * h + j]), A.k_scale + (in ? at + j : 0), in);
+                        cp_async4(smem_u32(&sc_v[st][64 * h + j]), A.v_scale + (in ? at + j : 0), in);
+                    }
+                }
+                ++t;
+                ++i;
+            }
+            cp_async_commit();   // a group per round, an empty one past the last tile
+            if (t - m > RAW - 2 || !live) {
+                cp_async_wait<RAW - 2>();
+                if (!live) cp_async_wait_all();
+                make(m++);
             }
         }
         cp_async_wait_all();
@@ -732,18 +774,19 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
                 tc_commit(emptyK(st));
                 return true;
             };
-            int t = 0, jl = 0, nq = 0;
-            bool ok = W(qfirst, 0u), more = true, pre = false;   // pre: this item's first S went out with the last item
-            Item I = first;
-            while (ok && more) {
-                if (!pre && !qk(t)) break;
-                Item nx = I;
-                more = nx.next(A, it1);
-                pre = more && nx.same_q(I);   // the next item has this Q: its first S goes out before the last P V
-                for (int i = 0; i < I.ntiles; ++i) {
+            int t = 0, nq = 0;
+            bool ok = true;
+            for (int n = 0; ok && W(fullI(n), (n / IT) & 1u); ++n) {
+                const int nt = items[n % IT].ntiles;
+                const bool fresh = items[n % IT].fresh, pre = items[n % IT].pre;
+                mbar_arrive(emptyI(n));
+                if (!nt) break;
+                // with the last item's Q, this one's first S went out before the last P V
+                if (fresh && (!W(qready, nq++ & 1u) || !qk(t))) break;
+                for (int i = 0; i < nt; ++i) {
                     const int tt = t + i, sv = tt % SV;
-                    if ((i + 1 < I.ntiles || pre) && !qk(tt + 1)) { ok = false; break; }
-                    if (i == 0 && jl > 0 && !W(ofree, (jl - 1) & 1u)) { ok = false; break; }
+                    if ((i + 1 < nt || pre) && !qk(tt + 1)) { ok = false; break; }
+                    if (i == 0 && n > 0 && !W(ofree, (n - 1) & 1u)) { ok = false; break; }
                     if (!W(fullV(sv), (tt / SV) & 1u) || !W(pready(tt & 1), (tt >> 1) & 1u)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sP = base + S::P_OFF + (tt % PB) * 2 * S::PT;
@@ -758,10 +801,7 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
                     tc_commit(pfree(tt % PB));
                     tc_commit(emptyV(sv));
                 }
-                t += I.ntiles;
-                ++jl;
-                if (more && !pre && !W(qfull, nq++ & 1u)) break;
-                I = nx;
+                t += nt;
             }
             tc_commit(done);   // every MMA issued is complete before the CTA may leave
             mbar_wait(done, 0u, A.err);
@@ -770,17 +810,18 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
         // ---- epilogue: thread = dim of O^T (tensor memory lane), modulo 128
         const int d = tid - 32 * W_OUT;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        int t = 0, jl = 0;
-        Item I = first;
-        do {
-            const int tl = t + I.ntiles - 1;
-            if (!WW(mlready, jl & 1u) || !WW(pfree(tl % PB), (tl / PB) & 1u)) break;
+        int t = 0;
+        for (int n = 0; item(n); ++n) {
+            t += items[n % IT].ntiles;
+            const int rows = items[n % IT].v.rows, tl = t - 1;
+            item_done(n);
+            if (!WW(mlready, n & 1u) || !WW(pfree(tl % PB), (tl / PB) & 1u)) break;
             tc_fence_after();
             if (HD >= 128 || warp < W_OUT + 2) {
 #pragma unroll 1
                 for (int c = 0; c < S::MB * NR; c += 8) {
                     const int mb = c / NR, r0 = c % NR;
-                    if (r0 >= I.v.rows) continue;
+                    if (r0 >= rows) continue;
                     float a[8], b[8];
                     const uint32_t col = tO + lane_off + mb * 2 * NR + r0 / RW * 2 * RW + r0 % RW;
                     tmem_ld8(col, a);
@@ -788,48 +829,43 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (r0 + e < I.v.rows) A.opart[at_sm[r0 + e] * HD + mb * 128 + d] = __fmaf_rn(b[e], 1.f / LOW_SCALE, a[e]);
+                        if (r0 + e < rows) A.opart[at_sm[r0 + e] * HD + mb * 128 + d] = __fmaf_rn(b[e], 1.f / LOW_SCALE, a[e]);
                 }
             }
-            if (d < I.v.rows)
+            if (d < rows)
                 A.ml[at_sm[d]] = make_float2(m_sm[d], __fadd_rn(__fadd_rn(l_sm[0][d], l_sm[1][d]), __fadd_rn(l_sm[2][d], l_sm[3][d])));
             tc_fence_before();
             mbar_arrive(ofree);   // O, m and l may be overwritten by the next item
-            t += I.ntiles;
-            ++jl;
-        } while (I.next(A, it1));
+        }
     } else {
         // ---- softmax: thread = position of the tile (tensor memory lane), rows r_wg..  A wait that gives up
         // breaks no loop here, so that the four warps meet at the same barriers (later waits return at once)
         const int wg = warp >> 2, r_wg = wg * RW, pt = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t cS = tS + lane_off + r_wg, cO = tO + lane_off + 2 * r_wg;
-        int t = 0, jl = 0, nq = 0;
+        int t = 0, nq = 0;
         long long at = 0;   // of row r_wg + pt in the workspace, slot 0
-        bool fresh = true;
-        Item I = first;
-        W(qfirst, 0u);
-        __syncwarp();
-        for (;;) {
-            if (fresh) {
-                const int gr = I.v.row_base + r_wg + pt;
-                at = ((static_cast<long long>(I.b) * A.R + gr / A.G) * A.Hq + I.g * A.G + gr % A.G) * A.nslot;
-            }
-            if (fresh && jl > 0) {
+        for (int n = 0;; ++n) {
+            if (wg_any(1 + wg, !item(n))) break;
+            const Work& I = items[n % IT];
+            if (I.fresh) {
                 // every S of the old Q is complete (this warp has seen the last), and the MMA warp issues
-                // none of this item until qfull
+                // none of this item until qready
                 load_q<HD, NR, 128 * WG>(smem + S::Q_OFF, q_fac[(nq + 1) & 1], A, I, tid);
                 fence_proxy_async_smem();
-                mbar_arrive(qfull);
-                WW(qfull, nq & 1u);   // the other warps' factors too
+                mbar_arrive(qready);
+                const int gr = I.v.row_base + r_wg + pt, r = gr / A.G;
+                at = ((static_cast<long long>(I.b) * A.R + r) * A.Hq + I.g * A.G + gr - r * A.G) * A.nslot;
+                WW(qready, nq & 1u);   // the other warps' factors too
                 ++nq;
             }
+            const int nt = I.ntiles;
             const float* fac = q_fac[nq & 1] + r_wg;
             float l[RW], m = NEG_INF;   // l of this thread's positions; m of row r_wg + pt
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
 #pragma unroll 1
-            for (int i = 0; i < I.ntiles; ++i) {
+            for (int i = 0; i < nt; ++i) {
                 const int tt = t + i, st = tt % RAW, p0 = I.pos(i);
                 const bool whole = p0 >= I.v.from && p0 + T <= I.v.upto;
                 WW(fullS(st), (tt / RAW) & 1u);
@@ -966,19 +1002,16 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
                 mbar_arrive(pready(tt & 1));
             }
             // hand m and l to the epilogue warps (once they are done with the previous item's)
-            if (jl > 0) WW(ofree, (jl - 1) & 1u);
+            if (n > 0) WW(ofree, (n - 1) & 1u);
             int r0 = r_wg;
-            const int n = warp_sums<RW, 16>(l, lane, &r0);   // (lanes that hold the same sums write the same)
+            const int ns = warp_sums<RW, 16>(l, lane, &r0);   // (lanes that hold the same sums write the same)
 #pragma unroll
             for (int k = 0; k < RW; ++k)
-                if (k < n) l_sm[warp & 3][r0 + k] = l[k];
+                if (k < ns) l_sm[warp & 3][r0 + k] = l[k];
             if (pt < RW && r_wg + pt < I.v.rows) m_sm[r_wg + pt] = m, at_sm[r_wg + pt] = at + I.slot;
             mbar_arrive(mlready);
-            t += I.ntiles;
-            ++jl;
-            const Item was = I;
-            if (!I.next(A, it1)) break;
-            fresh = !I.same_q(was);
+            item_done(n);
+            t += nt;
         }
     }
     tc_fence_before();
@@ -1002,23 +1035,21 @@ struct CombineArgs {
 };
 
 // One CTA per (row, q head): w_s = 2^(m_s - M) over the row's live slots s in order, out = sum w_s O_s /
-// sum w_s l_s.  CB_GROUPS groups of threads each add the slots of one residue, then the groups'
-// sums are added in order: fixed by the row alone, and a long context's partials (140 splits at
-// 131072) come in CB_GROUPS times fewer dependent steps.
-constexpr int CB_GROUPS = 8;
+// sum w_s l_s.  256 threads: 4 hd / 64 groups of threads each add the slots of one residue, then the
+// groups' sums are added in order: fixed by the row alone.
+constexpr int CB_THREADS = 256;
 constexpr int CB_SLOTS = 1 << 10;   // slots whose weights are staged at a time
 
 template <int HD>
-__global__ void __launch_bounds__(CB_GROUPS* HD / 4) attn_q8_combine_kernel(const __grid_constant__ CombineArgs C) {
+__global__ void __launch_bounds__(CB_THREADS) attn_q8_combine_kernel(const __grid_constant__ CombineArgs C) {
     griddep_launch();
     griddep_wait();
-    constexpr int LN = HD / 4, NT = CB_GROUPS * LN;
+    constexpr int CB_LANES = HD / 4, CB_GROUPS = CB_THREADS / CB_LANES;
     __shared__ float2 wl[CB_SLOTS];
-    __shared__ float4 acc_sm[CB_GROUPS][LN];
-    __shared__ float l_sm[CB_GROUPS], wmax[NT / 32];
-    const int hq = blockIdx.x % C.Hq;
-    const long long br = blockIdx.x / C.Hq;
-    const int b = static_cast<int>(br / C.R), r = static_cast<int>(br % C.R), tid = threadIdx.x;
+    __shared__ float4 acc_sm[CB_GROUPS][CB_LANES];
+    __shared__ float l_sm[CB_GROUPS], wmax[CB_THREADS / 32];
+    const int row = blockIdx.x, hq = row % C.Hq, b = row / C.Hq / C.R, r = row / C.Hq % C.R, tid = threadIdx.x;
+    const long long br = row / C.Hq;
     const int nr = q8_rows(C.n_rows, b, C.R), L0 = C.ctx_len[b];
     if (r >= nr || L0 < 1 || L0 > C.max_len - nr + 1) return;
     const int len = L0 + r;
@@ -1033,20 +1064,20 @@ __global__ void __launch_bounds__(CB_GROUPS* HD / 4) attn_q8_combine_kernel(cons
     };
     const long long idx0 = (br * C.Hq + hq) * C.nslot;
     float M = NEG_INF;
-    for (int i = tid; i < ns; i += NT) M = fmaxf(M, C.ml[idx0 + slot(i)].x);
+    for (int i = tid; i < ns; i += CB_THREADS) M = fmaxf(M, C.ml[idx0 + slot(i)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     if ((tid & 31) == 0) wmax[tid >> 5] = M;
     __syncthreads();
     M = wmax[0];
-    for (int w = 1; w < NT / 32; ++w) M = fmaxf(M, wmax[w]);
-    const int grp = tid / LN, ln = tid % LN;
+    for (int w = 1; w < CB_THREADS / 32; ++w) M = fmaxf(M, wmax[w]);
+    const int grp = tid / CB_LANES, ln = tid % CB_LANES, dim = 4 * ln;
     float L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = 0; c0 < ns; c0 += CB_SLOTS) {
         const int n = min(CB_SLOTS, ns - c0);
         __syncthreads();
-        for (int i = tid; i < n; i += NT) {
+        for (int i = tid; i < n; i += CB_THREADS) {
             const float2 v = C.ml[idx0 + slot(c0 + i)];
             wl[i] = make_float2(exp2f(__fsub_rn(v.x, M)), v.y);
         }
@@ -1054,7 +1085,7 @@ __global__ void __launch_bounds__(CB_GROUPS* HD / 4) attn_q8_combine_kernel(cons
 #pragma unroll 4
         for (int i = grp; i < n; i += CB_GROUPS) {
             const float2 w = wl[i];
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(C.opart + (idx0 + slot(c0 + i)) * HD) + ln);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(C.opart + (idx0 + slot(c0 + i)) * HD + dim));
             L = __fmaf_rn(w.x, w.y, L);
             a.x = __fmaf_rn(w.x, o.x, a.x);
             a.y = __fmaf_rn(w.x, o.y, a.y);
@@ -1075,13 +1106,13 @@ __global__ void __launch_bounds__(CB_GROUPS* HD / 4) attn_q8_combine_kernel(cons
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = __fadd_rn(__fdiv_rn(y[e], L), 0.f);
     if (C.gate) {
-        const uint2 g = *reinterpret_cast<const uint2*>(C.gate + br * C.gate_stride + static_cast<long long>(hq) * HD + 4 * ln);
+        const uint2 g = *reinterpret_cast<const uint2*>(C.gate + br * C.gate_stride + static_cast<long long>(hq) * HD + dim);
         const float gv[4] = {__uint_as_float(g.x << 16), __uint_as_float(g.x & 0xffff0000u), __uint_as_float(g.y << 16),
                              __uint_as_float(g.y & 0xffff0000u)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = __fmul_rn(y[e], __frcp_rn(__fadd_rn(1.f, expf(-gv[e]))));
     }
-    *reinterpret_cast<uint2*>(C.out + br * C.out_stride + static_cast<long long>(hq) * HD + 4 * ln) =
+    *reinterpret_cast<uint2*>(C.out + br * C.out_stride + static_cast<long long>(hq) * HD + dim) =
         make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
@@ -1136,7 +1167,7 @@ xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a
         return st;
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq;
     trace_pre(s);
-    launch_k(attn_q8_combine_kernel<HD>, dim3(static_cast<unsigned>(rows)), dim3(CB_GROUPS * HD / 4), 0, s, c);
+    launch_k(attn_q8_combine_kernel<HD>, dim3(static_cast<unsigned>(rows)), dim3(CB_THREADS), 0, s, c);
     return launched("attn_q8_combine_kernel", s, K_ATTN_Q8, 4 * rows * a.nslot * (HD + 2) + 2 * rows * HD * (c.gate ? 2 : 1));
 }
 
