@@ -221,7 +221,7 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
     long long total = 0, before = 0, at[2];
     it[0] = it[1] = A.nslot * A.nrt * A.Hkv * A.B;   // where no cost is left
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = A.B > 32 ? 0 : 1; pass < 2; ++pass) {   // the total, which 32 sequences show at once; the shares
 #pragma unroll 1
         for (int b0 = 0; b0 < A.B; b0 += 32) {
             Sight v;
@@ -238,10 +238,9 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
                 if (lane >= off) x += o;
             }
             const long long all = __shfl_sync(0xffffffffu, x, 31);
-            if (pass == 0) {
-                total += all;
-                continue;
-            }
+            if (pass == 0 || A.B <= 32) total += all;
+            if (pass == 0) continue;
+            if (b0 == 0) at[0] = total * c / n, at[1] = total * (c + 1) / n;
             // an item belongs to the CTA in whose share its cost begins
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
@@ -266,8 +265,6 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
             }
             before += all;
         }
-        at[0] = total * c / n;
-        at[1] = total * (c + 1) / n;
     }
 }
 
@@ -1035,21 +1032,21 @@ struct CombineArgs {
 };
 
 // One CTA per (row, q head): w_s = 2^(m_s - M) over the row's live slots s in order, out = sum w_s O_s /
-// sum w_s l_s.  256 threads: 4 hd / 64 groups of threads each add the slots of one residue, then the
-// groups' sums are added in order: fixed by the row alone.
-constexpr int CB_THREADS = 256;
-constexpr int CB_SLOTS = 1 << 10;   // slots whose weights are staged at a time
+// sum w_s l_s.  The i-th of them belongs to the sum of residue i mod CB_SUMS, and those sums are added in
+// order: fixed by the row alone, whether G = 4 groups of threads have 4 residues each (few slots: a
+// batch's rows fit the machine) or 16 have one (many: a row's loads are in flight together).
+constexpr int CB_SUMS = 16;
+constexpr int CB_SLOTS = 1 << 10;   // slots whose m and l are staged at a time
 
-template <int HD>
-__global__ void __launch_bounds__(CB_THREADS) attn_q8_combine_kernel(const __grid_constant__ CombineArgs C) {
+template <int HD, int G>
+__global__ void __launch_bounds__(G* HD / 4) attn_q8_combine_kernel(const __grid_constant__ CombineArgs C) {
     griddep_launch();
     griddep_wait();
-    constexpr int CB_LANES = HD / 4, CB_GROUPS = CB_THREADS / CB_LANES;
+    constexpr int LN = HD / 4, NT = G * LN, PER = CB_SUMS / G;
     __shared__ float2 wl[CB_SLOTS];
-    __shared__ float4 acc_sm[CB_GROUPS][CB_LANES];
-    __shared__ float l_sm[CB_GROUPS], wmax[CB_THREADS / 32];
-    const int row = blockIdx.x, hq = row % C.Hq, b = row / C.Hq / C.R, r = row / C.Hq % C.R, tid = threadIdx.x;
-    const long long br = row / C.Hq;
+    __shared__ float4 acc_sm[CB_SUMS][LN];
+    __shared__ float l_sm[CB_SUMS], wmax[NT / 32];
+    const int row = blockIdx.x, br = row / C.Hq, hq = row - br * C.Hq, b = br / C.R, r = br - b * C.R, tid = threadIdx.x;
     const int nr = q8_rows(C.n_rows, b, C.R), L0 = C.ctx_len[b];
     if (r >= nr || L0 < 1 || L0 > C.max_len - nr + 1) return;
     const int len = L0 + r;
@@ -1062,58 +1059,90 @@ __global__ void __launch_bounds__(CB_THREADS) attn_q8_combine_kernel(const __gri
         const int s = i < n0 ? i : s0 + i - n0;
         return s < C.nsink ? s : s - first + C.nsink;
     };
-    const long long idx0 = (br * C.Hq + hq) * C.nslot;
+    const float2* ml = C.ml + static_cast<long long>(row) * C.nslot;
+    const float4* op = reinterpret_cast<const float4*>(C.opart + static_cast<long long>(row) * C.nslot * HD) + tid % LN;
     float M = NEG_INF;
-    for (int i = tid; i < ns; i += CB_THREADS) M = fmaxf(M, C.ml[idx0 + slot(i)].x);
+#pragma unroll 1
+    for (int i = tid; i < ns; i += NT) {
+        const float2 v = __ldcg(ml + slot(i));
+        if (i < CB_SLOTS) wl[i] = v;
+        M = fmaxf(M, v.x);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     if ((tid & 31) == 0) wmax[tid >> 5] = M;
     __syncthreads();
     M = wmax[0];
-    for (int w = 1; w < CB_THREADS / 32; ++w) M = fmaxf(M, wmax[w]);
-    const int grp = tid / CB_LANES, ln = tid % CB_LANES, dim = 4 * ln;
-    float L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) M = fmaxf(M, wmax[w]);
+    const int grp = tid / LN, ln = tid % LN;
+    float L[PER];
+    float4 a[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) L[k] = 0.f, a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int c0 = 0; c0 < ns; c0 += CB_SLOTS) {
         const int n = min(CB_SLOTS, ns - c0);
-        __syncthreads();
-        for (int i = tid; i < n; i += CB_THREADS) {
-            const float2 v = C.ml[idx0 + slot(c0 + i)];
-            wl[i] = make_float2(exp2f(__fsub_rn(v.x, M)), v.y);
+        if (c0) {
+            __syncthreads();
+            for (int i = tid; i < n; i += NT) wl[i] = __ldcg(ml + slot(c0 + i));
+            __syncthreads();
         }
-        __syncthreads();
-#pragma unroll 4
-        for (int i = grp; i < n; i += CB_GROUPS) {
-            const float2 w = wl[i];
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(C.opart + (idx0 + slot(c0 + i)) * HD + dim));
-            L = __fmaf_rn(w.x, w.y, L);
-            a.x = __fmaf_rn(w.x, o.x, a.x);
-            a.y = __fmaf_rn(w.x, o.y, a.y);
-            a.z = __fmaf_rn(w.x, o.z, a.z);
-            a.w = __fmaf_rn(w.x, o.w, a.w);
-        }
-    }
-    acc_sm[grp][ln] = a;
-    if (ln == 0) l_sm[grp] = L;
-    __syncthreads();
-    if (grp) return;
-    for (int g = 1; g < CB_GROUPS; ++g) {
-        const float4 o = acc_sm[g][ln];
-        L = __fadd_rn(L, l_sm[g]);
-        a.x = __fadd_rn(a.x, o.x), a.y = __fadd_rn(a.y, o.y), a.z = __fadd_rn(a.z, o.z), a.w = __fadd_rn(a.w, o.w);
-    }
-    float y[4] = {a.x, a.y, a.z, a.w};
+        constexpr int UN = 8 / PER;   // 8 loads in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += CB_SUMS * UN) {
+            float4 o[UN][PER];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = __fadd_rn(__fdiv_rn(y[e], L), 0.f);
+            for (int u = 0; u < UN; ++u)
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    const int i = i0 + u * CB_SUMS + grp + k * G;
+                    if (i < n) o[u][k] = __ldcg(op + static_cast<long long>(slot(c0 + i)) * LN);
+                }
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    const int i = i0 + u * CB_SUMS + grp + k * G;
+                    if (i >= n) continue;
+                    const float w = ex2_approx(__fsub_rn(wl[i].x, M));
+                    L[k] = __fmaf_rn(w, wl[i].y, L[k]);
+                    a[k].x = __fmaf_rn(w, o[u][k].x, a[k].x);
+                    a[k].y = __fmaf_rn(w, o[u][k].y, a[k].y);
+                    a[k].z = __fmaf_rn(w, o[u][k].z, a[k].z);
+                    a[k].w = __fmaf_rn(w, o[u][k].w, a[k].w);
+                }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        acc_sm[grp + k * G][ln] = a[k];
+        if (ln == 0) l_sm[grp + k * G] = L[k];
+    }
+    __syncthreads();
+    if (tid >= LN) return;
+    float4 y = acc_sm[0][tid];
+    float sum = l_sm[0];
+#pragma unroll
+    for (int g = 1; g < CB_SUMS; ++g) {
+        const float4 o = acc_sm[g][tid];
+        sum = __fadd_rn(sum, l_sm[g]);
+        y.x = __fadd_rn(y.x, o.x), y.y = __fadd_rn(y.y, o.y), y.z = __fadd_rn(y.z, o.z), y.w = __fadd_rn(y.w, o.w);
+    }
+    // one reciprocal, as its rounding and the product's are far below the output's
+    const float inv = __frcp_rn(sum);
+    float out[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = __fadd_rn(__fmul_rn(out[e], inv), 0.f);
     if (C.gate) {
-        const uint2 g = *reinterpret_cast<const uint2*>(C.gate + br * C.gate_stride + static_cast<long long>(hq) * HD + dim);
+        const uint2 g = *reinterpret_cast<const uint2*>(C.gate + br * C.gate_stride + hq * HD + 4 * tid);
         const float gv[4] = {__uint_as_float(g.x << 16), __uint_as_float(g.x & 0xffff0000u), __uint_as_float(g.y << 16),
                              __uint_as_float(g.y & 0xffff0000u)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __fmul_rn(y[e], __frcp_rn(__fadd_rn(1.f, expf(-gv[e]))));
+        for (int e = 0; e < 4; ++e) out[e] = __fmul_rn(out[e], __frcp_rn(__fadd_rn(1.f, expf(-gv[e]))));
     }
-    *reinterpret_cast<uint2*>(C.out + br * C.out_stride + static_cast<long long>(hq) * HD + dim) =
-        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    *reinterpret_cast<uint2*>(C.out + br * C.out_stride + hq * HD + 4 * tid) =
+        make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
 }
 
 inline size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1167,7 +1196,8 @@ xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a
         return st;
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq;
     trace_pre(s);
-    launch_k(attn_q8_combine_kernel<HD>, dim3(static_cast<unsigned>(rows)), dim3(CB_THREADS), 0, s, c);
+    if (a.nslot <= 2 * CB_SUMS) launch_k(attn_q8_combine_kernel<HD, 4>, dim3(static_cast<unsigned>(rows)), dim3(HD), 0, s, c);
+    else launch_k(attn_q8_combine_kernel<HD, 16>, dim3(static_cast<unsigned>(rows)), dim3(4 * HD), 0, s, c);
     return launched("attn_q8_combine_kernel", s, K_ATTN_Q8, 4 * rows * a.nslot * (HD + 2) + 2 * rows * HD * (c.gate ? 2 : 1));
 }
 
