@@ -50,16 +50,18 @@ constexpr float P_SHIFT = 7.f, RESCALE_SLACK = 8.f;
 constexpr float DEAD = -3e38f;         // the reference of a row that has seen nothing: t - DEAD passes any slack
 constexpr float LOW_SCALE = 64.f;      // P's last two terms
 
-// Split boundaries: Q8_SHORT positions each below Q8_SWITCH, Q8_LONG beyond.
-constexpr int Q8_SHORT = 256, Q8_SWITCH = 4096, Q8_LONG = 1024;
-static_assert(Q8_SHORT % T == 0 && Q8_LONG <= 8 * T && Q8_SHORT <= Q8_LONG, "a lane per half tile of an item");
+// Split boundaries: every 256 positions below Q8_NEAR, 512 below Q8_FAR, 1024 beyond.  A short context
+// wants its splits spread over the machine (one verify at 2183: 512 instead of 256 costs 1.4 us of 14.6),
+// a batch wants few items (32 sequences at 4000 to 8000: 256 up to 4096 costs 5 us of 65), a long context
+// few partial results (131072: 512 instead of 1024 costs 4 us of 73).
+constexpr int Q8_NEAR = 2048, Q8_FAR = 32768, Q8_NS = Q8_NEAR / 256, Q8_FS = Q8_NS + (Q8_FAR - Q8_NEAR) / 512;
+static_assert(256 % T == 0 && 1024 <= 8 * T, "a lane per half tile of an item");
 __host__ __device__ inline int q8_split_begin(int s) {
-    constexpr int NS = Q8_SWITCH / Q8_SHORT;
-    return s < NS ? s * Q8_SHORT : Q8_SWITCH + (s - NS) * Q8_LONG;
+    return s < Q8_NS ? s * 256 : s < Q8_FS ? Q8_NEAR + (s - Q8_NS) * 512 : Q8_FAR + (s - Q8_FS) * 1024;
 }
 // The split that position p lies in.
 __host__ __device__ inline int q8_split_of(int p) {
-    return p < Q8_SWITCH ? p / Q8_SHORT : Q8_SWITCH / Q8_SHORT + (p - Q8_SWITCH) / Q8_LONG;
+    return p < Q8_NEAR ? p / 256 : p < Q8_FAR ? Q8_NS + (p - Q8_NEAR) / 512 : Q8_FS + (p - Q8_FAR) / 1024;
 }
 
 // NR: rows of a row tile, padded (a multiple of 8, as 2 NR is an N of the MMAs).
@@ -150,11 +152,11 @@ struct Sight {
     __device__ __forceinline__ bool half(int p) const { return p < end && (p + 64 > lo || p < sinks); }
     // tiles of sinks before those of the windows
     __device__ __forceinline__ int heads() const { return min(lo / T, (min(sinks, lo) + T - 1) / T); }
-    // cost of the splits before split s: two a tile, one a split
+    // cost of the splits before split s: one a tile, one a split
     __device__ __forceinline__ int cost(int s) const {
         const int last = q8_split_of(end - 1) + 1, h = heads(), n = s >= last ? (end + T - 1) / T : q8_split_begin(s) / T;
         const int hs = h ? q8_split_of(h * T - 1) + 1 : 0, m = min(s, last);
-        return 2 * (min(n, h) + max(0, n - max(lo / T, h))) + min(m, hs) + max(0, m - max(q8_split_of(lo), hs));
+        return min(n, h) + max(0, n - max(lo / T, h)) + min(m, hs) + max(0, m - max(q8_split_of(lo), hs));
     }
 };
 
@@ -1154,7 +1156,7 @@ inline int slots(int R, int max_len, int window, int sinks, int* nsink) {
     *nsink = 0;
     if (!window || window >= max_len) return all;
     const int ns = sinks ? q8_split_of(min(sinks, max_len) - 1) + 1 : 0;
-    const long long w = (static_cast<long long>(window) + R - 2) / Q8_SHORT + 2;
+    const long long w = (static_cast<long long>(window) + R - 2) / 256 + 2;
     if (ns + w >= all) return all;   // then no slot is left out and none counts as a sink's
     *nsink = ns;
     return ns + static_cast<int>(w);
