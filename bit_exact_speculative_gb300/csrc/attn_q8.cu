@@ -443,32 +443,6 @@ __device__ __forceinline__ bool wg_any(int id, bool f) {
                  : "memory");
     return r != 0;
 }
-// Largest value of a warp's lanes, NaN passed over.
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Two fp32 operations in one instruction: (a, b) *= (x, y); (u, v) = (u, v) (x, y) + (a, b);
-// (u, v) += (x, y) (a, b); (a, b) += (x, y).
-__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
-}
-__device__ __forceinline__ void fma2(float& u, float& v, float x, float y, float a, float b) {
-    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\t"
-        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(u), "+f"(v) : "f"(x), "f"(y), "f"(a), "f"(b));
-}
-__device__ __forceinline__ void fma2_acc(float& u, float& v, float x, float y, float a, float b) {
-    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
-        "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "+f"(u), "+f"(v) : "f"(x), "f"(y), "f"(a), "f"(b));
-}
-__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
-}
 // L2 policy of lines read once, or of any.
 __device__ __forceinline__ uint64_t l2_policy(bool once) {
     uint64_t p;
@@ -1174,7 +1148,7 @@ template <int HD, int NR>
 xv_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a, cudaStream_t s) {
     using S = Shape<HD, NR>;
     int sms = 0;
-    if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(attn_q8_kernel<HD, NR>), S::SMEM, false, "attn_q8: set shared memory size"))
+    if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(attn_q8_kernel<HD, NR>), S::SMEM, true, "attn_q8: set shared memory size"))
         return st;
     if (xv_status st = device_sm_count(&sms)) return st;
     const long long n_items = static_cast<long long>(a.nslot) * a.nrt * a.Hkv * a.B;

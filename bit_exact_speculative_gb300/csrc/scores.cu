@@ -5,16 +5,30 @@
 //     logprob(t) = (x_t - m) - log S,   entropy = log S - D / S,
 // and the n largest x_i, the lowest index first among equals (a NaN below every number).
 //
-// A row is cut into chunks of SC_CHUNK logits, one CTA each, every logit read once into a register.
-// A chunk's (m, S, D) and its n best go to the workspace; the CTA that finishes a row last (an
-// atomic counter) joins the chunks in order.  Chunks, threads' shares of them and the order of every
-// sum are fixed by V and the logits' type, so a row has the same bits in a call of any number of
-// rows, at any position and alignment.
+// A row is cut into chunks of SC_CHUNK logits, a chunk into a share of 32 logits per thread; a warp's
+// shares give one (m, S, D), and a row's are joined in order.  Chunks, shares and the order of every sum
+// are fixed by V alone, so a row has the same bits in a call of any number of rows, at any position and
+// alignment.
 //
-// A chunk's n best: SC_GROUPS groups of threads give their largest values; the n-th largest of those
-// bounds the n-th largest logit from below, and the few logits (usually 1 to 2 n) at or above the
-// bound are ranked by comparing each with each.  Groups that tie at the bound are told apart by
-// their lowest index there, so a chunk of one value (a masked one, all -inf) has few candidates too.
+// Persistent CTAs take equal runs of the call's chunks, each logit read once: bulk copies of whole
+// 16-byte pieces bring a ring of chunks into shared memory (rows may start at any address: the pieces
+// that hold a chunk's two ends are read whole), from where a thread takes every 256th logit.  Most rows
+// lie in one CTA, which finishes them; of a row that reaches into other CTAs each leaves its warps' sums
+// and its n best in the workspace, and the one that ends last (an atomic counter) joins them.
+// (A CTA per chunk, its loads straight into registers: 392 us for 2048 rows of 151936, of 184 at the
+// memory's rate, and 54 us for 500 rows of 50257 bf16 logits, whose odd rows were read one by one.)
+//
+// The exponentials alone are 512 cycles a chunk and SM, where the memory's rate leaves 720 for bf16
+// logits, so what is done per logit and per chunk is kept small: one barrier a chunk, two logits an
+// instruction, no reduction wider than a warp before a row's end, a warp of its own for the ring.  What a row's end needs (the join, the
+// token's logit, the lists) is warp 0's alone, while the other warps take up the next chunk.
+//
+// Each warp keeps the 32 best of its shares of a row, one a lane, in order.  A logit has to pass the n-th
+// of them, and the smallest of the eight warps' (n / 8)-th: n logits reach that.  (In a row's first
+// chunk: their lanes' (n / 8)-th largest.)  A few that pass are put in one by one, more by a bitonic sort
+// and merge, and at a row's end the warps' lists are merged.  (With one list for the CTA, and a barrier a
+// chunk for it, 2048 rows of 151936 took 234 us with n = 1, 290 us with n = 20.)
+#include <algorithm>
 #include <cmath>
 
 #include "xv_internal.h"
@@ -23,17 +37,27 @@
 namespace xv {
 namespace {
 
-constexpr int SC_THREADS = 256;
+constexpr int SC_THREADS = 256, SC_WARPS = SC_THREADS / 32;
 constexpr int SC_PER = 32;                          // logits per thread
 constexpr int SC_CHUNK = SC_THREADS * SC_PER;
-constexpr int SC_GROUPS = 64;                       // groups of 4 neighbouring threads, 128 logits each
-constexpr int SC_CAND = XV_TOP_MAX * SC_CHUNK / SC_GROUPS;   // logits of the XV_TOP_MAX best groups
 constexpr int SC_V_MAX = 1 << 19;
 constexpr int SC_C_MAX = SC_V_MAX / SC_CHUNK;
-static_assert(SC_C_MAX * XV_TOP_MAX <= SC_CAND, "the join's keys share the candidates' buffer");
-static_assert(XV_TOP_MAX <= SC_GROUPS, "");
+constexpr int SC_G_MAX = 1024;                      // CTAs
+constexpr int SC_HEADER = SC_G_MAX * 4;             // their counters, wherever the rest lies
+constexpr float LOG2E = 1.4426950408889634f;
+static_assert(XV_TOP_MAX <= 32, "a lane each");
 
-using Key = unsigned long long;   // (order of the value) << 32 | ~index: larger is better, 0 is none
+// Ring of chunks: as many as fit beside the CTAs of an SM.
+template <typename T>
+struct Ring {
+    static constexpr int PER_SM = 2, N = sizeof(T) == 4 ? 3 : 5;
+    static constexpr int BYTES = SC_CHUNK * static_cast<int>(sizeof(T)) + 16;   // any alignment
+    static constexpr int STRIDE = (BYTES + 127) / 128 * 128;
+    static constexpr int SMEM = N * STRIDE + 128;
+    static_assert(PER_SM * (SMEM + 9 * 1024 + 1024) <= 228 * 1024, "");
+};
+
+using Key = unsigned long long;   // (1 + order of the value) << 32 | ~index: larger is better, 0 is none
 
 struct ScoreArgs {
     const void* logits;
@@ -45,52 +69,24 @@ struct ScoreArgs {
     float* entropy;
     int32_t* ids;
     float* lps;
-    unsigned* cnt;     // [M], zero between calls
-    float4* part;      // [M][C] (m, S, D, -)
-    Key* keys;         // [M][C][top]
+    unsigned* cnt;     // [SC_G_MAX], zero between calls: of the row that starts in a CTA and leaves it
+    float4* part;      // [CTAs][C][SC_WARPS] (m, S, D, -) of that row
+    Key* keys;         // [CTAs][2][top] n best of the row that entered the CTA, and of the one that leaves it
     unsigned* err;
 };
 
-// Unsigned order of a float: NaN 0, then -inf .. +inf, -0 as +0.
+// Unsigned order of a float: NaN 1, then -inf .. +inf, -0 as +0; 0 is none.
 __device__ __forceinline__ unsigned order_of(float x) {
     const unsigned u = __float_as_uint(__fadd_rn(x, 0.f));
-    return x != x ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    return x != x ? 1u : ((u & 0x80000000u) ? ~u : u | 0x80000000u) + 1u;
 }
 __device__ __forceinline__ float value_of(unsigned o) {
+    --o;
     return o == 0 ? __uint_as_float(0x7fc00000u) : __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
 
-template <typename T>
-struct Logits;
-template <>
-struct Logits<float> {
-    static constexpr int W = 4;   // logits per 16 bytes
-    static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
-    static __device__ __forceinline__ void wide(const float* p, float* v) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(p));
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-    }
-};
-template <>
-struct Logits<uint16_t> {
-    static constexpr int W = 8;
-    static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(__ldg(p)); }
-    static __device__ __forceinline__ void wide(const uint16_t* p, float* v) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-};
-
-// Index, within its chunk, of a thread's i-th logit: runs of W neighbours, SC_THREADS * W apart.
-template <int W>
-__device__ __forceinline__ int chunk_index(int t, int i) {
-    return (i / W) * (SC_THREADS * W) + t * W + i % W;
-}
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(uint16_t x) { return bf16_to_f32(x); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -98,214 +94,267 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(SC_THREADS) logprobs_kernel(const __grid_constant__ ScoreArgs A) {
-    griddep_launch();
-    griddep_wait();
-    using L = Logits<T>;
-    constexpr int W = L::W;
-    __shared__ __align__(16) Key cand[TOP ? SC_CAND : 1];
-    __shared__ unsigned gmax[SC_GROUPS], gidx[SC_GROUPS];
-    __shared__ float wm[8], ws_[8], wd[8];
-    __shared__ float4 parts[SC_C_MAX];
-    __shared__ Key s_bound;
-    __shared__ unsigned s_tau, s_more, s_n;
-    __shared__ int s_last;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x / A.C, chunk = blockIdx.x - row * A.C;
-    if (A.n_rows && row >= *A.n_rows) return;
-    const T* x = static_cast<const T*>(A.logits) + row * A.ld;
-    const int base = chunk * SC_CHUNK, left = A.V - base;   // logits from the chunk's first on
+// Sorts a warp's bitonic keys, the largest into lane 0.
+__device__ __forceinline__ Key bitonic_down(Key k, int lane) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const Key o = __shfl_xor_sync(0xffffffffu, k, off);
+        k = (lane & off) == 0 ? (k > o ? k : o) : (k < o ? k : o);
+    }
+    return k;
+}
+// The 32 best of two sorted lists (the largest in lane 0), the second one read backwards.
+__device__ __forceinline__ Key merge_best(Key list, Key backwards, int lane) {
+    return bitonic_down(list > backwards ? list : backwards, lane);
+}
+__device__ __forceinline__ Key reversed(Key k, int lane) { return __shfl_sync(0xffffffffu, k, 31 - lane); }
+// Sorts a warp's keys, the smallest into lane 0.
+__device__ __forceinline__ Key sort_up(Key k, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int off = size / 2; off > 0; off >>= 1) {
+            const Key o = __shfl_xor_sync(0xffffffffu, k, off);
+            const bool up = (lane & size) == 0 || size == 32, low = (lane & off) == 0;
+            k = low == up ? (k < o ? k : o) : (k > o ? k : o);
+        }
+    return k;
+}
 
-    float v[SC_PER];
-    if (left >= SC_CHUNK && (reinterpret_cast<uintptr_t>(x) & 15) == 0) {
-#pragma unroll
-        for (int i = 0; i < SC_PER; i += W) L::wide(x + base + chunk_index<W>(tid, i), v + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < SC_PER; ++i) {
-            const int at = chunk_index<W>(tid, i);
-            v[i] = at < left ? L::one(x + base + at) : -INFINITY;
-        }
-    }
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < SC_PER; ++i) mx = fmaxf(mx, v[i]);
-    // a thread without a number (all NaN, or behind the row) stays below every number
-    unsigned best = 0;
-    if (TOP) {
-        best = order_of(mx);
-        if (mx == -INFINITY) {
-            best = 0;
-#pragma unroll
-            for (int i = 0; i < SC_PER; ++i)
-                if (v[i] == -INFINITY && chunk_index<W>(tid, i) < left) best = order_of(-INFINITY);
-        }
-        unsigned g = best;
-        g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
-        g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-        if ((tid & 3) == 0) gmax[tid >> 2] = g;
-        if (tid == 0) s_n = 0;
-    }
-    float m = mx;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) wm[warp] = m;
-    __syncthreads();
-    m = wm[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) m = fmaxf(m, wm[w]);
-    if (TOP && tid < SC_GROUPS) {
-        // tau: the top-th largest of the groups' values
-        const unsigned mine = gmax[tid];
-        int gt = 0, ge = 0;
-#pragma unroll 8
-        for (int g = 0; g < SC_GROUPS; ++g) {
-            const unsigned o = gmax[g];
-            gt += o > mine;
-            ge += o >= mine;
-        }
-        if (gt < A.top && ge >= A.top) {   // the same values by every thread of this value
-            s_tau = mine;
-            s_more = ge > A.top ? A.top - gt : 0;   // ties at tau: this many of its groups are in
-        }
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float s = 0.f, d = 0.f;
-#pragma unroll
-    for (int i = 0; i < SC_PER; ++i) {
-        const float c = __fsub_rn(v[i], ref);
-        const float e = ex2_approx(__fmul_rn(c, 1.4426950408889634f));
-        s = __fadd_rn(s, e);
-        d = __fmaf_rn(e, fmaxf(c, -3e38f), d);   // exp(-inf) (-inf) is 0 here
-    }
-    s = warp_sum(s);
-    d = warp_sum(d);
-    if (lane == 0) ws_[warp] = s, wd[warp] = d;
-    __syncthreads();
-    const long long slot = static_cast<long long>(row) * A.C + chunk;
+// Barrier of the warps that compute.
+__device__ __forceinline__ void sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(SC_THREADS) : "memory"); }
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_kernel(const __grid_constant__ ScoreArgs A) {
+    griddep_launch();
+    using R = Ring<T>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[R::N], empty[R::N];
+    __shared__ Key lists[TOP ? SC_WARPS : 1][32];
+    __shared__ volatile unsigned floors[SC_WARPS];   // what part_n of a warp's logits reach
+    __shared__ float pm[SC_C_MAX * SC_WARPS], ps[SC_C_MAX * SC_WARPS], pd[SC_C_MAX * SC_WARPS];   // [chunk][warp]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, top = A.top, C = A.C;
+    const uint32_t raw = smem_u32(smem_raw), ring = (raw + 127u) & ~127u;
+    uint8_t* bufs = smem_raw + (ring - raw);
     if (tid == 0) {
-        s = ws_[0], d = wd[0];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) s = __fadd_rn(s, ws_[w]), d = __fadd_rn(d, wd[w]);
-        __stcg(A.part + slot, make_float4(ref, s, d, 0.f));
+        for (int st = 0; st < R::N; ++st) mbar_init(smem_u32(&full[st]), 1), mbar_init(smem_u32(&empty[st]), SC_WARPS);
+        fence_mbar_init();
     }
-    if (TOP) {
-        const unsigned tau = s_tau;
-        unsigned lim = 0xffffffffu;   // of the logits equal to tau, those up to this index
-        if (s_more) {
-            unsigned lo = 0xffffffffu;
-            if (best == tau)
-#pragma unroll
-                for (int i = SC_PER - 1; i >= 0; --i)
-                    if (order_of(v[i]) == tau && chunk_index<W>(tid, i) < left) lo = chunk_index<W>(tid, i);
-            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
-            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
-            if ((tid & 3) == 0) gidx[tid >> 2] = gmax[tid >> 2] == tau ? lo : 0xffffffffu;
-            __syncthreads();
-            if (tid < SC_GROUPS) {
-                const unsigned mine = gidx[tid];
-                int lt = 0;
-#pragma unroll 8
-                for (int g = 0; g < SC_GROUPS; ++g) lt += gidx[g] < mine || (gidx[g] == mine && g < tid);
-                if (lt == static_cast<int>(s_more) - 1) s_bound = mine;   // 0xffffffff: fewer logits than top
-            }
-            __syncthreads();
-            lim = static_cast<unsigned>(s_bound);
+    __syncthreads();
+    griddep_wait();
+    const int rows = A.n_rows ? min(max(*A.n_rows, 0), A.M) : A.M;
+    const int n_chunks = rows * C;   // below 2^31
+    const int G = min(static_cast<int>(gridDim.x), n_chunks);   // CTAs with a chunk at least
+    if (static_cast<int>(blockIdx.x) >= G) return;
+    const int i0 = static_cast<int>(static_cast<long long>(blockIdx.x) * n_chunks / G);
+    const int i1 = static_cast<int>((blockIdx.x + 1ll) * n_chunks / G);
+
+    const T* base = static_cast<const T*>(A.logits);
+    int row = i0 / C, c = i0 - row * C;
+    if (warp == SC_WARPS) {
+        // ---- the chunks into the ring, in whole 16-byte pieces
+        if (lane) return;
+        const int count = i1 - i0;
+        int j = 0;
+        for (; j < count; ++j) {
+            const int st = j % R::N;
+            if (j >= R::N && !mbar_wait(smem_u32(&empty[st]), ((j / R::N) & 1u) ^ 1u, A.err)) break;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(base + row * A.ld + c * SC_CHUNK);
+            const uintptr_t lo = a & ~static_cast<uintptr_t>(15);
+            const uintptr_t hi = (a + min(SC_CHUNK, A.V - c * SC_CHUNK) * sizeof(T) + 15) & ~static_cast<uintptr_t>(15);
+            const uint32_t bar = smem_u32(&full[st]);
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(hi - lo));
+            bulk_load(ring + st * R::STRIDE, reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), bar);
+            if (++c == C) c = 0, ++row;
         }
-        if (best >= tau) {
+        // every copy issued lands before the CTA leaves
+        for (int k = max(0, j - R::N); k < j; ++k) mbar_wait(smem_u32(&full[k % R::N]), (k / R::N) & 1u, A.err);
+        return;
+    }
+
+    Key list = 0, least = 0;      // the lane's of the warp's best; a new key has to pass the last of n
+    unsigned floor = 0;
+    const int part_n = (top + SC_WARPS - 1) / SC_WARPS;
+    int first_c = c;              // of this row in this CTA
+    int st = 0, ph = 0;
+    int token = 0;                // warp 0: the row's token, its logit
+    float token_x = 0.f;
+    bool ok = true;
+    for (int i = i0; i < i1; ++i) {
+        const int at0 = c * SC_CHUNK, n = min(SC_CHUNK, A.V - at0);
+        if (warp == 0 && c == first_c) token = __ldg(A.tokens + row);
+        // (a wait that gave up is recorded; what follows reads stale logits, but ends)
+        if (ok) ok = mbar_wait(smem_u32(&full[st]), ph, A.err);
+        const T* x = reinterpret_cast<const T*>(bufs + st * R::STRIDE + (reinterpret_cast<uintptr_t>(base + row * A.ld + at0) & 15)) + tid;
+        float v[SC_PER];
+        if (n == SC_CHUNK) {
 #pragma unroll
-            for (int i = 0; i < SC_PER; ++i) {
-                const unsigned o = order_of(v[i]), at = chunk_index<W>(tid, i);
-                if ((o > tau || (o == tau && at <= lim)) && static_cast<int>(at) < left) {
-                    const unsigned k = atomicAdd(&s_n, 1u);
-                    if (k < SC_CAND) cand[k] = static_cast<Key>(o) << 32 | static_cast<unsigned>(~(base + at));
+            for (int k = 0; k < SC_PER; ++k) v[k] = to_float(x[k * SC_THREADS]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < SC_PER; ++k) v[k] = k * SC_THREADS + tid < n ? to_float(x[k * SC_THREADS]) : -INFINITY;
+        }
+        if (warp == 0 && c == first_c && token >= 0 && token < A.V) token_x = to_float(__ldg(base + row * A.ld + token));
+        float mx4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int k = 4; k < SC_PER; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], v[k]);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));   // NaN only if all are
+        if (c == first_c && !TOP) sync();   // warp 0 has done with the row before
+        if (TOP) {
+            // (0 where every logit of the thread is NaN, masked or behind the row)
+            const unsigned need = static_cast<unsigned>(least >> 32), best = mx > -INFINITY ? order_of(mx) : 0u;
+            if (c == first_c) {
+                int reach = 0;
+#pragma unroll 8
+                for (int k = 0; k < 32; ++k) reach += __shfl_sync(0xffffffffu, best, k) >= best;
+                floor = __reduce_max_sync(0xffffffffu, reach >= part_n ? best : 0u);
+                if (lane == 0) floors[warp] = floor;
+                sync();   // and warp 0 has done with the row before
+            }
+            unsigned pass = floors[0];
+#pragma unroll
+            for (int w = 1; w < SC_WARPS; ++w) pass = min(pass, floors[w]);
+            const bool some = best > need && best >= pass;
+            pass = max(pass, need);
+            const bool rest = pass <= order_of(-INFINITY);   // what is not a number above -inf counts, too
+            if (__any_sync(0xffffffffu, some || rest)) {
+                const float low = rest ? -INFINITY : value_of(pass);
+                unsigned hit = 0;
+#pragma unroll
+                for (int k = 0; k < SC_PER; ++k) hit |= v[k] < low ? 0u : 1u << k;
+                if (rest && n < SC_CHUNK) hit &= n > tid ? 0xffffffffu >> (31 - (n - tid - 1) / SC_THREADS) : 0u;
+                for (;;) {
+                    Key mine = 0;   // the lane's next that passes
+                    while (hit) {
+                        const int k = __ffs(hit) - 1;
+                        mine = static_cast<Key>(order_of(to_float(x[k * SC_THREADS]))) << 32 | static_cast<unsigned>(~(at0 + k * SC_THREADS + tid));
+                        if (mine > least) break;
+                        mine = 0;
+                        hit &= hit - 1;
+                    }
+                    const unsigned who = __ballot_sync(0xffffffffu, mine != 0);
+                    if (!who) break;
+                    if (__popc(who) > 4) {
+                        list = merge_best(list, sort_up(mine, lane), lane);
+                        hit &= hit - 1;
+                    } else {
+                        const int src = __ffs(who) - 1;
+                        const Key key = __shfl_sync(0xffffffffu, mine, src), before = __shfl_up_sync(0xffffffffu, list, 1);
+                        const int at = __popc(__ballot_sync(0xffffffffu, list > key));
+                        list = lane < at ? list : lane == at ? key : before;
+                        if (lane == src) hit &= hit - 1;
+                    }
+                    least = __shfl_sync(0xffffffffu, list, top - 1);
+                }
+                floor = max(floor, static_cast<unsigned>(__shfl_sync(0xffffffffu, list, part_n - 1) >> 32));
+                if (lane == 0) floors[warp] = floor;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty[st]));   // the stage may be filled again
+        const float m = warp_max(mx), ref = m > -INFINITY ? m : 0.f;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f}, d4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < SC_PER; k += 2) {
+            float a = v[k], b = v[k + 1];
+            add2(a, b, -ref, -ref);
+            float ea = a, eb = b;
+            mul2(ea, eb, LOG2E, LOG2E);
+            ea = ex2_approx(ea), eb = ex2_approx(eb);
+            add2(s4[k & 3], s4[(k & 3) + 1], ea, eb);
+            fma2_acc(d4[k & 3], d4[(k & 3) + 1], ea, eb, fmaxf(a, -3e38f), fmaxf(b, -3e38f));   // exp(-inf) (-inf) is 0 here
+        }
+        const float s = warp_sum(__fadd_rn(__fadd_rn(s4[0], s4[1]), __fadd_rn(s4[2], s4[3])));
+        const float d = warp_sum(__fadd_rn(__fadd_rn(d4[0], d4[1]), __fadd_rn(d4[2], d4[3])));
+        if (lane == 0) pm[c * SC_WARPS + warp] = ref, ps[c * SC_WARPS + warp] = s, pd[c * SC_WARPS + warp] = d;
+        if (++st == R::N) st = 0, ph ^= 1;
+        const bool row_ends = c == C - 1;
+        if (!row_ends && i + 1 < i1) {
+            ++c;
+            continue;
+        }
+        if (TOP) lists[warp][lane] = list;
+        sync();
+        if (warp == 0) {
+            bool last = true;
+            if (TOP) {
+                auto two = [&](int w) { return merge_best(lists[w][lane], lists[w + 1][31 - lane], lane); };
+                const Key a = merge_best(two(0), reversed(two(2), lane), lane), b = merge_best(two(4), reversed(two(6), lane), lane);
+                list = merge_best(a, reversed(b, lane), lane);
+            }
+            if (first_c != 0 || !row_ends) {
+                // the row lies in CTAs a to z; ((i + 1) G - 1) / n_chunks is the CTA of chunk i
+                const long long r0 = static_cast<long long>(row) * C;
+                const int a = static_cast<int>(((r0 + 1) * G - 1) / n_chunks), z = static_cast<int>(((r0 + C) * G - 1) / n_chunks);
+                float4* gp = A.part + static_cast<long long>(a) * C * SC_WARPS;
+                for (int k = first_c * SC_WARPS + lane; k < (c + 1) * SC_WARPS; k += 32) __stcg(gp + k, make_float4(pm[k], ps[k], pd[k], 0.f));
+                if (TOP && lane < top) __stcg(A.keys + (2ll * blockIdx.x + (first_c == 0)) * top + lane, list);
+                __threadfence();
+                __syncwarp();
+                unsigned seen = 0;
+                if (lane == 0) seen = atomicAdd(A.cnt + a, 1u);
+                last = __shfl_sync(0xffffffffu, seen, 0) == static_cast<unsigned>(z - a);
+                if (last) {
+                    if (lane == 0) A.cnt[a] = 0;
+                    __threadfence();
+#pragma unroll 8
+                    for (int k = lane; k < C * SC_WARPS; k += 32) {
+                        const float4 q = __ldcg(gp + k);
+                        pm[k] = q.x, ps[k] = q.y, pd[k] = q.z;
+                    }
+                    if (TOP) {
+                        list = lane < top ? __ldcg(A.keys + (2ll * a + 1) * top + lane) : 0;
+                        for (int g = a + 1; g <= z; g += 4) {
+                            auto theirs = [&](int h, int j) { return h <= z && j < top ? __ldcg(A.keys + 2ll * h * top + j) : Key(0); };
+                            const Key q0 = theirs(g, lane), q1 = theirs(g + 1, 31 - lane), q2 = theirs(g + 2, lane), q3 = theirs(g + 3, 31 - lane);
+                            const Key q = merge_best(merge_best(q0, q1, lane), reversed(merge_best(q2, q3, lane), lane), lane);
+                            list = merge_best(list, reversed(q, lane), lane);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (last) {
+                float mrow = -INFINITY;
+                for (int k = lane; k < C * SC_WARPS; k += 32)
+                    if (ps[k] != 0.f) mrow = fmaxf(mrow, pm[k]);   // S = 0: nothing but -inf
+                mrow = warp_max(mrow);
+                for (int k = lane; k < C * SC_WARPS; k += 32) {
+                    const float off = __fsub_rn(pm[k], mrow), S = ps[k];
+                    pm[k] = S == 0.f ? 0.f : expf(off);
+                    pd[k] = S == 0.f ? 0.f : __fmaf_rn(fmaxf(off, -3e38f), S, pd[k]);
+                }
+                __syncwarp();
+                float S = 0.f, D = 0.f;   // of a warp's shares, in lanes 0 to 7 and again in the others
+#pragma unroll 4
+                for (int k = lane % SC_WARPS; k < C * SC_WARPS; k += SC_WARPS) {
+                    S = __fmaf_rn(pm[k], ps[k], S);
+                    D = __fmaf_rn(pm[k], pd[k], D);
+                }
+#pragma unroll
+                for (int off = SC_WARPS / 2; off > 0; off >>= 1) {
+                    S = __fadd_rn(S, __shfl_xor_sync(0xffffffffu, S, off));
+                    D = __fadd_rn(D, __shfl_xor_sync(0xffffffffu, D, off));
+                }
+                const float logs = logf(S);
+                const bool empty = S == 0.f;   // every logit -inf
+                auto score = [&](float xv) { return empty ? -INFINITY : __fsub_rn(__fsub_rn(xv, mrow), logs); };
+                if (lane == 0) {
+                    if (A.entropy) A.entropy[row] = empty ? 0.f : __fsub_rn(logs, __fdiv_rn(D, S));
+                    const bool in = token >= 0 && token < A.V;
+                    if (!in && token != -1) atomicOr(A.err, ERR_BAD_TOKEN);
+                    A.logprob[row] = in ? score(token_x) : token == -1 ? 0.f : __uint_as_float(0x7fc00000u);
+                }
+                if (TOP && lane < top) {
+                    const long long o = static_cast<long long>(row) * top + lane;
+                    A.ids[o] = static_cast<int32_t>(~static_cast<unsigned>(list));
+                    A.lps[o] = score(value_of(static_cast<unsigned>(list >> 32)));
                 }
             }
         }
-        __syncthreads();
-        const int n = min(static_cast<int>(s_n), SC_CAND);
-        Key* out = A.keys + slot * A.top;
-        for (int i = tid; i < n; i += SC_THREADS) {
-            const Key mine = cand[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += cand[j] > mine;
-            if (rank < A.top) __stcg(out + rank, mine);
-        }
-        for (int i = n + tid; i < A.top; i += SC_THREADS) __stcg(out + i, Key(0));
-    }
-    // the row's last CTA joins its chunks
-    __syncthreads();
-    if (tid == 0) {
-        s_last = 1;
-        if (A.C > 1) {
-            __threadfence();
-            s_last = atomicAdd(A.cnt + row, 1u) == static_cast<unsigned>(A.C - 1);
-            if (s_last) A.cnt[row] = 0;
-        }
-        __threadfence();
-    }
-    __syncthreads();
-    if (!s_last) return;
-    for (int c = tid; c < A.C; c += SC_THREADS) parts[c] = __ldcg(A.part + static_cast<long long>(row) * A.C + c);
-    const int nk = TOP ? A.C * A.top : 0;
-    if (TOP) {
-        const Key* in = A.keys + static_cast<long long>(row) * nk;
-        for (int i = tid; i < nk; i += SC_THREADS) cand[i] = __ldcg(in + i);
-        if (tid == 0) s_n = 0, s_bound = 0;
-    }
-    __syncthreads();
-    float mrow = -INFINITY, srow = 0.f, drow = 0.f;
-    for (int c = 0; c < A.C; ++c)
-        if (parts[c].y != 0.f) mrow = fmaxf(mrow, parts[c].x);
-    for (int c = 0; c < A.C; ++c) {
-        const float4 p = parts[c];
-        if (p.y == 0.f) continue;   // nothing but -inf
-        const float off = __fsub_rn(p.x, mrow), w = expf(off);
-        srow = __fmaf_rn(w, p.y, srow);
-        drow = __fmaf_rn(w, __fmaf_rn(fmaxf(off, -3e38f), p.y, p.z), drow);
-    }
-    const bool empty = srow == 0.f;   // every logit -inf
-    const float logs = logf(srow);
-    auto score = [&](float xv) { return empty ? -INFINITY : __fsub_rn(__fsub_rn(xv, mrow), logs); };
-    if (tid == 0) {
-        if (A.entropy) A.entropy[row] = empty ? 0.f : __fsub_rn(logs, __fdiv_rn(drow, srow));
-        const int t = A.tokens[row];
-        float lp = 0.f;   // -1: no token
-        if (t >= 0 && t < A.V) {
-            lp = score(L::one(x + t));
-        } else if (t != -1) {
-            atomicOr(A.err, ERR_BAD_TOKEN);
-            lp = __uint_as_float(0x7fc00000u);
-        }
-        A.logprob[row] = lp;
-    }
-    if (TOP) {
-        // a lower bound of the top-th largest key: of the chunks' p-th keys the k-th largest, p k >= top
-        const int p = max(A.top > 1 ? 2 : 1, (A.top + A.C - 1) / A.C), k = (A.top + p - 1) / p;
-        if (tid < A.C) {
-            const Key mine = cand[tid * A.top + p - 1];
-            int gt = 0, ge = 0;
-            for (int c = 0; c < A.C; ++c) {
-                const Key o = cand[c * A.top + p - 1];
-                gt += o > mine;
-                ge += o >= mine;
-            }
-            if (gt < k && ge >= k) s_bound = mine;
-        }
-        __syncthreads();
-        const Key bound = s_bound;
-        for (int i = tid; i < nk; i += SC_THREADS) {
-            const Key mine = cand[i];
-            if (mine < bound || mine == 0) continue;
-            int rank = 0;   // keys above this one; a chunk's stand in order, so its first smaller one ends it
-            for (int c = 0; c < A.C && rank < A.top; ++c)
-                for (int j = 0; j < A.top && cand[c * A.top + j] > mine; ++j) ++rank;
-            if (rank >= A.top) continue;
-            const long long o = static_cast<long long>(row) * A.top + rank;
-            A.ids[o] = static_cast<int32_t>(~static_cast<unsigned>(mine));
-            A.lps[o] = score(value_of(static_cast<unsigned>(mine >> 32)));
-        }
+        ++row;
+        c = first_c = 0;
+        list = least = 0;
     }
 }
 
@@ -314,6 +363,9 @@ inline bool sizes_ok(int M, int V, int top) {
     return M >= 1 && V >= 1 && V <= SC_V_MAX && top >= 0 && top <= XV_TOP_MAX && top <= V &&
            static_cast<long long>(M) * ceil_div(V, SC_CHUNK) < (1ll << 31);
 }
+
+// CTAs at most
+inline size_t ctas(int M, int C) { return std::min<size_t>(SC_G_MAX, static_cast<size_t>(M) * C); }
 
 xv_status logprobs(const void* logits, bool f32, long long ld, const int32_t* tokens, const int32_t* n_rows, int M, int V,
                    float* logprob, float* entropy, int top, int32_t* ids, float* lps, void* ws, size_t ws_bytes,
@@ -335,15 +387,25 @@ xv_status logprobs(const void* logits, bool f32, long long ld, const int32_t* to
     uint8_t* w = static_cast<uint8_t*>(ws);
     ScoreArgs a{logits, ld, tokens, n_rows, M, V, C, top, logprob, entropy, ids, lps, reinterpret_cast<unsigned*>(w), nullptr,
                 nullptr, err};
-    w += round256(static_cast<size_t>(M) * 4);
+    w += SC_HEADER;
     a.part = reinterpret_cast<float4*>(w);
-    w += round256(static_cast<size_t>(M) * C * sizeof(float4));
+    w += ctas(M, C) * C * SC_WARPS * sizeof(float4);
     a.keys = reinterpret_cast<Key*>(w);
-    const dim3 grid(static_cast<unsigned>(static_cast<long long>(M) * C));
-    trace_pre(s);
-    auto go = [&](auto kern) { launch_k(kern, grid, dim3(SC_THREADS), 0, s, a); };
-    if (f32) top ? go(logprobs_kernel<float, true>) : go(logprobs_kernel<float, false>);
-    else top ? go(logprobs_kernel<uint16_t, true>) : go(logprobs_kernel<uint16_t, false>);
+    int sms = 0;
+    if (xv_status st = device_sm_count(&sms)) return st;
+    auto go = [&](auto kern, int smem, int per_sm) -> xv_status {
+        if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(kern), smem, true, "logprobs: set shared memory size")) return st;
+        const size_t grid = std::min(ctas(M, C), static_cast<size_t>(sms) * per_sm);
+        trace_pre(s);
+        launch_k(kern, dim3(static_cast<unsigned>(grid)), dim3(SC_THREADS + 32), smem, s, a);
+        return XV_OK;
+    };
+    using F = Ring<float>;
+    using H = Ring<uint16_t>;
+    if (xv_status st = f32 ? (top ? go(logprobs_kernel<float, true>, F::SMEM, F::PER_SM) : go(logprobs_kernel<float, false>, F::SMEM, F::PER_SM))
+                           : (top ? go(logprobs_kernel<uint16_t, true>, H::SMEM, H::PER_SM)
+                                  : go(logprobs_kernel<uint16_t, false>, H::SMEM, H::PER_SM)))
+        return st;
     return launched("logprobs_kernel", s, K_LOGPROBS, (f32 ? 4ll : 2ll) * M * V + M * (12ll + 8 * top));
 }
 
@@ -356,8 +418,9 @@ extern "C" {
 
 size_t xv_logprobs_workspace_size(int M, int V, int top) {
     if (!sizes_ok(M, V, top)) return 0;
-    const size_t n = static_cast<size_t>(M) * ceil_div(V, SC_CHUNK);
-    return round256(static_cast<size_t>(M) * 4) + round256(n * sizeof(float4)) + round256(n * top * sizeof(Key));
+    const int C = ceil_div(V, SC_CHUNK);
+    const size_t n = ctas(M, C);
+    return SC_HEADER + round256(n * C * SC_WARPS * sizeof(float4) + 2 * n * top * sizeof(Key));
 }
 
 xv_status xv_logprobs(const float* logits, long long ld, const int32_t* tokens, const int32_t* n_rows, int M, int V,
