@@ -167,6 +167,30 @@ def test_append_codes_and_scales(xv, Hkv, hd, paged):
         assert torch.equal(got, w)
 
 
+def test_every_quotient_of_two_significands(xv):
+    """Codes of all values of 8 bits of significand down to 2^-18 of the largest, for every largest: borders of
+    two codes are hit exactly, and missed by 2^-13 at least."""
+    hd, Hkv = 256, 1
+    m = 1 + torch.arange(128, device="cuda", dtype=torch.float64) / 128
+    e = torch.tensor([2.0 ** -i for i in range(19)], dtype=torch.float64, device="cuda")
+    values = (m[None] * e[:, None]).reshape(-1)                       # all in [2^-18, 2)
+    rows = []
+    for big in m.tolist():
+        v = values[values <= big]
+        v = torch.nn.functional.pad(v, (0, -v.numel() % (hd - 1))).reshape(-1, hd - 1)
+        rows.append(torch.cat([torch.full((v.shape[0], 1), big, device="cuda", dtype=torch.float64), v], 1))
+    x = torch.cat(rows)
+    x[:, 2::2] *= -1
+    N = x.shape[0]
+    c = Cache(xv, 1, Hkv, N, hd)
+    src = torch.cat([x, x.flip(1)], 1).to(torch.bfloat16)
+    assert torch.equal(src[:, :hd].double(), x)
+    xv.xv_kv_append_q8(src, i32([1]), N, 1, Hkv, hd, N, c.q8)
+    codes = (x * 448 / x.abs().amax(-1, keepdim=True)).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    for got, want in ((c.k[0, 0], codes), (c.v[0, 0], codes.flip(1))):
+        assert torch.equal(torch.where(got == 128, 0, got), torch.where(want == 128, 0, want))
+
+
 def test_append_of_values_that_are_not_finite(xv):
     B, R, Hkv, hd, page = 1, 4, 2, 64, 64
     c = Cache(xv, 1, Hkv, page, hd)
