@@ -34,7 +34,8 @@
 // Kernel 1 (attn_q8_kernel): work items (slot, row tile, kv head, sequence); a slot is a split, or
 // with a window one of the splits that the window and the sinks can touch.  One CTA per item where
 // all fit at once, else persistent CTAs that walk contiguous ranges of equal cost.  Kernel 2
-// (attn_q8_combine_kernel) joins each row's splits.
+// (attn_q8_combine_kernel) joins each row's splits,
+// where there are several.
 #include <algorithm>
 #include <cmath>
 
@@ -114,6 +115,7 @@ struct Q8Args {
     int nslot, nsink;    // slots per row, of which the first nsink are the sinks' splits
     int max_len, window, sinks;
     int shift;           // the window, where the slots past the sinks' begin at it; 0: slots are splits
+    int joined;          // nslot = 1, and each CTA makes its rows' output of their only split
     float sl2;           // scale * log2(e)
     float* opart;        // [B*R*Hq][nslot][HD]
     float2* ml;          // [B*R*Hq][nslot]
@@ -496,6 +498,73 @@ __device__ __forceinline__ int warp_sums(float* v, int lane, int* first) {
     }
 }
 
+struct CombineArgs {
+    const int32_t* ctx_len;
+    const int32_t* n_rows;
+    int R, Hq, nslot, nsink, max_len, window, sinks, shift;
+    const float* opart;
+    const float2* ml;
+    const uint16_t* gate;
+    long long gate_stride;
+    uint16_t* out;
+    long long out_stride;
+};
+
+constexpr int CB_SUMS = 16;   // a row's splits are joined in so many sums
+
+// The slots of a row that hold what it sees: those of the sinks it sees beside its window, then its window's.
+struct RowSlots {
+    int first, nsink, n0, s0, n;
+    __device__ __forceinline__ RowSlots(const CombineArgs& C, int L0, int r) {
+        const int len = L0 + r, from = C.window ? max(0, len - C.window) : 0, upto = min(C.sinks, from);
+        first = q8_first(L0, C.shift, C.nsink);
+        nsink = C.nsink;
+        n0 = upto ? q8_split_of(upto - 1) + 1 : 0;   // splits with a sink
+        s0 = max(n0, q8_split_of(from));
+        n = n0 + q8_split_of(len - 1) + 1 - s0;
+    }
+    __device__ __forceinline__ int operator[](int i) const {
+        const int s = i < n0 ? i : s0 + i - n0;
+        return s < nsink ? s : s - first + nsink;
+    }
+};
+// Whether row r of sequence b is there (L0: the first row's length).
+__device__ __forceinline__ bool q8_row(const CombineArgs& C, int b, int r, int* L0) {
+    const int nr = q8_rows(C.n_rows, b, C.R);
+    *L0 = C.ctx_len[b];
+    return r < nr && *L0 >= 1 && *L0 <= C.max_len - nr + 1;
+}
+// Four dims of a row's output from their sum and the weights': br = b R + r.
+template <int HD>
+__device__ __forceinline__ void q8_output(const CombineArgs& C, int br, int hq, int dim, float4 y, float sum) {
+    // one reciprocal, as its rounding and the product's are far below the output's
+    const float inv = __frcp_rn(sum);
+    float out[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = __fadd_rn(__fmul_rn(out[e], inv), 0.f);
+    if (C.gate) {
+        const uint2 g = *reinterpret_cast<const uint2*>(C.gate + br * C.gate_stride + hq * HD + dim);
+        const float gv[4] = {__uint_as_float(g.x << 16), __uint_as_float(g.x & 0xffff0000u), __uint_as_float(g.y << 16),
+                             __uint_as_float(g.y & 0xffff0000u)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = __fmul_rn(out[e], __frcp_rn(__fadd_rn(1.f, expf(-gv[e]))));
+    }
+    *reinterpret_cast<uint2*>(C.out + br * C.out_stride + hq * HD + dim) = make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
+}
+// Four dims of a row whose only slot is 0: the bits that attn_q8_combine_kernel gives for one slot.
+template <int HD>
+__device__ __forceinline__ void q8_join_one(const CombineArgs& C, int b, int r, int hq, int dim) {
+    int L0;
+    if (!q8_row(C, b, r, &L0)) return;
+    const int br = b * C.R + r;
+    const long long row = static_cast<long long>(br) * C.Hq + hq;
+    const float2 v = __ldcg(C.ml + row);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(C.opart + row * HD + dim));
+    const float w = ex2_approx(__fsub_rn(v.x, v.x));   // 1, or NaN
+    const float4 y = make_float4(__fmaf_rn(w, o.x, 0.f), __fmaf_rn(w, o.y, 0.f), __fmaf_rn(w, o.z, 0.f), __fmaf_rn(w, o.w, 0.f));
+    q8_output<HD>(C, br, hq, dim, y, __fmaf_rn(w, v.y, 0.f));
+}
+
 // Warps of a CTA and what they do per tile t (counted over the CTA's items):
 //   0..4 WG - 1   softmax, warpgroup w for rows RW w.., a thread per position: S out of tensor memory,
 //          t_j, mask; the references stand unless some row's t_j passes its by RESCALE_SLACK (or the
@@ -510,7 +579,8 @@ __device__ __forceinline__ int warp_sums(float* v, int lane, int* first) {
 //          the items itself the code outgrew the instruction caches: 113 KB, and 20 cycles an instruction.)
 template <int HD, int NR>
 __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
-    attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args A) {
+    attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args A,
+                   const __grid_constant__ CombineArgs C) {
     griddep_launch();
     using S = Shape<HD, NR>;
     constexpr int SK = S::SK, SV = S::SV, RAW = S::RAW, PB = S::PB, RW = S::RW, WG = S::WG;
@@ -791,18 +861,25 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
             if (!WW(mlready, n & 1u) || !WW(pfree(tl % PB), (tl / PB) & 1u)) break;
             tc_fence_after();
             if (HD >= 128 || warp < W_OUT + 2) {
+                constexpr int CH = RW;   // rows at a time: a warpgroup's
 #pragma unroll 1
-                for (int c = 0; c < S::MB * NR; c += 8) {
+                for (int c = 0; c < S::MB * NR; c += CH) {
                     const int mb = c / NR, r0 = c % NR;
                     if (r0 >= rows) continue;
-                    float a[8], b[8];
-                    const uint32_t col = tO + lane_off + mb * 2 * NR + r0 / RW * 2 * RW + r0 % RW;
-                    tmem_ld8(col, a);
-                    tmem_ld8(col + RW, b);
+                    float a[CH], b[CH];
+                    const uint32_t col = tO + lane_off + mb * 2 * NR + 2 * r0;
+                    if constexpr (CH == 16) {
+                        tmem_ld16(col, a);
+                        tmem_ld16(col + RW, b);
+                    } else {
+                        tmem_ld8(col, a);
+                        tmem_ld8(col + RW, b);
+                    }
                     tmem_ld_wait();
+                    float* out = A.opart + mb * 128 + d;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (r0 + e < rows) A.opart[at_sm[r0 + e] * HD + mb * 128 + d] = __fmaf_rn(b[e], 1.f / LOW_SCALE, a[e]);
+                    for (int e = 0; e < CH; ++e)
+                        if (r0 + e < rows) out[at_sm[r0 + e] * HD] = __fmaf_rn(b[e], 1.f / LOW_SCALE, a[e]);
                 }
             }
             if (d < rows)
@@ -993,25 +1070,21 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
         tc_fence_after();
         tmem_dealloc(tS, S::TMEM_COLS);
     }
+    if (A.joined) {
+        __threadfence_block();
+        const int rt = blockIdx.x % A.nrt, g = blockIdx.x / A.nrt % A.Hkv, b = blockIdx.x / A.nrt / A.Hkv;
+        const int last = min((rt + 1) * A.tile_rows, A.R * A.G);
+        for (int k = tid; k < A.tile_rows * (HD / 4); k += S::THREADS) {
+            const int gr = rt * A.tile_rows + k / (HD / 4), r = gr / A.G;
+            if (gr < last) q8_join_one<HD>(C, b, r, g * A.G + gr - r * A.G, k % (HD / 4) * 4);
+        }
+    }
 }
-
-struct CombineArgs {
-    const int32_t* ctx_len;
-    const int32_t* n_rows;
-    int R, Hq, nslot, nsink, max_len, window, sinks, shift;
-    const float* opart;
-    const float2* ml;
-    const uint16_t* gate;
-    long long gate_stride;
-    uint16_t* out;
-    long long out_stride;
-};
 
 // One CTA per (row, q head): w_s = 2^(m_s - M) over the row's live slots s in order, out = sum w_s O_s /
 // sum w_s l_s.  The i-th of them belongs to the sum of residue i mod CB_SUMS, and those sums are added in
 // order: fixed by the row alone, whether G = 4 groups of threads have 4 residues each (few slots: a
 // batch's rows fit the machine) or 16 have one (many: a row's loads are in flight together).
-constexpr int CB_SUMS = 16;
 constexpr int CB_SLOTS = 1 << 10;   // slots whose m and l are staged at a time
 
 template <int HD, int G>
@@ -1023,24 +1096,16 @@ __global__ void __launch_bounds__(G* HD / 4) attn_q8_combine_kernel(const __grid
     __shared__ float4 acc_sm[CB_SUMS][LN];
     __shared__ float l_sm[CB_SUMS], wmax[NT / 32];
     const int row = blockIdx.x, br = row / C.Hq, hq = row - br * C.Hq, b = br / C.R, r = br - b * C.R, tid = threadIdx.x;
-    const int nr = q8_rows(C.n_rows, b, C.R), L0 = C.ctx_len[b];
-    if (r >= nr || L0 < 1 || L0 > C.max_len - nr + 1) return;
-    const int len = L0 + r;
-    // the row's slots: those of the sinks it sees beside its window, then its window's
-    const int first = q8_first(L0, C.shift, C.nsink);
-    const int from = C.window ? max(0, len - C.window) : 0, upto = min(C.sinks, from);
-    const int n0 = upto ? q8_split_of(upto - 1) + 1 : 0;             // splits with a sink
-    const int s0 = max(n0, q8_split_of(from)), ns = n0 + q8_split_of(len - 1) + 1 - s0;
-    auto slot = [&](int i) {
-        const int s = i < n0 ? i : s0 + i - n0;
-        return s < C.nsink ? s : s - first + C.nsink;
-    };
+    int L0;
+    if (!q8_row(C, b, r, &L0)) return;
+    const RowSlots slot(C, L0, r);
+    const int ns = slot.n;
     const float2* ml = C.ml + static_cast<long long>(row) * C.nslot;
     const float4* op = reinterpret_cast<const float4*>(C.opart + static_cast<long long>(row) * C.nslot * HD) + tid % LN;
     float M = NEG_INF;
 #pragma unroll 1
     for (int i = tid; i < ns; i += NT) {
-        const float2 v = __ldcg(ml + slot(i));
+        const float2 v = __ldcg(ml + slot[i]);
         if (i < CB_SLOTS) wl[i] = v;
         M = fmaxf(M, v.x);
     }
@@ -1061,7 +1126,7 @@ __global__ void __launch_bounds__(G* HD / 4) attn_q8_combine_kernel(const __grid
         const int n = min(CB_SLOTS, ns - c0);
         if (c0) {
             __syncthreads();
-            for (int i = tid; i < n; i += NT) wl[i] = __ldcg(ml + slot(c0 + i));
+            for (int i = tid; i < n; i += NT) wl[i] = __ldcg(ml + slot[c0 + i]);
             __syncthreads();
         }
         constexpr int UN = 8 / PER;   // 8 loads in flight
@@ -1073,7 +1138,7 @@ __global__ void __launch_bounds__(G* HD / 4) attn_q8_combine_kernel(const __grid
 #pragma unroll
                 for (int k = 0; k < PER; ++k) {
                     const int i = i0 + u * CB_SUMS + grp + k * G;
-                    if (i < n) o[u][k] = __ldcg(op + static_cast<long long>(slot(c0 + i)) * LN);
+                    if (i < n) o[u][k] = __ldcg(op + static_cast<long long>(slot[c0 + i]) * LN);
                 }
 #pragma unroll
             for (int u = 0; u < UN; ++u)
@@ -1105,20 +1170,7 @@ __global__ void __launch_bounds__(G* HD / 4) attn_q8_combine_kernel(const __grid
         sum = __fadd_rn(sum, l_sm[g]);
         y.x = __fadd_rn(y.x, o.x), y.y = __fadd_rn(y.y, o.y), y.z = __fadd_rn(y.z, o.z), y.w = __fadd_rn(y.w, o.w);
     }
-    // one reciprocal, as its rounding and the product's are far below the output's
-    const float inv = __frcp_rn(sum);
-    float out[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = __fadd_rn(__fmul_rn(out[e], inv), 0.f);
-    if (C.gate) {
-        const uint2 g = *reinterpret_cast<const uint2*>(C.gate + br * C.gate_stride + hq * HD + 4 * tid);
-        const float gv[4] = {__uint_as_float(g.x << 16), __uint_as_float(g.x & 0xffff0000u), __uint_as_float(g.y << 16),
-                             __uint_as_float(g.y & 0xffff0000u)};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = __fmul_rn(out[e], __frcp_rn(__fadd_rn(1.f, expf(-gv[e]))));
-    }
-    *reinterpret_cast<uint2*>(C.out + br * C.out_stride + hq * HD + 4 * tid) =
-        make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
+    q8_output<HD>(C, br, hq, 4 * tid, y, sum);
 }
 
 inline size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1145,31 +1197,37 @@ inline bool sizes_ok(int B, int R, int Hq, int hd, int max_ctx, int window, int 
 inline int row_tiles(int rows) { return (rows + 63) / 64; }
 
 template <int HD, int NR>
-xv_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a, cudaStream_t s) {
+xv_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, Q8Args& a, const CombineArgs& c, cudaStream_t s) {
     using S = Shape<HD, NR>;
+    const auto kern = attn_q8_kernel<HD, NR>;
+    const void* fn = reinterpret_cast<const void*>(kern);
     int sms = 0;
-    if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(attn_q8_kernel<HD, NR>), S::SMEM, true, "attn_q8: set shared memory size"))
-        return st;
+    if (xv_status st = kernel_smem_once(fn, S::SMEM, true, "attn_q8: set shared memory size")) return st;
     if (xv_status st = device_sm_count(&sms)) return st;
-    const long long n_items = static_cast<long long>(a.nslot) * a.nrt * a.Hkv * a.B;
+    const long long n_tiles = static_cast<long long>(a.nrt) * a.Hkv * a.B, n_items = n_tiles * a.nslot;
     if (n_items > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "attn_q8: %lld work items", n_items);
     const int room = sms * S::PER_SM;
+    // The only split of each row is its output: a second kernel would begin 1.5 to 3 us after the first
+    // one's end (one token at 128: 6.9 us with it, 6.3 us without; clusters that join up to 16 splits took
+    // 15.2 us for one verify at 2183, the second kernel 14.6)
+    a.joined = n_items <= room && a.nslot == 1;
     trace_pre(s);
-    launch_k(attn_q8_kernel<HD, NR>, dim3(static_cast<unsigned>(std::min<long long>(room, n_items))), dim3(S::THREADS), S::SMEM, s, tmK, tmV, a);
+    launch_k(kern, dim3(static_cast<unsigned>(std::min<long long>(room, n_items))), dim3(S::THREADS), S::SMEM, s, tmK, tmV, a, c);
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq, seen = a.window && a.window < a.max_len ? a.window + a.sinks : a.max_len;
     return launched("attn_q8_kernel", s, K_ATTN_Q8, (2ll * HD + 8) * a.B * a.Hkv * seen + 2 * rows * HD + 4 * rows * a.nslot * (HD + 2));
 }
 
 template <int HD>
-xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const Q8Args& a, const CombineArgs& c, cudaStream_t s) {
+xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, Q8Args& a, const CombineArgs& c, cudaStream_t s) {
     const int n = a.tile_rows;
-    if (xv_status st = n <= 8    ? launch_attn<HD, 8>(tmK, tmV, a, s)
-                       : n <= 16 ? launch_attn<HD, 16>(tmK, tmV, a, s)
-                       : n <= 24 ? launch_attn<HD, 24>(tmK, tmV, a, s)
-                       : n <= 32 ? launch_attn<HD, 32>(tmK, tmV, a, s)
-                       : n <= 48 ? launch_attn<HD, 48>(tmK, tmV, a, s)
-                                 : launch_attn<HD, 64>(tmK, tmV, a, s))
+    if (xv_status st = n <= 8    ? launch_attn<HD, 8>(tmK, tmV, a, c, s)
+                       : n <= 16 ? launch_attn<HD, 16>(tmK, tmV, a, c, s)
+                       : n <= 24 ? launch_attn<HD, 24>(tmK, tmV, a, c, s)
+                       : n <= 32 ? launch_attn<HD, 32>(tmK, tmV, a, c, s)
+                       : n <= 48 ? launch_attn<HD, 48>(tmK, tmV, a, c, s)
+                                 : launch_attn<HD, 64>(tmK, tmV, a, c, s))
         return st;
+    if (a.joined) return XV_OK;
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq;
     trace_pre(s);
     if (a.nslot <= 2 * CB_SUMS) launch_k(attn_q8_combine_kernel<HD, 4>, dim3(static_cast<unsigned>(rows)), dim3(HD), 0, s, c);
@@ -1213,8 +1271,8 @@ xv_status attn_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, 
     float* opart = static_cast<float*>(ws);
     float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + round256(rows * hd * sizeof(float)));
     const int grp = R * (Hq / Hkv), nrt = row_tiles(grp);
-    const Q8Args a{q, q_stride, kv, cache->k_scale, cache->v_scale, ctx_len, n_rows, R, Hq / Hkv, Hq, Hkv, B,
-                   (grp + nrt - 1) / nrt, nrt, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, scale * 1.4426950408889634f, opart, ml, err};
+    Q8Args a{q, q_stride, kv, cache->k_scale, cache->v_scale, ctx_len, n_rows, R, Hq / Hkv, Hq, Hkv, B,
+                   (grp + nrt - 1) / nrt, nrt, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, 0, scale * 1.4426950408889634f, opart, ml, err};
     const CombineArgs c{ctx_len, n_rows, R, Hq, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, opart, ml, gate, gate_stride, out,
                         out_stride};
     return hd == 256 ? launch<256>(tmK, tmV, a, c, s) : hd == 128 ? launch<128>(tmK, tmV, a, c, s) : launch<64>(tmK, tmV, a, c, s);
