@@ -112,6 +112,7 @@ struct Q8Args {
     const int32_t* n_rows;
     int R, G, Hq, Hkv, B;
     int tile_rows, nrt;  // rows of a row tile, row tiles
+    Divisor by_g, by_nrt, by_hkv, by_nslot, by_page;
     int nslot, nsink;    // slots per row, of which the first nsink are the sinks' splits
     int max_len, window, sinks;
     int shift;           // the window, where the slots past the sinks' begin at it; 0: slots are splits
@@ -145,8 +146,8 @@ struct Sight {
         end = lo = sinks = from = upto = 0;
         if (rows <= 0) return;
         // what other rows see beside a row changes nothing of it
-        end = L0 + (row_base + rows - 1) / A.G;
-        upto = L0 + row_base / A.G;
+        end = L0 + A.by_g.div(row_base + rows - 1);
+        upto = L0 + A.by_g.div(row_base);
         if (A.window) from = max(0, end - A.window);
         if (A.window && upto > A.window) lo = upto - A.window, sinks = A.sinks;
     }
@@ -187,13 +188,12 @@ struct Item {
     // the first live item of [i, it1); false if there is none
     __device__ __forceinline__ bool open(const Q8Args& A, int i, int it1) {
         it = i;
-        slot = i % A.nslot;
-        int rest = i / A.nslot;
-        rt = rest % A.nrt;
-        rest /= A.nrt;
-        g = rest % A.Hkv;
-        b = rest / A.Hkv;
         if (it >= it1) return false;
+        const int tile = A.by_nslot.div(i), head = A.by_nrt.div(tile);
+        slot = i - tile * A.nslot;
+        rt = tile - head * A.nrt;
+        b = A.by_hkv.div(head);
+        g = head - b * A.Hkv;
         sight(A);
         place(A);
         return ntiles > 0 || next(A, it1);
@@ -219,21 +219,23 @@ struct Item {
     __device__ __forceinline__ bool same_q(const Item& o) const { return b == o.b && g == o.g && rt == o.rt; }
 };
 
-// The items [it[0], it[1]) of persistent CTA c of n: equal shares of the cost.  One warp.
+// The items [it[0], it[1]) of persistent CTA c of n: equal shares of the cost.  One warp.  (What it takes
+// the CTA waits for: with divisions in 64 bits and a look at the same sequence three times 3.5 us.)
 __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it) {
     const int lane = threadIdx.x & 31;
-    long long total = 0, before = 0, at[2];
+    long long total = 0, before = 0, at0 = 0, at1 = 0;
     it[0] = it[1] = A.nslot * A.nrt * A.Hkv * A.B;   // where no cost is left
 #pragma unroll 1
     for (int pass = A.B > 32 ? 0 : 1; pass < 2; ++pass) {   // the total, which 32 sequences show at once; the shares
 #pragma unroll 1
         for (int b0 = 0; b0 < A.B; b0 += 32) {
             Sight v;
+            v.rows = 0;
             int one = 0, tiles = 0;   // cost of a row tile of a head, live row tiles
             if (b0 + lane < A.B) v.of(A, b0 + lane, 0);
-            if (b0 + lane < A.B && v.rows > 0) {
+            if (v.rows > 0) {
                 one = v.cost(1 << 24);
-                tiles = v.rows < A.tile_rows ? 1 : (q8_rows(A.n_rows, b0 + lane, A.R) * A.G + A.tile_rows - 1) / A.tile_rows;
+                tiles = A.nrt == 1 ? 1 : (q8_rows(A.n_rows, b0 + lane, A.R) * A.G + A.tile_rows - 1) / A.tile_rows;
             }
             long long x = static_cast<long long>(one) * (tiles * A.Hkv);
 #pragma unroll
@@ -244,18 +246,27 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
             const long long all = __shfl_sync(0xffffffffu, x, 31);
             if (pass == 0 || A.B <= 32) total += all;
             if (pass == 0) continue;
-            if (b0 == 0) at[0] = total * c / n, at[1] = total * (c + 1) / n;
+            if (b0 == 0) {   // shares of total / n, the first total % n of them one more
+                const bool small = total < (1ll << 31);
+                const long long share = small ? static_cast<unsigned>(total) / static_cast<unsigned>(n) : total / n;
+                const int more = static_cast<int>(total - share * n);
+                at0 = share * c + min(c, more);
+                at1 = share * (c + 1) + min(c + 1, more);
+            }
             // an item belongs to the CTA in whose share its cost begins
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
-                long long off = at[e] - before;
+                long long off = (e ? at1 : at0) - before;
                 if (off < 0 || off >= all) continue;
                 const int own = __ffs(__ballot_sync(0xffffffffu, x > off)) - 1;
                 off -= own ? __shfl_sync(0xffffffffu, x, own - 1) : 0;
                 const int o1 = __shfl_sync(0xffffffffu, one, own), tl = __shfl_sync(0xffffffffu, tiles, own);
                 const int pair = static_cast<int>(off) / o1, in = static_cast<int>(off) - pair * o1;   // (head, row tile), cost in it
                 Sight w;
-                w.of(A, b0 + own, 0);
+                w.L0 = __shfl_sync(0xffffffffu, v.L0, own);
+                w.end = __shfl_sync(0xffffffffu, v.end, own);
+                w.lo = __shfl_sync(0xffffffffu, v.lo, own);
+                w.sinks = __shfl_sync(0xffffffffu, v.sinks, own);
                 const int first = q8_first(w.L0, A.shift, A.nsink);
                 int slot = 0;   // the first whose cost begins at `in` or later
 #pragma unroll 1
@@ -264,7 +275,7 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
                     slot += __popc(less);
                     if (less != 0xffffffffu) break;
                 }
-                const int h = pair / tl;
+                const int h = tl == 1 ? pair : pair / tl;
                 it[e] = (((b0 + own) * A.Hkv + h) * A.nrt + pair - h * tl) * A.nslot + slot;
             }
             before += all;
@@ -331,7 +342,7 @@ __device__ __forceinline__ void load_q(uint8_t* sq, float* fac, const Q8Args& A,
             const int row = r0 + k * RPP + t0 / LPH;
             v[k] = make_uint4(0, 0, 0, 0);
             if (row < n) {
-                const int r = (I.v.row_base + row) / A.G, h = I.g * A.G + (I.v.row_base + row) % A.G;
+                const int r = A.by_g.div(I.v.row_base + row), h = I.g * A.G + I.v.row_base + row - r * A.G;
                 v[k] = *reinterpret_cast<const uint4*>(A.q + (static_cast<long long>(I.b) * A.R + r) * A.q_stride +
                                                        static_cast<long long>(h) * HD + c * 8);
             }
@@ -656,11 +667,8 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
 
     if (warp == W_IT) {
         // ---- items
-        const int n_items = A.nslot * A.nrt * A.Hkv * A.B, per_slot = n_items / A.nslot;
-        // one item per CTA: slots slowest, so that a row's last splits, often short, come last
-        int it[2] = {static_cast<int>(blockIdx.x) % per_slot * A.nslot + static_cast<int>(blockIdx.x) / per_slot, 0};
-        it[1] = it[0] + 1;
-        if (static_cast<int>(gridDim.x) < n_items) q8_range(A, blockIdx.x, gridDim.x, it);
+        int it[2] = {static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.x) + 1};   // one item per CTA
+        if (static_cast<int>(gridDim.x) < A.nslot * A.nrt * A.Hkv * A.B) q8_range(A, blockIdx.x, gridDim.x, it);
         Item I;
         bool more = I.open(A, it[0], it[1]), fresh = true;
         for (int n = 0;; ++n) {
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
             if (lane < 2 * I.ntiles && I.v.half(p)) {
                 int page = I.b;
                 if (A.kv.table) {
-                    const int j = p / A.kv.page;
+                    const int j = A.by_page.div(p);
                     row = p - j * A.kv.page;
                     page = A.kv.table[static_cast<long long>(I.b) * A.kv.max_pages + j];
                     if (page < 0 || page >= A.kv.n_pages) {
@@ -904,7 +912,7 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
                 load_q<HD, NR, 128 * WG>(smem + S::Q_OFF, q_fac[(nq + 1) & 1], A, I, tid);
                 fence_proxy_async_smem();
                 mbar_arrive(qready);
-                const int gr = I.v.row_base + r_wg + pt, r = gr / A.G;
+                const int gr = I.v.row_base + r_wg + pt, r = A.by_g.div(gr);
                 at = ((static_cast<long long>(I.b) * A.R + r) * A.Hq + I.g * A.G + gr - r * A.G) * A.nslot;
                 WW(qready, nq & 1u);   // the other warps' factors too
                 ++nq;
@@ -1272,7 +1280,7 @@ xv_status attn_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, 
     float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + round256(rows * hd * sizeof(float)));
     const int grp = R * (Hq / Hkv), nrt = row_tiles(grp);
     Q8Args a{q, q_stride, kv, cache->k_scale, cache->v_scale, ctx_len, n_rows, R, Hq / Hkv, Hq, Hkv, B,
-                   (grp + nrt - 1) / nrt, nrt, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, 0, scale * 1.4426950408889634f, opart, ml, err};
+             (grp + nrt - 1) / nrt, nrt, Divisor(Hq / Hkv), Divisor(nrt), Divisor(Hkv), Divisor(nslot), Divisor(kv.page), nslot, nsink, max_ctx, win, win ? sinks : 0, shift, 0, scale * 1.4426950408889634f, opart, ml, err};
     const CombineArgs c{ctx_len, n_rows, R, Hq, nslot, nsink, max_ctx, win, win ? sinks : 0, shift, opart, ml, gate, gate_stride, out,
                         out_stride};
     return hd == 256 ? launch<256>(tmK, tmV, a, c, s) : hd == 128 ? launch<128>(tmK, tmV, a, c, s) : launch<64>(tmK, tmV, a, c, s);

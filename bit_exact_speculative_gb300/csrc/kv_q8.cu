@@ -25,22 +25,6 @@
 namespace xv {
 namespace {
 
-// n / d for n < 2^31 by a multiplication (Granlund and Montgomery, 1994): with 2^l >= d and m = ceil(2^(31 + l) / d),
-// n m / 2^(31 + l) exceeds n / d by less than n 2^l / (d 2^(31 + l)) < 1 / d.
-struct Divisor {
-    uint32_t m;
-    int shift;
-    explicit Divisor(int d) {
-        int l = 0;
-        while ((1ll << l) < d) ++l;
-        shift = 31 + l;
-        m = static_cast<uint32_t>(((1ull << shift) + d - 1) / d);
-    }
-    __device__ __forceinline__ int div(int n) const {
-        return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(n)) * m >> shift);
-    }
-};
-
 struct AppendQ8Args {
     const uint16_t* src;
     long long src_stride;
