@@ -1237,9 +1237,14 @@ xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, Q8Args& a, cons
         return st;
     if (a.joined) return XV_OK;
     const long long rows = static_cast<long long>(a.B) * a.R * a.Hq;
-    trace_pre(s);
-    if (a.nslot <= 2 * CB_SUMS) launch_k(attn_q8_combine_kernel<HD, 4>, dim3(static_cast<unsigned>(rows)), dim3(HD), 0, s, c);
-    else launch_k(attn_q8_combine_kernel<HD, 16>, dim3(static_cast<unsigned>(rows)), dim3(4 * HD), 0, s, c);
+    // (with the first kernel's division of an SM's memory: another one would wait for the SMs to empty)
+    auto go = [&](auto kern, int threads) -> xv_status {
+        if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(kern), 0, true, "attn_q8: set shared memory size")) return st;
+        trace_pre(s);
+        launch_k(kern, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, c);
+        return XV_OK;
+    };
+    if (xv_status st = a.nslot <= 2 * CB_SUMS ? go(attn_q8_combine_kernel<HD, 4>, HD) : go(attn_q8_combine_kernel<HD, 16>, 4 * HD)) return st;
     return launched("attn_q8_combine_kernel", s, K_ATTN_Q8, 4 * rows * a.nslot * (HD + 2) + 2 * rows * HD * (c.gate ? 2 : 1));
 }
 

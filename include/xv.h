@@ -557,7 +557,8 @@ typedef struct {
 /* Quantises and writes the K and V rows of a step: row (b, r) of kv_src (k at
  * column 0, v at column Hkv*hd, row stride src_stride) goes to position
  * ctx_len[b] - 1 + r of sequence b, for r < n_rows[b] (device [B], 0..R; NULL: R
- * everywhere).  Other rows are not read, and nothing else is written.  Per head:
+ * everywhere).  Nothing else is written; kv_src holds B*R rows, all of which may
+ * be read.  Per head:
  *     den = min(max(max |x_i|, 448 2^-40), 448 2^60), scale = den / 448,
  *     code_i = e4m3(448 x_i / den)   (nearest, ties to even).
  * A head with a non-finite value gets the scale NaN and codes 0, and reads as
@@ -578,12 +579,13 @@ xv_status xv_kv_append_q8_paged(const uint16_t* kv_src, long long src_stride, co
  * rounded to bf16 once.  Rows from n_rows[b] on are neither read nor written.
  * Arguments as in xv_attn_decode_rows; n_rows as above.  A row's bits depend on
  * its own length, q and visible positions alone: positions are cut into splits
- * at fixed boundaries (xv_attn_q8_split_begin), tiles of 64 inside them, and the
+ * at fixed boundaries (xv_attn_q8_split_begin), tiles of 128 inside them, and the
  * splits joined in order, so a verify row has the bits of the decode row at its
- * position.  Only tiles with a visible position are read, so pages wholly before
- * every row's window (and past the sinks) may be given up.  q is held as two e4m3
- * terms (to 2^-18 of its row's largest value or 2^-9 of the value, whichever is larger),
- * weights in fp16 before their product with V, sums in fp32.  A row that sees a
+ * position.  Only runs of 64 positions with a visible one are read, so pages wholly
+ * before every row's window (and past the sinks) may be given up.  q is held as two
+ * e4m3 terms (to 2^-18 of its row's largest value or 2^-9 of the value, whichever is
+ * larger), weights in fp16 before their product with V (those below 2^-29 of the
+ * split's largest are 0), sums in fp32.  A row that sees a
  * NaN scale, or whose q is not finite, is NaN; other rows are not touched.  V
  * scales are taken to lie in [2^-40, 2^60] (clamped to it), codes not to be NaN.
  *   hd in {64, 128, 256}; 1 <= R <= XV_KMAX; Hq % Hkv == 0; window >= 0 (0:
@@ -622,9 +624,11 @@ xv_status xv_attn_decode_rows_q8_paged(const uint16_t* q, long long q_stride, co
  * in a call of any M, at any position.  A logit of -inf is a masked token (p = 0);
  * a row of nothing else has logprobs -inf and entropy 0; one with a NaN or +inf
  * has NaN logprobs and entropy.  n_rows: device count of rows to do (rows from
- * *n_rows on are left as they were), or NULL for all M.  Workspace:
- * xv_logprobs_workspace_size(M, V, top) bytes, 16-byte aligned, zero-filled once
- * (0 for sizes outside what the call takes).  Errors: XV_ERR_ARG (null pointer,
+ * *n_rows on are left as they were), or NULL for all M.  Rows are read in whole
+ * 16-byte pieces, those of their two ends included.  Workspace:
+ * xv_logprobs_workspace_size(M, V, top) bytes, 16-byte aligned, zero-filled once;
+ * calls of other sizes may use the same buffer, one after another (the size is 0
+ * for sizes outside what the call takes).  Errors: XV_ERR_ARG (null pointer,
  * M or V < 1, ld < V, top outside [0, V]), XV_ERR_UNSUPPORTED (top above
  * XV_TOP_MAX, V above 2^19, M * ceil(V / 8192) above 2^31, unaligned workspace),
  * XV_ERR_WORKSPACE, XV_ERR_CUDA.  A token outside [-1, V) is recorded (2) and its

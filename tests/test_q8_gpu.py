@@ -5,7 +5,8 @@ computed in calls of different shapes.
 Tolerance of an attention output (vs the 64-bit value over the same codes), per element:
     |err| <= 2^-8 |ref| + (2^-10 + 2^-12) A,   A = sum_j w_j |V_j|  (w the row's weights)
 The output's rounding to bf16 is half a step, 2^-8 of the value at most.  A weight before its product
-with V is rounded to fp16 (2^-11).  Its exponent t_j carries the score's errors: q's second e4m3 term
+with V is rounded to fp16 (2^-11; what is cut off below 2^-29 of the largest weight is at most
+8192 2^-29 = 2^-16 of A in these lengths).  Its exponent t_j carries the score's errors: q's second e4m3 term
 is off by at most 2^-18 of the row's largest value or 2^-9 of the value, whichever is larger, so the
 score by 2^-9 sum |q_d k_d| scale at worst and a random walk of hd such terms in fact; for q, k ~
 N(0, 1) at hd 64..256 that is 2^-9 0.6 rms(score) sqrt(2) ~ 2^-10 in the weight, and as the errors of
@@ -265,6 +266,25 @@ def test_rows_and_heads(xv, Hq, Hkv, hd, R):
     close(out, *reference(c, table, q, ctx, [R, R], R, Hq, Hkv, hd, 1280, 0, 0, hd ** -0.5))
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 7, 9])
+def test_row_tiles_of_every_size(xv, hd, R):
+    """8 to 72 rows of a kv head in a call, with and without a window, and each row's bits when it is alone."""
+    Hq, Hkv, page = 8, 1, 192
+    ctx, per = [3000, 129, 40], 17
+    c = Cache(xv, 3 * per, Hkv, page, hd)
+    table = shuffled(3, per, 3 * per, 10)
+    q = normal((3 * R, Hq * hd), R)
+    for window, sinks in ((0, 0), (200, 5)):
+        out = run(xv, c, table, q, ctx, R, Hq, Hkv, hd, page, 3 * per, per * page, window, sinks)
+        close(out, *reference(c, table, q, ctx, [R] * 3, R, Hq, Hkv, hd, page, window, sinks, hd ** -0.5))
+        for b in range(3):
+            one = run(xv, c, table[b:b + 1].contiguous(), q[b * R + R - 1:b * R + R].contiguous(), [ctx[b] + R - 1], 1, Hq, Hkv, hd, page,
+                      3 * per, ctx[b] + R - 1, window, sinks)
+            assert torch.equal(one.view(torch.int16), out[b * R + R - 1:b * R + R].view(torch.int16)), b
+    assert xv.xv_device_check() == 0
+
+
 @pytest.mark.parametrize("Lmax", [1, 2, 63, 65, 97, 1001])
 @pytest.mark.parametrize("Hq,Hkv,hd", HEADS)
 def test_contiguous_caches_of_any_length(xv, Lmax, Hq, Hkv, hd):
@@ -473,6 +493,33 @@ def test_many_items_per_cta(xv, hd, Hq, Hkv):
         out = run(xv, c, table, q, ctx, R, Hq, Hkv, hd, page, n_pages, 5001, window, sinks, counts=counts)
         assert xv.xv_device_check() == 0
         close(out, *reference(c, table, q, ctx, counts, R, Hq, Hkv, hd, page, window, sinks, hd ** -0.5))
+
+
+def test_many_sequences_with_bad_ones_among_them(xv):
+    """More sequences than one pass of the shares takes, in persistent CTAs: bad lengths, counts of 0 and bad
+    counts between good ones, which keep the bits they have alone."""
+    Hq, Hkv, hd, R, page, per, B = 16, 8, 128, 3, 64, 40, 70
+    n_pages = 500
+    c = Cache(xv, n_pages, Hkv, page, hd)
+    table = torch.randint(0, n_pages, (B, per), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    ctx = [2500 - 35 * b for b in range(B)]
+    counts = [3 - b % 4 for b in range(B)]
+    q = normal((B * R, Hq * hd), 21)
+    bad = {5: -7, 33: 0, 34: 2 ** 31 - 1, 69: 3000}
+    for b, v in bad.items():
+        ctx[b] = v
+    out = run(xv, c, table, q, ctx, R, Hq, Hkv, hd, page, n_pages, 2560, counts=counts, fill=5.0)
+    with pytest.raises(xv.XVError):
+        xv.xv_device_check()
+    for b in (0, 1, 4, 6, 32, 35, 66, 68):
+        n = counts[b]
+        if n:
+            one = run(xv, c, table[b:b + 1].contiguous(), q[b * R:b * R + n].contiguous(), [ctx[b]], n, Hq, Hkv, hd, page, n_pages, 2560)
+            assert torch.equal(one.view(torch.int16), out[b * R:b * R + n].view(torch.int16)), b
+        assert (out[b * R + n:(b + 1) * R] == 5).all()
+    for b in bad:
+        assert counts[b] == 0 or (out[b * R:(b + 1) * R] == 5).all()
+    assert xv.xv_device_check() == 0
 
 
 def test_a_captured_step_replayed_with_new_lengths_on_another_stream(xv):

@@ -177,6 +177,28 @@ def test_no_entropy_no_top_and_one_buffer_for_many_sizes(xv):
         assert torch.equal(lp, score(xv, x, t, 0)[0])
 
 
+def test_small_calls_before_large_ones_in_one_buffer(xv):
+    """What a call leaves in the workspace is nothing that another one counts on."""
+    ws = xv.workspace(xv.xv_logprobs_workspace_size(1000, 151936, 32))
+    for M, V, top in ((1, 151936, 20), (1000, 20000, 32), (3, 524288, 7), (700, 151936, 1), (2, 16385, 32), (1000, 20000, 5)):
+        x, t = logits(M, V, torch.float32, M + V), toks(M, V)
+        lp, en = torch.zeros(M, device="cuda"), torch.zeros(M, device="cuda")
+        ids, tl = torch.zeros((M, top), dtype=torch.int32, device="cuda"), torch.zeros((M, top), device="cuda")
+        xv.xv_logprobs(x, t, lp, ws, entropy=en, top_ids=ids, top_logprobs=tl)
+        for a, b in zip((lp, en, ids, tl), score(xv, x, t, top)):
+            assert torch.equal(a, b), (M, V)
+        assert torch.equal(ids, order(x, top))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [150, 151, 303, 305, 457, 613])
+def test_rows_over_the_borders_of_ctas(xv, M, dtype):
+    """Numbers of rows about the number of CTAs, chunks that do not divide among them."""
+    V, top = 33333, 9
+    x, t = logits(M, V, dtype, M), toks(M, V)
+    check(xv, x, t, top)
+
+
 def test_captured_and_replayed_on_another_stream(xv):
     M, V, top = 8, 151936, 20
     x, t = logits(M, V, torch.float32, 8), toks(M, V)
