@@ -26,7 +26,7 @@
 // Each warp keeps the 32 best of its shares of a row, one a lane, in order.  A logit has to pass the n-th
 // of them, and the smallest of the eight warps' (n / 8)-th: n logits reach that.  (In a row's first
 // chunk: their lanes' (n / 8)-th largest.)  A few that pass are put in one by one, more by a bitonic sort
-// and merge, and at a row's end the warps' lists are merged.  (With one list for the CTA, and a barrier a
+// and merge, and at a row's end the best of the warps' lists are taken.  (With one list for the CTA, and a barrier a
 // chunk for it, 2048 rows of 151936 took 234 us with n = 1, 290 us with n = 20.)
 #include <algorithm>
 #include <cmath>
@@ -38,6 +38,7 @@ namespace xv {
 namespace {
 
 constexpr int SC_THREADS = 256, SC_WARPS = SC_THREADS / 32;
+constexpr int SC_KEYS = 512;                        // lists' keys at a time
 constexpr int SC_PER = 32;                          // logits per thread
 constexpr int SC_CHUNK = SC_THREADS * SC_PER;
 constexpr int SC_V_MAX = 1 << 19;
@@ -45,7 +46,7 @@ constexpr int SC_C_MAX = SC_V_MAX / SC_CHUNK;
 constexpr int SC_G_MAX = 1024;                      // CTAs
 constexpr int SC_HEADER = SC_G_MAX * 4;             // their counters, wherever the rest lies
 constexpr float LOG2E = 1.4426950408889634f;
-static_assert(XV_TOP_MAX <= 32, "a lane each");
+static_assert(XV_TOP_MAX <= 32 && SC_WARPS == 8 && SC_KEYS >= 32 * SC_WARPS, "a lane each");
 
 // Ring of chunks: as many as fit beside the CTAs of an SM.
 template <typename T>
@@ -54,7 +55,7 @@ struct Ring {
     static constexpr int BYTES = SC_CHUNK * static_cast<int>(sizeof(T)) + 16;   // any alignment
     static constexpr int STRIDE = (BYTES + 127) / 128 * 128;
     static constexpr int SMEM = N * STRIDE + 128;
-    static_assert(PER_SM * (SMEM + 9 * 1024 + 1024) <= 228 * 1024, "");
+    static_assert(PER_SM * (SMEM + 11 * 1024 + 1024) <= 228 * 1024, "");
 };
 
 using Key = unsigned long long;   // (1 + order of the value) << 32 | ~index: larger is better, 0 is none
@@ -107,7 +108,24 @@ __device__ __forceinline__ Key bitonic_down(Key k, int lane) {
 __device__ __forceinline__ Key merge_best(Key list, Key backwards, int lane) {
     return bitonic_down(list > backwards ? list : backwards, lane);
 }
-__device__ __forceinline__ Key reversed(Key k, int lane) { return __shfl_sync(0xffffffffu, k, 31 - lane); }
+// The n best of a warp's sorted lists, one per lane, `have` keys long (0: none): n times the largest head.
+// The k-th best ends in lane k.
+__device__ __forceinline__ Key best_of_heads(const Key* list, int have, int n, int lane) {
+    Key h = have > 0 ? list[0] : 0, next = have > 1 ? list[1] : 0, mine = 0;
+    int at = 1;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        const unsigned hi = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(h >> 32));
+        const unsigned lo = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(h >> 32) == hi ? static_cast<unsigned>(h) : 0u);
+        const Key w = static_cast<Key>(hi) << 32 | lo;
+        if (lane == k) mine = w;
+        if (h == w) {
+            h = next;
+            next = ++at < have ? list[at] : 0;
+        }
+    }
+    return mine;
+}
 // Sorts a warp's keys, the smallest into lane 0.
 __device__ __forceinline__ Key sort_up(Key k, int lane) {
 #pragma unroll
@@ -121,6 +139,14 @@ __device__ __forceinline__ Key sort_up(Key k, int lane) {
     return k;
 }
 
+// The smallest of 8 words in shared memory, as they are now.
+__device__ __forceinline__ unsigned lowest(uint32_t at) {
+    uint4 a, b;
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(at) : "memory");
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(at + 16) : "memory");
+    return min(min(min(a.x, a.y), min(a.z, a.w)), min(min(b.x, b.y), min(b.z, b.w)));
+}
+
 // Barrier of the warps that compute.
 __device__ __forceinline__ void sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(SC_THREADS) : "memory"); }
 
@@ -130,8 +156,8 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
     using R = Ring<T>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[R::N], empty[R::N];
-    __shared__ Key lists[TOP ? SC_WARPS : 1][32];
-    __shared__ volatile unsigned floors[SC_WARPS];   // what part_n of a warp's logits reach
+    __shared__ Key lists[TOP ? SC_KEYS : 1];                 // of the warps at a row's end, or of other CTAs
+    __shared__ __align__(16) unsigned floors[SC_WARPS];     // what part_n of a warp's logits reach
     __shared__ float pm[SC_C_MAX * SC_WARPS], ps[SC_C_MAX * SC_WARPS], pd[SC_C_MAX * SC_WARPS];   // [chunk][warp]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, top = A.top, C = A.C;
     const uint32_t raw = smem_u32(smem_raw), ring = (raw + 127u) & ~127u;
@@ -204,16 +230,16 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
             // (0 where every logit of the thread is NaN, masked or behind the row)
             const unsigned need = static_cast<unsigned>(least >> 32), best = mx > -INFINITY ? order_of(mx) : 0u;
             if (c == first_c) {
-                int reach = 0;
-#pragma unroll 8
-                for (int k = 0; k < 32; ++k) reach += __shfl_sync(0xffffffffu, best, k) >= best;
-                floor = __reduce_max_sync(0xffffffffu, reach >= part_n ? best : 0u);
+                unsigned b = best;
+                for (int k = part_n;; --k) {   // the part_n-th largest
+                    floor = __reduce_max_sync(0xffffffffu, b);
+                    if (k == 1) break;
+                    if (lane == __ffs(__ballot_sync(0xffffffffu, b == floor)) - 1) b = 0;
+                }
                 if (lane == 0) floors[warp] = floor;
                 sync();   // and warp 0 has done with the row before
             }
-            unsigned pass = floors[0];
-#pragma unroll
-            for (int w = 1; w < SC_WARPS; ++w) pass = min(pass, floors[w]);
+            unsigned pass = lowest(smem_u32(floors));
             const bool some = best > need && best >= pass;
             pass = max(pass, need);
             const bool rest = pass <= order_of(-INFINITY);   // what is not a number above -inf counts, too
@@ -273,15 +299,11 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
             ++c;
             continue;
         }
-        if (TOP) lists[warp][lane] = list;
+        if (TOP) lists[warp * 32 + lane] = list;
         sync();
         if (warp == 0) {
             bool last = true;
-            if (TOP) {
-                auto two = [&](int w) { return merge_best(lists[w][lane], lists[w + 1][31 - lane], lane); };
-                const Key a = merge_best(two(0), reversed(two(2), lane), lane), b = merge_best(two(4), reversed(two(6), lane), lane);
-                list = merge_best(a, reversed(b, lane), lane);
-            }
+            if (TOP) list = best_of_heads(lists + lane * 32, lane < SC_WARPS ? top : 0, top, lane);
             if (first_c != 0 || !row_ends) {
                 // the row lies in CTAs a to z; ((i + 1) G - 1) / n_chunks is the CTA of chunk i
                 const long long r0 = static_cast<long long>(row) * C;
@@ -303,12 +325,21 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
                         pm[k] = q.x, ps[k] = q.y, pd[k] = q.z;
                     }
                     if (TOP) {
+                        // lane 0 has the list so far, the others a CTA's each
                         list = lane < top ? __ldcg(A.keys + (2ll * a + 1) * top + lane) : 0;
-                        for (int g = a + 1; g <= z; g += 4) {
-                            auto theirs = [&](int h, int j) { return h <= z && j < top ? __ldcg(A.keys + 2ll * h * top + j) : Key(0); };
-                            const Key q0 = theirs(g, lane), q1 = theirs(g + 1, 31 - lane), q2 = theirs(g + 2, lane), q3 = theirs(g + 3, 31 - lane);
-                            const Key q = merge_best(merge_best(q0, q1, lane), reversed(merge_best(q2, q3, lane), lane), lane);
-                            list = merge_best(list, reversed(q, lane), lane);
+                        const int most = min(31, SC_KEYS / top - 1);
+                        for (int g = a + 1; g <= z; g += most) {
+                            const int nl = min(most, z + 1 - g);
+                            if (lane < top) lists[lane] = list;
+                            // list h of the round, key j: after the first, in order
+#pragma unroll 8
+                            for (int k = lane; k < nl * top; k += 32) {
+                                const int h = k / top;
+                                lists[top + k] = __ldcg(A.keys + 2ll * (g + h) * top + k - h * top);
+                            }
+                            __syncwarp();
+                            list = best_of_heads(lists + lane * top, lane <= nl ? top : 0, top, lane);
+                            __syncwarp();
                         }
                     }
                     __syncwarp();
