@@ -19,9 +19,10 @@
 // memory's rate, and 54 us for 500 rows of 50257 bf16 logits, whose odd rows were read one by one.)
 //
 // The exponentials alone are 512 cycles a chunk and SM, where the memory's rate leaves 720 for bf16
-// logits, so what is done per logit and per chunk is kept small: one barrier a chunk, two logits an
-// instruction, no reduction wider than a warp before a row's end, a warp of its own for the ring.  What a row's end needs (the join, the
-// token's logit, the lists) is warp 0's alone, while the other warps take up the next chunk.
+// logits, so what is done per logit and per chunk is kept small: no barrier but one a row, two logits an
+// instruction, no reduction wider than a warp before a row's end, a warp of its own for the ring and one
+// for the ends of rows (the join, the token's logit, the lists), while the others go on with the next
+// row: 500 rows of 50257 bf16 logits took 33 us with a row's end in one of the computing warps.
 //
 // Each warp keeps the 32 best of its shares of a row, one a lane, in order.  A logit has to pass the n-th
 // of them, and the smallest of the eight warps' (n / 8)-th: n logits reach that.  (In a row's first
@@ -55,7 +56,7 @@ struct Ring {
     static constexpr int BYTES = SC_CHUNK * static_cast<int>(sizeof(T)) + 16;   // any alignment
     static constexpr int STRIDE = (BYTES + 127) / 128 * 128;
     static constexpr int SMEM = N * STRIDE + 128;
-    static_assert(PER_SM * (SMEM + 11 * 1024 + 1024) <= 228 * 1024, "");
+    static_assert(PER_SM * (SMEM + 15 * 1024 + 1024) <= 228 * 1024, "");
 };
 
 using Key = unsigned long long;   // (1 + order of the value) << 32 | ~index: larger is better, 0 is none
@@ -151,19 +152,20 @@ __device__ __forceinline__ unsigned lowest(uint32_t at) {
 __device__ __forceinline__ void sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(SC_THREADS) : "memory"); }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_kernel(const __grid_constant__ ScoreArgs A) {
+__global__ void __launch_bounds__(SC_THREADS + 64, Ring<T>::PER_SM) logprobs_kernel(const __grid_constant__ ScoreArgs A) {
     griddep_launch();
     using R = Ring<T>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[R::N], empty[R::N];
-    __shared__ Key lists[TOP ? SC_KEYS : 1];                 // of the warps at a row's end, or of other CTAs
-    __shared__ __align__(16) unsigned floors[SC_WARPS];     // what part_n of a warp's logits reach
+    __shared__ __align__(8) uint64_t full[R::N], empty[R::N], ends[2], freed[2];
+    __shared__ Key lists[2][TOP ? 32 * SC_WARPS : 1], others[TOP ? SC_KEYS : 1];   // of the warps at a row's end; of other CTAs
+    __shared__ __align__(16) unsigned floors[2][SC_WARPS];   // what part_n of a warp's logits reach, by the row's parity
     __shared__ float pm[SC_C_MAX * SC_WARPS], ps[SC_C_MAX * SC_WARPS], pd[SC_C_MAX * SC_WARPS];   // [chunk][warp]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, top = A.top, C = A.C;
     const uint32_t raw = smem_u32(smem_raw), ring = (raw + 127u) & ~127u;
     uint8_t* bufs = smem_raw + (ring - raw);
     if (tid == 0) {
         for (int st = 0; st < R::N; ++st) mbar_init(smem_u32(&full[st]), 1), mbar_init(smem_u32(&empty[st]), SC_WARPS);
+        for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&ends[k]), SC_WARPS), mbar_init(smem_u32(&freed[k]), 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -177,6 +179,9 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
 
     const T* base = static_cast<const T*>(A.logits);
     int row = i0 / C, c = i0 - row * C;
+    // a row's sums and lists stand in one of two buffers, while the next row fills the other; a row of more
+    // than half the chunks there can be has both
+    const int bufs2 = C <= SC_C_MAX / 2 ? 2 : 1, half = SC_C_MAX / 2 * SC_WARPS;
     if (warp == SC_WARPS) {
         // ---- the chunks into the ring, in whole 16-byte pieces
         if (lane) return;
@@ -198,17 +203,114 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
         return;
     }
 
+    if (warp == SC_WARPS + 1) {
+        // ---- the ends of rows, and of the run
+        bool ok = true;
+        for (int i = i0, seg = 0; i < i1; ++seg, ++row, c = 0) {
+            const int first_c = c, last_c = min(C - 1, c + i1 - i - 1), buf = seg % bufs2;
+            const bool row_ends = last_c == C - 1;
+            i += last_c - first_c + 1;
+            float *pmr = pm + buf * half, *psr = ps + buf * half, *pdr = pd + buf * half;
+            const int token = __ldg(A.tokens + row);
+            const float token_x = token >= 0 && token < A.V ? to_float(__ldg(base + row * A.ld + token)) : 0.f;
+            if (ok) ok = mbar_wait(smem_u32(&ends[buf]), (seg / bufs2) & 1u, A.err);
+            bool last = true;
+            Key list = 0;
+            if (TOP) list = best_of_heads(lists[buf] + lane * 32, lane < SC_WARPS ? top : 0, top, lane);
+            if (first_c != 0 || !row_ends) {
+                // the row lies in CTAs a to z; ((i + 1) G - 1) / n_chunks is the CTA of chunk i
+                const long long r0 = static_cast<long long>(row) * C;
+                const int a = static_cast<int>(((r0 + 1) * G - 1) / n_chunks), z = static_cast<int>(((r0 + C) * G - 1) / n_chunks);
+                float4* gp = A.part + static_cast<long long>(a) * C * SC_WARPS;
+                for (int k = first_c * SC_WARPS + lane; k < (last_c + 1) * SC_WARPS; k += 32) __stcg(gp + k, make_float4(pmr[k], psr[k], pdr[k], 0.f));
+                if (TOP && lane < top) __stcg(A.keys + (2ll * blockIdx.x + (first_c == 0)) * top + lane, list);
+                __threadfence();
+                __syncwarp();
+                unsigned seen = 0;
+                if (lane == 0) seen = atomicAdd(A.cnt + a, 1u);
+                last = __shfl_sync(0xffffffffu, seen, 0) == static_cast<unsigned>(z - a);
+                if (last) {
+                    if (lane == 0) A.cnt[a] = 0;
+                    __threadfence();
+#pragma unroll 8
+                    for (int k = lane; k < C * SC_WARPS; k += 32) {
+                        const float4 q = __ldcg(gp + k);
+                        pmr[k] = q.x, psr[k] = q.y, pdr[k] = q.z;
+                    }
+                    if (TOP) {
+                        // lane 0 has the list so far, the others a CTA's each
+                        list = lane < top ? __ldcg(A.keys + (2ll * a + 1) * top + lane) : 0;
+                        const int most = min(31, SC_KEYS / top - 1);
+                        for (int g = a + 1; g <= z; g += most) {
+                            const int nl = min(most, z + 1 - g);
+                            if (lane < top) others[lane] = list;
+                            // list h of the round, key j: after the first, in order
+#pragma unroll 8
+                            for (int k = lane; k < nl * top; k += 32) {
+                                const int h = k / top;
+                                others[top + k] = __ldcg(A.keys + 2ll * (g + h) * top + k - h * top);
+                            }
+                            __syncwarp();
+                            list = best_of_heads(others + lane * top, lane <= nl ? top : 0, top, lane);
+                            __syncwarp();
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (last) {
+                float mrow = -INFINITY;
+                for (int k = lane; k < C * SC_WARPS; k += 32)
+                    if (psr[k] != 0.f) mrow = fmaxf(mrow, pmr[k]);   // S = 0: nothing but -inf
+                mrow = warp_max(mrow);
+                for (int k = lane; k < C * SC_WARPS; k += 32) {
+                    const float off = __fsub_rn(pmr[k], mrow), S = psr[k];
+                    pmr[k] = S == 0.f ? 0.f : expf(off);
+                    pdr[k] = S == 0.f ? 0.f : __fmaf_rn(fmaxf(off, -3e38f), S, pdr[k]);
+                }
+                __syncwarp();
+                float S = 0.f, D = 0.f;   // of a warp's shares, in lanes 0 to 7 and again in the others
+#pragma unroll 4
+                for (int k = lane % SC_WARPS; k < C * SC_WARPS; k += SC_WARPS) {
+                    S = __fmaf_rn(pmr[k], psr[k], S);
+                    D = __fmaf_rn(pmr[k], pdr[k], D);
+                }
+#pragma unroll
+                for (int off = SC_WARPS / 2; off > 0; off >>= 1) {
+                    S = __fadd_rn(S, __shfl_xor_sync(0xffffffffu, S, off));
+                    D = __fadd_rn(D, __shfl_xor_sync(0xffffffffu, D, off));
+                }
+                const float logs = logf(S);
+                const bool empty = S == 0.f;   // every logit -inf
+                auto score = [&](float xv) { return empty ? -INFINITY : __fsub_rn(__fsub_rn(xv, mrow), logs); };
+                if (lane == 0) {
+                    if (A.entropy) A.entropy[row] = empty ? 0.f : __fsub_rn(logs, __fdiv_rn(D, S));
+                    const bool in = token >= 0 && token < A.V;
+                    if (!in && token != -1) atomicOr(A.err, ERR_BAD_TOKEN);
+                    A.logprob[row] = in ? score(token_x) : token == -1 ? 0.f : __uint_as_float(0x7fc00000u);
+                }
+                if (TOP && lane < top) {
+                    const long long o = static_cast<long long>(row) * top + lane;
+                    A.ids[o] = static_cast<int32_t>(~static_cast<unsigned>(list));
+                    A.lps[o] = score(value_of(static_cast<unsigned>(list >> 32)));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&freed[buf]));
+        }
+        return;
+    }
+
     Key list = 0, least = 0;      // the lane's of the warp's best; a new key has to pass the last of n
     unsigned floor = 0;
     const int part_n = (top + SC_WARPS - 1) / SC_WARPS;
     int first_c = c;              // of this row in this CTA
     int st = 0, ph = 0;
-    int token = 0;                // warp 0: the row's token, its logit
-    float token_x = 0.f;
+    int seg = 0;                  // rows begun in this CTA
     bool ok = true;
     for (int i = i0; i < i1; ++i) {
         const int at0 = c * SC_CHUNK, n = min(SC_CHUNK, A.V - at0);
-        if (warp == 0 && c == first_c) token = __ldg(A.tokens + row);
+        const int buf = seg % bufs2;
         // (a wait that gave up is recorded; what follows reads stale logits, but ends)
         if (ok) ok = mbar_wait(smem_u32(&full[st]), ph, A.err);
         const T* x = reinterpret_cast<const T*>(bufs + st * R::STRIDE + (reinterpret_cast<uintptr_t>(base + row * A.ld + at0) & 15)) + tid;
@@ -220,12 +322,11 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
 #pragma unroll
             for (int k = 0; k < SC_PER; ++k) v[k] = k * SC_THREADS + tid < n ? to_float(x[k * SC_THREADS]) : -INFINITY;
         }
-        if (warp == 0 && c == first_c && token >= 0 && token < A.V) token_x = to_float(__ldg(base + row * A.ld + token));
+        if (c == first_c && seg >= bufs2 && ok) ok = mbar_wait(smem_u32(&freed[buf]), (seg / bufs2 - 1) & 1u, A.err);
         float mx4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int k = 4; k < SC_PER; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], v[k]);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));   // NaN only if all are
-        if (c == first_c && !TOP) sync();   // warp 0 has done with the row before
         if (TOP) {
             // (0 where every logit of the thread is NaN, masked or behind the row)
             const unsigned need = static_cast<unsigned>(least >> 32), best = mx > -INFINITY ? order_of(mx) : 0u;
@@ -236,10 +337,10 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
                     if (k == 1) break;
                     if (lane == __ffs(__ballot_sync(0xffffffffu, b == floor)) - 1) b = 0;
                 }
-                if (lane == 0) floors[warp] = floor;
-                sync();   // and warp 0 has done with the row before
+                if (lane == 0) floors[seg & 1][warp] = floor;
+                sync();
             }
-            unsigned pass = lowest(smem_u32(floors));
+            unsigned pass = lowest(smem_u32(floors[seg & 1]));
             const bool some = best > need && best >= pass;
             pass = max(pass, need);
             const bool rest = pass <= order_of(-INFINITY);   // what is not a number above -inf counts, too
@@ -273,7 +374,7 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
                     least = __shfl_sync(0xffffffffu, list, top - 1);
                 }
                 floor = max(floor, static_cast<unsigned>(__shfl_sync(0xffffffffu, list, part_n - 1) >> 32));
-                if (lane == 0) floors[warp] = floor;
+                if (lane == 0) floors[seg & 1][warp] = floor;
             }
         }
         __syncwarp();
@@ -292,97 +393,20 @@ __global__ void __launch_bounds__(SC_THREADS + 32, Ring<T>::PER_SM) logprobs_ker
         }
         const float s = warp_sum(__fadd_rn(__fadd_rn(s4[0], s4[1]), __fadd_rn(s4[2], s4[3])));
         const float d = warp_sum(__fadd_rn(__fadd_rn(d4[0], d4[1]), __fadd_rn(d4[2], d4[3])));
-        if (lane == 0) pm[c * SC_WARPS + warp] = ref, ps[c * SC_WARPS + warp] = s, pd[c * SC_WARPS + warp] = d;
+        if (lane == 0) {
+            const int k = buf * half + c * SC_WARPS + warp;
+            pm[k] = ref, ps[k] = s, pd[k] = d;
+        }
         if (++st == R::N) st = 0, ph ^= 1;
         const bool row_ends = c == C - 1;
         if (!row_ends && i + 1 < i1) {
             ++c;
             continue;
         }
-        if (TOP) lists[warp * 32 + lane] = list;
-        sync();
-        if (warp == 0) {
-            bool last = true;
-            if (TOP) list = best_of_heads(lists + lane * 32, lane < SC_WARPS ? top : 0, top, lane);
-            if (first_c != 0 || !row_ends) {
-                // the row lies in CTAs a to z; ((i + 1) G - 1) / n_chunks is the CTA of chunk i
-                const long long r0 = static_cast<long long>(row) * C;
-                const int a = static_cast<int>(((r0 + 1) * G - 1) / n_chunks), z = static_cast<int>(((r0 + C) * G - 1) / n_chunks);
-                float4* gp = A.part + static_cast<long long>(a) * C * SC_WARPS;
-                for (int k = first_c * SC_WARPS + lane; k < (c + 1) * SC_WARPS; k += 32) __stcg(gp + k, make_float4(pm[k], ps[k], pd[k], 0.f));
-                if (TOP && lane < top) __stcg(A.keys + (2ll * blockIdx.x + (first_c == 0)) * top + lane, list);
-                __threadfence();
-                __syncwarp();
-                unsigned seen = 0;
-                if (lane == 0) seen = atomicAdd(A.cnt + a, 1u);
-                last = __shfl_sync(0xffffffffu, seen, 0) == static_cast<unsigned>(z - a);
-                if (last) {
-                    if (lane == 0) A.cnt[a] = 0;
-                    __threadfence();
-#pragma unroll 8
-                    for (int k = lane; k < C * SC_WARPS; k += 32) {
-                        const float4 q = __ldcg(gp + k);
-                        pm[k] = q.x, ps[k] = q.y, pd[k] = q.z;
-                    }
-                    if (TOP) {
-                        // lane 0 has the list so far, the others a CTA's each
-                        list = lane < top ? __ldcg(A.keys + (2ll * a + 1) * top + lane) : 0;
-                        const int most = min(31, SC_KEYS / top - 1);
-                        for (int g = a + 1; g <= z; g += most) {
-                            const int nl = min(most, z + 1 - g);
-                            if (lane < top) lists[lane] = list;
-                            // list h of the round, key j: after the first, in order
-#pragma unroll 8
-                            for (int k = lane; k < nl * top; k += 32) {
-                                const int h = k / top;
-                                lists[top + k] = __ldcg(A.keys + 2ll * (g + h) * top + k - h * top);
-                            }
-                            __syncwarp();
-                            list = best_of_heads(lists + lane * top, lane <= nl ? top : 0, top, lane);
-                            __syncwarp();
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            if (last) {
-                float mrow = -INFINITY;
-                for (int k = lane; k < C * SC_WARPS; k += 32)
-                    if (ps[k] != 0.f) mrow = fmaxf(mrow, pm[k]);   // S = 0: nothing but -inf
-                mrow = warp_max(mrow);
-                for (int k = lane; k < C * SC_WARPS; k += 32) {
-                    const float off = __fsub_rn(pm[k], mrow), S = ps[k];
-                    pm[k] = S == 0.f ? 0.f : expf(off);
-                    pd[k] = S == 0.f ? 0.f : __fmaf_rn(fmaxf(off, -3e38f), S, pd[k]);
-                }
-                __syncwarp();
-                float S = 0.f, D = 0.f;   // of a warp's shares, in lanes 0 to 7 and again in the others
-#pragma unroll 4
-                for (int k = lane % SC_WARPS; k < C * SC_WARPS; k += SC_WARPS) {
-                    S = __fmaf_rn(pm[k], ps[k], S);
-                    D = __fmaf_rn(pm[k], pd[k], D);
-                }
-#pragma unroll
-                for (int off = SC_WARPS / 2; off > 0; off >>= 1) {
-                    S = __fadd_rn(S, __shfl_xor_sync(0xffffffffu, S, off));
-                    D = __fadd_rn(D, __shfl_xor_sync(0xffffffffu, D, off));
-                }
-                const float logs = logf(S);
-                const bool empty = S == 0.f;   // every logit -inf
-                auto score = [&](float xv) { return empty ? -INFINITY : __fsub_rn(__fsub_rn(xv, mrow), logs); };
-                if (lane == 0) {
-                    if (A.entropy) A.entropy[row] = empty ? 0.f : __fsub_rn(logs, __fdiv_rn(D, S));
-                    const bool in = token >= 0 && token < A.V;
-                    if (!in && token != -1) atomicOr(A.err, ERR_BAD_TOKEN);
-                    A.logprob[row] = in ? score(token_x) : token == -1 ? 0.f : __uint_as_float(0x7fc00000u);
-                }
-                if (TOP && lane < top) {
-                    const long long o = static_cast<long long>(row) * top + lane;
-                    A.ids[o] = static_cast<int32_t>(~static_cast<unsigned>(list));
-                    A.lps[o] = score(value_of(static_cast<unsigned>(list >> 32)));
-                }
-            }
-        }
+        if (TOP) lists[buf][warp * 32 + lane] = list;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ends[buf]));
+        ++seg;
         ++row;
         c = first_c = 0;
         list = least = 0;
@@ -428,7 +452,7 @@ xv_status logprobs(const void* logits, bool f32, long long ld, const int32_t* to
         if (xv_status st = kernel_smem_once(reinterpret_cast<const void*>(kern), smem, true, "logprobs: set shared memory size")) return st;
         const size_t grid = std::min(ctas(M, C), static_cast<size_t>(sms) * per_sm);
         trace_pre(s);
-        launch_k(kern, dim3(static_cast<unsigned>(grid)), dim3(SC_THREADS + 32), smem, s, a);
+        launch_k(kern, dim3(static_cast<unsigned>(grid)), dim3(SC_THREADS + 64), smem, s, a);
         return XV_OK;
     };
     using F = Ring<float>;
