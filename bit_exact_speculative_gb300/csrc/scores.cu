@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(SC_THREADS + 64, Ring<T>::PER_SM) logprobs_ker
         float s4[4] = {0.f, 0.f, 0.f, 0.f}, d4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < SC_PER; k += 2) {
+            if (k % 8 == 0 && k * SC_THREADS >= n) break;   // behind the row: they would add 0
             float a = v[k], b = v[k + 1];
             add2(a, b, -ref, -ref);
             float ea = a, eb = b;
