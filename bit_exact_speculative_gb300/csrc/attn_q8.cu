@@ -163,6 +163,8 @@ struct Sight {
     }
 };
 
+constexpr int Q_COST = 1;   // in tiles
+
 // Split of slot s, where the slots past the sinks' begin at split `first`.
 __device__ __forceinline__ int q8_slot_split(int s, int nsink, int first) { return s < nsink ? s : first + s - nsink; }
 
@@ -219,7 +221,8 @@ struct Item {
     __device__ __forceinline__ bool same_q(const Item& o) const { return b == o.b && g == o.g && rt == o.rt; }
 };
 
-// The items [it[0], it[1]) of persistent CTA c of n: equal shares of the cost.  One warp.  (What it takes
+// The items [it[0], it[1]) of persistent CTA c of n: equal shares of the cost (measured: 1.4 to 1.6 us a tile, 1 to
+// 1.2 an item, some more where the Q changes).  One warp.  (What it takes
 // the CTA waits for: with divisions in 64 bits and a look at the same sequence three times 3.5 us.)
 __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it) {
     const int lane = threadIdx.x & 31;
@@ -234,7 +237,7 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
             int one = 0, tiles = 0;   // cost of a row tile of a head, live row tiles
             if (b0 + lane < A.B) v.of(A, b0 + lane, 0);
             if (v.rows > 0) {
-                one = v.cost(1 << 24);
+                one = Q_COST + v.cost(1 << 24);
                 tiles = A.nrt == 1 ? 1 : (q8_rows(A.n_rows, b0 + lane, A.R) * A.G + A.tile_rows - 1) / A.tile_rows;
             }
             long long x = static_cast<long long>(one) * (tiles * A.Hkv);
@@ -271,7 +274,9 @@ __device__ __forceinline__ void q8_range(const Q8Args& A, int c, int n, int* it)
                 int slot = 0;   // the first whose cost begins at `in` or later
 #pragma unroll 1
                 for (int s = 0; s < A.nslot; s += 32) {
-                    const unsigned less = __ballot_sync(0xffffffffu, s + lane < A.nslot && w.cost(q8_slot_split(s + lane, A.nsink, first)) < in);
+                    // (the first item of a row tile begins with its Q)
+                    const int ahead = w.cost(q8_slot_split(s + lane, A.nsink, first)), begin = ahead ? ahead + Q_COST : 0;
+                    const unsigned less = __ballot_sync(0xffffffffu, s + lane < A.nslot && begin < in);
                     slot += __popc(less);
                     if (less != 0xffffffffu) break;
                 }
