@@ -495,6 +495,27 @@ def test_many_items_per_cta(xv, hd, Hq, Hkv):
         close(out, *reference(c, table, q, ctx, counts, R, Hq, Hkv, hd, page, window, sinks, hd ** -0.5))
 
 
+@pytest.mark.parametrize("Hq,Hkv,hd,R", [(2, 1, 64, 5), (8, 2, 128, 1), (24, 4, 256, 8)])
+def test_contexts_past_the_last_change_of_splits(xv, Hq, Hkv, hd, R):
+    """Contexts around and far past 32768, where splits are the longest, short ones between them, and a row's
+    bits alone."""
+    ctx, page = [90000, 32768 - R, 200, 32769, 41000], 128
+    B, per = len(ctx), 704
+    n_pages = 1500
+    c = Cache(xv, n_pages, Hkv, page, hd)
+    table = torch.randint(0, n_pages, (B, per), generator=torch.Generator().manual_seed(5), dtype=torch.int32).cuda()
+    q = normal((B * R, Hq * hd), 22)
+    for window, sinks in ((0, 0), (40000, 300)):
+        out = run(xv, c, table, q, ctx, R, Hq, Hkv, hd, page, n_pages, per * page, window, sinks)
+        close(out, *reference(c, table, q, ctx, [R] * B, R, Hq, Hkv, hd, page, window, sinks, hd ** -0.5))
+        for b in (0, 3):
+            r = R - 1
+            one = run(xv, c, table[b:b + 1].contiguous(), q[b * R + r:b * R + r + 1].contiguous(), [ctx[b] + r], 1, Hq, Hkv, hd, page, n_pages,
+                      ctx[b] + r, window, sinks)
+            assert torch.equal(one.view(torch.int16), out[b * R + r:b * R + r + 1].view(torch.int16)), b
+    assert xv.xv_device_check() == 0
+
+
 def test_many_sequences_with_bad_ones_among_them(xv):
     """More sequences than one pass of the shares takes, in persistent CTAs: bad lengths, counts of 0 and bad
     counts between good ones, which keep the bits they have alone."""
