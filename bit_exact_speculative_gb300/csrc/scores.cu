@@ -25,10 +25,11 @@
 // row: 500 rows of 50257 bf16 logits took 33 us with a row's end in one of the computing warps.
 //
 // Each warp keeps the 32 best of its shares of a row, one a lane, in order.  A logit has to pass the n-th
-// of them, and the smallest of the eight warps' (n / 8)-th: n logits reach that.  (In a row's first
-// chunk: their lanes' (n / 8)-th largest.)  A few that pass are put in one by one, more by a bitonic sort
-// and merge, and at a row's end the best of the warps' lists are taken.  (With one list for the CTA, and a barrier a
-// chunk for it, 2048 rows of 151936 took 234 us with n = 1, 290 us with n = 20.)
+// of them, and what n logits of the warps' reach: with k = n / 8, rounded up, the (n / k)-th largest of
+// their k-th best (in a row's first chunk: of their lanes' best).  A few that pass are put in one by one,
+// more by a bitonic sort and merge, and at a row's end the best of the warps' lists are taken.  (With one
+// list for the CTA, and a barrier a chunk for it, 2048 rows of 151936 took 234 us with n = 1, 290 us with
+// n = 20.)
 #include <algorithm>
 #include <cmath>
 
@@ -140,12 +141,14 @@ __device__ __forceinline__ Key sort_up(Key k, int lane) {
     return k;
 }
 
-// The smallest of 8 words in shared memory, as they are now.
-__device__ __forceinline__ unsigned lowest(uint32_t at) {
-    uint4 a, b;
-    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(at) : "memory");
-    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(at + 16) : "memory");
-    return min(min(min(a.x, a.y), min(a.z, a.w)), min(min(b.x, b.y), min(b.z, b.w)));
+// The q-th largest of 8 words in shared memory, as they are now.
+__device__ __forceinline__ unsigned largest8(uint32_t at, int q, int lane) {
+    unsigned v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + 4 * (lane % 8)) : "memory");
+    int reach = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) reach += __shfl_sync(0xffffffffu, v, k) >= v;
+    return __reduce_max_sync(0xffffffffu, reach >= q ? v : 0u);
 }
 
 // Barrier of the warps that compute.
@@ -303,7 +306,8 @@ __global__ void __launch_bounds__(SC_THREADS + 64, Ring<T>::PER_SM) logprobs_ker
 
     Key list = 0, least = 0;      // the lane's of the warp's best; a new key has to pass the last of n
     unsigned floor = 0;
-    const int part_n = (top + SC_WARPS - 1) / SC_WARPS;
+    // part_w warps with part_n logits each make n at least
+    const int part_n = (top + SC_WARPS - 1) / SC_WARPS, part_w = part_n ? (top + part_n - 1) / part_n : 0;
     int first_c = c;              // of this row in this CTA
     int st = 0, ph = 0;
     int seg = 0;                  // rows begun in this CTA
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(SC_THREADS + 64, Ring<T>::PER_SM) logprobs_ker
                 if (lane == 0) floors[seg & 1][warp] = floor;
                 sync();
             }
-            unsigned pass = lowest(smem_u32(floors[seg & 1]));
+            unsigned pass = largest8(smem_u32(floors[seg & 1]), part_w, lane);
             const bool some = best > need && best >= pass;
             pass = max(pass, need);
             const bool rest = pass <= order_of(-INFINITY);   // what is not a number above -inf counts, too
