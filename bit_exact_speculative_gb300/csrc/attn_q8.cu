@@ -23,7 +23,7 @@
 //                  values: e5m2 is fp16's upper byte, so cutting the byte off three times leaves
 //                  nothing (11 bits of significand, 3 by 3).  What is left after two is scaled by
 //                  2^6, against e5m2's smallest value, and has an accumulator of its own.  P_SHIFT
-//                  puts p at up to 2^15: P keeps weights to 2^-21 of the reference at full precision
+//                  puts p at up to 2^15: P keeps weights to 2^-19 of the reference at full precision
 //                  and to 2^-29 at all (a long context can hold half its weight in such), and the
 //                  reference may stay up to RESCALE_SLACK below the row's largest t_j.
 // With rows in M instead (a first form: 64 rows of 128 used, P in fp16, V widened to fp16 by warps of
@@ -34,8 +34,7 @@
 // Kernel 1 (attn_q8_kernel): work items (slot, row tile, kv head, sequence); a slot is a split, or
 // with a window one of the splits that the window and the sinks can touch.  One CTA per item where
 // all fit at once, else persistent CTAs that walk contiguous ranges of equal cost.  Kernel 2
-// (attn_q8_combine_kernel) joins each row's splits,
-// where there are several.
+// (attn_q8_combine_kernel) joins each row's splits, where there are several.
 #include <algorithm>
 #include <cmath>
 
@@ -1096,8 +1095,8 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
 
 // One CTA per (row, q head): w_s = 2^(m_s - M) over the row's live slots s in order, out = sum w_s O_s /
 // sum w_s l_s.  The i-th of them belongs to the sum of residue i mod CB_SUMS, and those sums are added in
-// order: fixed by the row alone, whether G = 4 groups of threads have 4 residues each (few slots: a
-// batch's rows fit the machine) or 16 have one (many: a row's loads are in flight together).
+// order: fixed by the row alone, whether G = 4 groups of threads have 4 residues each (few slots, or
+// many rows) or 16 have one (many slots of few rows: their loads are in flight together).
 constexpr int CB_SLOTS = 1 << 10;   // slots whose m and l are staged at a time
 
 template <int HD, int G>
@@ -1249,7 +1248,12 @@ xv_status launch(const CUtensorMap& tmK, const CUtensorMap& tmV, Q8Args& a, cons
         launch_k(kern, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, c);
         return XV_OK;
     };
-    if (xv_status st = a.nslot <= 2 * CB_SUMS ? go(attn_q8_combine_kernel<HD, 4>, HD) : go(attn_q8_combine_kernel<HD, 16>, 4 * HD)) return st;
+    int sms = 0;
+    if (xv_status st = device_sm_count(&sms)) return st;
+    // 16 groups for many slots of few rows, 1024 threads per SM at most.  The whole call with 16 and with 4, in us:
+    // 32 rows of 128 slots 53.6, 56.1; 128 of 30 43.9, 44.9; 192 of 128 71.2, 69.3; 1536 of 62 135, 118
+    const bool wide = a.nslot > 2 * CB_SUMS && rows * 4 * HD <= 1024ll * sms;
+    if (xv_status st = wide ? go(attn_q8_combine_kernel<HD, 16>, 4 * HD) : go(attn_q8_combine_kernel<HD, 4>, HD)) return st;
     return launched("attn_q8_combine_kernel", s, K_ATTN_Q8, 4 * rows * a.nslot * (HD + 2) + 2 * rows * HD * (c.gate ? 2 : 1));
 }
 
