@@ -53,7 +53,7 @@ constexpr float LOW_SCALE = 64.f;      // P's last two terms
 // Split boundaries: every 256 positions below Q8_NEAR, 512 below Q8_FAR, 1024 beyond.  A short context
 // wants its splits spread over the machine (one verify at 2183: 512 instead of 256 costs 1.4 us of 14.6),
 // a batch wants few items (32 sequences at 4000 to 8000: 256 up to 4096 costs 5 us of 65), a long context
-// few partial results (131072: 512 instead of 1024 costs 4 us of 73).
+// few partial results (131072: 512 instead of 1024 costs 3 us of 69).
 constexpr int Q8_NEAR = 2048, Q8_FAR = 32768, Q8_NS = Q8_NEAR / 256, Q8_FS = Q8_NS + (Q8_FAR - Q8_NEAR) / 512;
 static_assert(256 % T == 0 && 1024 <= 8 * T, "a lane per half tile of an item");
 __host__ __device__ inline int q8_split_begin(int s) {
