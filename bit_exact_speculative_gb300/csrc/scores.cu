@@ -279,7 +279,9 @@ __global__ void __launch_bounds__(SC_THREADS + 64, Ring<T>::PER_SM) logprobs_ker
                 for (int k = lane; k < C * SC_WARPS; k += 32) {
                     const float off = __fsub_rn(pmr[k], mrow), S = psr[k];
                     pmr[k] = S == 0.f ? 0.f : expf(off);
-                    pdr[k] = S == 0.f ? 0.f : __fmaf_rn(fmaxf(off, -3e38f), S, pdr[k]);
+                    // a share of finite mask values, far below the row's maximum: its weight is 0 from off = -104 on, and
+                    // -1e30 S, S <= 1024, stays finite beside it (0 times infinity is not 0)
+                    pdr[k] = S == 0.f ? 0.f : __fmaf_rn(fmaxf(off, -1e30f), S, pdr[k]);
                 }
                 __syncwarp();
                 float S = 0.f, D = 0.f;   // of a warp's shares, in lanes 0 to 7 and again in the others

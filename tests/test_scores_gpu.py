@@ -108,6 +108,33 @@ def test_rows_of_hard_values(xv, kind, dtype):
     check(xv, x.to(dtype), toks(4, V), top)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", ["finfo.min", -1e36, -1e30, -65504.0])
+@pytest.mark.parametrize("M,V", [(4, 20001), (3, 1000), (307, 33333), (2, 524288)])
+def test_masks_of_a_finite_low_value(xv, M, V, low, dtype):
+    """Masked logits that are finite: whole shares of a warp, parts of one, the row's end, all but a few logits of
+    the row, all of it, -inf among them, and rows that lie in several CTAs.  A masked term is 0 in 64 bits, too, so the
+    tolerances stay those of the terms that weigh."""
+    low = torch.finfo(dtype).min if low == "finfo.min" else torch.tensor(low).to(dtype).item()
+    x = logits(M, V, torch.float32, V + 11)
+    at = torch.arange(V, device="cuda")
+    off = torch.zeros((M, V), dtype=torch.bool, device="cuda")
+    for r in range(M):
+        kind = r % 7 if M > 4 else (r + V) % 7
+        off[r] = ((at >= V // 7), (at // 32) % 8 == 3, at >= V - 50, (at % 997 != 5), at >= 0, at < V // 2, at % 3 == 0)[kind]
+    x = x.to(dtype).masked_fill(off, low)
+    x[0, V // 3: V // 2] = -INF
+    t = toks(M, V)
+    check(xv, x, t, 0)
+    lp, en, ids, tl = check(xv, x, t, 9)
+    assert en.isfinite().all()
+    if M > 4 or V == 20001:      # few allowed tokens, more alternatives asked for
+        few = torch.full_like(x, low)
+        few[:, [3, V // 2, V - 1]] = x[:, [3, V // 2, V - 1]]
+        assert check(xv, few, t, 20)[1].isfinite().all()
+    assert xv.xv_device_check() == 0
+
+
 @pytest.mark.parametrize("V", [40, 9000])
 def test_rows_that_are_empty_or_not_finite(xv, V):
     x = logits(6, V, torch.float32, 4)
