@@ -1225,7 +1225,7 @@ xv_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, Q8Args& a,
     a.joined = n_items <= room && a.nslot == 1;
     trace_pre(s);
     launch_k(kern, dim3(static_cast<unsigned>(std::min<long long>(room, n_items))), dim3(S::THREADS), S::SMEM, s, tmK, tmV, a, c);
-    const long long rows = static_cast<long long>(a.B) * a.R * a.Hq, seen = a.window && a.window < a.max_len ? a.window + a.sinks : a.max_len;
+    const long long rows = static_cast<long long>(a.B) * a.R * a.Hq, seen = a.window ? std::min(a.window + static_cast<long long>(a.sinks), static_cast<long long>(a.max_len)) : a.max_len;
     return launched("attn_q8_kernel", s, K_ATTN_Q8, (2ll * HD + 8) * a.B * a.Hkv * seen + 2 * rows * HD + 4 * rows * a.nslot * (HD + 2));
 }
 
@@ -1273,6 +1273,7 @@ xv_status attn_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, 
         return fail(XV_ERR_UNSUPPORTED, "attn_q8: R above %d, B or Hkv above 65535, or B*R*Hq above 2^30", XV_KMAX);
     if (!aligned16(q) || !aligned16(out) || !aligned16(gate) || q_stride % 8 || out_stride % 8 || (gate && gate_stride % 8))
         return fail(XV_ERR_UNSUPPORTED, "attn_q8: rows must be 16-byte aligned");
+    sinks = std::min(sinks, max_ctx);   // further ones are behind every row (and sums with them would pass 2^31)
     const size_t need = xv_attn_q8_workspace_size(B, R, Hq, hd, max_ctx, window, sinks);
     if (!ws || ws_bytes < need) return fail(XV_ERR_WORKSPACE, "attn_q8: workspace of %zu bytes needed", need);
     if (!aligned16(ws)) return fail(XV_ERR_UNSUPPORTED, "attn_q8: workspace must be 16-byte aligned");

@@ -253,6 +253,54 @@ def test_windows_and_sinks(xv, Hq, Hkv, hd, window, sinks):
     assert (out[~live] == 7.0).all()          # rows behind a sequence's count: left as they were
 
 
+@pytest.mark.parametrize("Hq,Hkv,hd", HEADS)
+@pytest.mark.parametrize("sinks", [10 ** 6, 2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 1])
+def test_sinks_past_every_length_are_the_whole_context(xv, Hq, Hkv, hd, sinks):
+    """Any number of sinks may be asked for: past the context they leave nothing out, so a window changes no bit.
+    The workspace holds NaN, so a split that is not computed shows."""
+    ctx, R, page = [5300, 700, 40, 1], 3, 64
+    B, per = len(ctx), 84
+    n_pages = B * per
+    c, table = Cache(xv, n_pages, Hkv, page, hd), shuffled(B, per, n_pages, 4)
+    q = normal((B * R, Hq * hd), 23)
+    pages = xv.kv_pages(table, page, n_pages)
+    max_ctx = per * page
+    def go(window, sinks):
+        out = torch.zeros((B * R, Hq * hd), dtype=torch.bfloat16, device="cuda")
+        ws = xv.workspace(xv.xv_attn_q8_workspace_size(B, R, Hq, hd, max_ctx, window, sinks))
+        ws.fill_(0xff)
+        xv.xv_attn_decode_rows_q8_paged(q, c.q8, pages, i32(ctx), R, B, Hq, Hkv, hd, max_ctx, hd ** -0.5, out, ws, window=window,
+                                        sinks=sinks)
+        return out
+    want = go(0, 0)
+    close(want, *reference(c, table, q, ctx, [R] * B, R, Hq, Hkv, hd, page, 0, 0, hd ** -0.5))
+    for window in (1, 100, 2000, max_ctx - 1):
+        assert torch.equal(go(window, sinks).view(torch.int16), want.view(torch.int16)), window
+    assert xv.xv_device_check() == 0
+
+
+def test_traced_bytes_of_a_window(xv):
+    """What the trace says of a windowed call: the window's and the sinks' positions, at most the context's."""
+    Hq, Hkv, hd, R, page = 8, 2, 64, 2, 2048
+    c = Cache(xv, 1, Hkv, page, hd)
+    q = normal((R, Hq * hd), 24)
+    traced = {}
+    for window, sinks in ((0, 0), (100, 0), (100, 28), (100, 5000), (100, 2 ** 31 - 1), (2000, 2 ** 31 - 1)):
+        xv.xv_trace_enable(16)
+        try:
+            run(xv, c, None, q, [1500], R, Hq, Hkv, hd, page, 1, page, window, sinks, paged=False)
+            torch.cuda.synchronize()
+            traced[window, sinks] = next(b for kind, _, b in xv.xv_trace_read() if kind == "attn_q8")
+        finally:
+            xv.xv_trace_disable()
+    per = Hkv * (2 * hd + 8)      # bytes a position
+    slots = lambda w, s: xv.xv_attn_q8_workspace_size(1, R, Hq, hd, page, w, s) // (R * Hq * (hd + 2) * 4)   # noqa: E731
+    fixed = lambda w, s: 2 * R * Hq * hd + 4 * R * Hq * slots(w, s) * (hd + 2)   # noqa: E731
+    for (window, sinks), got in traced.items():
+        seen = min(window + sinks, page) if window else page
+        assert got == per * seen + fixed(window, sinks), (window, sinks)
+
+
 @pytest.mark.parametrize("Hq,Hkv,hd", [(6, 2, 64), (8, 8, 128), (24, 4, 256), (5, 1, 64), (128, 1, 128)])
 @pytest.mark.parametrize("R", [1, 17, 64])
 def test_rows_and_heads(xv, Hq, Hkv, hd, R):
