@@ -596,7 +596,6 @@ template <int HD, int NR>
 __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args A,
                    const __grid_constant__ CombineArgs C) {
-    griddep_launch();
     using S = Shape<HD, NR>;
     constexpr int SK = S::SK, SV = S::SV, RAW = S::RAW, PB = S::PB, RW = S::RW, WG = S::WG;
     constexpr int IT = S::ITEMS;
@@ -648,15 +647,17 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
         fence_mbar_init();
         s_abort = 0;
     }
-    if (warp == W_MMA) {
-        tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tS = tmem_slot, tO = tS + S::O_COL;
     griddep_wait();
+    // The tensor memory's columns, for the warps that use them.  No limit bounds the wait for them: the MMA warp takes
+    // them once the kernels before are done, which may have none yet themselves, and lets the kernels behind go only
+    // then (the GEMM takes its own before it waits for this one: at hd 64 both fit an SM's memory, but 512 columns and
+    // 64 not its tensor memory).
+    auto columns = [&]() -> uint32_t {
+        asm volatile("barrier.cta.sync 8, %0;" ::"n"(128 * (WG + 1) + 32) : "memory");
+        tc_fence_after();
+        return tmem_slot;
+    };
 
     auto W = [&](uint32_t bar, uint32_t par) -> bool { return mbar_try_wait(bar, par) || wait_slow(bar, par, &s_abort, A.err); };
     // the same verdict for every lane of a warp
@@ -813,6 +814,11 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
         cp_async_wait_all();
     } else if (warp == W_MMA) {
         // ---- MMAs
+        tmem_alloc(smem_u32(&tmem_slot), S::TMEM_COLS);
+        tmem_relinquish();
+        griddep_launch();
+        tc_fence_before();
+        const uint32_t tS = columns(), tO = tS + S::O_COL;
         if (lane == 0) {
             constexpr uint32_t IDS = idesc_f8(128, 2 * NR, false, false, false), IDO = idesc_f8(128, 2 * NR, true, true, true);
             constexpr int KS = S::KROW / 32;   // MMAs of 32 codes per block row
@@ -864,7 +870,7 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     } else if (warp >= W_OUT) {
         // ---- epilogue: thread = dim of O^T (tensor memory lane), modulo 128
         const int d = tid - 32 * W_OUT;
-        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16, tO = columns() + S::O_COL;
         int t = 0;
         for (int n = 0; item(n); ++n) {
             t += items[n % IT].ntiles;
@@ -904,7 +910,7 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
         // breaks no loop here, so that the four warps meet at the same barriers (later waits return at once)
         const int wg = warp >> 2, r_wg = wg * RW, pt = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t cS = tS + lane_off + r_wg, cO = tO + lane_off + 2 * r_wg;
+        const uint32_t cS = columns() + lane_off + r_wg, cO = cS + S::O_COL + r_wg;
         int t = 0, nq = 0;
         long long at = 0;   // of row r_wg + pt in the workspace, slot 0
         for (int n = 0;; ++n) {
@@ -1080,7 +1086,7 @@ __global__ void __launch_bounds__(Shape<HD, NR>::THREADS, Shape<HD, NR>::PER_SM)
     __syncthreads();
     if (warp == W_MMA) {
         tc_fence_after();
-        tmem_dealloc(tS, S::TMEM_COLS);
+        tmem_dealloc(tmem_slot, S::TMEM_COLS);
     }
     if (A.joined) {
         __threadfence_block();

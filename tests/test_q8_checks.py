@@ -234,3 +234,17 @@ def test_split_boundaries(xv):
         rows = 2 * 8
         up = lambda n: -(-n // 256) * 256   # noqa: E731
         assert xv.xv_attn_q8_workspace_size(1, 2, 8, 64, ctx) == up(rows * slots * 64 * 4) + up(rows * slots * 8)
+
+
+def test_tensor_memory_is_taken_between_the_wait_and_the_launch():
+    """The wait for tensor memory has no limit.  Columns taken before the kernels ahead are done may be columns that one
+    of them still needs; kernels behind that are let go before the columns are there may take them (the GEMM does,
+    while it waits)."""
+    import os
+    from bit_exact_speculative_gb300 import build
+    text = open(os.path.join(build.CSRC, "attn_q8.cu")).read()
+    body = text[text.index("attn_q8_kernel(const __grid_constant__"):]
+    body = body[:body.index("constexpr int CB_SLOTS")]
+    at = [body.index(name + "(") for name in ("griddep_wait", "tmem_alloc", "griddep_launch")]
+    assert at == sorted(at)
+    assert body.count("griddep_launch(") == body.count("tmem_alloc(") == 1

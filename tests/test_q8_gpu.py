@@ -679,3 +679,42 @@ def test_appended_verify_equals_sequential_decode(xv):
             assert torch.equal(one.view(torch.int16), out[r:r + 1].view(torch.int16)), (step, r)
         L += keep
     assert xv.xv_device_check() == 0
+
+
+def test_a_stream_of_kernels_that_take_tensor_memory(xv):
+    """bf16 attention, 8-bit attention of row tiles with 512 columns, GEMM and back, at sizes of which two fit an SM's
+    memory together (hd 64), launched while the first still waits: each has the bits of a call by itself."""
+    B, R, Hq, Hkv, hd, L = 8, 8, 12, 2, 64, 1500
+    c = Cache(xv, B, Hkv, L, hd)
+    q = normal((B * R, Hq * hd), 70)
+    kc, vc = normal((B, Hkv, L, hd), 71), normal((B, Hkv, L, hd), 72)
+    X, W = normal((8, 1024), 73), normal((4096, 1024), 74, 0.05)
+    ctx = i32([1400 - 100 * b for b in range(B)])
+    scale = hd ** -0.5
+    new = lambda: [torch.zeros_like(q), torch.zeros_like(q),   # noqa: E731
+                   torch.zeros((8, 4096), dtype=torch.bfloat16, device="cuda")]
+    ws = [xv.workspace(xv.xv_attn_workspace_size(B, R, Hq, hd, L)), xv.workspace(xv.xv_attn_q8_workspace_size(B, R, Hq, hd, L)),
+          xv.workspace(xv.xv_gemm_workspace_size(8, 4096, 1024))]
+    def bf16(o):
+        xv.xv_attn_decode_rows(q, Hq * hd, kc, vc, ctx, R, B, Hq, Hkv, hd, L, L, scale, o[0], Hq * hd, ws[0])
+    def q8(o):
+        xv.xv_attn_decode_rows_q8(q, c.q8, ctx, R, B, Hq, Hkv, hd, L, L, scale, o[1], ws[1])
+    def gemm(o):
+        xv.xv_gemm_small_m(X, W, o[2], ws[2])
+    want = new()
+    for f in (bf16, q8, gemm):
+        f(want)
+        torch.cuda.synchronize()
+    for order in ((bf16, q8), (q8, gemm), (bf16, q8, gemm), (gemm, q8, bf16), (q8, bf16), (q8, q8, gemm, gemm)):
+        outs = []
+        torch.cuda._sleep(2_000_000)      # about a millisecond, while the launches queue up
+        for _ in range(6):
+            outs.append(new())
+            for f in order:
+                f(outs[-1])
+        torch.cuda.synchronize()
+        for o in outs:
+            for f, a, b in zip((bf16, q8, gemm), o, want):
+                if f in order:
+                    assert torch.equal(a.view(torch.int16), b.view(torch.int16)), [g.__name__ for g in order]
+    assert xv.xv_device_check() == 0
