@@ -767,6 +767,8 @@ def xv_logprobs(logits, tokens, logprob, ws, entropy=None, top_ids=None, top_log
         if top_ids.dim() != 2:
             _refuse("top_ids", top_ids, f"[{M}, top] int32")
         top = top_ids.shape[1]
+        if top_logprobs.dim() != 2 or top_logprobs.shape[1] != top:   # another width would be another layout of the entries
+            _refuse("top_logprobs", top_logprobs, f"[{M}, {top}] float32")
     f = torch.float32
     fn = lib().xv_logprobs if f32 else lib().xv_logprobs_bf16
     _check(fn(logits.data_ptr(), max(ld, V) if M == 1 else ld, _flat("tokens", tokens, M, dev), None if n_rows is None else _one("n_rows", n_rows, dev),

@@ -133,6 +133,19 @@ def test_alternatives_without_their_scores_are_refused(xv):
             xv.xv_logprobs(**dict(args, **{k: None}))
 
 
+def test_alternatives_of_another_width_than_their_scores_are_refused(xv):
+    """Both are written as [M, top]: a wider one has its rows elsewhere."""
+    args = calls(xv)["xv_logprobs"]
+    for scores in (f32(M, 8), f32(M, 3), f32(2 * M, 2), f32(4 * M), f32(1, M, 4)):
+        with pytest.raises(ValueError, match="^top_logprobs:"):
+            xv.xv_logprobs(**dict(args, top_logprobs=scores))
+    for ids in (i32(M, 8), i32(2 * M, 2), i32(M, 5)):
+        with pytest.raises(ValueError, match="^top_"):
+            xv.xv_logprobs(**dict(args, top_ids=ids))
+    with pytest.raises(ValueError, match="current device"):      # more rows than the call's: as everywhere
+        xv.xv_logprobs(**dict(args, top_ids=i32(M + 2, 4), top_logprobs=f32(M + 1, 4)))
+
+
 P, ODD = 0x10000, 0x10008
 
 
