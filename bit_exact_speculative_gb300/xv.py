@@ -260,23 +260,27 @@ def _one(name, t, dev):
     return t.data_ptr()
 
 
+# bf16, or its bits; a 16-bit float of the other kind would be read as bf16
+_BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
 def _flat16(name, t, n, dev):
-    """n or more contiguous 2-byte values."""
-    if t.itemsize != 2 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(name, t, f"{n} contiguous 2-byte values")
+    """n or more contiguous bf16 values."""
+    if t.dtype not in _BITS16 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, f"{n} contiguous bfloat16 values (or their bits)")
     return t.data_ptr()
 
 
 def _rows(name, t, m, width, dev):
-    """m or more rows (the first dimension) of width or more 2-byte values."""
+    """m or more rows (the first dimension) of width or more bf16 values."""
     shape, stride = t.shape, t.stride()
     try:
         (have, cols), (step, one) = shape, stride
     except ValueError:   # another number of dimensions: a row's must lie densely
         ok = len(shape) > 2 and shape[0] > 0 and t[0].is_contiguous()
         (have, cols), (step, one) = (shape[0], t[0].numel()) if ok else (0, 0), (stride[0], 1) if ok else (0, 0)
-    if have < m or cols < width or one != 1 or t.itemsize != 2 or t.get_device() != dev:
-        _refuse(name, t, f"{m} rows of {width} contiguous 2-byte values")
+    if have < m or cols < width or one != 1 or t.dtype not in _BITS16 or t.get_device() != dev:
+        _refuse(name, t, f"{m} rows of {width} contiguous bfloat16 values (or their bits)")
     return t.data_ptr(), step
 
 

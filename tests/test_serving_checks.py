@@ -83,6 +83,20 @@ def test_other_types_are_refused(xv, name):
 
 
 @pytest.mark.parametrize("name", NAMES)
+def test_16_bit_floats_of_the_other_kind_are_refused(xv, name):
+    """float16 would be read as bf16; bf16 may be given as its bits."""
+    args = calls(xv)[name]
+    for k, t in args.items():
+        if not torch.is_tensor(t) or t.itemsize != 2:
+            continue
+        with pytest.raises(ValueError, match=f"^{k}:.*bfloat16"):
+            getattr(xv, name)(**dict(args, **{k: torch.zeros(t.shape, dtype=torch.float16)}))
+        for bits in (torch.bfloat16, torch.int16, torch.uint16):
+            with pytest.raises(ValueError, match="current device"):
+                getattr(xv, name)(**dict(args, **{k: torch.zeros(t.shape, dtype=bits)}))
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_tensors_with_too_few_entries_are_refused(xv, name):
     args = calls(xv)[name]
     for k, t in args.items():
