@@ -126,8 +126,9 @@ xv_status append_q8(const uint16_t* src, long long src_stride, const int32_t* ct
     if (hd != 64 && hd != 128 && hd != 256) return fail(XV_ERR_UNSUPPORTED, "kv_append_q8: hd must be 64, 128 or 256 (got %d)", hd);
     if (src_stride < 2ll * Hkv * hd) return fail(XV_ERR_ARG, "kv_append_q8: row stride %lld below its row", src_stride);
     if (!aligned16(src) || src_stride % 8) return fail(XV_ERR_UNSUPPORTED, "kv_append_q8: rows must be 16-byte aligned");
-    const long long units = 2ll * B * R * Hkv;
-    if (units > (1ll << 30)) return fail(XV_ERR_UNSUPPORTED, "kv_append_q8: more than 2^29 rows times heads");
+    const long long rows = static_cast<long long>(B) * R;   // (times the heads it may pass 2^63)
+    if (rows > (1ll << 29) / Hkv) return fail(XV_ERR_UNSUPPORTED, "kv_append_q8: more than 2^29 rows times heads");
+    const long long units = 2 * rows * Hkv;
     AppendQ8Args a{src, src_stride, ctx_len, n_rows, R, Hkv, static_cast<int>(units),
                    Divisor(2 * Hkv), Divisor(R), Divisor(kv.page), kv, {cache->k, cache->v},
                    {cache->k_scale, cache->v_scale}, device_error_word()};

@@ -194,6 +194,14 @@ def test_c_append_refusals(xv):
     assert call(True, pages=c_pages(xv, page_size=100)) == xv.XV_ERR_UNSUPPORTED      # not a multiple of 64
 
 
+@pytest.mark.parametrize("R,B,Hkv", [(1 << 30, 1 << 30, 16), ((1 << 31) - 1, (1 << 31) - 1, 2), (1 << 20, 1 << 22, 1 << 21),
+                                     (1 << 29, 1, 2), (1, 1, (1 << 29) + 1), ((1 << 29) + 1, 1, 1)])
+def test_more_rows_times_heads_than_an_append_takes(xv, R, B, Hkv):
+    """Products past 2^63, which come out as any number in 64 bits, and the least ones past 2^29."""
+    code = xv.lib().xv_kv_append_q8_paged(P, 2 * Hkv * 64, P, None, R, B, Hkv, 64, c_pages(xv, n_pages=1), c_cache(xv), None)
+    assert code == xv.XV_ERR_UNSUPPORTED
+
+
 def test_c_attention_refusals(xv):
     L = xv.lib()
 
