@@ -36,6 +36,7 @@
 // all fit at once, else persistent CTAs that walk contiguous ranges of equal cost.  Kernel 2
 // (attn_q8_combine_kernel) joins each row's splits, where there are several.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "xv_internal.h"
@@ -1314,7 +1315,10 @@ using namespace xv;
 
 extern "C" {
 
-int xv_attn_q8_split_begin(int s) { return s < 0 ? -1 : q8_split_begin(s); }
+int xv_attn_q8_split_begin(int s) {
+    constexpr int LAST = Q8_FS + (INT_MAX - Q8_FAR) / 1024;   // the last split that begins below 2^31
+    return s < 0 ? -1 : s > LAST ? INT_MAX : q8_split_begin(s);
+}
 
 size_t xv_attn_q8_workspace_size(int B, int R, int Hq, int hd, int max_ctx, int window, int sinks) {
     if (!sizes_ok(B, R, Hq, hd, max_ctx, window, sinks)) return 0;

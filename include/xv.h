@@ -600,7 +600,7 @@ xv_status xv_kv_append_q8_paged(const uint16_t* kv_src, long long src_stride, co
  * length is out of range is skipped and recorded (4), n_rows outside [0, R]
  * recorded (8) and clamped, a page outside the pool recorded (16) and read as
  * page 0. */
-int xv_attn_q8_split_begin(int s);   /* -1 for s < 0 */
+int xv_attn_q8_split_begin(int s);   /* -1 for s < 0; 2^31 - 1 for splits that begin past it */
 size_t xv_attn_q8_workspace_size(int B, int R, int Hq, int hd, int max_ctx, int window, int sinks);
 xv_status xv_attn_decode_rows_q8(const uint16_t* q, long long q_stride, const xv_kv_q8* cache, const int32_t* ctx_len,
                                  const int32_t* n_rows, int R, int B, int Hq, int Hkv, int hd, int Lmax, int max_ctx,

@@ -283,3 +283,12 @@ def test_tensor_memory_is_taken_between_the_wait_and_the_launch():
     at = [body.index(name + "(") for name in ("griddep_wait", "tmem_alloc", "griddep_launch")]
     assert at == sorted(at)
     assert body.count("griddep_launch(") == body.count("tmem_alloc(") == 1
+
+
+def test_split_boundaries_past_every_position(xv):
+    """Rising to the last split that an int can say, and 2^31 - 1 from there on."""
+    at = xv.xv_attn_q8_split_begin
+    last = next(s for s in range(2_090_000, 2_110_000) if at(s + 1) == 2 ** 31 - 1)
+    assert at(last) % 1024 == 0 and 2 ** 31 - 1024 <= at(last) < 2 ** 31 - 1 and at(last) - at(last - 1) == 1024
+    for s in (last + 2, 2 ** 22, 2 ** 30, 2 ** 31 - 1):
+        assert at(s) == 2 ** 31 - 1, s
