@@ -583,9 +583,9 @@ xv_status xv_kv_append_q8_paged(const uint16_t* kv_src, long long src_stride, co
  * splits joined in order, so a verify row has the bits of the decode row at its
  * position.  Only runs of 64 positions with a visible one are read, so pages wholly
  * before every row's window (and past the sinks) may be given up.  q is held as two
- * e4m3 terms (to 2^-18 of its row's largest value or 2^-9 of the value, whichever is
- * larger), weights in fp16 before their product with V (those below 2^-29 of the
- * split's largest are 0), sums in fp32.  A row that sees a
+ * e4m3 terms (exact for values from 2^-9 of their row's largest on, to 2^-17 of that
+ * largest for smaller ones), weights times V scales in fp16 before their product with
+ * the V codes (those below 2^-29 of the split's largest are 0), sums in fp32.  A row that sees a
  * NaN scale, or whose q is not finite, is NaN; other rows are not touched.  V
  * scales are taken to lie in [2^-40, 2^60] (clamped to it), codes not to be NaN.
  *   hd in {64, 128, 256}; 1 <= R <= XV_KMAX; Hq % Hkv == 0; window >= 0 (0:
@@ -595,7 +595,7 @@ xv_status xv_kv_append_q8_paged(const uint16_t* kv_src, long long src_stride, co
  * outside what the call takes).  Errors: XV_ERR_ARG (null pointer, sizes < 1, Hq
  * not a multiple of Hkv, max_ctx outside [1, Lmax], row strides below Hq*hd,
  * window or sinks < 0), XV_ERR_UNSUPPORTED (hd, R > XV_KMAX, B or Hkv above 65535,
- * unaligned rows, cache or workspace, more than 2^30 work items),
+ * unaligned rows, cache or workspace, B*R*Hq or work items above 2^30),
  * XV_ERR_WORKSPACE, XV_ERR_CUDA.  A sequence whose ctx_len[b] or last row's
  * length is out of range is skipped and recorded (4), n_rows outside [0, R]
  * recorded (8) and clamped, a page outside the pool recorded (16) and read as
@@ -630,7 +630,7 @@ xv_status xv_attn_decode_rows_q8_paged(const uint16_t* q, long long q_stride, co
  * calls of other sizes may use the same buffer, one after another (the size is 0
  * for sizes outside what the call takes).  Errors: XV_ERR_ARG (null pointer,
  * M or V < 1, ld < V, top outside [0, V]), XV_ERR_UNSUPPORTED (top above
- * XV_TOP_MAX, V above 2^19, M * ceil(V / 8192) above 2^31, unaligned workspace),
+ * XV_TOP_MAX, V above 2^19, M * ceil(V / 8192) of 2^31 or more, unaligned workspace),
  * XV_ERR_WORKSPACE, XV_ERR_CUDA.  A token outside [-1, V) is recorded (2) and its
  * logprob NaN. */
 size_t xv_logprobs_workspace_size(int M, int V, int top);

@@ -292,3 +292,16 @@ def test_split_boundaries_past_every_position(xv):
     assert at(last) % 1024 == 0 and 2 ** 31 - 1024 <= at(last) < 2 ** 31 - 1 and at(last) - at(last - 1) == 1024
     for s in (last + 2, 2 ** 22, 2 ** 30, 2 ** 31 - 1):
         assert at(s) == 2 ** 31 - 1, s
+
+
+def test_what_two_terms_hold_of_q():
+    """The two e4m3 terms of a q whose row's largest value lies in [128, 256), as the attention scales it: exact for
+    values from 2^-9 of the largest on, and off by at most 2^-17 of it for smaller ones (2^-10, half of e4m3's smallest
+    step, against 128).  Every significand of bf16 at every size that matters, and the bound is reached."""
+    m = 1 + torch.arange(128, dtype=torch.float32) / 128
+    x = torch.cat([m * 2.0 ** e for e in range(-20, 8)])        # up to 255, all of them bf16
+    e4m3 = lambda v: v.to(torch.float8_e4m3fn).float()   # noqa: E731
+    first = e4m3(x)
+    off = (x - first - e4m3(x - first)).abs()
+    assert not off[x >= 0.25].any() and 0.25 == 128 * 2.0 ** -9
+    assert off.max() == 2.0 ** -10 == 128 * 2.0 ** -17
